@@ -18,7 +18,8 @@ import ctypes
 import os
 
 __all__ = ["Plan", "ConvError", "conv2d_nhwc", "library_path", "load_library", "DTYPES", "ACTS",
-           "ALGOS", "status_str", "abi_version", "run_i8_noalloc", "NOALLOC_MAX_COUT", "spp", "DwpwPlan"]
+           "ALGOS", "status_str", "abi_version", "run_i8_noalloc", "NOALLOC_MAX_COUT", "spp", "DwpwPlan",
+           "GroupNormPlan", "W4Plan", "w4_quantize"]
 
 # Largest c_out conv_run_i8_noalloc accepts (its fixed scratch array holds
 # that many requantisation multipliers).
@@ -30,7 +31,8 @@ _LIB_PATH = os.path.join(_HERE, "libconv_nhwc.so")
 DTYPES = {"f32": 0, "bf16": 1, "i8": 2}
 ACTS = {"none": 0, "relu": 1, "mish": 2}
 ALGOS = {"auto": 0, "direct": 1, "depthwise": 2, "igemm": 3, "igemm_swapped": 4, "igemm_n256": 5,
-         "igemm_n128": 6, "igemm_n64": 7, "igemm_pair": 8, "dwpw": 9, "igemm_pair128": 10}
+         "igemm_n128": 6, "igemm_n64": 7, "igemm_pair": 8, "dwpw": 9, "igemm_pair128": 10,
+         "groupnorm": 11, "w4": 12}
 ALGO_NAMES = {v: k for k, v in ALGOS.items()}
 # Staging, epilogue and int8-widening flags of the tensor-core family
 # (CONV_ALGO_STAGE_*, CONV_ALGO_EPI_*, CONV_ALGO_WIDEN_*), written as suffixes
@@ -124,6 +126,20 @@ def load_library():
     lib.conv_spp_run.argtypes = [c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
                                  c_int, c_void_p]
     lib.conv_spp_run.restype = c_int
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    for name, args in (
+            ("conv_plan_workspace", [c_void_p, ctypes.POINTER(ctypes.c_size_t)]),
+            ("conv_plan_create_groupnorm", [i32, i32, i32, i32, i32, ctypes.c_float, c_int, c_int, pp]),
+            ("conv_run_groupnorm", [c_void_p, c_void_p, i64, c_void_p, c_void_p, c_void_p, i64] + [c_void_p] * 4),
+            ("conv_run_groupnorm_bwd", [c_void_p, c_void_p, i64] + [c_void_p] * 4 + [c_void_p, i64, c_void_p, i64] +
+             [c_void_p] * 4),
+            ("conv_plan_create_w4", [i32, i32, i32, i32, c_int, c_int, pp]),
+            ("conv_w4_packed_bytes", [i32, i32, ctypes.POINTER(ctypes.c_size_t)]),
+            ("conv_w4_pack", [i32, i32, c_void_p, c_void_p, c_void_p]),
+            ("conv_w4_quantize", [i32, i32, i32, c_int] + [c_void_p] * 4),
+            ("conv_run_w4", [c_void_p] * 7)):
+        getattr(lib, name).argtypes = args
+        getattr(lib, name).restype = c_int
     _lib = lib
     return lib
 
@@ -332,3 +348,185 @@ class DwpwPlan(Plan):
                                      _ptr(y), _stream_handle(stream))
         if rc != 0:
             raise ConvError("conv_run_dwpw", rc)
+
+
+def _dtype_name(t) -> str:
+    name = {"torch.float32": "f32", "torch.bfloat16": "bf16", "torch.int8": "i8"}.get(str(t.dtype))
+    if name is None:
+        raise TypeError(f"tensors of {t.dtype} are not supported")
+    return name
+
+
+def _check(name, t, shape, dtype, optional=False):
+    """Checks a dense CUDA tensor argument and returns its device pointer."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if str(t.dtype) != dtype:
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+class _OpPlan(Plan):
+    """What the plans of the operators around the layer share."""
+
+    def _create(self, fn, *args):
+        self._lib = load_library()
+        self._handle = ctypes.c_void_p()
+        rc = getattr(self._lib, fn)(*args, ctypes.byref(self._handle))
+        if rc != 0:
+            raise ConvError(fn, rc)
+        n = ctypes.c_size_t()
+        self._lib.conv_plan_workspace(self._handle, ctypes.byref(n))
+        self.workspace_bytes = n.value
+
+    def _workspace(self, like, stream):
+        """Scratch of one run, from torch's allocator on the run's stream (an
+        explicit `stream` other than the current one is told to the allocator)."""
+        if not self.workspace_bytes:
+            return None
+        import torch
+        ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=like.device)
+        if stream is not None and not isinstance(stream, int):
+            ws.record_stream(stream)
+        elif stream is not None:
+            ws.record_stream(torch.cuda.ExternalStream(stream, device=like.device))
+        return ws
+
+
+_TORCH_NAMES = {"f32": "torch.float32", "bf16": "torch.bfloat16", "i8": "torch.int8"}
+
+
+class GroupNormPlan(_OpPlan):
+    """Group norm with an activation over NHWC maps (conv_plan_create_groupnorm).
+
+    x, y, dy and dx are [n, h, w, c] CUDA tensors, dense or channel slices of a
+    wider dense buffer (``buf[..., a:a + c]``); gamma, beta, dgamma and dbeta
+    float32 [c]; mean and rstd float32 [n, groups]."""
+
+    def __init__(self, n, h, w, c, groups, eps=1e-5, dtype="bf16", act="none"):
+        self.shape = (n, h, w, c)
+        self.groups, self.eps, self.dtype, self.act = groups, eps, dtype, act
+        self._create("conv_plan_create_groupnorm", n, h, w, c, groups, float(eps), DTYPES[dtype], ACTS[act])
+        self._tdt = _TORCH_NAMES[dtype]
+
+    @property
+    def output_shape(self):
+        return self.shape
+
+    y_shape = output_shape
+
+    def _map(self, name, t):
+        """Pointer and pixel pitch of a feature map."""
+        n, h, w, c = self.shape
+        if t is None:
+            raise ValueError(f"{name} is missing")
+        if str(t.dtype) != self._tdt:
+            raise TypeError(f"{name} is {t.dtype}, expected {self._tdt}")
+        if tuple(t.shape) != self.shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {self.shape}")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.is_contiguous():
+            return t.data_ptr(), c
+        sn, sh, sw, sc = t.stride()
+        # a size of one says nothing about its stride
+        pitch = sw if w > 1 else (sh if h > 1 else (sn if n > 1 else c))
+        if ((c > 1 and sc != 1) or pitch < c or (h > 1 and sh != w * pitch) or (n > 1 and sn != h * w * pitch)):
+            raise ValueError(f"{name}: pixels must lie one pitch apart with their channels together, got strides {t.stride()}")
+        return t.data_ptr(), pitch
+
+    def run(self, x, gamma, beta, y, mean=None, rstd=None, stream=None) -> None:  # noqa: D401
+        """Enqueue y = act(group_norm(x) * gamma + beta) on `stream` (default: torch's current stream)."""
+        n, _, _, c = self.shape
+        f32 = "torch.float32"
+        (px, pitch_x), (py, pitch_y) = self._map("x", x), self._map("y", y)
+        g, b = _check("gamma", gamma, (c,), f32, True), _check("beta", beta, (c,), f32, True)
+        m, r = (_check(k, t, (n, self.groups), f32, True) for k, t in (("mean", mean), ("rstd", rstd)))
+        ws = self._workspace(x, stream)
+        rc = self._lib.conv_run_groupnorm(self._handle, px, pitch_x, g, b, py, pitch_y, m, r, _ptr(ws),
+                                          _stream_handle(stream))
+        if rc != 0:
+            raise ConvError("conv_run_groupnorm", rc)
+
+    def run_backward(self, x, gamma, beta, mean, rstd, dy, dx, dgamma=None, dbeta=None, stream=None) -> None:
+        """Enqueue the gradient: dx, and dgamma and dbeta where given."""
+        n, _, _, c = self.shape
+        f32 = "torch.float32"
+        (px, pitch_x), (pdy, pitch_dy), (pdx, pitch_dx) = self._map("x", x), self._map("dy", dy), self._map("dx", dx)
+        g, b = _check("gamma", gamma, (c,), f32, True), _check("beta", beta, (c,), f32, True)
+        m, r = (_check(k, t, (n, self.groups), f32) for k, t in (("mean", mean), ("rstd", rstd)))
+        dg, db = _check("dgamma", dgamma, (c,), f32, True), _check("dbeta", dbeta, (c,), f32, True)
+        ws = self._workspace(x, stream)
+        rc = self._lib.conv_run_groupnorm_bwd(self._handle, px, pitch_x, g, b, m, r, pdy, pitch_dy, pdx, pitch_dx, dg, db,
+                                              _ptr(ws), _stream_handle(stream))
+        if rc != 0:
+            raise ConvError("conv_run_groupnorm_bwd", rc)
+
+
+class W4Plan(_OpPlan):
+    """Pointwise layer on few rows with 4-bit weights and group scales
+    (conv_plan_create_w4): y = act(x W^T + bias), W = (code - 8) * scale.
+
+    codes: uint8 [c_out, ceil(c_in / 2)], laid out once by ``pack``; scales
+    [c_out, ceil(c_in / group)] of the plan's dtype; bias float32 [c_out] or
+    None; x [rows, c_in] and y [rows, c_out] dense."""
+
+    def __init__(self, rows, c_in, c_out, group=128, dtype="bf16", act="none"):
+        self.shape = (rows, c_in, c_out)
+        self.group, self.dtype, self.act = group, dtype, act
+        self._create("conv_plan_create_w4", rows, c_in, c_out, group, DTYPES[dtype], ACTS[act])
+        self._tdt = _TORCH_NAMES[dtype]
+        n = ctypes.c_size_t()
+        self._lib.conv_w4_packed_bytes(c_in, c_out, ctypes.byref(n))
+        self.packed_bytes = n.value
+        self._ng = -(-c_in // group)
+
+    @property
+    def output_shape(self):
+        return (self.shape[0], self.shape[2])
+
+    y_shape = output_shape
+
+    def pack(self, codes, stream=None):
+        """The codes laid out for the kernel, in a new uint8 tensor."""
+        import torch
+        _, c_in, c_out = self.shape
+        pc = _check("codes", codes, (c_out, (c_in + 1) // 2), "torch.uint8")
+        packed = torch.empty(self.packed_bytes, dtype=torch.uint8, device=codes.device)
+        rc = self._lib.conv_w4_pack(c_in, c_out, pc, packed.data_ptr(), _stream_handle(stream))
+        if rc != 0:
+            raise ConvError("conv_w4_pack", rc)
+        return packed
+
+    def run(self, x, packed, scales, bias, y, stream=None) -> None:  # noqa: D401
+        """Enqueue the layer on `stream` (default: torch's current stream)."""
+        rows, c_in, c_out = self.shape
+        px = _check("x", x, (rows, c_in), self._tdt)
+        pw = _check("packed", packed, (self.packed_bytes,), "torch.uint8")
+        ps = _check("scales", scales, (c_out, self._ng), self._tdt)
+        pb = _check("bias", bias, (c_out,), "torch.float32", True)
+        py = _check("y", y, (rows, c_out), self._tdt)
+        rc = self._lib.conv_run_w4(self._handle, px, pw, ps, pb, py, _stream_handle(stream))
+        if rc != 0:
+            raise ConvError("conv_run_w4", rc)
+
+
+def w4_quantize(w, group=128, stream=None):
+    """Codes and scales of float weights [c_out, c_in] (conv_w4_quantize)."""
+    import torch
+    dt = _dtype_name(w)
+    c_out, c_in = w.shape
+    pw = _check("w", w, (c_out, c_in), _TORCH_NAMES[dt])
+    codes = torch.empty(c_out, (c_in + 1) // 2, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(c_out, -(-c_in // group), dtype=w.dtype, device=w.device)
+    rc = load_library().conv_w4_quantize(c_in, c_out, group, DTYPES[dt], pw, codes.data_ptr(), scales.data_ptr(),
+                                         _stream_handle(stream))
+    if rc != 0:
+        raise ConvError("conv_w4_quantize", rc)
+    return codes, scales

@@ -132,6 +132,20 @@ int conv_grant_smem(const void *k, int device, int need) {
     return CONV_OK;
 }
 
+int conv_plan_bind_device(conv_plan *p, bool status_word) {
+    int major = 0, minor = 0;
+    if (cudaGetDevice(&p->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, p->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, p->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&p->num_sms, cudaDevAttrMultiProcessorCount, p->device) != cudaSuccess)
+        return CONV_ERR_CUDA;
+    if (major != 10 || minor != 3) return CONV_ERR_UNSUPPORTED;
+    if (!status_word) return CONV_OK;
+    if (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess) return CONV_ERR_OOM;
+    if (cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess) return CONV_ERR_CUDA;
+    return CONV_OK;
+}
+
 extern "C" {
 
 int conv_abi_version(void) { return CONV_NHWC_ABI_VERSION; }
@@ -404,14 +418,22 @@ const char *conv_plan_describe(const conv_plan_t *plan) { return plan ? plan->de
 int conv_plan_launches(const conv_plan_t *plan) {
     if (!plan) return CONV_ERR_NULL_ARG;
     if (plan->s.n == 0) return 0;
+    if (plan->algo == CONV_ALGO_GROUPNORM) return 2;  // either direction
     return (plan->algo == CONV_ALGO_IGEMM && plan->ig.prep) ? 2 : 1;
+}
+
+int conv_plan_workspace(const conv_plan_t *plan, size_t *bytes) {
+    if (!plan || !bytes) return CONV_ERR_NULL_ARG;
+    *bytes = plan->ws_bytes;
+    return CONV_OK;
 }
 
 int conv_run_fused(const conv_plan_t *plan, const void *x, const void *w, const void *bias, const void *residual,
                    void *y, void *stream) {
     if (!plan) return CONV_ERR_NULL_ARG;
     const conv_plan *p = plan;
-    if (p->algo == CONV_ALGO_DWPW) return CONV_ERR_INVALID_ARG;  // runs through conv_run_dwpw
+    // (plans that run through entry points of their own: conv_run_dwpw, conv_run_groupnorm, conv_run_w4)
+    if (p->algo == CONV_ALGO_DWPW || p->algo == CONV_ALGO_GROUPNORM || p->algo == CONV_ALGO_W4) return CONV_ERR_INVALID_ARG;
     if (p->has_res && !residual) return CONV_ERR_NULL_ARG;
     if (!p->has_res && residual) return CONV_ERR_INVALID_ARG;
     if (p->s.n == 0) return CONV_OK;  // empty batch: nothing to compute
@@ -448,6 +470,7 @@ int conv_plan_check_device_status(conv_plan_t *plan, void *stream) {
     cudaStream_t st = (cudaStream_t)stream;
     int h = 0;
     if (cudaStreamSynchronize(st) != cudaSuccess) return CONV_ERR_CUDA;
+    if (!plan->d_status) return CONV_OK;  // kernels without waits
     if (cudaMemcpy(&h, plan->d_status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return CONV_ERR_CUDA;
     if (h != 0) {
         if (cudaMemset(plan->d_status, 0, sizeof(int)) != cudaSuccess) return CONV_ERR_CUDA;

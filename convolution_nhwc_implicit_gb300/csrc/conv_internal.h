@@ -72,6 +72,18 @@ struct DwpwGeom {
     int smem;          // dynamic shared memory bytes
 };
 
+// Group norm: every image's pixels in S runs of ppx.
+struct GnGeom {
+    float eps;
+    int S, ppx;
+};
+
+// 4-bit pointwise layer: scale groups, runs of 128 input channels, and blocks
+// of eight rows a CTA.
+struct W4Geom {
+    int group, ng, units, nt;
+};
+
 struct conv_plan {
     conv_shape_t s;
     int stride, pad_h, pad_w, groups;
@@ -94,8 +106,15 @@ struct conv_plan {
     // writes channels [y_coff, y_coff + c_out) of a (up*OH) x (up*OW) grid,
     // adding the residual tensor when has_res.
     int y_c, y_coff, up, has_res;
+    GnGeom gn;
+    W4Geom w4;
+    size_t ws_bytes;   // device scratch a run takes from the caller (conv_plan_workspace)
     char desc[192];
 };
+
+// Binds a new plan to the current device (sm_103a only) and gives it a status
+// word if its kernels have waits to report on.  Returns a CONV_* status.
+int conv_plan_bind_device(conv_plan *p, bool status_word);
 
 // Element size of a conv_dtype_t.
 static inline int conv_esize(conv_dtype_t t) { return t == CONV_F32 ? 4 : (t == CONV_BF16 ? 2 : 1); }

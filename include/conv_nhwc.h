@@ -105,6 +105,11 @@ typedef enum {
      * family conv_plan_create_ex can force) */
     CONV_ALGO_DWPW = 9,          /* fused depthwise 3x3 -> pointwise 1x1 pair */
     CONV_ALGO_IGEMM_PAIR128 = 10, /* CTA-pair MMA: M = 256 pixels, N = 128 output channels */
+    /* (reported by conv_plan_algo for the plans of the operators around the
+     * layer; conv_plan_create_ex cannot force them and conv_run refuses their
+     * plans with CONV_ERR_INVALID_ARG) */
+    CONV_ALGO_GROUPNORM = 11, /* conv_plan_create_groupnorm  */
+    CONV_ALGO_W4 = 12,        /* conv_plan_create_w4         */
 } conv_algo_t;
 
 /* Staging of the tensor-core family's pixel operand, OR-ed into CONV_ALGO_IGEMM
@@ -266,6 +271,75 @@ CONV_API int conv_plan_create_dwpw(const conv_shape_t *shape, int stride, int pa
                                    conv_act_t act_dw, conv_act_t act_pw, conv_plan_t **out_plan);
 CONV_API int conv_run_dwpw(const conv_plan_t *plan, const void *x, const void *w_dw, const void *b_dw,
                            const void *w_pw, const void *b_pw, void *y, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Group norm with an activation, channels last.  A norm that depends on its
+ * input cannot be folded into a layer's weights, so it follows the layer as
+ * an operator of its own.  A group is the c / groups consecutive channels of
+ * one image, m = h * w * c / groups values:
+ *   mean = sum x / m       rstd = 1 / sqrt( sum (x - mean)^2 / m + eps )
+ *   xhat = (x - mean) rstd    z = gamma[c] xhat + beta[c]    y = act(z)
+ * and the gradient, with dz = dy act'(z):
+ *   dbeta[c] = sum_{n,h,w} dz         dgamma[c] = sum_{n,h,w} dz xhat
+ *   dx = rstd ( gamma dz - ( sum_group gamma dz + xhat sum_group gamma dz xhat ) / m )
+ * dtype CONV_F32 or CONV_BF16 for x, y, dy, dx (CONV_I8: CONV_ERR_UNSUPPORTED);
+ * gamma, beta, dgamma, dbeta [c] and mean, rstd [n][groups] are float32, all
+ * statistics and sums fp32.  eps >= 0 (CONV_ERR_INVALID_ARG); c <= 8192,
+ * n <= 65534, h * w < 2^30 (CONV_ERR_UNSUPPORTED).
+ *
+ * x, y, dy and dx are [n][h][w] pixels of c channels, *_pitch elements from
+ * one pixel to the next (0: c): a channel slice of a concatenated buffer is
+ * its first channel's address and the buffer's channel count.  Any address
+ * that is a multiple of the element size is accepted; 16-byte addresses,
+ * pitches and channel counts give the widest loads.
+ *   conv_run_groupnorm       gamma, beta may be NULL (1 and 0); mean and rstd
+ *                            may be NULL (not written)
+ *   conv_run_groupnorm_bwd   mean and rstd as the forward run wrote them;
+ *                            dgamma, dbeta may be NULL (not written)
+ * y must not share an element with x, nor dx with x or dy (CONV_ERR_ALIASING;
+ * interleaved channel slices of one buffer share none).  n = 0 does nothing
+ * (the gradient writes zeros to dgamma and dbeta). */
+CONV_API int conv_plan_create_groupnorm(int32_t n, int32_t h, int32_t w, int32_t c, int32_t groups, float eps,
+                                        conv_dtype_t dtype, conv_act_t act, conv_plan_t **out_plan);
+CONV_API int conv_run_groupnorm(const conv_plan_t *plan, const void *x, int64_t x_pitch, const float *gamma,
+                                const float *beta, void *y, int64_t y_pitch, float *mean, float *rstd,
+                                void *workspace, void *stream);
+CONV_API int conv_run_groupnorm_bwd(const conv_plan_t *plan, const void *x, int64_t x_pitch, const float *gamma,
+                                    const float *beta, const float *mean, const float *rstd, const void *dy,
+                                    int64_t dy_pitch, void *dx, int64_t dx_pitch, float *dgamma, float *dbeta,
+                                    void *workspace, void *stream);
+
+/* Bytes of device scratch that a run of this plan takes as `workspace` (0 for
+ * plans whose runs take none; NULL may then be given).  The caller owns it,
+ * 16-byte aligned; it holds nothing between calls, and calls that can overlap
+ * on the GPU take one each. */
+CONV_API int conv_plan_workspace(const conv_plan_t *plan, size_t *bytes);
+
+/* ---------------------------------------------------------------------------
+ * Pointwise (1x1) layer on few rows (pixels, feature vectors) with 4-bit
+ * weights and a scale for each output channel and group of input channels:
+ *   y[m,co] = act( bias[co] + sum_k scales[co][k / group] (code[co][k] - 8) x[m,k] )
+ * x [rows][c_in], y [rows][c_out] and scales [c_out][ceil(c_in / group)] are
+ * of dtype (CONV_F32 or CONV_BF16; CONV_I8: CONV_ERR_UNSUPPORTED), bias
+ * [c_out] float32 or NULL, group 32, 64 or 128 (CONV_ERR_INVALID_ARG), any
+ * c_in, c_out and rows >= 1.  Products and sums are fp32, one rounding to y.
+ *   codes   [c_out][ceil(c_in / 2)] bytes, two codes 0..15 a byte, the even
+ *           input channel in the low half (an odd c_in's last high half is
+ *           ignored); the weight is (code - 8) * scale
+ *   packed  the codes laid out for the kernel, conv_w4_packed_bytes of device
+ *           memory, 16-byte aligned: written once by conv_w4_pack, read by
+ *           every run
+ * conv_w4_quantize makes codes and scales of float weights [c_out][c_in]:
+ * scale = max |w| of the group / 7 (rounded to dtype), code =
+ * clamp(round_half_even(w / scale), -8, 7) + 8. */
+CONV_API int conv_plan_create_w4(int32_t rows, int32_t c_in, int32_t c_out, int32_t group, conv_dtype_t dtype,
+                                 conv_act_t act, conv_plan_t **out_plan);
+CONV_API int conv_w4_packed_bytes(int32_t c_in, int32_t c_out, size_t *bytes);
+CONV_API int conv_w4_pack(int32_t c_in, int32_t c_out, const void *codes, void *packed, void *stream);
+CONV_API int conv_w4_quantize(int32_t c_in, int32_t c_out, int32_t group, conv_dtype_t dtype, const void *w, void *codes,
+                              void *scales, void *stream);
+CONV_API int conv_run_w4(const conv_plan_t *plan, const void *x, const void *packed, const void *scales,
+                         const float *bias, void *y, void *stream);
 
 /* Enqueues the layer on `stream` (a cudaStream_t; NULL = legacy default
  * stream).  x, w, y are device pointers, bias a device pointer or NULL; all
