@@ -19,7 +19,7 @@ import os
 
 __all__ = ["Plan", "ConvError", "conv2d_nhwc", "library_path", "load_library", "DTYPES", "ACTS",
            "ALGOS", "status_str", "abi_version", "run_i8_noalloc", "NOALLOC_MAX_COUT", "spp", "DwpwPlan",
-           "GroupNormPlan", "W4Plan", "w4_quantize"]
+           "GroupNormPlan", "ClassLossPlan", "W4Plan", "w4_quantize"]
 
 # Largest c_out conv_run_i8_noalloc accepts (its fixed scratch array holds
 # that many requantisation multipliers).
@@ -32,7 +32,7 @@ DTYPES = {"f32": 0, "bf16": 1, "i8": 2}
 ACTS = {"none": 0, "relu": 1, "mish": 2}
 ALGOS = {"auto": 0, "direct": 1, "depthwise": 2, "igemm": 3, "igemm_swapped": 4, "igemm_n256": 5,
          "igemm_n128": 6, "igemm_n64": 7, "igemm_pair": 8, "dwpw": 9, "igemm_pair128": 10,
-         "groupnorm": 11, "w4": 12}
+         "groupnorm": 11, "w4": 12, "xent": 13}
 ALGO_NAMES = {v: k for k, v in ALGOS.items()}
 # Staging, epilogue and int8-widening flags of the tensor-core family
 # (CONV_ALGO_STAGE_*, CONV_ALGO_EPI_*, CONV_ALGO_WIDEN_*), written as suffixes
@@ -133,6 +133,9 @@ def load_library():
             ("conv_run_groupnorm", [c_void_p, c_void_p, i64, c_void_p, c_void_p, c_void_p, i64] + [c_void_p] * 4),
             ("conv_run_groupnorm_bwd", [c_void_p, c_void_p, i64] + [c_void_p] * 4 + [c_void_p, i64, c_void_p, i64] +
              [c_void_p] * 4),
+            ("conv_plan_create_xent", [i32, i32, i32, i32, c_int, pp]),
+            ("conv_run_xent", [c_void_p] * 9),
+            ("conv_run_xent_bwd", [c_void_p] * 10),
             ("conv_plan_create_w4", [i32, i32, i32, i32, c_int, c_int, pp]),
             ("conv_w4_packed_bytes", [i32, i32, ctypes.POINTER(ctypes.c_size_t)]),
             ("conv_w4_pack", [i32, i32, c_void_p, c_void_p, c_void_p]),
@@ -467,6 +470,52 @@ class GroupNormPlan(_OpPlan):
                                               _ptr(ws), _stream_handle(stream))
         if rc != 0:
             raise ConvError("conv_run_groupnorm_bwd", rc)
+
+
+class ClassLossPlan(_OpPlan):
+    """Softmax cross entropy of a class head over many classes, and its gradient
+    (conv_plan_create_xent): scores x w^T that are never stored.
+
+    x [rows, c_in] and w [classes, c_in] bf16; target int32 [rows], a row whose
+    target is no class is left out; the loss is the mean over the others.
+    ``piece`` bounds the classes the gradient works on at a time (0: chosen)."""
+
+    def __init__(self, rows, c_in, classes, piece=0, dtype="bf16"):
+        self.shape = (rows, c_in, classes)
+        self.dtype, self.act = dtype, "none"
+        self._create("conv_plan_create_xent", rows, c_in, classes, piece, DTYPES[dtype])
+
+    @property
+    def output_shape(self):
+        return ()
+
+    y_shape = output_shape
+
+    def run(self, x, w, target, loss, lse=None, row_loss=None, stream=None) -> None:  # noqa: D401
+        """Enqueue the loss (a float32 scalar) and, where given, lse and row_loss (float32 [rows])."""
+        rows, c_in, classes = self.shape
+        f32, bf16 = "torch.float32", "torch.bfloat16"
+        px, pw = _check("x", x, (rows, c_in), bf16), _check("w", w, (classes, c_in), bf16)
+        pt = _check("target", target, (rows,), "torch.int32")
+        pl, ps = _check("loss", loss, (), f32), _check("lse", lse, (rows,), f32, True)
+        pr = _check("row_loss", row_loss, (rows,), f32, True)
+        ws = self._workspace(x, stream)
+        rc = self._lib.conv_run_xent(self._handle, px, pw, pt, pl, pr, ps, _ptr(ws), _stream_handle(stream))
+        if rc != 0:
+            raise ConvError("conv_run_xent", rc)
+
+    def run_backward(self, x, w, target, lse, dx, dw, dloss=None, stream=None) -> None:
+        """Enqueue the gradient of the loss times dloss (a float32 scalar tensor; None: 1)."""
+        rows, c_in, classes = self.shape
+        f32, bf16 = "torch.float32", "torch.bfloat16"
+        px, pw = _check("x", x, (rows, c_in), bf16), _check("w", w, (classes, c_in), bf16)
+        pt, ps = _check("target", target, (rows,), "torch.int32"), _check("lse", lse, (rows,), f32)
+        pdx, pdw = _check("dx", dx, (rows, c_in), bf16), _check("dw", dw, (classes, c_in), bf16)
+        pd = _check("dloss", dloss, (), f32, True)
+        ws = self._workspace(x, stream)
+        rc = self._lib.conv_run_xent_bwd(self._handle, px, pw, pt, ps, pd, pdx, pdw, _ptr(ws), _stream_handle(stream))
+        if rc != 0:
+            raise ConvError("conv_run_xent_bwd", rc)
 
 
 class W4Plan(_OpPlan):

@@ -419,6 +419,8 @@ int conv_plan_launches(const conv_plan_t *plan) {
     if (!plan) return CONV_ERR_NULL_ARG;
     if (plan->s.n == 0) return 0;
     if (plan->algo == CONV_ALGO_GROUPNORM) return 2;  // either direction
+    // (the forward run; its gradient takes two launches a piece of the classes, and more for joined sums)
+    if (plan->algo == CONV_ALGO_XENT) return plan->xent.dp == plan->s.c_in ? 2 : 4;
     return (plan->algo == CONV_ALGO_IGEMM && plan->ig.prep) ? 2 : 1;
 }
 
@@ -432,8 +434,9 @@ int conv_run_fused(const conv_plan_t *plan, const void *x, const void *w, const 
                    void *y, void *stream) {
     if (!plan) return CONV_ERR_NULL_ARG;
     const conv_plan *p = plan;
-    // (plans that run through entry points of their own: conv_run_dwpw, conv_run_groupnorm, conv_run_w4)
-    if (p->algo == CONV_ALGO_DWPW || p->algo == CONV_ALGO_GROUPNORM || p->algo == CONV_ALGO_W4) return CONV_ERR_INVALID_ARG;
+    // (plans that run through entry points of their own: conv_run_dwpw, conv_run_groupnorm, conv_run_xent, conv_run_w4)
+    if (p->algo == CONV_ALGO_DWPW || p->algo == CONV_ALGO_GROUPNORM || p->algo == CONV_ALGO_W4 || p->algo == CONV_ALGO_XENT)
+        return CONV_ERR_INVALID_ARG;
     if (p->has_res && !residual) return CONV_ERR_NULL_ARG;
     if (!p->has_res && residual) return CONV_ERR_INVALID_ARG;
     if (p->s.n == 0) return CONV_OK;  // empty batch: nothing to compute

@@ -84,6 +84,15 @@ struct W4Geom {
     int group, ng, units, nt;
 };
 
+// Class loss: 256 x 256 tiles over rows, classes and features; the classes in
+// `pieces` of `piece`; the two gradient products' K axes in runs.
+struct XentGeom {
+    int dp;                                  // features of the operands TMA reads (padded to 8)
+    int tiles_m, tiles_n, tiles_d;
+    int piece, pieces;
+    int dx_split, dx_kper, dw_split, dw_kper;
+};
+
 struct conv_plan {
     conv_shape_t s;
     int stride, pad_h, pad_w, groups;
@@ -108,6 +117,7 @@ struct conv_plan {
     int y_c, y_coff, up, has_res;
     GnGeom gn;
     W4Geom w4;
+    XentGeom xent;
     size_t ws_bytes;   // device scratch a run takes from the caller (conv_plan_workspace)
     char desc[192];
 };

@@ -110,6 +110,7 @@ typedef enum {
      * plans with CONV_ERR_INVALID_ARG) */
     CONV_ALGO_GROUPNORM = 11, /* conv_plan_create_groupnorm  */
     CONV_ALGO_W4 = 12,        /* conv_plan_create_w4         */
+    CONV_ALGO_XENT = 13,      /* conv_plan_create_xent       */
 } conv_algo_t;
 
 /* Staging of the tensor-core family's pixel operand, OR-ed into CONV_ALGO_IGEMM
@@ -314,6 +315,33 @@ CONV_API int conv_run_groupnorm_bwd(const conv_plan_t *plan, const void *x, int6
  * 16-byte aligned; it holds nothing between calls, and calls that can overlap
  * on the GPU take one each. */
 CONV_API int conv_plan_workspace(const conv_plan_t *plan, size_t *bytes);
+
+/* ---------------------------------------------------------------------------
+ * Loss of a class head over many classes: softmax cross entropy of the scores
+ * l = x w^T (a 1x1 layer without bias), and its gradient, the scores never
+ * stored:
+ *   lse[i]  = log sum_v exp l[i,v]
+ *   loss    = sum over labelled rows of (lse[i] - l[i,target[i]]) / count
+ *   g[i,v]  = exp(l[i,v] - lse[i]) - (v == target[i])   (0 for the other rows)
+ *   dx = dloss / count * g w          dw = dloss / count * g^T x
+ * x and dx [rows][c_in], w and dw [classes][c_in], bf16 (other dtypes:
+ * CONV_ERR_UNSUPPORTED); target [rows] int32: a row whose target is negative
+ * or not below classes is left out, and count is the number of the others (at
+ * least 1: without any, loss and gradients are 0).  loss, row_loss [rows] (0
+ * for rows left out), lse [rows] and dloss (a device scalar) are float32;
+ * row_loss, lse and dloss may be NULL (not written; 1).  x, w, dx and dw are
+ * 16-byte aligned and dense; any rows, c_in and classes.
+ *
+ * The gradient takes the classes in pieces: workspace holds g of one piece, in
+ * bf16.  piece is the most classes at a time (rounded down to 256s, at least
+ * 256; 0: as many as keep g within 256 MB).  The scores are formed again.
+ * rows <= 2^24, classes <= 2^24, c_in <= 2^20. */
+CONV_API int conv_plan_create_xent(int32_t rows, int32_t c_in, int32_t classes, int32_t piece, conv_dtype_t dtype,
+                                   conv_plan_t **out_plan);
+CONV_API int conv_run_xent(const conv_plan_t *plan, const void *x, const void *w, const int32_t *target, float *loss,
+                           float *row_loss, float *lse, void *workspace, void *stream);
+CONV_API int conv_run_xent_bwd(const conv_plan_t *plan, const void *x, const void *w, const int32_t *target,
+                               const float *lse, const float *dloss, void *dx, void *dw, void *workspace, void *stream);
 
 /* ---------------------------------------------------------------------------
  * Pointwise (1x1) layer on few rows (pixels, feature vectors) with 4-bit

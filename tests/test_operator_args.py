@@ -84,3 +84,24 @@ def test_no_plan(lib):
     assert lib.conv_run_groupnorm(None, 16, 0, None, None, 16, 0, None, None, None, None) == NULL
     assert lib.conv_run_groupnorm_bwd(None, 16, 0, None, None, 16, 16, 16, 0, 16, 0, None, None, None, None) == NULL
     assert lib.conv_run_w4(None, 16, 16, 16, None, 16, None) == NULL
+
+
+@pytest.mark.parametrize("args,want", [
+    ((-1, 64, 100, 0, 1), SHAPE),
+    ((4, 0, 100, 0, 1), SHAPE),
+    ((4, 64, 0, 0, 1), SHAPE),
+    ((4, 64, 100, -1, 1), SHAPE),
+    ((4, 64, 100, 0, 5), ARG),
+    ((4, 64, 100, 0, 0), UNSUPPORTED),                 # fp32
+    ((4, 64, 100, 0, 2), UNSUPPORTED),                 # int8
+    ((4, 64, (1 << 24) + 1, 0, 1), UNSUPPORTED),
+    (((1 << 24) + 1, 64, 100, 0, 1), UNSUPPORTED),
+    ((4, (1 << 20) + 1, 100, 0, 1), UNSUPPORTED),
+])
+def test_xent_refusals(lib, args, want):
+    h = ctypes.c_void_p(12345)
+    assert lib.conv_plan_create_xent(*args, ctypes.byref(h)) == want
+    assert h.value is None
+    assert lib.conv_plan_create_xent(*args, None) == NULL
+    assert lib.conv_run_xent(None, 16, 16, 16, 16, None, None, 16, None) == NULL
+    assert lib.conv_run_xent_bwd(None, 16, 16, 16, 16, None, 16, 16, 16, None) == NULL
