@@ -129,6 +129,7 @@ def load_library():
     i32, i64 = ctypes.c_int32, ctypes.c_int64
     for name, args in (
             ("conv_plan_workspace", [c_void_p, ctypes.POINTER(ctypes.c_size_t)]),
+            ("conv_plan_workspace_bwd", [c_void_p, ctypes.POINTER(ctypes.c_size_t)]),
             ("conv_plan_create_groupnorm", [i32, i32, i32, i32, i32, ctypes.c_float, c_int, c_int, pp]),
             ("conv_run_groupnorm", [c_void_p, c_void_p, i64, c_void_p, c_void_p, c_void_p, i64] + [c_void_p] * 4),
             ("conv_run_groupnorm_bwd", [c_void_p, c_void_p, i64] + [c_void_p] * 4 + [c_void_p, i64, c_void_p, i64] +
@@ -164,10 +165,19 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _current_stream():
+    """Handle of torch's current stream (the raw form spares a small call the
+    3 us of building a Stream object)."""
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
+
+
 def _stream_handle(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -360,19 +370,22 @@ def _dtype_name(t) -> str:
     return name
 
 
-def _check(name, t, shape, dtype, optional=False):
+def _check(name, t, shape, dtype):
     """Checks a dense CUDA tensor argument and returns its device pointer."""
     if t is None:
-        if optional:
-            return None
         raise ValueError(f"{name} is missing")
-    if str(t.dtype) != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     return t.data_ptr()
+
+
+def _torch_dtype(name):
+    import torch
+    return {"f32": torch.float32, "bf16": torch.bfloat16, "i8": torch.int8, "u8": torch.uint8, "i32": torch.int32}[name]
 
 
 class _OpPlan(Plan):
@@ -387,22 +400,20 @@ class _OpPlan(Plan):
         n = ctypes.c_size_t()
         self._lib.conv_plan_workspace(self._handle, ctypes.byref(n))
         self.workspace_bytes = n.value
+        self._lib.conv_plan_workspace_bwd(self._handle, ctypes.byref(n))
+        self.workspace_bytes_backward = n.value
+        self._f32, self._dt = _torch_dtype("f32"), _torch_dtype(self.dtype)
 
-    def _workspace(self, like, stream):
+    def _workspace(self, nbytes, like, stream):
         """Scratch of one run, from torch's allocator on the run's stream (an
         explicit `stream` other than the current one is told to the allocator)."""
-        if not self.workspace_bytes:
+        if not nbytes:
             return None
         import torch
-        ws = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=like.device)
-        if stream is not None and not isinstance(stream, int):
-            ws.record_stream(stream)
-        elif stream is not None:
-            ws.record_stream(torch.cuda.ExternalStream(stream, device=like.device))
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            ws.record_stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream)
         return ws
-
-
-_TORCH_NAMES = {"f32": "torch.float32", "bf16": "torch.bfloat16", "i8": "torch.int8"}
 
 
 class GroupNormPlan(_OpPlan):
@@ -416,7 +427,7 @@ class GroupNormPlan(_OpPlan):
         self.shape = (n, h, w, c)
         self.groups, self.eps, self.dtype, self.act = groups, eps, dtype, act
         self._create("conv_plan_create_groupnorm", n, h, w, c, groups, float(eps), DTYPES[dtype], ACTS[act])
-        self._tdt = _TORCH_NAMES[dtype]
+        self._cshape, self._sshape = (c,), (n, groups)
 
     @property
     def output_shape(self):
@@ -429,9 +440,9 @@ class GroupNormPlan(_OpPlan):
         n, h, w, c = self.shape
         if t is None:
             raise ValueError(f"{name} is missing")
-        if str(t.dtype) != self._tdt:
-            raise TypeError(f"{name} is {t.dtype}, expected {self._tdt}")
-        if tuple(t.shape) != self.shape:
+        if t.dtype is not self._dt:
+            raise TypeError(f"{name} is {t.dtype}, expected {self._dt}")
+        if t.shape != self.shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {self.shape}")
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
@@ -446,12 +457,13 @@ class GroupNormPlan(_OpPlan):
 
     def run(self, x, gamma, beta, y, mean=None, rstd=None, stream=None) -> None:  # noqa: D401
         """Enqueue y = act(group_norm(x) * gamma + beta) on `stream` (default: torch's current stream)."""
-        n, _, _, c = self.shape
-        f32 = "torch.float32"
+        f32, cs, ss = self._f32, self._cshape, self._sshape
         (px, pitch_x), (py, pitch_y) = self._map("x", x), self._map("y", y)
-        g, b = _check("gamma", gamma, (c,), f32, True), _check("beta", beta, (c,), f32, True)
-        m, r = (_check(k, t, (n, self.groups), f32, True) for k, t in (("mean", mean), ("rstd", rstd)))
-        ws = self._workspace(x, stream)
+        g = None if gamma is None else _check("gamma", gamma, cs, f32)
+        b = None if beta is None else _check("beta", beta, cs, f32)
+        m = None if mean is None else _check("mean", mean, ss, f32)
+        r = None if rstd is None else _check("rstd", rstd, ss, f32)
+        ws = self._workspace(self.workspace_bytes, x, stream)
         rc = self._lib.conv_run_groupnorm(self._handle, px, pitch_x, g, b, py, pitch_y, m, r, _ptr(ws),
                                           _stream_handle(stream))
         if rc != 0:
@@ -459,13 +471,14 @@ class GroupNormPlan(_OpPlan):
 
     def run_backward(self, x, gamma, beta, mean, rstd, dy, dx, dgamma=None, dbeta=None, stream=None) -> None:
         """Enqueue the gradient: dx, and dgamma and dbeta where given."""
-        n, _, _, c = self.shape
-        f32 = "torch.float32"
+        f32, cs, ss = self._f32, self._cshape, self._sshape
         (px, pitch_x), (pdy, pitch_dy), (pdx, pitch_dx) = self._map("x", x), self._map("dy", dy), self._map("dx", dx)
-        g, b = _check("gamma", gamma, (c,), f32, True), _check("beta", beta, (c,), f32, True)
-        m, r = (_check(k, t, (n, self.groups), f32) for k, t in (("mean", mean), ("rstd", rstd)))
-        dg, db = _check("dgamma", dgamma, (c,), f32, True), _check("dbeta", dbeta, (c,), f32, True)
-        ws = self._workspace(x, stream)
+        g = None if gamma is None else _check("gamma", gamma, cs, f32)
+        b = None if beta is None else _check("beta", beta, cs, f32)
+        m, r = _check("mean", mean, ss, f32), _check("rstd", rstd, ss, f32)
+        dg = None if dgamma is None else _check("dgamma", dgamma, cs, f32)
+        db = None if dbeta is None else _check("dbeta", dbeta, cs, f32)
+        ws = self._workspace(self.workspace_bytes_backward, x, stream)
         rc = self._lib.conv_run_groupnorm_bwd(self._handle, px, pitch_x, g, b, m, r, pdy, pitch_dy, pdx, pitch_dx, dg, db,
                                               _ptr(ws), _stream_handle(stream))
         if rc != 0:
@@ -484,6 +497,7 @@ class ClassLossPlan(_OpPlan):
         self.shape = (rows, c_in, classes)
         self.dtype, self.act = dtype, "none"
         self._create("conv_plan_create_xent", rows, c_in, classes, piece, DTYPES[dtype])
+        self._i32 = _torch_dtype("i32")
 
     @property
     def output_shape(self):
@@ -494,12 +508,12 @@ class ClassLossPlan(_OpPlan):
     def run(self, x, w, target, loss, lse=None, row_loss=None, stream=None) -> None:  # noqa: D401
         """Enqueue the loss (a float32 scalar) and, where given, lse and row_loss (float32 [rows])."""
         rows, c_in, classes = self.shape
-        f32, bf16 = "torch.float32", "torch.bfloat16"
+        f32, bf16 = self._f32, self._dt
         px, pw = _check("x", x, (rows, c_in), bf16), _check("w", w, (classes, c_in), bf16)
-        pt = _check("target", target, (rows,), "torch.int32")
-        pl, ps = _check("loss", loss, (), f32), _check("lse", lse, (rows,), f32, True)
-        pr = _check("row_loss", row_loss, (rows,), f32, True)
-        ws = self._workspace(x, stream)
+        pt, pl = _check("target", target, (rows,), self._i32), _check("loss", loss, (), f32)
+        ps = None if lse is None else _check("lse", lse, (rows,), f32)
+        pr = None if row_loss is None else _check("row_loss", row_loss, (rows,), f32)
+        ws = self._workspace(self.workspace_bytes, x, stream)
         rc = self._lib.conv_run_xent(self._handle, px, pw, pt, pl, pr, ps, _ptr(ws), _stream_handle(stream))
         if rc != 0:
             raise ConvError("conv_run_xent", rc)
@@ -507,12 +521,12 @@ class ClassLossPlan(_OpPlan):
     def run_backward(self, x, w, target, lse, dx, dw, dloss=None, stream=None) -> None:
         """Enqueue the gradient of the loss times dloss (a float32 scalar tensor; None: 1)."""
         rows, c_in, classes = self.shape
-        f32, bf16 = "torch.float32", "torch.bfloat16"
+        f32, bf16 = self._f32, self._dt
         px, pw = _check("x", x, (rows, c_in), bf16), _check("w", w, (classes, c_in), bf16)
-        pt, ps = _check("target", target, (rows,), "torch.int32"), _check("lse", lse, (rows,), f32)
+        pt, ps = _check("target", target, (rows,), self._i32), _check("lse", lse, (rows,), f32)
         pdx, pdw = _check("dx", dx, (rows, c_in), bf16), _check("dw", dw, (classes, c_in), bf16)
-        pd = _check("dloss", dloss, (), f32, True)
-        ws = self._workspace(x, stream)
+        pd = None if dloss is None else _check("dloss", dloss, (), f32)
+        ws = self._workspace(self.workspace_bytes_backward, x, stream)
         rc = self._lib.conv_run_xent_bwd(self._handle, px, pw, pt, ps, pd, pdx, pdw, _ptr(ws), _stream_handle(stream))
         if rc != 0:
             raise ConvError("conv_run_xent_bwd", rc)
@@ -530,11 +544,11 @@ class W4Plan(_OpPlan):
         self.shape = (rows, c_in, c_out)
         self.group, self.dtype, self.act = group, dtype, act
         self._create("conv_plan_create_w4", rows, c_in, c_out, group, DTYPES[dtype], ACTS[act])
-        self._tdt = _TORCH_NAMES[dtype]
         n = ctypes.c_size_t()
         self._lib.conv_w4_packed_bytes(c_in, c_out, ctypes.byref(n))
         self.packed_bytes = n.value
-        self._ng = -(-c_in // group)
+        self._u8 = _torch_dtype("u8")
+        self._shapes = (rows, c_in), (self.packed_bytes,), (c_out, -(-c_in // group)), (c_out,), (rows, c_out)
 
     @property
     def output_shape(self):
@@ -546,7 +560,7 @@ class W4Plan(_OpPlan):
         """The codes laid out for the kernel, in a new uint8 tensor."""
         import torch
         _, c_in, c_out = self.shape
-        pc = _check("codes", codes, (c_out, (c_in + 1) // 2), "torch.uint8")
+        pc = _check("codes", codes, (c_out, (c_in + 1) // 2), self._u8)
         packed = torch.empty(self.packed_bytes, dtype=torch.uint8, device=codes.device)
         rc = self._lib.conv_w4_pack(c_in, c_out, pc, packed.data_ptr(), _stream_handle(stream))
         if rc != 0:
@@ -555,12 +569,11 @@ class W4Plan(_OpPlan):
 
     def run(self, x, packed, scales, bias, y, stream=None) -> None:  # noqa: D401
         """Enqueue the layer on `stream` (default: torch's current stream)."""
-        rows, c_in, c_out = self.shape
-        px = _check("x", x, (rows, c_in), self._tdt)
-        pw = _check("packed", packed, (self.packed_bytes,), "torch.uint8")
-        ps = _check("scales", scales, (c_out, self._ng), self._tdt)
-        pb = _check("bias", bias, (c_out,), "torch.float32", True)
-        py = _check("y", y, (rows, c_out), self._tdt)
+        sx, sw, ss, sb, sy = self._shapes
+        dt = self._dt
+        px, pw, ps = _check("x", x, sx, dt), _check("packed", packed, sw, self._u8), _check("scales", scales, ss, dt)
+        pb = None if bias is None else _check("bias", bias, sb, self._f32)
+        py = _check("y", y, sy, dt)
         rc = self._lib.conv_run_w4(self._handle, px, pw, ps, pb, py, _stream_handle(stream))
         if rc != 0:
             raise ConvError("conv_run_w4", rc)
@@ -571,7 +584,7 @@ def w4_quantize(w, group=128, stream=None):
     import torch
     dt = _dtype_name(w)
     c_out, c_in = w.shape
-    pw = _check("w", w, (c_out, c_in), _TORCH_NAMES[dt])
+    pw = _check("w", w, (c_out, c_in), w.dtype)
     codes = torch.empty(c_out, (c_in + 1) // 2, dtype=torch.uint8, device=w.device)
     scales = torch.empty(c_out, -(-c_in // group), dtype=w.dtype, device=w.device)
     rc = load_library().conv_w4_quantize(c_in, c_out, group, DTYPES[dt], pw, codes.data_ptr(), scales.data_ptr(),

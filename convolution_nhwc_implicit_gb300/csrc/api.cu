@@ -13,7 +13,9 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <mutex>
 #include <new>
+#include <vector>
 
 #include "conv_internal.h"
 
@@ -143,6 +145,29 @@ int conv_plan_bind_device(conv_plan *p, bool status_word) {
     if (!status_word) return CONV_OK;
     if (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess) return CONV_ERR_OOM;
     if (cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess) return CONV_ERR_CUDA;
+    return CONV_OK;
+}
+
+int conv_grant_smem_once(const void *k, int device, int need) {
+    // (the largest grant of each kernel and device; a grant lasts as long as the process)
+    struct Grant { const void *k; int device, bytes; };
+    static std::mutex mu;
+    static std::vector<Grant> done;
+    std::lock_guard<std::mutex> lock(mu);
+    for (const Grant &g : done)
+        if (g.k == k && g.device == device) return need <= g.bytes ? CONV_OK : CONV_ERR_UNSUPPORTED;
+    cudaFuncAttributes fa;
+    int optin = 0;
+    const int rc = conv_grant_smem(k, device, need);
+    if (rc != CONV_OK) return rc;
+    if (cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device) != cudaSuccess ||
+        cudaFuncGetAttributes(&fa, k) != cudaSuccess)
+        return CONV_ERR_CUDA;
+    try {
+        done.push_back({k, device, optin - (int)fa.sharedSizeBytes});
+    } catch (...) {
+        return CONV_ERR_OOM;
+    }
     return CONV_OK;
 }
 
@@ -418,7 +443,8 @@ const char *conv_plan_describe(const conv_plan_t *plan) { return plan ? plan->de
 int conv_plan_launches(const conv_plan_t *plan) {
     if (!plan) return CONV_ERR_NULL_ARG;
     if (plan->s.n == 0) return 0;
-    if (plan->algo == CONV_ALGO_GROUPNORM) return 2;  // either direction
+    if (plan->algo == CONV_ALGO_GROUPNORM)  // the forward run
+        return plan->gn.fwd.K > 0 ? 1 : 2 * ((plan->s.n + plan->gn.fwd.step - 1) / plan->gn.fwd.step);
     // (the forward run; its gradient takes two launches a piece of the classes, and more for joined sums)
     if (plan->algo == CONV_ALGO_XENT) return plan->xent.dp == plan->s.c_in ? 2 : 4;
     return (plan->algo == CONV_ALGO_IGEMM && plan->ig.prep) ? 2 : 1;
@@ -427,6 +453,12 @@ int conv_plan_launches(const conv_plan_t *plan) {
 int conv_plan_workspace(const conv_plan_t *plan, size_t *bytes) {
     if (!plan || !bytes) return CONV_ERR_NULL_ARG;
     *bytes = plan->ws_bytes;
+    return CONV_OK;
+}
+
+int conv_plan_workspace_bwd(const conv_plan_t *plan, size_t *bytes) {
+    if (!plan || !bytes) return CONV_ERR_NULL_ARG;
+    *bytes = plan->ws_bwd_bytes;
     return CONV_OK;
 }
 

@@ -72,10 +72,16 @@ struct DwpwGeom {
     int smem;          // dynamic shared memory bytes
 };
 
-// Group norm: every image's pixels in S runs of ppx.
+// Group norm.  Each direction: resident in a cluster's shared memory (K > 0: K
+// CTAs an image, runs of rppx pixels, gb groups = cb channels a CTA, NI images a
+// cluster), or in two launches over `step` images a pass (S runs of ppx
+// pixels an image).
 struct GnGeom {
     float eps;
-    int S, ppx;
+    struct Dir {
+        int S, ppx, step;
+        int K, rppx, gb, cb, NI;
+    } fwd, bwd;
 };
 
 // 4-bit pointwise layer: scale groups, runs of 128 input channels, and blocks
@@ -118,7 +124,7 @@ struct conv_plan {
     GnGeom gn;
     W4Geom w4;
     XentGeom xent;
-    size_t ws_bytes;   // device scratch a run takes from the caller (conv_plan_workspace)
+    size_t ws_bytes, ws_bwd_bytes;  // device scratch a run (its gradient) takes from the caller
     char desc[192];
 };
 
@@ -191,3 +197,6 @@ int conv_check_run_pointers(conv_dtype_t dtype, const conv_shape_t *s, int group
 // per-kernel permission shared by all plans, so it is never lowered to one
 // plan's size.  Returns a CONV_* status.
 int conv_grant_smem(const void *k, int device, int need);
+// The same, remembered per kernel and device: three CUDA calls the first time,
+// none after (for entry points that choose their kernel at each run).
+int conv_grant_smem_once(const void *k, int device, int need);

@@ -17,10 +17,10 @@
 // that end inside a vector, and channels meet their group only when the CTA's
 // sums are joined.  A CTA takes a run of whole pixels, one piece of memory.
 //
-// Variance: each thread sums (x - K) and (x - K)^2 about its own first value K
-// and the pieces are joined by Chan's update (count, mean, M2).  K belongs to
-// the values it is subtracted from, so the cancellation in M2 = q - s^2/n is
-// bounded by the thread's own count (at most a few hundred) times 2^-24
+// Variance: a CTA sums (x - K) and (x - K)^2 of each channel about the first
+// value K of its own run, and (mean, M2) of channels and runs are joined by
+// Chan's update.  K belongs to the values it is subtracted from, so that the
+// cancellation in M2 = q - s^2/n is bounded by the run's length times 2^-24
 // however far the mean lies from zero.  All statistics are fp32, in a fixed
 // order: results do not change from run to run.
 #include <cuda_bf16.h>
@@ -32,6 +32,7 @@
 
 #include "conv_internal.h"
 #include "epilogue.cuh"
+#include "tc_ptx.cuh"
 
 using namespace convk;
 
@@ -39,47 +40,48 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr long long kL2Bytes = 64ll << 20;  // of an input that two launches share
+constexpr int kStageRuns = 4096;            // partial results a CTA stages (32 KB)
+constexpr int kResident = 88 * 1024;        // map bytes of a resident CTA (two a SM)
 constexpr int kMaxC = 8192;  // channels: their sums stay in shared memory (16 bytes each)
 
-// VEC consecutive channels of one pixel as fp32.
+// VEC consecutive channels of one pixel, as fp32 pairs (VEC = 1: the first
+// lane of one pair).
 template <typename T, int VEC> struct Vec;
 template <int VEC> struct Vec<float, VEC> {
     static_assert(VEC == 4 || VEC == 1, "");
+    static constexpr int kPairs = (VEC + 1) / 2;
     using Raw = typename std::conditional<VEC == 4, float4, float>::type;
-    __device__ static __forceinline__ void unpack(const Raw &r, float (&f)[VEC]) {
-        if constexpr (VEC == 4) { f[0] = r.x; f[1] = r.y; f[2] = r.z; f[3] = r.w; } else f[0] = r;
+    __device__ static __forceinline__ void unpack(const Raw &r, float2 (&f)[kPairs]) {
+        if constexpr (VEC == 4) { f[0] = make_float2(r.x, r.y); f[1] = make_float2(r.z, r.w); }
+        else f[0] = make_float2(r, 0.0f);
     }
-    __device__ static __forceinline__ Raw pack(const float (&f)[VEC]) {
-        if constexpr (VEC == 4) return make_float4(f[0], f[1], f[2], f[3]);
-        else return f[0];
+    __device__ static __forceinline__ Raw pack(const float2 (&f)[kPairs]) {
+        if constexpr (VEC == 4) return make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+        else return f[0].x;
     }
 };
 template <int VEC> struct Vec<__nv_bfloat16, VEC> {
     static_assert(VEC == 8 || VEC == 2 || VEC == 1, "");
+    static constexpr int kPairs = (VEC + 1) / 2;
     using Raw = typename std::conditional<VEC == 8, uint4,
                                           typename std::conditional<VEC == 2, uint32_t, uint16_t>::type>::type;
-    __device__ static __forceinline__ void two(uint32_t v, float &a, float &b) {
-        a = __uint_as_float(v << 16);
-        b = __uint_as_float(v & 0xffff0000u);
+    __device__ static __forceinline__ float2 two(uint32_t v) {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
     }
-    __device__ static __forceinline__ uint32_t pair(float a, float b) {
-        __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
+    __device__ static __forceinline__ uint32_t pair(float2 v) {
+        __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
         return *reinterpret_cast<uint32_t *>(&p);
     }
-    __device__ static __forceinline__ void unpack(const Raw &r, float (&f)[VEC]) {
-        if constexpr (VEC == 8) {
-            two(r.x, f[0], f[1]); two(r.y, f[2], f[3]); two(r.z, f[4], f[5]); two(r.w, f[6], f[7]);
-        } else if constexpr (VEC == 2) {
-            two(r, f[0], f[1]);
-        } else {
-            f[0] = __uint_as_float((uint32_t)r << 16);
-        }
+    __device__ static __forceinline__ void unpack(const Raw &r, float2 (&f)[kPairs]) {
+        if constexpr (VEC == 8) { f[0] = two(r.x); f[1] = two(r.y); f[2] = two(r.z); f[3] = two(r.w); }
+        else if constexpr (VEC == 2) f[0] = two(r);
+        else f[0] = make_float2(__uint_as_float((uint32_t)r << 16), 0.0f);
     }
-    __device__ static __forceinline__ Raw pack(const float (&f)[VEC]) {
-        if constexpr (VEC == 8)
-            return make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
-        else if constexpr (VEC == 2) return pair(f[0], f[1]);
-        else return __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+    __device__ static __forceinline__ Raw pack(const float2 (&f)[kPairs]) {
+        if constexpr (VEC == 8) return make_uint4(pair(f[0]), pair(f[1]), pair(f[2]), pair(f[3]));
+        else if constexpr (VEC == 2) return pair(f[0]);
+        else return __bfloat16_as_ushort(__float2bfloat16_rn(f[0].x));
     }
 };
 
@@ -90,34 +92,48 @@ struct GnArgs {
     const float *gamma, *beta; // [C] or null
     float *mean, *rstd;        // [N][G] (forward: may be null)
     float *dgamma, *dbeta;     // [C] or null
-    float2 *part;              // [N][S][G]: (mean, M2), or (sum gamma dz, sum gamma dz xhat)
+    float2 *part;              // [N][G][S]: (mean, M2), or (sum gamma dz, sum gamma dz xhat)
     float2 *partc;             // [N][S][C]: (sum dz, sum dz xhat)
-    int N, HW, C, G, cg, S, ppx;  // S runs of ppx pixels an image
+    int N, n0, HW, C, G, cg;   // a launch takes images n0, n0 + 1, ...
+    int S, ppx;                // S runs of ppx pixels an image
+    // resident kernels: groups and channels of a CTA, CTAs an image (a run of
+    // pixels each), images of a cluster (gradient)
+    int gb, cb, K, NI, ent;    // ent: entries of the threads' sums in shared memory
     float eps;
 };
 
-// The activation's value and its derivative.  fp32 maps take CUDA's accurate
-// expf and division; bf16 ones the fast forms, ~1e-6 relative, far below the
-// 2^-9 of their results.  With n = e^z, t = n (n + 2): Mish = z t / (t + 2),
-// Mish' = t / (t + 2) + z 4 n (1 + n) / (t + 2)^2, the exponent clamped at 20
-// where both have reached their limits z and 1 in fp32.
-template <int ACT, bool FAST>
-__device__ __forceinline__ float act_val(float z) {
-    if constexpr (ACT == ACT_RELU) return z < 0.0f ? 0.0f : z;  // (NaN stays NaN)
-    else if constexpr (ACT == ACT_MISH) return FAST ? mish_fast(z) : mish_f32(z);
-    else return z;
-}
-template <int ACT, bool FAST>
-__device__ __forceinline__ float act_grad(float z) {
-    if constexpr (ACT == ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+// act(z) of a pair.  bf16 maps: the layer epilogue's packed Mish.  fp32 maps:
+// z t / (t + 2) with n = e^z, t = n (n + 2), which cancels nowhere, on the
+// hardware's exp2 and reciprocal (~5e-7 relative); the exponent is clamped at
+// 20, where t / (t + 2) is 1 in fp32.  ReLU passes NaN on.
+template <int ACT, bool BF16>
+__device__ __forceinline__ float2 act2(float2 z) {
+    if constexpr (ACT == ACT_RELU) return make_float2(z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y);
+    else if constexpr (ACT == ACT_MISH && BF16) return mish2_fast(z);
     else if constexpr (ACT == ACT_MISH) {
-        const float zc = fminf(z, 20.0f);
-        const float n = FAST ? __expf(zc) : expf(zc);
-        const float t = n * (n + 2.0f);
-        const float r = FAST ? __fdividef(1.0f, t + 2.0f) : 1.0f / (t + 2.0f);
-        return r * (t + z * (4.0f * n * (1.0f + n)) * r);
-    } else return 1.0f;
+        const float2 e = mul2(make_float2(fminf(z.x, 20.0f), fminf(z.y, 20.0f)), make_float2(1.4426950408889634f, 1.4426950408889634f));
+        const float2 n = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+        const float2 t = mul2(n, add2(n, make_float2(2.0f, 2.0f)));
+        const float2 d = add2(t, make_float2(2.0f, 2.0f));
+        return mul2(z, mul2(t, make_float2(rcp_approx(d.x), rcp_approx(d.y))));
+    } else return z;
 }
+// act'(z) of a pair: with w = 1 + e^z, r = 1 / (w^2 + 1), Mish' = 1 - 2 r + z 4 e^z w r^2.
+template <int ACT>
+__device__ __forceinline__ float2 dact2(float2 z) {
+    if constexpr (ACT == ACT_RELU) return make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
+    else if constexpr (ACT == ACT_MISH) {
+        const float2 one = make_float2(1.0f, 1.0f);
+        const float2 e = mul2(make_float2(fminf(z.x, 20.0f), fminf(z.y, 20.0f)), make_float2(1.4426950408889634f, 1.4426950408889634f));
+        const float2 n = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+        const float2 w = add2(n, one);
+        const float2 d = fma2(w, w, one);
+        const float2 r = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+        const float2 nr = mul2(mul2(n, r), mul2(w, r));
+        return fma2(mul2(z, make_float2(4.0f, 4.0f)), nr, fma2(r, make_float2(-2.0f, -2.0f), one));
+    } else return make_float2(1.0f, 1.0f);
+}
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
 
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -125,8 +141,8 @@ __device__ __forceinline__ float warp_sum(float v) {
     return v;
 }
 
-// How a CTA's threads cover a pixel's channel vectors: with cvn vectors a
-// pixel, R = kThreads / cvn pixels side by side (R = 1 and several rounds
+// How a CTA's threads cover the channel vectors of its pixels: with cvn vectors
+// a pixel, R = kThreads / cvn pixels side by side (R = 1 and several rounds
 // where a pixel has more vectors than the CTA threads).
 struct Cover {
     int cvn, R, r, col;
@@ -141,19 +157,93 @@ struct Cover {
             on = r < R;
         }
     }
-    // pixels of the run of `np` that thread row q takes
-    __device__ __forceinline__ int count(int q, int np) const { return np > q ? (np - q + R - 1) / R : 0; }
 };
+
+// The threads' pairs of sums, ent[r * C + c], summed over the R rows: channel c
+// into chan[c] (which may be ent itself only for R = 1).  L lanes a channel.
+// Every thread of the CTA calls it after a barrier; ends without one.
+template <typename F>
+__device__ __forceinline__ void join_rows(const float2 *ent, int R, int C, F &&done) {
+    int L = 1;
+    while (L < 32 && L * 2 * C <= kThreads && L < R) L *= 2;
+    const int per = kThreads / L, sub = threadIdx.x % L;
+    for (int c0 = 0; c0 < C; c0 += per) {
+        const int c = c0 + threadIdx.x / L;
+        float2 v = make_float2(0.0f, 0.0f);
+        if (c < C)
+            for (int r = sub; r < R; r += L) v = add2(v, ent[r * C + c]);
+        for (int o = L / 2; o > 0; o >>= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        }
+        if (c < C && sub == 0) done(c, v);
+    }
+}
+
+// (mean, M2) of a group from its channels' (mean, M2), each of `cnt` values;
+// every lane of the calling warp returns it.
+__device__ __forceinline__ float2 join_channels(const float2 *chan, int cg, float cnt, int lane) {
+    float sum = 0.0f;
+    for (int c = lane; c < cg; c += 32) sum += chan[c].x;
+    const float mu = warp_sum(sum) / (float)cg;
+    float m2 = 0.0f;
+    for (int c = lane; c < cg; c += 32) {
+        const float d = chan[c].x - mu;
+        m2 += fmaf(cnt * d, d, chan[c].y);
+    }
+    return make_float2(mu, warp_sum(m2));
+}
+
+// A thread's sums of (x - K) and (x - K)^2 over its pixels of one run, K the
+// run's first pixel.
+template <typename T, int VEC>
+struct StatSums {
+    using V = Vec<T, VEC>;
+    float2 K[V::kPairs], s1[V::kPairs], s2[V::kPairs];
+    __device__ __forceinline__ void start(const typename V::Raw &first) {
+        V::unpack(first, K);
+#pragma unroll
+        for (int e = 0; e < V::kPairs; ++e) {
+            K[e] = neg2(K[e]);
+            s1[e] = s2[e] = make_float2(0.0f, 0.0f);
+        }
+    }
+    __device__ __forceinline__ void take(const typename V::Raw &raw) {
+        float2 f[V::kPairs];
+        V::unpack(raw, f);
+#pragma unroll
+        for (int e = 0; e < V::kPairs; ++e) {
+            const float2 d = add2(f[e], K[e]);
+            s1[e] = add2(s1[e], d);
+            s2[e] = fma2(d, d, s2[e]);
+        }
+    }
+    // ent: this thread's row of sums; piv: the channels' K
+    __device__ __forceinline__ void put(float2 *ent, float *piv, bool first_row) const {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float2 a = s1[e / 2], b = s2[e / 2];
+            ent[e] = e % 2 ? make_float2(a.y, b.y) : make_float2(a.x, b.x);
+            if (first_row) piv[e] = -(e % 2 ? K[e / 2].y : K[e / 2].x);
+        }
+    }
+};
+// A channel's (mean, M2) from its sums about K over cnt values.
+__device__ __forceinline__ float2 about(float K, float2 s, float cnt) {
+    const float d = s.x / cnt;
+    return make_float2(K + d, fmaxf(s.y - s.x * d, 0.0f) + 0.0f * s.y);  // (NaN stays NaN)
+}
 
 // (mean, M2) of each group over this CTA's run of pixels.
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads) gn_stats_kernel(GnArgs a) {
     using V = Vec<T, VEC>;
-    extern __shared__ float sh[];  // mean[R*C], M2[R*C], then 3 floats a warp
+    using Raw = typename V::Raw;
+    extern __shared__ float2 sh2[];  // [R*C] sums, [C] channels, then [C] K
     const Cover cv(a.C, VEC);
-    const int entries = cv.R * a.C;
-    float *smean = sh, *sm2 = sh + entries, *swarp = sm2 + entries;
-    const int n = blockIdx.y, s = blockIdx.x;
+    float2 *ent = sh2, *chan = ent + cv.R * a.C;
+    float *piv = reinterpret_cast<float *>(chan + a.C);
+    const int n = a.n0 + blockIdx.y, s = blockIdx.x;
     const int p0 = s * a.ppx, np = min(a.ppx, a.HW - p0);
     pdl_trigger();
     pdl_wait();
@@ -161,98 +251,54 @@ __global__ void __launch_bounds__(kThreads) gn_stats_kernel(GnArgs a) {
     if (cv.on) {
         for (int col = cv.col; col < cv.cvn; col += kThreads) {
             const T *xc = x + col * VEC;
-            float K[VEC], s1[VEC], s2[VEC];
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) K[e] = s1[e] = s2[e] = 0.0f;
-            if (cv.r < np) V::unpack(*reinterpret_cast<const typename V::Raw *>(xc + cv.r * a.px), K);
+            StatSums<T, VEC> st;
+            st.start(*reinterpret_cast<const Raw *>(xc));
             constexpr int U = 4;
-            for (int p = cv.r; p < np; p += cv.R * U) {
-                typename V::Raw raw[U];
+            int p = cv.r;
+            for (; p + (U - 1) * cv.R < np; p += cv.R * U) {
+                Raw raw[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (p + u * cv.R < np) raw[u] = *reinterpret_cast<const typename V::Raw *>(xc + (p + u * cv.R) * a.px);
+                for (int u = 0; u < U; ++u) raw[u] = *reinterpret_cast<const Raw *>(xc + (p + u * cv.R) * a.px);
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (p + u * cv.R < np) {
-                        float f[VEC];
-                        V::unpack(raw[u], f);
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const float d = f[e] - K[e];
-                            s1[e] += d;
-                            s2[e] = fmaf(d, d, s2[e]);
-                        }
-                    }
+                for (int u = 0; u < U; ++u) st.take(raw[u]);
             }
-            const int cnt = cv.count(cv.r, np);
-            const float inv = cnt > 0 ? 1.0f / (float)cnt : 0.0f;
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int i = cv.r * a.C + col * VEC + e;
-                const float d = s1[e] * inv;
-                smean[i] = K[e] + d;
-                sm2[i] = s2[e] - s1[e] * d;
-            }
+            for (; p < np; p += cv.R) st.take(*reinterpret_cast<const Raw *>(xc + p * a.px));
+            st.put(ent + cv.r * a.C + col * VEC, piv + col * VEC, cv.r == 0);
         }
     }
     __syncthreads();
-    // Join: wpg warps a group, each an interleaved share of its R * cg
-    // entries; then one thread a group over the warps' results.
+    join_rows(ent, cv.R, a.C, [&](int c, float2 v) { chan[c] = about(piv[c], v, (float)np); });
+    __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int wpg = 1;
-    while (wpg * 2 * a.G <= kWarps) wpg *= 2;
-    const int per = cv.R * a.cg;
-    for (int g0 = 0; g0 < a.G; g0 += kWarps / wpg) {
-        const int g = g0 + warp / wpg, part = warp % wpg;
-        if (g < a.G) {
-            float cnt = 0.0f, sum = 0.0f;
-            for (int i = part * 32 + lane; i < per; i += wpg * 32) {
-                const int r = i / a.cg, c = g * a.cg + (i - r * a.cg);
-                const float nr = (float)cv.count(r, np);
-                cnt += nr;
-                if (nr > 0.0f) sum += nr * smean[r * a.C + c];
-            }
-            cnt = warp_sum(cnt);
-            sum = warp_sum(sum);
-            const float mu = cnt > 0.0f ? sum / cnt : 0.0f;
-            float m2 = 0.0f;
-            for (int i = part * 32 + lane; i < per; i += wpg * 32) {
-                const int r = i / a.cg, c = g * a.cg + (i - r * a.cg);
-                const float nr = (float)cv.count(r, np);
-                if (nr > 0.0f) {
-                    const float d = smean[r * a.C + c] - mu;
-                    m2 += sm2[r * a.C + c] + nr * d * d;
-                }
-            }
-            m2 = warp_sum(m2);
-            if (lane == 0) { swarp[warp * 3] = cnt; swarp[warp * 3 + 1] = mu; swarp[warp * 3 + 2] = m2; }
-        }
-        __syncthreads();
-        if (g < a.G && part == 0 && lane == 0) {
-            float cnt = 0.0f, sum = 0.0f, m2 = 0.0f;
-            for (int q = 0; q < wpg; ++q) { cnt += swarp[(warp + q) * 3]; sum += swarp[(warp + q) * 3] * swarp[(warp + q) * 3 + 1]; }
-            const float mu = sum / cnt;
-            for (int q = 0; q < wpg; ++q) {
-                const float nq = swarp[(warp + q) * 3], d = swarp[(warp + q) * 3 + 1] - mu;
-                if (nq > 0.0f) m2 += swarp[(warp + q) * 3 + 2] + nq * d * d;
-            }
-            a.part[((long long)n * a.S + s) * a.G + g] = make_float2(mu, m2);
-        }
-        __syncthreads();
+    for (int g = warp; g < a.G; g += kWarps) {
+        const float2 v = join_channels(chan + g * a.cg, a.cg, (float)np, lane);
+        if (lane == 0) a.part[((long long)n * a.G + g) * a.S + s] = v;
     }
 }
 
-// mean and rstd of group g of image n from the S runs' (mean, M2); every lane
-// of a warp returns them.
-__device__ __forceinline__ float2 join_stats(const GnArgs &a, int n, int g, int lane) {
-    const float2 *p = a.part + (long long)n * a.S * a.G + g;
+// The [G][S] partial results of image n, in shared memory if they fit: every
+// load of the CTA is then in flight together, where group by group each would
+// wait for L2.  Ends with a barrier.
+__device__ __forceinline__ const float2 *stage_runs(const GnArgs &a, int n, float2 *dst) {
+    const float2 *src = a.part + (long long)n * a.G * a.S;
+    const int total = a.G * a.S;
+    if (total > kStageRuns) return src;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < total; i += kThreads) dst[i] = src[i];
+    __syncthreads();
+    return dst;
+}
+
+// mean and rstd of a group of m values from the (mean, M2) of its S runs; every
+// lane of the calling warp returns them.
+__device__ __forceinline__ float2 join_runs(const GnArgs &a, const float2 *p, int lane) {
     const float inv = 1.0f / ((float)a.HW * (float)a.cg);
     float sum = 0.0f;
-    for (int s = lane; s < a.S; s += 32) sum += (float)min(a.ppx, a.HW - s * a.ppx) * (float)a.cg * p[(long long)s * a.G].x;
+    for (int s = lane; s < a.S; s += 32) sum += (float)min(a.ppx, a.HW - s * a.ppx) * (float)a.cg * p[s].x;
     const float mu = warp_sum(sum) * inv;
     float m2 = 0.0f;
     for (int s = lane; s < a.S; s += 32) {
-        const float2 v = p[(long long)s * a.G];
+        const float2 v = p[s];
         const float d = v.x - mu;
         m2 += v.y + (float)min(a.ppx, a.HW - s * a.ppx) * (float)a.cg * d * d;
     }
@@ -260,21 +306,32 @@ __device__ __forceinline__ float2 join_stats(const GnArgs &a, int n, int g, int 
     return make_float2(mu, 1.0f / sqrtf(m2 * inv + a.eps));
 }
 
-// y = act(gamma (x - mean) rstd + beta) over one run of pixels.
+// What a thread's channels need of the forward formula.
+template <int VEC, int PAIRS>
+__device__ __forceinline__ void set_lane(float2 (&v)[PAIRS], int e, float f) {
+    if (e % 2) v[e / 2].y = f; else v[e / 2].x = f;
+    if (VEC == 1) v[0].y = 0.0f;
+}
+
+// y = act(gamma (x - mean) rstd + beta) over one run of pixels.  The runs are
+// taken in the order opposite to the statistics': of maps larger than L2 the
+// last runs read are still there.
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads) gn_apply_kernel(GnArgs a) {
     using V = Vec<T, VEC>;
-    constexpr bool kFast = sizeof(T) == 2;
-    extern __shared__ float sh[];  // [G] (mean, rstd)
-    float2 *stat = reinterpret_cast<float2 *>(sh);
+    using Raw = typename V::Raw;
+    constexpr int P = V::kPairs;
+    extern __shared__ float2 sh2[];  // [G] (mean, rstd), then [G][S]
+    float2 *stat = sh2;
     const Cover cv(a.C, VEC);
-    const int n = blockIdx.y, s = blockIdx.x;
+    const int n = a.n0 + (int)(gridDim.y - 1 - blockIdx.y), s = (int)(gridDim.x - 1 - blockIdx.x);
     const int p0 = s * a.ppx, np = min(a.ppx, a.HW - p0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
+    const float2 *runs = stage_runs(a, n, sh2 + a.G);
     for (int g = warp; g < a.G; g += kWarps) {
-        const float2 st = join_stats(a, n, g, lane);
+        const float2 st = join_runs(a, runs + g * a.S, lane);
         if (lane == 0) {
             stat[g] = st;
             if (s == 0) {
@@ -288,46 +345,93 @@ __global__ void __launch_bounds__(kThreads) gn_apply_kernel(GnArgs a) {
     const T *x = static_cast<const T *>(a.x) + ((long long)n * a.HW + p0) * a.px;
     T *y = static_cast<T *>(a.out) + ((long long)n * a.HW + p0) * a.pout;
     for (int col = cv.col; col < cv.cvn; col += kThreads) {
-        float mu[VEC], sc[VEC], be[VEC];
+        float2 mu[P], sc[P], be[P];  // mu: minus the mean
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const int c = col * VEC + e;
             const float2 st = stat[c / a.cg];
-            mu[e] = st.x;
-            sc[e] = st.y * (a.gamma ? a.gamma[c] : 1.0f);
-            be[e] = a.beta ? a.beta[c] : 0.0f;
+            set_lane<VEC>(mu, e, -st.x);
+            set_lane<VEC>(sc, e, st.y * (a.gamma ? a.gamma[c] : 1.0f));
+            set_lane<VEC>(be, e, a.beta ? a.beta[c] : 0.0f);
         }
+        auto one = [&](const Raw &raw, int p) {
+            float2 f[P];
+            V::unpack(raw, f);
+#pragma unroll
+            for (int e = 0; e < P; ++e) f[e] = act2<ACT, sizeof(T) == 2>(fma2(add2(f[e], mu[e]), sc[e], be[e]));
+            *reinterpret_cast<Raw *>(y + p * a.pout + col * VEC) = V::pack(f);
+        };
         constexpr int U = 4;
-        for (int p = cv.r; p < np; p += cv.R * U) {
-            typename V::Raw raw[U];
+        int p = cv.r;
+        for (; p + (U - 1) * cv.R < np; p += cv.R * U) {
+            Raw raw[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (p + u * cv.R < np)
-                    raw[u] = *reinterpret_cast<const typename V::Raw *>(x + (p + u * cv.R) * a.px + col * VEC);
+            for (int u = 0; u < U; ++u) raw[u] = *reinterpret_cast<const Raw *>(x + (p + u * cv.R) * a.px + col * VEC);
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (p + u * cv.R < np) {
-                    float f[VEC];
-                    V::unpack(raw[u], f);
+            for (int u = 0; u < U; ++u) one(raw[u], p + u * cv.R);
+        }
+        for (; p < np; p += cv.R) one(*reinterpret_cast<const Raw *>(x + p * a.px + col * VEC), p);
+    }
+}
+
+// A thread's per-channel values of the gradient: xhat = x rs + mr, z = xhat ga + be.
+template <typename T, int VEC, int ACT>
+struct GradLane {
+    using V = Vec<T, VEC>;
+    using Raw = typename V::Raw;
+    static constexpr int P = V::kPairs;
+    float2 mu[P], rs[P], ga[P], be[P];  // mu: minus the mean
+    __device__ __forceinline__ void set(const GnArgs &a, int e, int c, float mean, float rstd) {
+        set_lane<VEC>(mu, e, -mean);
+        set_lane<VEC>(rs, e, rstd);
+        set_lane<VEC>(ga, e, a.gamma ? a.gamma[c] : 1.0f);
+        set_lane<VEC>(be, e, a.beta ? a.beta[c] : 0.0f);
+    }
+    __device__ __forceinline__ void eval(const Raw &rx, const Raw &rd, float2 (&xh)[P], float2 (&dz)[P]) const {
+        V::unpack(rx, xh);
+        V::unpack(rd, dz);
 #pragma unroll
-                    for (int e = 0; e < VEC; ++e) f[e] = act_val<ACT, kFast>(fmaf(f[e] - mu[e], sc[e], be[e]));
-                    *reinterpret_cast<typename V::Raw *>(y + (p + u * cv.R) * a.pout + col * VEC) = V::pack(f);
-                }
+        for (int e = 0; e < P; ++e) {
+            xh[e] = mul2(add2(xh[e], mu[e]), rs[e]);
+            if (ACT != ACT_NONE) dz[e] = mul2(dz[e], dact2<ACT>(fma2(xh[e], ga[e], be[e])));
         }
     }
+    // A += dz, B += dz xhat
+    __device__ __forceinline__ void sums(const Raw &rx, const Raw &rd, float2 (&A)[P], float2 (&B)[P]) const {
+        float2 xh[P], dz[P];
+        eval(rx, rd, xh, dz);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            A[e] = add2(A[e], dz[e]);
+            B[e] = fma2(dz[e], xh[e], B[e]);
+        }
+    }
+    // rstd (gamma dz - m1 - xhat m2), nm1 and nm2 the negated means
+    __device__ __forceinline__ Raw dx(const Raw &rx, const Raw &rd, const float2 (&nm1)[P], const float2 (&nm2)[P]) const {
+        float2 xh[P], dz[P];
+        eval(rx, rd, xh, dz);
+#pragma unroll
+        for (int e = 0; e < P; ++e) xh[e] = mul2(rs[e], fma2(xh[e], nm2[e], fma2(ga[e], dz[e], nm1[e])));
+        return V::pack(xh);
+    }
+};
+template <int VEC, int P>
+__device__ __forceinline__ void put_sums(float2 *ent, const float2 (&A)[P], const float2 (&B)[P]) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) ent[e] = e % 2 ? make_float2(A[e / 2].y, B[e / 2].y) : make_float2(A[e / 2].x, B[e / 2].x);
 }
 
 // Sums of dz and dz xhat per channel, and of gamma times them per group, over
 // one run of pixels.
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(GnArgs a) {
-    using V = Vec<T, VEC>;
-    constexpr bool kFast = sizeof(T) == 2;
-    extern __shared__ float sh[];  // [R*C] float2, then [C] float2
+    using L = GradLane<T, VEC, ACT>;
+    using Raw = typename L::Raw;
+    constexpr int P = L::P;
+    extern __shared__ float2 sh2[];  // [R*C], then [C]
     const Cover cv(a.C, VEC);
-    float2 *ent = reinterpret_cast<float2 *>(sh);
-    float2 *chan = ent + cv.R * a.C;
-    const int n = blockIdx.y, s = blockIdx.x;
+    float2 *ent = sh2, *chan = ent + cv.R * a.C;
+    const int n = a.n0 + blockIdx.y, s = blockIdx.x;
     const int p0 = s * a.ppx, np = min(a.ppx, a.HW - p0);
     pdl_trigger();
     pdl_wait();
@@ -335,134 +439,107 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(GnArgs a) {
     const T *dy = static_cast<const T *>(a.dy) + ((long long)n * a.HW + p0) * a.pdy;
     if (cv.on) {
         for (int col = cv.col; col < cv.cvn; col += kThreads) {
-            float mu[VEC], rs[VEC], ga[VEC], be[VEC], A[VEC], B[VEC];
+            L ln;
+            float2 A[P], B[P];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const int c = col * VEC + e;
                 const long long g = (long long)n * a.G + c / a.cg;
-                mu[e] = a.mean[g];
-                rs[e] = a.rstd[g];
-                ga[e] = a.gamma ? a.gamma[c] : 1.0f;
-                be[e] = a.beta ? a.beta[c] : 0.0f;
-                A[e] = B[e] = 0.0f;
+                ln.set(a, e, c, a.mean[g], a.rstd[g]);
             }
+#pragma unroll
+            for (int e = 0; e < P; ++e) A[e] = B[e] = make_float2(0.0f, 0.0f);
             constexpr int U = 2;
-            for (int p = cv.r; p < np; p += cv.R * U) {
-                typename V::Raw rx[U], rd[U];
+            int p = cv.r;
+            for (; p + (U - 1) * cv.R < np; p += cv.R * U) {
+                Raw rx[U], rd[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (p + u * cv.R < np) {
-                        rx[u] = *reinterpret_cast<const typename V::Raw *>(x + (p + u * cv.R) * a.px + col * VEC);
-                        rd[u] = *reinterpret_cast<const typename V::Raw *>(dy + (p + u * cv.R) * a.pdy + col * VEC);
-                    }
+                for (int u = 0; u < U; ++u) {
+                    rx[u] = *reinterpret_cast<const Raw *>(x + (p + u * cv.R) * a.px + col * VEC);
+                    rd[u] = *reinterpret_cast<const Raw *>(dy + (p + u * cv.R) * a.pdy + col * VEC);
+                }
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (p + u * cv.R < np) {
-                        float f[VEC], d[VEC];
-                        V::unpack(rx[u], f);
-                        V::unpack(rd[u], d);
-#pragma unroll
-                        for (int e = 0; e < VEC; ++e) {
-                            const float xh = (f[e] - mu[e]) * rs[e];
-                            const float dz = d[e] * act_grad<ACT, kFast>(fmaf(xh, ga[e], be[e]));
-                            A[e] += dz;
-                            B[e] = fmaf(dz, xh, B[e]);
-                        }
-                    }
+                for (int u = 0; u < U; ++u) ln.sums(rx[u], rd[u], A, B);
             }
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) ent[cv.r * a.C + col * VEC + e] = make_float2(A[e], B[e]);
+            for (; p < np; p += cv.R)
+                ln.sums(*reinterpret_cast<const Raw *>(x + p * a.px + col * VEC),
+                        *reinterpret_cast<const Raw *>(dy + p * a.pdy + col * VEC), A, B);
+            put_sums<VEC>(ent + cv.r * a.C + col * VEC, A, B);
         }
     }
     __syncthreads();
-    // channels over the R rows: L lanes a channel
-    int L = 1;
-    while (L < 32 && L * 2 * a.C <= kThreads) L *= 2;
-    const int per = kThreads / L, sub = threadIdx.x % L;
-    for (int c0 = 0; c0 < a.C; c0 += per) {
-        const int c = c0 + threadIdx.x / L;
-        float A = 0.0f, B = 0.0f;
-        if (c < a.C)
-            for (int r = sub; r < cv.R; r += L) {
-                const float2 v = ent[r * a.C + c];
-                A += v.x;
-                B += v.y;
-            }
-        for (int o = L / 2; o > 0; o >>= 1) {
-            A += __shfl_xor_sync(0xffffffffu, A, o);
-            B += __shfl_xor_sync(0xffffffffu, B, o);
-        }
-        if (c < a.C && sub == 0) {
-            a.partc[((long long)n * a.S + s) * a.C + c] = make_float2(A, B);
-            const float ga = a.gamma ? a.gamma[c] : 1.0f;
-            chan[c] = make_float2(ga * A, ga * B);
-        }
-    }
+    float2 *pc = a.partc + ((long long)n * a.S + s) * a.C;
+    join_rows(ent, cv.R, a.C, [&](int c, float2 v) {
+        pc[c] = v;
+        const float ga = a.gamma ? a.gamma[c] : 1.0f;
+        chan[c] = make_float2(ga * v.x, ga * v.y);
+    });
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int g = warp; g < a.G; g += kWarps) {
-        float A = 0.0f, B = 0.0f;
-        for (int c = lane; c < a.cg; c += 32) {
-            const float2 v = chan[g * a.cg + c];
-            A += v.x;
-            B += v.y;
-        }
-        A = warp_sum(A);
-        B = warp_sum(B);
-        if (lane == 0) a.part[((long long)n * a.S + s) * a.G + g] = make_float2(A, B);
+        float2 v = make_float2(0.0f, 0.0f);
+        for (int c = lane; c < a.cg; c += 32) v = add2(v, chan[g * a.cg + c]);
+        v.x = warp_sum(v.x);
+        v.y = warp_sum(v.y);
+        if (lane == 0) a.part[((long long)n * a.G + g) * a.S + s] = v;
     }
 }
 
-// dx over one run of pixels (grid rows 1..N); grid row 0 joins the channels'
-// sums of every image and run into dgamma and dbeta, 32 channels a CTA.
+// dgamma and dbeta from `rows` rows of channel sums, 32 channels a CTA.
+__device__ __forceinline__ void join_rows_of_channels(const GnArgs &a, long long rows, int block, int blocks, float2 *red) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int c0 = block * 32; c0 < a.C; c0 += blocks * 32) {
+        const int c = c0 + lane;
+        float2 v = make_float2(0.0f, 0.0f);
+        if (c < a.C) {
+            long long r = warp;
+            for (; r + 3 * kWarps < rows; r += 4 * kWarps) {
+                float2 t[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) t[u] = a.partc[(r + u * kWarps) * a.C + c];
+                v = add2(v, add2(add2(t[0], t[1]), add2(t[2], t[3])));
+            }
+            for (; r < rows; r += kWarps) v = add2(v, a.partc[r * a.C + c]);
+        }
+        red[warp * 32 + lane] = v;
+        __syncthreads();
+        if (warp == 0 && c < a.C) {
+            for (int q = 1; q < kWarps; ++q) v = add2(v, red[q * 32 + lane]);
+            if (a.dbeta) a.dbeta[c] = v.x;
+            if (a.dgamma) a.dgamma[c] = v.y;
+        }
+        __syncthreads();
+    }
+}
+// dx over one run of pixels (grid rows past the first `head`); the first
+// `head` (0 or 1) grid rows join the channels' sums of every image and run into
+// dgamma and dbeta, 32 channels a CTA.
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(GnArgs a) {
-    using V = Vec<T, VEC>;
-    constexpr bool kFast = sizeof(T) == 2;
-    extern __shared__ float sh[];  // [G] (s1, s2) / m, or [kWarps][32] float2
+__global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(GnArgs a, int head) {
+    using L = GradLane<T, VEC, ACT>;
+    using Raw = typename L::Raw;
+    constexpr int P = L::P;
+    extern __shared__ float2 sh2[];  // [G] minus (s1, s2) / m and [G][S], or [kWarps][32]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    if (blockIdx.y == 0) {
-        if (!a.dgamma && !a.dbeta) return;
-        float2 *red = reinterpret_cast<float2 *>(sh);
-        const long long rows = (long long)a.N * a.S;
-        for (int c0 = blockIdx.x * 32; c0 < a.C; c0 += gridDim.x * 32) {
-            const int c = c0 + lane;
-            float A = 0.0f, B = 0.0f;
-            if (c < a.C)
-                for (long long r = warp; r < rows; r += kWarps) {
-                    const float2 v = a.partc[r * a.C + c];
-                    A += v.x;
-                    B += v.y;
-                }
-            red[warp * 32 + lane] = make_float2(A, B);
-            __syncthreads();
-            if (warp == 0 && c < a.C) {
-                for (int q = 1; q < kWarps; ++q) { A += red[q * 32 + lane].x; B += red[q * 32 + lane].y; }
-                if (a.dbeta) a.dbeta[c] = A;
-                if (a.dgamma) a.dgamma[c] = B;
-            }
-            __syncthreads();
-        }
+    if ((int)blockIdx.y < head) {
+        join_rows_of_channels(a, (long long)a.N * a.S, blockIdx.x, gridDim.x, sh2);
         return;
     }
-    float2 *sum = reinterpret_cast<float2 *>(sh);
+    float2 *sum = sh2;
     const Cover cv(a.C, VEC);
-    const int n = blockIdx.y - 1, s = blockIdx.x;
+    const int n = a.n0 + (int)(gridDim.y - 1 - blockIdx.y), s = (int)(gridDim.x - 1 - blockIdx.x);
     const int p0 = s * a.ppx, np = min(a.ppx, a.HW - p0);
-    const float inv = 1.0f / ((float)a.HW * (float)a.cg);
+    const float inv = -1.0f / ((float)a.HW * (float)a.cg);
+    const float2 *runs = stage_runs(a, n, sh2 + a.G);
     for (int g = warp; g < a.G; g += kWarps) {
-        const float2 *p = a.part + (long long)n * a.S * a.G + g;
-        float A = 0.0f, B = 0.0f;
-        for (int q = lane; q < a.S; q += 32) {
-            const float2 v = p[(long long)q * a.G];
-            A += v.x;
-            B += v.y;
-        }
-        A = warp_sum(A);
-        B = warp_sum(B);
-        if (lane == 0) sum[g] = make_float2(A * inv, B * inv);
+        const float2 *p = runs + g * a.S;
+        float2 v = make_float2(0.0f, 0.0f);
+        for (int q = lane; q < a.S; q += 32) v = add2(v, p[q]);
+        v.x = warp_sum(v.x);
+        v.y = warp_sum(v.y);
+        if (lane == 0) sum[g] = make_float2(v.x * inv, v.y * inv);
     }
     __syncthreads();
     if (!cv.on) return;
@@ -470,46 +547,338 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(GnArgs a) {
     const T *dy = static_cast<const T *>(a.dy) + ((long long)n * a.HW + p0) * a.pdy;
     T *dx = static_cast<T *>(a.out) + ((long long)n * a.HW + p0) * a.pout;
     for (int col = cv.col; col < cv.cvn; col += kThreads) {
-        float mu[VEC], rs[VEC], ga[VEC], be[VEC], m1[VEC], m2[VEC];
+        L ln;
+        float2 m1[P], m2[P];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const int c = col * VEC + e, g = c / a.cg;
-            mu[e] = a.mean[(long long)n * a.G + g];
-            rs[e] = a.rstd[(long long)n * a.G + g];
-            ga[e] = a.gamma ? a.gamma[c] : 1.0f;
-            be[e] = a.beta ? a.beta[c] : 0.0f;
-            m1[e] = sum[g].x;
-            m2[e] = sum[g].y;
+            ln.set(a, e, c, a.mean[(long long)n * a.G + g], a.rstd[(long long)n * a.G + g]);
+            set_lane<VEC>(m1, e, sum[g].x);
+            set_lane<VEC>(m2, e, sum[g].y);
         }
         constexpr int U = 2;
-        for (int p = cv.r; p < np; p += cv.R * U) {
-            typename V::Raw rx[U], rd[U];
+        int p = cv.r;
+        for (; p + (U - 1) * cv.R < np; p += cv.R * U) {
+            Raw rx[U], rd[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                rx[u] = *reinterpret_cast<const Raw *>(x + (p + u * cv.R) * a.px + col * VEC);
+                rd[u] = *reinterpret_cast<const Raw *>(dy + (p + u * cv.R) * a.pdy + col * VEC);
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (p + u * cv.R < np) {
-                    rx[u] = *reinterpret_cast<const typename V::Raw *>(x + (p + u * cv.R) * a.px + col * VEC);
-                    rd[u] = *reinterpret_cast<const typename V::Raw *>(dy + (p + u * cv.R) * a.pdy + col * VEC);
-                }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (p + u * cv.R < np) {
-                    float f[VEC], d[VEC];
-                    V::unpack(rx[u], f);
-                    V::unpack(rd[u], d);
-#pragma unroll
-                    for (int e = 0; e < VEC; ++e) {
-                        const float xh = (f[e] - mu[e]) * rs[e];
-                        const float dz = d[e] * act_grad<ACT, kFast>(fmaf(xh, ga[e], be[e]));
-                        f[e] = rs[e] * (fmaf(ga[e], dz, -m1[e]) - xh * m2[e]);
-                    }
-                    *reinterpret_cast<typename V::Raw *>(dx + (p + u * cv.R) * a.pout + col * VEC) = V::pack(f);
-                }
+                *reinterpret_cast<Raw *>(dx + (p + u * cv.R) * a.pout + col * VEC) = ln.dx(rx[u], rd[u], m1, m2);
         }
+        for (; p < np; p += cv.R)
+            *reinterpret_cast<Raw *>(dx + p * a.pout + col * VEC) =
+                ln.dx(*reinterpret_cast<const Raw *>(x + p * a.px + col * VEC),
+                      *reinterpret_cast<const Raw *>(dy + p * a.pdy + col * VEC), m1, m2);
     }
 }
 
+
+// ------------------------------------------------------------ resident kernels
+// Where a few groups of an image fit the shared memory of a cluster, one launch
+// does all: each CTA copies its run of pixels of gb groups to shared memory
+// (cp.async, the whole run in flight at once), sums it, exchanges the groups'
+// sums with the cluster's other CTAs (8 bytes a group, through distributed
+// shared memory) and finishes from shared memory: every byte crosses HBM and
+// L2 once, nothing goes through a workspace.  A thread reads back only what it
+// copied itself.
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ float2 ld_peer(const float2 *p, uint32_t rank) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(tc::mapa_shared(tc::smem_u32(p), rank)) : "memory");
+    return v;
+}
+// (every thread of the CTA, warps converged)
+__device__ __forceinline__ void cluster_arrive() { __syncwarp(); asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { __syncwarp(); asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// One vector global -> shared (two-byte vectors through a register).
+template <typename Raw>
+__device__ __forceinline__ void copy_vec(Raw *dst, const Raw *src) {
+    if constexpr (sizeof(Raw) >= 4) copy_async<(int)sizeof(Raw)>(tc::smem_u32(dst), src);
+    else *dst = *src;
+}
+
+// Rows that a CTA's sums leave in shared memory: one a warp where a warp's
+// lanes cover whole pixels (folded with shuffles first), else one a thread row.
+__host__ __device__ inline bool folds(int cvn) { return cvn <= 32 && (cvn & (cvn - 1)) == 0; }
+template <int P>
+__device__ __forceinline__ void fold(float2 (&v)[P], int cvn) {
+    for (int o = cvn; o < 32; o <<= 1)
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            v[e].x += __shfl_xor_sync(0xffffffffu, v[e].x, o);
+            v[e].y += __shfl_xor_sync(0xffffffffu, v[e].y, o);
+        }
+}
+
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kThreads, 2) gn_resident_kernel(GnArgs a) {
+    using V = Vec<T, VEC>;
+    using Raw = typename V::Raw;
+    constexpr int P = V::kPairs;
+    extern __shared__ __align__(16) uint8_t shm[];
+    const int g0 = blockIdx.y * a.gb, gb = min(a.gb, a.G - g0), cb = gb * a.cg, c0 = g0 * a.cg;
+    const int n = blockIdx.z, k = blockIdx.x;
+    const int p0 = k * a.ppx, np = min(a.ppx, a.HW - p0);
+    const Cover cv(cb, VEC);
+    const bool fl = folds(cv.cvn);
+    const int rows = fl ? kWarps : cv.R;
+    float2 *gpart = reinterpret_cast<float2 *>(shm);          // [gb] this CTA's (mean, M2)
+    float2 *stat = gpart + a.gb;                              // [gb] (mean, rstd)
+    float2 *chan = stat + a.gb;                               // [cb]
+    float2 *ent = chan + a.cb;                                // [rows][cb], at most a.ent
+    float *piv = reinterpret_cast<float *>(ent + a.ent);      // [cb]
+    Raw *data = reinterpret_cast<Raw *>((reinterpret_cast<uintptr_t>(piv + a.cb) + 15) & ~(uintptr_t)15);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_trigger();
+    pdl_wait();
+    const T *x = static_cast<const T *>(a.x) + ((long long)n * a.HW + p0) * a.px + c0 + cv.col * VEC;
+    Raw *mine = data + cv.col;
+    StatSums<T, VEC> st;
+    float2 ga[P], be[P];
+    // the run in four parts, each summed as it lands
+    const int part = ((np + cv.R - 1) / cv.R + 3) / 4 * cv.R;
+    auto load = [&](int q) {
+        if (cv.on)
+            for (int p = q * part + cv.r; p < min(np, (q + 1) * part); p += cv.R)
+                copy_vec(mine + p * cv.cvn, reinterpret_cast<const Raw *>(x + p * a.px));
+        copy_commit();
+    };
+    auto take = [&](int q) {
+        if (cv.on)
+            for (int p = q * part + cv.r; p < min(np, (q + 1) * part); p += cv.R) st.take(mine[p * cv.cvn]);
+    };
+    load(0); load(1); load(2); load(3);
+    Raw first = {};
+    if (cv.on) first = *reinterpret_cast<const Raw *>(x);
+    if (cv.on)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int c = c0 + cv.col * VEC + e;
+            set_lane<VEC>(ga, e, a.gamma ? a.gamma[c] : 1.0f);
+            set_lane<VEC>(be, e, a.beta ? a.beta[c] : 0.0f);
+        }
+    st.start(first);
+    copy_wait<3>(); take(0);
+    copy_wait<2>(); take(1);
+    copy_wait<1>(); take(2);
+    copy_wait<0>(); take(3);
+    if (fl) {
+        fold(st.s1, cv.cvn);
+        fold(st.s2, cv.cvn);
+        if (lane < cv.cvn) st.put(ent + warp * cb + cv.col * VEC, piv + cv.col * VEC, warp == 0);
+    } else if (cv.on) {
+        st.put(ent + cv.r * cb + cv.col * VEC, piv + cv.col * VEC, cv.r == 0);
+    }
+    __syncthreads();
+    join_rows(ent, rows, cb, [&](int c, float2 v) { chan[c] = about(piv[c], v, (float)np); });
+    __syncthreads();
+    for (int g = warp; g < gb; g += kWarps) {
+        const float2 v = join_channels(chan + g * a.cg, a.cg, (float)np, lane);
+        if (lane == 0) gpart[g] = v;
+    }
+    if (a.K > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    for (int g = threadIdx.x; g < gb; g += kThreads) {
+        const float inv = 1.0f / ((float)a.HW * (float)a.cg);
+        float mu = 0.0f, m2 = 0.0f;
+        if (a.K > 1) {
+            float2 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < a.K) v[q] = ld_peer(gpart + g, q);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < a.K) mu += (float)min(a.ppx, a.HW - q * a.ppx) * (float)a.cg * v[q].x;
+            mu *= inv;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < a.K) m2 += v[q].y + (float)min(a.ppx, a.HW - q * a.ppx) * (float)a.cg * (v[q].x - mu) * (v[q].x - mu);
+        } else {
+            mu = gpart[g].x;
+            m2 = gpart[g].y;
+        }
+        const float rstd = 1.0f / sqrtf(m2 * inv + a.eps);
+        stat[g] = make_float2(mu, rstd);
+        if (k == 0) {
+            if (a.mean) a.mean[(long long)n * a.G + g0 + g] = mu;
+            if (a.rstd) a.rstd[(long long)n * a.G + g0 + g] = rstd;
+        }
+    }
+    __syncthreads();
+    if (a.K > 1) cluster_arrive();  // this CTA has read its peers' sums
+    if (cv.on) {
+        float2 mu[P];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float2 s = stat[(cv.col * VEC + e) / a.cg];
+            set_lane<VEC>(mu, e, -s.x);
+            set_lane<VEC>(ga, e, (e % 2 ? ga[e / 2].y : ga[e / 2].x) * s.y);
+        }
+        T *y = static_cast<T *>(a.out) + ((long long)n * a.HW + p0) * a.pout + c0 + cv.col * VEC;
+#pragma unroll 4
+        for (int p = cv.r; p < np; p += cv.R) {
+            float2 f[P];
+            V::unpack(mine[p * cv.cvn], f);
+#pragma unroll
+            for (int e = 0; e < P; ++e) f[e] = act2<ACT, sizeof(T) == 2>(fma2(add2(f[e], mu[e]), ga[e], be[e]));
+            *reinterpret_cast<Raw *>(y + p * a.pout) = V::pack(f);
+        }
+    }
+    if (a.K > 1) cluster_wait();  // no CTA leaves while its sums may be read
+}
+
+// The gradient: a cluster holds K CTAs of each of NI images; where NI is every
+// image, dgamma and dbeta are complete in the cluster, else each image's sums
+// go to partc[n][C] (S = 1) and gn_bwd_join_kernel adds them.
+template <typename T, int VEC, int ACT>
+__global__ void __launch_bounds__(kThreads, 2) gn_bwd_resident_kernel(GnArgs a) {
+    using L = GradLane<T, VEC, ACT>;
+    using V = Vec<T, VEC>;
+    using Raw = typename V::Raw;
+    constexpr int P = V::kPairs;
+    extern __shared__ __align__(16) uint8_t shm[];
+    const int g0 = blockIdx.y * a.gb, gb = min(a.gb, a.G - g0), cb = gb * a.cg, c0 = g0 * a.cg;
+    const int img = blockIdx.x / a.K, k = blockIdx.x - img * a.K;  // blockIdx.x: the rank in the cluster
+    const int n = blockIdx.z * a.NI + img;
+    const int p0 = k * a.ppx, np = min(a.ppx, a.HW - p0);
+    const Cover cv(cb, VEC);
+    const bool fl = folds(cv.cvn);
+    const int rows = fl ? kWarps : cv.R;
+    const int size = a.K * a.NI;
+    float2 *gpart = reinterpret_cast<float2 *>(shm);  // [gb] this CTA's sums of gamma dz, gamma dz xhat
+    float2 *sum = gpart + a.gb;                       // [gb] minus the image's, over m
+    float2 *chan = sum + a.gb;                        // [cb] this CTA's sums of dz, dz xhat
+    float2 *ent = chan + a.cb;                        // [rows][cb], at most a.ent
+    Raw *data = reinterpret_cast<Raw *>((reinterpret_cast<uintptr_t>(ent + a.ent) + 15) & ~(uintptr_t)15);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_trigger();
+    pdl_wait();
+    const T *x = static_cast<const T *>(a.x) + ((long long)n * a.HW + p0) * a.px + c0 + cv.col * VEC;
+    const T *dy = static_cast<const T *>(a.dy) + ((long long)n * a.HW + p0) * a.pdy + c0 + cv.col * VEC;
+    Raw *mx = data + cv.col, *md = mx + a.ppx * cv.cvn;
+    L ln;
+    float2 A[P], B[P];
+#pragma unroll
+    for (int e = 0; e < P; ++e) A[e] = B[e] = make_float2(0.0f, 0.0f);
+    const int part = ((np + cv.R - 1) / cv.R + 3) / 4 * cv.R;
+    auto load = [&](int q) {
+        if (cv.on)
+            for (int p = q * part + cv.r; p < min(np, (q + 1) * part); p += cv.R) {
+                copy_vec(mx + p * cv.cvn, reinterpret_cast<const Raw *>(x + p * a.px));
+                copy_vec(md + p * cv.cvn, reinterpret_cast<const Raw *>(dy + p * a.pdy));
+            }
+        copy_commit();
+    };
+    auto take = [&](int q) {
+        if (cv.on)
+            for (int p = q * part + cv.r; p < min(np, (q + 1) * part); p += cv.R) ln.sums(mx[p * cv.cvn], md[p * cv.cvn], A, B);
+    };
+    load(0); load(1); load(2); load(3);
+    if (cv.on)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int c = c0 + cv.col * VEC + e;
+            const long long g = (long long)n * a.G + c / a.cg;
+            ln.set(a, e, c, a.mean[g], a.rstd[g]);
+        }
+    copy_wait<3>(); take(0);
+    copy_wait<2>(); take(1);
+    copy_wait<1>(); take(2);
+    copy_wait<0>(); take(3);
+    if (fl) {
+        fold(A, cv.cvn);
+        fold(B, cv.cvn);
+        if (lane < cv.cvn) put_sums<VEC>(ent + warp * cb + cv.col * VEC, A, B);
+    } else if (cv.on) {
+        put_sums<VEC>(ent + cv.r * cb + cv.col * VEC, A, B);
+    }
+    __syncthreads();
+    join_rows(ent, rows, cb, [&](int c, float2 v) { chan[c] = v; });
+    __syncthreads();
+    for (int g = warp; g < gb; g += kWarps) {
+        float2 v = make_float2(0.0f, 0.0f);
+        for (int c = lane; c < a.cg; c += 32) {
+            const float w = a.gamma ? a.gamma[c0 + g * a.cg + c] : 1.0f;
+            const float2 u = chan[g * a.cg + c];
+            v.x = fmaf(w, u.x, v.x);
+            v.y = fmaf(w, u.y, v.y);
+        }
+        v.x = warp_sum(v.x);
+        v.y = warp_sum(v.y);
+        if (lane == 0) gpart[g] = v;
+    }
+    if (size > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+    const float inv = -1.0f / ((float)a.HW * (float)a.cg);
+    for (int g = threadIdx.x; g < gb; g += kThreads) {
+        float2 v = make_float2(0.0f, 0.0f);
+        for (int q = 0; q < a.K; ++q) v = add2(v, size > 1 ? ld_peer(gpart + g, img * a.K + q) : gpart[g]);
+        sum[g] = make_float2(v.x * inv, v.y * inv);
+    }
+    // the channels' sums: of the whole batch, or of this image
+    const bool all = a.NI == a.N;
+    if ((a.dgamma || a.dbeta) && k == 0 && (!all || img == 0)) {
+        const int q0 = all ? 0 : img * a.K, q1 = all ? size : q0 + a.K;
+        for (int c = threadIdx.x; c < cb; c += kThreads) {
+            float2 v = make_float2(0.0f, 0.0f);
+            for (int q = q0; q < q1; ++q) v = add2(v, size > 1 ? ld_peer(chan + c, q) : chan[c]);
+            if (all) {
+                if (a.dbeta) a.dbeta[c0 + c] = v.x;
+                if (a.dgamma) a.dgamma[c0 + c] = v.y;
+            } else {
+                a.partc[(long long)n * a.C + c0 + c] = v;
+            }
+        }
+    }
+    __syncthreads();
+    if (size > 1) cluster_arrive();
+    if (cv.on) {
+        float2 m1[P], m2[P];
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const float2 s = sum[(cv.col * VEC + e) / a.cg];
+            set_lane<VEC>(m1, e, s.x);
+            set_lane<VEC>(m2, e, s.y);
+        }
+        T *dx = static_cast<T *>(a.out) + ((long long)n * a.HW + p0) * a.pout + c0 + cv.col * VEC;
+#pragma unroll 2
+        for (int p = cv.r; p < np; p += cv.R) *reinterpret_cast<Raw *>(dx + p * a.pout) = ln.dx(mx[p * cv.cvn], md[p * cv.cvn], m1, m2);
+    }
+    if (size > 1) cluster_wait();
+}
+
+__global__ void __launch_bounds__(kThreads) gn_bwd_join_kernel(GnArgs a) {
+    __shared__ float2 red[kWarps * 32];
+    pdl_trigger();
+    pdl_wait();
+    join_rows_of_channels(a, (long long)a.N * a.S, blockIdx.x, gridDim.x, red);
+}
+
 // ------------------------------------------------------------------ host side
-enum { K_STATS, K_APPLY, K_SUMS, K_DX };
+enum { K_STATS, K_APPLY, K_SUMS, K_DX, K_RES, K_RES_BWD };
 
 template <typename T, int VEC>
 const void *pick(int which, int act) {
@@ -523,6 +892,14 @@ const void *pick(int which, int act) {
         return act == ACT_MISH ? (const void *)&gn_bwd_sums_kernel<T, VEC, ACT_MISH>
                                : (act == ACT_RELU ? (const void *)&gn_bwd_sums_kernel<T, VEC, ACT_RELU>
                                                   : (const void *)&gn_bwd_sums_kernel<T, VEC, ACT_NONE>);
+    case K_RES:
+        return act == ACT_MISH ? (const void *)&gn_resident_kernel<T, VEC, ACT_MISH>
+                               : (act == ACT_RELU ? (const void *)&gn_resident_kernel<T, VEC, ACT_RELU>
+                                                  : (const void *)&gn_resident_kernel<T, VEC, ACT_NONE>);
+    case K_RES_BWD:
+        return act == ACT_MISH ? (const void *)&gn_bwd_resident_kernel<T, VEC, ACT_MISH>
+                               : (act == ACT_RELU ? (const void *)&gn_bwd_resident_kernel<T, VEC, ACT_RELU>
+                                                  : (const void *)&gn_bwd_resident_kernel<T, VEC, ACT_NONE>);
     default:
         return act == ACT_MISH ? (const void *)&gn_bwd_dx_kernel<T, VEC, ACT_MISH>
                                : (act == ACT_RELU ? (const void *)&gn_bwd_dx_kernel<T, VEC, ACT_RELU>
@@ -579,24 +956,79 @@ int check_map(const conv_plan *p, const void *t, int64_t *pitch) {
 }
 bool bad_f32(const void *t) { return t && ((uintptr_t)t & 3u); }
 
-GnArgs base_args(const conv_plan *p, const void *x, long long px, void *out, long long pout, void *ws) {
+GnArgs base_args(const conv_plan *p, const GnGeom::Dir &d, const void *x, long long px, void *out, long long pout, void *ws) {
     GnArgs a = {};
     a.x = x; a.px = px; a.out = out; a.pout = pout;
-    a.N = p->s.n; a.HW = p->s.h * p->s.w; a.C = p->s.c_in; a.G = p->groups; a.cg = p->s.c_in / p->groups;
-    a.S = p->gn.S; a.ppx = p->gn.ppx; a.eps = p->gn.eps;
+    a.N = p->s.n; a.n0 = 0; a.HW = p->s.h * p->s.w; a.C = p->s.c_in; a.G = p->groups; a.cg = p->s.c_in / p->groups;
+    a.S = d.S; a.ppx = d.ppx; a.eps = p->gn.eps;
     a.part = static_cast<float2 *>(ws);
     a.partc = a.part + (long long)a.N * a.S * a.G;
     return a;
 }
 
-cudaError_t launch(const conv_plan *p, int which, int vec, GnArgs &a, dim3 grid, size_t smem, cudaStream_t st) {
+// The resident form of a run, and its shared memory.  The last CTA of a map
+// may have fewer channels than the others and then more thread rows: the sums'
+// entries are the larger of the two counts.
+size_t resident_args(const GnGeom::Dir &d, int vec, int es, int maps, GnArgs &a) {
+    a.gb = d.gb; a.cb = d.cb; a.K = d.K; a.NI = d.NI; a.ppx = d.rppx;
+    auto entries = [&](int cb) { return (folds(cb / vec) ? kWarps : rows_for(cb, vec)) * cb; };
+    const int last = (a.G - (a.G - 1) / a.gb * a.gb) * a.cg;
+    a.ent = entries(a.cb) > entries(last) ? entries(a.cb) : entries(last);
+    return (size_t)2 * a.gb * 8 + (size_t)a.cb * 8 + (size_t)a.ent * 8 + (size_t)a.cb * 4 + 16 + (size_t)a.ppx * a.cb * es * maps;
+}
+bool resident(const GnGeom::Dir &d, int vec) { return d.K > 0 && d.cb / vec <= kThreads; }
+
+// How one direction runs.  `maps`: input maps it reads (1, or x and dy).
+void plan_direction(const conv_plan *p, int maps, GnGeom::Dir &d, size_t &ws) {
+    const int es = conv_esize(p->dtype), C = p->s.c_in, G = p->groups, cg = C / G, HW = p->s.h * p->s.w, N = p->s.n;
+    const int wide = 16 / es, au = C % wide == 0 ? wide : (C % 2 == 0 && es == 2 ? 2 : 1);  // the widest vector there can be
+    // Two launches: as many images a pass as keep what the second launch reads
+    // again in L2, each in runs of pixels: four CTAs a SM over the pass, at
+    // least four pixels a thread.
+    const long long image = (long long)HW * C * es * maps;
+    d.step = (int)(kL2Bytes / image < 1 ? 1 : (kL2Bytes / image < N ? kL2Bytes / image : N));
+    const int R = rows_for(C, au);
+    long long S = d.step > 0 ? (4LL * p->num_sms + d.step - 1) / d.step : 1;
+    const long long most = ((long long)HW + 4LL * R - 1) / (4LL * R);
+    if (S > most) S = most;
+    if (S < 1) S = 1;
+    d.ppx = (int)((HW + S - 1) / S);
+    d.S = (HW + d.ppx - 1) / d.ppx;
+    ws = (size_t)N * d.S * ((size_t)G + (maps > 1 ? C : 0)) * sizeof(float2);
+    // Resident: the fewest groups of a CTA that fill whole vectors and 64
+    // bytes of a pixel (a DRAM burst); the fewest CTAs an image that hold their
+    // runs, more while SMs are idle and runs stay above 8 KB.
+    d.K = 0;
+    int gb = 1;
+    while (gb < G && ((gb * cg) % au != 0 || gb * cg * es < 64)) ++gb;
+    const int cb = gb * cg;
+    const bool always = cb <= kThreads;                   // whatever vector a call's addresses allow
+    if (!always && cb / au > kThreads) return;
+    auto bytes = [&](int k) { return (long long)((HW + k - 1) / k) * cb * es * maps; };
+    int K = 1;
+    while (K <= 8 && bytes(K) > kResident) ++K;
+    if (K > 8) return;
+    const long long blocks = (G + gb - 1) / gb;
+    while (K < 8 && blocks * N * K < p->num_sms && bytes(K) > 8 * 1024) ++K;
+    d.rppx = (HW + K - 1) / K;
+    d.K = (HW + d.rppx - 1) / d.rppx;
+    d.gb = gb; d.cb = cb;
+    d.NI = maps > 1 && (long long)N * d.K <= 8 && N > 0 ? N : 1;
+    if (blocks > 65535) { d.K = 0; return; }
+    // the workspace of the form that runs, or of both where addresses decide
+    const size_t res = maps > 1 && d.NI != N ? (size_t)N * C * sizeof(float2) : 0;
+    ws = always ? res : (ws > res ? ws : res);
+}
+
+cudaError_t launch(const conv_plan *p, int which, int vec, GnArgs &a, dim3 grid, size_t smem, cudaStream_t st, int head = 0,
+                   int cluster = 1) {
     const void *k = pick_kernel(which, p->dtype, vec, p->act);
     if (smem > 48 * 1024) {
-        const int rc = conv_grant_smem(k, p->device, (int)smem);
+        const int rc = conv_grant_smem_once(k, p->device, (int)smem);
         if (rc != CONV_OK) return cudaErrorInvalidValue;
     }
-    void *args[] = {&a};
-    return conv_launch(k, grid, dim3(kThreads), args, smem, st);
+    void *args[] = {&a, &head};  // (only gn_bwd_dx_kernel takes the second)
+    return conv_launch(k, grid, dim3(kThreads), args, smem, st, cluster);
 }
 
 }  // namespace
@@ -625,19 +1057,17 @@ extern "C" int conv_plan_create_groupnorm(int32_t n, int32_t h, int32_t w, int32
         conv_plan_destroy(p);
         return rc;
     }
-    // Runs of pixels: four CTAs a SM over the whole batch, but at least four
-    // pixels a thread.
-    const int HW = h * w;
-    const int R = rows_for(c, c % (16 / conv_esize(dtype)) == 0 ? 16 / conv_esize(dtype) : 1);
-    long long S = n > 0 ? (4LL * p->num_sms + n - 1) / n : 1;
-    const long long most = ((long long)HW + 4LL * R - 1) / (4LL * R);
-    if (S > most) S = most;
-    if (S < 1) S = 1;
-    p->gn.ppx = (int)((HW + S - 1) / S);
-    p->gn.S = (HW + p->gn.ppx - 1) / p->gn.ppx;
-    p->ws_bytes = (size_t)n * p->gn.S * ((size_t)groups + c) * sizeof(float2);
-    snprintf(p->desc, sizeof(p->desc), "groupnorm %s groups=%d x %d runs=%d x %d px", dtype == CONV_F32 ? "f32" : "bf16",
-             groups, c / groups, p->gn.S, p->gn.ppx);
+    plan_direction(p, 1, p->gn.fwd, p->ws_bytes);
+    plan_direction(p, 2, p->gn.bwd, p->ws_bwd_bytes);
+    auto say = [](const GnGeom::Dir &d, char *t, size_t n) {
+        if (d.K > 0) snprintf(t, n, "resident %d groups, %d CTAs an image", d.gb, d.K);
+        else snprintf(t, n, "%d runs of %d px, %d images a pass", d.S, d.ppx, d.step);
+    };
+    char f[64], b[64];
+    say(p->gn.fwd, f, sizeof(f));
+    say(p->gn.bwd, b, sizeof(b));
+    snprintf(p->desc, sizeof(p->desc), "groupnorm %s groups=%dx%d forward: %s; gradient: %s", dtype == CONV_F32 ? "f32" : "bf16",
+             groups, c / groups, f, b);
     *out_plan = p;
     return CONV_OK;
 }
@@ -664,17 +1094,28 @@ extern "C" int conv_run_groupnorm(const conv_plan_t *plan, const void *x, int64_
         range_overlaps(workspace, p->ws_bytes, x, x_pitch, rows, C, es) ||
         range_overlaps(workspace, p->ws_bytes, y, y_pitch, rows, C, es))
         return CONV_ERR_ALIASING;
-    GnArgs a = base_args(p, x, x_pitch, y, y_pitch, workspace);
+    const GnGeom::Dir &d = p->gn.fwd;
+    GnArgs a = base_args(p, d, x, x_pitch, y, y_pitch, workspace);
     a.gamma = gamma; a.beta = beta; a.mean = mean; a.rstd = rstd;
     const void *ptrs[2] = {x, y};
     const long long pitches[2] = {x_pitch, y_pitch};
     const int vec = vec_for(p, 2, ptrs, pitches);
     const int R = rows_for(C, vec);
     cudaStream_t st = (cudaStream_t)stream;
-    const dim3 grid(a.S, a.N);
-    cudaError_t e = launch(p, K_STATS, vec, a, grid, ((size_t)R * C * 2 + 3 * kWarps) * 4, st);
-    if (e == cudaSuccess) e = launch(p, K_APPLY, vec, a, grid, (size_t)a.G * 8, st);
-    return e == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+    if (resident(d, vec)) {
+        const size_t smem = resident_args(d, vec, es, 1, a);
+        const dim3 grid(d.K, (a.G + d.gb - 1) / d.gb, a.N);
+        return launch(p, K_RES, vec, a, grid, smem, st, 0, d.K) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+    }
+    const size_t runs = (size_t)a.G * a.S <= (size_t)kStageRuns ? (size_t)a.G * a.S : 0;
+    for (int n0 = 0; n0 < a.N; n0 += d.step) {
+        a.n0 = n0;
+        const dim3 grid(a.S, a.N - n0 < d.step ? a.N - n0 : d.step);
+        cudaError_t e = launch(p, K_STATS, vec, a, grid, ((size_t)R * C + C) * 8 + (size_t)C * 4, st);
+        if (e == cudaSuccess) e = launch(p, K_APPLY, vec, a, grid, ((size_t)a.G + runs) * 8, st);
+        if (e != cudaSuccess) return CONV_ERR_CUDA;
+    }
+    return CONV_OK;
 }
 
 extern "C" int conv_run_groupnorm_bwd(const conv_plan_t *plan, const void *x, int64_t x_pitch, const float *gamma,
@@ -697,7 +1138,7 @@ extern "C" int conv_run_groupnorm_bwd(const conv_plan_t *plan, const void *x, in
     if ((rc = check_map(p, x, &x_pitch)) != CONV_OK || (rc = check_map(p, dy, &dy_pitch)) != CONV_OK ||
         (rc = check_map(p, dx, &dx_pitch)) != CONV_OK)
         return rc;
-    if (!mean || !rstd || (p->ws_bytes && !workspace)) return CONV_ERR_NULL_ARG;
+    if (!mean || !rstd || (p->ws_bwd_bytes && !workspace)) return CONV_ERR_NULL_ARG;
     if (((uintptr_t)workspace & 15u) || bad_f32(gamma) || bad_f32(beta) || bad_f32(mean) || bad_f32(rstd))
         return CONV_ERR_MISALIGNED;
     const long long rows = (long long)p->s.n * p->s.h * p->s.w;
@@ -711,17 +1152,37 @@ extern "C" int conv_run_groupnorm_bwd(const conv_plan_t *plan, const void *x, in
     for (int i = 0; i < 3; ++i)
         bad = bad || range_overlaps(dgamma, cb, maps[i], mp[i], rows, C, es) ||
               range_overlaps(dbeta, cb, maps[i], mp[i], rows, C, es) ||
-              range_overlaps(workspace, p->ws_bytes, maps[i], mp[i], rows, C, es);
+              range_overlaps(workspace, p->ws_bwd_bytes, maps[i], mp[i], rows, C, es);
     if (bad) return CONV_ERR_ALIASING;
-    GnArgs a = base_args(p, x, x_pitch, dx, dx_pitch, workspace);
+    const GnGeom::Dir &d = p->gn.bwd;
+    GnArgs a = base_args(p, d, x, x_pitch, dx, dx_pitch, workspace);
     a.dy = dy; a.pdy = dy_pitch;
     a.gamma = gamma; a.beta = beta; a.mean = const_cast<float *>(mean); a.rstd = const_cast<float *>(rstd);
     a.dgamma = dgamma; a.dbeta = dbeta;
     const long long pitches[3] = {x_pitch, dy_pitch, dx_pitch};
     const int vec = vec_for(p, 3, maps, pitches);
     const int R = rows_for(C, vec);
-    cudaError_t e = launch(p, K_SUMS, vec, a, dim3(a.S, a.N), ((size_t)R * C + C) * 8, st);
-    const size_t dxs = (size_t)a.G * 8 > kWarps * 32 * 8 ? (size_t)a.G * 8 : (size_t)kWarps * 32 * 8;
-    if (e == cudaSuccess) e = launch(p, K_DX, vec, a, dim3(a.S, a.N + 1), dxs, st);
-    return e == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+    if (resident(d, vec)) {
+        const size_t smem = resident_args(d, vec, es, 2, a);
+        a.S = 1;
+        a.partc = static_cast<float2 *>(workspace);
+        const dim3 grid(d.K * d.NI, (a.G + d.gb - 1) / d.gb, a.N / d.NI);
+        cudaError_t e = launch(p, K_RES_BWD, vec, a, grid, smem, st, 0, d.K * d.NI);
+        if (e == cudaSuccess && d.NI != a.N && (dgamma || dbeta)) {
+            void *args[] = {&a};
+            e = conv_launch((const void *)&gn_bwd_join_kernel, dim3((C + 31) / 32), dim3(kThreads), args, 0, st);
+        }
+        return e == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+    }
+    const size_t runs = (size_t)a.G * a.S <= (size_t)kStageRuns ? (size_t)a.G * a.S : 0;
+    const size_t need = ((size_t)a.G + runs) * 8, dxs = need > kWarps * 32 * 8 ? need : (size_t)kWarps * 32 * 8;
+    for (int n0 = 0; n0 < a.N; n0 += d.step) {
+        a.n0 = n0;
+        const int n = a.N - n0 < d.step ? a.N - n0 : d.step;
+        const int head = n0 + n == a.N && (dgamma || dbeta) ? 1 : 0;  // (once every image's sums are there)
+        cudaError_t e = launch(p, K_SUMS, vec, a, dim3(a.S, n), ((size_t)R * C + C) * 8, st);
+        if (e == cudaSuccess) e = launch(p, K_DX, vec, a, dim3(a.S, n + head), dxs, st, head);
+        if (e != cudaSuccess) return CONV_ERR_CUDA;
+    }
+    return CONV_OK;
 }

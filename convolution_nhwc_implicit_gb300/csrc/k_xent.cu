@@ -614,7 +614,7 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // Workspace of a run, in order.
 struct Space {
-    size_t xp, wp, part, tlogit, row_loss, lse, counter, scale, g, dxp, dwp, total;
+    size_t xp, wp, part, tlogit, row_loss, lse, counter, scale, g, dxp, dwp, fwd, bwd;
 };
 Space space_of(const conv_plan *p) {
     const XentGeom &g = p->xent;
@@ -632,13 +632,13 @@ Space space_of(const conv_plan *p) {
     take(s.tlogit, (size_t)N * 4);
     take(s.row_loss, (size_t)N * 4);
     take(s.lse, (size_t)N * 4);
-    const size_t fwd = o;
-    // gradient (over the forward's)
+    s.fwd = o;
+    // gradient
     o = common;
     take(s.g, (size_t)N * g.piece * 2);
     take(s.dxp, (g.pieces > 1 || g.dx_split > 1) ? (size_t)g.dx_split * g.tiles_m * g.tiles_d * kTile * kTile * 4 : 0);
     take(s.dwp, g.dw_split > 1 ? (size_t)g.dw_split * ceil_div(g.piece, kTile) * g.tiles_d * kTile * kTile * 4 : 0);
-    s.total = o > fwd ? o : fwd;
+    s.bwd = o;
     return s;
 }
 
@@ -699,7 +699,7 @@ extern "C" int conv_plan_create_xent(int32_t rows, int32_t c_in, int32_t classes
     p->stride = 1; p->groups = 1; p->dtype = dtype; p->act = CONV_ACT_NONE; p->oh = 1; p->ow = 1;
     p->y_c = classes; p->up = 1; p->algo = CONV_ALGO_XENT;
     int rc = conv_plan_bind_device(p, true);
-    for (int k = FWD; k <= PROD && rc == CONV_OK; ++k) rc = conv_grant_smem(kernel_of(k), p->device, kSmem);
+    for (int k = FWD; k <= PROD && rc == CONV_OK; ++k) rc = conv_grant_smem_once(kernel_of(k), p->device, kSmem);
     if (rc == CONV_OK && !encoder()) rc = CONV_ERR_CUDA;
     if (rc != CONV_OK) {
         conv_plan_destroy(p);
@@ -733,7 +733,11 @@ extern "C" int conv_plan_create_xent(int32_t rows, int32_t c_in, int32_t classes
     g.dx_split = ceil_div(kx, g.dx_kper);
     g.dw_kper = kw > 0 ? ceil_div(kw, sw) : 1;
     g.dw_split = kw > 0 ? ceil_div(kw, g.dw_kper) : 1;
-    p->ws_bytes = rows > 0 ? space_of(p).total : 0;
+    if (rows > 0) {
+        const Space sp = space_of(p);
+        p->ws_bytes = sp.fwd;
+        p->ws_bwd_bytes = sp.bwd;
+    }
     snprintf(p->desc, sizeof(p->desc), "xent bf16 tcgen05 pair tiles=%dx%d pieces=%d x %d classes dx_split=%d dw_split=%d",
              g.tiles_m, g.tiles_n, g.pieces, g.piece, g.dx_split, g.dw_split);
     *out_plan = p;
@@ -810,7 +814,7 @@ extern "C" int conv_run_xent_bwd(const conv_plan_t *plan, const void *x, const v
     const void *in[5] = {x, w, target, lse, dloss};
     const size_t inb[5] = {N * D * 2, V * D * 2, N * 4, N * 4, 4};
     const void *out[3] = {dx, dw, workspace};
-    const size_t outb[3] = {N * D * 2, V * D * 2, p->ws_bytes};
+    const size_t outb[3] = {N * D * 2, V * D * 2, p->ws_bwd_bytes};
     for (int i = 0; i < 3; ++i) {
         for (int j = 0; j < 5; ++j)
             if (overlap(out[i], outb[i], in[j], inb[j])) return CONV_ERR_ALIASING;

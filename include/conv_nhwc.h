@@ -310,11 +310,12 @@ CONV_API int conv_run_groupnorm_bwd(const conv_plan_t *plan, const void *x, int6
                                     int64_t dy_pitch, void *dx, int64_t dx_pitch, float *dgamma, float *dbeta,
                                     void *workspace, void *stream);
 
-/* Bytes of device scratch that a run of this plan takes as `workspace` (0 for
- * plans whose runs take none; NULL may then be given).  The caller owns it,
- * 16-byte aligned; it holds nothing between calls, and calls that can overlap
- * on the GPU take one each. */
+/* Bytes of device scratch that a run of this plan, or its gradient, takes as
+ * `workspace` (0 where it takes none; NULL may then be given).  The caller
+ * owns it, 16-byte aligned; it holds nothing between calls, and calls that can
+ * overlap on the GPU take one each. */
 CONV_API int conv_plan_workspace(const conv_plan_t *plan, size_t *bytes);
+CONV_API int conv_plan_workspace_bwd(const conv_plan_t *plan, size_t *bytes);
 
 /* ---------------------------------------------------------------------------
  * Loss of a class head over many classes: softmax cross entropy of the scores

@@ -112,6 +112,14 @@ CASES = [
     (2, 10, 10, 48, 6, "f32", "mish", 3, 1),
     (1, 160, 160, 32, 8, "bf16", "mish", 0, 0),
     (5, 31, 33, 96, 12, "f32", "none", 0, 0),
+    (2, 130, 131, 33, 3, "bf16", "mish", 0, 0),      # maps too large for shared memory: odd channels
+    (1, 150, 151, 66, 6, "f32", "relu", 2, 1),       # ... a slice at odd addresses
+    (3, 120, 120, 60, 6, "bf16", "none", 0, 0),
+    (2, 90, 90, 512, 4, "bf16", "mish", 0, 0),       # ... groups of 128 channels
+    (1, 100, 100, 300, 300, "f32", "mish", 0, 0),    # more groups than a CTA stages runs of
+    (9, 12, 12, 64, 8, "bf16", "relu", 0, 0),        # more images than a cluster holds
+    (4, 40, 40, 60, 10, "f32", "mish", 0, 0),        # a last CTA with fewer groups than the others
+    (6, 160, 160, 128, 32, "f32", "mish", 0, 0),     # more than one pass over L2
 ]
 
 
@@ -299,12 +307,17 @@ def test_refusals(cl):
         plan.run_backward(x, None, None, st, st, y, y)
     assert e.value.code == -5
     lib = cl.load_library()
-    ws = torch.empty(plan.workspace_bytes, dtype=torch.uint8, device="cuda")
-    args = [plan.handle, x.data_ptr(), 0, None, None, y.data_ptr(), 0, None, None, ws.data_ptr(), None]
-    assert lib.conv_run_groupnorm(*args) == 0
+    args = [plan.handle, x.data_ptr(), 0, None, None, y.data_ptr(), 0, None, None, None, None]
+    assert plan.workspace_bytes == 0 and lib.conv_run_groupnorm(*args) == 0
     assert lib.conv_run_groupnorm(*(args[:2] + [8] + args[3:])) == -9          # a pitch below the channels
     assert lib.conv_run_groupnorm(*(args[:1] + [x.data_ptr() + 1] + args[2:])) == -4
-    assert lib.conv_run_groupnorm(*(args[:9] + [None, None])) == -1            # no workspace
+    big = cl.GroupNormPlan(1, 160, 160, 64, 4)
+    xb, yb = torch.zeros(2, 1, 160, 160, 64, device="cuda", dtype=torch.bfloat16)
+    assert big.workspace_bytes > 0
+    big.run(xb, None, None, yb)
+    args = [big.handle, xb.data_ptr(), 0, None, None, yb.data_ptr(), 0, None, None, None, None]
+    assert lib.conv_run_groupnorm(*args) == -1                                 # no workspace
+    assert lib.conv_run_groupnorm(*(args[:9] + [xb.data_ptr(), None])) == -5   # a workspace over x
     assert lib.conv_run(plan.handle, x.data_ptr(), x.data_ptr(), None, y.data_ptr(), None) == -9
     assert plan.algo == "groupnorm" and plan.launches >= 1 and plan.describe().startswith("groupnorm")
     plan.check_device_status()
