@@ -72,22 +72,21 @@ struct DwpwGeom {
     int smem;          // dynamic shared memory bytes
 };
 
-// Group norm.  Each direction: resident in a cluster's shared memory (K > 0: K
-// CTAs an image, runs of rppx pixels, gb groups = cb channels a CTA, NI images a
-// cluster), or in two launches over `step` images a pass (S runs of ppx
-// pixels an image).
+// Group norm.  Each direction: one launch of clusters (K > 0: K CTAs an image,
+// runs of cpx pixels, gb groups = cb channels a CTA; the gradient's hold every
+// image), or two launches (S runs of ppx pixels an image).
 struct GnGeom {
     float eps;
     struct Dir {
-        int S, ppx, step;
-        int K, rppx, gb, cb, NI;
+        int S, ppx;
+        int K, cpx, gb, cb;
     } fwd, bwd;
 };
 
-// 4-bit pointwise layer: scale groups, runs of 128 input channels, and blocks
-// of eight rows a CTA.
+// 4-bit pointwise layer: scale groups, runs of 128 input channels; x whole in
+// shared memory (nt blocks of eight rows) or in pieces (many); warps a CTA.
 struct W4Geom {
-    int group, ng, units, nt;
+    int group, ng, units, nt, many, warps, smem, grid;
 };
 
 // Class loss: 256 x 256 tiles over rows, classes and features; the classes in

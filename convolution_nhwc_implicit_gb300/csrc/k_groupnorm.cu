@@ -40,9 +40,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr long long kL2Bytes = 64ll << 20;  // of an input that two launches share
+// CTAs a SM of the two-launch form: three of the forward kernels' 80 registers;
+// two of the gradient's 128 for bf16 (eight channels a thread), three for fp32.
+constexpr int kCtas = 3;
+__host__ __device__ constexpr int grad_ctas(int es) { return es == 2 ? 2 : kCtas; }
 constexpr int kStageRuns = 4096;            // partial results a CTA stages (32 KB)
-constexpr int kResident = 88 * 1024;        // map bytes of a resident CTA (two a SM)
+constexpr int kResident = 50 * 1024, kResidentMost = 88 * 1024;  // map bytes of a resident CTA (four a SM, two)
 constexpr int kMaxC = 8192;  // channels: their sums stay in shared memory (16 bytes each)
 
 // VEC consecutive channels of one pixel, as fp32 pairs (VEC = 1: the first
@@ -94,28 +97,38 @@ struct GnArgs {
     float *dgamma, *dbeta;     // [C] or null
     float2 *part;              // [N][G][S]: (mean, M2), or (sum gamma dz, sum gamma dz xhat)
     float2 *partc;             // [N][S][C]: (sum dz, sum dz xhat)
-    int N, n0, HW, C, G, cg;   // a launch takes images n0, n0 + 1, ...
-    int S, ppx;                // S runs of ppx pixels an image
-    // resident kernels: groups and channels of a CTA, CTAs an image (a run of
-    // pixels each), images of a cluster (gradient)
-    int gb, cb, K, NI, ent;    // ent: entries of the threads' sums in shared memory
+    int N, HW, C, G, cg;
+    int ppx, S;                // a CTA takes a run of ppx pixels; two launches: S runs an image
+    // cluster kernels: groups and channels of a CTA, CTAs an image (a run of
+    // pixels each)
+    int gb, cb, K, ent;    // ent: entries of the threads' sums in shared memory
     float eps;
 };
 
-// act(z) of a pair.  bf16 maps: the layer epilogue's packed Mish.  fp32 maps:
-// z t / (t + 2) with n = e^z, t = n (n + 2), which cancels nowhere, on the
-// hardware's exp2 and reciprocal (~5e-7 relative); the exponent is clamped at
-// 20, where t / (t + 2) is 1 in fp32.  ReLU passes NaN on.
-template <int ACT, bool BF16>
+// 1/d of a pair from one hardware reciprocal (its unit is the bound of the
+// activations): 1 / (d.x d.y), times the other.  d <= 2.4e17, so that the
+// product stays finite; a NaN is put back by its caller's product with z.
+__device__ __forceinline__ float2 rcp2(float2 d) {
+    const float r = rcp_approx(d.x * d.y);
+    return mul2(make_float2(r, r), make_float2(d.y, d.x));
+}
+// e^z of a pair, z clamped at 20, where Mish and its derivative have reached
+// their limits z and 1 in fp32 (fminf drops a NaN: see rcp2).
+__device__ __forceinline__ float2 exp2_clamped(float2 z) {
+    const float2 e = mul2(make_float2(fminf(z.x, 20.0f), fminf(z.y, 20.0f)), make_float2(1.4426950408889634f, 1.4426950408889634f));
+    return make_float2(ex2_approx(e.x), ex2_approx(e.y));
+}
+// act(z) of a pair.  Mish = z t / (t + 2) with n = e^z, t = n (n + 2): it
+// cancels nowhere (~5e-7 relative on the hardware's exp2 and reciprocal).
+// ReLU passes NaN on.
+template <int ACT>
 __device__ __forceinline__ float2 act2(float2 z) {
     if constexpr (ACT == ACT_RELU) return make_float2(z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y);
-    else if constexpr (ACT == ACT_MISH && BF16) return mish2_fast(z);
     else if constexpr (ACT == ACT_MISH) {
-        const float2 e = mul2(make_float2(fminf(z.x, 20.0f), fminf(z.y, 20.0f)), make_float2(1.4426950408889634f, 1.4426950408889634f));
-        const float2 n = make_float2(ex2_approx(e.x), ex2_approx(e.y));
-        const float2 t = mul2(n, add2(n, make_float2(2.0f, 2.0f)));
-        const float2 d = add2(t, make_float2(2.0f, 2.0f));
-        return mul2(z, mul2(t, make_float2(rcp_approx(d.x), rcp_approx(d.y))));
+        const float2 two = make_float2(2.0f, 2.0f);
+        const float2 n = exp2_clamped(z);
+        const float2 t = mul2(n, add2(n, two));
+        return mul2(z, mul2(t, rcp2(add2(t, two))));
     } else return z;
 }
 // act'(z) of a pair: with w = 1 + e^z, r = 1 / (w^2 + 1), Mish' = 1 - 2 r + z 4 e^z w r^2.
@@ -124,11 +137,9 @@ __device__ __forceinline__ float2 dact2(float2 z) {
     if constexpr (ACT == ACT_RELU) return make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
     else if constexpr (ACT == ACT_MISH) {
         const float2 one = make_float2(1.0f, 1.0f);
-        const float2 e = mul2(make_float2(fminf(z.x, 20.0f), fminf(z.y, 20.0f)), make_float2(1.4426950408889634f, 1.4426950408889634f));
-        const float2 n = make_float2(ex2_approx(e.x), ex2_approx(e.y));
+        const float2 n = exp2_clamped(z);
         const float2 w = add2(n, one);
-        const float2 d = fma2(w, w, one);
-        const float2 r = make_float2(rcp_approx(d.x), rcp_approx(d.y));
+        const float2 r = rcp2(fma2(w, w, one));
         const float2 nr = mul2(mul2(n, r), mul2(w, r));
         return fma2(mul2(z, make_float2(4.0f, 4.0f)), nr, fma2(r, make_float2(-2.0f, -2.0f), one));
     } else return make_float2(1.0f, 1.0f);
@@ -157,7 +168,92 @@ struct Cover {
             on = r < R;
         }
     }
+    // pixels of a run of np that this thread takes
+    __device__ __forceinline__ int count(int np) const { return np > r ? (np - r + R - 1) / R : 0; }
 };
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// One vector global -> shared (two-byte vectors through a register).
+template <typename Raw>
+__device__ __forceinline__ void copy_vec(Raw *dst, const Raw *src) {
+    if constexpr (sizeof(Raw) >= 4) copy_async<(int)sizeof(Raw)>(tc::smem_u32(dst), src);
+    else *dst = *src;
+}
+
+// A thread's way through its `cnt` vectors of MAPS maps, s[m] elements apart:
+// batches of four vectors a map in a ring of shared memory slots of its own (so
+// nothing waits for another thread), one batch of two maps or two of one always
+// on the way (cp.async): 128 bytes a thread in flight beside its arithmetic,
+// which registers could not hold.  Pointers advance by addition: with an index multiplied out
+// a vector, the address arithmetic was half of the instructions.  Two-byte
+// vectors, which cp.async does not copy, go through registers.
+constexpr int kBatch = 4;
+__host__ __device__ constexpr int batches(int maps) { return maps == 2 ? 2 : 3; }
+template <typename Raw>
+__host__ __device__ constexpr int ring_bytes(int maps) { return sizeof(Raw) >= 4 ? kBatch * batches(maps) * kThreads * (int)sizeof(Raw) * maps : 0; }
+template <int MAPS, typename Raw, typename T, typename F>
+__device__ __forceinline__ void walk(uint8_t *ring, const T *(&src)[MAPS], const long long (&step)[MAPS], int cnt, F &&use) {
+    if constexpr (sizeof(Raw) >= 4) {
+        Raw *const base = reinterpret_cast<Raw *>(ring) + threadIdx.x;
+        constexpr int kSlot = kThreads * MAPS, kBatches = batches(MAPS);
+        int to = 0, at = 0, left = cnt;  // batch slots to fill and to read, vectors not yet asked for
+        auto ask = [&]() {
+            Raw *d = base + to * (kBatch * kSlot);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (u < left)
+#pragma unroll
+                    for (int m = 0; m < MAPS; ++m) {
+                        copy_vec(d + u * kSlot + m * kThreads, reinterpret_cast<const Raw *>(src[m]));
+                        src[m] += step[m];
+                    }
+            left -= kBatch;
+            copy_commit();
+            if (++to == kBatches) to = 0;
+        };
+#pragma unroll
+        for (int i = 1; i < kBatches; ++i) ask();
+        for (int n = cnt; n > 0; n -= kBatch) {
+            copy_wait<kBatches - 2>();
+            ask();
+            const Raw *d = base + at * (kBatch * kSlot);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (u < n) {
+                    Raw v[MAPS];
+#pragma unroll
+                    for (int m = 0; m < MAPS; ++m) v[m] = d[u * kSlot + m * kThreads];
+                    use(v);
+                }
+            if (++at == kBatches) at = 0;
+        }
+        copy_wait<0>();
+    } else {
+        for (; cnt > 0; cnt -= kBatch) {
+            Raw v[kBatch][MAPS];
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (u < cnt)
+#pragma unroll
+                    for (int m = 0; m < MAPS; ++m) {
+                        v[u][m] = *reinterpret_cast<const Raw *>(src[m]);
+                        src[m] += step[m];
+                    }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (u < cnt) use(v[u]);
+        }
+    }
+}
 
 // The threads' pairs of sums, ent[r * C + c], summed over the R rows: channel c
 // into chan[c] (which may be ent itself only for R = 1).  L lanes a channel.
@@ -234,16 +330,51 @@ __device__ __forceinline__ float2 about(float K, float2 s, float cnt) {
     return make_float2(K + d, fmaxf(s.y - s.x * d, 0.0f) + 0.0f * s.y);  // (NaN stays NaN)
 }
 
-// (mean, M2) of each group over this CTA's run of pixels.
+// Distributed shared memory: another CTA's copy of a variable of this one's.
+__device__ __forceinline__ float2 ld_peer(const float2 *p, uint32_t rank) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(tc::mapa_shared(tc::smem_u32(p), rank)) : "memory");
+    return v;
+}
+// (every thread of the CTA, warps converged)
+__device__ __forceinline__ void cluster_arrive() { __syncwarp(); asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { __syncwarp(); asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// (mean, M2) of a group over `n` consecutive runs of `len` pixels of `total`
+// (the last ones short or empty), run q's from get(q); n <= 8.
+template <typename F>
+__device__ __forceinline__ float2 join_few(int n, int len, int total, int cg, F &&get) {
+    float2 v[8];
+    float mu = 0.0f, m2 = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (q < n) v[q] = get(q);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (q < n) {
+            const float c = (float)max(0, min(len, total - q * len));
+            if (c > 0.0f) mu = fmaf(c, v[q].x, mu);
+        }
+    mu /= (float)min(n * len, total);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (q < n) {
+            const float c = (float)max(0, min(len, total - q * len)) * (float)cg, d = v[q].x - mu;
+            if (c > 0.0f) m2 += fmaf(c * d, d, v[q].y);
+        }
+    return make_float2(mu, m2);
+}
+
+// (mean, M2) of each group over one run of pixels.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) gn_stats_kernel(GnArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) gn_stats_kernel(GnArgs a) {
     using V = Vec<T, VEC>;
     using Raw = typename V::Raw;
-    extern __shared__ float2 sh2[];  // [R*C] sums, [C] channels, then [C] K
+    extern __shared__ __align__(16) uint8_t ring[];  // the ring, then [C] channels, [R*C] sums, [C] K
     const Cover cv(a.C, VEC);
-    float2 *ent = sh2, *chan = ent + cv.R * a.C;
-    float *piv = reinterpret_cast<float *>(chan + a.C);
-    const int n = a.n0 + blockIdx.y, s = blockIdx.x;
+    float2 *chan = reinterpret_cast<float2 *>(ring + ring_bytes<Raw>(1)), *ent = chan + a.C;
+    float *piv = reinterpret_cast<float *>(ent + cv.R * a.C);
+    const int n = blockIdx.y, s = blockIdx.x;
     const int p0 = s * a.ppx, np = min(a.ppx, a.HW - p0);
     pdl_trigger();
     pdl_wait();
@@ -253,16 +384,9 @@ __global__ void __launch_bounds__(kThreads) gn_stats_kernel(GnArgs a) {
             const T *xc = x + col * VEC;
             StatSums<T, VEC> st;
             st.start(*reinterpret_cast<const Raw *>(xc));
-            constexpr int U = 4;
-            int p = cv.r;
-            for (; p + (U - 1) * cv.R < np; p += cv.R * U) {
-                Raw raw[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) raw[u] = *reinterpret_cast<const Raw *>(xc + (p + u * cv.R) * a.px);
-#pragma unroll
-                for (int u = 0; u < U; ++u) st.take(raw[u]);
-            }
-            for (; p < np; p += cv.R) st.take(*reinterpret_cast<const Raw *>(xc + p * a.px));
+            const T *from[1] = {xc + cv.r * a.px};
+            const long long step[1] = {cv.R * a.px};
+            walk<1, Raw>(ring, from, step, cv.count(np), [&](const Raw (&v)[1]) { st.take(v[0]); });
             st.put(ent + cv.r * a.C + col * VEC, piv + col * VEC, cv.r == 0);
         }
     }
@@ -281,8 +405,8 @@ __global__ void __launch_bounds__(kThreads) gn_stats_kernel(GnArgs a) {
 // wait for L2.  Ends with a barrier.
 __device__ __forceinline__ const float2 *stage_runs(const GnArgs &a, int n, float2 *dst) {
     const float2 *src = a.part + (long long)n * a.G * a.S;
+    if ((long long)a.G * a.S > kStageRuns) return src;
     const int total = a.G * a.S;
-    if (total > kStageRuns) return src;
 #pragma unroll 8
     for (int i = threadIdx.x; i < total; i += kThreads) dst[i] = src[i];
     __syncthreads();
@@ -317,21 +441,23 @@ __device__ __forceinline__ void set_lane(float2 (&v)[PAIRS], int e, float f) {
 // taken in the order opposite to the statistics': of maps larger than L2 the
 // last runs read are still there.
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads) gn_apply_kernel(GnArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(GnArgs a) {
     using V = Vec<T, VEC>;
     using Raw = typename V::Raw;
     constexpr int P = V::kPairs;
-    extern __shared__ float2 sh2[];  // [G] (mean, rstd), then [G][S]
-    float2 *stat = sh2;
+    extern __shared__ __align__(16) uint8_t ring[];  // the ring, then [G] (mean, rstd), [G][S]
+    float2 *stat = reinterpret_cast<float2 *>(ring + ring_bytes<Raw>(1));
     const Cover cv(a.C, VEC);
-    const int n = a.n0 + (int)(gridDim.y - 1 - blockIdx.y), s = (int)(gridDim.x - 1 - blockIdx.x);
+    const int n = (int)(gridDim.y - 1 - blockIdx.y), s = (int)(gridDim.x - 1 - blockIdx.x);
     const int p0 = s * a.ppx, np = min(a.ppx, a.HW - p0);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    const float2 *runs = stage_runs(a, n, sh2 + a.G);
+    const T *x = static_cast<const T *>(a.x) + ((long long)n * a.HW + p0) * a.px;
+    T *y = static_cast<T *>(a.out) + ((long long)n * a.HW + p0) * a.pout;
+    const float2 *runs = stage_runs(a, n, stat + a.G);
     for (int g = warp; g < a.G; g += kWarps) {
-        const float2 st = join_runs(a, runs + g * a.S, lane);
+        const float2 st = join_runs(a, runs + (long long)g * a.S, lane);
         if (lane == 0) {
             stat[g] = st;
             if (s == 0) {
@@ -342,8 +468,6 @@ __global__ void __launch_bounds__(kThreads) gn_apply_kernel(GnArgs a) {
     }
     __syncthreads();
     if (!cv.on) return;
-    const T *x = static_cast<const T *>(a.x) + ((long long)n * a.HW + p0) * a.px;
-    T *y = static_cast<T *>(a.out) + ((long long)n * a.HW + p0) * a.pout;
     for (int col = cv.col; col < cv.cvn; col += kThreads) {
         float2 mu[P], sc[P], be[P];  // mu: minus the mean
 #pragma unroll
@@ -354,67 +478,76 @@ __global__ void __launch_bounds__(kThreads) gn_apply_kernel(GnArgs a) {
             set_lane<VEC>(sc, e, st.y * (a.gamma ? a.gamma[c] : 1.0f));
             set_lane<VEC>(be, e, a.beta ? a.beta[c] : 0.0f);
         }
-        auto one = [&](const Raw &raw, int p) {
+        T *o = y + cv.r * a.pout + col * VEC;
+        const long long so = cv.R * a.pout;
+        const T *from[1] = {x + cv.r * a.px + col * VEC};
+        const long long step[1] = {cv.R * a.px};
+        walk<1, Raw>(ring, from, step, cv.count(np), [&](const Raw (&v)[1]) {
             float2 f[P];
-            V::unpack(raw, f);
+            V::unpack(v[0], f);
 #pragma unroll
-            for (int e = 0; e < P; ++e) f[e] = act2<ACT, sizeof(T) == 2>(fma2(add2(f[e], mu[e]), sc[e], be[e]));
-            *reinterpret_cast<Raw *>(y + p * a.pout + col * VEC) = V::pack(f);
-        };
-        constexpr int U = 4;
-        int p = cv.r;
-        for (; p + (U - 1) * cv.R < np; p += cv.R * U) {
-            Raw raw[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) raw[u] = *reinterpret_cast<const Raw *>(x + (p + u * cv.R) * a.px + col * VEC);
-#pragma unroll
-            for (int u = 0; u < U; ++u) one(raw[u], p + u * cv.R);
-        }
-        for (; p < np; p += cv.R) one(*reinterpret_cast<const Raw *>(x + p * a.px + col * VEC), p);
+            for (int e = 0; e < P; ++e) f[e] = act2<ACT>(fma2(add2(f[e], mu[e]), sc[e], be[e]));
+            *reinterpret_cast<Raw *>(o) = V::pack(f);
+            o += so;
+        });
     }
 }
 
-// A thread's per-channel values of the gradient: xhat = x rs + mr, z = xhat ga + be.
+// A thread's per-channel values of the gradient.  With xc = x - mean:
+// z = xc sc + be, sc = rstd gamma; dz = dy act'(z); the sums are of dz and
+// dz xc (rstd is multiplied in at the end); dx = dz sc - c1 - xc c2 with
+// c1 = rstd m1, c2 = rstd^2 m2'.
 template <typename T, int VEC, int ACT>
 struct GradLane {
     using V = Vec<T, VEC>;
     using Raw = typename V::Raw;
     static constexpr int P = V::kPairs;
-    float2 mu[P], rs[P], ga[P], be[P];  // mu: minus the mean
+    float2 nmu[P], sc[P], be[P];  // nmu: minus the mean
     __device__ __forceinline__ void set(const GnArgs &a, int e, int c, float mean, float rstd) {
-        set_lane<VEC>(mu, e, -mean);
-        set_lane<VEC>(rs, e, rstd);
-        set_lane<VEC>(ga, e, a.gamma ? a.gamma[c] : 1.0f);
+        set_lane<VEC>(nmu, e, -mean);
+        set_lane<VEC>(sc, e, rstd * (a.gamma ? a.gamma[c] : 1.0f));
         set_lane<VEC>(be, e, a.beta ? a.beta[c] : 0.0f);
     }
-    __device__ __forceinline__ void eval(const Raw &rx, const Raw &rd, float2 (&xh)[P], float2 (&dz)[P]) const {
-        V::unpack(rx, xh);
+    __device__ __forceinline__ void eval(const Raw &rx, const Raw &rd, float2 (&xc)[P], float2 (&dz)[P]) const {
+        V::unpack(rx, xc);
         V::unpack(rd, dz);
 #pragma unroll
         for (int e = 0; e < P; ++e) {
-            xh[e] = mul2(add2(xh[e], mu[e]), rs[e]);
-            if (ACT != ACT_NONE) dz[e] = mul2(dz[e], dact2<ACT>(fma2(xh[e], ga[e], be[e])));
+            xc[e] = add2(xc[e], nmu[e]);
+            if (ACT != ACT_NONE) dz[e] = mul2(dz[e], dact2<ACT>(fma2(xc[e], sc[e], be[e])));
         }
     }
-    // A += dz, B += dz xhat
+    // A += dz, B += dz xc
     __device__ __forceinline__ void sums(const Raw &rx, const Raw &rd, float2 (&A)[P], float2 (&B)[P]) const {
-        float2 xh[P], dz[P];
-        eval(rx, rd, xh, dz);
+        float2 xc[P], dz[P];
+        eval(rx, rd, xc, dz);
 #pragma unroll
         for (int e = 0; e < P; ++e) {
             A[e] = add2(A[e], dz[e]);
-            B[e] = fma2(dz[e], xh[e], B[e]);
+            B[e] = fma2(dz[e], xc[e], B[e]);
         }
     }
-    // rstd (gamma dz - m1 - xhat m2), nm1 and nm2 the negated means
-    __device__ __forceinline__ Raw dx(const Raw &rx, const Raw &rd, const float2 (&nm1)[P], const float2 (&nm2)[P]) const {
-        float2 xh[P], dz[P];
-        eval(rx, rd, xh, dz);
+    // dx, nc1 and nc2 the negated c1 and c2
+    __device__ __forceinline__ Raw dx(const Raw &rx, const Raw &rd, const float2 (&nc1)[P], const float2 (&nc2)[P]) const {
+        float2 xc[P], dz[P];
+        eval(rx, rd, xc, dz);
 #pragma unroll
-        for (int e = 0; e < P; ++e) xh[e] = mul2(rs[e], fma2(xh[e], nm2[e], fma2(ga[e], dz[e], nm1[e])));
-        return V::pack(xh);
+        for (int e = 0; e < P; ++e) xc[e] = fma2(xc[e], nc2[e], fma2(dz[e], sc[e], nc1[e]));
+        return V::pack(xc);
     }
 };
+// A group's sums of gamma times its channels'; every lane of the calling warp
+// returns it.  c0: the group's first channel.
+__device__ __forceinline__ float2 join_gamma(const GnArgs &a, const float2 *chan, int c0, int lane) {
+    float2 v = make_float2(0.0f, 0.0f);
+    for (int c = lane; c < a.cg; c += 32) {
+        const float w = a.gamma ? a.gamma[c0 + c] : 1.0f;
+        const float2 u = chan[c];
+        v.x = fmaf(w, u.x, v.x);
+        v.y = fmaf(w, u.y, v.y);
+    }
+    return make_float2(warp_sum(v.x), warp_sum(v.y));
+}
 template <int VEC, int P>
 __device__ __forceinline__ void put_sums(float2 *ent, const float2 (&A)[P], const float2 (&B)[P]) {
 #pragma unroll
@@ -424,14 +557,14 @@ __device__ __forceinline__ void put_sums(float2 *ent, const float2 (&A)[P], cons
 // Sums of dz and dz xhat per channel, and of gamma times them per group, over
 // one run of pixels.
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(GnArgs a) {
+__global__ void __launch_bounds__(kThreads, grad_ctas(sizeof(T))) gn_bwd_sums_kernel(GnArgs a) {
     using L = GradLane<T, VEC, ACT>;
     using Raw = typename L::Raw;
     constexpr int P = L::P;
-    extern __shared__ float2 sh2[];  // [R*C], then [C]
+    extern __shared__ __align__(16) uint8_t ring[];  // the ring, then [C] channels, [R*C] sums
     const Cover cv(a.C, VEC);
-    float2 *ent = sh2, *chan = ent + cv.R * a.C;
-    const int n = a.n0 + blockIdx.y, s = blockIdx.x;
+    float2 *chan = reinterpret_cast<float2 *>(ring + ring_bytes<Raw>(2)), *ent = chan + a.C;
+    const int n = blockIdx.y, s = blockIdx.x;
     const int p0 = s * a.ppx, np = min(a.ppx, a.HW - p0);
     pdl_trigger();
     pdl_wait();
@@ -449,38 +582,22 @@ __global__ void __launch_bounds__(kThreads) gn_bwd_sums_kernel(GnArgs a) {
             }
 #pragma unroll
             for (int e = 0; e < P; ++e) A[e] = B[e] = make_float2(0.0f, 0.0f);
-            constexpr int U = 2;
-            int p = cv.r;
-            for (; p + (U - 1) * cv.R < np; p += cv.R * U) {
-                Raw rx[U], rd[U];
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    rx[u] = *reinterpret_cast<const Raw *>(x + (p + u * cv.R) * a.px + col * VEC);
-                    rd[u] = *reinterpret_cast<const Raw *>(dy + (p + u * cv.R) * a.pdy + col * VEC);
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) ln.sums(rx[u], rd[u], A, B);
-            }
-            for (; p < np; p += cv.R)
-                ln.sums(*reinterpret_cast<const Raw *>(x + p * a.px + col * VEC),
-                        *reinterpret_cast<const Raw *>(dy + p * a.pdy + col * VEC), A, B);
+            const T *from[2] = {x + cv.r * a.px + col * VEC, dy + cv.r * a.pdy + col * VEC};
+            const long long step[2] = {cv.R * a.px, cv.R * a.pdy};
+            walk<2, Raw>(ring, from, step, cv.count(np), [&](const Raw (&v)[2]) { ln.sums(v[0], v[1], A, B); });
             put_sums<VEC>(ent + cv.r * a.C + col * VEC, A, B);
         }
     }
     __syncthreads();
     float2 *pc = a.partc + ((long long)n * a.S + s) * a.C;
     join_rows(ent, cv.R, a.C, [&](int c, float2 v) {
-        pc[c] = v;
-        const float ga = a.gamma ? a.gamma[c] : 1.0f;
-        chan[c] = make_float2(ga * v.x, ga * v.y);
+        v.y *= a.rstd[(long long)n * a.G + c / a.cg];
+        pc[c] = chan[c] = v;
     });
     __syncthreads();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int g = warp; g < a.G; g += kWarps) {
-        float2 v = make_float2(0.0f, 0.0f);
-        for (int c = lane; c < a.cg; c += 32) v = add2(v, chan[g * a.cg + c]);
-        v.x = warp_sum(v.x);
-        v.y = warp_sum(v.y);
+        const float2 v = join_gamma(a, chan + g * a.cg, g * a.cg, lane);
         if (lane == 0) a.part[((long long)n * a.G + g) * a.S + s] = v;
     }
 }
@@ -515,102 +632,67 @@ __device__ __forceinline__ void join_rows_of_channels(const GnArgs &a, long long
 // `head` (0 or 1) grid rows join the channels' sums of every image and run into
 // dgamma and dbeta, 32 channels a CTA.
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads) gn_bwd_dx_kernel(GnArgs a, int head) {
+__global__ void __launch_bounds__(kThreads, grad_ctas(sizeof(T))) gn_bwd_dx_kernel(GnArgs a, int head) {
     using L = GradLane<T, VEC, ACT>;
     using Raw = typename L::Raw;
     constexpr int P = L::P;
-    extern __shared__ float2 sh2[];  // [G] minus (s1, s2) / m and [G][S], or [kWarps][32]
+    extern __shared__ __align__(16) uint8_t ring[];  // the ring, then [G] minus c1 and c2, [G][S]; or [kWarps][32] sums
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
     if ((int)blockIdx.y < head) {
-        join_rows_of_channels(a, (long long)a.N * a.S, blockIdx.x, gridDim.x, sh2);
+        join_rows_of_channels(a, (long long)a.N * a.S, blockIdx.x, gridDim.x, reinterpret_cast<float2 *>(ring));
         return;
     }
-    float2 *sum = sh2;
+    float2 *sum = reinterpret_cast<float2 *>(ring + ring_bytes<Raw>(2));
     const Cover cv(a.C, VEC);
-    const int n = a.n0 + (int)(gridDim.y - 1 - blockIdx.y), s = (int)(gridDim.x - 1 - blockIdx.x);
+    const int n = (int)(gridDim.y - 1 - blockIdx.y), s = (int)(gridDim.x - 1 - blockIdx.x);
     const int p0 = s * a.ppx, np = min(a.ppx, a.HW - p0);
+    const T *x = static_cast<const T *>(a.x) + ((long long)n * a.HW + p0) * a.px;
+    const T *dy = static_cast<const T *>(a.dy) + ((long long)n * a.HW + p0) * a.pdy;
+    T *dx = static_cast<T *>(a.out) + ((long long)n * a.HW + p0) * a.pout;
     const float inv = -1.0f / ((float)a.HW * (float)a.cg);
-    const float2 *runs = stage_runs(a, n, sh2 + a.G);
+    const float2 *runs = stage_runs(a, n, sum + a.G);
     for (int g = warp; g < a.G; g += kWarps) {
-        const float2 *p = runs + g * a.S;
+        const float2 *p = runs + (long long)g * a.S;
         float2 v = make_float2(0.0f, 0.0f);
         for (int q = lane; q < a.S; q += 32) v = add2(v, p[q]);
         v.x = warp_sum(v.x);
         v.y = warp_sum(v.y);
-        if (lane == 0) sum[g] = make_float2(v.x * inv, v.y * inv);
+        const float rs = a.rstd[(long long)n * a.G + g];
+        if (lane == 0) sum[g] = make_float2(v.x * inv * rs, v.y * inv * rs * rs);
     }
     __syncthreads();
     if (!cv.on) return;
-    const T *x = static_cast<const T *>(a.x) + ((long long)n * a.HW + p0) * a.px;
-    const T *dy = static_cast<const T *>(a.dy) + ((long long)n * a.HW + p0) * a.pdy;
-    T *dx = static_cast<T *>(a.out) + ((long long)n * a.HW + p0) * a.pout;
     for (int col = cv.col; col < cv.cvn; col += kThreads) {
         L ln;
-        float2 m1[P], m2[P];
+        float2 c1[P], c2[P];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const int c = col * VEC + e, g = c / a.cg;
             ln.set(a, e, c, a.mean[(long long)n * a.G + g], a.rstd[(long long)n * a.G + g]);
-            set_lane<VEC>(m1, e, sum[g].x);
-            set_lane<VEC>(m2, e, sum[g].y);
+            set_lane<VEC>(c1, e, sum[g].x);
+            set_lane<VEC>(c2, e, sum[g].y);
         }
-        constexpr int U = 2;
-        int p = cv.r;
-        for (; p + (U - 1) * cv.R < np; p += cv.R * U) {
-            Raw rx[U], rd[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                rx[u] = *reinterpret_cast<const Raw *>(x + (p + u * cv.R) * a.px + col * VEC);
-                rd[u] = *reinterpret_cast<const Raw *>(dy + (p + u * cv.R) * a.pdy + col * VEC);
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                *reinterpret_cast<Raw *>(dx + (p + u * cv.R) * a.pout + col * VEC) = ln.dx(rx[u], rd[u], m1, m2);
-        }
-        for (; p < np; p += cv.R)
-            *reinterpret_cast<Raw *>(dx + p * a.pout + col * VEC) =
-                ln.dx(*reinterpret_cast<const Raw *>(x + p * a.px + col * VEC),
-                      *reinterpret_cast<const Raw *>(dy + p * a.pdy + col * VEC), m1, m2);
+        T *o = dx + cv.r * a.pout + col * VEC;
+        const long long so = cv.R * a.pout;
+        const T *from[2] = {x + cv.r * a.px + col * VEC, dy + cv.r * a.pdy + col * VEC};
+        const long long step[2] = {cv.R * a.px, cv.R * a.pdy};
+        walk<2, Raw>(ring, from, step, cv.count(np), [&](const Raw (&v)[2]) {
+            *reinterpret_cast<Raw *>(o) = ln.dx(v[0], v[1], c1, c2);
+            o += so;
+        });
     }
 }
 
-
-// ------------------------------------------------------------ resident kernels
-// Where a few groups of an image fit the shared memory of a cluster, one launch
-// does all: each CTA copies its run of pixels of gb groups to shared memory
-// (cp.async, the whole run in flight at once), sums it, exchanges the groups'
-// sums with the cluster's other CTAs (8 bytes a group, through distributed
-// shared memory) and finishes from shared memory: every byte crosses HBM and
-// L2 once, nothing goes through a workspace.  A thread reads back only what it
-// copied itself.
-
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
-template <int LEFT>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ float2 ld_peer(const float2 *p, uint32_t rank) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(tc::mapa_shared(tc::smem_u32(p), rank)) : "memory");
-    return v;
-}
-// (every thread of the CTA, warps converged)
-__device__ __forceinline__ void cluster_arrive() { __syncwarp(); asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { __syncwarp(); asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
-// One vector global -> shared (two-byte vectors through a register).
-template <typename Raw>
-__device__ __forceinline__ void copy_vec(Raw *dst, const Raw *src) {
-    if constexpr (sizeof(Raw) >= 4) copy_async<(int)sizeof(Raw)>(tc::smem_u32(dst), src);
-    else *dst = *src;
-}
+// ------------------------------------------------------------- cluster kernels
+// One launch where a few groups of an image fit a cluster: its K
+// CTAs take gb groups of an image (gradient: of every image), each CTA a run of
+// pixels.  Each sums its run, exchanges the groups' sums with the cluster's
+// other CTAs (8 bytes a group, through distributed shared memory) and finishes
+// its run, which waits in shared memory meanwhile (cp.async, the whole run in
+// flight at once; a thread reads back only what it copied itself): every byte
+// crosses HBM and L2 once.
 
 // Rows that a CTA's sums leave in shared memory: one a warp where a warp's
 // lanes cover whole pixels (folded with shuffles first), else one a thread row.
@@ -626,7 +708,7 @@ __device__ __forceinline__ void fold(float2 (&v)[P], int cvn) {
 }
 
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads, 2) gn_resident_kernel(GnArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) gn_cluster_kernel(GnArgs a) {
     using V = Vec<T, VEC>;
     using Raw = typename V::Raw;
     constexpr int P = V::kPairs;
@@ -647,31 +729,28 @@ __global__ void __launch_bounds__(kThreads, 2) gn_resident_kernel(GnArgs a) {
     pdl_trigger();
     pdl_wait();
     const T *x = static_cast<const T *>(a.x) + ((long long)n * a.HW + p0) * a.px + c0 + cv.col * VEC;
-    Raw *mine = data + cv.col;
+    // this thread's vectors lie kThreads (of which R cvn are at work) apart
+    Raw *mine = data + threadIdx.x;
+    const int cnt = cv.on ? cv.count(np) : 0, step = cv.R * cv.cvn;
     StatSums<T, VEC> st;
-    float2 ga[P], be[P];
     // the run in four parts, each summed as it lands
-    const int part = ((np + cv.R - 1) / cv.R + 3) / 4 * cv.R;
+    const int part = (cnt + 3) / 4;
+    const T *from = x + cv.r * a.px;
+    const long long sx = cv.R * a.px;
+    Raw *to = mine;
     auto load = [&](int q) {
-        if (cv.on)
-            for (int p = q * part + cv.r; p < min(np, (q + 1) * part); p += cv.R)
-                copy_vec(mine + p * cv.cvn, reinterpret_cast<const Raw *>(x + p * a.px));
+#pragma unroll 4
+        for (int i = min(part, cnt - q * part); i > 0; --i, from += sx, to += step) copy_vec(to, reinterpret_cast<const Raw *>(from));
         copy_commit();
     };
+    const Raw *at = mine;
     auto take = [&](int q) {
-        if (cv.on)
-            for (int p = q * part + cv.r; p < min(np, (q + 1) * part); p += cv.R) st.take(mine[p * cv.cvn]);
+#pragma unroll 4
+        for (int i = min(part, cnt - q * part); i > 0; --i, at += step) st.take(*at);
     };
     load(0); load(1); load(2); load(3);
     Raw first = {};
     if (cv.on) first = *reinterpret_cast<const Raw *>(x);
-    if (cv.on)
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int c = c0 + cv.col * VEC + e;
-            set_lane<VEC>(ga, e, a.gamma ? a.gamma[c] : 1.0f);
-            set_lane<VEC>(be, e, a.beta ? a.beta[c] : 0.0f);
-        }
     st.start(first);
     copy_wait<3>(); take(0);
     copy_wait<2>(); take(1);
@@ -691,6 +770,14 @@ __global__ void __launch_bounds__(kThreads, 2) gn_resident_kernel(GnArgs a) {
         const float2 v = join_channels(chan + g * a.cg, a.cg, (float)np, lane);
         if (lane == 0) gpart[g] = v;
     }
+    float2 ga[P], be[P];
+    if (cv.on)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int c = c0 + cv.col * VEC + e;
+            set_lane<VEC>(ga, e, a.gamma ? a.gamma[c] : 1.0f);
+            set_lane<VEC>(be, e, a.beta ? a.beta[c] : 0.0f);
+        }
     if (a.K > 1) {
         cluster_arrive();
         cluster_wait();
@@ -698,28 +785,11 @@ __global__ void __launch_bounds__(kThreads, 2) gn_resident_kernel(GnArgs a) {
         __syncthreads();
     }
     for (int g = threadIdx.x; g < gb; g += kThreads) {
-        const float inv = 1.0f / ((float)a.HW * (float)a.cg);
-        float mu = 0.0f, m2 = 0.0f;
-        if (a.K > 1) {
-            float2 v[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (q < a.K) v[q] = ld_peer(gpart + g, q);
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (q < a.K) mu += (float)min(a.ppx, a.HW - q * a.ppx) * (float)a.cg * v[q].x;
-            mu *= inv;
-#pragma unroll
-            for (int q = 0; q < 8; ++q)
-                if (q < a.K) m2 += v[q].y + (float)min(a.ppx, a.HW - q * a.ppx) * (float)a.cg * (v[q].x - mu) * (v[q].x - mu);
-        } else {
-            mu = gpart[g].x;
-            m2 = gpart[g].y;
-        }
-        const float rstd = 1.0f / sqrtf(m2 * inv + a.eps);
-        stat[g] = make_float2(mu, rstd);
+        const float2 v = a.K > 1 ? join_few(a.K, a.ppx, a.HW, a.cg, [&](int q) { return ld_peer(gpart + g, q); }) : gpart[g];
+        const float rstd = 1.0f / sqrtf(v.y / ((float)a.HW * (float)a.cg) + a.eps);
+        stat[g] = make_float2(v.x, rstd);
         if (k == 0) {
-            if (a.mean) a.mean[(long long)n * a.G + g0 + g] = mu;
+            if (a.mean) a.mean[(long long)n * a.G + g0 + g] = v.x;
             if (a.rstd) a.rstd[(long long)n * a.G + g0 + g] = rstd;
         }
     }
@@ -733,39 +803,41 @@ __global__ void __launch_bounds__(kThreads, 2) gn_resident_kernel(GnArgs a) {
             set_lane<VEC>(mu, e, -s.x);
             set_lane<VEC>(ga, e, (e % 2 ? ga[e / 2].y : ga[e / 2].x) * s.y);
         }
-        T *y = static_cast<T *>(a.out) + ((long long)n * a.HW + p0) * a.pout + c0 + cv.col * VEC;
-#pragma unroll 4
-        for (int p = cv.r; p < np; p += cv.R) {
+        T *y = static_cast<T *>(a.out) + ((long long)n * a.HW + p0 + cv.r) * a.pout + c0 + cv.col * VEC;
+        const long long so = cv.R * a.pout;
+        auto one = [&](const Raw &v) {
             float2 f[P];
-            V::unpack(mine[p * cv.cvn], f);
+            V::unpack(v, f);
 #pragma unroll
-            for (int e = 0; e < P; ++e) f[e] = act2<ACT, sizeof(T) == 2>(fma2(add2(f[e], mu[e]), ga[e], be[e]));
-            *reinterpret_cast<Raw *>(y + p * a.pout) = V::pack(f);
-        }
+            for (int e = 0; e < P; ++e) f[e] = act2<ACT>(fma2(add2(f[e], mu[e]), ga[e], be[e]));
+            *reinterpret_cast<Raw *>(y) = V::pack(f);
+            y += so;
+        };
+        const Raw *v = mine;
+#pragma unroll 4
+        for (int i = cnt; i > 0; --i, v += step) one(*v);
     }
     if (a.K > 1) cluster_wait();  // no CTA leaves while its sums may be read
 }
 
-// The gradient: a cluster holds K CTAs of each of NI images; where NI is every
-// image, dgamma and dbeta are complete in the cluster, else each image's sums
-// go to partc[n][C] (S = 1) and gn_bwd_join_kernel adds them.
+// The gradient: a cluster holds K CTAs of every image, so that dgamma and dbeta
+// are complete in it.
 template <typename T, int VEC, int ACT>
-__global__ void __launch_bounds__(kThreads, 2) gn_bwd_resident_kernel(GnArgs a) {
+__global__ void __launch_bounds__(kThreads, 3) gn_bwd_cluster_kernel(GnArgs a) {
     using L = GradLane<T, VEC, ACT>;
     using V = Vec<T, VEC>;
     using Raw = typename V::Raw;
     constexpr int P = V::kPairs;
     extern __shared__ __align__(16) uint8_t shm[];
     const int g0 = blockIdx.y * a.gb, gb = min(a.gb, a.G - g0), cb = gb * a.cg, c0 = g0 * a.cg;
-    const int img = blockIdx.x / a.K, k = blockIdx.x - img * a.K;  // blockIdx.x: the rank in the cluster
-    const int n = blockIdx.z * a.NI + img;
+    const int n = blockIdx.x / a.K, k = blockIdx.x - n * a.K;  // blockIdx.x: the rank in the cluster
     const int p0 = k * a.ppx, np = min(a.ppx, a.HW - p0);
     const Cover cv(cb, VEC);
     const bool fl = folds(cv.cvn);
     const int rows = fl ? kWarps : cv.R;
-    const int size = a.K * a.NI;
+    const int size = a.K * a.N;
     float2 *gpart = reinterpret_cast<float2 *>(shm);  // [gb] this CTA's sums of gamma dz, gamma dz xhat
-    float2 *sum = gpart + a.gb;                       // [gb] minus the image's, over m
+    float2 *sum = gpart + a.gb;                       // [gb] minus c1 and c2 of the image
     float2 *chan = sum + a.gb;                        // [cb] this CTA's sums of dz, dz xhat
     float2 *ent = chan + a.cb;                        // [rows][cb], at most a.ent
     Raw *data = reinterpret_cast<Raw *>((reinterpret_cast<uintptr_t>(ent + a.ent) + 15) & ~(uintptr_t)15);
@@ -774,23 +846,28 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_resident_kernel(GnArgs a) 
     pdl_wait();
     const T *x = static_cast<const T *>(a.x) + ((long long)n * a.HW + p0) * a.px + c0 + cv.col * VEC;
     const T *dy = static_cast<const T *>(a.dy) + ((long long)n * a.HW + p0) * a.pdy + c0 + cv.col * VEC;
-    Raw *mx = data + cv.col, *md = mx + a.ppx * cv.cvn;
+    Raw *mx = data + threadIdx.x, *md = mx + a.ppx * cv.cvn;
+    const int cnt = cv.on ? cv.count(np) : 0, step = cv.R * cv.cvn;
     L ln;
     float2 A[P], B[P];
 #pragma unroll
     for (int e = 0; e < P; ++e) A[e] = B[e] = make_float2(0.0f, 0.0f);
-    const int part = ((np + cv.R - 1) / cv.R + 3) / 4 * cv.R;
+    const int part = (cnt + 3) / 4;
+    const T *fx = x + cv.r * a.px, *fd = dy + cv.r * a.pdy;
+    const long long sx = cv.R * a.px, sd = cv.R * a.pdy;
+    Raw *to = mx, *td = md;
     auto load = [&](int q) {
-        if (cv.on)
-            for (int p = q * part + cv.r; p < min(np, (q + 1) * part); p += cv.R) {
-                copy_vec(mx + p * cv.cvn, reinterpret_cast<const Raw *>(x + p * a.px));
-                copy_vec(md + p * cv.cvn, reinterpret_cast<const Raw *>(dy + p * a.pdy));
-            }
+#pragma unroll 2
+        for (int i = min(part, cnt - q * part); i > 0; --i, fx += sx, fd += sd, to += step, td += step) {
+            copy_vec(to, reinterpret_cast<const Raw *>(fx));
+            copy_vec(td, reinterpret_cast<const Raw *>(fd));
+        }
         copy_commit();
     };
+    const Raw *at = mx, *ad = md;
     auto take = [&](int q) {
-        if (cv.on)
-            for (int p = q * part + cv.r; p < min(np, (q + 1) * part); p += cv.R) ln.sums(mx[p * cv.cvn], md[p * cv.cvn], A, B);
+#pragma unroll 2
+        for (int i = min(part, cnt - q * part); i > 0; --i, at += step, ad += step) ln.sums(*at, *ad, A, B);
     };
     load(0); load(1); load(2); load(3);
     if (cv.on)
@@ -812,18 +889,12 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_resident_kernel(GnArgs a) 
         put_sums<VEC>(ent + cv.r * cb + cv.col * VEC, A, B);
     }
     __syncthreads();
-    join_rows(ent, rows, cb, [&](int c, float2 v) { chan[c] = v; });
+    join_rows(ent, rows, cb, [&](int c, float2 v) {
+        chan[c] = make_float2(v.x, v.y * a.rstd[(long long)n * a.G + g0 + c / a.cg]);
+    });
     __syncthreads();
     for (int g = warp; g < gb; g += kWarps) {
-        float2 v = make_float2(0.0f, 0.0f);
-        for (int c = lane; c < a.cg; c += 32) {
-            const float w = a.gamma ? a.gamma[c0 + g * a.cg + c] : 1.0f;
-            const float2 u = chan[g * a.cg + c];
-            v.x = fmaf(w, u.x, v.x);
-            v.y = fmaf(w, u.y, v.y);
-        }
-        v.x = warp_sum(v.x);
-        v.y = warp_sum(v.y);
+        const float2 v = join_gamma(a, chan + g * a.cg, c0 + g * a.cg, lane);
         if (lane == 0) gpart[g] = v;
     }
     if (size > 1) {
@@ -835,24 +906,17 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_resident_kernel(GnArgs a) 
     const float inv = -1.0f / ((float)a.HW * (float)a.cg);
     for (int g = threadIdx.x; g < gb; g += kThreads) {
         float2 v = make_float2(0.0f, 0.0f);
-        for (int q = 0; q < a.K; ++q) v = add2(v, size > 1 ? ld_peer(gpart + g, img * a.K + q) : gpart[g]);
-        sum[g] = make_float2(v.x * inv, v.y * inv);
+        for (int q = 0; q < a.K; ++q) v = add2(v, size > 1 ? ld_peer(gpart + g, n * a.K + q) : gpart[g]);
+        const float rs = a.rstd[(long long)n * a.G + g0 + g];
+        sum[g] = make_float2(v.x * inv * rs, v.y * inv * rs * rs);
     }
-    // the channels' sums: of the whole batch, or of this image
-    const bool all = a.NI == a.N;
-    if ((a.dgamma || a.dbeta) && k == 0 && (!all || img == 0)) {
-        const int q0 = all ? 0 : img * a.K, q1 = all ? size : q0 + a.K;
+    if ((a.dgamma || a.dbeta) && blockIdx.x == 0)
         for (int c = threadIdx.x; c < cb; c += kThreads) {
             float2 v = make_float2(0.0f, 0.0f);
-            for (int q = q0; q < q1; ++q) v = add2(v, size > 1 ? ld_peer(chan + c, q) : chan[c]);
-            if (all) {
-                if (a.dbeta) a.dbeta[c0 + c] = v.x;
-                if (a.dgamma) a.dgamma[c0 + c] = v.y;
-            } else {
-                a.partc[(long long)n * a.C + c0 + c] = v;
-            }
+            for (int q = 0; q < size; ++q) v = add2(v, size > 1 ? ld_peer(chan + c, q) : chan[c]);
+            if (a.dbeta) a.dbeta[c0 + c] = v.x;
+            if (a.dgamma) a.dgamma[c0 + c] = v.y;
         }
-    }
     __syncthreads();
     if (size > 1) cluster_arrive();
     if (cv.on) {
@@ -863,48 +927,37 @@ __global__ void __launch_bounds__(kThreads, 2) gn_bwd_resident_kernel(GnArgs a) 
             set_lane<VEC>(m1, e, s.x);
             set_lane<VEC>(m2, e, s.y);
         }
-        T *dx = static_cast<T *>(a.out) + ((long long)n * a.HW + p0) * a.pout + c0 + cv.col * VEC;
+        T *dx = static_cast<T *>(a.out) + ((long long)n * a.HW + p0 + cv.r) * a.pout + c0 + cv.col * VEC;
+        const long long so = cv.R * a.pout;
+        auto one = [&](const Raw &v, const Raw &w) {
+            *reinterpret_cast<Raw *>(dx) = ln.dx(v, w, m1, m2);
+            dx += so;
+        };
+        const Raw *v = mx, *w = md;
 #pragma unroll 2
-        for (int p = cv.r; p < np; p += cv.R) *reinterpret_cast<Raw *>(dx + p * a.pout) = ln.dx(mx[p * cv.cvn], md[p * cv.cvn], m1, m2);
+        for (int i = cnt; i > 0; --i, v += step, w += step) one(*v, *w);
     }
     if (size > 1) cluster_wait();
 }
 
-__global__ void __launch_bounds__(kThreads) gn_bwd_join_kernel(GnArgs a) {
-    __shared__ float2 red[kWarps * 32];
-    pdl_trigger();
-    pdl_wait();
-    join_rows_of_channels(a, (long long)a.N * a.S, blockIdx.x, gridDim.x, red);
-}
-
 // ------------------------------------------------------------------ host side
-enum { K_STATS, K_APPLY, K_SUMS, K_DX, K_RES, K_RES_BWD };
+enum { K_STATS, K_APPLY, K_SUMS, K_DX, K_CLUSTER, K_CLUSTER_BWD };
 
-template <typename T, int VEC>
-const void *pick(int which, int act) {
+template <typename T, int VEC, int ACT>
+const void *pick_act(int which) {
     switch (which) {
     case K_STATS: return (const void *)&gn_stats_kernel<T, VEC>;
-    case K_APPLY:
-        return act == ACT_MISH ? (const void *)&gn_apply_kernel<T, VEC, ACT_MISH>
-                               : (act == ACT_RELU ? (const void *)&gn_apply_kernel<T, VEC, ACT_RELU>
-                                                  : (const void *)&gn_apply_kernel<T, VEC, ACT_NONE>);
-    case K_SUMS:
-        return act == ACT_MISH ? (const void *)&gn_bwd_sums_kernel<T, VEC, ACT_MISH>
-                               : (act == ACT_RELU ? (const void *)&gn_bwd_sums_kernel<T, VEC, ACT_RELU>
-                                                  : (const void *)&gn_bwd_sums_kernel<T, VEC, ACT_NONE>);
-    case K_RES:
-        return act == ACT_MISH ? (const void *)&gn_resident_kernel<T, VEC, ACT_MISH>
-                               : (act == ACT_RELU ? (const void *)&gn_resident_kernel<T, VEC, ACT_RELU>
-                                                  : (const void *)&gn_resident_kernel<T, VEC, ACT_NONE>);
-    case K_RES_BWD:
-        return act == ACT_MISH ? (const void *)&gn_bwd_resident_kernel<T, VEC, ACT_MISH>
-                               : (act == ACT_RELU ? (const void *)&gn_bwd_resident_kernel<T, VEC, ACT_RELU>
-                                                  : (const void *)&gn_bwd_resident_kernel<T, VEC, ACT_NONE>);
-    default:
-        return act == ACT_MISH ? (const void *)&gn_bwd_dx_kernel<T, VEC, ACT_MISH>
-                               : (act == ACT_RELU ? (const void *)&gn_bwd_dx_kernel<T, VEC, ACT_RELU>
-                                                  : (const void *)&gn_bwd_dx_kernel<T, VEC, ACT_NONE>);
+    case K_APPLY: return (const void *)&gn_apply_kernel<T, VEC, ACT>;
+    case K_SUMS: return (const void *)&gn_bwd_sums_kernel<T, VEC, ACT>;
+    case K_DX: return (const void *)&gn_bwd_dx_kernel<T, VEC, ACT>;
+    case K_CLUSTER: return (const void *)&gn_cluster_kernel<T, VEC, ACT>;
+    default: return (const void *)&gn_bwd_cluster_kernel<T, VEC, ACT>;
     }
+}
+template <typename T, int VEC>
+const void *pick(int which, int act) {
+    return act == ACT_MISH ? pick_act<T, VEC, ACT_MISH>(which)
+                           : (act == ACT_RELU ? pick_act<T, VEC, ACT_RELU>(which) : pick_act<T, VEC, ACT_NONE>(which));
 }
 
 const void *pick_kernel(int which, conv_dtype_t dt, int vec, int act) {
@@ -959,45 +1012,45 @@ bool bad_f32(const void *t) { return t && ((uintptr_t)t & 3u); }
 GnArgs base_args(const conv_plan *p, const GnGeom::Dir &d, const void *x, long long px, void *out, long long pout, void *ws) {
     GnArgs a = {};
     a.x = x; a.px = px; a.out = out; a.pout = pout;
-    a.N = p->s.n; a.n0 = 0; a.HW = p->s.h * p->s.w; a.C = p->s.c_in; a.G = p->groups; a.cg = p->s.c_in / p->groups;
+    a.N = p->s.n; a.HW = p->s.h * p->s.w; a.C = p->s.c_in; a.G = p->groups; a.cg = p->s.c_in / p->groups;
     a.S = d.S; a.ppx = d.ppx; a.eps = p->gn.eps;
     a.part = static_cast<float2 *>(ws);
     a.partc = a.part + (long long)a.N * a.S * a.G;
     return a;
 }
 
-// The resident form of a run, and its shared memory.  The last CTA of a map
-// may have fewer channels than the others and then more thread rows: the sums'
+// The cluster form of a run, and its shared memory.  The last CTA of a map may
+// have fewer channels than the others and then more thread rows: the sums'
 // entries are the larger of the two counts.
-size_t resident_args(const GnGeom::Dir &d, int vec, int es, int maps, GnArgs &a) {
-    a.gb = d.gb; a.cb = d.cb; a.K = d.K; a.NI = d.NI; a.ppx = d.rppx;
+size_t cluster_args(const GnGeom::Dir &d, int vec, int es, int maps, GnArgs &a) {
+    a.gb = d.gb; a.cb = d.cb; a.K = d.K; a.ppx = d.cpx;
     auto entries = [&](int cb) { return (folds(cb / vec) ? kWarps : rows_for(cb, vec)) * cb; };
     const int last = (a.G - (a.G - 1) / a.gb * a.gb) * a.cg;
     a.ent = entries(a.cb) > entries(last) ? entries(a.cb) : entries(last);
-    return (size_t)2 * a.gb * 8 + (size_t)a.cb * 8 + (size_t)a.ent * 8 + (size_t)a.cb * 4 + 16 + (size_t)a.ppx * a.cb * es * maps;
+    return (size_t)2 * a.gb * 8 + (size_t)a.cb * 8 + (size_t)a.ent * 8 + (size_t)a.cb * 4 + 16 +
+           (size_t)a.ppx * a.cb * es * maps;
 }
-bool resident(const GnGeom::Dir &d, int vec) { return d.K > 0 && d.cb / vec <= kThreads; }
+bool clustered(const GnGeom::Dir &d, int vec) { return d.K > 0 && d.cb / vec <= kThreads; }
 
 // How one direction runs.  `maps`: input maps it reads (1, or x and dy).
 void plan_direction(const conv_plan *p, int maps, GnGeom::Dir &d, size_t &ws) {
     const int es = conv_esize(p->dtype), C = p->s.c_in, G = p->groups, cg = C / G, HW = p->s.h * p->s.w, N = p->s.n;
     const int wide = 16 / es, au = C % wide == 0 ? wide : (C % 2 == 0 && es == 2 ? 2 : 1);  // the widest vector there can be
-    // Two launches: as many images a pass as keep what the second launch reads
-    // again in L2, each in runs of pixels: four CTAs a SM over the pass, at
-    // least four pixels a thread.
-    const long long image = (long long)HW * C * es * maps;
-    d.step = (int)(kL2Bytes / image < 1 ? 1 : (kL2Bytes / image < N ? kL2Bytes / image : N));
+    // Two launches: runs of pixels, one wave of CTAs, at least four pixels a
+    // thread.
     const int R = rows_for(C, au);
-    long long S = d.step > 0 ? (4LL * p->num_sms + d.step - 1) / d.step : 1;
+    const int ctas = maps > 1 ? grad_ctas(es) : kCtas;
+    long long runs = N > 0 ? ((long long)ctas * p->num_sms) / N : 1;
     const long long most = ((long long)HW + 4LL * R - 1) / (4LL * R);
-    if (S > most) S = most;
-    if (S < 1) S = 1;
-    d.ppx = (int)((HW + S - 1) / S);
+    if (runs > most) runs = most;
+    if (runs < 1) runs = 1;
+    d.ppx = (int)((HW + runs - 1) / runs);
     d.S = (HW + d.ppx - 1) / d.ppx;
     ws = (size_t)N * d.S * ((size_t)G + (maps > 1 ? C : 0)) * sizeof(float2);
-    // Resident: the fewest groups of a CTA that fill whole vectors and 64
+    // Clusters: the fewest groups of a CTA that fill whole vectors and 64
     // bytes of a pixel (a DRAM burst); the fewest CTAs an image that hold their
-    // runs, more while SMs are idle and runs stay above 8 KB.
+    // runs in shared memory, more while SMs are idle and runs stay above 8 KB.
+    // The gradient takes this form where one cluster holds every image.
     d.K = 0;
     int gb = 1;
     while (gb < G && ((gb * cg) % au != 0 || gb * cg * es < 64)) ++gb;
@@ -1005,23 +1058,29 @@ void plan_direction(const conv_plan *p, int maps, GnGeom::Dir &d, size_t &ws) {
     const bool always = cb <= kThreads;                   // whatever vector a call's addresses allow
     if (!always && cb / au > kThreads) return;
     auto bytes = [&](int k) { return (long long)((HW + k - 1) / k) * cb * es * maps; };
+    const int most_k = maps > 1 ? (N > 0 ? 8 / N : 1) : 8;
+    if (most_k < 1) return;
     int K = 1;
-    while (K <= 8 && bytes(K) > kResident) ++K;
-    if (K > 8) return;
+    while (K < most_k && bytes(K) > kResident) ++K;
+    if (bytes(K) > kResidentMost) return;
     const long long blocks = (G + gb - 1) / gb;
-    while (K < 8 && blocks * N * K < p->num_sms && bytes(K) > 8 * 1024) ++K;
-    d.rppx = (HW + K - 1) / K;
-    d.K = (HW + d.rppx - 1) / d.rppx;
+    while (K < most_k && blocks * N * K < p->num_sms && bytes(K) > 8 * 1024) ++K;
+    d.cpx = (HW + K - 1) / K;
+    d.K = (HW + d.cpx - 1) / d.cpx;
     d.gb = gb; d.cb = cb;
-    d.NI = maps > 1 && (long long)N * d.K <= 8 && N > 0 ? N : 1;
     if (blocks > 65535) { d.K = 0; return; }
-    // the workspace of the form that runs, or of both where addresses decide
-    const size_t res = maps > 1 && d.NI != N ? (size_t)N * C * sizeof(float2) : 0;
-    ws = always ? res : (ws > res ? ws : res);
+    if (always) ws = 0;  // (else a call's addresses decide between the forms)
 }
 
-cudaError_t launch(const conv_plan *p, int which, int vec, GnArgs &a, dim3 grid, size_t smem, cudaStream_t st, int head = 0,
-                   int cluster = 1) {
+// (ring_bytes, for a vector of so many bytes)
+size_t ring_size(int bytes, int maps) { return bytes >= 4 ? (size_t)kBatch * batches(maps) * kThreads * bytes * maps : 0; }
+// (groups' statistics, and the runs' results where a CTA stages them)
+size_t runs_smem(const GnArgs &a) {
+    return ((size_t)a.G + ((long long)a.G * a.S <= kStageRuns ? (size_t)a.G * a.S : 0)) * 8;
+}
+
+cudaError_t launch(const conv_plan *p, int which, int vec, GnArgs &a, dim3 grid, size_t smem, cudaStream_t st, int cluster = 1,
+                   int head = 0) {
     const void *k = pick_kernel(which, p->dtype, vec, p->act);
     if (smem > 48 * 1024) {
         const int rc = conv_grant_smem_once(k, p->device, (int)smem);
@@ -1059,13 +1118,13 @@ extern "C" int conv_plan_create_groupnorm(int32_t n, int32_t h, int32_t w, int32
     }
     plan_direction(p, 1, p->gn.fwd, p->ws_bytes);
     plan_direction(p, 2, p->gn.bwd, p->ws_bwd_bytes);
-    auto say = [](const GnGeom::Dir &d, char *t, size_t n) {
-        if (d.K > 0) snprintf(t, n, "resident %d groups, %d CTAs an image", d.gb, d.K);
-        else snprintf(t, n, "%d runs of %d px, %d images a pass", d.S, d.ppx, d.step);
+    auto say = [](const GnGeom::Dir &d, int images, char *t, size_t n) {
+        if (d.K > 0) snprintf(t, n, "clusters of %d, %d groups", d.K * images, d.gb);
+        else snprintf(t, n, "%d runs of %d px", d.S, d.ppx);
     };
     char f[64], b[64];
-    say(p->gn.fwd, f, sizeof(f));
-    say(p->gn.bwd, b, sizeof(b));
+    say(p->gn.fwd, 1, f, sizeof(f));
+    say(p->gn.bwd, n, b, sizeof(b));
     snprintf(p->desc, sizeof(p->desc), "groupnorm %s groups=%dx%d forward: %s; gradient: %s", dtype == CONV_F32 ? "f32" : "bf16",
              groups, c / groups, f, b);
     *out_plan = p;
@@ -1102,20 +1161,16 @@ extern "C" int conv_run_groupnorm(const conv_plan_t *plan, const void *x, int64_
     const int vec = vec_for(p, 2, ptrs, pitches);
     const int R = rows_for(C, vec);
     cudaStream_t st = (cudaStream_t)stream;
-    if (resident(d, vec)) {
-        const size_t smem = resident_args(d, vec, es, 1, a);
+    if (clustered(d, vec)) {
+        const size_t smem = cluster_args(d, vec, es, 1, a);
         const dim3 grid(d.K, (a.G + d.gb - 1) / d.gb, a.N);
-        return launch(p, K_RES, vec, a, grid, smem, st, 0, d.K) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+        return launch(p, K_CLUSTER, vec, a, grid, smem, st, d.K) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
     }
-    const size_t runs = (size_t)a.G * a.S <= (size_t)kStageRuns ? (size_t)a.G * a.S : 0;
-    for (int n0 = 0; n0 < a.N; n0 += d.step) {
-        a.n0 = n0;
-        const dim3 grid(a.S, a.N - n0 < d.step ? a.N - n0 : d.step);
-        cudaError_t e = launch(p, K_STATS, vec, a, grid, ((size_t)R * C + C) * 8 + (size_t)C * 4, st);
-        if (e == cudaSuccess) e = launch(p, K_APPLY, vec, a, grid, ((size_t)a.G + runs) * 8, st);
-        if (e != cudaSuccess) return CONV_ERR_CUDA;
-    }
-    return CONV_OK;
+    const dim3 grid(a.S, a.N);
+    const size_t ring = ring_size(vec * es, 1);
+    cudaError_t e = launch(p, K_STATS, vec, a, grid, ring + ((size_t)R * C + C) * 8 + (size_t)C * 4, st);
+    if (e == cudaSuccess) e = launch(p, K_APPLY, vec, a, grid, ring + runs_smem(a), st);
+    return e == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }
 
 extern "C" int conv_run_groupnorm_bwd(const conv_plan_t *plan, const void *x, int64_t x_pitch, const float *gamma,
@@ -1162,27 +1217,15 @@ extern "C" int conv_run_groupnorm_bwd(const conv_plan_t *plan, const void *x, in
     const long long pitches[3] = {x_pitch, dy_pitch, dx_pitch};
     const int vec = vec_for(p, 3, maps, pitches);
     const int R = rows_for(C, vec);
-    if (resident(d, vec)) {
-        const size_t smem = resident_args(d, vec, es, 2, a);
-        a.S = 1;
-        a.partc = static_cast<float2 *>(workspace);
-        const dim3 grid(d.K * d.NI, (a.G + d.gb - 1) / d.gb, a.N / d.NI);
-        cudaError_t e = launch(p, K_RES_BWD, vec, a, grid, smem, st, 0, d.K * d.NI);
-        if (e == cudaSuccess && d.NI != a.N && (dgamma || dbeta)) {
-            void *args[] = {&a};
-            e = conv_launch((const void *)&gn_bwd_join_kernel, dim3((C + 31) / 32), dim3(kThreads), args, 0, st);
-        }
-        return e == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+    if (clustered(d, vec)) {
+        const size_t smem = cluster_args(d, vec, es, 2, a);
+        const dim3 grid(d.K * a.N, (a.G + d.gb - 1) / d.gb, 1);
+        return launch(p, K_CLUSTER_BWD, vec, a, grid, smem, st, d.K * a.N) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
     }
-    const size_t runs = (size_t)a.G * a.S <= (size_t)kStageRuns ? (size_t)a.G * a.S : 0;
-    const size_t need = ((size_t)a.G + runs) * 8, dxs = need > kWarps * 32 * 8 ? need : (size_t)kWarps * 32 * 8;
-    for (int n0 = 0; n0 < a.N; n0 += d.step) {
-        a.n0 = n0;
-        const int n = a.N - n0 < d.step ? a.N - n0 : d.step;
-        const int head = n0 + n == a.N && (dgamma || dbeta) ? 1 : 0;  // (once every image's sums are there)
-        cudaError_t e = launch(p, K_SUMS, vec, a, dim3(a.S, n), ((size_t)R * C + C) * 8, st);
-        if (e == cudaSuccess) e = launch(p, K_DX, vec, a, dim3(a.S, n + head), dxs, st, head);
-        if (e != cudaSuccess) return CONV_ERR_CUDA;
-    }
-    return CONV_OK;
+    const int head = dgamma || dbeta ? 1 : 0;
+    const size_t ring = ring_size(vec * es, 2);
+    cudaError_t e = launch(p, K_SUMS, vec, a, dim3(a.S, a.N), ring + ((size_t)R * C + C) * 8, st);
+    const size_t need = ring + runs_smem(a), red = (size_t)kWarps * 32 * 8;
+    if (e == cudaSuccess) e = launch(p, K_DX, vec, a, dim3(a.S, a.N + head), need > red ? need : red, st, 1, head);
+    return e == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }

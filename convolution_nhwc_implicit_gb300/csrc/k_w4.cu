@@ -22,8 +22,15 @@
 // i + 4, so that (word >> 4 i) & 0x000f000f is one operand register.  k is
 // padded to 128 and rows to 16 with code 8 (zero).
 //
-// A CTA's eight warps share 16 output channels, each every eighth run of 128
-// input channels; the partial sums meet in shared memory in a fixed order.
+// Two kernels:
+//   w4_few   x, whole, in every CTA's shared memory (as the MMA's operand rows:
+//            zeros past c_in, fp32 rows already split).  A CTA's warps share 16
+//            output channels, each every kWarps-th run of 128 input channels,
+//            and go on to the next 16 with the loads for them already under
+//            way; the warps' sums meet in shared memory in a fixed order.
+//   w4_many  where x does not fit: each warp has 16 output channels of its own
+//            and all of k, x passing through shared memory 128 channels at a
+//            time, loaded once for all the CTA's warps.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -38,9 +45,12 @@ using namespace convk;
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 128;       // input channels a warp takes at a time (two tiles)
+constexpr int kPad = 64;         // bytes between x rows in shared memory: 16-byte reads of eight
+                                 // rows' same channels then touch every bank once
+constexpr int kManyPitch = kUnit * 2 + kPad;
+constexpr int kManyRows = 64;
+constexpr int kFewSmem = 200 * 1024;  // x bytes that w4_few keeps (one CTA a SM)
 
 struct W4Args {
     const void *x;
@@ -48,7 +58,7 @@ struct W4Args {
     const void *scales;
     const float *bias;
     void *y;
-    int rows, ci, co, ng, units, act;
+    int rows, ci, co, ng, units, act, tiles;
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -70,25 +80,22 @@ __device__ __forceinline__ uint32_t decode(uint32_t w, int i) {
     return *reinterpret_cast<const uint32_t *>(&d);
 }
 
-// Eight consecutive channels of one x row as MMA operand registers (bf16
-// pairs); channels at and past ci, and rows past the last, are zero.
+// An x row's eight consecutive channels from k on as bf16 parts: the value
+// itself (bf16 rows), or three parts of eight bits each (fp32 rows); zeros at
+// and past ci.
 struct XBf16 {
     static constexpr int kParts = 1;
     using Elem = __nv_bfloat16;
-    template <bool VEC>
-    __device__ static __forceinline__ void load(const Elem *row, int k, int ci, bool on, uint32_t (&b)[1][4]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[0][i] = 0u;
-        if (!on) return;
-        if (VEC) {
-            if (k + 8 <= ci) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(row + k);
-                b[0][0] = v.x; b[0][1] = v.y; b[0][2] = v.z; b[0][3] = v.w;
-            }
+    __device__ static __forceinline__ void load(const Elem *row, int k, int ci, bool vec, uint4 (&out)[1]) {
+        out[0] = make_uint4(0u, 0u, 0u, 0u);
+        if (vec && k + 8 <= ci) {
+            out[0] = *reinterpret_cast<const uint4 *>(row + k);
         } else {
+            uint32_t b[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (k + i < ci) b[0][i >> 1] |= (uint32_t)__bfloat16_as_ushort(row[k + i]) << (16 * (i & 1));
+                if (k + i < ci) b[i >> 1] |= (uint32_t)__bfloat16_as_ushort(row[k + i]) << (16 * (i & 1));
+            out[0] = make_uint4(b[0], b[1], b[2], b[3]);
         }
     }
 };
@@ -111,23 +118,16 @@ struct XF32 {
             p[1] = p[2] = 0u;
         }
     }
-    template <bool VEC>
-    __device__ static __forceinline__ void load(const Elem *row, int k, int ci, bool on, uint32_t (&b)[3][4]) {
+    __device__ static __forceinline__ void load(const Elem *row, int k, int ci, bool vec, uint4 (&out)[3]) {
         float f[8];
+        if (vec && k + 8 <= ci) {
+            const float4 u = *reinterpret_cast<const float4 *>(row + k), v = *reinterpret_cast<const float4 *>(row + k + 4);
+            f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w; f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-        if (on) {
-            if (VEC) {
-                if (k + 8 <= ci) {
-                    const float4 u = *reinterpret_cast<const float4 *>(row + k), v = *reinterpret_cast<const float4 *>(row + k + 4);
-                    f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w; f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (k + i < ci) f[i] = row[k + i];
-            }
+            for (int i = 0; i < 8; ++i) f[i] = k + i < ci ? row[k + i] : 0.0f;
         }
+        uint32_t b[3][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t lo[3], hi[3];
@@ -136,103 +136,221 @@ struct XF32 {
 #pragma unroll
             for (int q = 0; q < 3; ++q) b[q][i] = lo[q] | (hi[q] << 16);
         }
+#pragma unroll
+        for (int q = 0; q < 3; ++q) out[q] = make_uint4(b[q][0], b[q][1], b[q][2], b[q][3]);
     }
 };
 
-// NT: blocks of eight x rows.  GROUP: channels a scale (32, 64 or 128).
-// XVEC: x rows allow 16-byte loads of whole eights of channels.
-template <typename X, int NT, int GROUP, bool XVEC>
-__global__ void __launch_bounds__(kThreads) w4_kernel(W4Args a) {
+// A warp's 16 output channels by 128 input channels, as loaded.
+template <int GROUP>
+struct Unit {
+    static constexpr int kGroups = kUnit / GROUP;
+    uint4 wa, wb;
+    float f0[kGroups], f1[kGroups];  // scales of rows g and g + 8
+    template <typename Elem>
+    __device__ __forceinline__ void fetch(const uint4 *w, int u, const Elem *s0, const Elem *s1, int ng, bool on0, bool on1) {
+        wa = __ldcs(w + (long long)u * 64);
+        wb = __ldcs(w + (long long)u * 64 + 32);
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+            const int gi = u * kGroups + j;
+            f0[j] = on0 && gi < ng ? elem_f(s0[gi]) : 0.0f;
+            f1[j] = on1 && gi < ng ? elem_f(s1[gi]) : 0.0f;
+        }
+    }
+};
+
+// acc += the unit's products with NT blocks of eight x rows; xs: this lane's
+// address in the first part's row g (of the first block), channel 8 t of the
+// unit; part_step and the 8-row block's step in bytes.  on[n]: row 8 n + g exists.
+template <typename X, int NT, int GROUP>
+__device__ __forceinline__ void products(const Unit<GROUP> &un, float (&acc)[NT][4], const uint8_t *xs, int block_step, int part_step,
+                                         const bool (&on)[NT]) {
+    constexpr int kHalves = GROUP / 32;  // steps of 32 channels a scale
+    float c[NT][4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        if (h % kHalves == 0) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[n][e] = 0.0f;
+        }
+        const uint32_t lo = h == 0 ? un.wa.x : (h == 1 ? un.wa.z : (h == 2 ? un.wb.x : un.wb.z));
+        const uint32_t hi = h == 0 ? un.wa.y : (h == 1 ? un.wa.w : (h == 2 ? un.wb.y : un.wb.w));
+        uint32_t p[4], q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p[i] = decode(lo, i);
+            q[i] = decode(hi, i);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int r = 0; r < X::kParts; ++r) {
+                uint4 b = make_uint4(0u, 0u, 0u, 0u);
+                if (on[n]) b = *reinterpret_cast<const uint4 *>(xs + n * block_step + r * part_step + h * 64);
+                mma16816(c[n], p[0], q[0], p[1], q[1], b.x, b.y);
+                mma16816(c[n], p[2], q[2], p[3], q[3], b.z, b.w);
+            }
+        if (h % kHalves == kHalves - 1) {
+            const int j = h / kHalves;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                acc[n][0] = fmaf(un.f0[j], c[n][0], acc[n][0]);
+                acc[n][1] = fmaf(un.f0[j], c[n][1], acc[n][1]);
+                acc[n][2] = fmaf(un.f1[j], c[n][2], acc[n][2]);
+                acc[n][3] = fmaf(un.f1[j], c[n][3], acc[n][3]);
+            }
+        }
+    }
+}
+
+// CTAs of eight warps a SM: as many as their registers allow without spilling.
+__host__ __device__ constexpr int few_ctas(int parts, int nt) { return nt * (parts == 3 ? 2 : 1) >= 4 ? 2 : 3; }
+
+template <typename X, int NT, int GROUP, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? few_ctas(X::kParts, NT) : 1) w4_few_kernel(W4Args a, int vec) {
     using Elem = typename X::Elem;
-    extern __shared__ float red[];  // [kWarps][16][NT * 8]
+    constexpr int kThreads = WARPS * 32;
+    extern __shared__ __align__(16) uint8_t shm[];
+    float *red = reinterpret_cast<float *>(shm);  // [2][WARPS][NT * 8][16]
+    constexpr int kRed = WARPS * NT * 8 * 16;
+    uint8_t *xs = shm + 2 * kRed * 4;             // [parts][rows] of pitch bytes
+    const int pitch = a.units * kUnit * 2 + kPad, part_step = a.rows * pitch;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int co0 = blockIdx.x * 16, m0 = blockIdx.y * (NT * 8);
     pdl_trigger();
     pdl_wait();
     const Elem *x = static_cast<const Elem *>(a.x);
     const Elem *sc = static_cast<const Elem *>(a.scales);
-    const uint4 *w = a.w + (long long)blockIdx.x * a.units * 64 + lane;
-    const bool on0 = co0 + g < a.co, on1 = co0 + g + 8 < a.co;
-    const Elem *s0 = sc + (long long)(co0 + g) * a.ng, *s1 = s0 + 8LL * a.ng;
-
+    const int per = (a.units + WARPS - 1) / WARPS;        // steps of a warp a tile
+    const int mine = ((int)gridDim.x < a.tiles ? (a.tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 1) * per;
+    Unit<GROUP> un[2];
+    // step j: tile blockIdx.x + (j / per) gridDim.x, unit warp + (j % per) WARPS
+    int ft = blockIdx.x, fi = 0;                          // the next step to fetch
+    auto fetch = [&](Unit<GROUP> &d) {
+        const int u = warp + fi * WARPS, co = ft * 16 + g;
+        if (ft < a.tiles && u < a.units)
+            d.fetch(a.w + (long long)ft * a.units * 64 + lane, u, sc + (long long)co * a.ng, sc + (long long)(co + 8) * a.ng, a.ng,
+                    co < a.co, co + 8 < a.co);
+        if (++fi == per) { fi = 0; ft += gridDim.x; }
+    };
+    fetch(un[0]);
+    fetch(un[1]);
+    // x into shared memory, eight channels a thread at a time
+    const int eights = a.units * (kUnit / 8);
+    for (int i = threadIdx.x; i < a.rows * eights; i += kThreads) {
+        const int m = i / eights, k = (i - m * eights) * 8;
+        uint4 v[X::kParts];
+        X::load(x + (long long)m * a.ci, k, a.ci, vec != 0, v);
+#pragma unroll
+        for (int r = 0; r < X::kParts; ++r) *reinterpret_cast<uint4 *>(xs + r * part_step + m * pitch + k * 2) = v[r];
+    }
+    __syncthreads();
+    bool on[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) on[n] = n * 8 + g < a.rows;
+    const uint8_t *xl = xs + g * pitch + t * 16;
     float acc[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
-
-    constexpr int kHalvesPerGroup = GROUP / 32;
-    constexpr int kGroupsPerUnit = 4 / kHalvesPerGroup;
-    for (int u = warp; u < a.units; u += kWarps) {
-        const uint4 wa = w[(long long)u * 64], wb = w[(long long)u * 64 + 32];
-        float f0[kGroupsPerUnit], f1[kGroupsPerUnit];
+    int i = 0, tile = blockIdx.x, side = 0;
+    auto step = [&](Unit<GROUP> &cur) {
+        const int u = warp + i * WARPS;
+        if (u < a.units) products<X, NT, GROUP>(cur, acc, xl + u * (kUnit * 2), 8 * pitch, part_step, on);
+        fetch(cur);
+        if (++i < per) return;
+        i = 0;
+        // the tile's sums: one barrier a tile, two sides in turn (a side is
+        // written again only after the next tile's barrier)
+        float *mine_red = red + side * kRed + warp * (NT * 8 * 16);
 #pragma unroll
-        for (int j = 0; j < kGroupsPerUnit; ++j) {
-            const int gi = u * kGroupsPerUnit + j;
-            f0[j] = on0 && gi < a.ng ? elem_f(s0[gi]) : 0.0f;
-            f1[j] = on1 && gi < a.ng ? elem_f(s1[gi]) : 0.0f;
+        for (int n = 0; n < NT; ++n) {
+            mine_red[(n * 8 + 2 * t) * 16 + g] = acc[n][0];
+            mine_red[(n * 8 + 2 * t + 1) * 16 + g] = acc[n][1];
+            mine_red[(n * 8 + 2 * t) * 16 + g + 8] = acc[n][2];
+            mine_red[(n * 8 + 2 * t + 1) * 16 + g + 8] = acc[n][3];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
         }
-        float c[NT][4];
+        __syncthreads();
+        for (int o = threadIdx.x; o < a.rows * 16; o += kThreads) {
+            const int m = o >> 4, co = tile * 16 + (o & 15);
+            if (co >= a.co) continue;
+            float v = 0.0f;
 #pragma unroll
-        for (int h = 0; h < 4; ++h) {
-            if (h % kHalvesPerGroup == 0) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) c[n][e] = 0.0f;
-            }
-            const uint32_t lo = h == 0 ? wa.x : (h == 1 ? wa.z : (h == 2 ? wb.x : wb.z));
-            const uint32_t hi = h == 0 ? wa.y : (h == 1 ? wa.w : (h == 2 ? wb.y : wb.w));
-            uint32_t p[4], q[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[i] = decode(lo, i);
-                q[i] = decode(hi, i);
-            }
-            const int k = u * kUnit + h * 32 + t * 8;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int m = m0 + n * 8 + g;
-                uint32_t b[X::kParts][4];
-                X::template load<XVEC>(x + (long long)m * a.ci, k, a.ci, m < a.rows, b);
-#pragma unroll
-                for (int r = 0; r < X::kParts; ++r) {
-                    mma16816(c[n], p[0], q[0], p[1], q[1], b[r][0], b[r][1]);
-                    mma16816(c[n], p[2], q[2], p[3], q[3], b[r][2], b[r][3]);
-                }
-            }
-            if (h % kHalvesPerGroup == kHalvesPerGroup - 1) {
-                const int j = h / kHalvesPerGroup;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    acc[n][0] = fmaf(f0[j], c[n][0], acc[n][0]);
-                    acc[n][1] = fmaf(f0[j], c[n][1], acc[n][1]);
-                    acc[n][2] = fmaf(f1[j], c[n][2], acc[n][2]);
-                    acc[n][3] = fmaf(f1[j], c[n][3], acc[n][3]);
-                }
-            }
+            for (int q = 0; q < WARPS; ++q) v += red[side * kRed + q * (NT * 8 * 16) + o];
+            v = activate(v + (a.bias ? a.bias[co] : 0.0f), a.act);
+            static_cast<Elem *>(a.y)[(long long)m * a.co + co] = elem_from<Elem>(v);
         }
+        side ^= 1;
+        tile += gridDim.x;
+    };
+    int j = 0;
+    for (; j + 1 < mine; j += 2) {
+        step(un[0]);
+        step(un[1]);
     }
-    // [warp][x row][16 output channels]
-    float *mine = red + warp * (NT * 8 * 16);
+    if (j < mine) step(un[0]);
+}
+
+template <typename X, int GROUP, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) w4_many_kernel(W4Args a, int vec) {
+    using Elem = typename X::Elem;
+    constexpr int kThreads = WARPS * 32, NT = kManyRows / 8;
+    constexpr int kPart = kManyRows * kManyPitch, kSide = X::kParts * kPart;
+    extern __shared__ __align__(16) uint8_t shm[];  // [2][parts][64] rows of kManyPitch bytes
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int m0 = blockIdx.y * kManyRows, rows = min(kManyRows, a.rows - m0);
+    const int tile = blockIdx.x * WARPS + warp;
+    const bool live = tile < a.tiles;
+    pdl_trigger();
+    pdl_wait();
+    const Elem *x = static_cast<const Elem *>(a.x) + (long long)m0 * a.ci;
+    const int co = tile * 16 + g;
+    const Elem *s0 = static_cast<const Elem *>(a.scales) + (long long)co * a.ng, *s1 = s0 + 8LL * a.ng;
+    const uint4 *w = a.w + (long long)tile * a.units * 64 + lane;
+    const bool on0 = co < a.co, on1 = co + 8 < a.co;
+    auto stage = [&](int u) {
+        uint8_t *dst = shm + (u & 1) * kSide;
+        for (int i = threadIdx.x; i < rows * (kUnit / 8); i += kThreads) {
+            const int m = i / (kUnit / 8), k = (i % (kUnit / 8)) * 8;
+            uint4 v[X::kParts];
+            X::load(x + (long long)m * a.ci, u * kUnit + k, a.ci, vec != 0, v);
+#pragma unroll
+            for (int r = 0; r < X::kParts; ++r) *reinterpret_cast<uint4 *>(dst + r * kPart + m * kManyPitch + k * 2) = v[r];
+        }
+    };
+    bool on[NT];
+    float acc[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        mine[(n * 8 + 2 * t) * 16 + g] = acc[n][0];
-        mine[(n * 8 + 2 * t + 1) * 16 + g] = acc[n][1];
-        mine[(n * 8 + 2 * t) * 16 + g + 8] = acc[n][2];
-        mine[(n * 8 + 2 * t + 1) * 16 + g + 8] = acc[n][3];
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < NT * 8 * 16; i += kThreads) {
-        const int m = m0 + (i >> 4), co = co0 + (i & 15);
-        if (m >= a.rows || co >= a.co) continue;
-        float v = a.bias ? a.bias[co] : 0.0f;
-        float s = 0.0f;
+        on[n] = n * 8 + g < rows;
 #pragma unroll
-        for (int q = 0; q < kWarps; ++q) s += red[q * (NT * 8 * 16) + i];
-        v = activate(s + v, a.act);
-        static_cast<Elem *>(a.y)[(long long)m * a.co + co] = elem_from<Elem>(v);
+        for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
     }
+    Unit<GROUP> cur, nxt;
+    if (live) cur.fetch(w, 0, s0, s1, a.ng, on0, on1);
+    stage(0);
+    for (int u = 0; u < a.units; ++u) {
+        __syncthreads();  // unit u is staged, and everyone has left unit u - 1
+        if (live && u + 1 < a.units) nxt.fetch(w, u + 1, s0, s1, a.ng, on0, on1);
+        if (u + 1 < a.units) stage(u + 1);
+        if (live) products<X, NT, GROUP>(cur, acc, shm + (u & 1) * kSide + g * kManyPitch + t * 16, 8 * kManyPitch, kPart, on);
+        cur = nxt;
+    }
+    if (!live) return;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int m = n * 8 + 2 * t + (e & 1), c = co + (e >> 1) * 8;
+            if (m < rows && c < a.co)
+                static_cast<Elem *>(a.y)[(long long)(m0 + m) * a.co + c] =
+                    elem_from<Elem>(activate(acc[n][e] + (a.bias ? a.bias[c] : 0.0f), a.act));
+        }
 }
 
 // One 32-bit word of the laid-out codes a thread.
@@ -293,22 +411,28 @@ __global__ void w4_quantize_kernel(const T *w, uint8_t *codes, T *scales, int ci
 }
 
 // ------------------------------------------------------------------ host side
-template <typename X, int NT, int GROUP>
-const void *pick_vec(bool vec) {
-    return vec ? (const void *)&w4_kernel<X, NT, GROUP, true> : (const void *)&w4_kernel<X, NT, GROUP, false>;
+template <typename X, int NT, int WARPS>
+const void *few_group(int group) {
+    return group == 32 ? (const void *)&w4_few_kernel<X, NT, 32, WARPS>
+                       : (group == 64 ? (const void *)&w4_few_kernel<X, NT, 64, WARPS> : (const void *)&w4_few_kernel<X, NT, 128, WARPS>);
 }
-template <typename X, int NT>
-const void *pick_group(int group, bool vec) {
-    return group == 32 ? pick_vec<X, NT, 32>(vec) : (group == 64 ? pick_vec<X, NT, 64>(vec) : pick_vec<X, NT, 128>(vec));
+template <typename X, int WARPS>
+const void *few_nt(int nt, int group) {
+    switch (nt) {
+    case 1: return few_group<X, 1, WARPS>(group);
+    case 2: return few_group<X, 2, WARPS>(group);
+    default: return few_group<X, 4, WARPS>(group);
+    }
+}
+template <typename X, int WARPS>
+const void *many_group(int group) {
+    return group == 32 ? (const void *)&w4_many_kernel<X, 32, WARPS>
+                       : (group == 64 ? (const void *)&w4_many_kernel<X, 64, WARPS> : (const void *)&w4_many_kernel<X, 128, WARPS>);
 }
 template <typename X>
-const void *pick_nt(int nt, int group, bool vec) {
-    switch (nt) {
-    case 1: return pick_group<X, 1>(group, vec);
-    case 2: return pick_group<X, 2>(group, vec);
-    case 4: return pick_group<X, 4>(group, vec);
-    default: return pick_group<X, 8>(group, vec);
-    }
+const void *pick(const W4Geom &g) {
+    if (g.many) return g.warps == 8 ? many_group<X, 8>(g.group) : (g.warps == 4 ? many_group<X, 4>(g.group) : many_group<X, 2>(g.group));
+    return g.warps == 8 ? few_nt<X, 8>(g.nt, g.group) : few_nt<X, 16>(g.nt, g.group);
 }
 
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
@@ -340,12 +464,30 @@ extern "C" int conv_plan_create_w4(int32_t rows, int32_t c_in, int32_t c_out, in
         conv_plan_destroy(p);
         return rc;
     }
-    p->w4.group = group;
-    p->w4.ng = (c_in + group - 1) / group;
-    p->w4.units = (c_in + kUnit - 1) / kUnit;
-    p->w4.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : (rows <= 32 ? 4 : 8));
-    snprintf(p->desc, sizeof(p->desc), "w4 %s group=%d rows/cta=%d tiles=%d", dtype == CONV_F32 ? "f32" : "bf16", group,
-             p->w4.nt * 8, (c_out + 15) / 16);
+    W4Geom &g = p->w4;
+    const int parts = dtype == CONV_F32 ? 3 : 1, tiles = (c_out + 15) / 16;
+    g.group = group;
+    g.ng = (c_in + group - 1) / group;
+    g.units = (c_in + kUnit - 1) / kUnit;
+    g.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
+    const long long xb = (long long)parts * rows * (g.units * (kUnit * 2) + kPad);
+    // x whole in shared memory while it fits (with the warps' sums), else in
+    // pieces; CTAs of 16 warps where it takes more than a third of a SM's.
+    g.many = rows > 32 || xb + 2LL * 16 * g.nt * 128 * 4 > kFewSmem;
+    if (g.many) {
+        g.warps = 8;
+        while (g.warps > 2 && (tiles + g.warps - 1) / g.warps * ((rows + kManyRows - 1) / kManyRows) < p->num_sms) g.warps /= 2;
+        g.smem = 2 * parts * kManyRows * kManyPitch;
+        g.grid = (tiles + g.warps - 1) / g.warps;
+    } else {
+        const long long red8 = 2LL * 8 * g.nt * 128 * 4;
+        g.warps = xb + red8 <= 72 * 1024 ? 8 : 16;
+        g.smem = (int)(xb + red8 * (g.warps / 8));
+        const int wave = p->num_sms * (g.warps == 8 ? few_ctas(parts, g.nt) : 1);
+        g.grid = tiles < wave ? tiles : wave;
+    }
+    snprintf(p->desc, sizeof(p->desc), "w4 %s group=%d %s warps=%d tiles=%d", dtype == CONV_F32 ? "f32" : "bf16", group,
+             g.many ? "x in pieces" : "x in shared memory", g.warps, tiles);
     *out_plan = p;
     return CONV_OK;
 }
@@ -412,12 +554,16 @@ extern "C" int conv_run_w4(const conv_plan_t *plan, const void *x, const void *p
     if (overlap(y, yb, x, (size_t)rows * ci * es) || overlap(y, yb, packed, pb) ||
         overlap(y, yb, scales, (size_t)co * p->w4.ng * es) || overlap(y, yb, bias, (size_t)co * 4))
         return CONV_ERR_ALIASING;
-    W4Args a = {x, static_cast<const uint4 *>(packed), scales, bias, y, rows, ci, co, p->w4.ng, p->w4.units, p->act};
-    const int nt = p->w4.nt;
-    const bool vec = ci % 8 == 0 && ((uintptr_t)x & 15u) == 0;
-    const void *k = p->dtype == CONV_F32 ? pick_nt<XF32>(nt, p->w4.group, vec) : pick_nt<XBf16>(nt, p->w4.group, vec);
-    void *args[] = {&a};
-    const cudaError_t e = conv_launch(k, dim3((unsigned)((co + 15) / 16), (unsigned)((rows + nt * 8 - 1) / (nt * 8))),
-                                      dim3(kThreads), args, (size_t)kWarps * nt * 8 * 16 * 4, (cudaStream_t)stream);
+    const W4Geom &g = p->w4;
+    W4Args a = {x, static_cast<const uint4 *>(packed), scales, bias, y, rows, ci, co, g.ng, g.units, p->act, (co + 15) / 16};
+    int vec = ci % 8 == 0 && ((uintptr_t)x & 15u) == 0 ? 1 : 0;
+    const void *k = p->dtype == CONV_F32 ? pick<XF32>(g) : pick<XBf16>(g);
+    if (g.smem > 48 * 1024) {
+        const int rc = conv_grant_smem_once(k, p->device, g.smem);
+        if (rc != CONV_OK) return rc;
+    }
+    void *args[] = {&a, &vec};
+    const dim3 grid((unsigned)g.grid, (unsigned)(g.many ? (rows + kManyRows - 1) / kManyRows : 1));
+    const cudaError_t e = conv_launch(k, grid, dim3(g.warps * 32), args, (size_t)g.smem, (cudaStream_t)stream);
     return e == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }
