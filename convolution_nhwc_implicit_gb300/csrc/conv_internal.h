@@ -84,9 +84,10 @@ struct GnGeom {
 };
 
 // 4-bit pointwise layer: scale groups, runs of 128 input channels; x whole in
-// shared memory (nt blocks of eight rows) or in pieces (many); warps a CTA.
+// shared memory or in turns (many); nt blocks of eight rows, warps and wc times
+// 16 output channels a CTA.
 struct W4Geom {
-    int group, ng, units, nt, many, warps, smem, grid;
+    int group, ng, units, nt, many, warps, wc, smem, grid;
 };
 
 // Class loss: 256 x 256 tiles over rows, classes and features; the classes in

@@ -6,9 +6,12 @@
 // used twice (two multiply-adds), so all that counts is to stream them.  The
 // codes are laid out once (w4_pack_kernel) so that a warp's 16-byte loads are
 // whole 512-byte runs and every lane finds in them the A operands of
-// mma.sync m16n8k16: a code is turned into the bf16 number u - 8, which is
-// exact (bits 0x4300 | u are 128 + u; minus 136), the products and sums are
-// the tensor core's in fp32, and a group's sum is scaled in fp32 when it ends.
+// mma.sync m16n8k16.  A code becomes the bf16 number (u - 8) / 64, exactly, with
+// one AND and one multiply-add a pair: four bits at the foot of a bf16 are the
+// subnormal u 2^-133, and the four above them, which reach into the exponent,
+// are 16 u 2^-133 (subnormals and the first normal binade lie on one line), so
+// 2^127 or 2^123 times them is u / 64.  The products and sums are the tensor
+// core's in fp32, and a group's sum is scaled in fp32 when it ends.
 // Nothing is rounded to fewer bits before the result.  fp32 rows are split
 // into three bf16 parts (8 + 8 + 8 bits, the whole significand), three MMAs.
 // (tcgen05 would need the decoded weights written to shared memory, four
@@ -22,15 +25,17 @@
 // i + 4, so that (word >> 4 i) & 0x000f000f is one operand register.  k is
 // padded to 128 and rows to 16 with code 8 (zero).
 //
-// Two kernels:
+// Every warp streams its weights through a ring of shared memory slots of its
+// own (cp.async, 1 KB units, kAhead on the way), so that a SM keeps ~100 KB in
+// flight whatever the arithmetic does.  Two kernels:
 //   w4_few   x, whole, in every CTA's shared memory (as the MMA's operand rows:
 //            zeros past c_in, fp32 rows already split).  A CTA's warps share 16
-//            output channels, each every kWarps-th run of 128 input channels,
-//            and go on to the next 16 with the loads for them already under
-//            way; the warps' sums meet in shared memory in a fixed order.
-//   w4_many  where x does not fit: each warp has 16 output channels of its own
-//            and all of k, x passing through shared memory 128 channels at a
-//            time, loaded once for all the CTA's warps.
+//            output channels, each every WARPS-th run of 128 input channels,
+//            and go on to the next 16 without a pause; the warps' sums meet in
+//            shared memory in a fixed order.
+//   w4_many  where x does not fit: a CTA's warps have WC times 16 output
+//            channels and take k in turns of WK = 8 / WC units, x passing
+//            through shared memory, loaded once for all of them.
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -46,11 +51,10 @@ using namespace convk;
 namespace {
 
 constexpr int kUnit = 128;       // input channels a warp takes at a time (two tiles)
+constexpr int kAhead = 4;        // units of a warp's ring (a power of two)
 constexpr int kPad = 64;         // bytes between x rows in shared memory: 16-byte reads of eight
                                  // rows' same channels then touch every bank once
-constexpr int kManyPitch = kUnit * 2 + kPad;
-constexpr int kManyRows = 64;
-constexpr int kFewSmem = 200 * 1024;  // x bytes that w4_few keeps (one CTA a SM)
+constexpr int kSmemMost = 200 * 1024, kFewMost = 226 * 1024;
 
 struct W4Args {
     const void *x;
@@ -61,6 +65,13 @@ struct W4Args {
     int rows, ci, co, ng, units, act, tiles;
 };
 
+// c = a b, and c += a b
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -72,13 +83,20 @@ __device__ __forceinline__ float elem_f(float v) { return v; }
 __device__ __forceinline__ float elem_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <typename T> __device__ __forceinline__ T elem_from(float v) { return convk::Elem<T>::from_f(v); }
 
-// Codes i and i + 4 of a word as the bf16 pair (u - 8).
-__device__ __forceinline__ uint32_t decode(uint32_t w, int i) {
-    const uint32_t v = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
-    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&v),
-                                     __halves2bfloat162(__ushort_as_bfloat16(0x4308), __ushort_as_bfloat16(0x4308)));
-    return *reinterpret_cast<const uint32_t *>(&d);
+// A word's eight codes as four bf16 pairs (u - 8) / 64, pair i codes i and i + 4.
+__device__ __forceinline__ void decode(uint32_t w, uint32_t (&p)[4]) {
+    const uint32_t h = w >> 8;
+    auto line = [](uint32_t bits, uint32_t scale) {  // bits * scale - 1/8
+        uint32_t r;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(bits), "r"(scale), "r"(0xbe00be00u));
+        return r;
+    };
+    p[0] = line(w & 0x000f000fu, 0x7f007f00u);  // times 2^127
+    p[1] = line(w & 0x00f000f0u, 0x7d007d00u);  // times 2^123
+    p[2] = line(h & 0x000f000fu, 0x7f007f00u);
+    p[3] = line(h & 0x00f000f0u, 0x7d007d00u);
 }
+constexpr float kCodeScale = 64.0f;
 
 // An x row's eight consecutive channels from k on as bf16 parts: the value
 // itself (bf16 rows), or three parts of eight bits each (fp32 rows); zeros at
@@ -141,102 +159,129 @@ struct XF32 {
     }
 };
 
-// A warp's 16 output channels by 128 input channels, as loaded.
-template <int GROUP>
-struct Unit {
-    static constexpr int kGroups = kUnit / GROUP;
-    uint4 wa, wb;
-    float f0[kGroups], f1[kGroups];  // scales of rows g and g + 8
-    template <typename Elem>
-    __device__ __forceinline__ void fetch(const uint4 *w, int u, const Elem *s0, const Elem *s1, int ng, bool on0, bool on1) {
-        wa = __ldcs(w + (long long)u * 64);
-        wb = __ldcs(w + (long long)u * 64 + 32);
-#pragma unroll
-        for (int j = 0; j < kGroups; ++j) {
-            const int gi = u * kGroups + j;
-            f0[j] = on0 && gi < ng ? elem_f(s0[gi]) : 0.0f;
-            f1[j] = on1 && gi < ng ? elem_f(s1[gi]) : 0.0f;
-        }
-    }
-};
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// acc += the unit's products with NT blocks of eight x rows; xs: this lane's
-// address in the first part's row g (of the first block), channel 8 t of the
-// unit; part_step and the 8-row block's step in bytes.  on[n]: row 8 n + g exists.
+// acc += 16 output channels by 128 input channels (the codes wa, wb of a lane,
+// over 64) times NT blocks of eight x rows.  xs[n]: this lane's row of block n in the
+// first part, channel 8 t of the unit; part_step in bytes.  Lanes whose row
+// does not exist read another: an MMA column is its own.  f0, f1: the unit's
+// scales of rows g and g + 8.
 template <typename X, int NT, int GROUP>
-__device__ __forceinline__ void products(const Unit<GROUP> &un, float (&acc)[NT][4], const uint8_t *xs, int block_step, int part_step,
-                                         const bool (&on)[NT]) {
+__device__ __forceinline__ void products(uint4 wa, uint4 wb, float (&acc)[NT][4], const uint8_t *const (&xs)[NT], int offset,
+                                         int part_step, const float (&f0)[kUnit / GROUP], const float (&f1)[kUnit / GROUP]) {
     constexpr int kHalves = GROUP / 32;  // steps of 32 channels a scale
     float c[NT][4];
 #pragma unroll
     for (int h = 0; h < 4; ++h) {
-        if (h % kHalves == 0) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) c[n][e] = 0.0f;
-        }
-        const uint32_t lo = h == 0 ? un.wa.x : (h == 1 ? un.wa.z : (h == 2 ? un.wb.x : un.wb.z));
-        const uint32_t hi = h == 0 ? un.wa.y : (h == 1 ? un.wa.w : (h == 2 ? un.wb.y : un.wb.w));
+        const uint32_t lo = h == 0 ? wa.x : (h == 1 ? wa.z : (h == 2 ? wb.x : wb.z));
+        const uint32_t hi = h == 0 ? wa.y : (h == 1 ? wa.w : (h == 2 ? wb.y : wb.w));
         uint32_t p[4], q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            p[i] = decode(lo, i);
-            q[i] = decode(hi, i);
-        }
+        decode(lo, p);
+        decode(hi, q);
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int r = 0; r < X::kParts; ++r) {
-                uint4 b = make_uint4(0u, 0u, 0u, 0u);
-                if (on[n]) b = *reinterpret_cast<const uint4 *>(xs + n * block_step + r * part_step + h * 64);
-                mma16816(c[n], p[0], q[0], p[1], q[1], b.x, b.y);
+                const uint4 b = *reinterpret_cast<const uint4 *>(xs[n] + offset + r * part_step + h * 64);
+                if (h % kHalves == 0 && r == 0) mma16816_first(c[n], p[0], q[0], p[1], q[1], b.x, b.y);
+                else mma16816(c[n], p[0], q[0], p[1], q[1], b.x, b.y);
                 mma16816(c[n], p[2], q[2], p[3], q[3], b.z, b.w);
             }
         if (h % kHalves == kHalves - 1) {
-            const int j = h / kHalves;
+            const float s0 = f0[h / kHalves], s1 = f1[h / kHalves];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                acc[n][0] = fmaf(un.f0[j], c[n][0], acc[n][0]);
-                acc[n][1] = fmaf(un.f0[j], c[n][1], acc[n][1]);
-                acc[n][2] = fmaf(un.f1[j], c[n][2], acc[n][2]);
-                acc[n][3] = fmaf(un.f1[j], c[n][3], acc[n][3]);
+                acc[n][0] = fmaf(s0, c[n][0], acc[n][0]);
+                acc[n][1] = fmaf(s0, c[n][1], acc[n][1]);
+                acc[n][2] = fmaf(s1, c[n][2], acc[n][2]);
+                acc[n][3] = fmaf(s1, c[n][3], acc[n][3]);
             }
         }
     }
 }
 
+// N scales, side by side in shared memory.
+template <int N, typename Elem>
+__device__ __forceinline__ void load_scales(const uint8_t *p, float (&f)[N]) {
+    struct alignas(N * sizeof(Elem)) Group { Elem v[N]; };
+    const Group q = *reinterpret_cast<const Group *>(p);
+#pragma unroll
+    for (int j = 0; j < N; ++j) f[j] = elem_f(q.v[j]);
+}
+
 // CTAs of eight warps a SM: as many as their registers allow without spilling.
 __host__ __device__ constexpr int few_ctas(int parts, int nt) { return nt * (parts == 3 ? 2 : 1) >= 4 ? 2 : 3; }
+// Shared memory of w4_few before x: the warps' sums (two sides), their rings,
+// and 16 rows of scales (two sides).
+__host__ __device__ inline int few_sums(int warps, int nt) { return 2 * warps * nt * 128 * 4; }
+__host__ __device__ inline int few_ring(int warps) { return warps * kAhead * 1024; }
+// (a row of scales: whole units, zeros past the last group, and 16 bytes more,
+// so that eight rows' same scales lie in different banks)
+__host__ __device__ inline int scale_pitch(int units, int group, int es) { return (units * (kUnit / group) * es + 15) / 16 * 16 + 16; }
+__host__ __device__ inline int few_scales(int units, int group, int es) { return 16 * scale_pitch(units, group, es); }
 
 template <typename X, int NT, int GROUP, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? few_ctas(X::kParts, NT) : 1) w4_few_kernel(W4Args a, int vec) {
     using Elem = typename X::Elem;
-    constexpr int kThreads = WARPS * 32;
+    constexpr int kThreads = WARPS * 32, kSum = WARPS * NT * 128, kGroups = kUnit / GROUP;
     extern __shared__ __align__(16) uint8_t shm[];
-    float *red = reinterpret_cast<float *>(shm);  // [2][WARPS][NT * 8][16]
-    constexpr int kRed = WARPS * NT * 8 * 16;
-    uint8_t *xs = shm + 2 * kRed * 4;             // [parts][rows] of pitch bytes
+    float *red = reinterpret_cast<float *>(shm);
+    const int spitch = scale_pitch(a.units, GROUP, (int)sizeof(Elem)), sside = 16 * spitch;
+    uint8_t *scales = shm + few_sums(WARPS, NT) + few_ring(WARPS);
+    uint8_t *xs = scales + 2 * sside;                     // [parts][rows] of pitch bytes
     const int pitch = a.units * kUnit * 2 + kPad, part_step = a.rows * pitch;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint4 *ring = reinterpret_cast<uint4 *>(shm + few_sums(WARPS, NT) + warp * (kAhead * 1024)) + lane;
     pdl_trigger();
     pdl_wait();
     const Elem *x = static_cast<const Elem *>(a.x);
     const Elem *sc = static_cast<const Elem *>(a.scales);
-    const int per = (a.units + WARPS - 1) / WARPS;        // steps of a warp a tile
-    const int mine = ((int)gridDim.x < a.tiles ? (a.tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 1) * per;
-    Unit<GROUP> un[2];
-    // step j: tile blockIdx.x + (j / per) gridDim.x, unit warp + (j % per) WARPS
-    int ft = blockIdx.x, fi = 0;                          // the next step to fetch
-    auto fetch = [&](Unit<GROUP> &d) {
-        const int u = warp + fi * WARPS, co = ft * 16 + g;
-        if (ft < a.tiles && u < a.units)
-            d.fetch(a.w + (long long)ft * a.units * 64 + lane, u, sc + (long long)co * a.ng, sc + (long long)(co + 8) * a.ng, a.ng,
-                    co < a.co, co + 8 < a.co);
-        if (++fi == per) { fi = 0; ft += gridDim.x; }
+    const int per = (a.units - warp + WARPS - 1) / WARPS;  // this warp's units of a tile
+    // what is left to ask for, and where the next unit lies
+    int left = ((a.tiles - 1 - (int)blockIdx.x) / (int)gridDim.x + 1) * per, fi = per;
+    uint32_t fslot = 0;
+    const uint32_t ring0 = smem_addr(ring);
+    const uint4 *fw = a.w + ((long long)blockIdx.x * a.units + warp) * 64 + lane;
+    const long long jump = ((long long)gridDim.x * a.units - (long long)per * WARPS) * 64;  // from a tile's end to the next
+    auto ask = [&]() {
+        if (left > 0) {
+            copy16(ring0 + fslot, fw);
+            copy16(ring0 + fslot + 512, fw + 32);
+            fw += WARPS * 64;
+            --left;
+            if (--fi == 0) {
+                fi = per;
+                fw += jump;
+            }
+        }
+        copy_commit();
+        fslot = (fslot + 1024) & (kAhead * 1024 - 1);
     };
-    fetch(un[0]);
-    fetch(un[1]);
+    // 16 rows of scales (rows past the last: as they are, for outputs that
+    // nobody stores)
+    const bool svec = (reinterpret_cast<uintptr_t>(sc) & 15u) == 0 && a.ng * (int)sizeof(Elem) % 16 == 0;
+    auto ask_scales = [&](int tile, int side) {
+        if (tile >= a.tiles) return;
+        const Elem *src = sc + (long long)tile * 16 * a.ng;
+        uint8_t *d = scales + side * sside;
+        const int rows = min(16, a.co - tile * 16), n = svec ? a.ng * (int)sizeof(Elem) / 16 : a.ng;
+        for (int i = threadIdx.x; i < rows * n; i += kThreads) {
+            const int r = i / n, e = i - r * n;
+            if (svec) copy16(smem_addr(d + r * spitch) + 16 * e, reinterpret_cast<const uint8_t *>(src + (long long)r * a.ng) + 16 * e);
+            else reinterpret_cast<Elem *>(d + r * spitch)[e] = src[(long long)r * a.ng + e];
+        }
+    };
+    for (int i = threadIdx.x; i < 32 * (a.units * kGroups - a.ng); i += kThreads)
+        reinterpret_cast<Elem *>(scales + (i & 31) * spitch)[a.ng + (i >> 5)] = elem_from<Elem>(0.0f);
+    ask_scales(blockIdx.x, 0);
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) ask();  // (the first group holds the scales too)
     // x into shared memory, eight channels a thread at a time
     const int eights = a.units * (kUnit / 8);
     for (int i = threadIdx.x; i < a.rows * eights; i += kThreads) {
@@ -246,34 +291,46 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? few_ctas(X::kParts, N
 #pragma unroll
         for (int r = 0; r < X::kParts; ++r) *reinterpret_cast<uint4 *>(xs + r * part_step + m * pitch + k * 2) = v[r];
     }
+    copy_wait<kAhead - 2>();
     __syncthreads();
-    bool on[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) on[n] = n * 8 + g < a.rows;
-    const uint8_t *xl = xs + g * pitch + t * 16;
+    const uint8_t *xl[NT];
     float acc[NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+        xl[n] = xs + min(n * 8 + g, a.rows - 1) * pitch + t * 16;
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
-    int i = 0, tile = blockIdx.x, side = 0;
-    auto step = [&](Unit<GROUP> &cur) {
-        const int u = warp + i * WARPS;
-        if (u < a.units) products<X, NT, GROUP>(cur, acc, xl + u * (kUnit * 2), 8 * pitch, part_step, on);
-        fetch(cur);
-        if (++i < per) return;
-        i = 0;
+    }
+    int side = 0;
+    uint32_t slot = 0;
+    for (int tile = blockIdx.x; tile < a.tiles; tile += gridDim.x, side ^= 1) {
+        ask_scales(tile + gridDim.x, side ^ 1);  // (joins the next group; complete before this tile's barrier)
+        const uint8_t *sl = scales + side * sside + g * spitch;
+        for (int u = warp; u < a.units; u += WARPS) {
+            copy_wait<kAhead - 2>();
+            const uint4 wa = ring[slot], wb = ring[slot + 32];
+            slot = (slot + 64) & (kAhead * 64 - 1);
+            float f0[kGroups], f1[kGroups];
+            load_scales<kGroups, Elem>(sl + u * (kGroups * (int)sizeof(Elem)), f0);
+            load_scales<kGroups, Elem>(sl + 8 * spitch + u * (kGroups * (int)sizeof(Elem)), f1);
+            products<X, NT, GROUP>(wa, wb, acc, xl, u * (kUnit * 2), part_step, f0, f1);
+            ask();  // into the slot read last time
+        }
         // the tile's sums: one barrier a tile, two sides in turn (a side is
         // written again only after the next tile's barrier)
-        float *mine_red = red + side * kRed + warp * (NT * 8 * 16);
+        float *mine = red + side * kSum + warp * (NT * 128);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            mine_red[(n * 8 + 2 * t) * 16 + g] = acc[n][0];
-            mine_red[(n * 8 + 2 * t + 1) * 16 + g] = acc[n][1];
-            mine_red[(n * 8 + 2 * t) * 16 + g + 8] = acc[n][2];
-            mine_red[(n * 8 + 2 * t + 1) * 16 + g + 8] = acc[n][3];
+            mine[(n * 8 + 2 * t) * 16 + g] = acc[n][0];
+            mine[(n * 8 + 2 * t + 1) * 16 + g] = acc[n][1];
+            mine[(n * 8 + 2 * t) * 16 + g + 8] = acc[n][2];
+            mine[(n * 8 + 2 * t + 1) * 16 + g + 8] = acc[n][3];
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
+        }
+        if (per < kAhead) {  // the next scales may be in a group still on the way, or in none
+            copy_commit();
+            copy_wait<0>();
         }
         __syncthreads();
         for (int o = threadIdx.x; o < a.rows * 16; o += kThreads) {
@@ -281,75 +338,132 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? few_ctas(X::kParts, N
             if (co >= a.co) continue;
             float v = 0.0f;
 #pragma unroll
-            for (int q = 0; q < WARPS; ++q) v += red[side * kRed + q * (NT * 8 * 16) + o];
-            v = activate(v + (a.bias ? a.bias[co] : 0.0f), a.act);
+            for (int q = 0; q < WARPS; ++q) v += red[side * kSum + q * (NT * 128) + o];
+            v = activate(fmaf(v, kCodeScale, a.bias ? a.bias[co] : 0.0f), a.act);
             static_cast<Elem *>(a.y)[(long long)m * a.co + co] = elem_from<Elem>(v);
         }
-        side ^= 1;
-        tile += gridDim.x;
-    };
-    int j = 0;
-    for (; j + 1 < mine; j += 2) {
-        step(un[0]);
-        step(un[1]);
     }
-    if (j < mine) step(un[0]);
+    copy_wait<0>();
 }
 
-template <typename X, int GROUP, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32) w4_many_kernel(W4Args a, int vec) {
+// WC: co tiles of a CTA; its eight warps take k in turns of WK = 8 / WC units.
+template <typename X, int NT, int GROUP, int WC>
+__global__ void __launch_bounds__(256) w4_many_kernel(W4Args a, int vec) {
     using Elem = typename X::Elem;
-    constexpr int kThreads = WARPS * 32, NT = kManyRows / 8;
-    constexpr int kPart = kManyRows * kManyPitch, kSide = X::kParts * kPart;
-    extern __shared__ __align__(16) uint8_t shm[];  // [2][parts][64] rows of kManyPitch bytes
+    constexpr int WK = 8 / WC, kTurn = WK * kUnit, kPitch = kTurn * 2 + kPad, kGroups = kUnit / GROUP;
+    constexpr int kPart = NT * 8 * kPitch, kSide = X::kParts * kPart;
+    extern __shared__ __align__(16) uint8_t shm[];  // rings, then x [3][parts][8 NT] rows of kPitch bytes; at the end the warps' sums
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int m0 = blockIdx.y * kManyRows, rows = min(kManyRows, a.rows - m0);
-    const int tile = blockIdx.x * WARPS + warp;
-    const bool live = tile < a.tiles;
+    const int wc = warp % WC, wk = warp / WC;
+    uint4 *ring = reinterpret_cast<uint4 *>(shm + warp * (kAhead * 1024)) + lane;
+    uint8_t *xs = shm + 8 * kAhead * 1024;
+    const int m0 = blockIdx.y * (NT * 8), rows = min(NT * 8, a.rows - m0);
+    const int tile = blockIdx.x * WC + wc;
+    const int turns = (a.units + WK - 1) / WK;
     pdl_trigger();
     pdl_wait();
     const Elem *x = static_cast<const Elem *>(a.x) + (long long)m0 * a.ci;
-    const int co = tile * 16 + g;
-    const Elem *s0 = static_cast<const Elem *>(a.scales) + (long long)co * a.ng, *s1 = s0 + 8LL * a.ng;
-    const uint4 *w = a.w + (long long)tile * a.units * 64 + lane;
-    const bool on0 = co < a.co, on1 = co + 8 < a.co;
-    auto stage = [&](int u) {
-        uint8_t *dst = shm + (u & 1) * kSide;
-        for (int i = threadIdx.x; i < rows * (kUnit / 8); i += kThreads) {
-            const int m = i / (kUnit / 8), k = (i % (kUnit / 8)) * 8;
-            uint4 v[X::kParts];
-            X::load(x + (long long)m * a.ci, u * kUnit + k, a.ci, vec != 0, v);
+    const int r0 = min(tile * 16 + g, a.co - 1), r1 = min(tile * 16 + g + 8, a.co - 1);  // (rows past the last are not stored)
+    const Elem *s0 = static_cast<const Elem *>(a.scales) + (long long)r0 * a.ng, *s1 = static_cast<const Elem *>(a.scales) + (long long)r1 * a.ng;
+    const uint4 *fw = a.w + ((long long)tile * a.units + wk) * 64 + lane;
+    int fu = tile < a.tiles ? wk : a.units, fslot = 0;
+    auto ask = [&]() {
+        if (fu < a.units) {
+            const uint32_t d = smem_addr(ring + fslot * 64);
+            copy16(d, fw);
+            copy16(d + 512, fw + 32);
+            fw += WK * 64;
+            fu += WK;
+        }
+        copy_commit();
+        fslot = fslot + 1 == kAhead ? 0 : fslot + 1;
+    };
+    auto stage = [&](int turn) {
+        uint8_t *dst = xs + turn % 3 * kSide;
+        for (int i = threadIdx.x; i < rows * (kTurn / 8); i += 256) {
+            const int m = i / (kTurn / 8), kk = (i % (kTurn / 8)) * 8, k = turn * kTurn + kk;
+            uint8_t *d = dst + m * kPitch + kk * 2;
+            const Elem *src = x + (long long)m * a.ci;
+            if (X::kParts == 1 && vec && k + 8 <= a.ci) {
+                copy16(smem_addr(d), src + k);
+            } else {
+                uint4 v[X::kParts];
+                X::load(src, k, a.ci, vec != 0, v);
 #pragma unroll
-            for (int r = 0; r < X::kParts; ++r) *reinterpret_cast<uint4 *>(dst + r * kPart + m * kManyPitch + k * 2) = v[r];
+                for (int r = 0; r < X::kParts; ++r) *reinterpret_cast<uint4 *>(d + r * kPart) = v[r];
+            }
         }
     };
-    bool on[NT];
     float acc[NT][4];
+    int row[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        on[n] = n * 8 + g < rows;
+        row[n] = min(n * 8 + g, rows - 1) * kPitch + t * 16 + wk * (kUnit * 2);
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[n][e] = 0.0f;
     }
-    Unit<GROUP> cur, nxt;
-    if (live) cur.fetch(w, 0, s0, s1, a.ng, on0, on1);
+    // x goes two turns ahead, the weights three: x of turn T is in the group
+    // before the last when turn T begins
     stage(0);
-    for (int u = 0; u < a.units; ++u) {
-        __syncthreads();  // unit u is staged, and everyone has left unit u - 1
-        if (live && u + 1 < a.units) nxt.fetch(w, u + 1, s0, s1, a.ng, on0, on1);
-        if (u + 1 < a.units) stage(u + 1);
-        if (live) products<X, NT, GROUP>(cur, acc, shm + (u & 1) * kSide + g * kManyPitch + t * 16, 8 * kManyPitch, kPart, on);
-        cur = nxt;
+    ask();
+    if (turns > 1) stage(1);
+    ask();
+    ask();
+    int slot = 0;
+    float f0[kGroups], f1[kGroups];
+    auto scales = [&](int u) {
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) {
+            const int gi = min(u * kGroups + j, a.ng - 1);
+            f0[j] = elem_f(s0[gi]);
+            f1[j] = elem_f(s1[gi]);
+        }
+    };
+    scales(wk);
+    for (int turn = 0; turn < turns; ++turn) {
+        copy_wait<1>();
+        __syncthreads();  // ... for every thread, and everyone has left the side that is staged next
+        if (turn + 2 < turns) stage(turn + 2);
+        const int u = turn * WK + wk;
+        float c0[kGroups], c1[kGroups];
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j) { c0[j] = f0[j]; c1[j] = f1[j]; }
+        scales(u + WK);
+        const uint4 wa = ring[slot * 64], wb = ring[slot * 64 + 32];
+        slot = slot + 1 == kAhead ? 0 : slot + 1;
+        if (u < a.units && tile < a.tiles) {
+            const uint8_t *xl[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) xl[n] = xs + turn % 3 * kSide + row[n];
+            products<X, NT, GROUP>(wa, wb, acc, xl, 0, kPart, c0, c1);
+        }
+        ask();
     }
-    if (!live) return;
+    copy_wait<0>();
+    if constexpr (WK > 1) {  // the turns' sums, in order
+        float *red = reinterpret_cast<float *>(shm);  // [8][NT * 128]
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) red[warp * (NT * 128) + (n * 4 + e) * 32 + lane] = acc[n][e];
+        __syncthreads();
+        if (wk > 0) return;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                for (int q = 1; q < WK; ++q) acc[n][e] += red[(q * WC + wc) * (NT * 128) + (n * 4 + e) * 32 + lane];
+    }
+    if (tile >= a.tiles) return;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int m = n * 8 + 2 * t + (e & 1), c = co + (e >> 1) * 8;
+            const int m = n * 8 + 2 * t + (e & 1), c = tile * 16 + g + (e >> 1) * 8;
             if (m < rows && c < a.co)
                 static_cast<Elem *>(a.y)[(long long)(m0 + m) * a.co + c] =
-                    elem_from<Elem>(activate(acc[n][e] + (a.bias ? a.bias[c] : 0.0f), a.act));
+                    elem_from<Elem>(activate(fmaf(acc[n][e], kCodeScale, a.bias ? a.bias[c] : 0.0f), a.act));
         }
 }
 
@@ -424,14 +538,18 @@ const void *few_nt(int nt, int group) {
     default: return few_group<X, 4, WARPS>(group);
     }
 }
-template <typename X, int WARPS>
+template <typename X, int NT, int WC>
 const void *many_group(int group) {
-    return group == 32 ? (const void *)&w4_many_kernel<X, 32, WARPS>
-                       : (group == 64 ? (const void *)&w4_many_kernel<X, 64, WARPS> : (const void *)&w4_many_kernel<X, 128, WARPS>);
+    return group == 32 ? (const void *)&w4_many_kernel<X, NT, 32, WC>
+                       : (group == 64 ? (const void *)&w4_many_kernel<X, NT, 64, WC> : (const void *)&w4_many_kernel<X, NT, 128, WC>);
+}
+template <typename X, int NT>
+const void *many_wc(const W4Geom &g) {
+    return g.wc == 8 ? many_group<X, NT, 8>(g.group) : (g.wc == 4 ? many_group<X, NT, 4>(g.group) : many_group<X, NT, 2>(g.group));
 }
 template <typename X>
 const void *pick(const W4Geom &g) {
-    if (g.many) return g.warps == 8 ? many_group<X, 8>(g.group) : (g.warps == 4 ? many_group<X, 4>(g.group) : many_group<X, 2>(g.group));
+    if (g.many) return g.nt == 2 ? many_wc<X, 2>(g) : (g.nt == 4 ? many_wc<X, 4>(g) : many_wc<X, 8>(g));
     return g.warps == 8 ? few_nt<X, 8>(g.nt, g.group) : few_nt<X, 16>(g.nt, g.group);
 }
 
@@ -470,24 +588,35 @@ extern "C" int conv_plan_create_w4(int32_t rows, int32_t c_in, int32_t c_out, in
     g.ng = (c_in + group - 1) / group;
     g.units = (c_in + kUnit - 1) / kUnit;
     g.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
-    const long long xb = (long long)parts * rows * (g.units * (kUnit * 2) + kPad);
-    // x whole in shared memory while it fits (with the warps' sums), else in
-    // pieces; CTAs of 16 warps where it takes more than a third of a SM's.
-    g.many = rows > 32 || xb + 2LL * 16 * g.nt * 128 * 4 > kFewSmem;
+    const int es = conv_esize(dtype);
+    const long long xb = (long long)parts * rows * (g.units * (kUnit * 2) + kPad), sb = 2LL * few_scales(g.units, group, es);
+    auto few = [&](int warps) { return xb + sb + few_sums(warps, g.nt) + few_ring(warps); };
+    // x whole in shared memory while two CTAs of eight warps or one of sixteen
+    // fit a SM, else in turns (fp32 rows, whose splitting is on the way of
+    // every turn, only where not even eight warps fit).
+    g.warps = few(8) <= 112 * 1024 || few(16) > kFewMost ? 8 : 16;
+    g.many = rows > 32 || few(g.warps) > (parts == 3 || g.warps == 16 ? kFewMost : 112 * 1024);
     if (g.many) {
         g.warps = 8;
-        while (g.warps > 2 && (tiles + g.warps - 1) / g.warps * ((rows + kManyRows - 1) / kManyRows) < p->num_sms) g.warps /= 2;
-        g.smem = 2 * parts * kManyRows * kManyPitch;
-        g.grid = (tiles + g.warps - 1) / g.warps;
+        g.nt = rows <= 16 ? 2 : (rows <= 32 ? 4 : 8);
+        const int blocks = (rows + g.nt * 8 - 1) / (g.nt * 8);
+        auto smem = [&](int wc) {
+            const int x = 3 * parts * g.nt * 8 * (8 / wc * kUnit * 2 + kPad), ring = 8 * kAhead * 1024, sums = 8 * g.nt * 128 * 4;
+            return ring + x > sums ? ring + x : sums;
+        };
+        // fewer output channels a CTA, and longer turns, until the card is full
+        g.wc = 8;
+        while (g.wc > 2 && (long long)((tiles + g.wc - 1) / g.wc) * blocks < p->num_sms && smem(g.wc / 2) <= kSmemMost) g.wc /= 2;
+        g.smem = smem(g.wc);
+        g.grid = (tiles + g.wc - 1) / g.wc;
     } else {
-        const long long red8 = 2LL * 8 * g.nt * 128 * 4;
-        g.warps = xb + red8 <= 72 * 1024 ? 8 : 16;
-        g.smem = (int)(xb + red8 * (g.warps / 8));
-        const int wave = p->num_sms * (g.warps == 8 ? few_ctas(parts, g.nt) : 1);
-        g.grid = tiles < wave ? tiles : wave;
+        g.smem = (int)few(g.warps);
+        int ctas = g.warps == 8 ? few_ctas(parts, g.nt) : 1;
+        while (ctas > 1 && ctas * (g.smem + 1024) > 227 * 1024) --ctas;
+        g.grid = tiles < ctas * p->num_sms ? tiles : ctas * p->num_sms;
     }
     snprintf(p->desc, sizeof(p->desc), "w4 %s group=%d %s warps=%d tiles=%d", dtype == CONV_F32 ? "f32" : "bf16", group,
-             g.many ? "x in pieces" : "x in shared memory", g.warps, tiles);
+             g.many ? "x in turns" : "x in shared memory", g.warps, tiles);
     *out_plan = p;
     return CONV_OK;
 }
@@ -563,7 +692,7 @@ extern "C" int conv_run_w4(const conv_plan_t *plan, const void *x, const void *p
         if (rc != CONV_OK) return rc;
     }
     void *args[] = {&a, &vec};
-    const dim3 grid((unsigned)g.grid, (unsigned)(g.many ? (rows + kManyRows - 1) / kManyRows : 1));
+    const dim3 grid((unsigned)g.grid, (unsigned)(g.many ? (rows + g.nt * 8 - 1) / (g.nt * 8) : 1));
     const cudaError_t e = conv_launch(k, grid, dim3(g.warps * 32), args, (size_t)g.smem, (cudaStream_t)stream);
     return e == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }
