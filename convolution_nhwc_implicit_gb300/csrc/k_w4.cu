@@ -104,18 +104,16 @@ constexpr float kCodeScale = 64.0f;
 struct XBf16 {
     static constexpr int kParts = 1;
     using Elem = __nv_bfloat16;
-    __device__ static __forceinline__ void load(const Elem *row, int k, int ci, bool vec, uint4 (&out)[1]) {
-        out[0] = make_uint4(0u, 0u, 0u, 0u);
-        if (vec && k + 8 <= ci) {
-            out[0] = *reinterpret_cast<const uint4 *>(row + k);
-        } else {
-            uint32_t b[4] = {0u, 0u, 0u, 0u};
+    using Raw = uint4;
+    __device__ static __forceinline__ Raw fetch(const Elem *row, int k, int ci, bool vec) {
+        if (vec && k + 8 <= ci) return *reinterpret_cast<const uint4 *>(row + k);
+        uint32_t b[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (k + i < ci) b[i >> 1] |= (uint32_t)__bfloat16_as_ushort(row[k + i]) << (16 * (i & 1));
-            out[0] = make_uint4(b[0], b[1], b[2], b[3]);
-        }
+        for (int i = 0; i < 8; ++i)
+            if (k + i < ci) b[i >> 1] |= (uint32_t)__bfloat16_as_ushort(row[k + i]) << (16 * (i & 1));
+        return make_uint4(b[0], b[1], b[2], b[3]);
     }
+    __device__ static __forceinline__ void parts(const Raw &r, uint4 (&out)[1]) { out[0] = r; }
 };
 struct XF32 {
     static constexpr int kParts = 3;
@@ -136,21 +134,25 @@ struct XF32 {
             p[1] = p[2] = 0u;
         }
     }
-    __device__ static __forceinline__ void load(const Elem *row, int k, int ci, bool vec, uint4 (&out)[3]) {
-        float f[8];
+    struct Raw { float f[8]; };
+    __device__ static __forceinline__ Raw fetch(const Elem *row, int k, int ci, bool vec) {
+        Raw r;
         if (vec && k + 8 <= ci) {
             const float4 u = *reinterpret_cast<const float4 *>(row + k), v = *reinterpret_cast<const float4 *>(row + k + 4);
-            f[0] = u.x; f[1] = u.y; f[2] = u.z; f[3] = u.w; f[4] = v.x; f[5] = v.y; f[6] = v.z; f[7] = v.w;
+            r.f[0] = u.x; r.f[1] = u.y; r.f[2] = u.z; r.f[3] = u.w; r.f[4] = v.x; r.f[5] = v.y; r.f[6] = v.z; r.f[7] = v.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = k + i < ci ? row[k + i] : 0.0f;
+            for (int i = 0; i < 8; ++i) r.f[i] = k + i < ci ? row[k + i] : 0.0f;
         }
+        return r;
+    }
+    __device__ static __forceinline__ void parts(const Raw &r, uint4 (&out)[3]) {
         uint32_t b[3][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t lo[3], hi[3];
-            split(f[2 * i], lo);
-            split(f[2 * i + 1], hi);
+            split(r.f[2 * i], lo);
+            split(r.f[2 * i + 1], hi);
 #pragma unroll
             for (int q = 0; q < 3; ++q) b[q][i] = lo[q] | (hi[q] << 16);
         }
@@ -282,14 +284,25 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? few_ctas(X::kParts, N
     ask_scales(blockIdx.x, 0);
 #pragma unroll
     for (int i = 0; i < kAhead - 1; ++i) ask();  // (the first group holds the scales too)
-    // x into shared memory, eight channels a thread at a time
-    const int eights = a.units * (kUnit / 8);
-    for (int i = threadIdx.x; i < a.rows * eights; i += kThreads) {
-        const int m = i / eights, k = (i - m * eights) * 8;
-        uint4 v[X::kParts];
-        X::load(x + (long long)m * a.ci, k, a.ci, vec != 0, v);
+    // x into shared memory, eight channels a thread at a time, four times over
+    // before the first is used
+    const int eights = a.units * (kUnit / 8), items = a.rows * eights;
+    for (int i = threadIdx.x; i < items; i += 4 * kThreads) {
+        typename X::Raw raw[4];
 #pragma unroll
-        for (int r = 0; r < X::kParts; ++r) *reinterpret_cast<uint4 *>(xs + r * part_step + m * pitch + k * 2) = v[r];
+        for (int q = 0; q < 4; ++q) {
+            const int j = i + q * kThreads, m = j / eights;
+            if (j < items) raw[q] = X::fetch(x + (long long)m * a.ci, (j - m * eights) * 8, a.ci, vec != 0);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int j = i + q * kThreads, m = j / eights;
+            if (j >= items) continue;
+            uint4 v[X::kParts];
+            X::parts(raw[q], v);
+#pragma unroll
+            for (int r = 0; r < X::kParts; ++r) *reinterpret_cast<uint4 *>(xs + r * part_step + m * pitch + (j - m * eights) * 16) = v[r];
+        }
     }
     copy_wait<kAhead - 2>();
     __syncthreads();
@@ -378,21 +391,42 @@ __global__ void __launch_bounds__(256) w4_many_kernel(W4Args a, int vec) {
         copy_commit();
         fslot = fslot + 1 == kAhead ? 0 : fslot + 1;
     };
-    auto stage = [&](int turn) {
-        uint8_t *dst = xs + turn % 3 * kSide;
-        for (int i = threadIdx.x; i < rows * (kTurn / 8); i += 256) {
-            const int m = i / (kTurn / 8), kk = (i % (kTurn / 8)) * 8, k = turn * kTurn + kk;
-            uint8_t *d = dst + m * kPitch + kk * 2;
-            const Elem *src = x + (long long)m * a.ci;
-            if (X::kParts == 1 && vec && k + 8 <= a.ci) {
-                copy16(smem_addr(d), src + k);
-            } else {
-                uint4 v[X::kParts];
-                X::load(src, k, a.ci, vec != 0, v);
+    // A turn's x: copied as it is (cp.async) where it can be, else fetched into
+    // registers before the products of the turn at hand and written after them.
+    const bool straight = X::kParts == 1 && vec && a.ci % 8 == 0;
+    constexpr int kItems = (NT * 8 * (kTurn / 8) + 255) / 256, kHeld = kItems < 4 ? kItems : 4;
+    typename X::Raw held[kHeld];
+    auto each = [&](int from, int count, auto &&use) {
 #pragma unroll
-                for (int r = 0; r < X::kParts; ++r) *reinterpret_cast<uint4 *>(d + r * kPart) = v[r];
-            }
+        for (int q = 0; q < count; ++q) {
+            const int i = threadIdx.x + (from + q) * 256, m = i / (kTurn / 8);
+            if (m < rows) use(q, m, (i % (kTurn / 8)) * 8);
         }
+    };
+    auto store = [&](int turn, int m, int kk, const typename X::Raw &r) {
+        uint4 v[X::kParts];
+        X::parts(r, v);
+#pragma unroll
+        for (int p = 0; p < X::kParts; ++p)
+            *reinterpret_cast<uint4 *>(xs + turn % 3 * kSide + p * kPart + m * kPitch + kk * 2) = v[p];
+    };
+    auto begin = [&](int turn) {
+        if (straight) {
+            each(0, kItems, [&](int, int m, int kk) {
+                const int k = turn * kTurn + kk;
+                uint8_t *d = xs + turn % 3 * kSide + m * kPitch + kk * 2;
+                if (k < a.ci) copy16(smem_addr(d), x + (long long)m * a.ci + k);
+                else *reinterpret_cast<uint4 *>(d) = make_uint4(0u, 0u, 0u, 0u);
+            });
+        } else {
+            each(0, kHeld, [&](int q, int m, int kk) { held[q] = X::fetch(x + (long long)m * a.ci, turn * kTurn + kk, a.ci, vec != 0); });
+        }
+    };
+    auto end = [&](int turn) {
+        if (straight) return;
+        each(0, kHeld, [&](int q, int m, int kk) { store(turn, m, kk, held[q]); });
+        for (int f = kHeld; f < kItems; ++f)
+            each(f, 1, [&](int, int m, int kk) { store(turn, m, kk, X::fetch(x + (long long)m * a.ci, turn * kTurn + kk, a.ci, vec != 0)); });
     };
     float acc[NT][4];
     int row[NT];
@@ -404,9 +438,13 @@ __global__ void __launch_bounds__(256) w4_many_kernel(W4Args a, int vec) {
     }
     // x goes two turns ahead, the weights three: x of turn T is in the group
     // before the last when turn T begins
-    stage(0);
+    begin(0);
+    end(0);
     ask();
-    if (turns > 1) stage(1);
+    if (turns > 1) {
+        begin(1);
+        end(1);
+    }
     ask();
     ask();
     int slot = 0;
@@ -423,7 +461,7 @@ __global__ void __launch_bounds__(256) w4_many_kernel(W4Args a, int vec) {
     for (int turn = 0; turn < turns; ++turn) {
         copy_wait<1>();
         __syncthreads();  // ... for every thread, and everyone has left the side that is staged next
-        if (turn + 2 < turns) stage(turn + 2);
+        if (turn + 2 < turns) begin(turn + 2);
         const int u = turn * WK + wk;
         float c0[kGroups], c1[kGroups];
 #pragma unroll
@@ -437,6 +475,7 @@ __global__ void __launch_bounds__(256) w4_many_kernel(W4Args a, int vec) {
             for (int n = 0; n < NT; ++n) xl[n] = xs + turn % 3 * kSide + row[n];
             products<X, NT, GROUP>(wa, wb, acc, xl, 0, kPart, c0, c1);
         }
+        if (turn + 2 < turns) end(turn + 2);
         ask();
     }
     copy_wait<0>();

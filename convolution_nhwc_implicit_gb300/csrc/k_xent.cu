@@ -59,6 +59,8 @@ constexpr uint32_t kStage = 2 * kHalf;
 constexpr uint32_t kBox = 32 * 128;            // staging of one warp: 32 rows x 64 bf16
 constexpr uint32_t kSmem = 1024 + kStages * kStage + 8 * kBox + 256;
 constexpr int kThreads = 320;
+// K blocks of a run worth the launch that joins runs (3 us, ten blocks' time).
+constexpr int kMinRun = 16;
 constexpr int kGroupM = 32;         // tile rows walked before the next tile column
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kSmem <= 232448, "shared memory of a CTA");
@@ -719,15 +721,17 @@ extern "C" int conv_plan_create_xent(int32_t rows, int32_t c_in, int32_t classes
     g.piece = ceil_div(g.tiles_n, g.pieces) * kTile;
     g.pieces = ceil_div(all, g.piece);
     // Few output tiles: each product's K axis in runs, so that every pair of
-    // SMs has one (runs of at least eight blocks).
+    // SMs has one.
     const int pairs = p->num_sms / 2, pt = g.piece / kTile;
     const int tiles = (g.tiles_m + pt) * g.tiles_d;
     const int kx = g.piece / kBK, kw = ceil_div(rows, kBK);
     int sx = 1, sw = 1;
     if (tiles > 0 && tiles < pairs) {
         const int want = pairs / tiles;
-        sx = want < (kx + 7) / 8 ? want : (kx + 7) / 8;
-        if (g.pieces == 1) sw = want < (kw + 7) / 8 ? want : (kw + 7) / 8;
+        sx = want < kx / kMinRun ? want : kx / kMinRun;
+        if (g.pieces == 1) sw = want < kw / kMinRun ? want : kw / kMinRun;
+        if (sx < 1) sx = 1;
+        if (sw < 1) sw = 1;
     }
     g.dx_kper = ceil_div(kx, sx);
     g.dx_split = ceil_div(kx, g.dx_kper);

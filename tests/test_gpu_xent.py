@@ -90,9 +90,11 @@ CASES = [
     (1000, 256, 300, 0),
     (300, 64, 2000, 512),          # pieces, the last one short
     (130, 77, 1300, 256),          # pieces with padded copies
-    (40, 96, 3000, 1024),          # pieces with products in runs, the last piece with fewer runs
+    (40, 96, 3000, 1024),          # pieces, few rows
     (513, 264, 2100, 768),
     (5, 2048, 20000, 0),
+    (40, 96, 12000, 4096),         # pieces with products in runs, the last piece with fewer runs
+    (3000, 48, 600, 0),            # dw in runs
 ]
 
 
