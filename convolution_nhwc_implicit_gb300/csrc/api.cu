@@ -443,9 +443,10 @@ const char *conv_plan_describe(const conv_plan_t *plan) { return plan ? plan->de
 int conv_plan_launches(const conv_plan_t *plan) {
     if (!plan) return CONV_ERR_NULL_ARG;
     if (plan->s.n == 0) return 0;
-    if (plan->algo == CONV_ALGO_GROUPNORM) return plan->gn.fwd.K > 0 ? 1 : 2;  // the forward run
+    if (plan->algo == CONV_ALGO_GROUPNORM) // the forward run
+        return plan->gn.fwd.K > 0 ? 1 : 2;
     // (the forward run; its gradient takes two launches a piece of the classes, and more for joined sums)
-    if (plan->algo == CONV_ALGO_XENT) return plan->xent.dp == plan->s.c_in ? 2 : 4;
+    if (plan->algo == CONV_ALGO_XENT) return plan->xent.dp == plan->s.c_in ? 2 : 3;
     return (plan->algo == CONV_ALGO_IGEMM && plan->ig.prep) ? 2 : 1;
 }
 

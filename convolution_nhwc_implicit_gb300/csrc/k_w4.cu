@@ -637,16 +637,21 @@ extern "C" int conv_plan_create_w4(int32_t rows, int32_t c_in, int32_t c_out, in
     g.many = rows > 32 || few(g.warps) > (parts == 3 || g.warps == 16 ? kFewMost : 112 * 1024);
     if (g.many) {
         g.warps = 8;
-        g.nt = rows <= 16 ? 2 : (rows <= 32 ? 4 : 8);
-        const int blocks = (rows + g.nt * 8 - 1) / (g.nt * 8);
-        auto smem = [&](int wc) {
-            const int x = 3 * parts * g.nt * 8 * (8 / wc * kUnit * 2 + kPad), ring = 8 * kAhead * 1024, sums = 8 * g.nt * 128 * 4;
+        auto smem = [&](int nt, int wc) {
+            const int x = 3 * parts * nt * 8 * (8 / wc * kUnit * 2 + kPad), ring = 8 * kAhead * 1024, sums = 8 * nt * 128 * 4;
             return ring + x > sums ? ring + x : sums;
         };
-        // fewer output channels a CTA, and longer turns, until the card is full
+        auto ctas = [&](int nt, int wc) { return (long long)((tiles + wc - 1) / wc) * ((rows + nt * 8 - 1) / (nt * 8)); };
+        // until the card is full: fewer output channels a CTA and longer turns,
+        // then fewer rows
+        g.nt = rows <= 16 ? 2 : (rows <= 32 ? 4 : 8);
         g.wc = 8;
-        while (g.wc > 2 && (long long)((tiles + g.wc - 1) / g.wc) * blocks < p->num_sms && smem(g.wc / 2) <= kSmemMost) g.wc /= 2;
-        g.smem = smem(g.wc);
+        while (ctas(g.nt, g.wc) < p->num_sms) {
+            if (g.wc > 2 && smem(g.nt, g.wc / 2) <= kSmemMost) g.wc /= 2;
+            else if (g.nt > 2) g.nt /= 2;
+            else break;
+        }
+        g.smem = smem(g.nt, g.wc);
         g.grid = (tiles + g.wc - 1) / g.wc;
     } else {
         g.smem = (int)few(g.warps);

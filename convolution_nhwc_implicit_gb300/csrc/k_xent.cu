@@ -573,16 +573,25 @@ __global__ void __launch_bounds__(256) xent_finish_kernel(const float *part, int
     }
 }
 
-// Rows of d values copied to rows of dp >= d, the rest zeros (rows whose
-// length is not a multiple of eight cannot be addressed by TMA).
-__global__ void __launch_bounds__(256) xent_pad_kernel(const __nv_bfloat16 *src, __nv_bfloat16 *dst, int d, int dp, long long total) {
+// The rows of x and w, d values each, copied to rows of dp >= d, the rest
+// zeros (rows whose length is not a multiple of eight cannot be addressed by
+// TMA).  Eight values of a row a thread.
+__global__ void __launch_bounds__(256) xent_pad_kernel(const __nv_bfloat16 *x, __nv_bfloat16 *xp, int rows, const __nv_bfloat16 *w,
+                                                       __nv_bfloat16 *wp, int classes, int d, int dp) {
     pdl_trigger();
     pdl_wait();
-    const __nv_bfloat16 zero = __ushort_as_bfloat16(0);
+    const int eights = dp / 8;
+    const long long total = ((long long)rows + classes) * eights;
     for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long long)gridDim.x * 256) {
-        const long long r = i / dp;
-        const int c = (int)(i - r * dp);
-        dst[i] = c < d ? src[r * d + c] : zero;
+        const long long r = i / eights;
+        const int c = (int)(i - r * eights) * 8;
+        const __nv_bfloat16 *src = r < rows ? x + r * d : w + (r - rows) * d;
+        __nv_bfloat16 *dst = r < rows ? xp + r * dp : wp + (r - rows) * dp;
+        uint32_t v[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (c + e < d) v[e / 2] |= (uint32_t)__bfloat16_as_ushort(src[c + e]) << (16 * (e & 1));
+        *reinterpret_cast<uint4 *>(dst + c) = make_uint4(v[0], v[1], v[2], v[3]);
     }
 }
 
@@ -664,21 +673,16 @@ bool overlap(const void *a, size_t na, const void *b, size_t nb) {
 // Operands as TMA can address them: as given, or padded copies.
 int operands(const conv_plan *p, const Space &sp, char *ws, const void *&x, const void *&w, cudaStream_t st) {
     if (p->xent.dp == p->s.c_in) return CONV_OK;
-    const long long n[2] = {p->s.n, p->s.c_out};
-    const void **src[2] = {&x, &w};
-    char *dst[2] = {ws + sp.xp, ws + sp.wp};
-    for (int i = 0; i < 2; ++i) {
-        const __nv_bfloat16 *s = static_cast<const __nv_bfloat16 *>(*src[i]);
-        __nv_bfloat16 *d = reinterpret_cast<__nv_bfloat16 *>(dst[i]);
-        int cols = p->s.c_in, dp = p->xent.dp;
-        long long total = n[i] * dp;
-        void *args[] = {&s, &d, &cols, &dp, &total};
-        const long long blocks = (total + 255) / 256;
-        if (conv_launch((const void *)&xent_pad_kernel, dim3((unsigned)(blocks < 8LL * p->num_sms ? blocks : 8LL * p->num_sms)),
-                        dim3(256), args, 0, st) != cudaSuccess)
-            return CONV_ERR_CUDA;
-        *src[i] = d;
-    }
+    const __nv_bfloat16 *xs = static_cast<const __nv_bfloat16 *>(x), *wsrc = static_cast<const __nv_bfloat16 *>(w);
+    __nv_bfloat16 *xp = reinterpret_cast<__nv_bfloat16 *>(ws + sp.xp), *wp = reinterpret_cast<__nv_bfloat16 *>(ws + sp.wp);
+    int rows = p->s.n, classes = p->s.c_out, d = p->s.c_in, dp = p->xent.dp;
+    void *args[] = {&xs, &xp, &rows, &wsrc, &wp, &classes, &d, &dp};
+    const long long blocks = (((long long)rows + classes) * (dp / 8) + 255) / 256, most = 8LL * p->num_sms;
+    if (conv_launch((const void *)&xent_pad_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), args, 0, st) !=
+        cudaSuccess)
+        return CONV_ERR_CUDA;
+    x = xp;
+    w = wp;
     return CONV_OK;
 }
 
