@@ -78,7 +78,7 @@ struct DwpwGeom {
 struct GnGeom {
     float eps;
     struct Dir {
-        int S, ppx;
+        int S, ppx, past_l2;
         int K, cpx, gb, cb;
     } fwd, bwd;
 };

@@ -44,6 +44,7 @@ constexpr int kWarps = kThreads / 32;
 // two of the gradient's 128 for bf16 (eight channels a thread), three for fp32.
 constexpr int kCtas = 3;
 __host__ __device__ constexpr int grad_ctas(int es) { return es == 2 ? 2 : kCtas; }
+constexpr long long kL2Bytes = 100ll << 20;  // of maps that L2 holds from one launch to the next
 constexpr int kStageRuns = 4096;            // partial results a CTA stages (32 KB)
 constexpr int kResident = 50 * 1024, kResidentMost = 88 * 1024;  // map bytes of a resident CTA (four a SM, two)
 constexpr int kMaxC = 8192;  // channels: their sums stay in shared memory (16 bytes each)
@@ -103,6 +104,7 @@ struct GnArgs {
     // pixels each)
     int gb, cb, K, ent;    // ent: entries of the threads' sums in shared memory
     float eps;
+    int past_l2;               // two launches: the maps are larger than L2
 };
 
 // 1/d of a pair from one hardware reciprocal (its unit is the bound of the
@@ -430,6 +432,13 @@ __device__ __forceinline__ float2 join_runs(const GnArgs &a, const float2 *p, in
     return make_float2(mu, 1.0f / sqrtf(m2 * inv + a.eps));
 }
 
+// Stores one vector, as data that is not read again soon if `past`.
+template <typename Raw>
+__device__ __forceinline__ void put(Raw *p, const Raw &v, bool past) {
+    if (past) __stcs(p, v);
+    else *p = v;
+}
+
 // What a thread's channels need of the forward formula.
 template <int VEC, int PAIRS>
 __device__ __forceinline__ void set_lane(float2 (&v)[PAIRS], int e, float f) {
@@ -437,9 +446,10 @@ __device__ __forceinline__ void set_lane(float2 (&v)[PAIRS], int e, float f) {
     if (VEC == 1) v[0].y = 0.0f;
 }
 
-// y = act(gamma (x - mean) rstd + beta) over one run of pixels.  The runs are
-// taken in the order opposite to the statistics': of maps larger than L2 the
-// last runs read are still there.
+// y = act(gamma (x - mean) rstd + beta) over one run of pixels, from its end to
+// its start: of maps larger than L2 the statistics left the ends of the runs
+// there.  Results of such maps are written past it (a.past_l2), so that they do
+// not drive out what is still to be read.
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(GnArgs a) {
     using V = Vec<T, VEC>;
@@ -478,17 +488,18 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(GnArgs a) {
             set_lane<VEC>(sc, e, st.y * (a.gamma ? a.gamma[c] : 1.0f));
             set_lane<VEC>(be, e, a.beta ? a.beta[c] : 0.0f);
         }
-        T *o = y + cv.r * a.pout + col * VEC;
+        const int cnt = cv.count(np), end = cv.r + (cnt - 1) * cv.R;  // this thread's last pixel
+        T *o = y + end * a.pout + col * VEC;
         const long long so = cv.R * a.pout;
-        const T *from[1] = {x + cv.r * a.px + col * VEC};
-        const long long step[1] = {cv.R * a.px};
-        walk<1, Raw>(ring, from, step, cv.count(np), [&](const Raw (&v)[1]) {
+        const T *from[1] = {x + end * a.px + col * VEC};
+        const long long step[1] = {-cv.R * a.px};
+        walk<1, Raw>(ring, from, step, cnt, [&](const Raw (&v)[1]) {
             float2 f[P];
             V::unpack(v[0], f);
 #pragma unroll
             for (int e = 0; e < P; ++e) f[e] = act2<ACT>(fma2(add2(f[e], mu[e]), sc[e], be[e]));
-            *reinterpret_cast<Raw *>(o) = V::pack(f);
-            o += so;
+            put(reinterpret_cast<Raw *>(o), V::pack(f), a.past_l2);
+            o -= so;
         });
     }
 }
@@ -628,7 +639,7 @@ __device__ __forceinline__ void join_rows_of_channels(const GnArgs &a, long long
         __syncthreads();
     }
 }
-// dx over one run of pixels (grid rows past the first `head`); the first
+// dx over one run of pixels, backwards like y (grid rows past the first `head`); the first
 // `head` (0 or 1) grid rows join the channels' sums of every image and run into
 // dgamma and dbeta, 32 channels a CTA.
 template <typename T, int VEC, int ACT>
@@ -674,13 +685,14 @@ __global__ void __launch_bounds__(kThreads, grad_ctas(sizeof(T))) gn_bwd_dx_kern
             set_lane<VEC>(c1, e, sum[g].x);
             set_lane<VEC>(c2, e, sum[g].y);
         }
-        T *o = dx + cv.r * a.pout + col * VEC;
+        const int cnt = cv.count(np), end = cv.r + (cnt - 1) * cv.R;
+        T *o = dx + end * a.pout + col * VEC;
         const long long so = cv.R * a.pout;
-        const T *from[2] = {x + cv.r * a.px + col * VEC, dy + cv.r * a.pdy + col * VEC};
-        const long long step[2] = {cv.R * a.px, cv.R * a.pdy};
-        walk<2, Raw>(ring, from, step, cv.count(np), [&](const Raw (&v)[2]) {
-            *reinterpret_cast<Raw *>(o) = ln.dx(v[0], v[1], c1, c2);
-            o += so;
+        const T *from[2] = {x + end * a.px + col * VEC, dy + end * a.pdy + col * VEC};
+        const long long step[2] = {-cv.R * a.px, -cv.R * a.pdy};
+        walk<2, Raw>(ring, from, step, cnt, [&](const Raw (&v)[2]) {
+            put(reinterpret_cast<Raw *>(o), ln.dx(v[0], v[1], c1, c2), a.past_l2);
+            o -= so;
         });
     }
 }
@@ -1013,7 +1025,7 @@ GnArgs base_args(const conv_plan *p, const GnGeom::Dir &d, const void *x, long l
     GnArgs a = {};
     a.x = x; a.px = px; a.out = out; a.pout = pout;
     a.N = p->s.n; a.HW = p->s.h * p->s.w; a.C = p->s.c_in; a.G = p->groups; a.cg = p->s.c_in / p->groups;
-    a.S = d.S; a.ppx = d.ppx; a.eps = p->gn.eps;
+    a.S = d.S; a.ppx = d.ppx; a.past_l2 = d.past_l2; a.eps = p->gn.eps;
     a.part = static_cast<float2 *>(ws);
     a.partc = a.part + (long long)a.N * a.S * a.G;
     return a;
@@ -1046,6 +1058,7 @@ void plan_direction(const conv_plan *p, int maps, GnGeom::Dir &d, size_t &ws) {
     if (runs < 1) runs = 1;
     d.ppx = (int)((HW + runs - 1) / runs);
     d.S = (HW + d.ppx - 1) / d.ppx;
+    d.past_l2 = (long long)N * HW * C * es * maps > kL2Bytes;
     ws = (size_t)N * d.S * ((size_t)G + (maps > 1 ? C : 0)) * sizeof(float2);
     // Clusters: the fewest groups of a CTA that fill whole vectors and 64
     // bytes of a pixel (a DRAM burst); the fewest CTAs an image that hold their

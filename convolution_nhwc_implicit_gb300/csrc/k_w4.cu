@@ -588,7 +588,7 @@ const void *many_wc(const W4Geom &g) {
 }
 template <typename X>
 const void *pick(const W4Geom &g) {
-    if (g.many) return g.nt == 2 ? many_wc<X, 2>(g) : (g.nt == 4 ? many_wc<X, 4>(g) : many_wc<X, 8>(g));
+    if (g.many) return g.nt == 1 ? many_wc<X, 1>(g) : (g.nt == 2 ? many_wc<X, 2>(g) : (g.nt == 4 ? many_wc<X, 4>(g) : many_wc<X, 8>(g)));
     return g.warps == 8 ? few_nt<X, 8>(g.nt, g.group) : few_nt<X, 16>(g.nt, g.group);
 }
 
@@ -644,11 +644,11 @@ extern "C" int conv_plan_create_w4(int32_t rows, int32_t c_in, int32_t c_out, in
         auto ctas = [&](int nt, int wc) { return (long long)((tiles + wc - 1) / wc) * ((rows + nt * 8 - 1) / (nt * 8)); };
         // until the card is full: fewer output channels a CTA and longer turns,
         // then fewer rows
-        g.nt = rows <= 16 ? 2 : (rows <= 32 ? 4 : 8);
+        g.nt = rows <= 8 ? 1 : (rows <= 16 ? 2 : (rows <= 32 ? 4 : 8));
         g.wc = 8;
         while (ctas(g.nt, g.wc) < p->num_sms) {
             if (g.wc > 2 && smem(g.nt, g.wc / 2) <= kSmemMost) g.wc /= 2;
-            else if (g.nt > 2) g.nt /= 2;
+            else if (g.nt > 1) g.nt /= 2;
             else break;
         }
         g.smem = smem(g.nt, g.wc);

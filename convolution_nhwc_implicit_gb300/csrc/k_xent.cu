@@ -498,9 +498,13 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2 *part, int 
         m = nm;
     };
     if (row < rows)
-        for (int j = warp; j < pairs; j += 8) {
-            const float2 v = part[(long long)j * rows + row];
-            join(v.x, v.y);
+        for (int j = warp; j < pairs; j += 64) {  // eight pairs on their way together
+            float2 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                v[u] = j + 8 * u < pairs ? part[(long long)(j + 8 * u) * rows + row] : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) join(v[u].x, v[u].y);
         }
     sm[warp][lane] = m;
     ss[warp][lane] = s;
