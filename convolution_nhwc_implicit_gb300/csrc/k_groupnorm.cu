@@ -202,60 +202,78 @@ constexpr int kBatch = 4;
 __host__ __device__ constexpr int batches(int maps) { return maps == 2 ? 2 : 3; }
 template <typename Raw>
 __host__ __device__ constexpr int ring_bytes(int maps) { return sizeof(Raw) >= 4 ? kBatch * batches(maps) * kThreads * (int)sizeof(Raw) * maps : 0; }
-template <int MAPS, typename Raw, typename T, typename F>
-__device__ __forceinline__ void walk(uint8_t *ring, const T *(&src)[MAPS], const long long (&step)[MAPS], int cnt, F &&use) {
-    if constexpr (sizeof(Raw) >= 4) {
-        Raw *const base = reinterpret_cast<Raw *>(ring) + threadIdx.x;
-        constexpr int kSlot = kThreads * MAPS, kBatches = batches(MAPS);
-        int to = 0, at = 0, left = cnt;  // batch slots to fill and to read, vectors not yet asked for
-        auto ask = [&]() {
-            Raw *d = base + to * (kBatch * kSlot);
+// The first batches are asked for at construction, so that they are on their
+// way while the thread sets up what it will do with them.
+template <int MAPS, typename Raw, typename T>
+struct Walk {
+    const T *src[MAPS];
+    long long step[MAPS];
+    Raw *base;
+    int cnt, left, to;  // vectors, those not yet asked for, the batch slot to fill
+    __device__ __forceinline__ void ask() {
+        constexpr int kSlot = kThreads * MAPS;
+        Raw *d = base + to * (kBatch * kSlot);
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (u < left)
+        for (int u = 0; u < kBatch; ++u)
+            if (u < left)
 #pragma unroll
-                    for (int m = 0; m < MAPS; ++m) {
-                        copy_vec(d + u * kSlot + m * kThreads, reinterpret_cast<const Raw *>(src[m]));
-                        src[m] += step[m];
-                    }
-            left -= kBatch;
-            copy_commit();
-            if (++to == kBatches) to = 0;
-        };
-#pragma unroll
-        for (int i = 1; i < kBatches; ++i) ask();
-        for (int n = cnt; n > 0; n -= kBatch) {
-            copy_wait<kBatches - 2>();
-            ask();
-            const Raw *d = base + at * (kBatch * kSlot);
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (u < n) {
-                    Raw v[MAPS];
-#pragma unroll
-                    for (int m = 0; m < MAPS; ++m) v[m] = d[u * kSlot + m * kThreads];
-                    use(v);
+                for (int m = 0; m < MAPS; ++m) {
+                    copy_vec(d + u * kSlot + m * kThreads, reinterpret_cast<const Raw *>(src[m]));
+                    src[m] += step[m];
                 }
-            if (++at == kBatches) at = 0;
+        left -= kBatch;
+        copy_commit();
+        if (++to == batches(MAPS)) to = 0;
+    }
+    __device__ __forceinline__ Walk(uint8_t *ring, const T *const (&from)[MAPS], const long long (&by)[MAPS], int n)
+        : base(reinterpret_cast<Raw *>(ring) + threadIdx.x), cnt(n), left(n), to(0) {
+#pragma unroll
+        for (int m = 0; m < MAPS; ++m) {
+            src[m] = from[m];
+            step[m] = by[m];
         }
-        copy_wait<0>();
-    } else {
-        for (; cnt > 0; cnt -= kBatch) {
-            Raw v[kBatch][MAPS];
+        if constexpr (sizeof(Raw) >= 4)
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (u < cnt)
+            for (int i = 1; i < batches(MAPS); ++i) ask();
+    }
+    template <typename F>
+    __device__ __forceinline__ void run(F &&use) {
+        if constexpr (sizeof(Raw) >= 4) {
+            constexpr int kBatches = batches(MAPS), kSlot = kThreads * MAPS;
+            int at = 0;
+            for (int n = cnt; n > 0; n -= kBatch) {
+                copy_wait<kBatches - 2>();
+                ask();
+                const Raw *d = base + at * (kBatch * kSlot);
 #pragma unroll
-                    for (int m = 0; m < MAPS; ++m) {
-                        v[u][m] = *reinterpret_cast<const Raw *>(src[m]);
-                        src[m] += step[m];
+                for (int u = 0; u < kBatch; ++u)
+                    if (u < n) {
+                        Raw v[MAPS];
+#pragma unroll
+                        for (int m = 0; m < MAPS; ++m) v[m] = d[u * kSlot + m * kThreads];
+                        use(v);
                     }
+                if (++at == kBatches) at = 0;
+            }
+            copy_wait<0>();
+        } else {
+            for (; cnt > 0; cnt -= kBatch) {
+                Raw v[kBatch][MAPS];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (u < cnt) use(v[u]);
+                for (int u = 0; u < kBatch; ++u)
+                    if (u < cnt)
+#pragma unroll
+                        for (int m = 0; m < MAPS; ++m) {
+                            v[u][m] = *reinterpret_cast<const Raw *>(src[m]);
+                            src[m] += step[m];
+                        }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)
+                    if (u < cnt) use(v[u]);
+            }
         }
     }
-}
+};
 
 // The threads' pairs of sums, ent[r * C + c], summed over the R rows: channel c
 // into chan[c] (which may be ent itself only for R = 1).  L lanes a channel.
@@ -384,11 +402,12 @@ __global__ void __launch_bounds__(kThreads, 3) gn_stats_kernel(GnArgs a) {
     if (cv.on) {
         for (int col = cv.col; col < cv.cvn; col += kThreads) {
             const T *xc = x + col * VEC;
+            const T *const from[1] = {xc + cv.r * a.px};
+            const long long step[1] = {cv.R * a.px};
+            Walk<1, Raw, T> walk(ring, from, step, cv.count(np));
             StatSums<T, VEC> st;
             st.start(*reinterpret_cast<const Raw *>(xc));
-            const T *from[1] = {xc + cv.r * a.px};
-            const long long step[1] = {cv.R * a.px};
-            walk<1, Raw>(ring, from, step, cv.count(np), [&](const Raw (&v)[1]) { st.take(v[0]); });
+            walk.run([&](const Raw (&v)[1]) { st.take(v[0]); });
             st.put(ent + cv.r * a.C + col * VEC, piv + col * VEC, cv.r == 0);
         }
     }
@@ -404,15 +423,20 @@ __global__ void __launch_bounds__(kThreads, 3) gn_stats_kernel(GnArgs a) {
 
 // The [G][S] partial results of image n, in shared memory if they fit: every
 // load of the CTA is then in flight together, where group by group each would
-// wait for L2.  Ends with a barrier.
+// wait for L2.  Asked for here, a copy group of its own; there after
+// staged_runs, which leaves the `later` groups committed since on their way.
 __device__ __forceinline__ const float2 *stage_runs(const GnArgs &a, int n, float2 *dst) {
     const float2 *src = a.part + (long long)n * a.G * a.S;
     if ((long long)a.G * a.S > kStageRuns) return src;
     const int total = a.G * a.S;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < total; i += kThreads) dst[i] = src[i];
-    __syncthreads();
+    for (int i = threadIdx.x; i < total; i += kThreads) copy_async<8>(tc::smem_u32(dst + i), src + i);
+    copy_commit();
     return dst;
+}
+template <int LATER>
+__device__ __forceinline__ void staged_runs() {
+    copy_wait<LATER>();
+    __syncthreads();
 }
 
 // mean and rstd of a group of m values from the (mean, M2) of its S runs; every
@@ -465,7 +489,15 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(GnArgs a) {
     pdl_wait();
     const T *x = static_cast<const T *>(a.x) + ((long long)n * a.HW + p0) * a.px;
     T *y = static_cast<T *>(a.out) + ((long long)n * a.HW + p0) * a.pout;
+    const int cnt = cv.on ? cv.count(np) : 0, end = cv.r + (cnt - 1) * cv.R;  // this thread's last pixel
+    const long long step[1] = {-cv.R * a.px};
+    auto walk_at = [&](int col) {
+        const T *const from[1] = {x + end * a.px + col * VEC};
+        return Walk<1, Raw, T>(ring, from, step, cnt);
+    };
     const float2 *runs = stage_runs(a, n, stat + a.G);
+    Walk<1, Raw, T> walk = walk_at(cv.col);
+    staged_runs<sizeof(Raw) >= 4 ? batches(1) - 1 : 0>();
     for (int g = warp; g < a.G; g += kWarps) {
         const float2 st = join_runs(a, runs + (long long)g * a.S, lane);
         if (lane == 0) {
@@ -479,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(GnArgs a) {
     __syncthreads();
     if (!cv.on) return;
     for (int col = cv.col; col < cv.cvn; col += kThreads) {
+        if (col != cv.col) walk = walk_at(col);
         float2 mu[P], sc[P], be[P];  // mu: minus the mean
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
@@ -488,12 +521,9 @@ __global__ void __launch_bounds__(kThreads, 3) gn_apply_kernel(GnArgs a) {
             set_lane<VEC>(sc, e, st.y * (a.gamma ? a.gamma[c] : 1.0f));
             set_lane<VEC>(be, e, a.beta ? a.beta[c] : 0.0f);
         }
-        const int cnt = cv.count(np), end = cv.r + (cnt - 1) * cv.R;  // this thread's last pixel
         T *o = y + end * a.pout + col * VEC;
         const long long so = cv.R * a.pout;
-        const T *from[1] = {x + end * a.px + col * VEC};
-        const long long step[1] = {-cv.R * a.px};
-        walk<1, Raw>(ring, from, step, cnt, [&](const Raw (&v)[1]) {
+        walk.run([&](const Raw (&v)[1]) {
             float2 f[P];
             V::unpack(v[0], f);
 #pragma unroll
@@ -583,6 +613,9 @@ __global__ void __launch_bounds__(kThreads, grad_ctas(sizeof(T))) gn_bwd_sums_ke
     const T *dy = static_cast<const T *>(a.dy) + ((long long)n * a.HW + p0) * a.pdy;
     if (cv.on) {
         for (int col = cv.col; col < cv.cvn; col += kThreads) {
+            const T *const from[2] = {x + cv.r * a.px + col * VEC, dy + cv.r * a.pdy + col * VEC};
+            const long long step[2] = {cv.R * a.px, cv.R * a.pdy};
+            Walk<2, Raw, T> walk(ring, from, step, cv.count(np));
             L ln;
             float2 A[P], B[P];
 #pragma unroll
@@ -593,9 +626,7 @@ __global__ void __launch_bounds__(kThreads, grad_ctas(sizeof(T))) gn_bwd_sums_ke
             }
 #pragma unroll
             for (int e = 0; e < P; ++e) A[e] = B[e] = make_float2(0.0f, 0.0f);
-            const T *from[2] = {x + cv.r * a.px + col * VEC, dy + cv.r * a.pdy + col * VEC};
-            const long long step[2] = {cv.R * a.px, cv.R * a.pdy};
-            walk<2, Raw>(ring, from, step, cv.count(np), [&](const Raw (&v)[2]) { ln.sums(v[0], v[1], A, B); });
+            walk.run([&](const Raw (&v)[2]) { ln.sums(v[0], v[1], A, B); });
             put_sums<VEC>(ent + cv.r * a.C + col * VEC, A, B);
         }
     }
@@ -620,14 +651,18 @@ __device__ __forceinline__ void join_rows_of_channels(const GnArgs &a, long long
         const int c = c0 + lane;
         float2 v = make_float2(0.0f, 0.0f);
         if (c < a.C) {
-            long long r = warp;
-            for (; r + 3 * kWarps < rows; r += 4 * kWarps) {
-                float2 t[4];
+            // (sixteen rows on their way together: this is the launch's tail)
+            for (long long r = warp; r < rows; r += 16 * kWarps) {
+                float2 t[16];
 #pragma unroll
-                for (int u = 0; u < 4; ++u) t[u] = a.partc[(r + u * kWarps) * a.C + c];
-                v = add2(v, add2(add2(t[0], t[1]), add2(t[2], t[3])));
+                for (int u = 0; u < 16; ++u)
+                    t[u] = r + u * kWarps < rows ? a.partc[(r + u * kWarps) * a.C + c] : make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1)
+#pragma unroll
+                    for (int u = 0; u < o; ++u) t[u] = add2(t[u], t[u + o]);
+                v = add2(v, t[0]);
             }
-            for (; r < rows; r += kWarps) v = add2(v, a.partc[r * a.C + c]);
         }
         red[warp * 32 + lane] = v;
         __syncthreads();
@@ -639,9 +674,9 @@ __device__ __forceinline__ void join_rows_of_channels(const GnArgs &a, long long
         __syncthreads();
     }
 }
-// dx over one run of pixels, backwards like y (grid rows past the first `head`); the first
-// `head` (0 or 1) grid rows join the channels' sums of every image and run into
-// dgamma and dbeta, 32 channels a CTA.
+// dx over one run of pixels, backwards like y; with `head`, the last grid row
+// joins the channels' sums of every image and run into dgamma and dbeta, 32
+// channels a CTA (last, so that no run waits for a place on the card).
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads, grad_ctas(sizeof(T))) gn_bwd_dx_kernel(GnArgs a, int head) {
     using L = GradLane<T, VEC, ACT>;
@@ -651,46 +686,63 @@ __global__ void __launch_bounds__(kThreads, grad_ctas(sizeof(T))) gn_bwd_dx_kern
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    if ((int)blockIdx.y < head) {
+    if (head && blockIdx.y == gridDim.y - 1) {
         join_rows_of_channels(a, (long long)a.N * a.S, blockIdx.x, gridDim.x, reinterpret_cast<float2 *>(ring));
         return;
     }
     float2 *sum = reinterpret_cast<float2 *>(ring + ring_bytes<Raw>(2));
     const Cover cv(a.C, VEC);
-    const int n = (int)(gridDim.y - 1 - blockIdx.y), s = (int)(gridDim.x - 1 - blockIdx.x);
+    const int n = a.N - 1 - (int)blockIdx.y, s = (int)(gridDim.x - 1 - blockIdx.x);
     const int p0 = s * a.ppx, np = min(a.ppx, a.HW - p0);
     const T *x = static_cast<const T *>(a.x) + ((long long)n * a.HW + p0) * a.px;
     const T *dy = static_cast<const T *>(a.dy) + ((long long)n * a.HW + p0) * a.pdy;
     T *dx = static_cast<T *>(a.out) + ((long long)n * a.HW + p0) * a.pout;
-    const float inv = -1.0f / ((float)a.HW * (float)a.cg);
+    const int cnt = cv.on ? cv.count(np) : 0, end = cv.r + (cnt - 1) * cv.R;
+    const long long step[2] = {-cv.R * a.px, -cv.R * a.pdy};
+    auto walk_at = [&](int col) {
+        const T *const from[2] = {x + end * a.px + col * VEC, dy + end * a.pdy + col * VEC};
+        return Walk<2, Raw, T>(ring, from, step, cnt);
+    };
     const float2 *runs = stage_runs(a, n, sum + a.G);
+    Walk<2, Raw, T> walk = walk_at(cv.col);
+    L ln;
+    auto set = [&](int col) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int c = col * VEC + e;
+            const long long g = (long long)n * a.G + c / a.cg;
+            ln.set(a, e, c, a.mean[g], a.rstd[g]);
+        }
+    };
+    if (cv.on) set(cv.col);
+    const float inv = -1.0f / ((float)a.HW * (float)a.cg);
+    staged_runs<sizeof(Raw) >= 4 ? batches(2) - 1 : 0>();
     for (int g = warp; g < a.G; g += kWarps) {
         const float2 *p = runs + (long long)g * a.S;
+        const float rs = a.rstd[(long long)n * a.G + g];
         float2 v = make_float2(0.0f, 0.0f);
         for (int q = lane; q < a.S; q += 32) v = add2(v, p[q]);
         v.x = warp_sum(v.x);
         v.y = warp_sum(v.y);
-        const float rs = a.rstd[(long long)n * a.G + g];
         if (lane == 0) sum[g] = make_float2(v.x * inv * rs, v.y * inv * rs * rs);
     }
     __syncthreads();
     if (!cv.on) return;
     for (int col = cv.col; col < cv.cvn; col += kThreads) {
-        L ln;
+        if (col != cv.col) {
+            walk = walk_at(col);
+            set(col);
+        }
         float2 c1[P], c2[P];
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-            const int c = col * VEC + e, g = c / a.cg;
-            ln.set(a, e, c, a.mean[(long long)n * a.G + g], a.rstd[(long long)n * a.G + g]);
-            set_lane<VEC>(c1, e, sum[g].x);
-            set_lane<VEC>(c2, e, sum[g].y);
+            const float2 v = sum[(col * VEC + e) / a.cg];
+            set_lane<VEC>(c1, e, v.x);
+            set_lane<VEC>(c2, e, v.y);
         }
-        const int cnt = cv.count(np), end = cv.r + (cnt - 1) * cv.R;
         T *o = dx + end * a.pout + col * VEC;
         const long long so = cv.R * a.pout;
-        const T *from[2] = {x + end * a.px + col * VEC, dy + end * a.pdy + col * VEC};
-        const long long step[2] = {-cv.R * a.px, -cv.R * a.pdy};
-        walk<2, Raw>(ring, from, step, cnt, [&](const Raw (&v)[2]) {
+        walk.run([&](const Raw (&v)[2]) {
             put(reinterpret_cast<Raw *>(o), ln.dx(v[0], v[1], c1, c2), a.past_l2);
             o -= so;
         });
