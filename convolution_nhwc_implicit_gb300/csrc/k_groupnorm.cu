@@ -23,6 +23,28 @@
 // cancellation in M2 = q - s^2/n is bounded by the run's length times 2^-24
 // however far the mean lies from zero.  All statistics are fp32, in a fixed
 // order: results do not change from run to run.
+//
+// Two forms, chosen by sizes alone (plan_direction), measured on a GB300 by
+// graph replay over changing inputs:
+//   clusters    a few groups of an image in the shared memory of one to eight
+//               CTAs, one launch.  7x7x512 bf16 3.8 us (as two launches 8.8);
+//               8x80x80x256 bf16 with Mish 19.9 us (25.5), 2.6 TB/s of its 52
+//               MB; without an activation 17.8 us (22.9), of which a median CTA
+//               (clock stamps in an instrumented build) takes 6.3 until its run
+//               has come and is summed, 4.7 to join and exchange the sums and
+//               3.3 to finish and write.
+//   two launches  sums, then results, where a run does not fit.
+//               16x160x160x128 fp32 with Mish 110 us: the map is read twice,
+//               5.7 TB/s over the three passes of HBM, against 62 us for the two
+//               that cannot be avoided.  The gradient of 8x80x80x256 bf16 29.5
+//               us: a median CTA takes 7.9 at its pixels in the first launch (x and
+//               dy at 6.6 TB/s) and 9.4 in the second, which reads them again
+//               from L2 and writes dx; the rest is the launches' starts and ends.
+// Tried and slower: one cooperative launch whose CTAs wait for one another's
+// sums by image (each further pass adds about 16 us: 8x80x80x256 took 35, 51 and
+// 82 us in one, two and four; 151 us at best for the fp32 map); the clusters
+// reading the fp32 map twice (113 us against 108 as two launches of the time);
+// passes of images that fit L2 (127 to 205 us, each pass paying both launches).
 #include <cuda_bf16.h>
 #include <math.h>
 #include <stdint.h>
@@ -44,9 +66,13 @@ constexpr int kWarps = kThreads / 32;
 // two of the gradient's 128 for bf16 (eight channels a thread), three for fp32.
 constexpr int kCtas = 3;
 __host__ __device__ constexpr int grad_ctas(int es) { return es == 2 ? 2 : kCtas; }
-constexpr long long kL2Bytes = 100ll << 20;  // of maps that L2 holds from one launch to the next
-constexpr int kStageRuns = 4096;            // partial results a CTA stages (32 KB)
-constexpr int kResident = 50 * 1024, kResidentMost = 88 * 1024;  // map bytes of a resident CTA (four a SM, two)
+constexpr long long kL2Bytes = 100ll << 20;  // maps beyond this do not stay in L2 from one launch to the next
+constexpr int kStageRuns = 4096;             // partial results a CTA stages (32 KB)
+// Map bytes of a CTA of a cluster: four CTAs a SM, or two where a cluster of
+// eight cannot hold its runs otherwise.  (8x80x80x256 bf16 by CTAs a cluster: 6
+// 19.6 us, 8 20.0; 5 and 7, whose clusters need a second wave, 26.7 and 24.5.
+// 4 need 102 KB a CTA: 19.3 us in a build that allowed it, where 8 took 19.9.)
+constexpr int kResident = 50 * 1024, kResidentMost = 88 * 1024;
 constexpr int kMaxC = 8192;  // channels: their sums stay in shared memory (16 bytes each)
 
 // VEC consecutive channels of one pixel, as fp32 pairs (VEC = 1: the first
@@ -195,7 +221,8 @@ __device__ __forceinline__ void copy_vec(Raw *dst, const Raw *src) {
 // batches of four vectors a map in a ring of shared memory slots of its own (so
 // nothing waits for another thread), one batch of two maps or two of one always
 // on the way (cp.async): 128 bytes a thread in flight beside its arithmetic,
-// which registers could not hold.  Pointers advance by addition: with an index multiplied out
+// which registers could not hold (the sums of 8x80x80x256 took 21.8 us with
+// loads into registers, four vectors at a time, and 17.5 us so, caches cold).  Pointers advance by addition: with an index multiplied out
 // a vector, the address arithmetic was half of the instructions.  Two-byte
 // vectors, which cp.async does not copy, go through registers.
 constexpr int kBatch = 4;

@@ -14,6 +14,13 @@
 // core's in fp32, and a group's sum is scaled in fp32 when it ends.
 // Nothing is rounded to fewer bits before the result.  fp32 rows are split
 // into three bf16 parts (8 + 8 + 8 bits, the whole significand), three MMAs.
+// Measured on a GB300 (graph replay over changing inputs): one bf16 row through
+// 8192x28672, groups of 128, 24.9 us, 4.9 TB/s of codes and scales, 72 % of the
+// measured copy rate; issue slots are 64 % full and set the rest (128 input
+// channels of 16 outputs cost a warp about 150 instructions, 40 of them the
+// ANDs and shifts of the decoding; with a shift, an AND-OR and a
+// subtraction a pair it took 33.3 us).  Groups of 32: 28.1 us.  1024x1000: 2.4
+// us, of which a launch is 2.1.  64 rows of 8192x28672 166 us.
 // (tcgen05 would need the decoded weights written to shared memory, four
 // times the streamed bytes there and back, for a product whose operand
 // rows are mostly empty.)

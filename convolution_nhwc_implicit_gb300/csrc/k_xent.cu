@@ -24,6 +24,13 @@
 // probability is small stays exact; dloss / count multiplies the fp32 sums.
 // Nothing depends on the order of atomics: results repeat bit for bit.
 //
+// Measured on a GB300: 8192 x 1024 x 65536 with the gradient 2.5 to 2.8 ms (the
+// longer in calls back to back, by the clock that the power limit leaves), 1580 to 1770
+// TFLOP/s of the 8NDV that it does, 82 to 91 % of the measured burst rate; 1600 x 1024 x 32003, loss alone, 73 to 74 us, 1410
+// to 1440 TFLOP/s (tensor pipe 81 % busy; its 882 tiles fill 11.6 waves of pairs, and
+// the last of seven row tiles is a quarter full); 20 x 512 x 1000 with the
+// gradient 25 us, four launches of a few K blocks each.
+//
 // The tile machine: a cluster of two CTAs (two SMs) computes 256 x 256 outputs
 // with tcgen05.mma.cta_group::2, each CTA staging 128 rows of A and 128 of B
 // per K block of 64 (32 KB a stage, six stages) and holding 128 rows of the
