@@ -20,7 +20,7 @@
 // channels of 16 outputs cost a warp about 150 instructions, 40 of them the
 // ANDs and shifts of the decoding; with a shift, an AND-OR and a
 // subtraction a pair it took 33.3 us).  Groups of 32: 28.1 us.  1024x1000: 2.4
-// us, of which a launch is 2.1.  64 rows of 8192x28672 166 us.
+// us, of which a launch is 2.1.  64 rows of 8192x28672 143 us.
 // (tcgen05 would need the decoded weights written to shared memory, four
 // times the streamed bytes there and back, for a product whose operand
 // rows are mostly empty.)
@@ -367,8 +367,24 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? few_ctas(X::kParts, N
 }
 
 // WC: co tiles of a CTA; its eight warps take k in turns of WK = 8 / WC units.
+__host__ __device__ constexpr int many_smem(int parts, int nt, int wc) {
+    const int x = 3 * parts * nt * 8 * (8 / wc * kUnit * 2 + kPad), ring = 8 * kAhead * 1024, sums = 8 * nt * 128 * 4;
+    return ring + x > sums ? ring + x : sums;
+}
+// CTAs a SM that registers are kept for: one with eight blocks of rows (more
+// than 128 registers), and with four whose shared memory leaves room for one
+// CTA; else two.
+// Left to itself the compiler held some to 80 registers for three CTAs: over 136
+// sizes of 10 to 64 rows this takes 0.89 of the time (64 rows of 8192x8192 bf16
+// 41.7 us against 63.1, 32 of 4096x16384 22.7 against 33.7, 64 of 8192x28672 143
+// against 165; the worst, 10 of 8192x28672 in groups of 64, 60.9 against 58.4).
+// Two everywhere: 24 of 8192x8192 37.3 against 33.3; one wherever two do not fit:
+// 32 of 8192x8192 fp32, groups of 64, 103 against 75.
+__host__ __device__ constexpr int many_ctas(int parts, int nt, int wc) {
+    return nt >= 8 || (nt >= 4 && 2 * (many_smem(parts, nt, wc) + 1024) > 227 * 1024) ? 1 : 2;
+}
 template <typename X, int NT, int GROUP, int WC>
-__global__ void __launch_bounds__(256) w4_many_kernel(W4Args a, int vec) {
+__global__ void __launch_bounds__(256, many_ctas(X::kParts, NT, WC)) w4_many_kernel(W4Args a, int vec) {
     using Elem = typename X::Elem;
     constexpr int WK = 8 / WC, kTurn = WK * kUnit, kPitch = kTurn * 2 + kPad, kGroups = kUnit / GROUP;
     constexpr int kPart = NT * 8 * kPitch, kSide = X::kParts * kPart;
@@ -644,10 +660,7 @@ extern "C" int conv_plan_create_w4(int32_t rows, int32_t c_in, int32_t c_out, in
     g.many = rows > 32 || few(g.warps) > (parts == 3 || g.warps == 16 ? kFewMost : 112 * 1024);
     if (g.many) {
         g.warps = 8;
-        auto smem = [&](int nt, int wc) {
-            const int x = 3 * parts * nt * 8 * (8 / wc * kUnit * 2 + kPad), ring = 8 * kAhead * 1024, sums = 8 * nt * 128 * 4;
-            return ring + x > sums ? ring + x : sums;
-        };
+        auto smem = [&](int nt, int wc) { return many_smem(parts, nt, wc); };
         auto ctas = [&](int nt, int wc) { return (long long)((tiles + wc - 1) / wc) * ((rows + nt * 8 - 1) / (nt * 8)); };
         // until the card is full: fewer output channels a CTA and longer turns,
         // then fewer rows
