@@ -14,6 +14,7 @@ Names follow the C ABI in ``include/conv_nhwc.h``::
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -181,6 +182,19 @@ def _stream_handle(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _allocating_on(stream, device):
+    """A context in which torch's allocator hands out blocks of `stream` (None:
+    the current one).  A block of another stream may still be in use by kernels
+    queued there, whatever it is told afterwards."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream_handle(stream)
+        stream = torch.cuda.ExternalStream(handle, device=device) if handle else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 class Plan:
@@ -405,15 +419,15 @@ class _OpPlan(Plan):
         self._f32, self._dt = _torch_dtype("f32"), _torch_dtype(self.dtype)
 
     def _workspace(self, nbytes, like, stream):
-        """Scratch of one run, from torch's allocator on the run's stream (an
-        explicit `stream` other than the current one is told to the allocator)."""
+        """Scratch of one run, a block of the run's own stream: whoever gets it
+        next from torch's allocator is ordered after the run."""
         if not nbytes:
             return None
         import torch
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
-        if stream is not None:
-            ws.record_stream(torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream)
-        return ws
+        if stream is None:
+            return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        with _allocating_on(stream, like.device):
+            return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
 
 
 class GroupNormPlan(_OpPlan):
@@ -557,11 +571,14 @@ class W4Plan(_OpPlan):
     y_shape = output_shape
 
     def pack(self, codes, stream=None):
-        """The codes laid out for the kernel, in a new uint8 tensor."""
+        """The codes laid out for the kernel, in a new uint8 tensor.  It belongs
+        to `stream`, like any tensor that torch makes there: another stream waits
+        for that one before it reads it."""
         import torch
         _, c_in, c_out = self.shape
         pc = _check("codes", codes, (c_out, (c_in + 1) // 2), self._u8)
-        packed = torch.empty(self.packed_bytes, dtype=torch.uint8, device=codes.device)
+        with _allocating_on(stream, codes.device):
+            packed = torch.empty(self.packed_bytes, dtype=torch.uint8, device=codes.device)
         rc = self._lib.conv_w4_pack(c_in, c_out, pc, packed.data_ptr(), _stream_handle(stream))
         if rc != 0:
             raise ConvError("conv_w4_pack", rc)
@@ -580,13 +597,15 @@ class W4Plan(_OpPlan):
 
 
 def w4_quantize(w, group=128, stream=None):
-    """Codes and scales of float weights [c_out, c_in] (conv_w4_quantize)."""
+    """Codes and scales of float weights [c_out, c_in] (conv_w4_quantize), new
+    tensors that belong to `stream` as W4Plan.pack's does."""
     import torch
     dt = _dtype_name(w)
     c_out, c_in = w.shape
     pw = _check("w", w, (c_out, c_in), w.dtype)
-    codes = torch.empty(c_out, (c_in + 1) // 2, dtype=torch.uint8, device=w.device)
-    scales = torch.empty(c_out, -(-c_in // group), dtype=w.dtype, device=w.device)
+    with _allocating_on(stream, w.device):
+        codes = torch.empty(c_out, (c_in + 1) // 2, dtype=torch.uint8, device=w.device)
+        scales = torch.empty(c_out, -(-c_in // group), dtype=w.dtype, device=w.device)
     rc = load_library().conv_w4_quantize(c_in, c_out, group, DTYPES[dt], pw, codes.data_ptr(), scales.data_ptr(),
                                          _stream_handle(stream))
     if rc != 0:
