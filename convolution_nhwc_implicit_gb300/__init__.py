@@ -166,12 +166,20 @@ def _ptr(t):
     return t.data_ptr()
 
 
+def _current_device():
+    import torch
+    try:
+        return torch._C._cuda_getDevice()
+    except AttributeError:
+        return torch.cuda.current_device()
+
+
 def _current_stream():
     """Handle of torch's current stream (the raw form spares a small call the
     3 us of building a Stream object)."""
     import torch
     try:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return torch._C._cuda_getCurrentRawStream(_current_device())
     except AttributeError:
         return torch.cuda.current_stream().cuda_stream
 
@@ -384,16 +392,16 @@ def _dtype_name(t) -> str:
     return name
 
 
-def _check(name, t, shape, dtype):
-    """Checks a dense CUDA tensor argument and returns its device pointer."""
+def _check(name, t, shape, dtype, device):
+    """Checks a dense tensor argument on CUDA device `device` and returns its device pointer."""
     if t is None:
         raise ValueError(f"{name} is missing")
     if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor on cuda:{device}, got one on {t.device}")
     return t.data_ptr()
 
 
@@ -403,7 +411,9 @@ def _torch_dtype(name):
 
 
 class _OpPlan(Plan):
-    """What the plans of the operators around the layer share."""
+    """What the plans of the operators around the layer share.  A plan belongs
+    to the device that is current when it is made; its runs take tensors of that
+    device, with it current."""
 
     def _create(self, fn, *args):
         self._lib = load_library()
@@ -411,12 +421,20 @@ class _OpPlan(Plan):
         rc = getattr(self._lib, fn)(*args, ctypes.byref(self._handle))
         if rc != 0:
             raise ConvError(fn, rc)
+        self._device = _current_device()
         n = ctypes.c_size_t()
         self._lib.conv_plan_workspace(self._handle, ctypes.byref(n))
         self.workspace_bytes = n.value
         self._lib.conv_plan_workspace_bwd(self._handle, ctypes.byref(n))
         self.workspace_bytes_backward = n.value
         self._f32, self._dt = _torch_dtype("f32"), _torch_dtype(self.dtype)
+
+    def _on_device(self):
+        """The plan's device, which a run needs to be the current one."""
+        now = _current_device()
+        if now != self._device:
+            raise ValueError(f"the plan belongs to cuda:{self._device}, and cuda:{now} is current")
+        return now
 
     def _workspace(self, nbytes, like, stream):
         """Scratch of one run, a block of the run's own stream: whoever gets it
@@ -458,8 +476,8 @@ class GroupNormPlan(_OpPlan):
             raise TypeError(f"{name} is {t.dtype}, expected {self._dt}")
         if t.shape != self.shape:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {self.shape}")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != self._device:
+            raise ValueError(f"{name} must be on cuda:{self._device}, got a tensor on {t.device}")
         if t.is_contiguous():
             return t.data_ptr(), c
         sn, sh, sw, sc = t.stride()
@@ -471,12 +489,12 @@ class GroupNormPlan(_OpPlan):
 
     def run(self, x, gamma, beta, y, mean=None, rstd=None, stream=None) -> None:  # noqa: D401
         """Enqueue y = act(group_norm(x) * gamma + beta) on `stream` (default: torch's current stream)."""
-        f32, cs, ss = self._f32, self._cshape, self._sshape
+        f32, cs, ss, dev = self._f32, self._cshape, self._sshape, self._on_device()
         (px, pitch_x), (py, pitch_y) = self._map("x", x), self._map("y", y)
-        g = None if gamma is None else _check("gamma", gamma, cs, f32)
-        b = None if beta is None else _check("beta", beta, cs, f32)
-        m = None if mean is None else _check("mean", mean, ss, f32)
-        r = None if rstd is None else _check("rstd", rstd, ss, f32)
+        g = None if gamma is None else _check("gamma", gamma, cs, f32, dev)
+        b = None if beta is None else _check("beta", beta, cs, f32, dev)
+        m = None if mean is None else _check("mean", mean, ss, f32, dev)
+        r = None if rstd is None else _check("rstd", rstd, ss, f32, dev)
         ws = self._workspace(self.workspace_bytes, x, stream)
         rc = self._lib.conv_run_groupnorm(self._handle, px, pitch_x, g, b, py, pitch_y, m, r, _ptr(ws),
                                           _stream_handle(stream))
@@ -485,13 +503,13 @@ class GroupNormPlan(_OpPlan):
 
     def run_backward(self, x, gamma, beta, mean, rstd, dy, dx, dgamma=None, dbeta=None, stream=None) -> None:
         """Enqueue the gradient: dx, and dgamma and dbeta where given."""
-        f32, cs, ss = self._f32, self._cshape, self._sshape
+        f32, cs, ss, dev = self._f32, self._cshape, self._sshape, self._on_device()
         (px, pitch_x), (pdy, pitch_dy), (pdx, pitch_dx) = self._map("x", x), self._map("dy", dy), self._map("dx", dx)
-        g = None if gamma is None else _check("gamma", gamma, cs, f32)
-        b = None if beta is None else _check("beta", beta, cs, f32)
-        m, r = _check("mean", mean, ss, f32), _check("rstd", rstd, ss, f32)
-        dg = None if dgamma is None else _check("dgamma", dgamma, cs, f32)
-        db = None if dbeta is None else _check("dbeta", dbeta, cs, f32)
+        g = None if gamma is None else _check("gamma", gamma, cs, f32, dev)
+        b = None if beta is None else _check("beta", beta, cs, f32, dev)
+        m, r = _check("mean", mean, ss, f32, dev), _check("rstd", rstd, ss, f32, dev)
+        dg = None if dgamma is None else _check("dgamma", dgamma, cs, f32, dev)
+        db = None if dbeta is None else _check("dbeta", dbeta, cs, f32, dev)
         ws = self._workspace(self.workspace_bytes_backward, x, stream)
         rc = self._lib.conv_run_groupnorm_bwd(self._handle, px, pitch_x, g, b, m, r, pdy, pitch_dy, pdx, pitch_dx, dg, db,
                                               _ptr(ws), _stream_handle(stream))
@@ -522,11 +540,11 @@ class ClassLossPlan(_OpPlan):
     def run(self, x, w, target, loss, lse=None, row_loss=None, stream=None) -> None:  # noqa: D401
         """Enqueue the loss (a float32 scalar) and, where given, lse and row_loss (float32 [rows])."""
         rows, c_in, classes = self.shape
-        f32, bf16 = self._f32, self._dt
-        px, pw = _check("x", x, (rows, c_in), bf16), _check("w", w, (classes, c_in), bf16)
-        pt, pl = _check("target", target, (rows,), self._i32), _check("loss", loss, (), f32)
-        ps = None if lse is None else _check("lse", lse, (rows,), f32)
-        pr = None if row_loss is None else _check("row_loss", row_loss, (rows,), f32)
+        f32, bf16, dev = self._f32, self._dt, self._on_device()
+        px, pw = _check("x", x, (rows, c_in), bf16, dev), _check("w", w, (classes, c_in), bf16, dev)
+        pt, pl = _check("target", target, (rows,), self._i32, dev), _check("loss", loss, (), f32, dev)
+        ps = None if lse is None else _check("lse", lse, (rows,), f32, dev)
+        pr = None if row_loss is None else _check("row_loss", row_loss, (rows,), f32, dev)
         ws = self._workspace(self.workspace_bytes, x, stream)
         rc = self._lib.conv_run_xent(self._handle, px, pw, pt, pl, pr, ps, _ptr(ws), _stream_handle(stream))
         if rc != 0:
@@ -535,11 +553,11 @@ class ClassLossPlan(_OpPlan):
     def run_backward(self, x, w, target, lse, dx, dw, dloss=None, stream=None) -> None:
         """Enqueue the gradient of the loss times dloss (a float32 scalar tensor; None: 1)."""
         rows, c_in, classes = self.shape
-        f32, bf16 = self._f32, self._dt
-        px, pw = _check("x", x, (rows, c_in), bf16), _check("w", w, (classes, c_in), bf16)
-        pt, ps = _check("target", target, (rows,), self._i32), _check("lse", lse, (rows,), f32)
-        pdx, pdw = _check("dx", dx, (rows, c_in), bf16), _check("dw", dw, (classes, c_in), bf16)
-        pd = None if dloss is None else _check("dloss", dloss, (), f32)
+        f32, bf16, dev = self._f32, self._dt, self._on_device()
+        px, pw = _check("x", x, (rows, c_in), bf16, dev), _check("w", w, (classes, c_in), bf16, dev)
+        pt, ps = _check("target", target, (rows,), self._i32, dev), _check("lse", lse, (rows,), f32, dev)
+        pdx, pdw = _check("dx", dx, (rows, c_in), bf16, dev), _check("dw", dw, (classes, c_in), bf16, dev)
+        pd = None if dloss is None else _check("dloss", dloss, (), f32, dev)
         ws = self._workspace(self.workspace_bytes_backward, x, stream)
         rc = self._lib.conv_run_xent_bwd(self._handle, px, pw, pt, ps, pd, pdx, pdw, _ptr(ws), _stream_handle(stream))
         if rc != 0:
@@ -576,7 +594,7 @@ class W4Plan(_OpPlan):
         for that one before it reads it."""
         import torch
         _, c_in, c_out = self.shape
-        pc = _check("codes", codes, (c_out, (c_in + 1) // 2), self._u8)
+        pc = _check("codes", codes, (c_out, (c_in + 1) // 2), self._u8, self._on_device())
         with _allocating_on(stream, codes.device):
             packed = torch.empty(self.packed_bytes, dtype=torch.uint8, device=codes.device)
         rc = self._lib.conv_w4_pack(c_in, c_out, pc, packed.data_ptr(), _stream_handle(stream))
@@ -587,10 +605,10 @@ class W4Plan(_OpPlan):
     def run(self, x, packed, scales, bias, y, stream=None) -> None:  # noqa: D401
         """Enqueue the layer on `stream` (default: torch's current stream)."""
         sx, sw, ss, sb, sy = self._shapes
-        dt = self._dt
-        px, pw, ps = _check("x", x, sx, dt), _check("packed", packed, sw, self._u8), _check("scales", scales, ss, dt)
-        pb = None if bias is None else _check("bias", bias, sb, self._f32)
-        py = _check("y", y, sy, dt)
+        dt, dev = self._dt, self._on_device()
+        px, pw, ps = _check("x", x, sx, dt, dev), _check("packed", packed, sw, self._u8, dev), _check("scales", scales, ss, dt, dev)
+        pb = None if bias is None else _check("bias", bias, sb, self._f32, dev)
+        py = _check("y", y, sy, dt, dev)
         rc = self._lib.conv_run_w4(self._handle, px, pw, ps, pb, py, _stream_handle(stream))
         if rc != 0:
             raise ConvError("conv_run_w4", rc)
@@ -602,7 +620,7 @@ def w4_quantize(w, group=128, stream=None):
     import torch
     dt = _dtype_name(w)
     c_out, c_in = w.shape
-    pw = _check("w", w, (c_out, c_in), w.dtype)
+    pw = _check("w", w, (c_out, c_in), w.dtype, _current_device())
     with _allocating_on(stream, w.device):
         codes = torch.empty(c_out, (c_in + 1) // 2, dtype=torch.uint8, device=w.device)
         scales = torch.empty(c_out, -(-c_in // group), dtype=w.dtype, device=w.device)

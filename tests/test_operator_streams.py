@@ -74,6 +74,7 @@ def world(monkeypatch):
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle))
     monkeypatch.setattr(torch.cuda, "default_stream", lambda device=None: Stream(0))
     monkeypatch.setattr(cl, "_current_stream", lambda *a: now[-1])
+    monkeypatch.setattr(cl, "_current_device", lambda: 0, raising=False)
     lib = Lib()
     monkeypatch.setattr(cl, "load_library", lambda: lib)
     return made, lib
