@@ -89,6 +89,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 __device__ __forceinline__ float elem_f(float v) { return v; }
 __device__ __forceinline__ float elem_f(__nv_bfloat16 v) { return __bfloat162float(v); }
 template <typename T> __device__ __forceinline__ T elem_from(float v) { return convk::Elem<T>::from_f(v); }
+// The activation; ReLU passes a NaN on, which activate's maximum would answer with 0.
+__device__ __forceinline__ float act_out(float v, int act) {
+    if (act == ACT_RELU) return v < 0.0f ? 0.0f : v;
+    return activate(v, act);
+}
 
 // A word's eight codes as four bf16 pairs (u - 8) / 64, pair i codes i and i + 4.
 __device__ __forceinline__ void decode(uint32_t w, uint32_t (&p)[4]) {
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? few_ctas(X::kParts, N
             float v = 0.0f;
 #pragma unroll
             for (int q = 0; q < WARPS; ++q) v += red[side * kSum + q * (NT * 128) + o];
-            v = activate(fmaf(v, kCodeScale, a.bias ? a.bias[co] : 0.0f), a.act);
+            v = act_out(fmaf(v, kCodeScale, a.bias ? a.bias[co] : 0.0f), a.act);
             static_cast<Elem *>(a.y)[(long long)m * a.co + co] = elem_from<Elem>(v);
         }
     }
@@ -525,7 +530,7 @@ __global__ void __launch_bounds__(256, many_ctas(X::kParts, NT, WC)) w4_many_ker
             const int m = n * 8 + 2 * t + (e & 1), c = tile * 16 + g + (e >> 1) * 8;
             if (m < rows && c < a.co)
                 static_cast<Elem *>(a.y)[(long long)(m0 + m) * a.co + c] =
-                    elem_from<Elem>(activate(fmaf(acc[n][e], kCodeScale, a.bias ? a.bias[c] : 0.0f), a.act));
+                    elem_from<Elem>(act_out(fmaf(acc[n][e], kCodeScale, a.bias ? a.bias[c] : 0.0f), a.act));
         }
 }
 
