@@ -561,8 +561,17 @@ __global__ void w4_pack_kernel(const uint8_t *codes, uint32_t *out, int ci, int 
     out[i] = v;
 }
 
+// max(a, b), NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Codes and scales of a weight row's group, one warp a group: s = max |w| / 7
 // rounded to the scales' type, u = clamp(round_half_even(w / s), -8, 7) + 8.
+// A NaN or an infinity among the weights is the scale's too, and every code of
+// its group is 8: the layer answers 0 times that, NaN.
 template <typename T>
 __global__ void w4_quantize_kernel(const T *w, uint8_t *codes, T *scales, int ci, int ng, int group, long long total) {
     pdl_trigger();
@@ -573,9 +582,9 @@ __global__ void w4_quantize_kernel(const T *w, uint8_t *codes, T *scales, int ci
     const long long row = i / ng;
     const int k0 = (int)(i % ng) * group, k1 = min(ci, k0 + group);
     float top = 0.0f;
-    for (int k = k0 + lane; k < k1; k += 32) top = fmaxf(top, fabsf(elem_f(w[row * ci + k])));
+    for (int k = k0 + lane; k < k1; k += 32) top = max_nan(top, fabsf(elem_f(w[row * ci + k])));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
     const T s = elem_from<T>(top / 7.0f);
     const float sf = elem_f(s);
     if (lane == 0) scales[i] = s;
@@ -584,7 +593,7 @@ __global__ void w4_quantize_kernel(const T *w, uint8_t *codes, T *scales, int ci
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             int q = 0;
-            if (k + e < k1 && sf > 0.0f) q = max(-8, min(7, __float2int_rn(elem_f(w[row * ci + k + e]) / sf)));
+            if (k + e < k1 && sf > 0.0f && isfinite(sf)) q = max(-8, min(7, __float2int_rn(elem_f(w[row * ci + k + e]) / sf)));
             byte |= (uint32_t)(q + 8) << (4 * e);
         }
         codes[row * ((ci + 1) / 2) + (k >> 1)] = (uint8_t)byte;

@@ -360,7 +360,8 @@ CONV_API int conv_run_xent_bwd(const conv_plan_t *plan, const void *x, const voi
  *           every run
  * conv_w4_quantize makes codes and scales of float weights [c_out][c_in]:
  * scale = max |w| of the group / 7 (rounded to dtype), code =
- * clamp(round_half_even(w / scale), -8, 7) + 8. */
+ * clamp(round_half_even(w / scale), -8, 7) + 8.  A group that holds a NaN or an
+ * infinity gets that for its scale and answers NaN. */
 CONV_API int conv_plan_create_w4(int32_t rows, int32_t c_in, int32_t c_out, int32_t group, conv_dtype_t dtype,
                                  conv_act_t act, conv_plan_t **out_plan);
 CONV_API int conv_w4_packed_bytes(int32_t c_in, int32_t c_out, size_t *bytes);
