@@ -69,12 +69,6 @@ int validate(const conv_shape_t *s, int stride, int pad_h, int pad_w, int groups
     return CONV_OK;
 }
 
-bool overlaps(const void *a, size_t na, const void *b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + nb && b0 < a0 + na;
-}
-
 bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 }  // namespace
@@ -94,7 +88,7 @@ int conv_check_run_pointers(conv_dtype_t dtype, const conv_shape_t *s, int group
     const size_t wb = (size_t)s->c_out * s->k_h * s->k_w * (s->c_in / groups) * es;
     const size_t bb = bias ? (size_t)s->c_out * 4 : 0;
     const size_t yb = (size_t)s->n * oh * ow * s->c_out * es;
-    if (overlaps(y, yb, x, xb) || overlaps(y, yb, w, wb) || overlaps(y, yb, bias, bb)) return CONV_ERR_ALIASING;
+    if (conv_overlaps(y, yb, x, xb) || conv_overlaps(y, yb, w, wb) || conv_overlaps(y, yb, bias, bb)) return CONV_ERR_ALIASING;
     return CONV_OK;
 }
 
@@ -397,8 +391,8 @@ int conv_run_dwpw(const conv_plan_t *plan, const void *x, const void *w_dw, cons
     const size_t C = (size_t)p->s.c_in, Co = (size_t)p->s.c_out;
     const size_t xb = (size_t)p->s.n * p->s.h * p->s.w * C * es;
     const size_t yb = (size_t)p->s.n * p->oh * p->ow * Co * es;
-    if (overlaps(y, yb, x, xb) || overlaps(y, yb, w_dw, C * 9 * es) || overlaps(y, yb, w_pw, Co * C * es) ||
-        overlaps(y, yb, b_dw, b_dw ? C * 4 : 0) || overlaps(y, yb, b_pw, b_pw ? Co * 4 : 0))
+    if (conv_overlaps(y, yb, x, xb) || conv_overlaps(y, yb, w_dw, C * 9 * es) || conv_overlaps(y, yb, w_pw, Co * C * es) ||
+        conv_overlaps(y, yb, b_dw, b_dw ? C * 4 : 0) || conv_overlaps(y, yb, b_pw, b_pw ? Co * 4 : 0))
         return CONV_ERR_ALIASING;
     return launch_dwpw(p, x, w_dw, b_dw, w_pw, b_pw, y, (cudaStream_t)stream) == cudaSuccess ? CONV_OK
                                                                                              : CONV_ERR_CUDA;
@@ -482,8 +476,8 @@ int conv_run_fused(const conv_plan_t *plan, const void *x, const void *w, const 
     const size_t bb = bias ? (size_t)p->s.c_out * 4 : 0;
     const size_t rb = residual ? (size_t)p->s.n * p->oh * p->ow * p->s.c_out * es : 0;
     const size_t yb = (size_t)p->s.n * p->oh * p->up * p->ow * p->up * p->y_c * es;
-    if (overlaps(y, yb, x, xb) || overlaps(y, yb, w, wb) || overlaps(y, yb, bias, bb) ||
-        overlaps(y, yb, residual, rb))
+    if (conv_overlaps(y, yb, x, xb) || conv_overlaps(y, yb, w, wb) || conv_overlaps(y, yb, bias, bb) ||
+        conv_overlaps(y, yb, residual, rb))
         return CONV_ERR_ALIASING;
 
     cudaStream_t st = (cudaStream_t)stream;

@@ -132,6 +132,13 @@ struct conv_plan {
 // word if its kernels have waits to report on.  Returns a CONV_* status.
 int conv_plan_bind_device(conv_plan *p, bool status_word);
 
+// Whether [a, a + na) and [b, b + nb) share a byte (a null pointer: no).
+static inline bool conv_overlaps(const void *a, size_t na, const void *b, size_t nb) {
+    if (!a || !b || na == 0 || nb == 0) return false;
+    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+    return a0 < b0 + nb && b0 < a0 + na;
+}
+
 // Element size of a conv_dtype_t.
 static inline int conv_esize(conv_dtype_t t) { return t == CONV_F32 ? 4 : (t == CONV_BF16 ? 2 : 1); }
 

@@ -1090,6 +1090,27 @@ bool range_overlaps(const void *small, size_t bytes, const void *map, long long 
     return a0 < b0 + (uintptr_t)((rows - 1) * pitch + C) * es && b0 < a0 + bytes;
 }
 
+// The buffers of a run besides its maps, and its maps: whether one that it
+// writes shares a byte with any other (CTAs read the inputs while others write).
+struct Small { const void *p; size_t bytes; };
+struct Map { const void *p; long long pitch; };
+template <int I, int O, int M>
+bool results_overlap(const Small (&in)[I], const Small (&out)[O], const Map (&maps_in)[M], const Map &result, long long rows, int C,
+                     int es) {
+    for (const Small &i : in)
+        if (range_overlaps(i.p, i.bytes, result.p, result.pitch, rows, C, es)) return true;
+    for (int k = 0; k < O; ++k) {
+        if (range_overlaps(out[k].p, out[k].bytes, result.p, result.pitch, rows, C, es)) return true;
+        for (const Map &m : maps_in)
+            if (range_overlaps(out[k].p, out[k].bytes, m.p, m.pitch, rows, C, es)) return true;
+        for (const Small &i : in)
+            if (conv_overlaps(out[k].p, out[k].bytes, i.p, i.bytes)) return true;
+        for (int j = 0; j < k; ++j)
+            if (conv_overlaps(out[k].p, out[k].bytes, out[j].p, out[j].bytes)) return true;
+    }
+    return false;
+}
+
 int check_map(const conv_plan *p, const void *t, int64_t *pitch) {
     if (!t) return CONV_ERR_NULL_ARG;
     if (*pitch == 0) *pitch = p->s.c_in;
@@ -1238,12 +1259,10 @@ extern "C" int conv_run_groupnorm(const conv_plan_t *plan, const void *x, int64_
     const int es = conv_esize(p->dtype), C = p->s.c_in;
     const long long rows = (long long)p->s.n * p->s.h * p->s.w;
     const size_t sb = (size_t)p->s.n * p->groups * 4;
-    if (maps_overlap(x, x_pitch, y, y_pitch, rows, C, es) || range_overlaps(gamma, (size_t)C * 4, y, y_pitch, rows, C, es) ||
-        range_overlaps(beta, (size_t)C * 4, y, y_pitch, rows, C, es) || range_overlaps(mean, sb, y, y_pitch, rows, C, es) ||
-        range_overlaps(rstd, sb, y, y_pitch, rows, C, es) || range_overlaps(mean, sb, x, x_pitch, rows, C, es) ||
-        range_overlaps(rstd, sb, x, x_pitch, rows, C, es) ||
-        range_overlaps(workspace, p->ws_bytes, x, x_pitch, rows, C, es) ||
-        range_overlaps(workspace, p->ws_bytes, y, y_pitch, rows, C, es))
+    const size_t cb = (size_t)C * 4;
+    const Small in[2] = {{gamma, cb}, {beta, cb}}, out[3] = {{mean, sb}, {rstd, sb}, {workspace, p->ws_bytes}};
+    const Map maps_in[1] = {{x, x_pitch}};
+    if (maps_overlap(x, x_pitch, y, y_pitch, rows, C, es) || results_overlap(in, out, maps_in, {y, y_pitch}, rows, C, es))
         return CONV_ERR_ALIASING;
     const GnGeom::Dir &d = p->gn.fwd;
     GnArgs a = base_args(p, d, x, x_pitch, y, y_pitch, workspace);
@@ -1290,17 +1309,13 @@ extern "C" int conv_run_groupnorm_bwd(const conv_plan_t *plan, const void *x, in
         return CONV_ERR_MISALIGNED;
     const long long rows = (long long)p->s.n * p->s.h * p->s.w;
     const size_t sb = (size_t)p->s.n * p->groups * 4, cb = (size_t)C * 4;
-    const void *in_small[4] = {gamma, beta, mean, rstd};
-    const size_t in_bytes[4] = {cb, cb, sb, sb};
-    bool bad = maps_overlap(x, x_pitch, dx, dx_pitch, rows, C, es) || maps_overlap(dy, dy_pitch, dx, dx_pitch, rows, C, es);
-    for (int i = 0; i < 4; ++i) bad = bad || range_overlaps(in_small[i], in_bytes[i], dx, dx_pitch, rows, C, es);
+    const Small in[4] = {{gamma, cb}, {beta, cb}, {mean, sb}, {rstd, sb}};
+    const Small out[3] = {{dgamma, cb}, {dbeta, cb}, {workspace, p->ws_bwd_bytes}};
+    const Map maps_in[2] = {{x, x_pitch}, {dy, dy_pitch}};
+    if (maps_overlap(x, x_pitch, dx, dx_pitch, rows, C, es) || maps_overlap(dy, dy_pitch, dx, dx_pitch, rows, C, es) ||
+        results_overlap(in, out, maps_in, {dx, dx_pitch}, rows, C, es))
+        return CONV_ERR_ALIASING;
     const void *maps[3] = {x, dy, dx};
-    const int64_t mp[3] = {x_pitch, dy_pitch, dx_pitch};
-    for (int i = 0; i < 3; ++i)
-        bad = bad || range_overlaps(dgamma, cb, maps[i], mp[i], rows, C, es) ||
-              range_overlaps(dbeta, cb, maps[i], mp[i], rows, C, es) ||
-              range_overlaps(workspace, p->ws_bwd_bytes, maps[i], mp[i], rows, C, es);
-    if (bad) return CONV_ERR_ALIASING;
     const GnGeom::Dir &d = p->gn.bwd;
     GnArgs a = base_args(p, d, x, x_pitch, dx, dx_pitch, workspace);
     a.dy = dy; a.pdy = dy_pitch;

@@ -242,11 +242,6 @@ __global__ void __launch_bounds__(kThreads, 2) spp_image_kernel(const uint4 *__r
     }
 }
 
-bool overlaps(const void *p, size_t np, const void *q, size_t nq) {
-    const uintptr_t a0 = (uintptr_t)p, b0 = (uintptr_t)q;
-    return np && nq && a0 < b0 + nq && b0 < a0 + np;
-}
-
 }  // namespace
 
 extern "C" int conv_spp_run(int32_t n, int32_t h, int32_t w, int32_t c, conv_dtype_t dtype, const void *x, void *y,
@@ -270,7 +265,7 @@ extern "C" int conv_spp_run(int32_t n, int32_t h, int32_t w, int32_t c, conv_dty
     if (n == 0) return CONV_OK;
     if (!x || !y) return CONV_ERR_NULL_ARG;
     if (((uintptr_t)x & 15) || ((uintptr_t)y & 15)) return CONV_ERR_MISALIGNED;
-    if (overlaps(x, (size_t)n * h * w * c * es, y, (size_t)n * h * w * y_channels * es)) return CONV_ERR_ALIASING;
+    if (conv_overlaps(x, (size_t)n * h * w * c * es, y, (size_t)n * h * w * y_channels * es)) return CONV_ERR_ALIASING;
 
     SppArgs a;
     a.N = n; a.H = h; a.W = w; a.CV = c * es / 16;

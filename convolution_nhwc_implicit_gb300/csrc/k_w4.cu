@@ -629,12 +629,6 @@ const void *pick(const W4Geom &g) {
     return g.warps == 8 ? few_nt<X, 8>(g.nt, g.group) : few_nt<X, 16>(g.nt, g.group);
 }
 
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    if (!a || !b || !na || !nb) return false;
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + nb && b0 < a0 + na;
-}
-
 }  // namespace
 
 extern "C" int conv_plan_create_w4(int32_t rows, int32_t c_in, int32_t c_out, int32_t group, conv_dtype_t dtype,
@@ -712,7 +706,7 @@ extern "C" int conv_w4_pack(int32_t c_in, int32_t c_out, const void *codes, void
     if (rc != CONV_OK) return rc;
     if (!codes || !packed) return CONV_ERR_NULL_ARG;
     if ((uintptr_t)packed & 15u) return CONV_ERR_MISALIGNED;
-    if (overlap(packed, bytes, codes, (size_t)c_out * ((c_in + 1) / 2))) return CONV_ERR_ALIASING;
+    if (conv_overlaps(packed, bytes, codes, (size_t)c_out * ((c_in + 1) / 2))) return CONV_ERR_ALIASING;
     long long words = (long long)(bytes / 4);
     if ((words + 255) / 256 > 0x7fffffffll) return CONV_ERR_UNSUPPORTED;
     int units = (c_in + kUnit - 1) / kUnit;
@@ -737,7 +731,7 @@ extern "C" int conv_w4_quantize(int32_t c_in, int32_t c_out, int32_t group, conv
     long long total = (long long)c_out * ng;
     if ((total + 7) / 8 > 0x7fffffffll) return CONV_ERR_UNSUPPORTED;
     const size_t wb = (size_t)c_in * c_out * es, cb = (size_t)c_out * ((c_in + 1) / 2), sb = (size_t)total * es;
-    if (overlap(codes, cb, w, wb) || overlap(scales, sb, w, wb) || overlap(codes, cb, scales, sb)) return CONV_ERR_ALIASING;
+    if (conv_overlaps(codes, cb, w, wb) || conv_overlaps(scales, sb, w, wb) || conv_overlaps(codes, cb, scales, sb)) return CONV_ERR_ALIASING;
     const void *k = dtype == CONV_F32 ? (const void *)&w4_quantize_kernel<float> : (const void *)&w4_quantize_kernel<__nv_bfloat16>;
     void *args[] = {(void *)&w, (void *)&codes, (void *)&scales, &c_in, &ng, &group, &total};
     const cudaError_t e = conv_launch(k, dim3((unsigned)((total + 7) / 8)), dim3(256), args, 0, (cudaStream_t)stream);
@@ -758,8 +752,8 @@ extern "C" int conv_run_w4(const conv_plan_t *plan, const void *x, const void *p
     size_t pb = 0;
     conv_w4_packed_bytes(ci, co, &pb);
     const size_t yb = (size_t)rows * co * es;
-    if (overlap(y, yb, x, (size_t)rows * ci * es) || overlap(y, yb, packed, pb) ||
-        overlap(y, yb, scales, (size_t)co * p->w4.ng * es) || overlap(y, yb, bias, (size_t)co * 4))
+    if (conv_overlaps(y, yb, x, (size_t)rows * ci * es) || conv_overlaps(y, yb, packed, pb) ||
+        conv_overlaps(y, yb, scales, (size_t)co * p->w4.ng * es) || conv_overlaps(y, yb, bias, (size_t)co * 4))
         return CONV_ERR_ALIASING;
     const W4Geom &g = p->w4;
     W4Args a = {x, static_cast<const uint4 *>(packed), scales, bias, y, rows, ci, co, g.ng, g.units, p->act, (co + 15) / 16};

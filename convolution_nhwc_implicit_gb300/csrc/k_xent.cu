@@ -675,12 +675,6 @@ cudaError_t launch_tiles(const conv_plan *p, int kind, Maps &maps, XArgs &a, cud
     return conv_launch(kernel_of(kind), dim3((unsigned)grid), dim3(kThreads), args, kSmem, st, 2);
 }
 
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    if (!a || !b || !na || !nb) return false;
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + nb && b0 < a0 + na;
-}
-
 // Operands as TMA can address them: as given, or padded copies.
 int operands(const conv_plan *p, const Space &sp, char *ws, const void *&x, const void *&w, cudaStream_t st) {
     if (p->xent.dp == p->s.c_in) return CONV_OK;
@@ -783,9 +777,9 @@ extern "C" int conv_run_xent(const conv_plan_t *plan, const void *x, const void 
     const size_t outb[4] = {4, N * 4, N * 4, p->ws_bytes};
     for (int i = 0; i < 4; ++i) {
         for (int j = 0; j < 3; ++j)
-            if (overlap(out[i], outb[i], in[j], inb[j])) return CONV_ERR_ALIASING;
+            if (conv_overlaps(out[i], outb[i], in[j], inb[j])) return CONV_ERR_ALIASING;
         for (int j = 0; j < i; ++j)
-            if (overlap(out[i], outb[i], out[j], outb[j])) return CONV_ERR_ALIASING;
+            if (conv_overlaps(out[i], outb[i], out[j], outb[j])) return CONV_ERR_ALIASING;
     }
     const XentGeom &g = p->xent;
     const Space sp = space_of(p);
@@ -836,9 +830,9 @@ extern "C" int conv_run_xent_bwd(const conv_plan_t *plan, const void *x, const v
     const size_t outb[3] = {N * D * 2, V * D * 2, p->ws_bwd_bytes};
     for (int i = 0; i < 3; ++i) {
         for (int j = 0; j < 5; ++j)
-            if (overlap(out[i], outb[i], in[j], inb[j])) return CONV_ERR_ALIASING;
+            if (conv_overlaps(out[i], outb[i], in[j], inb[j])) return CONV_ERR_ALIASING;
         for (int j = 0; j < i; ++j)
-            if (overlap(out[i], outb[i], out[j], outb[j])) return CONV_ERR_ALIASING;
+            if (conv_overlaps(out[i], outb[i], out[j], outb[j])) return CONV_ERR_ALIASING;
     }
     const XentGeom &g = p->xent;
     const Space sp = space_of(p);

@@ -297,9 +297,11 @@ CONV_API int conv_run_dwpw(const conv_plan_t *plan, const void *x, const void *w
  *                            may be NULL (not written)
  *   conv_run_groupnorm_bwd   mean and rstd as the forward run wrote them;
  *                            dgamma, dbeta may be NULL (not written)
- * y must not share an element with x, nor dx with x or dy (CONV_ERR_ALIASING;
- * interleaved channel slices of one buffer share none).  n = 0 does nothing
- * (the gradient writes zeros to dgamma and dbeta). */
+ * y must not share an element with x, nor dx with x or dy (interleaved channel
+ * slices of one buffer share none); mean, rstd, dgamma, dbeta, workspace and the
+ * written map share no byte with one another or with an input
+ * (CONV_ERR_ALIASING).  n = 0 does nothing (the gradient writes zeros to dgamma
+ * and dbeta). */
 CONV_API int conv_plan_create_groupnorm(int32_t n, int32_t h, int32_t w, int32_t c, int32_t groups, float eps,
                                         conv_dtype_t dtype, conv_act_t act, conv_plan_t **out_plan);
 CONV_API int conv_run_groupnorm(const conv_plan_t *plan, const void *x, int64_t x_pitch, const float *gamma,
