@@ -629,6 +629,11 @@ const void *pick(const W4Geom &g) {
     return g.warps == 8 ? few_nt<X, 8>(g.nt, g.group) : few_nt<X, 16>(g.nt, g.group);
 }
 
+// 32-bit channel counts and unit indices, with room to round up.
+bool too_large(int32_t c_in, int32_t c_out) {
+    return c_in >= (1 << 28) || c_out >= (1 << 30) || (long long)c_in * c_out >= (1ll << 40);
+}
+
 }  // namespace
 
 extern "C" int conv_plan_create_w4(int32_t rows, int32_t c_in, int32_t c_out, int32_t group, conv_dtype_t dtype,
@@ -640,8 +645,7 @@ extern "C" int conv_plan_create_w4(int32_t rows, int32_t c_in, int32_t c_out, in
     if ((int)act < CONV_ACT_NONE || (int)act > CONV_ACT_MISH) return CONV_ERR_INVALID_ARG;
     if (group != 32 && group != 64 && group != 128) return CONV_ERR_INVALID_ARG;
     if (dtype == CONV_I8) return CONV_ERR_UNSUPPORTED;
-    if (c_in >= (1 << 28) || c_out >= (1 << 30) || rows >= (1 << 21) || (long long)c_in * c_out >= (1ll << 40))
-        return CONV_ERR_UNSUPPORTED;
+    if (too_large(c_in, c_out) || rows >= (1 << 21)) return CONV_ERR_UNSUPPORTED;
     conv_plan *p = new (std::nothrow) conv_plan();
     if (!p) return CONV_ERR_OOM;
     p->s = {rows, 1, 1, c_in, c_out, 1, 1};
@@ -696,6 +700,7 @@ extern "C" int conv_plan_create_w4(int32_t rows, int32_t c_in, int32_t c_out, in
 extern "C" int conv_w4_packed_bytes(int32_t c_in, int32_t c_out, size_t *bytes) {
     if (!bytes) return CONV_ERR_NULL_ARG;
     if (c_in < 1 || c_out < 1) return CONV_ERR_INVALID_SHAPE;
+    if (too_large(c_in, c_out)) return CONV_ERR_UNSUPPORTED;
     *bytes = (size_t)((c_out + 15) / 16) * ((c_in + kUnit - 1) / kUnit) * 1024;
     return CONV_OK;
 }
@@ -723,7 +728,7 @@ extern "C" int conv_w4_quantize(int32_t c_in, int32_t c_out, int32_t group, conv
     if (c_in < 1 || c_out < 1) return CONV_ERR_INVALID_SHAPE;
     if ((int)dtype < CONV_F32 || (int)dtype > CONV_I8) return CONV_ERR_INVALID_ARG;
     if (group != 32 && group != 64 && group != 128) return CONV_ERR_INVALID_ARG;
-    if (dtype == CONV_I8) return CONV_ERR_UNSUPPORTED;
+    if (dtype == CONV_I8 || too_large(c_in, c_out)) return CONV_ERR_UNSUPPORTED;
     if (!w || !codes || !scales) return CONV_ERR_NULL_ARG;
     const size_t es = (size_t)conv_esize(dtype);
     if ((uintptr_t)w % es || (uintptr_t)scales % es) return CONV_ERR_MISALIGNED;

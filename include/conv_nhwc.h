@@ -352,8 +352,10 @@ CONV_API int conv_run_xent_bwd(const conv_plan_t *plan, const void *x, const voi
  *   y[m,co] = act( bias[co] + sum_k scales[co][k / group] (code[co][k] - 8) x[m,k] )
  * x [rows][c_in], y [rows][c_out] and scales [c_out][ceil(c_in / group)] are
  * of dtype (CONV_F32 or CONV_BF16; CONV_I8: CONV_ERR_UNSUPPORTED), bias
- * [c_out] float32 or NULL, group 32, 64 or 128 (CONV_ERR_INVALID_ARG), any
- * c_in, c_out and rows >= 1.  Products and sums are fp32, one rounding to y.
+ * [c_out] float32 or NULL, group 32, 64 or 128 (CONV_ERR_INVALID_ARG),
+ * rows >= 0, c_in and c_out >= 1; c_in < 2^28, c_out < 2^30, c_in * c_out <
+ * 2^40 and rows < 2^21 (CONV_ERR_UNSUPPORTED; packing and quantising take the
+ * same sizes).  Products and sums are fp32, one rounding to y.
  *   codes   [c_out][ceil(c_in / 2)] bytes, two codes 0..15 a byte, the even
  *           input channel in the low half (an odd c_in's last high half is
  *           ignored); the weight is (code - 8) * scale
