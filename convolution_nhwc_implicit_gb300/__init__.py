@@ -619,7 +619,7 @@ def w4_quantize(w, group=128, stream=None):
     tensors that belong to `stream` as W4Plan.pack's does."""
     import torch
     dt = _dtype_name(w)
-    if w.dim() != 2 or group < 1:
+    if len(w.shape) != 2 or group < 1:
         raise ValueError(f"w must be [c_out, c_in] and group positive, got {tuple(w.shape)} and {group}")
     c_out, c_in = w.shape
     pw = _check("w", w, (c_out, c_in), w.dtype, _current_device())
