@@ -142,6 +142,14 @@ __device__ __forceinline__ float ex2(float v) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
 }
+// e^(l - v) is 2^(l log2 e - v log2 e).  With ref, v log2 e rounded (__fmul_rn,
+// which no multiply-add absorbs), in the multiply-add of every l, what is left
+// over is this factor of all of them: without it they are off by ref's rounding,
+// which grows with |v| (1e-5 of the result at 200).  (v infinite or NaN: 1, ref
+// says it.)
+__device__ __forceinline__ float exp2_rest(float v, float ref) {
+    return fabsf(v) < INFINITY ? ex2(-fmaf(v, kLog2e, -ref)) : 1.0f;
+}
 __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
     __nv_bfloat162 p = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<uint32_t *>(&p);
@@ -359,7 +367,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                 if (lane == 0) tc::mbar_arrive_cluster(tempty0 + 8u * buf);
             };
             if constexpr (KIND == FWD) {
-                float m = -INFINITY, s = 0.0f;
+                // s: sum of 2^(l log2 e - ref), ref the rounded m log2 e
+                float m = -INFINITY, s = 0.0f, ref = -INFINITY;
 #pragma unroll 1
                 for (int c = 0; c < 128; c += 32) {
                     uint32_t r[32];
@@ -377,17 +386,18 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
 #pragma unroll
                     for (int j = 1; j < 32; ++j) top = fmaxf(top, __uint_as_float(r[j]));
                     const float nm = fmaxf(m, top);
-                    const float ref = nm == -INFINITY ? 0.0f : nm * kLog2e;
-                    float s0 = s * ex2(m * kLog2e - ref), s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
+                    const float use = nm == -INFINITY ? 0.0f : __fmul_rn(nm, kLog2e);
+                    float s0 = s * ex2(ref - use), s1 = 0.0f, s2 = 0.0f, s3 = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        s0 += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
-                        s1 += ex2(fmaf(__uint_as_float(r[j + 1]), kLog2e, -ref));
-                        s2 += ex2(fmaf(__uint_as_float(r[j + 2]), kLog2e, -ref));
-                        s3 += ex2(fmaf(__uint_as_float(r[j + 3]), kLog2e, -ref));
+                        s0 += ex2(fmaf(__uint_as_float(r[j]), kLog2e, -use));
+                        s1 += ex2(fmaf(__uint_as_float(r[j + 1]), kLog2e, -use));
+                        s2 += ex2(fmaf(__uint_as_float(r[j + 2]), kLog2e, -use));
+                        s3 += ex2(fmaf(__uint_as_float(r[j + 3]), kLog2e, -use));
                     }
                     s = (s0 + s1) + (s2 + s3);
                     m = nm;
+                    ref = __fmul_rn(nm, kLog2e);
                     const int at = tg - (col0 + c);
                     if (on && at >= 0 && at < 32) {
                         float v = 0.0f;
@@ -396,9 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                         a.tlogit[row] = v;
                     }
                 }
+                s *= exp2_rest(m, ref);
                 if (row < a.rows) a.part[(long long)(t.ni * 2 + grp) * a.rows + row] = make_float2(m, s);
             } else {
-                const float ref = ls * kLog2e;
+                const float ref = __fmul_rn(ls, kLog2e), rest = exp2_rest(ls, ref);
                 const bool fin = KIND == PROD && (t.dw ? a.dw_final : a.dx_final) != 0;
                 float *slot = nullptr;
                 bool add = false;
@@ -423,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
 #pragma unroll
                         for (int j = 0; j < 64; ++j) {
                             const float p = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
-                            r[j] = __float_as_uint(on ? (j == at ? p - 1.0f : p) : 0.0f);
+                            r[j] = __float_as_uint(on ? fmaf(p, rest, j == at ? -1.0f : 0.0f) : 0.0f);
                         }
                     } else {
                         if (add) {
