@@ -140,12 +140,12 @@ __device__ __forceinline__ float2 rcp2(float2 d) {
     const float r = rcp_approx(d.x * d.y);
     return mul2(make_float2(r, r), make_float2(d.y, d.x));
 }
-// e^z of a pair, z clamped at 20, where Mish and its derivative have reached
+// log2 e times a pair clamped at 20, where Mish and its derivative have reached
 // their limits z and 1 in fp32 (fminf drops a NaN: see rcp2).
-__device__ __forceinline__ float2 exp2_clamped(float2 z) {
-    const float2 e = mul2(make_float2(fminf(z.x, 20.0f), fminf(z.y, 20.0f)), make_float2(1.4426950408889634f, 1.4426950408889634f));
-    return make_float2(ex2_approx(e.x), ex2_approx(e.y));
+__device__ __forceinline__ float2 exponent(float2 z) {
+    return mul2(make_float2(fminf(z.x, 20.0f), fminf(z.y, 20.0f)), make_float2(1.4426950408889634f, 1.4426950408889634f));
 }
+__device__ __forceinline__ float2 exp2_pair(float2 e) { return make_float2(ex2_approx(e.x), ex2_approx(e.y)); }
 // act(z) of a pair.  Mish = z t / (t + 2) with n = e^z, t = n (n + 2): it
 // cancels nowhere (~5e-7 relative on the hardware's exp2 and reciprocal).
 // ReLU passes NaN on.
@@ -154,22 +154,26 @@ __device__ __forceinline__ float2 act2(float2 z) {
     if constexpr (ACT == ACT_RELU) return make_float2(z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y);
     else if constexpr (ACT == ACT_MISH) {
         const float2 two = make_float2(2.0f, 2.0f);
-        const float2 n = exp2_clamped(z);
+        const float2 n = exp2_pair(exponent(z));
         const float2 t = mul2(n, add2(n, two));
         return mul2(z, mul2(t, rcp2(add2(t, two))));
     } else return z;
 }
 // act'(z) of a pair: with w = 1 + e^z, r = 1 / (w^2 + 1), Mish' = 1 - 2 r + z 4 e^z w r^2.
+// The factor z is the clamped one too (e^z w r^2, 4e-18 where the exponential
+// stops, times a huge z would not be 0, from about 1e9 on): the exponent over
+// log2 e.  0 z puts a NaN back.
 template <int ACT>
 __device__ __forceinline__ float2 dact2(float2 z) {
     if constexpr (ACT == ACT_RELU) return make_float2(z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f);
     else if constexpr (ACT == ACT_MISH) {
-        const float2 one = make_float2(1.0f, 1.0f);
-        const float2 n = exp2_clamped(z);
+        const float2 one = make_float2(1.0f, 1.0f), e = exponent(z);
+        const float2 n = exp2_pair(e);
         const float2 w = add2(n, one);
         const float2 r = rcp2(fma2(w, w, one));
         const float2 nr = mul2(mul2(n, r), mul2(w, r));
-        return fma2(mul2(z, make_float2(4.0f, 4.0f)), nr, fma2(r, make_float2(-2.0f, -2.0f), one));
+        return fma2(mul2(e, make_float2(2.772588722239781f, 2.772588722239781f)), nr,
+                    fma2(r, make_float2(-2.0f, -2.0f), fma2(z, make_float2(0.0f, 0.0f), one)));
     } else return make_float2(1.0f, 1.0f);
 }
 __device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
