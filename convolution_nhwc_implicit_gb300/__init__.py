@@ -166,27 +166,36 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_cuda = None
+
+
+def _cuda_getters():
+    """Torch's getters of the current device and of the handle of a device's
+    current stream, looked up once (the raw forms spare a small call the 3 us of
+    building a Stream object)."""
+    global _cuda
+    if _cuda is None:
+        import torch
+        try:
+            _cuda = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        except AttributeError:
+            _cuda = torch.cuda.current_device, lambda device: torch.cuda.current_stream(device).cuda_stream
+    return _cuda
+
+
 def _current_device():
-    import torch
-    try:
-        return torch._C._cuda_getDevice()
-    except AttributeError:
-        return torch.cuda.current_device()
+    return _cuda_getters()[0]()
 
 
-def _current_stream():
-    """Handle of torch's current stream (the raw form spares a small call the
-    3 us of building a Stream object)."""
-    import torch
-    try:
-        return torch._C._cuda_getCurrentRawStream(_current_device())
-    except AttributeError:
-        return torch.cuda.current_stream().cuda_stream
+def _current_stream(device=None):
+    """Handle of torch's current stream (on `device`, if the caller knows the current one)."""
+    device_of, stream_of = _cuda_getters()
+    return stream_of(device_of() if device is None else device)
 
 
-def _stream_handle(stream):
+def _stream_handle(stream, device=None):
     if stream is None:
-        return _current_stream()
+        return _current_stream(device)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -497,7 +506,7 @@ class GroupNormPlan(_OpPlan):
         r = None if rstd is None else _check("rstd", rstd, ss, f32, dev)
         ws = self._workspace(self.workspace_bytes, x, stream)
         rc = self._lib.conv_run_groupnorm(self._handle, px, pitch_x, g, b, py, pitch_y, m, r, _ptr(ws),
-                                          _stream_handle(stream))
+                                          _stream_handle(stream, dev))
         if rc != 0:
             raise ConvError("conv_run_groupnorm", rc)
 
@@ -512,7 +521,7 @@ class GroupNormPlan(_OpPlan):
         db = None if dbeta is None else _check("dbeta", dbeta, cs, f32, dev)
         ws = self._workspace(self.workspace_bytes_backward, x, stream)
         rc = self._lib.conv_run_groupnorm_bwd(self._handle, px, pitch_x, g, b, m, r, pdy, pitch_dy, pdx, pitch_dx, dg, db,
-                                              _ptr(ws), _stream_handle(stream))
+                                              _ptr(ws), _stream_handle(stream, dev))
         if rc != 0:
             raise ConvError("conv_run_groupnorm_bwd", rc)
 
@@ -546,7 +555,7 @@ class ClassLossPlan(_OpPlan):
         ps = None if lse is None else _check("lse", lse, (rows,), f32, dev)
         pr = None if row_loss is None else _check("row_loss", row_loss, (rows,), f32, dev)
         ws = self._workspace(self.workspace_bytes, x, stream)
-        rc = self._lib.conv_run_xent(self._handle, px, pw, pt, pl, pr, ps, _ptr(ws), _stream_handle(stream))
+        rc = self._lib.conv_run_xent(self._handle, px, pw, pt, pl, pr, ps, _ptr(ws), _stream_handle(stream, dev))
         if rc != 0:
             raise ConvError("conv_run_xent", rc)
 
@@ -559,7 +568,7 @@ class ClassLossPlan(_OpPlan):
         pdx, pdw = _check("dx", dx, (rows, c_in), bf16, dev), _check("dw", dw, (classes, c_in), bf16, dev)
         pd = None if dloss is None else _check("dloss", dloss, (), f32, dev)
         ws = self._workspace(self.workspace_bytes_backward, x, stream)
-        rc = self._lib.conv_run_xent_bwd(self._handle, px, pw, pt, ps, pd, pdx, pdw, _ptr(ws), _stream_handle(stream))
+        rc = self._lib.conv_run_xent_bwd(self._handle, px, pw, pt, ps, pd, pdx, pdw, _ptr(ws), _stream_handle(stream, dev))
         if rc != 0:
             raise ConvError("conv_run_xent_bwd", rc)
 
@@ -594,10 +603,11 @@ class W4Plan(_OpPlan):
         for that one before it reads it."""
         import torch
         _, c_in, c_out = self.shape
-        pc = _check("codes", codes, (c_out, (c_in + 1) // 2), self._u8, self._on_device())
+        dev = self._on_device()
+        pc = _check("codes", codes, (c_out, (c_in + 1) // 2), self._u8, dev)
         with _allocating_on(stream, codes.device):
             packed = torch.empty(self.packed_bytes, dtype=torch.uint8, device=codes.device)
-        rc = self._lib.conv_w4_pack(c_in, c_out, pc, packed.data_ptr(), _stream_handle(stream))
+        rc = self._lib.conv_w4_pack(c_in, c_out, pc, packed.data_ptr(), _stream_handle(stream, dev))
         if rc != 0:
             raise ConvError("conv_w4_pack", rc)
         return packed
@@ -609,7 +619,7 @@ class W4Plan(_OpPlan):
         px, pw, ps = _check("x", x, sx, dt, dev), _check("packed", packed, sw, self._u8, dev), _check("scales", scales, ss, dt, dev)
         pb = None if bias is None else _check("bias", bias, sb, self._f32, dev)
         py = _check("y", y, sy, dt, dev)
-        rc = self._lib.conv_run_w4(self._handle, px, pw, ps, pb, py, _stream_handle(stream))
+        rc = self._lib.conv_run_w4(self._handle, px, pw, ps, pb, py, _stream_handle(stream, dev))
         if rc != 0:
             raise ConvError("conv_run_w4", rc)
 
@@ -622,12 +632,13 @@ def w4_quantize(w, group=128, stream=None):
     if len(w.shape) != 2 or group < 1:
         raise ValueError(f"w must be [c_out, c_in] and group positive, got {tuple(w.shape)} and {group}")
     c_out, c_in = w.shape
-    pw = _check("w", w, (c_out, c_in), w.dtype, _current_device())
+    dev = _current_device()
+    pw = _check("w", w, (c_out, c_in), w.dtype, dev)
     with _allocating_on(stream, w.device):
         codes = torch.empty(c_out, (c_in + 1) // 2, dtype=torch.uint8, device=w.device)
         scales = torch.empty(c_out, -(-c_in // group), dtype=w.dtype, device=w.device)
     rc = load_library().conv_w4_quantize(c_in, c_out, group, DTYPES[dt], pw, codes.data_ptr(), scales.data_ptr(),
-                                         _stream_handle(stream))
+                                         _stream_handle(stream, dev))
     if rc != 0:
         raise ConvError("conv_w4_quantize", rc)
     return codes, scales

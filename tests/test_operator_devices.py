@@ -39,7 +39,7 @@ class Lib:
 def lib(monkeypatch):
     lib = Lib()
     monkeypatch.setattr(cl, "load_library", lambda: lib)
-    monkeypatch.setattr(cl, "_current_stream", lambda: 0)
+    monkeypatch.setattr(cl, "_current_stream", lambda *a: 0)
     monkeypatch.setattr(cl, "_current_device", lambda: 0, raising=False)
     return lib
 
