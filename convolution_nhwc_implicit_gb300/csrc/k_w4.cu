@@ -619,9 +619,15 @@ const void *many_group(int group) {
     return group == 32 ? (const void *)&w4_many_kernel<X, NT, 32, WC>
                        : (group == 64 ? (const void *)&w4_many_kernel<X, NT, 64, WC> : (const void *)&w4_many_kernel<X, NT, 128, WC>);
 }
+// (the shapes that a plan can choose: the others' x does not fit, see create)
+template <typename X, int NT, int WC>
+const void *many_fits(int group) {
+    if constexpr (WC == 8 || many_smem(X::kParts, NT, WC) <= kSmemMost) return many_group<X, NT, WC>(group);
+    else return nullptr;
+}
 template <typename X, int NT>
 const void *many_wc(const W4Geom &g) {
-    return g.wc == 8 ? many_group<X, NT, 8>(g.group) : (g.wc == 4 ? many_group<X, NT, 4>(g.group) : many_group<X, NT, 2>(g.group));
+    return g.wc == 8 ? many_fits<X, NT, 8>(g.group) : (g.wc == 4 ? many_fits<X, NT, 4>(g.group) : many_fits<X, NT, 2>(g.group));
 }
 template <typename X>
 const void *pick(const W4Geom &g) {
@@ -764,6 +770,7 @@ extern "C" int conv_run_w4(const conv_plan_t *plan, const void *x, const void *p
     W4Args a = {x, static_cast<const uint4 *>(packed), scales, bias, y, rows, ci, co, g.ng, g.units, p->act, (co + 15) / 16};
     int vec = ci % 8 == 0 && ((uintptr_t)x & 15u) == 0 ? 1 : 0;
     const void *k = p->dtype == CONV_F32 ? pick<XF32>(g) : pick<XBf16>(g);
+    if (!k) return CONV_ERR_UNSUPPORTED;
     if (g.smem > 48 * 1024) {
         const int rc = conv_grant_smem_once(k, p->device, g.smem);
         if (rc != CONV_OK) return rc;
