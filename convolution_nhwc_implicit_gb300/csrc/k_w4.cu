@@ -697,8 +697,13 @@ extern "C" int conv_plan_create_w4(int32_t rows, int32_t c_in, int32_t c_out, in
         while (ctas > 1 && ctas * (g.smem + 1024) > 227 * 1024) --ctas;
         g.grid = tiles < ctas * p->num_sms ? tiles : ctas * p->num_sms;
     }
-    snprintf(p->desc, sizeof(p->desc), "w4 %s group=%d %s warps=%d tiles=%d", dtype == CONV_F32 ? "f32" : "bf16", group,
-             g.many ? "x in turns" : "x in shared memory", g.warps, tiles);
+    const char *type = dtype == CONV_F32 ? "f32" : "bf16";
+    if (g.many)
+        snprintf(p->desc, sizeof(p->desc), "w4 %s group=%d x in turns rows=%dx8 warps=%d wc=%d tiles=%d ctas=%dx%d", type, group, g.nt,
+                 g.warps, g.wc, tiles, g.grid, (rows + g.nt * 8 - 1) / (g.nt * 8));
+    else
+        snprintf(p->desc, sizeof(p->desc), "w4 %s group=%d x in shared memory rows=%dx8 warps=%d tiles=%d ctas=%d", type, group, g.nt,
+                 g.warps, tiles, g.grid);
     *out_plan = p;
     return CONV_OK;
 }
