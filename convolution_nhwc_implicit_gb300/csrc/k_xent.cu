@@ -430,11 +430,16 @@ __global__ void __launch_bounds__(kThreads, 1) xent_kernel(const __grid_constant
                     tc::tmem_ld_wait();
                     if (c == 64) release();
                     if constexpr (KIND == GRAD) {
-                        const int at = tg - (col0 + c);
 #pragma unroll
                         for (int j = 0; j < 64; ++j) {
-                            const float p = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref));
-                            r[j] = __float_as_uint(on ? fmaf(p, rest, j == at ? -1.0f : 0.0f) : 0.0f);
+                            const float p = ex2(fmaf(__uint_as_float(r[j]), kLog2e, -ref)) * rest;
+                            r[j] = __float_as_uint(on ? p : 0.0f);
+                        }
+                        const int at = tg - (col0 + c);
+                        if (on && at >= 0 && at < 64) {  // (few lanes: classes are many)
+#pragma unroll
+                            for (int j = 0; j < 64; ++j)
+                                if (j == at) r[j] = __float_as_uint(__uint_as_float(r[j]) - 1.0f);
                         }
                     } else {
                         if (add) {
