@@ -24,8 +24,9 @@
 // however far the mean lies from zero.  All statistics are fp32, in a fixed
 // order: results do not change from run to run.
 //
-// Two forms, chosen by sizes alone (plan_direction), measured on a GB300 by
-// graph replay over changing inputs:
+// Two forms, chosen by sizes (plan_direction; where a CTA would hold more than
+// 256 channels, by a call's addresses too), measured on a GB300 by graph replay
+// over changing inputs:
 //   clusters    a few groups of an image in the shared memory of one to eight
 //               CTAs, one launch.  7x7x512 bf16 3.8 us (as two launches 8.8);
 //               8x80x80x256 bf16 with Mish 19.9 us (25.5), 2.6 TB/s of its 52
@@ -36,8 +37,9 @@
 //   two launches  sums, then results, where a run does not fit.
 //               16x160x160x128 fp32 with Mish 110 us: the map is read twice,
 //               5.7 TB/s over the three passes of HBM, against 62 us for the two
-//               that cannot be avoided.  The gradient of 8x80x80x256 bf16 29.5
-//               us: a median CTA takes 7.9 at its pixels in the first launch (x and
+//               that cannot be avoided.  The gradient of 8x80x80x256 bf16 29.9
+//               us: a median CTA (stamped before Mish's slope was clamped, 0.4
+//               less in all) takes 7.9 at its pixels in the first launch (x and
 //               dy at 6.6 TB/s) and 9.4 in the second, which reads them again
 //               from L2 and writes dx; the rest is the launches' starts and ends.
 // Tried and slower: one cooperative launch whose CTAs wait for one another's
@@ -71,7 +73,9 @@ constexpr int kStageRuns = 4096;             // partial results a CTA stages (32
 // Map bytes of a CTA of a cluster: four CTAs a SM, or two where a cluster of
 // eight cannot hold its runs otherwise.  (8x80x80x256 bf16 by CTAs a cluster: 6
 // 19.6 us, 8 20.0; 5 and 7, whose clusters need a second wave, 26.7 and 24.5.
-// 4 need 102 KB a CTA: 19.3 us in a build that allowed it, where 8 took 19.9.)
+// 4 need 102 KB a CTA: 19.3 us in a build that allowed it, where 8 took 19.9.
+// That one size is all that was measured above 88 KB, up to which the limit is
+// not known to be the best.)
 constexpr int kResident = 50 * 1024, kResidentMost = 88 * 1024;
 constexpr int kMaxC = 8192;  // channels: their sums stay in shared memory (16 bytes each)
 
@@ -707,7 +711,10 @@ __device__ __forceinline__ void join_rows_of_channels(const GnArgs &a, long long
 }
 // dx over one run of pixels, backwards like y; with `head`, the last grid row
 // joins the channels' sums of every image and run into dgamma and dbeta, 32
-// channels a CTA (last, so that no run waits for a place on the card).
+// channels a CTA (last, so that no run waits for a place on the card).  The row
+// is as wide as an image has runs: with one run an image, as in batches of more
+// images than the card holds CTAs, one CTA joins all channels (1024x7x7x1024
+// bf16 with Mish 711 us, forward and gradient, where its bytes take 61).
 template <typename T, int VEC, int ACT>
 __global__ void __launch_bounds__(kThreads, grad_ctas(sizeof(T))) gn_bwd_dx_kernel(GnArgs a, int head) {
     using L = GradLane<T, VEC, ACT>;

@@ -13,7 +13,8 @@
 // 2^127 or 2^123 times them is u / 64.  The products and sums are the tensor
 // core's in fp32, and a group's sum is scaled in fp32 when it ends.
 // Nothing is rounded to fewer bits before the result.  fp32 rows are split
-// into three bf16 parts (8 + 8 + 8 bits, the whole significand), three MMAs.
+// into three bf16 parts (8 + 8 + 8 bits, the whole significand; of values below
+// 2^-102 the last parts pass bf16's subnormals and are cut at 2^-133), three MMAs.
 // Measured on a GB300 (graph replay over changing inputs): one bf16 row through
 // 8192x28672, groups of 128, 24.9 us, 4.9 TB/s of codes and scales, 72 % of the
 // measured copy rate; issue slots are 64 % full and set the rest (128 input
@@ -21,9 +22,9 @@
 // ANDs and shifts of the decoding; with a shift, an AND-OR and a
 // subtraction a pair it took 33.3 us).  Groups of 32: 28.1 us.  1024x1000: 2.4
 // us, of which a launch is 2.1.  64 rows of 8192x28672 143 us.
-// (tcgen05 would need the decoded weights written to shared memory, four
-// times the streamed bytes there and back, for a product whose operand
-// rows are mostly empty.)
+// (One or a few rows leave most of a tcgen05 tile empty.  From some tens of rows
+// on this is mma.sync's rate and not the bytes: tcgen05 with the decoded weights
+// in TMEM as A and x in shared memory as B was not built.)
 //
 // Layout: tiles of 16 output channels x 64 input channels, 512 bytes, the
 // tiles of 16 output channels one after the other along k.  Lane l (g = l / 4,

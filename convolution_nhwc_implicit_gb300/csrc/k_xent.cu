@@ -29,7 +29,7 @@
 // TFLOP/s of the 8NDV that it does, 82 to 91 % of the measured burst rate; 1600 x 1024 x 32003, loss alone, 73 to 74 us, 1410
 // to 1440 TFLOP/s (tensor pipe 81 % busy; its 882 tiles fill 11.6 waves of pairs, and
 // the last of seven row tiles is a quarter full); 20 x 512 x 1000 with the
-// gradient 25 us, four launches of a few K blocks each.
+// gradient 25.6 us, four launches of a few K blocks each.
 //
 // The tile machine: a cluster of two CTAs (two SMs) computes 256 x 256 outputs
 // with tcgen05.mma.cta_group::2, each CTA staging 128 rows of A and 128 of B
@@ -737,7 +737,8 @@ extern "C" int conv_plan_create_xent(int32_t rows, int32_t c_in, int32_t classes
     g.tiles_m = ceil_div(rows, kTile);
     g.tiles_n = ceil_div(classes, kTile);
     g.tiles_d = ceil_div(c_in, kTile);
-    // Classes of a piece: the g workspace stays within 256 MB, whole tiles.
+    // Classes of a piece: whole tiles, one at least; as many as keep g within 256
+    // MB where one does (up to 524,288 rows).
     long long most = piece > 0 ? piece : (256ll << 20) / 2 / (rows > 0 ? rows : 1);
     if (most < kTile) most = kTile;
     most = most / kTile * kTile;
@@ -745,8 +746,10 @@ extern "C" int conv_plan_create_xent(int32_t rows, int32_t c_in, int32_t classes
     g.pieces = ceil_div(all, most < all ? most : all);
     g.piece = ceil_div(g.tiles_n, g.pieces) * kTile;
     g.pieces = ceil_div(all, g.piece);
-    // Few output tiles: each product's K axis in runs, so that every pair of
-    // SMs has one.
+    // Fewer output tiles than pairs of SMs: each product's K axis in runs, so
+    // that they all work.  (Few rows and many classes have tiles enough, of dw and
+    // one K block each, and dx's few long ones are then left to a few pairs:
+    // 20x512x65536 with the gradient takes 351 us.)
     const int pairs = p->num_sms / 2, pt = g.piece / kTile;
     const int tiles = (g.tiles_m + pt) * g.tiles_d;
     const int kx = g.piece / kBK, kw = ceil_div(rows, kBK);

@@ -335,9 +335,16 @@ CONV_API int conv_plan_workspace_bwd(const conv_plan_t *plan, size_t *bytes);
  * row_loss, lse and dloss may be NULL (not written; 1).  x, w, dx and dw are
  * 16-byte aligned and dense; any rows, c_in and classes.
  *
+ * A row that is left out still stands in dw's sum, times 0: a NaN or an infinity
+ * in its x makes dw NaN.
+ *
  * The gradient takes the classes in pieces: workspace holds g of one piece, in
- * bf16.  piece is the most classes at a time (rounded down to 256s, at least
- * 256; 0: as many as keep g within 256 MB).  The scores are formed again.
+ * bf16, and where there are several pieces or few output tiles the fp32 partial
+ * sums of dx (at least rows * c_in * 4 bytes, in whole 256 x 256 tiles) or dw.
+ * piece is the most classes at a time (rounded down to 256s, at least 256; 0: as
+ * many as keep g within 256 MB, or 256 where rows are more than 524288).  The
+ * scores are formed again.  A c_in that is not a multiple of 8 costs a padded
+ * copy of x and w in the workspace of either run.
  * rows <= 2^24, classes <= 2^24, c_in <= 2^20. */
 CONV_API int conv_plan_create_xent(int32_t rows, int32_t c_in, int32_t classes, int32_t piece, conv_dtype_t dtype,
                                    conv_plan_t **out_plan);
