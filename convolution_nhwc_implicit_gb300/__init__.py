@@ -20,7 +20,7 @@ import os
 
 __all__ = ["Plan", "ConvError", "conv2d_nhwc", "library_path", "load_library", "DTYPES", "ACTS",
            "ALGOS", "status_str", "abi_version", "run_i8_noalloc", "NOALLOC_MAX_COUT", "spp", "DwpwPlan",
-           "GroupNormPlan", "ClassLossPlan", "W4Plan", "w4_quantize"]
+           "GroupNormPlan", "ClassLossPlan", "W4Plan", "w4_quantize", "BlockNormPlan", "GradClipPlan", "NORMS"]
 
 # Largest c_out conv_run_i8_noalloc accepts (its fixed scratch array holds
 # that many requantisation multipliers).
@@ -31,9 +31,10 @@ _LIB_PATH = os.path.join(_HERE, "libconv_nhwc.so")
 
 DTYPES = {"f32": 0, "bf16": 1, "i8": 2}
 ACTS = {"none": 0, "relu": 1, "mish": 2}
+NORMS = {"none": 0, "layer": 1, "rms": 2}
 ALGOS = {"auto": 0, "direct": 1, "depthwise": 2, "igemm": 3, "igemm_swapped": 4, "igemm_n256": 5,
          "igemm_n128": 6, "igemm_n64": 7, "igemm_pair": 8, "dwpw": 9, "igemm_pair128": 10,
-         "groupnorm": 11, "w4": 12, "xent": 13}
+         "groupnorm": 11, "w4": 12, "xent": 13, "blocknorm": 14, "gradclip": 15}
 ALGO_NAMES = {v: k for k, v in ALGOS.items()}
 # Staging, epilogue and int8-widening flags of the tensor-core family
 # (CONV_ALGO_STAGE_*, CONV_ALGO_EPI_*, CONV_ALGO_WIDEN_*), written as suffixes
@@ -67,6 +68,11 @@ class _Output(ctypes.Structure):
 class _Quant(ctypes.Structure):
     _fields_ = [("in_scale", ctypes.c_float), ("out_scale", ctypes.c_float),
                 ("w_scales", ctypes.POINTER(ctypes.c_float))]
+
+
+class _BlockNormPointers(ctypes.Structure):
+    """conv_blocknorm_params_t and conv_blocknorm_grads_t."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("scale", "gate", "post_gamma", "post_beta", "pre_gamma", "pre_beta")]
 
 
 _lib = None
@@ -142,7 +148,14 @@ def load_library():
             ("conv_w4_packed_bytes", [i32, i32, ctypes.POINTER(ctypes.c_size_t)]),
             ("conv_w4_pack", [i32, i32, c_void_p, c_void_p, c_void_p]),
             ("conv_w4_quantize", [i32, i32, i32, c_int] + [c_void_p] * 4),
-            ("conv_run_w4", [c_void_p] * 7)):
+            ("conv_run_w4", [c_void_p] * 7),
+            ("conv_plan_create_blocknorm", [i32, i32, i32, i32, c_int, c_int, ctypes.c_float, c_int, pp]),
+            ("conv_run_blocknorm", [c_void_p, c_void_p, i64, c_void_p, i64, ctypes.POINTER(_BlockNormPointers), c_void_p, i64,
+                                    c_void_p, i64, c_void_p, c_void_p]),
+            ("conv_run_blocknorm_bwd", [c_void_p, c_void_p, i64, c_void_p, i64, ctypes.POINTER(_BlockNormPointers), c_void_p] +
+             [c_void_p, i64] * 4 + [ctypes.POINTER(_BlockNormPointers), c_void_p, c_void_p]),
+            ("conv_plan_create_gradclip", [i32, ctypes.POINTER(i64), ctypes.POINTER(c_int), pp]),
+            ("conv_run_gradclip", [c_void_p, pp, pp, ctypes.c_float, c_void_p, c_void_p, c_void_p])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = c_int
     _lib = lib
@@ -457,24 +470,9 @@ class _OpPlan(Plan):
             return torch.empty(nbytes, dtype=torch.uint8, device=like.device)
 
 
-class GroupNormPlan(_OpPlan):
-    """Group norm with an activation over NHWC maps (conv_plan_create_groupnorm).
-
-    x, y, dy and dx are [n, h, w, c] CUDA tensors, dense or channel slices of a
-    wider dense buffer (``buf[..., a:a + c]``); gamma, beta, dgamma and dbeta
-    float32 [c]; mean and rstd float32 [n, groups]."""
-
-    def __init__(self, n, h, w, c, groups, eps=1e-5, dtype="bf16", act="none"):
-        self.shape = (n, h, w, c)
-        self.groups, self.eps, self.dtype, self.act = groups, eps, dtype, act
-        self._create("conv_plan_create_groupnorm", n, h, w, c, groups, float(eps), DTYPES[dtype], ACTS[act])
-        self._cshape, self._sshape = (c,), (n, groups)
-
-    @property
-    def output_shape(self):
-        return self.shape
-
-    y_shape = output_shape
+class _MapPlan(_OpPlan):
+    """Plans whose runs take feature maps [n, h, w, c], ``shape``, dense or
+    channel slices of a wider dense buffer (``buf[..., a:a + c]``)."""
 
     def _map(self, name, t):
         """Pointer and pixel pitch of a feature map."""
@@ -495,6 +493,26 @@ class GroupNormPlan(_OpPlan):
         if ((c > 1 and sc != 1) or pitch < c or (h > 1 and sh != w * pitch) or (n > 1 and sn != h * w * pitch)):
             raise ValueError(f"{name}: pixels must lie one pitch apart with their channels together, got strides {t.stride()}")
         return t.data_ptr(), pitch
+
+
+class GroupNormPlan(_MapPlan):
+    """Group norm with an activation over NHWC maps (conv_plan_create_groupnorm).
+
+    x, y, dy and dx are [n, h, w, c] CUDA tensors, dense or channel slices of a
+    wider dense buffer (``buf[..., a:a + c]``); gamma, beta, dgamma and dbeta
+    float32 [c]; mean and rstd float32 [n, groups]."""
+
+    def __init__(self, n, h, w, c, groups, eps=1e-5, dtype="bf16", act="none"):
+        self.shape = (n, h, w, c)
+        self.groups, self.eps, self.dtype, self.act = groups, eps, dtype, act
+        self._create("conv_plan_create_groupnorm", n, h, w, c, groups, float(eps), DTYPES[dtype], ACTS[act])
+        self._cshape, self._sshape = (c,), (n, groups)
+
+    @property
+    def output_shape(self):
+        return self.shape
+
+    y_shape = output_shape
 
     def run(self, x, gamma, beta, y, mean=None, rstd=None, stream=None) -> None:  # noqa: D401
         """Enqueue y = act(group_norm(x) * gamma + beta) on `stream` (default: torch's current stream)."""
@@ -622,6 +640,139 @@ class W4Plan(_OpPlan):
         rc = self._lib.conv_run_w4(self._handle, px, pw, ps, pb, py, _stream_handle(stream, dev))
         if rc != 0:
             raise ConvError("conv_run_w4", rc)
+
+
+class BlockNormPlan(_MapPlan):
+    """The norms before and after a block, fused with the block's gate, its
+    residual scale and the residual add (conv_plan_create_blocknorm)::
+
+        y = x + scale * gate * (post(f) * post_gamma + post_beta)
+        z = pre(y) * pre_gamma + pre_beta
+
+    x is the residual stream and f the block's output; ``post`` and ``pre`` are
+    "layer", "rms" or "none", over each pixel's channels.  Maps (x, f, y, z and
+    their gradients) are [n, h, w, c] CUDA tensors, dense or channel slices of a
+    wider dense buffer; gate and dgate float32 [n, c], the other parameters and
+    their gradients float32 [c]; stats float32 [n, h, w, 4].  A parameter that is
+    None is 1 (scale, gate, gammas) or 0 (betas)."""
+
+    def __init__(self, n, h, w, c, post="layer", pre="layer", eps=1e-5, dtype="bf16"):
+        self.shape = (n, h, w, c)
+        self.post, self.pre, self.eps, self.dtype, self.act = post, pre, eps, dtype, "none"
+        self._create("conv_plan_create_blocknorm", n, h, w, c, NORMS[post], NORMS[pre], float(eps), DTYPES[dtype])
+        self._cshape, self._gshape, self._sshape = (c,), (n, c), (n, h, w, 4)
+
+    @property
+    def output_shape(self):
+        return self.shape
+
+    y_shape = output_shape
+
+    def _pointers(self, dev, prefix, scale, gate, post_gamma, post_beta, pre_gamma, pre_beta):
+        """The parameters, or their gradients, as the library takes them."""
+        f32, cs = self._f32, self._cshape
+        return _BlockNormPointers(
+            None if scale is None else _check(prefix + "scale", scale, cs, f32, dev),
+            None if gate is None else _check(prefix + "gate", gate, self._gshape, f32, dev),
+            None if post_gamma is None else _check(prefix + "post_gamma", post_gamma, cs, f32, dev),
+            None if post_beta is None else _check(prefix + "post_beta", post_beta, cs, f32, dev),
+            None if pre_gamma is None else _check(prefix + "pre_gamma", pre_gamma, cs, f32, dev),
+            None if pre_beta is None else _check(prefix + "pre_beta", pre_beta, cs, f32, dev))
+
+    def run(self, x, f, y, z, stats=None, scale=None, gate=None, post_gamma=None, post_beta=None, pre_gamma=None,
+            pre_beta=None, stream=None) -> None:  # noqa: D401
+        """Enqueue y and z on `stream` (default: torch's current stream).
+
+        f None (``post`` "none"): z is the norm of x, and y is None.  y may be
+        None where there is a z; z is None where ``pre`` is "none".  y or z may
+        be x or f itself.  stats, where given, is what the gradient needs."""
+        dev = self._on_device()
+        px, pitch_x = self._map("x", x)
+        pf, pitch_f = (None, 0) if f is None else self._map("f", f)
+        py, pitch_y = (None, 0) if y is None else self._map("y", y)
+        pz, pitch_z = (None, 0) if z is None else self._map("z", z)
+        ps = None if stats is None else _check("stats", stats, self._sshape, self._f32, dev)
+        w = self._pointers(dev, "", scale, gate, post_gamma, post_beta, pre_gamma, pre_beta)
+        rc = self._lib.conv_run_blocknorm(self._handle, px, pitch_x, pf, pitch_f, w, py, pitch_y, pz, pitch_z, ps,
+                                          _stream_handle(stream, dev))
+        if rc != 0:
+            raise ConvError("conv_run_blocknorm", rc)
+
+    def run_backward(self, x, f, stats, dy, dz, dx, df, scale=None, gate=None, post_gamma=None, post_beta=None,
+                     pre_gamma=None, dscale=None, dgate=None, dpost_gamma=None, dpost_beta=None, dpre_gamma=None,
+                     dpre_beta=None, stream=None) -> None:
+        """Enqueue the gradient: dx and df, and those of the parameters where
+        given.  x, f, stats and the parameters as the forward run had them; dy
+        None is 0; dx or df may be any of the maps that are read."""
+        dev = self._on_device()
+        px, pitch_x = self._map("x", x)
+        pf, pitch_f = (None, 0) if f is None else self._map("f", f)
+        pdy, pitch_dy = (None, 0) if dy is None else self._map("dy", dy)
+        pdz, pitch_dz = (None, 0) if dz is None else self._map("dz", dz)
+        pdx, pitch_dx = self._map("dx", dx)
+        pdf, pitch_df = (None, 0) if df is None else self._map("df", df)
+        ps = _check("stats", stats, self._sshape, self._f32, dev)
+        w = self._pointers(dev, "", scale, gate, post_gamma, post_beta, pre_gamma, None)
+        d = self._pointers(dev, "d", dscale, dgate, dpost_gamma, dpost_beta, dpre_gamma, dpre_beta)
+        ws = self._workspace(self.workspace_bytes_backward, x, stream)
+        rc = self._lib.conv_run_blocknorm_bwd(self._handle, px, pitch_x, pf, pitch_f, w, ps, pdy, pitch_dy, pdz, pitch_dz,
+                                              pdx, pitch_dx, pdf, pitch_df, d, _ptr(ws), _stream_handle(stream, dev))
+        if rc != 0:
+            raise ConvError("conv_run_blocknorm_bwd", rc)
+
+
+class GradClipPlan(_OpPlan):
+    """The global norm of many gradients, and clipping (conv_plan_create_gradclip)::
+
+        norm = sqrt(sum of all squares)
+        out = min(1, max_norm / (norm + 1e-6)) * g
+
+    ``shapes``: a shape (or a number of elements) for each tensor; ``dtypes``:
+    "bf16" or "f32" for all of them, or one for each."""
+
+    def __init__(self, shapes, dtypes="bf16"):
+        import math
+        self.shapes = [(s,) if isinstance(s, int) else tuple(s) for s in shapes]
+        count = len(self.shapes)
+        names = [dtypes] * count if isinstance(dtypes, str) else list(dtypes)
+        if len(names) != count:
+            raise ValueError(f"{len(names)} dtypes for {count} tensors")
+        self.dtypes, self.act = names, "none"
+        self.dtype, self.shape = (names[0] if names else "f32"), (count,)
+        counts = (ctypes.c_int64 * count)(*(math.prod(s) for s in self.shapes))
+        codes = (ctypes.c_int * count)(*(DTYPES[d] for d in names))
+        self._create("conv_plan_create_gradclip", count, counts, codes)
+        self._each = [(s, _torch_dtype(d)) for s, d in zip(self.shapes, names)]
+        self._array = ctypes.c_void_p * count
+
+    @property
+    def output_shape(self):
+        return ()
+
+    y_shape = output_shape
+
+    def _addresses(self, name, tensors, dev):
+        if len(tensors) != len(self._each):
+            raise ValueError(f"{len(tensors)} {name} for a plan of {len(self._each)}")
+        for t, (shape, dtype) in zip(tensors, self._each):
+            if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+                i = next(i for i, u in enumerate(tensors) if u is t)
+                _check(f"{name}[{i}]", t, shape, dtype, dev)
+        return self._array(*[t.data_ptr() for t in tensors])
+
+    def run(self, grads, max_norm, norm, out=None, stream=None) -> None:  # noqa: D401
+        """Enqueue the norm (a float32 scalar tensor) and the clipped gradients
+        on `stream` (default: torch's current stream): into the tensors of `out`
+        (any of which may be the gradient itself), or in place.  max_norm
+        infinite: the norm alone.  A norm that is not finite clips nothing."""
+        dev = self._on_device()
+        g = self._addresses("grads", grads, dev)
+        o = None if out is None else self._addresses("out", out, dev)
+        pn = _check("norm", norm, (), self._f32, dev)
+        ws = self._workspace(self.workspace_bytes, norm, stream)
+        rc = self._lib.conv_run_gradclip(self._handle, g, o, float(max_norm), pn, _ptr(ws), _stream_handle(stream, dev))
+        if rc != 0:
+            raise ConvError("conv_run_gradclip", rc)
 
 
 def w4_quantize(w, group=128, stream=None):

@@ -417,6 +417,7 @@ void conv_plan_destroy(conv_plan_t *plan) {
     if (plan->d_mult) cudaFree(plan->d_mult);
     if (plan->d_xprep) cudaFree(plan->d_xprep);
     if (plan->d_wprep) cudaFree(plan->d_wprep);
+    clip_destroy(plan->clip);
     delete plan;
 }
 
@@ -441,6 +442,7 @@ int conv_plan_launches(const conv_plan_t *plan) {
         return plan->gn.fwd.K > 0 ? 1 : 2;
     // (the forward run; its gradient takes two launches a piece of the classes, and more for joined sums)
     if (plan->algo == CONV_ALGO_XENT) return plan->xent.dp == plan->s.c_in ? 2 : 3;
+    if (plan->algo == CONV_ALGO_GRADCLIP) return clip_launches(plan->clip);
     return (plan->algo == CONV_ALGO_IGEMM && plan->ig.prep) ? 2 : 1;
 }
 
@@ -460,8 +462,10 @@ int conv_run_fused(const conv_plan_t *plan, const void *x, const void *w, const 
                    void *y, void *stream) {
     if (!plan) return CONV_ERR_NULL_ARG;
     const conv_plan *p = plan;
-    // (plans that run through entry points of their own: conv_run_dwpw, conv_run_groupnorm, conv_run_xent, conv_run_w4)
-    if (p->algo == CONV_ALGO_DWPW || p->algo == CONV_ALGO_GROUPNORM || p->algo == CONV_ALGO_W4 || p->algo == CONV_ALGO_XENT)
+    // (plans that run through entry points of their own: conv_run_dwpw, conv_run_groupnorm, conv_run_xent,
+    // conv_run_w4, conv_run_blocknorm, conv_run_gradclip)
+    if (p->algo == CONV_ALGO_DWPW || p->algo == CONV_ALGO_GROUPNORM || p->algo == CONV_ALGO_W4 ||
+        p->algo == CONV_ALGO_XENT || p->algo == CONV_ALGO_BLOCKNORM || p->algo == CONV_ALGO_GRADCLIP)
         return CONV_ERR_INVALID_ARG;
     if (p->has_res && !residual) return CONV_ERR_NULL_ARG;
     if (!p->has_res && residual) return CONV_ERR_INVALID_ARG;

@@ -99,6 +99,19 @@ struct XentGeom {
     int dx_split, dx_kper, dw_split, dw_kper;
 };
 
+// Norms around a block: threads of a row, rows side by side, k times 8 channels
+// a thread; rows of a forward CTA; the gradient's division without a gate and
+// with one (runs of S an image, or of all rows; whole: a unit is an image).
+struct BnGeom {
+    int post, pre;
+    float eps;
+    int k, tpr, slots, threads;
+    int run, grid;
+    struct Bwd { int run, S, units, whole, grid; } open, gated;
+};
+
+struct ClipGeom;  // gradient norm and clipping (k_gradclip.cu)
+
 struct conv_plan {
     conv_shape_t s;
     int stride, pad_h, pad_w, groups;
@@ -124,6 +137,8 @@ struct conv_plan {
     GnGeom gn;
     W4Geom w4;
     XentGeom xent;
+    BnGeom bn;
+    ClipGeom *clip;
     size_t ws_bytes, ws_bwd_bytes;  // device scratch a run (its gradient) takes from the caller
     char desc[192];
 };
@@ -165,6 +180,10 @@ cudaError_t launch_dwpw(const conv_plan *p, const void *x, const void *wdw, cons
                         const void *bpw, void *y, cudaStream_t st);
 bool dwpw_supported(const conv_plan *p);
 int dwpw_configure(conv_plan *p);  // CONV_* status
+
+// Frees what the plan of a gradient norm holds on host and device (null: nothing).
+void clip_destroy(ClipGeom *g);
+int clip_launches(const ClipGeom *g);
 
 // Widens int8 to bf16 / pads channels into the plan's d_xprep, d_wprep.
 cudaError_t launch_prep(const conv_plan *p, const void *x, const void *w, cudaStream_t st);

@@ -111,6 +111,8 @@ typedef enum {
     CONV_ALGO_GROUPNORM = 11, /* conv_plan_create_groupnorm  */
     CONV_ALGO_W4 = 12,        /* conv_plan_create_w4         */
     CONV_ALGO_XENT = 13,      /* conv_plan_create_xent       */
+    CONV_ALGO_BLOCKNORM = 14, /* conv_plan_create_blocknorm  */
+    CONV_ALGO_GRADCLIP = 15,  /* conv_plan_create_gradclip   */
 } conv_algo_t;
 
 /* Staging of the tensor-core family's pixel operand, OR-ed into CONV_ALGO_IGEMM
@@ -381,6 +383,98 @@ CONV_API int conv_w4_quantize(int32_t c_in, int32_t c_out, int32_t group, conv_d
                               void *scales, void *stream);
 CONV_API int conv_run_w4(const conv_plan_t *plan, const void *x, const void *packed, const void *scales,
                          const float *bias, void *y, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The norms before and after a block, fused with the block's gate, its residual
+ * scale and the residual add, channels last.  x is the residual stream, f the
+ * block's output, each pixel a row of c channels; a norm is of one of these
+ * kinds over the row:
+ *   layer  m = sum v / c   r = 1 / sqrt( sum (v - m)^2 / c + eps )
+ *   rms    m = 0           r = 1 / sqrt( sum v^2 / c + eps )
+ *   none   m = 0           r = 1
+ * With (m1, r1) of f under `post` and (m2, r2) of y under `pre`:
+ *   u = post_gamma[c] (f - m1) r1 + post_beta[c]
+ *   y = x + scale[c] gate[n][c] u
+ *   z = pre_gamma[c] (y - m2) r2 + pre_beta[c]
+ * y is rounded to dtype where it is written; z is formed of the y before that
+ * rounding.  f NULL (post none, no scale and no gate): z is the norm of x, and
+ * y is NULL.  pre none: there is no z.  y may be NULL where there is a z.
+ *
+ * The gradient, with u^ = (f - m1) r1, y^ = (y - m2) r2 and means over the row:
+ *   e = pre_gamma dz    dx = dy + r2 ( e - [layer] mean(e) - y^ mean(e y^) )
+ *   v = scale gate post_gamma dx
+ *   df = r1 ( v - [layer] mean(v) - u^ mean(v u^) )
+ *   dpre_gamma = sum dz y^         dpre_beta = sum dz
+ *   A[n] = sum over an image's pixels of dx u^     B[n] = that of dx
+ *   dgate[n] = scale ( post_gamma A[n] + post_beta B[n] )
+ *   dscale = sum_n gate[n] ( post_gamma A[n] + post_beta B[n] )
+ *   dpost_gamma = scale sum_n gate[n] A[n]    dpost_beta = scale sum_n gate[n] B[n]
+ * (dx before its rounding).  It forms y again of x and f, so these must still
+ * be what the forward run read.
+ *
+ * dtype CONV_F32 or CONV_BF16 for the maps (CONV_I8: CONV_ERR_UNSUPPORTED);
+ * parameters and their gradients float32: gate and dgate [n][c], the others
+ * [c].  A parameter that is NULL is 1 (scale, gate, gammas) or 0 (betas); a
+ * gradient that is NULL is not written; post_ and pre_ ones go with a norm of
+ * their own, dgate with a gate (CONV_ERR_INVALID_ARG).  stats [n][h][w][4]
+ * float32, 16-byte aligned, is (m1, r1, m2, r2) of each pixel: written where
+ * given by the forward run, required by the gradient.  All statistics and sums
+ * are fp32.  eps >= 0 (CONV_ERR_INVALID_ARG); c <= 8192, n * h * w < 2^30
+ * (CONV_ERR_UNSUPPORTED).
+ *
+ * The maps are [n][h][w] pixels of c channels, *_pitch elements from one pixel
+ * to the next (0: c), as for group norm.  dy may be NULL (0) where there is a
+ * z, dz is required there and NULL otherwise.  A written map may be one of the
+ * input maps itself (address and pitch alike: y over x in a stream that is not
+ * trained, df over dz); otherwise nothing that a run writes shares an element
+ * with another map or a byte with anything else (CONV_ERR_ALIASING).  n = 0
+ * does nothing (the gradient writes zeros to the sums over pixels).  The
+ * gradient takes conv_plan_workspace_bwd bytes of scratch. */
+typedef enum { CONV_NORM_NONE = 0, CONV_NORM_LAYER = 1, CONV_NORM_RMS = 2 } conv_norm_t;
+
+typedef struct {
+    const float *scale, *gate, *post_gamma, *post_beta, *pre_gamma, *pre_beta;
+} conv_blocknorm_params_t;
+
+typedef struct {
+    float *scale, *gate, *post_gamma, *post_beta, *pre_gamma, *pre_beta;
+} conv_blocknorm_grads_t;
+
+CONV_API int conv_plan_create_blocknorm(int32_t n, int32_t h, int32_t w, int32_t c, conv_norm_t post, conv_norm_t pre,
+                                        float eps, conv_dtype_t dtype, conv_plan_t **out_plan);
+/* params NULL: none of them. */
+CONV_API int conv_run_blocknorm(const conv_plan_t *plan, const void *x, int64_t x_pitch, const void *f, int64_t f_pitch,
+                                const conv_blocknorm_params_t *params, void *y, int64_t y_pitch, void *z,
+                                int64_t z_pitch, float *stats, void *stream);
+CONV_API int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, int64_t x_pitch, const void *f,
+                                    int64_t f_pitch, const conv_blocknorm_params_t *params, const float *stats,
+                                    const void *dy, int64_t dy_pitch, const void *dz, int64_t dz_pitch, void *dx,
+                                    int64_t dx_pitch, void *df, int64_t df_pitch, const conv_blocknorm_grads_t *grads,
+                                    void *workspace, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The global norm of many gradients, and clipping:
+ *   norm = sqrt( sum over all tensors and elements of g^2 )
+ *   k = min( 1, max_norm / (norm + 1e-6) )        out = k g
+ * A norm that is not finite clips nothing (k = 1): it says itself that the
+ * step is to be left out.  `counts` and `dtypes` (HOST arrays of `tensors`
+ * entries, copied) give each tensor's elements (>= 0; all together < 2^40) and
+ * type, CONV_F32 or CONV_BF16 (CONV_I8: CONV_ERR_UNSUPPORTED).
+ *   grads  HOST array of `tensors` device addresses, multiples of the element
+ *          size; 16-byte ones give the widest loads (NULL where count is 0)
+ *   outs   the same for the results, NULL: in place (then a set that needs no
+ *          clipping is not written).  outs[i] may be grads[i]; otherwise no
+ *          written tensor shares a byte with any other (CONV_ERR_ALIASING)
+ *   max_norm  > 0 (CONV_ERR_INVALID_ARG); infinity: only the norm, outs copied
+ *   norm   float32, a device scalar
+ * Squares are summed in fp32 over a few thousand elements, scaled by a power of
+ * two where they would overflow or vanish, and those sums in fp64, in a fixed
+ * order; k is rounded once to fp32, each product once to the tensor's type.
+ * Takes conv_plan_workspace bytes of scratch. */
+CONV_API int conv_plan_create_gradclip(int32_t tensors, const int64_t *counts, const conv_dtype_t *dtypes,
+                                       conv_plan_t **out_plan);
+CONV_API int conv_run_gradclip(const conv_plan_t *plan, void *const *grads, void *const *outs, float max_norm,
+                               float *norm, void *workspace, void *stream);
 
 /* Enqueues the layer on `stream` (a cudaStream_t; NULL = legacy default
  * stream).  x, w, y are device pointers, bias a device pointer or NULL; all
