@@ -100,14 +100,14 @@ struct XentGeom {
 };
 
 // Norms around a block: threads of a row, rows side by side, k times 8 channels
-// a thread; rows of a forward CTA; the gradient's division without a gate and
-// with one (runs of S an image, or of all rows; whole: a unit is an image).
+// a thread.  How each direction divides the rows, without a gate and with one:
+// units of `run` rows, S an image (or of all rows); rb rows at a time (0: the
+// gradient); whole: a unit is an image.
 struct BnGeom {
     int post, pre;
     float eps;
-    int k, tpr, slots, threads;
-    int run, grid;
-    struct Bwd { int run, S, units, whole, grid; } open, gated;
+    int k, tpr, slots, threads, full;
+    struct Part { int rb, run, S, units, grid, whole; } fwd, fwd_gated, bwd, bwd_gated;
 };
 
 struct ClipGeom;  // gradient norm and clipping (k_gradclip.cu)

@@ -56,10 +56,10 @@ struct BnArgs {
     float eps, inv_c;
     int rows, HW, C, N;
     int post, pre;                 // conv_norm_t
-    int tpr, slots;                // threads of a row, rows side by side
-    int run;                       // rows of a CTA (gradient: of a unit)
-    int S, units;                  // gradient: runs an image (of all rows without a gate), runs in all
+    int tpr, slots, full;          // threads of a row, rows side by side; full: every thread has channels, all of them
+    int run, S, units;             // rows of a unit, units an image (of all rows without a gate), units in all
     int whole;                     // gradient: a unit is a whole image of a gated map
+    int want_b;                    // gradient: B is asked for
 };
 
 // Where a thread stands: which row of those side by side, which of the row's
@@ -75,11 +75,12 @@ struct Lane {
     }
     __device__ __forceinline__ int first(int v) const { return (v * tpr + t) * VEC; }
     __device__ __forceinline__ bool on(int v) const { return first(v) < C; }
+    // (channels are whole vectors: a vector's are all in the row, or none)
+    __device__ __forceinline__ bool has(int i, int h) const { return VEC == 1 ? on(2 * i + h) : on(i / (VEC < 2 ? 1 : VEC / 2)); }
     __device__ __forceinline__ int chan(int i, int h) const {
         if constexpr (VEC == 1) return first(2 * i + h);
         else return first(i / (VEC / 2)) + i % (VEC / 2) * 2 + h;
     }
-    __device__ __forceinline__ bool has(int i, int h) const { return chan(i, h) < C; }
     // src at the thread's channels (null: `other`), 0 beyond the row's end
     __device__ __forceinline__ void params(float2 (&v)[P], const float *src, float other) const {
 #pragma unroll
@@ -90,22 +91,21 @@ struct Lane {
     }
 };
 
+// A thread's vectors of one row: from its ring of shared memory, to a map, and
+// from a map to the ring.  Vectors beyond the row's end stay 0 in the ring.
 template <typename T, int VEC, int K>
 struct Row {
     using V = Vec<T, VEC>;
     using Raw = typename V::Raw;
     using L = Lane<VEC, K>;
     static constexpr int NV = L::NV, P = L::P;
-    // a thread's vectors of one map, `step` apart in shared memory, 0 beyond the row's end
-    __device__ static __forceinline__ void get(const L &l, const Raw *src, int step, float2 (&f)[P]) {
+    __device__ static __forceinline__ void get(const Raw *src, int step, float2 (&f)[P]) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             float2 one[V::kPairs];
             V::unpack(src[v * step], one);
-            const bool on = l.on(v);
 #pragma unroll
             for (int e = 0; e < V::kPairs; ++e) {
-                if (!on) one[e] = make_float2(0.0f, 0.0f);
                 if constexpr (VEC == 1) {
                     if (v % 2) f[v / 2].y = one[0].x;
                     else f[v / 2].x = one[0].x;
@@ -113,6 +113,7 @@ struct Row {
             }
         }
     }
+    // (row: the address of the thread's first vector)
     __device__ static __forceinline__ void put(const L &l, T *row, const float2 (&f)[P]) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -122,69 +123,115 @@ struct Row {
                 if constexpr (VEC == 1) one[0].x = v % 2 ? f[v / 2].y : f[v / 2].x;
                 else one[e] = f[v * V::kPairs + e];
             }
-            if (l.on(v)) *reinterpret_cast<Raw *>(row + l.first(v)) = V::pack(one);
+            if (l.on(v)) *reinterpret_cast<Raw *>(row + v * l.tpr * VEC) = V::pack(one);
         }
     }
     __device__ static __forceinline__ void ask(const L &l, const T *row, Raw *dst, int step) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            if (l.on(v)) copy_vec(dst + v * step, reinterpret_cast<const Raw *>(row + l.first(v)));
+            if (l.on(v)) copy_vec(dst + v * step, reinterpret_cast<const Raw *>(row + v * l.tpr * VEC));
+    }
+    // the vectors beyond the row's end in `rows` rows of the ring
+    template <int ROWS>
+    __device__ static __forceinline__ void blank(const L &l, Raw *dst, int step) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+            if (!l.on(v))
+                for (int i = 0; i < ROWS; ++i) dst[(i * NV + v) * step] = Raw{};
+    }
+    __device__ static __forceinline__ void zero(Raw *dst, int step) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) dst[v * step] = Raw{};
     }
 };
 
-// Sums over the threads of a row.  Rows of more than a warp meet in one of two
-// sets of shared entries in turn: whoever writes an entry again has passed the
-// barrier of the other set, and with it everyone's reading of this one.
+// Two sums over the threads of a row, to all of them.  The first exchange
+// leaves one sum to each half of the lanes, which halves the exchanges.  Rows of
+// more than a warp then meet in one of two sets of shared entries in turn:
+// whoever writes an entry again has passed the barrier of the other set, and
+// with it everyone's reading of this one.
 struct RowSum {
     int tpr, slot;
-    float2 *buf;
+    float *buf;  // [2][warps][2]
     int flip;
-    __device__ __forceinline__ RowSum(int tpr_, int slot_, float2 *b) : tpr(tpr_), slot(slot_), buf(b), flip(0) {}
-    __device__ __forceinline__ float2 operator()(float2 v) {
+    __device__ __forceinline__ RowSum(int tpr_, int slot_, float *b) : tpr(tpr_), slot(slot_), buf(b), flip(0) {}
+    __device__ static __forceinline__ float across(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+    __device__ __forceinline__ float2 operator()(float a, float b) {
+        const int lane = threadIdx.x & 31;
+        if (tpr >= 32) {
+            const bool hi = lane & 16;
+            float v = (hi ? b : a) + across(hi ? a : b, 16);
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            if (o < tpr) {
-                const float2 w = make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
-                v = add2(v, w);
+            for (int o = 8; o > 0; o >>= 1) v += across(v, o);
+            if (tpr > 32) {
+                float *e = buf + flip;
+                flip ^= kMostThreads / 32 * 2;
+                if ((lane & 15) == 0) e[(threadIdx.x >> 5) * 2 + (lane >> 4)] = v;
+                asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
+                const int n = tpr >> 5, k = lane & 15;
+                v = k < n ? e[(slot * n + k) * 2 + (lane >> 4)] : 0.0f;
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) v += across(v, o);
             }
-        if (tpr > 32) {
-            float2 *b = buf + flip;
-            flip ^= kMostThreads / 32;
-            if ((threadIdx.x & 31) == 0) b[threadIdx.x >> 5] = v;
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
-            const int n = tpr >> 5;
-            v = b[slot * n];
-            for (int i = 1; i < n; ++i) v = add2(v, b[slot * n + i]);
+            const float w = across(v, 16);
+            return hi ? make_float2(w, v) : make_float2(v, w);
         }
-        return v;
+        if (tpr == 1) return make_float2(a, b);
+        const int top = tpr >> 1;
+        const bool hi = lane & top;
+        float v = (hi ? b : a) + across(hi ? a : b, top);
+        for (int o = top >> 1; o > 0; o >>= 1) v += across(v, o);
+        const float w = across(v, top);
+        return hi ? make_float2(w, v) : make_float2(v, w);
     }
 };
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+template <int P>
+__device__ __forceinline__ float total(const float2 (&v)[P]) {
+    float2 s = v[0];
+#pragma unroll
+    for (int i = 1; i < P; ++i) s = add2(s, v[i]);
+    return s.x + s.y;
+}
 
-// m and r of one norm of a row, and the values normalised in place.
-template <int VEC, int K>
-__device__ __forceinline__ float2 normalise(const Lane<VEC, K> &l, RowSum &sum, float2 (&v)[4 * K], int kind, float inv_c, float eps) {
+// m and r of one norm of RB rows (1 or 2), and the values normalised in place.
+template <int VEC, int K, int RB>
+__device__ __forceinline__ void normalise(const Lane<VEC, K> &l, RowSum &sum, float2 (&v)[RB][4 * K], int kind, const BnArgs &a,
+                                          float2 (&mr)[RB]) {
     constexpr int P = 4 * K;
-    float m = 0.0f;
+    float2 m = make_float2(0.0f, 0.0f);
     if (kind == CONV_NORM_LAYER) {
-        float2 s = make_float2(0.0f, 0.0f);
+        m = mul2(sum(total(v[0]), RB > 1 ? total(v[RB - 1]) : 0.0f), both(a.inv_c));
 #pragma unroll
-        for (int i = 0; i < P; ++i) s = add2(s, v[i]);
-        m = sum(make_float2(s.x + s.y, 0.0f)).x * inv_c;
+        for (int b = 0; b < RB; ++b)
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            v[i].x = l.has(i, 0) ? v[i].x - m : 0.0f;
-            v[i].y = l.has(i, 1) ? v[i].y - m : 0.0f;
-        }
+            for (int i = 0; i < P; ++i) v[b][i] = add2(v[b][i], both(b ? -m.y : -m.x));
+        if (!a.full)
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    if (!l.has(i, 0)) v[b][i].x = 0.0f;
+                    if (!l.has(i, 1)) v[b][i].y = 0.0f;
+                }
     }
-    float2 q = make_float2(0.0f, 0.0f);
+    float q[RB];
 #pragma unroll
-    for (int i = 0; i < P; ++i) q = fma2(v[i], v[i], q);
-    const float r = 1.0f / sqrtf(sum(make_float2(q.x + q.y, 0.0f)).x * inv_c + eps);
+    for (int b = 0; b < RB; ++b) {
+        float2 s = mul2(v[b][0], v[b][0]);
 #pragma unroll
-    for (int i = 0; i < P; ++i) v[i] = mul2(v[i], both(r));
-    return make_float2(m, r);
+        for (int i = 1; i < P; ++i) s = fma2(v[b][i], v[b][i], s);
+        q[b] = s.x + s.y;
+    }
+    const float2 s = sum(q[0], RB > 1 ? q[RB - 1] : 0.0f);
+#pragma unroll
+    for (int b = 0; b < RB; ++b) {
+        const float r = __frsqrt_rn(fmaf(b ? s.y : s.x, a.inv_c, a.eps));
+        mr[b] = make_float2(b ? m.y : m.x, r);
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[b][i] = mul2(v[b][i], both(r));
+    }
 }
 
 // scale gate g1 and scale gate b1 at a thread's channels.
@@ -205,67 +252,107 @@ __device__ __forceinline__ void factors(const Lane<VEC, K> &l, const BnArgs &a, 
 }
 
 constexpr int kFwdStages = 3;
+constexpr int kFwdCtas = 2, kBwdCtas = 2;  // of 256 threads, a SM
 
-// y and z of a run of rows.
-template <typename T, int VEC, int K>
+// y and z of a run of rows, RB at a time.  ANY: the rows of a gated map that a
+// CTA takes may be of several images (RB = 1); otherwise a run is of one.
+template <typename T, int VEC, int K, int RB>
 __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_constant__ BnArgs a) {
     using R = Row<T, VEC, K>;
     using Raw = typename R::Raw;
-    constexpr int P = R::P, NV = R::NV, D = kFwdStages;
+    constexpr int P = R::P, NV = R::NV, D = kFwdStages, MAP = RB * NV;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float2 meet[2 * kMostThreads / 32];
+    __shared__ float meet[2 * kMostThreads / 32 * 2];
     const int nt = blockDim.x;
-    Raw *ring = reinterpret_cast<Raw *>(smem) + threadIdx.x;  // [D][2][NV][threads]
+    Raw *ring = reinterpret_cast<Raw *>(smem) + threadIdx.x;  // [D][2][RB][NV][threads]
     const Lane<VEC, K> l(a);
     RowSum sum(a.tpr, l.slot, meet);
-    const int r0 = blockIdx.x * a.run, r1 = min(a.rows, r0 + a.run);
-    const int iters = (r1 - r0 + a.slots - 1) / a.slots;
-    const T *x = static_cast<const T *>(a.x), *f = static_cast<const T *>(a.f);
+    const int n = RB > 1 ? blockIdx.x / a.S : 0, s0 = RB > 1 ? blockIdx.x - n * a.S : blockIdx.x;
+    const int span = RB > 1 && a.S < a.units ? a.HW : a.rows;
+    const int r0 = n * span + s0 * a.run, r1 = n * span + min(span, (s0 + 1) * a.run);
+    int row = r0 + l.slot, asked = row;
+    const bool block = a.f != nullptr;
+    const T *x = static_cast<const T *>(a.x) + row * a.px + l.first(0), *f = static_cast<const T *>(a.f) + row * a.pf + l.first(0);
+    T *y = static_cast<T *>(a.o0) + row * a.p0 + l.first(0), *z = static_cast<T *>(a.o1) + row * a.p1 + l.first(0);
+    const long long sx = a.slots * a.px, sf = a.slots * a.pf, sy = a.slots * a.p0, sz = a.slots * a.p1;
     pdl_trigger();
+    if (!a.full) R::template blank<D * 2 * RB>(l, ring, nt);
     pdl_wait();
-    auto ask = [&](int i) {
-        const int row = r0 + i * a.slots + l.slot;
-        if (row < r1) {
-            Raw *d = ring + (i % D) * (2 * NV) * nt;
-            R::ask(l, x + row * a.px, d, nt);
-            if (f) R::ask(l, f + row * a.pf, d + NV * nt, nt);
+    int to = 0, at = 0;
+    auto ask = [&] {
+        Raw *d = ring + to * (2 * MAP) * nt;
+#pragma unroll
+        for (int b = 0; b < RB; ++b, d += NV * nt) {
+            if (asked < r1) {
+                R::ask(l, x, d, nt);
+                if (block) R::ask(l, f, d + MAP * nt, nt);
+            }
+            asked += a.slots;
+            x += sx;
+            f += sf;
         }
         copy_commit();
+        if (++to == D) to = 0;
     };
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i) ask(i);
+    for (int i = 0; i < D - 1; ++i) ask();
     float2 q[P], p[P], g2[P], b2[P];
-    int image = a.gate ? -1 : 0;
-    if (f && !a.gate) factors(l, a, 0, q, p);
+    int image = n;
+    const bool by_row = RB == 1 && a.gate;
+    if (by_row) image = min(row, a.rows - 1) / a.HW;
+    if (block) factors(l, a, image, q, p);
     l.params(g2, a.g2, 1.0f);
     l.params(b2, a.b2, 0.0f);
-    for (int i = 0; i < iters; ++i) {
-        const int row = r0 + i * a.slots + l.slot;
-        const bool on = row < r1;
+    for (int base = r0; base < r1; base += a.slots * RB) {
         copy_wait<D - 2>();
-        const Raw *d = ring + (i % D) * (2 * NV) * nt;
-        float2 y[P], u[P];
-        R::get(l, d, nt, y);
-        if (f) R::get(l, d + NV * nt, nt, u);
-        ask(i + D - 1);
-        float2 one = make_float2(0.0f, 1.0f), two = one;
-        if (f) {
-            if (a.gate && on) {
-                const int n = row / a.HW;
-                if (n != image) factors(l, a, image = n, q, p);
-            }
-            if (a.post != CONV_NORM_NONE) one = normalise<VEC, K>(l, sum, u, a.post, a.inv_c, a.eps);
+        const Raw *d = ring + at * (2 * MAP) * nt;
+        float2 v[RB][P], u[RB][P];
 #pragma unroll
-            for (int k = 0; k < P; ++k) y[k] = fma2(q[k], u[k], add2(y[k], p[k]));
-            if (a.o0 && on) R::put(l, static_cast<T *>(a.o0) + row * a.p0, y);
+        for (int b = 0; b < RB; ++b) {
+            R::get(d + b * NV * nt, nt, v[b]);
+            if (block) R::get(d + (MAP + b * NV) * nt, nt, u[b]);
+        }
+        if (++at == D) at = 0;
+        ask();
+        float2 one[RB], two[RB];
+#pragma unroll
+        for (int b = 0; b < RB; ++b) one[b] = two[b] = make_float2(0.0f, 1.0f);
+        if (block) {
+            if (by_row && row < r1) {
+                const int k = row / a.HW;
+                if (k != image) factors(l, a, image = k, q, p);
+            }
+            if (a.post != CONV_NORM_NONE) normalise<VEC, K, RB>(l, sum, u, a.post, a, one);
+            if (a.b1)
+#pragma unroll
+                for (int b = 0; b < RB; ++b)
+#pragma unroll
+                    for (int i = 0; i < P; ++i) v[b][i] = add2(v[b][i], p[i]);
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+#pragma unroll
+                for (int i = 0; i < P; ++i) v[b][i] = fma2(q[i], u[b][i], v[b][i]);
+            if (a.o0)
+#pragma unroll
+                for (int b = 0; b < RB; ++b)
+                    if (row + b * a.slots < r1) R::put(l, y + b * sy, v[b]);
         }
         if (a.o1) {
-            two = normalise<VEC, K>(l, sum, y, a.pre, a.inv_c, a.eps);
+            normalise<VEC, K, RB>(l, sum, v, a.pre, a, two);
 #pragma unroll
-            for (int k = 0; k < P; ++k) y[k] = fma2(y[k], g2[k], b2[k]);
-            if (on) R::put(l, static_cast<T *>(a.o1) + row * a.p1, y);
+            for (int b = 0; b < RB; ++b) {
+#pragma unroll
+                for (int i = 0; i < P; ++i) v[b][i] = fma2(v[b][i], g2[i], b2[i]);
+                if (row + b * a.slots < r1) R::put(l, z + b * sz, v[b]);
+            }
         }
-        if (a.stats && on && l.t == 0) a.stats[row] = make_float4(one.x, one.y, two.x, two.y);
+        if (a.stats && l.t == 0)
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+                if (row + b * a.slots < r1) a.stats[row + b * a.slots] = make_float4(one[b].x, one[b].y, two[b].x, two[b].y);
+        row += RB * a.slots;
+        y += RB * sy;
+        z += RB * sz;
     }
     copy_wait<0>();
 }
@@ -313,20 +400,24 @@ __host__ __device__ constexpr int bwd_stages(int es, int k) { return k == 1 ? 3 
 
 // dx and df of the rows of a CTA's units, and the units' channel sums.
 template <typename T, int VEC, int K>
-__global__ void __launch_bounds__(K == 1 ? kThreads * 2 : kMostThreads) bn_bwd_kernel(const __grid_constant__ BnArgs a) {
+__global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_constant__ BnArgs a) {
     using R = Row<T, VEC, K>;
     using Raw = typename R::Raw;
     constexpr int P = R::P, NV = R::NV, D = bwd_stages(sizeof(T), K);
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float2 meet[2 * kMostThreads / 32];
+    __shared__ float meet[2 * kMostThreads / 32 * 2];
     const int nt = blockDim.x;
     Raw *ring = reinterpret_cast<Raw *>(smem) + threadIdx.x;  // [D][4][NV][threads]
     float *held = reinterpret_cast<float *>(smem + (size_t)D * 4 * NV * nt * sizeof(Raw));  // whole images: gate A, gate B [2][C]
     const Lane<VEC, K> l(a);
     RowSum sum(a.tpr, l.slot, meet);
-    const T *x = static_cast<const T *>(a.x), *f = static_cast<const T *>(a.f);
-    const T *dy = static_cast<const T *>(a.dy), *dz = static_cast<const T *>(a.dz);
+    const bool block = a.f != nullptr, stream = a.dy != nullptr, norm = a.dz != nullptr;
+    const long long sx = a.slots * a.px, sf = a.slots * a.pf, sdy = a.slots * a.pdy, sdz = a.slots * a.pdz;
+    const long long s0 = a.slots * a.p0, s1 = a.slots * a.p1;
     pdl_trigger();
+    if (a.whole)
+        for (int c = threadIdx.x; c < 2 * a.C; c += nt) held[c] = 0.0f;
+    __syncthreads();
     pdl_wait();
     float2 q[P], p[P], g2[P], acc[SUMS][P];
 #pragma unroll
@@ -334,79 +425,104 @@ __global__ void __launch_bounds__(K == 1 ? kThreads * 2 : kMostThreads) bn_bwd_k
 #pragma unroll
         for (int i = 0; i < P; ++i) acc[s][i] = make_float2(0.0f, 0.0f);
     l.params(g2, a.g2, 1.0f);
-    if (f && !a.gate) factors(l, a, 0, q, p);
-    if (a.whole) {
-        for (int c = threadIdx.x; c < 2 * a.C; c += nt) held[c] = 0.0f;
-        __syncthreads();
-    }
+    if (block && !a.gate) factors(l, a, 0, q, p);
     for (int unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
-        const int n = unit / a.S, s0 = unit - n * a.S;
+        const int n = unit / a.S, k0 = unit - n * a.S;
         const int span = a.gate ? a.HW : a.rows;
-        const int r0 = n * span + min(span, s0 * a.run), r1 = n * span + min(span, (s0 + 1) * a.run);
-        const int iters = (r1 - r0 + a.slots - 1) / a.slots;
-        auto ask = [&](int i) {
-            const int row = r0 + i * a.slots + l.slot;
-            if (row < r1) {
-                Raw *d = ring + (i % D) * (4 * NV) * nt;
-                R::ask(l, x + row * a.px, d, nt);
-                if (f) R::ask(l, f + row * a.pf, d + NV * nt, nt);
-                if (dy) R::ask(l, dy + row * a.pdy, d + 2 * NV * nt, nt);
-                if (dz) R::ask(l, dz + row * a.pdz, d + 3 * NV * nt, nt);
+        const int r0 = n * span + min(span, k0 * a.run), r1 = n * span + min(span, (k0 + 1) * a.run);
+        int row = r0 + l.slot, asked = row;
+        const T *x = static_cast<const T *>(a.x) + row * a.px + l.first(0), *f = static_cast<const T *>(a.f) + row * a.pf + l.first(0);
+        const T *dy = static_cast<const T *>(a.dy) + row * a.pdy + l.first(0), *dz = static_cast<const T *>(a.dz) + row * a.pdz + l.first(0);
+        T *dx = static_cast<T *>(a.o0) + row * a.p0 + l.first(0), *df = static_cast<T *>(a.o1) + row * a.p1 + l.first(0);
+        if (!a.full) R::template blank<D * 4>(l, ring, nt);  // (the sums were there between units)
+        int to = 0, at = 0;
+        // A row beyond the run counts as zeros.
+        auto ask = [&] {
+            Raw *d = ring + to * (4 * NV) * nt;
+            if (asked < r1) {
+                R::ask(l, x, d, nt);
+                if (block) R::ask(l, f, d + NV * nt, nt);
+                if (stream) R::ask(l, dy, d + 2 * NV * nt, nt);
+                if (norm) R::ask(l, dz, d + 3 * NV * nt, nt);
+            } else {
+#pragma unroll
+                for (int m = 0; m < 4; ++m) R::zero(d + m * NV * nt, nt);
             }
             copy_commit();
+            asked += a.slots;
+            x += sx;
+            f += sf;
+            dy += sdy;
+            dz += sdz;
+            if (++to == D) to = 0;
         };
 #pragma unroll
-        for (int i = 0; i < (D > 1 ? D - 1 : 1); ++i) ask(i);
-        if (f && a.gate) factors(l, a, n, q, p);
-        for (int i = 0; i < iters; ++i) {
-            const int row = r0 + i * a.slots + l.slot;
+        for (int i = 0; i < (D > 1 ? D - 1 : 1); ++i) ask();
+        auto statistics = [&](int r) { return r < r1 ? a.stats[r] : make_float4(0.0f, 0.0f, 0.0f, 0.0f); };
+        float4 st = statistics(row);
+        if (block && a.gate) factors(l, a, n, q, p);
+        for (int base = r0; base < r1; base += a.slots) {
             const bool on = row < r1;
-            const float4 st = on ? a.stats[row] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             copy_wait<(D > 1 ? D - 2 : 0)>();
-            const Raw *d = ring + (i % D) * (4 * NV) * nt;
+            const Raw *d = ring + at * (4 * NV) * nt;
+            if (++at == D) at = 0;
             float2 u[P], y[P], t[P];  // u^, y^, dY
-            R::get(l, d, nt, y);
-            if (f) R::get(l, d + NV * nt, nt, u);
-            if (dy) R::get(l, d + 2 * NV * nt, nt, t);
+            R::get(d, nt, y);
+            if (block) {
+                R::get(d + NV * nt, nt, u);
+                const float2 r = both(st.y), c = both(-st.x * st.y);
+                if (a.b1)
+#pragma unroll
+                    for (int k = 0; k < P; ++k) y[k] = add2(y[k], p[k]);
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    u[k] = fma2(u[k], r, c);
+                    y[k] = fma2(q[k], u[k], y[k]);
+                }
+            }
+            if (stream) R::get(d + 2 * NV * nt, nt, t);
             else
 #pragma unroll
                 for (int k = 0; k < P; ++k) t[k] = make_float2(0.0f, 0.0f);
-            if (f)
-#pragma unroll
-                for (int k = 0; k < P; ++k) {
-                    u[k] = mul2(add2(u[k], both(-st.x)), both(st.y));
-                    y[k] = fma2(q[k], u[k], add2(y[k], p[k]));
-                }
-            if (dz) {
+            if (norm) {
                 float2 e[P], w = make_float2(0.0f, 0.0f), v = w;
-                R::get(l, d + 3 * NV * nt, nt, e);
+                R::get(d + 3 * NV * nt, nt, e);
+                const float2 r = both(st.w), c = both(-st.z * st.w);
+                if (a.db2)
+#pragma unroll
+                    for (int k = 0; k < P; ++k) acc[SUM_B2][k] = add2(acc[SUM_B2][k], e[k]);
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
-                    y[k] = mul2(add2(y[k], both(-st.z)), both(st.w));
-                    if (on) {
-                        acc[SUM_G2][k] = fma2(e[k], y[k], acc[SUM_G2][k]);
-                        acc[SUM_B2][k] = add2(acc[SUM_B2][k], e[k]);
-                    }
+                    y[k] = fma2(y[k], r, c);
+                    acc[SUM_G2][k] = fma2(e[k], y[k], acc[SUM_G2][k]);
                     e[k] = mul2(e[k], g2[k]);
                     w = add2(w, e[k]);
                     v = fma2(e[k], y[k], v);
                 }
-                const float2 s = sum(make_float2(w.x + w.y, v.x + v.y));
-                const float m = a.pre == CONV_NORM_LAYER ? -s.x * a.inv_c : 0.0f, my = -s.y * a.inv_c;
+                const float2 s = sum(w.x + w.y, v.x + v.y);
+                const float2 my = both(-s.y * a.inv_c * st.w);
+                if (a.pre == CONV_NORM_LAYER) {
+                    const float2 m = both(-s.x * a.inv_c * st.w);
 #pragma unroll
-                for (int k = 0; k < P; ++k) t[k] = fma2(fma2(y[k], both(my), add2(e[k], both(m))), both(st.w), t[k]);
+                    for (int k = 0; k < P; ++k) t[k] = add2(t[k], m);
+                }
+#pragma unroll
+                for (int k = 0; k < P; ++k) t[k] = fma2(y[k], my, fma2(e[k], r, t[k]));
             }
-            if (D > 1) ask(i + D - 1);
-            if (on) R::put(l, static_cast<T *>(a.o0) + row * a.p0, t);
-            if (f) {
-                if (on)
+            if (D > 1) ask();
+            const float4 now = st;
+            st = statistics(row + a.slots);
+            if (on) R::put(l, dx, t);
+            if (block) {
+                // (what the mean's terms leave in a row beyond the run is 0: its sums are)
+                if (a.want_b)
 #pragma unroll
-                    for (int k = 0; k < P; ++k) {
-                        acc[SUM_A][k] = fma2(t[k], u[k], acc[SUM_A][k]);
-                        acc[SUM_B][k] = add2(acc[SUM_B][k], t[k]);
-                    }
+                    for (int k = 0; k < P; ++k) acc[SUM_B][k] = add2(acc[SUM_B][k], t[k]);
 #pragma unroll
-                for (int k = 0; k < P; ++k) t[k] = mul2(t[k], q[k]);
+                for (int k = 0; k < P; ++k) {
+                    acc[SUM_A][k] = fma2(t[k], u[k], acc[SUM_A][k]);
+                    t[k] = mul2(t[k], q[k]);
+                }
                 if (a.post != CONV_NORM_NONE) {
                     float2 w = make_float2(0.0f, 0.0f), v = w;
 #pragma unroll
@@ -414,14 +530,18 @@ __global__ void __launch_bounds__(K == 1 ? kThreads * 2 : kMostThreads) bn_bwd_k
                         w = add2(w, t[k]);
                         v = fma2(t[k], u[k], v);
                     }
-                    const float2 s = sum(make_float2(w.x + w.y, v.x + v.y));
-                    const float m = a.post == CONV_NORM_LAYER ? -s.x * a.inv_c : 0.0f, mu = -s.y * a.inv_c;
+                    const float2 s = sum(w.x + w.y, v.x + v.y);
+                    const float2 r = both(now.y), mu = both(-s.y * a.inv_c * now.y);
+                    const float2 m = both(a.post == CONV_NORM_LAYER ? -s.x * a.inv_c * now.y : 0.0f);
 #pragma unroll
-                    for (int k = 0; k < P; ++k) t[k] = mul2(fma2(u[k], both(mu), add2(t[k], both(m))), both(st.y));
+                    for (int k = 0; k < P; ++k) t[k] = fma2(u[k], mu, fma2(t[k], r, m));
                 }
-                if (on) R::put(l, static_cast<T *>(a.o1) + row * a.p1, t);
+                if (on) R::put(l, df, t);
             }
-            if (D == 1) ask(i + 1);
+            if (D == 1) ask();
+            row += a.slots;
+            dx += s0;
+            df += s1;
         }
         copy_wait<0>();
         float2 *ent = reinterpret_cast<float2 *>(smem);
@@ -518,15 +638,17 @@ __global__ void __launch_bounds__(kJoin) bn_join_kernel(const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ host side
+// (rb: rows at a time of the forward kernel, 0: the gradient)
 template <typename T, int VEC>
-const void *pick_k(bool bwd, int k) {
-    if (bwd) return k == 1 ? (const void *)&bn_bwd_kernel<T, VEC, 1> : (const void *)&bn_bwd_kernel<T, VEC, 2>;
-    return k == 1 ? (const void *)&bn_fwd_kernel<T, VEC, 1> : (const void *)&bn_fwd_kernel<T, VEC, 2>;
+const void *pick_k(int k, int rb) {
+    if (rb == 0) return k == 1 ? (const void *)&bn_bwd_kernel<T, VEC, 1> : (const void *)&bn_bwd_kernel<T, VEC, 2>;
+    if (rb == 2) return (const void *)&bn_fwd_kernel<T, VEC, 1, 2>;
+    return k == 1 ? (const void *)&bn_fwd_kernel<T, VEC, 1, 1> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1>;
 }
-const void *pick_kernel(bool bwd, conv_dtype_t dt, int vec, int k) {
-    if (dt == CONV_F32) return vec == 4 ? pick_k<float, 4>(bwd, k) : pick_k<float, 1>(bwd, k);
-    return vec == 8 ? pick_k<__nv_bfloat16, 8>(bwd, k)
-                    : (vec == 2 ? pick_k<__nv_bfloat16, 2>(bwd, k) : pick_k<__nv_bfloat16, 1>(bwd, k));
+const void *pick_kernel(conv_dtype_t dt, int vec, int k, int rb) {
+    if (dt == CONV_F32) return vec == 4 ? pick_k<float, 4>(k, rb) : pick_k<float, 1>(k, rb);
+    return vec == 8 ? pick_k<__nv_bfloat16, 8>(k, rb)
+                    : (vec == 2 ? pick_k<__nv_bfloat16, 2>(k, rb) : pick_k<__nv_bfloat16, 1>(k, rb));
 }
 
 // Channels a vector access takes: the widest that the channel count, every
@@ -549,18 +671,19 @@ int vec_for(const conv_plan *p, const Map (&maps)[N]) {
 // rows side by side have k = 1, so that it has 96 elements a thread where the
 // sums are SUMS * 8 in fp32.)
 static_assert(3 * 4 * 8 * 2 >= SUMS * 8 * 4, "");
-size_t ring_bytes(const BnGeom &g, int es, bool bwd) {
-    return (size_t)(bwd ? 4 * bwd_stages(es, g.k) : 2 * kFwdStages) * g.threads * 8 * g.k * es;
+size_t ring_bytes(const BnGeom &g, int es, int rb) {
+    return (size_t)(rb == 0 ? 4 * bwd_stages(es, g.k) : 2 * kFwdStages * rb) * g.threads * 8 * g.k * es;
 }
 
-cudaError_t launch(const conv_plan *p, bool bwd, int vec, BnArgs &a, int grid, size_t smem, cudaStream_t st) {
-    const void *k = pick_kernel(bwd, p->dtype, vec, p->bn.k);
+cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a, size_t smem, cudaStream_t st) {
+    const void *k = pick_kernel(p->dtype, vec, p->bn.k, d.rb);
     if (smem > 40 * 1024) {  // (with the kernel's static shared memory: 48 KB are free)
         const int rc = conv_grant_smem_once(k, p->device, (int)smem);
         if (rc != CONV_OK) return cudaErrorInvalidValue;
     }
+    a.run = d.run; a.S = d.S; a.units = d.units; a.whole = d.whole;
     void *args[] = {&a};
-    return conv_launch(k, dim3((unsigned)grid), dim3((unsigned)p->bn.threads), args, smem, st);
+    return conv_launch(k, dim3((unsigned)d.grid), dim3((unsigned)p->bn.threads), args, smem, st);
 }
 
 int check_map(const conv_plan *p, const void *t, int64_t *pitch) {
@@ -603,6 +726,33 @@ bool shared(const Map (&in)[M], const Map (&out)[W], const Small (&small_in)[I],
 }
 bool bad_f32(const void *t) { return t && ((uintptr_t)t & 3u); }
 
+long long up(long long a, long long b) { return (a + b - 1) / b; }
+
+// All rows in runs of whole sets of rows side by side, one wave of CTAs.
+void divide_rows(BnGeom::Part &d, long long rows, long long set, long long wave) {
+    long long run = up(up(rows, wave), set) * set;
+    if (run < set) run = set;
+    d.run = (int)run;
+    d.S = d.units = d.grid = (int)up(rows, run);
+    d.whole = 0;
+}
+// Each image in runs of whole sets, as many as fill the CTAs best: a run costs
+// its sets and about four more for its start and end.
+void divide_images(BnGeom::Part &d, long long N, long long HW, long long set, long long wave) {
+    long long best = -1;
+    for (long long S = 1; S <= 1024; ++S) {
+        const long long sets = up(up(HW, S), set);
+        if (S > 1 && up(HW, sets * set) != S) continue;
+        const long long cost = up(N * S, wave) * (sets + 4);
+        if (best >= 0 && cost >= best) continue;
+        best = cost;
+        d.S = (int)S;
+        d.run = (int)(S == 1 ? HW : sets * set);
+    }
+    d.units = d.grid = (int)(N * d.S);
+    d.whole = 0;
+}
+
 // Threads of a row, rows of a CTA, and how the rows are divided.
 void plan_geometry(conv_plan *p) {
     BnGeom &g = p->bn;
@@ -615,48 +765,33 @@ void plan_geometry(conv_plan *p) {
     g.tpr = tpr;
     g.slots = tpr <= kThreads ? kThreads / tpr : 1;
     g.threads = g.tpr * g.slots;
-    const long long rows = (long long)p->s.n * p->s.h * p->s.w;
-    auto per_sm = [&](size_t smem, int most) {
-        int n = (int)((size_t)(220 * 1024) / (smem + 1024));
-        if (n > most) n = most;
-        return n < 1 ? 1 : n;
+    g.full = C == tpr * 8 * g.k;
+    const long long N = p->s.n, HW = (long long)p->s.h * p->s.w, rows = N * HW;
+    p->ws_bytes = p->ws_bwd_bytes = 0;
+    if (rows == 0) return;
+    auto wave = [&](int rb, int most) {
+        int n = (int)((size_t)(220 * 1024) / (ring_bytes(g, es, rb) + 1024));
+        if (n > most * kThreads / g.threads) n = most * kThreads / g.threads;
+        return (long long)p->num_sms * (n < 1 ? 1 : n);
     };
-    const int regs = 512 * 128 / (g.threads * 128);  // CTAs a SM of 128 registers a thread
-    const long long fwd = (long long)p->num_sms * per_sm(ring_bytes(g, es, false), regs > 4 ? 4 : regs);
-    const long long bwd = (long long)p->num_sms * per_sm(ring_bytes(g, es, true), regs > 2 ? 2 : regs);
-    auto up = [](long long a, long long b) { return (a + b - 1) / b; };
-    // forward: runs of whole sets of rows side by side, one wave of CTAs
-    long long run = up(up(rows, fwd), g.slots) * g.slots;
-    if (run < g.slots) run = g.slots;
-    g.run = (int)run;
-    g.grid = (int)up(rows, run);
-    // gradient without a gate: the same over all rows
-    run = up(up(rows, bwd), g.slots) * g.slots;
-    if (run < g.slots) run = g.slots;
-    g.open.run = (int)run;
-    g.open.S = g.open.units = g.open.grid = (int)up(rows, run);
-    g.open.whole = 0;
-    // with one: whole images, or runs of an image where that leaves SMs idle.
-    // A run costs its sets of rows and about four more for its start and end.
-    const long long N = p->s.n, HW = (long long)p->s.h * p->s.w;
-    long long best = -1;
-    for (int S = 1; S <= 1024 && N > 0; ++S) {
-        const long long sets = up(up(HW, S), g.slots);
-        if (S > 1 && up(HW, sets * g.slots) != S) continue;
-        const long long cost = up(N * S, bwd) * (sets + 4);
-        if (best < 0 || cost < best) {
-            best = cost;
-            g.gated.S = S;
-            g.gated.run = (int)(S == 1 ? HW : sets * g.slots);
+    // two rows at a time where a CTA takes more than one set of rows
+    g.fwd.rb = g.k == 1 && rows > (long long)p->num_sms * g.slots ? 2 : 1;
+    divide_rows(g.fwd, rows, (long long)g.slots * g.fwd.rb, wave(g.fwd.rb, kFwdCtas));
+    g.fwd_gated = g.fwd;
+    if (g.fwd.rb == 2) {
+        if (HW >= 4LL * g.slots) divide_images(g.fwd_gated, N, HW, 2LL * g.slots, wave(2, kFwdCtas));
+        else {
+            g.fwd_gated.rb = 1;
+            divide_rows(g.fwd_gated, rows, g.slots, wave(1, kFwdCtas));
         }
     }
-    if (N > 0) {
-        g.gated.units = (int)(N * g.gated.S);
-        g.gated.whole = g.gated.S == 1;
-        g.gated.grid = (int)(g.gated.whole && N > bwd ? bwd : g.gated.units);
-    }
-    const long long parts = g.open.grid > g.gated.grid ? g.open.grid : g.gated.grid;
-    p->ws_bytes = 0;
+    g.bwd.rb = g.bwd_gated.rb = 0;
+    const long long w = wave(0, kBwdCtas);
+    divide_rows(g.bwd, rows, g.slots, w);
+    divide_images(g.bwd_gated, N, HW, g.slots, w);
+    g.bwd_gated.whole = g.bwd_gated.S == 1;
+    if (g.bwd_gated.whole && N > w) g.bwd_gated.grid = (int)w;
+    const long long parts = g.bwd.grid > g.bwd_gated.grid ? g.bwd.grid : g.bwd_gated.grid;
     p->ws_bwd_bytes = (size_t)parts * SUMS * C * 4;
 }
 
@@ -688,8 +823,8 @@ extern "C" int conv_plan_create_blocknorm(int32_t n, int32_t h, int32_t w, int32
     plan_geometry(p);
     static const char *const names[] = {"none", "layer", "rms"};
     snprintf(p->desc, sizeof(p->desc), "blocknorm %s post=%s pre=%s threads=%dx%d channels/thread=%d ctas=%d gradient: %d, gated %d in %d",
-             dtype == CONV_F32 ? "f32" : "bf16", names[post], names[pre], p->bn.slots, p->bn.tpr, 8 * p->bn.k, p->bn.grid,
-             p->bn.open.grid, p->bn.gated.units, p->bn.gated.grid);
+             dtype == CONV_F32 ? "f32" : "bf16", names[post], names[pre], p->bn.slots, p->bn.tpr, 8 * p->bn.k, p->bn.fwd.grid,
+             p->bn.bwd.grid, p->bn.bwd_gated.units, p->bn.bwd_gated.grid);
     *out_plan = p;
     return CONV_OK;
 }
@@ -702,7 +837,7 @@ BnArgs base_args(const conv_plan *p, const conv_blocknorm_params_t &w, const voi
     a.eps = p->bn.eps; a.inv_c = 1.0f / (float)p->s.c_in;
     a.N = p->s.n; a.HW = p->s.h * p->s.w; a.rows = a.N * a.HW; a.C = p->s.c_in;
     a.post = p->bn.post; a.pre = p->bn.pre;
-    a.tpr = p->bn.tpr; a.slots = p->bn.slots;
+    a.tpr = p->bn.tpr; a.slots = p->bn.slots; a.full = p->bn.full;
     return a;
 }
 int check_params(const conv_plan *p, const conv_blocknorm_params_t &w, const void *f) {
@@ -744,10 +879,9 @@ extern "C" int conv_run_blocknorm(const conv_plan_t *plan, const void *x, int64_
     BnArgs a = base_args(p, w, x, x_pitch, f, f_pitch);
     a.o0 = y; a.p0 = y_pitch; a.o1 = z; a.p1 = z_pitch;
     a.stats = reinterpret_cast<float4 *>(stats);
-    a.run = p->bn.run;
     const Map all[4] = {in[0], in[1], out[0], out[1]};
-    return launch(p, false, vec_for(p, all), a, p->bn.grid, ring_bytes(p->bn, es, false), (cudaStream_t)stream) == cudaSuccess
-               ? CONV_OK : CONV_ERR_CUDA;
+    const BnGeom::Part &g = w.gate ? p->bn.fwd_gated : p->bn.fwd;
+    return launch(p, g, vec_for(p, all), a, ring_bytes(p->bn, es, g.rb), (cudaStream_t)stream) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }
 
 extern "C" int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, int64_t x_pitch, const void *f, int64_t f_pitch,
@@ -801,11 +935,11 @@ extern "C" int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, in
     a.stats = reinterpret_cast<float4 *>(const_cast<float *>(stats));
     a.part = static_cast<float *>(workspace);
     a.dscale = d.scale; a.dgate = d.gate; a.dg1 = d.post_gamma; a.db1 = d.post_beta; a.dg2 = d.pre_gamma; a.db2 = d.pre_beta;
-    const BnGeom::Bwd &g = w.gate ? p->bn.gated : p->bn.open;
-    a.run = g.run; a.S = g.S; a.units = g.units; a.whole = g.whole;
+    a.want_b = d.post_beta || (w.post_beta && (d.scale || d.gate));
+    const BnGeom::Part &g = w.gate ? p->bn.bwd_gated : p->bn.bwd;
     const Map all[6] = {in[0], in[1], in[2], in[3], out[0], out[1]};
-    const size_t smem = ring_bytes(p->bn, es, true) + (g.whole ? 2 * cb : 0);
-    if (launch(p, true, vec_for(p, all), a, g.grid, smem, st) != cudaSuccess) return CONV_ERR_CUDA;
+    const size_t smem = ring_bytes(p->bn, es, 0) + (g.whole ? 2 * cb : 0);
+    if (launch(p, g, vec_for(p, all), a, smem, st) != cudaSuccess) return CONV_ERR_CUDA;
     const bool sums = d.scale || d.post_gamma || d.post_beta || d.pre_gamma || d.pre_beta, images = d.gate && !g.whole;
     if (!sums && !images) return CONV_OK;
     int parts = g.grid;

@@ -46,8 +46,8 @@ struct ClipGeom {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCtas = 4;          // a SM
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kCtas = 2;          // a SM
 constexpr int kItem = 4096;       // elements of an item, at most
 constexpr int kItemLeast = 256;   // ... and at least, but for a tensor's end: a vector a lane
 constexpr int kMostTensors = 1900;  // of a launch: their addresses are kernel parameters (32 KB at most)
@@ -129,17 +129,6 @@ __device__ __forceinline__ double warp_sum64(double v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-// The sum of the CTA's threads' values, to all of them.
-__device__ __forceinline__ double cta_sum(double v, double *red) {
-    v = warp_sum64(v);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    double s = 0.0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += red[w];
-    return s;
-}
-
 template <int M>
 __global__ void __launch_bounds__(kThreads, kCtas) clip_norm_kernel(const __grid_constant__ Tensors<M> t, const uint4 *items,
                                                                     const int *first, double *part) {
@@ -159,8 +148,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) clip_norm_kernel(const __grid
         if (now.x >> 31) s += item_sum(static_cast<const float *>(p) + at, (int)now.y);
         else s += item_sum(static_cast<const __nv_bfloat16 *>(p) + at, (int)now.y);
     }
-    s = cta_sum(s, red);
-    if (threadIdx.x == 0) part[blockIdx.x] = s;
+    s = warp_sum64(s);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        s = warp_sum64(threadIdx.x < kWarps ? red[threadIdx.x] : 0.0);
+        if (threadIdx.x == 0) part[blockIdx.x] = s;
+    }
 }
 
 template <typename T>
@@ -196,24 +190,39 @@ __device__ __forceinline__ void scale_item(const T *p, T *q, int n, float k) {
     }
 }
 
+// The root of a sum in fp32, off by a rounding and a half: s = m 4^e with m in
+// [1, 4).  (fp64 has a root of its own, some forty instructions on a unit that
+// takes sixteen clocks for each: with it and a division in every warp the second
+// launch took 12 us where nothing was to be clipped.)
+__device__ __forceinline__ float root32(double s) {
+    const int high = __double2hiint(s), e = (high >> 20) - 1023;
+    if (s == 0.0 || e >= 1024) return (float)s;  // (infinite or NaN)
+    const double m = __hiloint2double((high & 0xfffff) | (1023 + (e & 1)) << 20, __double2loint(s));
+    return scalbnf(sqrtf((float)m), (e - (e & 1)) / 2);
+}
+
 // in place: outs are the gradients, which stay as they are where k = 1.
 template <int M>
 __global__ void __launch_bounds__(kThreads, kCtas) clip_scale_kernel(const __grid_constant__ Tensors<M> t,
                                                                      const __grid_constant__ Tensors<M> o, const uint4 *items,
                                                                      const int *first, const double *part, int parts,
                                                                      float max_norm, float *norm, int in_place) {
-    __shared__ double red[kWarps];
+    __shared__ float factor;
     pdl_trigger();
     const int start = first[blockIdx.x];
     int i = first[blockIdx.x + 1] - 1 - (int)(threadIdx.x >> 5);  // from the end: what the first launch left in L2
     pdl_wait();
-    double s = 0.0;
-    for (int j = threadIdx.x; j < parts; j += kThreads) s += part[j];
-    const double root = sqrt(cta_sum(s, red));
-    const float whole = (float)root;
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = whole;
-    float k = 1.0f;
-    if (isfinite(whole)) k = fminf(1.0f, (float)((double)max_norm / (root + 1e-6)));
+    if (threadIdx.x < 32) {
+        double s = 0.0;
+        for (int j = threadIdx.x; j < parts; j += 32) s += part[j];
+        const float whole = root32(warp_sum64(s));
+        if (threadIdx.x == 0) {
+            factor = isfinite(whole) ? fminf(1.0f, max_norm / (whole + 1e-6f)) : 1.0f;
+            if (norm && blockIdx.x == 0) *norm = whole;
+        }
+    }
+    __syncthreads();
+    const float k = factor;
     if (in_place && k == 1.0f) return;
     for (; i >= start; i -= kWarps) {
         const uint4 now = items[i];

@@ -1,10 +1,10 @@
 """The global gradient norm and clipping against 64 bits.
 
-The norm: squares in fp32 (2^-24 each), up to 160 of them summed by a lane, then
-fp64: the sum is off by at most 161 u of itself, its root by half of that, and
-the result's rounding adds one: 82 u, u = 2^-24.  The factor follows the norm
-before its rounding (81 u and its own rounding), a product rounds once more, and
-a bf16 result by 2^-8: 83 u + 2^-8 of an element."""
+The norm: a lane sums up to 160 squares of an item in four chains of fp32
+multiply-adds, at most 40 roundings one after another and two to join them, then
+fp64: the sum is off by at most 43 u of itself, u = 2^-24, its root by half of
+that and two roundings, 24 u; allowed are 82 u.  The factor adds two roundings,
+a product one, 27 u (allowed 83 u), and a bf16 result 2^-8 of an element."""
 import math
 
 import pytest
