@@ -99,15 +99,16 @@ struct XentGeom {
     int dx_split, dx_kper, dw_split, dw_kper;
 };
 
-// Norms around a block: threads of a row, rows side by side, k times 8 channels
-// a thread.  How each direction divides the rows, without a gate and with one:
-// units of `run` rows, S an image (or of all rows); rb rows at a time (0: the
-// gradient); whole: a unit is an image.
+// Norms around a block: threads of a row, k times 8 channels a thread (full: all
+// of them in the row).  How each direction divides the rows, without a gate and
+// with one: rows side by side in a CTA and rb of them at a time in a thread (0:
+// the gradient), units of `run` rows, S an image (or of all rows); whole: a unit
+// is an image.
 struct BnGeom {
     int post, pre;
     float eps;
-    int k, tpr, slots, threads, full;
-    struct Part { int rb, run, S, units, grid, whole; } fwd, fwd_gated, bwd, bwd_gated;
+    int k, tpr, full;
+    struct Part { int rb, slots, threads, run, S, units, grid, whole; } fwd, fwd_gated, bwd, bwd_gated;
 };
 
 struct ClipGeom;  // gradient norm and clipping (k_gradclip.cu)

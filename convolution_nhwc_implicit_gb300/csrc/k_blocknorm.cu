@@ -41,8 +41,8 @@ using namespace convk;
 namespace {
 
 constexpr int kMaxC = 8192;        // channels: 512 threads of 16
-constexpr int kThreads = 256;      // of a CTA whose rows take no more
-constexpr int kMostThreads = 512;  // of a row
+constexpr int kThreads = 256;      // of a forward CTA whose rows take no more
+constexpr int kMostThreads = 512;  // of a row, and of the gradient's CTAs
 enum { SUM_A, SUM_B, SUM_G2, SUM_B2, SUMS };
 
 struct BnArgs {
@@ -54,7 +54,7 @@ struct BnArgs {
     float *part;                   // gradient: [units or CTAs][SUMS][C]
     float *dscale, *dgate, *dg1, *db1, *dg2, *db2;
     float eps, inv_c;
-    int rows, HW, C, N;
+    int rows, HW, C, Cp, N;        // Cp: C in whole fours, of the workspace
     int post, pre;                 // conv_norm_t
     int tpr, slots, full;          // threads of a row, rows side by side; full: every thread has channels, all of them
     int run, S, units;             // rows of a unit, units an image (of all rows without a gate), units in all
@@ -83,6 +83,16 @@ struct Lane {
     }
     // src at the thread's channels (null: `other`), 0 beyond the row's end
     __device__ __forceinline__ void params(float2 (&v)[P], const float *src, float other) const {
+        constexpr int W = VEC % 4 == 0 ? 4 : 1;
+        if (W == 4 && src && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+                const float4 f = has(i, 0) ? *reinterpret_cast<const float4 *>(src + chan(i, 0)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                v[i] = make_float2(f.x, f.y);
+                v[i + 1] = make_float2(f.z, f.w);
+            }
+            return;
+        }
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             v[i].x = has(i, 0) ? (src ? src[chan(i, 0)] : other) : 0.0f;
@@ -99,7 +109,12 @@ struct Row {
     using Raw = typename V::Raw;
     using L = Lane<VEC, K>;
     static constexpr int NV = L::NV, P = L::P;
-    __device__ static __forceinline__ void get(const Raw *src, int step, float2 (&f)[P]) {
+    static constexpr int step = 32;  // of a thread's vectors in the ring: a warp's lie together
+    // the thread's first vector in a ring of `rows` rows
+    __device__ static __forceinline__ Raw *ring(uint8_t *smem, int rows) {
+        return reinterpret_cast<Raw *>(smem) + (threadIdx.x >> 5) * (rows * NV * step) + (threadIdx.x & 31);
+    }
+    __device__ static __forceinline__ void get(const Raw *src, float2 (&f)[P]) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             float2 one[V::kPairs];
@@ -126,20 +141,20 @@ struct Row {
             if (l.on(v)) *reinterpret_cast<Raw *>(row + v * l.tpr * VEC) = V::pack(one);
         }
     }
-    __device__ static __forceinline__ void ask(const L &l, const T *row, Raw *dst, int step) {
+    __device__ static __forceinline__ void ask(const L &l, const T *row, Raw *dst) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
             if (l.on(v)) copy_vec(dst + v * step, reinterpret_cast<const Raw *>(row + v * l.tpr * VEC));
     }
     // the vectors beyond the row's end in `rows` rows of the ring
     template <int ROWS>
-    __device__ static __forceinline__ void blank(const L &l, Raw *dst, int step) {
+    __device__ static __forceinline__ void blank(const L &l, Raw *dst) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
             if (!l.on(v))
                 for (int i = 0; i < ROWS; ++i) dst[(i * NV + v) * step] = Raw{};
     }
-    __device__ static __forceinline__ void zero(Raw *dst, int step) {
+    __device__ static __forceinline__ void zero(Raw *dst) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) dst[v * step] = Raw{};
     }
@@ -252,7 +267,6 @@ __device__ __forceinline__ void factors(const Lane<VEC, K> &l, const BnArgs &a, 
 }
 
 constexpr int kFwdStages = 3;
-constexpr int kFwdCtas = 2, kBwdCtas = 2;  // of 256 threads, a SM
 
 // y and z of a run of rows, RB at a time.  ANY: the rows of a gated map that a
 // CTA takes may be of several images (RB = 1); otherwise a run is of one.
@@ -260,11 +274,10 @@ template <typename T, int VEC, int K, int RB>
 __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_constant__ BnArgs a) {
     using R = Row<T, VEC, K>;
     using Raw = typename R::Raw;
-    constexpr int P = R::P, NV = R::NV, D = kFwdStages, MAP = RB * NV;
+    constexpr int P = R::P, D = kFwdStages, ROW = R::NV * R::step, STAGE = 2 * RB * ROW;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float meet[2 * kMostThreads / 32 * 2];
-    const int nt = blockDim.x;
-    Raw *ring = reinterpret_cast<Raw *>(smem) + threadIdx.x;  // [D][2][RB][NV][threads]
+    Raw *ring = R::ring(smem, D * 2 * RB);  // [D][x, f][RB]
     const Lane<VEC, K> l(a);
     RowSum sum(a.tpr, l.slot, meet);
     const int n = RB > 1 ? blockIdx.x / a.S : 0, s0 = RB > 1 ? blockIdx.x - n * a.S : blockIdx.x;
@@ -276,23 +289,23 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
     T *y = static_cast<T *>(a.o0) + row * a.p0 + l.first(0), *z = static_cast<T *>(a.o1) + row * a.p1 + l.first(0);
     const long long sx = a.slots * a.px, sf = a.slots * a.pf, sy = a.slots * a.p0, sz = a.slots * a.p1;
     pdl_trigger();
-    if (!a.full) R::template blank<D * 2 * RB>(l, ring, nt);
+    if (!a.full) R::template blank<D * 2 * RB>(l, ring);
     pdl_wait();
-    int to = 0, at = 0;
+    const Raw *d = ring;
+    Raw *to = ring;
     auto ask = [&] {
-        Raw *d = ring + to * (2 * MAP) * nt;
 #pragma unroll
-        for (int b = 0; b < RB; ++b, d += NV * nt) {
+        for (int b = 0; b < RB; ++b) {
             if (asked < r1) {
-                R::ask(l, x, d, nt);
-                if (block) R::ask(l, f, d + MAP * nt, nt);
+                R::ask(l, x, to + b * ROW);
+                if (block) R::ask(l, f, to + (RB + b) * ROW);
             }
             asked += a.slots;
             x += sx;
             f += sf;
         }
         copy_commit();
-        if (++to == D) to = 0;
+        to = to == ring + (D - 1) * STAGE ? ring : to + STAGE;
     };
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) ask();
@@ -305,14 +318,13 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
     l.params(b2, a.b2, 0.0f);
     for (int base = r0; base < r1; base += a.slots * RB) {
         copy_wait<D - 2>();
-        const Raw *d = ring + at * (2 * MAP) * nt;
         float2 v[RB][P], u[RB][P];
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-            R::get(d + b * NV * nt, nt, v[b]);
-            if (block) R::get(d + (MAP + b * NV) * nt, nt, u[b]);
+            R::get(d + b * ROW, v[b]);
+            if (block) R::get(d + (RB + b) * ROW, u[b]);
         }
-        if (++at == D) at = 0;
+        d = d == ring + (D - 1) * STAGE ? ring : d + STAGE;
         ask();
         float2 one[RB], two[RB];
 #pragma unroll
@@ -403,12 +415,12 @@ template <typename T, int VEC, int K>
 __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_constant__ BnArgs a) {
     using R = Row<T, VEC, K>;
     using Raw = typename R::Raw;
-    constexpr int P = R::P, NV = R::NV, D = bwd_stages(sizeof(T), K);
+    constexpr int P = R::P, D = bwd_stages(sizeof(T), K), ROW = R::NV * R::step, STAGE = 4 * ROW;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float meet[2 * kMostThreads / 32 * 2];
     const int nt = blockDim.x;
-    Raw *ring = reinterpret_cast<Raw *>(smem) + threadIdx.x;  // [D][4][NV][threads]
-    float *held = reinterpret_cast<float *>(smem + (size_t)D * 4 * NV * nt * sizeof(Raw));  // whole images: gate A, gate B [2][C]
+    Raw *ring = R::ring(smem, D * 4);  // [D][x, f, dy, dz]
+    float *held = reinterpret_cast<float *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Raw));  // whole images: gate A, gate B [2][C]
     const Lane<VEC, K> l(a);
     RowSum sum(a.tpr, l.slot, meet);
     const bool block = a.f != nullptr, stream = a.dy != nullptr, norm = a.dz != nullptr;
@@ -434,19 +446,19 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
         const T *x = static_cast<const T *>(a.x) + row * a.px + l.first(0), *f = static_cast<const T *>(a.f) + row * a.pf + l.first(0);
         const T *dy = static_cast<const T *>(a.dy) + row * a.pdy + l.first(0), *dz = static_cast<const T *>(a.dz) + row * a.pdz + l.first(0);
         T *dx = static_cast<T *>(a.o0) + row * a.p0 + l.first(0), *df = static_cast<T *>(a.o1) + row * a.p1 + l.first(0);
-        if (!a.full) R::template blank<D * 4>(l, ring, nt);  // (the sums were there between units)
-        int to = 0, at = 0;
+        if (!a.full) R::template blank<D * 4>(l, ring);  // (the sums were there between units)
+        const Raw *d = ring;
+        Raw *to = ring;
         // A row beyond the run counts as zeros.
         auto ask = [&] {
-            Raw *d = ring + to * (4 * NV) * nt;
             if (asked < r1) {
-                R::ask(l, x, d, nt);
-                if (block) R::ask(l, f, d + NV * nt, nt);
-                if (stream) R::ask(l, dy, d + 2 * NV * nt, nt);
-                if (norm) R::ask(l, dz, d + 3 * NV * nt, nt);
+                R::ask(l, x, to);
+                if (block) R::ask(l, f, to + ROW);
+                if (stream) R::ask(l, dy, to + 2 * ROW);
+                if (norm) R::ask(l, dz, to + 3 * ROW);
             } else {
 #pragma unroll
-                for (int m = 0; m < 4; ++m) R::zero(d + m * NV * nt, nt);
+                for (int m = 0; m < 4; ++m) R::zero(to + m * ROW);
             }
             copy_commit();
             asked += a.slots;
@@ -454,7 +466,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             f += sf;
             dy += sdy;
             dz += sdz;
-            if (++to == D) to = 0;
+            to = to == ring + (D - 1) * STAGE ? ring : to + STAGE;
         };
 #pragma unroll
         for (int i = 0; i < (D > 1 ? D - 1 : 1); ++i) ask();
@@ -464,12 +476,10 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
         for (int base = r0; base < r1; base += a.slots) {
             const bool on = row < r1;
             copy_wait<(D > 1 ? D - 2 : 0)>();
-            const Raw *d = ring + at * (4 * NV) * nt;
-            if (++at == D) at = 0;
             float2 u[P], y[P], t[P];  // u^, y^, dY
-            R::get(d, nt, y);
+            R::get(d, y);
             if (block) {
-                R::get(d + NV * nt, nt, u);
+                R::get(d + ROW, u);
                 const float2 r = both(st.y), c = both(-st.x * st.y);
                 if (a.b1)
 #pragma unroll
@@ -480,13 +490,13 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
                     y[k] = fma2(q[k], u[k], y[k]);
                 }
             }
-            if (stream) R::get(d + 2 * NV * nt, nt, t);
+            if (stream) R::get(d + 2 * ROW, t);
             else
 #pragma unroll
                 for (int k = 0; k < P; ++k) t[k] = make_float2(0.0f, 0.0f);
             if (norm) {
                 float2 e[P], w = make_float2(0.0f, 0.0f), v = w;
-                R::get(d + 3 * NV * nt, nt, e);
+                R::get(d + 3 * ROW, e);
                 const float2 r = both(st.w), c = both(-st.z * st.w);
                 if (a.db2)
 #pragma unroll
@@ -509,6 +519,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
 #pragma unroll
                 for (int k = 0; k < P; ++k) t[k] = fma2(y[k], my, fma2(e[k], r, t[k]));
             }
+            d = d == ring + (D - 1) * STAGE ? ring : d + STAGE;
             if (D > 1) ask();
             const float4 now = st;
             st = statistics(row + a.slots);
@@ -552,87 +563,124 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
                 if (a.dgate) {
                     const float k = (a.scale ? a.scale[c] : 1.0f) * (s == SUM_A ? (a.g1 ? a.g1[c] : 1.0f) : (a.b1 ? a.b1[c] : 0.0f)) * v;
                     // (A and B of a channel are two threads': they meet in the CTA's part of the workspace)
-                    a.part[((long long)blockIdx.x * SUMS + s) * a.C + c] = k;
+                    a.part[((long long)blockIdx.x * SUMS + s) * a.Cp + c] = k;
                 }
             });
             if (a.dgate) {
                 __syncthreads();
-                const float *one = a.part + (long long)blockIdx.x * SUMS * a.C;
-                for (int c = threadIdx.x; c < a.C; c += nt) a.dgate[(long long)n * a.C + c] = one[c] + one[a.C + c];
+                const float *one = a.part + (long long)blockIdx.x * SUMS * a.Cp;
+                for (int c = threadIdx.x; c < a.C; c += nt) a.dgate[(long long)n * a.C + c] = one[c] + one[a.Cp + c];
                 __syncthreads();
             }
 #pragma unroll
             for (int i = 0; i < P; ++i) acc[SUM_A][i] = acc[SUM_B][i] = make_float2(0.0f, 0.0f);
         } else {
             combine<0, SUMS, VEC, K>(l, a.slots, acc, ent, [&](int s, int c, float v) {
-                a.part[((long long)unit * SUMS + s) * a.C + c] = v;
+                a.part[((long long)unit * SUMS + s) * a.Cp + c] = v;
             });
         }
     }
     if (a.whole) {
         combine<SUM_G2, 2, VEC, K>(l, a.slots, acc, reinterpret_cast<float2 *>(smem), [&](int s, int c, float v) {
-            a.part[((long long)blockIdx.x * SUMS + s) * a.C + c] = v;
+            a.part[((long long)blockIdx.x * SUMS + s) * a.Cp + c] = v;
         });
         __syncthreads();
-        for (int c = threadIdx.x; c < 2 * a.C; c += nt) a.part[(long long)blockIdx.x * SUMS * a.C + c] = held[c];
+        for (int c = threadIdx.x; c < a.C; c += nt) {
+            float *one = a.part + (long long)blockIdx.x * SUMS * a.Cp + c;
+            one[0] = held[c];
+            one[a.Cp] = held[a.C + c];
+        }
     }
 }
 
-// Joins the units' sums.  A CTA takes eight channels; four units a warp at a
-// time.  Blocks y = 0 sum over all units, those above one image a warp.
-constexpr int kJoin = 1024;
+// Joins the units' sums: a CTA takes sixteen channels, four a thread, and 128
+// units at a time.  Blocks y = 0 sum over all units; those above an image's
+// units for its dgate, an image a warp.
+constexpr int kJoin = 512, kJoinC = 16;
+__device__ __forceinline__ void add4(float4 &s, const float4 &v, float k) {
+    s.x = fmaf(k, v.x, s.x);
+    s.y = fmaf(k, v.y, s.y);
+    s.z = fmaf(k, v.z, s.z);
+    s.w = fmaf(k, v.w, s.w);
+}
+__device__ __forceinline__ float4 sum8(float4 v) {  // over the lanes of one four of channels
+#pragma unroll
+    for (int o = 4; o < 32; o *= 2) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+        v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+    }
+    return v;
+}
 __global__ void __launch_bounds__(kJoin) bn_join_kernel(const __grid_constant__ BnArgs a, int parts) {
-    __shared__ float red[SUMS][8][kJoin / 32];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 8 + (lane & 7), group = lane >> 3;
+    __shared__ float4 red[SUMS][kJoin / 32][kJoinC / 4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, four = lane & 3, group = lane >> 2;
+    const int c = blockIdx.x * kJoinC + four * 4;  // (channels are padded to fours in the workspace)
+    const bool on = c < a.C;
     pdl_trigger();
     pdl_wait();
-    const float scale = a.scale && c < a.C ? a.scale[c] : 1.0f, g1 = a.g1 && c < a.C ? a.g1[c] : 1.0f;
-    const float b1 = a.b1 && c < a.C ? a.b1[c] : 0.0f;
-    if (blockIdx.y > 0) {  // dgate of one image (its units are the runs of that image)
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (blockIdx.y > 0) {
         const int n = (blockIdx.y - 1) * (kJoin / 32) + warp;
-        float A = 0.0f, B = 0.0f;
-        if (n < a.N && c < a.C)
-            for (int s = group; s < a.S; s += 4) {
-                const float *u = a.part + ((long long)n * a.S + s) * SUMS * a.C + c;
-                A += u[SUM_A * a.C];
-                B += u[SUM_B * a.C];
+        float4 A = zero, B = zero;
+        if (n < a.N && on)
+            for (int s = group; s < a.S; s += 8) {
+                const float *u = a.part + ((long long)n * a.S + s) * SUMS * a.Cp + c;
+                add4(A, *reinterpret_cast<const float4 *>(u + SUM_A * a.Cp), 1.0f);
+                add4(B, *reinterpret_cast<const float4 *>(u + SUM_B * a.Cp), 1.0f);
             }
-#pragma unroll
-        for (int o = 8; o < 32; o *= 2) {
-            A += __shfl_xor_sync(0xffffffffu, A, o);
-            B += __shfl_xor_sync(0xffffffffu, B, o);
+        A = sum8(A);
+        B = sum8(B);
+        if (n < a.N && group < 4 && c + group < a.C) {
+            const int k = c + group;
+            const float g1 = a.g1 ? a.g1[k] : 1.0f, b1 = a.b1 ? a.b1[k] : 0.0f;
+            const float va = group == 0 ? A.x : (group == 1 ? A.y : (group == 2 ? A.z : A.w));
+            const float vb = group == 0 ? B.x : (group == 1 ? B.y : (group == 2 ? B.z : B.w));
+            a.dgate[(long long)n * a.C + k] = (a.scale ? a.scale[k] : 1.0f) * (g1 * va + b1 * vb);
         }
-        if (n < a.N && c < a.C && group == 0) a.dgate[(long long)n * a.C + c] = scale * (g1 * A + b1 * B);
         return;
     }
-    float v[SUMS] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (c < a.C)
-        for (int u = warp * 4 + group; u < parts; u += kJoin / 8) {
-            const float *one = a.part + (long long)u * SUMS * a.C + c;
-            const float gate = a.gate && !a.whole ? a.gate[(long long)(u / a.S) * a.C + c] : 1.0f;
-            v[SUM_A] += gate * one[SUM_A * a.C];
-            v[SUM_B] += gate * one[SUM_B * a.C];
-            v[SUM_G2] += one[SUM_G2 * a.C];
-            v[SUM_B2] += one[SUM_B2 * a.C];
+    float4 v[SUMS] = {zero, zero, zero, zero};
+    const bool gated = a.gate && !a.whole;
+    if (on)
+        for (int u = warp * 8 + group; u < parts; u += kJoin / 4) {
+            const float4 *one = reinterpret_cast<const float4 *>(a.part + (long long)u * SUMS * a.Cp + c);
+            float4 w[SUMS];
+#pragma unroll
+            for (int s = 0; s < SUMS; ++s) w[s] = one[s * (a.Cp / 4)];
+            if (gated) {
+                const float *g = a.gate + (long long)(u / a.S) * a.C + c;
+                const float4 k = make_float4(g[0], c + 1 < a.C ? g[1] : 0.0f, c + 2 < a.C ? g[2] : 0.0f, c + 3 < a.C ? g[3] : 0.0f);
+#pragma unroll
+                for (int s = 0; s < SUM_G2; ++s) w[s] = make_float4(k.x * w[s].x, k.y * w[s].y, k.z * w[s].z, k.w * w[s].w);
+            }
+#pragma unroll
+            for (int s = 0; s < SUMS; ++s) add4(v[s], w[s], 1.0f);
         }
 #pragma unroll
     for (int s = 0; s < SUMS; ++s) {
-#pragma unroll
-        for (int o = 8; o < 32; o *= 2) v[s] += __shfl_xor_sync(0xffffffffu, v[s], o);
-        if (group == 0) red[s][lane & 7][warp] = v[s];
+        v[s] = sum8(v[s]);
+        if (group == 0) red[s][warp][four] = v[s];
     }
     __syncthreads();
-    if (warp < 8) {  // a channel a warp
-        const int k = blockIdx.x * 8 + warp;
+    if (warp == 0) {  // a channel a lane, twice
+        const int at = lane & 15, k = blockIdx.x * kJoinC + at;
+        float t[SUMS];
 #pragma unroll
-        for (int s = 0; s < SUMS; ++s) v[s] = warp_sum(red[s][warp][lane]);
-        if (lane == 0 && k < a.C) {
+        for (int s = 0; s < SUMS; ++s) {
+            t[s] = 0.0f;
+            const float *r = reinterpret_cast<const float *>(red[s]) + at;
+            for (int w = lane >> 4; w < kJoin / 32; w += 2) t[s] += r[w * kJoinC];
+            t[s] += __shfl_xor_sync(0xffffffffu, t[s], 16);
+        }
+        if (lane < 16 && k < a.C) {
             const float sc = a.scale ? a.scale[k] : 1.0f;
-            if (a.dscale) a.dscale[k] = (a.g1 ? a.g1[k] : 1.0f) * v[SUM_A] + (a.b1 ? a.b1[k] : 0.0f) * v[SUM_B];
-            if (a.dg1) a.dg1[k] = sc * v[SUM_A];
-            if (a.db1) a.db1[k] = sc * v[SUM_B];
-            if (a.dg2) a.dg2[k] = v[SUM_G2];
-            if (a.db2) a.db2[k] = v[SUM_B2];
+            if (a.dscale) a.dscale[k] = (a.g1 ? a.g1[k] : 1.0f) * t[SUM_A] + (a.b1 ? a.b1[k] : 0.0f) * t[SUM_B];
+            if (a.dg1) a.dg1[k] = sc * t[SUM_A];
+            if (a.db1) a.db1[k] = sc * t[SUM_B];
+            if (a.dg2) a.dg2[k] = t[SUM_G2];
+            if (a.db2) a.db2[k] = t[SUM_B2];
         }
     }
 }
@@ -671,8 +719,8 @@ int vec_for(const conv_plan *p, const Map (&maps)[N]) {
 // rows side by side have k = 1, so that it has 96 elements a thread where the
 // sums are SUMS * 8 in fp32.)
 static_assert(3 * 4 * 8 * 2 >= SUMS * 8 * 4, "");
-size_t ring_bytes(const BnGeom &g, int es, int rb) {
-    return (size_t)(rb == 0 ? 4 * bwd_stages(es, g.k) : 2 * kFwdStages * rb) * g.threads * 8 * g.k * es;
+size_t ring_bytes(const BnGeom &g, const BnGeom::Part &d, int es) {
+    return (size_t)(d.rb == 0 ? 4 * bwd_stages(es, g.k) : 2 * kFwdStages * d.rb) * d.threads * 8 * g.k * es;
 }
 
 cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a, size_t smem, cudaStream_t st) {
@@ -681,9 +729,9 @@ cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a
         const int rc = conv_grant_smem_once(k, p->device, (int)smem);
         if (rc != CONV_OK) return cudaErrorInvalidValue;
     }
-    a.run = d.run; a.S = d.S; a.units = d.units; a.whole = d.whole;
+    a.slots = d.slots; a.run = d.run; a.S = d.S; a.units = d.units; a.whole = d.whole;
     void *args[] = {&a};
-    return conv_launch(k, dim3((unsigned)d.grid), dim3((unsigned)p->bn.threads), args, smem, st);
+    return conv_launch(k, dim3((unsigned)d.grid), dim3((unsigned)d.threads), args, smem, st);
 }
 
 int check_map(const conv_plan *p, const void *t, int64_t *pitch) {
@@ -763,36 +811,41 @@ void plan_geometry(conv_plan *p) {
     if (want > 32) tpr = (want + 31) / 32 * 32;
     else while (tpr < want) tpr *= 2;
     g.tpr = tpr;
-    g.slots = tpr <= kThreads ? kThreads / tpr : 1;
-    g.threads = g.tpr * g.slots;
     g.full = C == tpr * 8 * g.k;
     const long long N = p->s.n, HW = (long long)p->s.h * p->s.w, rows = N * HW;
     p->ws_bytes = p->ws_bwd_bytes = 0;
     if (rows == 0) return;
-    auto wave = [&](int rb, int most) {
-        int n = (int)((size_t)(220 * 1024) / (ring_bytes(g, es, rb) + 1024));
-        if (n > most * kThreads / g.threads) n = most * kThreads / g.threads;
+    auto part = [&](BnGeom::Part &d, int rb, int threads) {
+        d.rb = rb;
+        d.slots = tpr <= threads ? threads / tpr : 1;
+        d.threads = tpr * d.slots;
+    };
+    // CTAs of one wave: 512 threads a SM, where their rings fit
+    auto wave = [&](const BnGeom::Part &d) {
+        const long long smem = (220 * 1024) / (long long)(ring_bytes(g, d, es) + 1024), regs = kMostThreads / d.threads;
+        const long long n = smem < regs ? smem : regs;
         return (long long)p->num_sms * (n < 1 ? 1 : n);
     };
     // two rows at a time where a CTA takes more than one set of rows
-    g.fwd.rb = g.k == 1 && rows > (long long)p->num_sms * g.slots ? 2 : 1;
-    divide_rows(g.fwd, rows, (long long)g.slots * g.fwd.rb, wave(g.fwd.rb, kFwdCtas));
+    part(g.fwd, 1, kThreads);
+    if (g.k == 1 && rows > (long long)p->num_sms * g.fwd.slots) g.fwd.rb = 2;
     g.fwd_gated = g.fwd;
-    if (g.fwd.rb == 2) {
-        if (HW >= 4LL * g.slots) divide_images(g.fwd_gated, N, HW, 2LL * g.slots, wave(2, kFwdCtas));
-        else {
-            g.fwd_gated.rb = 1;
-            divide_rows(g.fwd_gated, rows, g.slots, wave(1, kFwdCtas));
-        }
+    divide_rows(g.fwd, rows, (long long)g.fwd.slots * g.fwd.rb, wave(g.fwd));
+    if (g.fwd.rb == 2 && HW >= 4LL * g.fwd.slots) divide_images(g.fwd_gated, N, HW, 2LL * g.fwd.slots, wave(g.fwd_gated));
+    else {
+        g.fwd_gated.rb = 1;
+        divide_rows(g.fwd_gated, rows, g.fwd.slots, wave(g.fwd_gated));
     }
-    g.bwd.rb = g.bwd_gated.rb = 0;
-    const long long w = wave(0, kBwdCtas);
-    divide_rows(g.bwd, rows, g.slots, w);
-    divide_images(g.bwd_gated, N, HW, g.slots, w);
+    // the gradient in large CTAs: a part of the sums from each
+    part(g.bwd, 0, kMostThreads);
+    g.bwd_gated = g.bwd;
+    const long long w = wave(g.bwd);
+    divide_rows(g.bwd, rows, g.bwd.slots, w);
+    divide_images(g.bwd_gated, N, HW, g.bwd.slots, w);
     g.bwd_gated.whole = g.bwd_gated.S == 1;
     if (g.bwd_gated.whole && N > w) g.bwd_gated.grid = (int)w;
     const long long parts = g.bwd.grid > g.bwd_gated.grid ? g.bwd.grid : g.bwd_gated.grid;
-    p->ws_bwd_bytes = (size_t)parts * SUMS * C * 4;
+    p->ws_bwd_bytes = (size_t)parts * SUMS * ((C + 3) / 4 * 4) * 4;
 }
 
 }  // namespace
@@ -823,7 +876,7 @@ extern "C" int conv_plan_create_blocknorm(int32_t n, int32_t h, int32_t w, int32
     plan_geometry(p);
     static const char *const names[] = {"none", "layer", "rms"};
     snprintf(p->desc, sizeof(p->desc), "blocknorm %s post=%s pre=%s threads=%dx%d channels/thread=%d ctas=%d gradient: %d, gated %d in %d",
-             dtype == CONV_F32 ? "f32" : "bf16", names[post], names[pre], p->bn.slots, p->bn.tpr, 8 * p->bn.k, p->bn.fwd.grid,
+             dtype == CONV_F32 ? "f32" : "bf16", names[post], names[pre], p->bn.fwd.slots, p->bn.tpr, 8 * p->bn.k, p->bn.fwd.grid,
              p->bn.bwd.grid, p->bn.bwd_gated.units, p->bn.bwd_gated.grid);
     *out_plan = p;
     return CONV_OK;
@@ -835,9 +888,9 @@ BnArgs base_args(const conv_plan *p, const conv_blocknorm_params_t &w, const voi
     a.x = x; a.px = px; a.f = f; a.pf = pf;
     a.scale = w.scale; a.gate = w.gate; a.g1 = w.post_gamma; a.b1 = w.post_beta; a.g2 = w.pre_gamma; a.b2 = w.pre_beta;
     a.eps = p->bn.eps; a.inv_c = 1.0f / (float)p->s.c_in;
-    a.N = p->s.n; a.HW = p->s.h * p->s.w; a.rows = a.N * a.HW; a.C = p->s.c_in;
+    a.N = p->s.n; a.HW = p->s.h * p->s.w; a.rows = a.N * a.HW; a.C = p->s.c_in; a.Cp = (a.C + 3) / 4 * 4;
     a.post = p->bn.post; a.pre = p->bn.pre;
-    a.tpr = p->bn.tpr; a.slots = p->bn.slots; a.full = p->bn.full;
+    a.tpr = p->bn.tpr; a.full = p->bn.full;
     return a;
 }
 int check_params(const conv_plan *p, const conv_blocknorm_params_t &w, const void *f) {
@@ -881,7 +934,7 @@ extern "C" int conv_run_blocknorm(const conv_plan_t *plan, const void *x, int64_
     a.stats = reinterpret_cast<float4 *>(stats);
     const Map all[4] = {in[0], in[1], out[0], out[1]};
     const BnGeom::Part &g = w.gate ? p->bn.fwd_gated : p->bn.fwd;
-    return launch(p, g, vec_for(p, all), a, ring_bytes(p->bn, es, g.rb), (cudaStream_t)stream) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+    return launch(p, g, vec_for(p, all), a, ring_bytes(p->bn, g, es), (cudaStream_t)stream) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }
 
 extern "C" int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, int64_t x_pitch, const void *f, int64_t f_pitch,
@@ -938,12 +991,12 @@ extern "C" int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, in
     a.want_b = d.post_beta || (w.post_beta && (d.scale || d.gate));
     const BnGeom::Part &g = w.gate ? p->bn.bwd_gated : p->bn.bwd;
     const Map all[6] = {in[0], in[1], in[2], in[3], out[0], out[1]};
-    const size_t smem = ring_bytes(p->bn, es, 0) + (g.whole ? 2 * cb : 0);
+    const size_t smem = ring_bytes(p->bn, g, es) + (g.whole ? 2 * cb : 0);
     if (launch(p, g, vec_for(p, all), a, smem, st) != cudaSuccess) return CONV_ERR_CUDA;
     const bool sums = d.scale || d.post_gamma || d.post_beta || d.pre_gamma || d.pre_beta, images = d.gate && !g.whole;
     if (!sums && !images) return CONV_OK;
     int parts = g.grid;
     void *args[] = {&a, &parts};
-    const dim3 grid((unsigned)((C + 7) / 8), 1 + (unsigned)(images ? (a.N + kJoin / 32 - 1) / (kJoin / 32) : 0));
+    const dim3 grid((unsigned)((C + kJoinC - 1) / kJoinC), 1 + (unsigned)(images ? (a.N + kJoin / 32 - 1) / (kJoin / 32) : 0));
     return conv_launch((const void *)&bn_join_kernel, grid, dim3(kJoin), args, 0, st) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }
