@@ -160,11 +160,15 @@ struct Row {
     }
 };
 
+// Rows of a part of a warp, of a warp, of several; or any of these.
+enum { ROW_PART, ROW_WARP, ROW_WARPS, ROW_ANY };
+
 // Two sums over the threads of a row, to all of them.  The first exchange
 // leaves one sum to each half of the lanes, which halves the exchanges.  Rows of
 // more than a warp then meet in one of two sets of shared entries in turn:
 // whoever writes an entry again has passed the barrier of the other set, and
 // with it everyone's reading of this one.
+template <int ROW>
 struct RowSum {
     int tpr, slot;
     float *buf;  // [2][warps][2]
@@ -173,30 +177,30 @@ struct RowSum {
     __device__ static __forceinline__ float across(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
     __device__ __forceinline__ float2 operator()(float a, float b) {
         const int lane = threadIdx.x & 31;
-        if (tpr >= 32) {
-            const bool hi = lane & 16;
-            float v = (hi ? b : a) + across(hi ? a : b, 16);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) v += across(v, o);
-            if (tpr > 32) {
-                float *e = buf + flip;
-                flip ^= kMostThreads / 32 * 2;
-                if ((lane & 15) == 0) e[(threadIdx.x >> 5) * 2 + (lane >> 4)] = v;
-                asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
-                const int n = tpr >> 5, k = lane & 15;
-                v = k < n ? e[(slot * n + k) * 2 + (lane >> 4)] : 0.0f;
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1) v += across(v, o);
-            }
-            const float w = across(v, 16);
+        if (ROW == ROW_PART || (ROW == ROW_ANY && tpr < 32)) {
+            if (tpr == 1) return make_float2(a, b);
+            const int top = tpr >> 1;
+            const bool hi = lane & top;
+            float v = (hi ? b : a) + across(hi ? a : b, top);
+            for (int o = top >> 1; o > 0; o >>= 1) v += across(v, o);
+            const float w = across(v, top);
             return hi ? make_float2(w, v) : make_float2(v, w);
         }
-        if (tpr == 1) return make_float2(a, b);
-        const int top = tpr >> 1;
-        const bool hi = lane & top;
-        float v = (hi ? b : a) + across(hi ? a : b, top);
-        for (int o = top >> 1; o > 0; o >>= 1) v += across(v, o);
-        const float w = across(v, top);
+        const bool hi = lane & 16;
+        float v = (hi ? b : a) + across(hi ? a : b, 16);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) v += across(v, o);
+        if (ROW == ROW_WARPS || (ROW == ROW_ANY && tpr > 32)) {
+            float *e = buf + flip;
+            flip ^= kMostThreads / 32 * 2;
+            if ((lane & 15) == 0) e[(threadIdx.x >> 5) * 2 + (lane >> 4)] = v;
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
+            const int n = tpr >> 5, k = lane & 15;
+            v = k < n ? e[(slot * n + k) * 2 + (lane >> 4)] : 0.0f;
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) v += across(v, o);
+        }
+        const float w = across(v, 16);
         return hi ? make_float2(w, v) : make_float2(v, w);
     }
 };
@@ -211,8 +215,8 @@ __device__ __forceinline__ float total(const float2 (&v)[P]) {
 }
 
 // m and r of one norm of RB rows (1 or 2), and the values normalised in place.
-template <int VEC, int K, int RB>
-__device__ __forceinline__ void normalise(const Lane<VEC, K> &l, RowSum &sum, float2 (&v)[RB][4 * K], int kind, const BnArgs &a,
+template <int VEC, int K, int RB, int ROW>
+__device__ __forceinline__ void normalise(const Lane<VEC, K> &l, RowSum<ROW> &sum, float2 (&v)[RB][4 * K], int kind, const BnArgs &a,
                                           float2 (&mr)[RB]) {
     constexpr int P = 4 * K;
     float2 m = make_float2(0.0f, 0.0f);
@@ -274,12 +278,12 @@ template <typename T, int VEC, int K, int RB>
 __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_constant__ BnArgs a) {
     using R = Row<T, VEC, K>;
     using Raw = typename R::Raw;
-    constexpr int P = R::P, D = kFwdStages, ROW = R::NV * R::step, STAGE = 2 * RB * ROW;
+    constexpr int P = R::P, D = kFwdStages, LINE = R::NV * R::step, STAGE = 2 * RB * LINE;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float meet[2 * kMostThreads / 32 * 2];
     Raw *ring = R::ring(smem, D * 2 * RB);  // [D][x, f][RB]
     const Lane<VEC, K> l(a);
-    RowSum sum(a.tpr, l.slot, meet);
+    RowSum<ROW_ANY> sum(a.tpr, l.slot, meet);
     const int n = RB > 1 ? blockIdx.x / a.S : 0, s0 = RB > 1 ? blockIdx.x - n * a.S : blockIdx.x;
     const int span = RB > 1 && a.S < a.units ? a.HW : a.rows;
     const int r0 = n * span + s0 * a.run, r1 = n * span + min(span, (s0 + 1) * a.run);
@@ -297,8 +301,8 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
             if (asked < r1) {
-                R::ask(l, x, to + b * ROW);
-                if (block) R::ask(l, f, to + (RB + b) * ROW);
+                R::ask(l, x, to + b * LINE);
+                if (block) R::ask(l, f, to + (RB + b) * LINE);
             }
             asked += a.slots;
             x += sx;
@@ -321,8 +325,8 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
         float2 v[RB][P], u[RB][P];
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-            R::get(d + b * ROW, v[b]);
-            if (block) R::get(d + (RB + b) * ROW, u[b]);
+            R::get(d + b * LINE, v[b]);
+            if (block) R::get(d + (RB + b) * LINE, u[b]);
         }
         d = d == ring + (D - 1) * STAGE ? ring : d + STAGE;
         ask();
@@ -410,20 +414,28 @@ __device__ __forceinline__ void combine(const Lane<VEC, K> &l, int slots, const 
 // Stages of the gradient's ring: what fits beside one another in shared memory.
 __host__ __device__ constexpr int bwd_stages(int es, int k) { return k == 1 ? 3 : (es == 2 ? 2 : 1); }
 
-// dx and df of the rows of a CTA's units, and the units' channel sums.
-template <typename T, int VEC, int K>
+// dx and df of the rows of a CTA's units, and the units' channel sums.  ALL: the
+// block, dy and dz are given; what is then not asked for is formed all the same,
+// which is fewer instructions than asking.
+template <typename T, int VEC, int K, int ROW, bool ALL>
 __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_constant__ BnArgs a) {
     using R = Row<T, VEC, K>;
     using Raw = typename R::Raw;
-    constexpr int P = R::P, D = bwd_stages(sizeof(T), K), ROW = R::NV * R::step, STAGE = 4 * ROW;
+    constexpr int P = R::P, D = bwd_stages(sizeof(T), K), LINE = R::NV * R::step, STAGE = 4 * LINE;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float meet[2 * kMostThreads / 32 * 2];
     const int nt = blockDim.x;
     Raw *ring = R::ring(smem, D * 4);  // [D][x, f, dy, dz]
-    float *held = reinterpret_cast<float *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Raw));  // whole images: gate A, gate B [2][C]
     const Lane<VEC, K> l(a);
-    RowSum sum(a.tpr, l.slot, meet);
-    const bool block = a.f != nullptr, stream = a.dy != nullptr, norm = a.dz != nullptr;
+    // statistics [warp][D][rows of a warp], copied by a lane of each row
+    const int line = l.tpr < 32 ? l.tpr : 32, lane = threadIdx.x & 31;
+    float4 *const seen = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Raw)) +
+                         (threadIdx.x >> 5) * (D * (32 / line)) + lane / line;
+    const bool copies = lane % line == 0;
+    float *held = reinterpret_cast<float *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Raw) + (size_t)D * (nt / line) * 16);  // whole images: gate A, gate B [2][C]
+    RowSum<ROW> sum(a.tpr, l.slot, meet);
+    const bool block = ALL || a.f, stream = ALL || a.dy, norm = ALL || a.dz;
+    const float mean_post = a.post == CONV_NORM_LAYER ? -a.inv_c : 0.0f, mean_pre = a.pre == CONV_NORM_LAYER ? -a.inv_c : 0.0f;
     const long long sx = a.slots * a.px, sf = a.slots * a.pf, sdy = a.slots * a.pdy, sdz = a.slots * a.pdz;
     const long long s0 = a.slots * a.p0, s1 = a.slots * a.p1;
     pdl_trigger();
@@ -449,16 +461,20 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
         if (!a.full) R::template blank<D * 4>(l, ring);  // (the sums were there between units)
         const Raw *d = ring;
         Raw *to = ring;
+        const float4 *sd = seen;
+        float4 *sto = seen;
         // A row beyond the run counts as zeros.
         auto ask = [&] {
             if (asked < r1) {
+                if (copies) copy_async<16>(tc::smem_u32(sto), a.stats + asked);
                 R::ask(l, x, to);
-                if (block) R::ask(l, f, to + ROW);
-                if (stream) R::ask(l, dy, to + 2 * ROW);
-                if (norm) R::ask(l, dz, to + 3 * ROW);
+                if (block) R::ask(l, f, to + LINE);
+                if (stream) R::ask(l, dy, to + 2 * LINE);
+                if (norm) R::ask(l, dz, to + 3 * LINE);
             } else {
+                if (copies) *sto = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-                for (int m = 0; m < 4; ++m) R::zero(to + m * ROW);
+                for (int m = 0; m < 4; ++m) R::zero(to + m * LINE);
             }
             copy_commit();
             asked += a.slots;
@@ -466,22 +482,24 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             f += sf;
             dy += sdy;
             dz += sdz;
-            to = to == ring + (D - 1) * STAGE ? ring : to + STAGE;
+            const bool last = to == ring + (D - 1) * STAGE;
+            to = last ? ring : to + STAGE;
+            sto = last ? seen : sto + 32 / line;
         };
 #pragma unroll
         for (int i = 0; i < (D > 1 ? D - 1 : 1); ++i) ask();
-        auto statistics = [&](int r) { return r < r1 ? a.stats[r] : make_float4(0.0f, 0.0f, 0.0f, 0.0f); };
-        float4 st = statistics(row);
         if (block && a.gate) factors(l, a, n, q, p);
         for (int base = r0; base < r1; base += a.slots) {
             const bool on = row < r1;
             copy_wait<(D > 1 ? D - 2 : 0)>();
+            __syncwarp();
+            const float4 st = *sd;
             float2 u[P], y[P], t[P];  // u^, y^, dY
             R::get(d, y);
             if (block) {
-                R::get(d + ROW, u);
+                R::get(d + LINE, u);
                 const float2 r = both(st.y), c = both(-st.x * st.y);
-                if (a.b1)
+                if (ALL || a.b1)
 #pragma unroll
                     for (int k = 0; k < P; ++k) y[k] = add2(y[k], p[k]);
 #pragma unroll
@@ -490,15 +508,15 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
                     y[k] = fma2(q[k], u[k], y[k]);
                 }
             }
-            if (stream) R::get(d + 2 * ROW, t);
+            if (stream) R::get(d + 2 * LINE, t);
             else
 #pragma unroll
                 for (int k = 0; k < P; ++k) t[k] = make_float2(0.0f, 0.0f);
             if (norm) {
                 float2 e[P], w = make_float2(0.0f, 0.0f), v = w;
-                R::get(d + 3 * ROW, e);
+                R::get(d + 3 * LINE, e);
                 const float2 r = both(st.w), c = both(-st.z * st.w);
-                if (a.db2)
+                if (ALL || a.db2)
 #pragma unroll
                     for (int k = 0; k < P; ++k) acc[SUM_B2][k] = add2(acc[SUM_B2][k], e[k]);
 #pragma unroll
@@ -510,23 +528,18 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
                     v = fma2(e[k], y[k], v);
                 }
                 const float2 s = sum(w.x + w.y, v.x + v.y);
-                const float2 my = both(-s.y * a.inv_c * st.w);
-                if (a.pre == CONV_NORM_LAYER) {
-                    const float2 m = both(-s.x * a.inv_c * st.w);
+                const float2 my = both(-s.y * a.inv_c * st.w), m = both(s.x * mean_pre * st.w);
 #pragma unroll
-                    for (int k = 0; k < P; ++k) t[k] = add2(t[k], m);
-                }
-#pragma unroll
-                for (int k = 0; k < P; ++k) t[k] = fma2(y[k], my, fma2(e[k], r, t[k]));
+                for (int k = 0; k < P; ++k) t[k] = fma2(y[k], my, fma2(e[k], r, add2(t[k], m)));
             }
-            d = d == ring + (D - 1) * STAGE ? ring : d + STAGE;
+            const bool last = d == ring + (D - 1) * STAGE;
+            d = last ? ring : d + STAGE;
+            sd = last ? seen : sd + 32 / line;
             if (D > 1) ask();
-            const float4 now = st;
-            st = statistics(row + a.slots);
             if (on) R::put(l, dx, t);
             if (block) {
                 // (what the mean's terms leave in a row beyond the run is 0: its sums are)
-                if (a.want_b)
+                if (ALL || a.want_b)
 #pragma unroll
                     for (int k = 0; k < P; ++k) acc[SUM_B][k] = add2(acc[SUM_B][k], t[k]);
 #pragma unroll
@@ -542,14 +555,17 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
                         v = fma2(t[k], u[k], v);
                     }
                     const float2 s = sum(w.x + w.y, v.x + v.y);
-                    const float2 r = both(now.y), mu = both(-s.y * a.inv_c * now.y);
-                    const float2 m = both(a.post == CONV_NORM_LAYER ? -s.x * a.inv_c * now.y : 0.0f);
+                    const float2 r = both(st.y), mu = both(-s.y * a.inv_c * st.y);
+                    const float2 m = both(s.x * mean_post * st.y);
 #pragma unroll
                     for (int k = 0; k < P; ++k) t[k] = fma2(u[k], mu, fma2(t[k], r, m));
                 }
                 if (on) R::put(l, df, t);
             }
-            if (D == 1) ask();
+            if (D == 1) {
+                __syncwarp();
+                ask();
+            }
             row += a.slots;
             dx += s0;
             df += s1;
@@ -686,17 +702,27 @@ __global__ void __launch_bounds__(kJoin) bn_join_kernel(const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ host side
-// (rb: rows at a time of the forward kernel, 0: the gradient)
 template <typename T, int VEC>
-const void *pick_k(int k, int rb) {
-    if (rb == 0) return k == 1 ? (const void *)&bn_bwd_kernel<T, VEC, 1> : (const void *)&bn_bwd_kernel<T, VEC, 2>;
+const void *pick_fwd(int k, int rb) {
     if (rb == 2) return (const void *)&bn_fwd_kernel<T, VEC, 1, 2>;
     return k == 1 ? (const void *)&bn_fwd_kernel<T, VEC, 1, 1> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1>;
 }
-const void *pick_kernel(conv_dtype_t dt, int vec, int k, int rb) {
-    if (dt == CONV_F32) return vec == 4 ? pick_k<float, 4>(k, rb) : pick_k<float, 1>(k, rb);
-    return vec == 8 ? pick_k<__nv_bfloat16, 8>(k, rb)
-                    : (vec == 2 ? pick_k<__nv_bfloat16, 2>(k, rb) : pick_k<__nv_bfloat16, 1>(k, rb));
+template <typename T, int VEC>
+const void *pick_bwd(int k, int tpr, bool all) {
+    if (k == 2) return all ? (const void *)&bn_bwd_kernel<T, VEC, 2, ROW_WARPS, true> : (const void *)&bn_bwd_kernel<T, VEC, 2, ROW_WARPS, false>;
+    if (!all) return (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_ANY, false>;
+    return tpr < 32 ? (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_PART, true>
+                    : (tpr == 32 ? (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_WARP, true> : (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_WARPS, true>);
+}
+// (rb: rows at a time of the forward kernel, 0: the gradient)
+const void *pick_kernel(conv_dtype_t dt, int vec, int rb, int k, int tpr, bool all) {
+    using B = __nv_bfloat16;
+    if (rb) {
+        if (dt == CONV_F32) return vec == 4 ? pick_fwd<float, 4>(k, rb) : pick_fwd<float, 1>(k, rb);
+        return vec == 8 ? pick_fwd<B, 8>(k, rb) : (vec == 2 ? pick_fwd<B, 2>(k, rb) : pick_fwd<B, 1>(k, rb));
+    }
+    if (dt == CONV_F32) return vec == 4 ? pick_bwd<float, 4>(k, tpr, all) : pick_bwd<float, 1>(k, tpr, all);
+    return vec == 8 ? pick_bwd<B, 8>(k, tpr, all) : (vec == 2 ? pick_bwd<B, 2>(k, tpr, all) : pick_bwd<B, 1>(k, tpr, all));
 }
 
 // Channels a vector access takes: the widest that the channel count, every
@@ -720,11 +746,14 @@ int vec_for(const conv_plan *p, const Map (&maps)[N]) {
 // sums are SUMS * 8 in fp32.)
 static_assert(3 * 4 * 8 * 2 >= SUMS * 8 * 4, "");
 size_t ring_bytes(const BnGeom &g, const BnGeom::Part &d, int es) {
-    return (size_t)(d.rb == 0 ? 4 * bwd_stages(es, g.k) : 2 * kFwdStages * d.rb) * d.threads * 8 * g.k * es;
+    const size_t maps = (size_t)d.threads * 8 * g.k * es;
+    if (d.rb) return 2 * kFwdStages * d.rb * maps;
+    const int stages = bwd_stages(es, g.k);  // (and a row's statistics)
+    return stages * (4 * maps + (size_t)d.threads / (g.tpr < 32 ? g.tpr : 32) * 16);
 }
 
 cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a, size_t smem, cudaStream_t st) {
-    const void *k = pick_kernel(p->dtype, vec, p->bn.k, d.rb);
+    const void *k = pick_kernel(p->dtype, vec, d.rb, p->bn.k, p->bn.tpr, a.f && a.dy && a.dz);
     if (smem > 40 * 1024) {  // (with the kernel's static shared memory: 48 KB are free)
         const int rc = conv_grant_smem_once(k, p->device, (int)smem);
         if (rc != CONV_OK) return cudaErrorInvalidValue;
