@@ -197,7 +197,7 @@ def _cuda_getters():
 
 
 def _current_device():
-    return _cuda_getters()[0]()
+    return (_cuda or _cuda_getters())[0]()
 
 
 def _current_stream(device=None):
@@ -427,6 +427,23 @@ def _check(name, t, shape, dtype, device):
     return t.data_ptr()
 
 
+_getters = None
+
+
+def _tensor_getters():
+    """What is asked of every tensor of a call, to be mapped over all of them
+    (about 0.04 us each, where a loop takes twice that): its shape, dtype,
+    whether it is dense, its device and its address.  Looked up once."""
+    global _getters
+    if _getters is None:
+        import operator
+
+        import torch
+        t = torch.Tensor
+        _getters = operator.attrgetter("shape"), operator.attrgetter("dtype"), t.is_contiguous, t.get_device, t.data_ptr
+    return _getters
+
+
 def _torch_dtype(name):
     import torch
     return {"f32": torch.float32, "bf16": torch.bfloat16, "i8": torch.int8, "u8": torch.uint8, "i32": torch.int32}[name]
@@ -642,6 +659,12 @@ class W4Plan(_OpPlan):
             raise ConvError("conv_run_w4", rc)
 
 
+_BLOCKNORM_MAPS = {"x", "f", "y", "z", "dy", "dz", "dx", "df"}
+_BLOCKNORM_RUN = ("x", "f", "y", "z", "stats", "scale", "gate", "post_gamma", "post_beta", "pre_gamma", "pre_beta")
+_BLOCKNORM_BWD = ("x", "f", "dy", "dz", "dx", "df", "stats", "scale", "gate", "post_gamma", "post_beta", "pre_gamma",
+                  "dscale", "dgate", "dpost_gamma", "dpost_beta", "dpre_gamma", "dpre_beta")
+
+
 class BlockNormPlan(_MapPlan):
     """The norms before and after a block, fused with the block's gate, its
     residual scale and the residual add (conv_plan_create_blocknorm)::
@@ -661,6 +684,7 @@ class BlockNormPlan(_MapPlan):
         self.post, self.pre, self.eps, self.dtype, self.act = post, pre, eps, dtype, "none"
         self._create("conv_plan_create_blocknorm", n, h, w, c, NORMS[post], NORMS[pre], float(eps), DTYPES[dtype])
         self._cshape, self._gshape, self._sshape = (c,), (n, c), (n, h, w, 4)
+        self._known = {}  # shapes and types of a call's tensors, by which of them are given
 
     @property
     def output_shape(self):
@@ -668,16 +692,41 @@ class BlockNormPlan(_MapPlan):
 
     y_shape = output_shape
 
-    def _pointers(self, dev, prefix, scale, gate, post_gamma, post_beta, pre_gamma, pre_beta):
-        """The parameters, or their gradients, as the library takes them."""
-        f32, cs = self._f32, self._cshape
-        return _BlockNormPointers(
-            None if scale is None else _check(prefix + "scale", scale, cs, f32, dev),
-            None if gate is None else _check(prefix + "gate", gate, self._gshape, f32, dev),
-            None if post_gamma is None else _check(prefix + "post_gamma", post_gamma, cs, f32, dev),
-            None if post_beta is None else _check(prefix + "post_beta", post_beta, cs, f32, dev),
-            None if pre_gamma is None else _check(prefix + "pre_gamma", pre_gamma, cs, f32, dev),
-            None if pre_beta is None else _check(prefix + "pre_beta", pre_beta, cs, f32, dev))
+    def _addresses(self, names, tensors):
+        """Addresses of a call's tensors (None where there is none) and the pixel
+        pitches of its maps (0: dense).  Maps come first in `names`."""
+        none = tuple([t is None for t in tensors])
+        known = self._known.get((names, none))
+        if known is None:
+            maps = [k for k in names if k in _BLOCKNORM_MAPS]
+            shape = {"stats": self._sshape, "gate": self._gshape, "dgate": self._gshape, **{k: self.shape for k in maps}}
+            given = [k for k, absent in zip(names, none) if not absent]
+            known = (given, [shape.get(k, self._cshape) for k in given],
+                     [self._dt if k in maps else self._f32 for k in given], [self._device] * len(given), len(maps))
+            self._known[names, none] = known
+        given, shapes, dtypes, devices, maps = known
+        ts = tensors if len(given) == len(names) else [t for t in tensors if t is not None]
+        pitches = [0] * maps
+        shape_of, dtype_of, dense, device_of, address = _tensor_getters()
+        try:
+            good = (list(map(shape_of, ts)) == shapes and list(map(dtype_of, ts)) == dtypes and
+                    list(map(device_of, ts)) == devices and all(map(dense, ts)))
+            if good:
+                found = list(map(address, ts))
+        except (AttributeError, TypeError):  # (not tensors)
+            good = False
+        if not good:  # slices, or what is to be refused: one by one
+            found = []
+            for k, t, shape, dtype in zip(given, ts, shapes, dtypes):
+                if k in _BLOCKNORM_MAPS:
+                    at, pitches[names.index(k)] = self._map(k, t)
+                    found.append(at)
+                else:
+                    found.append(_check(k, t, shape, dtype, self._device))
+        if len(given) != len(names):
+            it = iter(found)
+            found = [None if absent else next(it) for absent in none]
+        return found, pitches
 
     def run(self, x, f, y, z, stats=None, scale=None, gate=None, post_gamma=None, post_beta=None, pre_gamma=None,
             pre_beta=None, stream=None) -> None:  # noqa: D401
@@ -687,14 +736,12 @@ class BlockNormPlan(_MapPlan):
         None where there is a z; z is None where ``pre`` is "none".  y or z may
         be x or f itself.  stats, where given, is what the gradient needs."""
         dev = self._on_device()
-        px, pitch_x = self._map("x", x)
-        pf, pitch_f = (None, 0) if f is None else self._map("f", f)
-        py, pitch_y = (None, 0) if y is None else self._map("y", y)
-        pz, pitch_z = (None, 0) if z is None else self._map("z", z)
-        ps = None if stats is None else _check("stats", stats, self._sshape, self._f32, dev)
-        w = self._pointers(dev, "", scale, gate, post_gamma, post_beta, pre_gamma, pre_beta)
-        rc = self._lib.conv_run_blocknorm(self._handle, px, pitch_x, pf, pitch_f, w, py, pitch_y, pz, pitch_z, ps,
-                                          _stream_handle(stream, dev))
+        if x is None:
+            raise ValueError("x is missing")
+        p, (ix, jf, iy, iz) = self._addresses(_BLOCKNORM_RUN, (x, f, y, z, stats, scale, gate, post_gamma, post_beta,
+                                                               pre_gamma, pre_beta))
+        rc = self._lib.conv_run_blocknorm(self._handle, p[0], ix, p[1], jf, _BlockNormPointers(*p[5:]), p[2], iy, p[3], iz,
+                                          p[4], _stream_handle(stream, dev))
         if rc != 0:
             raise ConvError("conv_run_blocknorm", rc)
 
@@ -705,18 +752,15 @@ class BlockNormPlan(_MapPlan):
         given.  x, f, stats and the parameters as the forward run had them; dy
         None is 0; dx or df may be any of the maps that are read."""
         dev = self._on_device()
-        px, pitch_x = self._map("x", x)
-        pf, pitch_f = (None, 0) if f is None else self._map("f", f)
-        pdy, pitch_dy = (None, 0) if dy is None else self._map("dy", dy)
-        pdz, pitch_dz = (None, 0) if dz is None else self._map("dz", dz)
-        pdx, pitch_dx = self._map("dx", dx)
-        pdf, pitch_df = (None, 0) if df is None else self._map("df", df)
-        ps = _check("stats", stats, self._sshape, self._f32, dev)
-        w = self._pointers(dev, "", scale, gate, post_gamma, post_beta, pre_gamma, None)
-        d = self._pointers(dev, "d", dscale, dgate, dpost_gamma, dpost_beta, dpre_gamma, dpre_beta)
+        if x is None or stats is None or dx is None:
+            raise ValueError("x, stats or dx is missing")
+        p, (ix, jf, iy, iz, kx, kf) = self._addresses(
+            _BLOCKNORM_BWD, (x, f, dy, dz, dx, df, stats, scale, gate, post_gamma, post_beta, pre_gamma, dscale, dgate,
+                             dpost_gamma, dpost_beta, dpre_gamma, dpre_beta))
         ws = self._workspace(self.workspace_bytes_backward, x, stream)
-        rc = self._lib.conv_run_blocknorm_bwd(self._handle, px, pitch_x, pf, pitch_f, w, ps, pdy, pitch_dy, pdz, pitch_dz,
-                                              pdx, pitch_dx, pdf, pitch_df, d, _ptr(ws), _stream_handle(stream, dev))
+        rc = self._lib.conv_run_blocknorm_bwd(self._handle, p[0], ix, p[1], jf, _BlockNormPointers(*p[7:12]), p[6], p[2], iy,
+                                              p[3], iz, p[4], kx, p[5], kf, _BlockNormPointers(*p[12:]), _ptr(ws),
+                                              _stream_handle(stream, dev))
         if rc != 0:
             raise ConvError("conv_run_blocknorm_bwd", rc)
 
@@ -727,8 +771,9 @@ class GradClipPlan(_OpPlan):
         norm = sqrt(sum of all squares)
         out = min(1, max_norm / (norm + 1e-6)) * g
 
-    ``shapes``: a shape (or a number of elements) for each tensor; ``dtypes``:
-    "bf16" or "f32" for all of them, or one for each."""
+    ``shapes``: a shape (or a number of elements) for each tensor, of which the
+    number of elements counts; ``dtypes``: "bf16" or "f32" for all of them, or
+    one for each."""
 
     def __init__(self, shapes, dtypes="bf16"):
         import math
@@ -739,10 +784,11 @@ class GradClipPlan(_OpPlan):
             raise ValueError(f"{len(names)} dtypes for {count} tensors")
         self.dtypes, self.act = names, "none"
         self.dtype, self.shape = (names[0] if names else "f32"), (count,)
-        counts = (ctypes.c_int64 * count)(*(math.prod(s) for s in self.shapes))
+        self._counts = [math.prod(s) for s in self.shapes]
+        counts = (ctypes.c_int64 * count)(*self._counts)
         codes = (ctypes.c_int * count)(*(DTYPES[d] for d in names))
         self._create("conv_plan_create_gradclip", count, counts, codes)
-        self._each = [(s, _torch_dtype(d)) for s, d in zip(self.shapes, names)]
+        self._dtypes, self._devices = [_torch_dtype(d) for d in names], [self._device] * count
         self._array = ctypes.c_void_p * count
 
     @property
@@ -751,14 +797,18 @@ class GradClipPlan(_OpPlan):
 
     y_shape = output_shape
 
-    def _addresses(self, name, tensors, dev):
-        if len(tensors) != len(self._each):
-            raise ValueError(f"{len(tensors)} {name} for a plan of {len(self._each)}")
-        for t, (shape, dtype) in zip(tensors, self._each):
-            if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-                i = next(i for i, u in enumerate(tensors) if u is t)
-                _check(f"{name}[{i}]", t, shape, dtype, dev)
-        return self._array(*[t.data_ptr() for t in tensors])
+    def _addresses(self, name, tensors):
+        if len(tensors) != len(self._counts):
+            raise ValueError(f"{len(tensors)} {name} for a plan of {len(self._counts)}")
+        _, dtype_of, dense, device_of, address = _tensor_getters()
+        try:
+            if (list(map(dtype_of, tensors)) == self._dtypes and list(map(device_of, tensors)) == self._devices and
+                    [t.numel() for t in tensors] == self._counts and all(map(dense, tensors))):
+                return self._array(*map(address, tensors))
+        except (AttributeError, TypeError):  # (not tensors)
+            pass
+        return self._array(*[_check(f"{name}[{i}]", t, t.shape if t is not None and t.numel() == k else self.shapes[i], d, self._device)
+                             for i, (t, k, d) in enumerate(zip(tensors, self._counts, self._dtypes))])
 
     def run(self, grads, max_norm, norm, out=None, stream=None) -> None:  # noqa: D401
         """Enqueue the norm (a float32 scalar tensor) and the clipped gradients
@@ -766,8 +816,8 @@ class GradClipPlan(_OpPlan):
         (any of which may be the gradient itself), or in place.  max_norm
         infinite: the norm alone.  A norm that is not finite clips nothing."""
         dev = self._on_device()
-        g = self._addresses("grads", grads, dev)
-        o = None if out is None else self._addresses("out", out, dev)
+        g = self._addresses("grads", grads)
+        o = None if out is None else self._addresses("out", out)
         pn = _check("norm", norm, (), self._f32, dev)
         ws = self._workspace(self.workspace_bytes, norm, stream)
         rc = self._lib.conv_run_gradclip(self._handle, g, o, float(max_norm), pn, _ptr(ws), _stream_handle(stream, dev))

@@ -24,257 +24,21 @@
 // warps that meet in shared memory), and a CTA takes several rows side by side.
 // All statistics and sums are fp32, in a fixed order: results do not change
 // from run to run.
-#include <cuda_bf16.h>
 #include <math.h>
-#include <stdint.h>
 #include <stdio.h>
 
 #include <new>
 
-#include "conv_internal.h"
-#include "epilogue.cuh"
-#include "maps.cuh"
-#include "tc_ptx.cuh"
+#include "blocknorm.cuh"
 
-using namespace convk;
+using namespace bn;
 
 namespace {
 
-constexpr int kMaxC = 8192;        // channels: 512 threads of 16
-constexpr int kThreads = 256;      // of a forward CTA whose rows take no more
-constexpr int kMostThreads = 512;  // of a row, and of the gradient's CTAs
-enum { SUM_A, SUM_B, SUM_G2, SUM_B2, SUMS };
-
-struct BnArgs {
-    const void *x, *f, *dy, *dz;   // f, dy and dz may be null
-    void *o0, *o1;                 // y, z or dx, df; may be null
-    long long px, pf, pdy, pdz, p0, p1;  // elements from one pixel to the next
-    const float *scale, *gate, *g1, *b1, *g2, *b2;  // each may be null
-    float4 *stats;                 // [rows] (m1, r1, m2, r2) (forward: may be null)
-    float *part;                   // gradient: [units or CTAs][SUMS][C]
-    float *dscale, *dgate, *dg1, *db1, *dg2, *db2;
-    float eps, inv_c;
-    int rows, HW, C, Cp, N;        // Cp: C in whole fours, of the workspace
-    int post, pre;                 // conv_norm_t
-    int tpr, slots, full;          // threads of a row, rows side by side; full: every thread has channels, all of them
-    int run, S, units;             // rows of a unit, units an image (of all rows without a gate), units in all
-    int whole;                     // gradient: a unit is a whole image of a gated map
-    int want_b;                    // gradient: B is asked for
-};
-
-// Where a thread stands: which row of those side by side, which of the row's
-// channels.  Vector v of a thread is number v * tpr + t of its row; pair i
-// holds two consecutive channels of a vector (VEC = 1: of two vectors).
-template <int VEC, int K>
-struct Lane {
-    static constexpr int NV = 8 * K / VEC, P = 4 * K;
-    int tpr, t, slot, C;
-    __device__ __forceinline__ explicit Lane(const BnArgs &a) : tpr(a.tpr), C(a.C) {
-        slot = threadIdx.x / tpr;
-        t = threadIdx.x - slot * tpr;
-    }
-    __device__ __forceinline__ int first(int v) const { return (v * tpr + t) * VEC; }
-    __device__ __forceinline__ bool on(int v) const { return first(v) < C; }
-    // (channels are whole vectors: a vector's are all in the row, or none)
-    __device__ __forceinline__ bool has(int i, int h) const { return VEC == 1 ? on(2 * i + h) : on(i / (VEC < 2 ? 1 : VEC / 2)); }
-    __device__ __forceinline__ int chan(int i, int h) const {
-        if constexpr (VEC == 1) return first(2 * i + h);
-        else return first(i / (VEC / 2)) + i % (VEC / 2) * 2 + h;
-    }
-    // src at the thread's channels (null: `other`), 0 beyond the row's end
-    __device__ __forceinline__ void params(float2 (&v)[P], const float *src, float other) const {
-        constexpr int W = VEC % 4 == 0 ? 4 : 1;
-        if (W == 4 && src && (reinterpret_cast<uintptr_t>(src) & 15) == 0) {
-#pragma unroll
-            for (int i = 0; i < P; i += 2) {
-                const float4 f = has(i, 0) ? *reinterpret_cast<const float4 *>(src + chan(i, 0)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                v[i] = make_float2(f.x, f.y);
-                v[i + 1] = make_float2(f.z, f.w);
-            }
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            v[i].x = has(i, 0) ? (src ? src[chan(i, 0)] : other) : 0.0f;
-            v[i].y = has(i, 1) ? (src ? src[chan(i, 1)] : other) : 0.0f;
-        }
-    }
-};
-
-// A thread's vectors of one row: from its ring of shared memory, to a map, and
-// from a map to the ring.  Vectors beyond the row's end stay 0 in the ring.
-template <typename T, int VEC, int K>
-struct Row {
-    using V = Vec<T, VEC>;
-    using Raw = typename V::Raw;
-    using L = Lane<VEC, K>;
-    static constexpr int NV = L::NV, P = L::P;
-    static constexpr int step = 32;  // of a thread's vectors in the ring: a warp's lie together
-    // the thread's first vector in a ring of `rows` rows
-    __device__ static __forceinline__ Raw *ring(uint8_t *smem, int rows) {
-        return reinterpret_cast<Raw *>(smem) + (threadIdx.x >> 5) * (rows * NV * step) + (threadIdx.x & 31);
-    }
-    __device__ static __forceinline__ void get(const Raw *src, float2 (&f)[P]) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            float2 one[V::kPairs];
-            V::unpack(src[v * step], one);
-#pragma unroll
-            for (int e = 0; e < V::kPairs; ++e) {
-                if constexpr (VEC == 1) {
-                    if (v % 2) f[v / 2].y = one[0].x;
-                    else f[v / 2].x = one[0].x;
-                } else f[v * V::kPairs + e] = one[e];
-            }
-        }
-    }
-    // (row: the address of the thread's first vector)
-    __device__ static __forceinline__ void put(const L &l, T *row, const float2 (&f)[P]) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            float2 one[V::kPairs];
-#pragma unroll
-            for (int e = 0; e < V::kPairs; ++e) {
-                if constexpr (VEC == 1) one[0].x = v % 2 ? f[v / 2].y : f[v / 2].x;
-                else one[e] = f[v * V::kPairs + e];
-            }
-            if (l.on(v)) *reinterpret_cast<Raw *>(row + v * l.tpr * VEC) = V::pack(one);
-        }
-    }
-    __device__ static __forceinline__ void ask(const L &l, const T *row, Raw *dst) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (l.on(v)) copy_vec(dst + v * step, reinterpret_cast<const Raw *>(row + v * l.tpr * VEC));
-    }
-    // the vectors beyond the row's end in `rows` rows of the ring
-    template <int ROWS>
-    __device__ static __forceinline__ void blank(const L &l, Raw *dst) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-            if (!l.on(v))
-                for (int i = 0; i < ROWS; ++i) dst[(i * NV + v) * step] = Raw{};
-    }
-    __device__ static __forceinline__ void zero(Raw *dst) {
-#pragma unroll
-        for (int v = 0; v < NV; ++v) dst[v * step] = Raw{};
-    }
-};
-
-// Rows of a part of a warp, of a warp, of several; or any of these.
-enum { ROW_PART, ROW_WARP, ROW_WARPS, ROW_ANY };
-
-// Two sums over the threads of a row, to all of them.  The first exchange
-// leaves one sum to each half of the lanes, which halves the exchanges.  Rows of
-// more than a warp then meet in one of two sets of shared entries in turn:
-// whoever writes an entry again has passed the barrier of the other set, and
-// with it everyone's reading of this one.
-template <int ROW>
-struct RowSum {
-    int tpr, slot;
-    float *buf;  // [2][warps][2]
-    int flip;
-    __device__ __forceinline__ RowSum(int tpr_, int slot_, float *b) : tpr(tpr_), slot(slot_), buf(b), flip(0) {}
-    __device__ static __forceinline__ float across(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
-    __device__ __forceinline__ float2 operator()(float a, float b) {
-        const int lane = threadIdx.x & 31;
-        if (ROW == ROW_PART || (ROW == ROW_ANY && tpr < 32)) {
-            if (tpr == 1) return make_float2(a, b);
-            const int top = tpr >> 1;
-            const bool hi = lane & top;
-            float v = (hi ? b : a) + across(hi ? a : b, top);
-            for (int o = top >> 1; o > 0; o >>= 1) v += across(v, o);
-            const float w = across(v, top);
-            return hi ? make_float2(w, v) : make_float2(v, w);
-        }
-        const bool hi = lane & 16;
-        float v = (hi ? b : a) + across(hi ? a : b, 16);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) v += across(v, o);
-        if (ROW == ROW_WARPS || (ROW == ROW_ANY && tpr > 32)) {
-            float *e = buf + flip;
-            flip ^= kMostThreads / 32 * 2;
-            if ((lane & 15) == 0) e[(threadIdx.x >> 5) * 2 + (lane >> 4)] = v;
-            asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
-            const int n = tpr >> 5, k = lane & 15;
-            v = k < n ? e[(slot * n + k) * 2 + (lane >> 4)] : 0.0f;
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) v += across(v, o);
-        }
-        const float w = across(v, 16);
-        return hi ? make_float2(w, v) : make_float2(v, w);
-    }
-};
-
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-template <int P>
-__device__ __forceinline__ float total(const float2 (&v)[P]) {
-    float2 s = v[0];
-#pragma unroll
-    for (int i = 1; i < P; ++i) s = add2(s, v[i]);
-    return s.x + s.y;
-}
-
-// m and r of one norm of RB rows (1 or 2), and the values normalised in place.
-template <int VEC, int K, int RB, int ROW>
-__device__ __forceinline__ void normalise(const Lane<VEC, K> &l, RowSum<ROW> &sum, float2 (&v)[RB][4 * K], int kind, const BnArgs &a,
-                                          float2 (&mr)[RB]) {
-    constexpr int P = 4 * K;
-    float2 m = make_float2(0.0f, 0.0f);
-    if (kind == CONV_NORM_LAYER) {
-        m = mul2(sum(total(v[0]), RB > 1 ? total(v[RB - 1]) : 0.0f), both(a.inv_c));
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-            for (int i = 0; i < P; ++i) v[b][i] = add2(v[b][i], both(b ? -m.y : -m.x));
-        if (!a.full)
-#pragma unroll
-            for (int b = 0; b < RB; ++b)
-#pragma unroll
-                for (int i = 0; i < P; ++i) {
-                    if (!l.has(i, 0)) v[b][i].x = 0.0f;
-                    if (!l.has(i, 1)) v[b][i].y = 0.0f;
-                }
-    }
-    float q[RB];
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-        float2 s = mul2(v[b][0], v[b][0]);
-#pragma unroll
-        for (int i = 1; i < P; ++i) s = fma2(v[b][i], v[b][i], s);
-        q[b] = s.x + s.y;
-    }
-    const float2 s = sum(q[0], RB > 1 ? q[RB - 1] : 0.0f);
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-        const float r = __frsqrt_rn(fmaf(b ? s.y : s.x, a.inv_c, a.eps));
-        mr[b] = make_float2(b ? m.y : m.x, r);
-#pragma unroll
-        for (int i = 0; i < P; ++i) v[b][i] = mul2(v[b][i], both(r));
-    }
-}
-
-// scale gate g1 and scale gate b1 at a thread's channels.
-template <int VEC, int K>
-__device__ __forceinline__ void factors(const Lane<VEC, K> &l, const BnArgs &a, int n, float2 (&q)[4 * K], float2 (&p)[4 * K]) {
-    constexpr int P = 4 * K;
-    float2 s[P], g[P];
-    l.params(s, a.scale, 1.0f);
-    l.params(g, a.gate ? a.gate + (long long)n * a.C : nullptr, 1.0f);
-    l.params(q, a.g1, 1.0f);
-    l.params(p, a.b1, 0.0f);
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        const float2 sg = mul2(s[i], g[i]);
-        q[i] = mul2(q[i], sg);
-        p[i] = mul2(p[i], sg);
-    }
-}
-
-constexpr int kFwdStages = 3;
-
-// y and z of a run of rows, RB at a time.  ANY: the rows of a gated map that a
-// CTA takes may be of several images (RB = 1); otherwise a run is of one.
-template <typename T, int VEC, int K, int RB>
+// y and z of a run of rows, RB at a time.  With RB = 1 and one row of 8 channels
+// a thread the rows that a CTA takes of a gated map may be of several images;
+// otherwise a run is of one.  ALL: f, y and z are given.
+template <typename T, int VEC, int K, int RB, int ROW, bool ALL>
 __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_constant__ BnArgs a) {
     using R = Row<T, VEC, K>;
     using Raw = typename R::Raw;
@@ -283,12 +47,12 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
     __shared__ float meet[2 * kMostThreads / 32 * 2];
     Raw *ring = R::ring(smem, D * 2 * RB);  // [D][x, f][RB]
     const Lane<VEC, K> l(a);
-    RowSum<ROW_ANY> sum(a.tpr, l.slot, meet);
+    RowSum<ROW> sum(a.tpr, l.slot, meet);
     const int n = RB > 1 ? blockIdx.x / a.S : 0, s0 = RB > 1 ? blockIdx.x - n * a.S : blockIdx.x;
     const int span = RB > 1 && a.S < a.units ? a.HW : a.rows;
     const int r0 = n * span + s0 * a.run, r1 = n * span + min(span, (s0 + 1) * a.run);
     int row = r0 + l.slot, asked = row;
-    const bool block = a.f != nullptr;
+    const bool block = ALL || a.f, norm = ALL || a.o1;
     const T *x = static_cast<const T *>(a.x) + row * a.px + l.first(0), *f = static_cast<const T *>(a.f) + row * a.pf + l.first(0);
     T *y = static_cast<T *>(a.o0) + row * a.p0 + l.first(0), *z = static_cast<T *>(a.o1) + row * a.p1 + l.first(0);
     const long long sx = a.slots * a.px, sf = a.slots * a.pf, sy = a.slots * a.p0, sz = a.slots * a.p1;
@@ -339,7 +103,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
                 if (k != image) factors(l, a, image = k, q, p);
             }
             if (a.post != CONV_NORM_NONE) normalise<VEC, K, RB>(l, sum, u, a.post, a, one);
-            if (a.b1)
+            if (ALL || a.b1)
 #pragma unroll
                 for (int b = 0; b < RB; ++b)
 #pragma unroll
@@ -348,12 +112,12 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
             for (int b = 0; b < RB; ++b)
 #pragma unroll
                 for (int i = 0; i < P; ++i) v[b][i] = fma2(q[i], u[b][i], v[b][i]);
-            if (a.o0)
+            if (ALL || a.o0)
 #pragma unroll
                 for (int b = 0; b < RB; ++b)
                     if (row + b * a.slots < r1) R::put(l, y + b * sy, v[b]);
         }
-        if (a.o1) {
+        if (norm) {
             normalise<VEC, K, RB>(l, sum, v, a.pre, a, two);
 #pragma unroll
             for (int b = 0; b < RB; ++b) {
@@ -373,356 +137,21 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
     copy_wait<0>();
 }
 
-// The sums of the CTA's threads over the rows side by side: take(sum, pair's
-// first channel, value), each channel by one thread.  ent: shared, of NS x
-// threads x P pairs; free on entry, free again on return.
-template <int FIRST, int NS, int VEC, int K, typename F>
-__device__ __forceinline__ void combine(const Lane<VEC, K> &l, int slots, const float2 (&acc)[SUMS][4 * K], float2 *ent, F &&take) {
-    constexpr int P = 4 * K;
-    if (slots == 1) {
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                if (l.has(i, 0)) take(FIRST + s, l.chan(i, 0), acc[FIRST + s][i].x);
-                if (l.has(i, 1)) take(FIRST + s, l.chan(i, 1), acc[FIRST + s][i].y);
-            }
-        return;
-    }
-    __syncthreads();
-    const int nt = blockDim.x;
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-        for (int i = 0; i < P; ++i) ent[(s * P + i) * nt + threadIdx.x] = acc[FIRST + s][i];
-    __syncthreads();
-    // one (sum, pair, thread of a row) at a time, those of a sum next to one another
-    for (int k = threadIdx.x; k < NS * P * l.tpr; k += nt) {
-        const int at = k / l.tpr, t = k - at * l.tpr;
-        const float2 *e = ent + at * nt + t;
-        float2 v = e[0];
-        for (int r = 1; r < slots; ++r) v = add2(v, e[r * l.tpr]);
-        Lane<VEC, K> o = l;
-        o.t = t;
-        const int s = at / P, i = at - s * P;
-        if (o.has(i, 0)) take(FIRST + s, o.chan(i, 0), v.x);
-        if (o.has(i, 1)) take(FIRST + s, o.chan(i, 1), v.y);
-    }
-    __syncthreads();
-}
-
-// Stages of the gradient's ring: what fits beside one another in shared memory.
-__host__ __device__ constexpr int bwd_stages(int es, int k) { return k == 1 ? 3 : (es == 2 ? 2 : 1); }
-
-// dx and df of the rows of a CTA's units, and the units' channel sums.  ALL: the
-// block, dy and dz are given; what is then not asked for is formed all the same,
-// which is fewer instructions than asking.
-template <typename T, int VEC, int K, int ROW, bool ALL>
-__global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_constant__ BnArgs a) {
-    using R = Row<T, VEC, K>;
-    using Raw = typename R::Raw;
-    constexpr int P = R::P, D = bwd_stages(sizeof(T), K), LINE = R::NV * R::step, STAGE = 4 * LINE;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float meet[2 * kMostThreads / 32 * 2];
-    const int nt = blockDim.x;
-    Raw *ring = R::ring(smem, D * 4);  // [D][x, f, dy, dz]
-    const Lane<VEC, K> l(a);
-    // statistics [warp][D][rows of a warp], copied by a lane of each row
-    const int line = l.tpr < 32 ? l.tpr : 32, lane = threadIdx.x & 31;
-    float4 *const seen = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Raw)) +
-                         (threadIdx.x >> 5) * (D * (32 / line)) + lane / line;
-    const bool copies = lane % line == 0;
-    float *held = reinterpret_cast<float *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Raw) + (size_t)D * (nt / line) * 16);  // whole images: gate A, gate B [2][C]
-    RowSum<ROW> sum(a.tpr, l.slot, meet);
-    const bool block = ALL || a.f, stream = ALL || a.dy, norm = ALL || a.dz;
-    const float mean_post = a.post == CONV_NORM_LAYER ? -a.inv_c : 0.0f, mean_pre = a.pre == CONV_NORM_LAYER ? -a.inv_c : 0.0f;
-    const long long sx = a.slots * a.px, sf = a.slots * a.pf, sdy = a.slots * a.pdy, sdz = a.slots * a.pdz;
-    const long long s0 = a.slots * a.p0, s1 = a.slots * a.p1;
-    pdl_trigger();
-    if (a.whole)
-        for (int c = threadIdx.x; c < 2 * a.C; c += nt) held[c] = 0.0f;
-    __syncthreads();
-    pdl_wait();
-    float2 q[P], p[P], g2[P], acc[SUMS][P];
-#pragma unroll
-    for (int s = 0; s < SUMS; ++s)
-#pragma unroll
-        for (int i = 0; i < P; ++i) acc[s][i] = make_float2(0.0f, 0.0f);
-    l.params(g2, a.g2, 1.0f);
-    if (block && !a.gate) factors(l, a, 0, q, p);
-    for (int unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
-        const int n = unit / a.S, k0 = unit - n * a.S;
-        const int span = a.gate ? a.HW : a.rows;
-        const int r0 = n * span + min(span, k0 * a.run), r1 = n * span + min(span, (k0 + 1) * a.run);
-        int row = r0 + l.slot, asked = row;
-        const T *x = static_cast<const T *>(a.x) + row * a.px + l.first(0), *f = static_cast<const T *>(a.f) + row * a.pf + l.first(0);
-        const T *dy = static_cast<const T *>(a.dy) + row * a.pdy + l.first(0), *dz = static_cast<const T *>(a.dz) + row * a.pdz + l.first(0);
-        T *dx = static_cast<T *>(a.o0) + row * a.p0 + l.first(0), *df = static_cast<T *>(a.o1) + row * a.p1 + l.first(0);
-        if (!a.full) R::template blank<D * 4>(l, ring);  // (the sums were there between units)
-        const Raw *d = ring;
-        Raw *to = ring;
-        const float4 *sd = seen;
-        float4 *sto = seen;
-        // A row beyond the run counts as zeros.
-        auto ask = [&] {
-            if (asked < r1) {
-                if (copies) copy_async<16>(tc::smem_u32(sto), a.stats + asked);
-                R::ask(l, x, to);
-                if (block) R::ask(l, f, to + LINE);
-                if (stream) R::ask(l, dy, to + 2 * LINE);
-                if (norm) R::ask(l, dz, to + 3 * LINE);
-            } else {
-                if (copies) *sto = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-                for (int m = 0; m < 4; ++m) R::zero(to + m * LINE);
-            }
-            copy_commit();
-            asked += a.slots;
-            x += sx;
-            f += sf;
-            dy += sdy;
-            dz += sdz;
-            const bool last = to == ring + (D - 1) * STAGE;
-            to = last ? ring : to + STAGE;
-            sto = last ? seen : sto + 32 / line;
-        };
-#pragma unroll
-        for (int i = 0; i < (D > 1 ? D - 1 : 1); ++i) ask();
-        if (block && a.gate) factors(l, a, n, q, p);
-        for (int base = r0; base < r1; base += a.slots) {
-            const bool on = row < r1;
-            copy_wait<(D > 1 ? D - 2 : 0)>();
-            __syncwarp();
-            const float4 st = *sd;
-            float2 u[P], y[P], t[P];  // u^, y^, dY
-            R::get(d, y);
-            if (block) {
-                R::get(d + LINE, u);
-                const float2 r = both(st.y), c = both(-st.x * st.y);
-                if (ALL || a.b1)
-#pragma unroll
-                    for (int k = 0; k < P; ++k) y[k] = add2(y[k], p[k]);
-#pragma unroll
-                for (int k = 0; k < P; ++k) {
-                    u[k] = fma2(u[k], r, c);
-                    y[k] = fma2(q[k], u[k], y[k]);
-                }
-            }
-            if (stream) R::get(d + 2 * LINE, t);
-            else
-#pragma unroll
-                for (int k = 0; k < P; ++k) t[k] = make_float2(0.0f, 0.0f);
-            if (norm) {
-                float2 e[P], w = make_float2(0.0f, 0.0f), v = w;
-                R::get(d + 3 * LINE, e);
-                const float2 r = both(st.w), c = both(-st.z * st.w);
-                if (ALL || a.db2)
-#pragma unroll
-                    for (int k = 0; k < P; ++k) acc[SUM_B2][k] = add2(acc[SUM_B2][k], e[k]);
-#pragma unroll
-                for (int k = 0; k < P; ++k) {
-                    y[k] = fma2(y[k], r, c);
-                    acc[SUM_G2][k] = fma2(e[k], y[k], acc[SUM_G2][k]);
-                    e[k] = mul2(e[k], g2[k]);
-                    w = add2(w, e[k]);
-                    v = fma2(e[k], y[k], v);
-                }
-                const float2 s = sum(w.x + w.y, v.x + v.y);
-                const float2 my = both(-s.y * a.inv_c * st.w), m = both(s.x * mean_pre * st.w);
-#pragma unroll
-                for (int k = 0; k < P; ++k) t[k] = fma2(y[k], my, fma2(e[k], r, add2(t[k], m)));
-            }
-            const bool last = d == ring + (D - 1) * STAGE;
-            d = last ? ring : d + STAGE;
-            sd = last ? seen : sd + 32 / line;
-            if (D > 1) ask();
-            if (on) R::put(l, dx, t);
-            if (block) {
-                // (what the mean's terms leave in a row beyond the run is 0: its sums are)
-                if (ALL || a.want_b)
-#pragma unroll
-                    for (int k = 0; k < P; ++k) acc[SUM_B][k] = add2(acc[SUM_B][k], t[k]);
-#pragma unroll
-                for (int k = 0; k < P; ++k) {
-                    acc[SUM_A][k] = fma2(t[k], u[k], acc[SUM_A][k]);
-                    t[k] = mul2(t[k], q[k]);
-                }
-                if (a.post != CONV_NORM_NONE) {
-                    float2 w = make_float2(0.0f, 0.0f), v = w;
-#pragma unroll
-                    for (int k = 0; k < P; ++k) {
-                        w = add2(w, t[k]);
-                        v = fma2(t[k], u[k], v);
-                    }
-                    const float2 s = sum(w.x + w.y, v.x + v.y);
-                    const float2 r = both(st.y), mu = both(-s.y * a.inv_c * st.y);
-                    const float2 m = both(s.x * mean_post * st.y);
-#pragma unroll
-                    for (int k = 0; k < P; ++k) t[k] = fma2(u[k], mu, fma2(t[k], r, m));
-                }
-                if (on) R::put(l, df, t);
-            }
-            if (D == 1) {
-                __syncwarp();
-                ask();
-            }
-            row += a.slots;
-            dx += s0;
-            df += s1;
-        }
-        copy_wait<0>();
-        float2 *ent = reinterpret_cast<float2 *>(smem);
-        if (a.whole) {  // the image's sums are complete
-            combine<SUM_A, 2, VEC, K>(l, a.slots, acc, ent, [&](int s, int c, float v) {
-                const float gate = a.gate[(long long)n * a.C + c];
-                held[s * a.C + c] += gate * v;
-                if (a.dgate) {
-                    const float k = (a.scale ? a.scale[c] : 1.0f) * (s == SUM_A ? (a.g1 ? a.g1[c] : 1.0f) : (a.b1 ? a.b1[c] : 0.0f)) * v;
-                    // (A and B of a channel are two threads': they meet in the CTA's part of the workspace)
-                    a.part[((long long)blockIdx.x * SUMS + s) * a.Cp + c] = k;
-                }
-            });
-            if (a.dgate) {
-                __syncthreads();
-                const float *one = a.part + (long long)blockIdx.x * SUMS * a.Cp;
-                for (int c = threadIdx.x; c < a.C; c += nt) a.dgate[(long long)n * a.C + c] = one[c] + one[a.Cp + c];
-                __syncthreads();
-            }
-#pragma unroll
-            for (int i = 0; i < P; ++i) acc[SUM_A][i] = acc[SUM_B][i] = make_float2(0.0f, 0.0f);
-        } else {
-            combine<0, SUMS, VEC, K>(l, a.slots, acc, ent, [&](int s, int c, float v) {
-                a.part[((long long)unit * SUMS + s) * a.Cp + c] = v;
-            });
-        }
-    }
-    if (a.whole) {
-        combine<SUM_G2, 2, VEC, K>(l, a.slots, acc, reinterpret_cast<float2 *>(smem), [&](int s, int c, float v) {
-            a.part[((long long)blockIdx.x * SUMS + s) * a.Cp + c] = v;
-        });
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.C; c += nt) {
-            float *one = a.part + (long long)blockIdx.x * SUMS * a.Cp + c;
-            one[0] = held[c];
-            one[a.Cp] = held[a.C + c];
-        }
-    }
-}
-
-// Joins the units' sums: a CTA takes sixteen channels, four a thread, and 128
-// units at a time.  Blocks y = 0 sum over all units; those above an image's
-// units for its dgate, an image a warp.
-constexpr int kJoin = 512, kJoinC = 16;
-__device__ __forceinline__ void add4(float4 &s, const float4 &v, float k) {
-    s.x = fmaf(k, v.x, s.x);
-    s.y = fmaf(k, v.y, s.y);
-    s.z = fmaf(k, v.z, s.z);
-    s.w = fmaf(k, v.w, s.w);
-}
-__device__ __forceinline__ float4 sum8(float4 v) {  // over the lanes of one four of channels
-#pragma unroll
-    for (int o = 4; o < 32; o *= 2) {
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
-        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-        v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
-        v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
-    }
-    return v;
-}
-__global__ void __launch_bounds__(kJoin) bn_join_kernel(const __grid_constant__ BnArgs a, int parts) {
-    __shared__ float4 red[SUMS][kJoin / 32][kJoinC / 4];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, four = lane & 3, group = lane >> 2;
-    const int c = blockIdx.x * kJoinC + four * 4;  // (channels are padded to fours in the workspace)
-    const bool on = c < a.C;
-    pdl_trigger();
-    pdl_wait();
-    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    if (blockIdx.y > 0) {
-        const int n = (blockIdx.y - 1) * (kJoin / 32) + warp;
-        float4 A = zero, B = zero;
-        if (n < a.N && on)
-            for (int s = group; s < a.S; s += 8) {
-                const float *u = a.part + ((long long)n * a.S + s) * SUMS * a.Cp + c;
-                add4(A, *reinterpret_cast<const float4 *>(u + SUM_A * a.Cp), 1.0f);
-                add4(B, *reinterpret_cast<const float4 *>(u + SUM_B * a.Cp), 1.0f);
-            }
-        A = sum8(A);
-        B = sum8(B);
-        if (n < a.N && group < 4 && c + group < a.C) {
-            const int k = c + group;
-            const float g1 = a.g1 ? a.g1[k] : 1.0f, b1 = a.b1 ? a.b1[k] : 0.0f;
-            const float va = group == 0 ? A.x : (group == 1 ? A.y : (group == 2 ? A.z : A.w));
-            const float vb = group == 0 ? B.x : (group == 1 ? B.y : (group == 2 ? B.z : B.w));
-            a.dgate[(long long)n * a.C + k] = (a.scale ? a.scale[k] : 1.0f) * (g1 * va + b1 * vb);
-        }
-        return;
-    }
-    float4 v[SUMS] = {zero, zero, zero, zero};
-    const bool gated = a.gate && !a.whole;
-    if (on)
-        for (int u = warp * 8 + group; u < parts; u += kJoin / 4) {
-            const float4 *one = reinterpret_cast<const float4 *>(a.part + (long long)u * SUMS * a.Cp + c);
-            float4 w[SUMS];
-#pragma unroll
-            for (int s = 0; s < SUMS; ++s) w[s] = one[s * (a.Cp / 4)];
-            if (gated) {
-                const float *g = a.gate + (long long)(u / a.S) * a.C + c;
-                const float4 k = make_float4(g[0], c + 1 < a.C ? g[1] : 0.0f, c + 2 < a.C ? g[2] : 0.0f, c + 3 < a.C ? g[3] : 0.0f);
-#pragma unroll
-                for (int s = 0; s < SUM_G2; ++s) w[s] = make_float4(k.x * w[s].x, k.y * w[s].y, k.z * w[s].z, k.w * w[s].w);
-            }
-#pragma unroll
-            for (int s = 0; s < SUMS; ++s) add4(v[s], w[s], 1.0f);
-        }
-#pragma unroll
-    for (int s = 0; s < SUMS; ++s) {
-        v[s] = sum8(v[s]);
-        if (group == 0) red[s][warp][four] = v[s];
-    }
-    __syncthreads();
-    if (warp == 0) {  // a channel a lane, twice
-        const int at = lane & 15, k = blockIdx.x * kJoinC + at;
-        float t[SUMS];
-#pragma unroll
-        for (int s = 0; s < SUMS; ++s) {
-            t[s] = 0.0f;
-            const float *r = reinterpret_cast<const float *>(red[s]) + at;
-            for (int w = lane >> 4; w < kJoin / 32; w += 2) t[s] += r[w * kJoinC];
-            t[s] += __shfl_xor_sync(0xffffffffu, t[s], 16);
-        }
-        if (lane < 16 && k < a.C) {
-            const float sc = a.scale ? a.scale[k] : 1.0f;
-            if (a.dscale) a.dscale[k] = (a.g1 ? a.g1[k] : 1.0f) * t[SUM_A] + (a.b1 ? a.b1[k] : 0.0f) * t[SUM_B];
-            if (a.dg1) a.dg1[k] = sc * t[SUM_A];
-            if (a.db1) a.db1[k] = sc * t[SUM_B];
-            if (a.dg2) a.dg2[k] = t[SUM_G2];
-            if (a.db2) a.db2[k] = t[SUM_B2];
-        }
-    }
-}
-
 // ------------------------------------------------------------------ host side
 template <typename T, int VEC>
-const void *pick_fwd(int k, int rb) {
-    if (rb == 2) return (const void *)&bn_fwd_kernel<T, VEC, 1, 2>;
-    return k == 1 ? (const void *)&bn_fwd_kernel<T, VEC, 1, 1> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1>;
-}
-template <typename T, int VEC>
-const void *pick_bwd(int k, int tpr, bool all) {
-    if (k == 2) return all ? (const void *)&bn_bwd_kernel<T, VEC, 2, ROW_WARPS, true> : (const void *)&bn_bwd_kernel<T, VEC, 2, ROW_WARPS, false>;
-    if (!all) return (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_ANY, false>;
-    return tpr < 32 ? (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_PART, true>
-                    : (tpr == 32 ? (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_WARP, true> : (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_WARPS, true>);
+const void *pick_fwd(int k, int rb, int tpr, bool all) {
+    if (k == 2) return all ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, true> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, false>;
+    if (rb == 1) return (const void *)&bn_fwd_kernel<T, VEC, 1, 1, ROW_ANY, false>;
+    if (!all) return (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_ANY, false>;
+    return tpr < 32 ? (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_PART, true>
+                    : (tpr == 32 ? (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_WARP, true> : (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_WARPS, true>);
 }
 // (rb: rows at a time of the forward kernel, 0: the gradient)
 const void *pick_kernel(conv_dtype_t dt, int vec, int rb, int k, int tpr, bool all) {
     using B = __nv_bfloat16;
-    if (rb) {
-        if (dt == CONV_F32) return vec == 4 ? pick_fwd<float, 4>(k, rb) : pick_fwd<float, 1>(k, rb);
-        return vec == 8 ? pick_fwd<B, 8>(k, rb) : (vec == 2 ? pick_fwd<B, 2>(k, rb) : pick_fwd<B, 1>(k, rb));
-    }
-    if (dt == CONV_F32) return vec == 4 ? pick_bwd<float, 4>(k, tpr, all) : pick_bwd<float, 1>(k, tpr, all);
-    return vec == 8 ? pick_bwd<B, 8>(k, tpr, all) : (vec == 2 ? pick_bwd<B, 2>(k, tpr, all) : pick_bwd<B, 1>(k, tpr, all));
+    if (!rb) return bn::pick_bwd(dt, vec, k, tpr, all);
+    if (dt == CONV_F32) return vec == 4 ? pick_fwd<float, 4>(k, rb, tpr, all) : pick_fwd<float, 1>(k, rb, tpr, all);
+    return vec == 8 ? pick_fwd<B, 8>(k, rb, tpr, all) : (vec == 2 ? pick_fwd<B, 2>(k, rb, tpr, all) : pick_fwd<B, 1>(k, rb, tpr, all));
 }
 
 // Channels a vector access takes: the widest that the channel count, every
@@ -753,7 +182,7 @@ size_t ring_bytes(const BnGeom &g, const BnGeom::Part &d, int es) {
 }
 
 cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a, size_t smem, cudaStream_t st) {
-    const void *k = pick_kernel(p->dtype, vec, d.rb, p->bn.k, p->bn.tpr, a.f && a.dy && a.dz);
+    const void *k = pick_kernel(p->dtype, vec, d.rb, p->bn.k, p->bn.tpr, d.rb ? a.f && a.o0 && a.o1 : a.f && a.dy && a.dz);
     if (smem > 40 * 1024) {  // (with the kernel's static shared memory: 48 KB are free)
         const int rc = conv_grant_smem_once(k, p->device, (int)smem);
         if (rc != CONV_OK) return cudaErrorInvalidValue;
@@ -1024,8 +453,5 @@ extern "C" int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, in
     if (launch(p, g, vec_for(p, all), a, smem, st) != cudaSuccess) return CONV_ERR_CUDA;
     const bool sums = d.scale || d.post_gamma || d.post_beta || d.pre_gamma || d.pre_beta, images = d.gate && !g.whole;
     if (!sums && !images) return CONV_OK;
-    int parts = g.grid;
-    void *args[] = {&a, &parts};
-    const dim3 grid((unsigned)((C + kJoinC - 1) / kJoinC), 1 + (unsigned)(images ? (a.N + kJoin / 32 - 1) / (kJoin / 32) : 0));
-    return conv_launch((const void *)&bn_join_kernel, grid, dim3(kJoin), args, 0, st) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+    return launch_join(a, g.grid, st) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }

@@ -1,0 +1,352 @@
+// The gradient of the norms around a block (k_blocknorm.cu has the formulas).
+#include "blocknorm.cuh"
+
+namespace bn {
+
+// The sums of the CTA's threads over the rows side by side: take(sum, pair's
+// first channel, value), each channel by one thread.  ent: shared, of NS x
+// threads x P pairs; free on entry, free again on return.
+template <int FIRST, int NS, int VEC, int K, typename F>
+__device__ __forceinline__ void combine(const Lane<VEC, K> &l, int slots, const float2 (&acc)[SUMS][4 * K], float2 *ent, F &&take) {
+    constexpr int P = 4 * K;
+    if (slots == 1) {
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                if (l.has(i, 0)) take(FIRST + s, l.chan(i, 0), acc[FIRST + s][i].x);
+                if (l.has(i, 1)) take(FIRST + s, l.chan(i, 1), acc[FIRST + s][i].y);
+            }
+        return;
+    }
+    __syncthreads();
+    const int nt = blockDim.x;
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int i = 0; i < P; ++i) ent[(s * P + i) * nt + threadIdx.x] = acc[FIRST + s][i];
+    __syncthreads();
+    // one (sum, pair, thread of a row) at a time, those of a sum next to one another
+    for (int k = threadIdx.x; k < NS * P * l.tpr; k += nt) {
+        const int at = k / l.tpr, t = k - at * l.tpr;
+        const float2 *e = ent + at * nt + t;
+        float2 v = e[0];
+        for (int r = 1; r < slots; ++r) v = add2(v, e[r * l.tpr]);
+        Lane<VEC, K> o = l;
+        o.t = t;
+        const int s = at / P, i = at - s * P;
+        if (o.has(i, 0)) take(FIRST + s, o.chan(i, 0), v.x);
+        if (o.has(i, 1)) take(FIRST + s, o.chan(i, 1), v.y);
+    }
+    __syncthreads();
+}
+
+// dx and df of the rows of a CTA's units, and the units' channel sums.  ALL: the
+// block, dy and dz are given; what is then not asked for is formed all the same,
+// which is fewer instructions than asking.
+template <typename T, int VEC, int K, int ROW, bool ALL>
+__global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_constant__ BnArgs a) {
+    using R = Row<T, VEC, K>;
+    using Raw = typename R::Raw;
+    constexpr int P = R::P, D = bwd_stages(sizeof(T), K), LINE = R::NV * R::step, STAGE = 4 * LINE;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float meet[2 * kMostThreads / 32 * 2];
+    const int nt = blockDim.x;
+    Raw *ring = R::ring(smem, D * 4);  // [D][x, f, dy, dz]
+    const Lane<VEC, K> l(a);
+    // statistics [warp][D][rows of a warp], copied by a lane of each row
+    const int line = l.tpr < 32 ? l.tpr : 32, lane = threadIdx.x & 31;
+    float4 *const seen = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Raw)) +
+                         (threadIdx.x >> 5) * (D * (32 / line)) + lane / line;
+    const bool copies = lane % line == 0;
+    float *held = reinterpret_cast<float *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Raw) + (size_t)D * (nt / line) * 16);  // whole images: gate A, gate B [2][C]
+    RowSum<ROW> sum(a.tpr, l.slot, meet);
+    const bool block = ALL || a.f, stream = ALL || a.dy, norm = ALL || a.dz;
+    const float mean_post = a.post == CONV_NORM_LAYER ? -a.inv_c : 0.0f, mean_pre = a.pre == CONV_NORM_LAYER ? -a.inv_c : 0.0f;
+    const long long sx = a.slots * a.px, sf = a.slots * a.pf, sdy = a.slots * a.pdy, sdz = a.slots * a.pdz;
+    const long long s0 = a.slots * a.p0, s1 = a.slots * a.p1;
+    pdl_trigger();
+    if (a.whole)
+        for (int c = threadIdx.x; c < 2 * a.C; c += nt) held[c] = 0.0f;
+    __syncthreads();
+    pdl_wait();
+    float2 q[P], p[P], g2[P], acc[SUMS][P];
+#pragma unroll
+    for (int s = 0; s < SUMS; ++s)
+#pragma unroll
+        for (int i = 0; i < P; ++i) acc[s][i] = make_float2(0.0f, 0.0f);
+    l.params(g2, a.g2, 1.0f);
+    if (block && !a.gate) factors(l, a, 0, q, p);
+    for (int unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
+        const int n = unit / a.S, k0 = unit - n * a.S;
+        const int span = a.gate ? a.HW : a.rows;
+        const int r0 = n * span + min(span, k0 * a.run), r1 = n * span + min(span, (k0 + 1) * a.run);
+        int row = r0 + l.slot, asked = row;
+        const T *x = static_cast<const T *>(a.x) + row * a.px + l.first(0), *f = static_cast<const T *>(a.f) + row * a.pf + l.first(0);
+        const T *dy = static_cast<const T *>(a.dy) + row * a.pdy + l.first(0), *dz = static_cast<const T *>(a.dz) + row * a.pdz + l.first(0);
+        T *dx = static_cast<T *>(a.o0) + row * a.p0 + l.first(0), *df = static_cast<T *>(a.o1) + row * a.p1 + l.first(0);
+        if (!a.full) R::template blank<D * 4>(l, ring);  // (the sums were there between units)
+        const Raw *d = ring;
+        Raw *to = ring;
+        const float4 *sd = seen;
+        float4 *sto = seen;
+        // A row beyond the run counts as zeros.
+        auto ask = [&] {
+            if (asked < r1) {
+                if (copies) copy_async<16>(tc::smem_u32(sto), a.stats + asked);
+                R::ask(l, x, to);
+                if (block) R::ask(l, f, to + LINE);
+                if (stream) R::ask(l, dy, to + 2 * LINE);
+                if (norm) R::ask(l, dz, to + 3 * LINE);
+            } else {
+                if (copies) *sto = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) R::zero(to + m * LINE);
+            }
+            copy_commit();
+            asked += a.slots;
+            x += sx;
+            f += sf;
+            dy += sdy;
+            dz += sdz;
+            const bool last = to == ring + (D - 1) * STAGE;
+            to = last ? ring : to + STAGE;
+            sto = last ? seen : sto + 32 / line;
+        };
+#pragma unroll
+        for (int i = 0; i < (D > 1 ? D - 1 : 1); ++i) ask();
+        if (block && a.gate) factors(l, a, n, q, p);
+        for (int base = r0; base < r1; base += a.slots) {
+            const bool on = row < r1;
+            copy_wait<(D > 1 ? D - 2 : 0)>();
+            __syncwarp();
+            const float4 st = *sd;
+            float2 u[P], y[P], t[P];  // u^, y^, dY
+            R::get(d, y);
+            if (block) {
+                R::get(d + LINE, u);
+                const float2 r = both(st.y), c = both(-st.x * st.y);
+                if (ALL || a.b1)
+#pragma unroll
+                    for (int k = 0; k < P; ++k) y[k] = add2(y[k], p[k]);
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    u[k] = fma2(u[k], r, c);
+                    y[k] = fma2(q[k], u[k], y[k]);
+                }
+            }
+            if (stream) R::get(d + 2 * LINE, t);
+            else
+#pragma unroll
+                for (int k = 0; k < P; ++k) t[k] = make_float2(0.0f, 0.0f);
+            if (norm) {
+                float2 e[P], w = make_float2(0.0f, 0.0f), v = w;
+                R::get(d + 3 * LINE, e);
+                const float2 r = both(st.w), c = both(-st.z * st.w);
+                if (ALL || a.db2)
+#pragma unroll
+                    for (int k = 0; k < P; ++k) acc[SUM_B2][k] = add2(acc[SUM_B2][k], e[k]);
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    y[k] = fma2(y[k], r, c);
+                    acc[SUM_G2][k] = fma2(e[k], y[k], acc[SUM_G2][k]);
+                    e[k] = mul2(e[k], g2[k]);
+                    w = add2(w, e[k]);
+                    v = fma2(e[k], y[k], v);
+                }
+                const float2 s = sum(w.x + w.y, v.x + v.y);
+                const float2 my = both(-s.y * a.inv_c * st.w), m = both(s.x * mean_pre * st.w);
+#pragma unroll
+                for (int k = 0; k < P; ++k) t[k] = fma2(y[k], my, fma2(e[k], r, add2(t[k], m)));
+            }
+            const bool last = d == ring + (D - 1) * STAGE;
+            d = last ? ring : d + STAGE;
+            sd = last ? seen : sd + 32 / line;
+            if (D > 1) ask();
+            if (on) R::put(l, dx, t);
+            if (block) {
+                // (what the mean's terms leave in a row beyond the run is 0: its sums are)
+                if (ALL || a.want_b)
+#pragma unroll
+                    for (int k = 0; k < P; ++k) acc[SUM_B][k] = add2(acc[SUM_B][k], t[k]);
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    acc[SUM_A][k] = fma2(t[k], u[k], acc[SUM_A][k]);
+                    t[k] = mul2(t[k], q[k]);
+                }
+                if (a.post != CONV_NORM_NONE) {
+                    float2 w = make_float2(0.0f, 0.0f), v = w;
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        w = add2(w, t[k]);
+                        v = fma2(t[k], u[k], v);
+                    }
+                    const float2 s = sum(w.x + w.y, v.x + v.y);
+                    const float2 r = both(st.y), mu = both(-s.y * a.inv_c * st.y);
+                    const float2 m = both(s.x * mean_post * st.y);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) t[k] = fma2(u[k], mu, fma2(t[k], r, m));
+                }
+                if (on) R::put(l, df, t);
+            }
+            if (D == 1) {
+                __syncwarp();
+                ask();
+            }
+            row += a.slots;
+            dx += s0;
+            df += s1;
+        }
+        copy_wait<0>();
+        float2 *ent = reinterpret_cast<float2 *>(smem);
+        if (a.whole) {  // the image's sums are complete
+            combine<SUM_A, 2, VEC, K>(l, a.slots, acc, ent, [&](int s, int c, float v) {
+                const float gate = a.gate[(long long)n * a.C + c];
+                held[s * a.C + c] += gate * v;
+                if (a.dgate) {
+                    const float k = (a.scale ? a.scale[c] : 1.0f) * (s == SUM_A ? (a.g1 ? a.g1[c] : 1.0f) : (a.b1 ? a.b1[c] : 0.0f)) * v;
+                    // (A and B of a channel are two threads': they meet in the CTA's part of the workspace)
+                    a.part[((long long)blockIdx.x * SUMS + s) * a.Cp + c] = k;
+                }
+            });
+            if (a.dgate) {
+                __syncthreads();
+                const float *one = a.part + (long long)blockIdx.x * SUMS * a.Cp;
+                for (int c = threadIdx.x; c < a.C; c += nt) a.dgate[(long long)n * a.C + c] = one[c] + one[a.Cp + c];
+                __syncthreads();
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i) acc[SUM_A][i] = acc[SUM_B][i] = make_float2(0.0f, 0.0f);
+        } else {
+            combine<0, SUMS, VEC, K>(l, a.slots, acc, ent, [&](int s, int c, float v) {
+                a.part[((long long)unit * SUMS + s) * a.Cp + c] = v;
+            });
+        }
+    }
+    if (a.whole) {
+        combine<SUM_G2, 2, VEC, K>(l, a.slots, acc, reinterpret_cast<float2 *>(smem), [&](int s, int c, float v) {
+            a.part[((long long)blockIdx.x * SUMS + s) * a.Cp + c] = v;
+        });
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.C; c += nt) {
+            float *one = a.part + (long long)blockIdx.x * SUMS * a.Cp + c;
+            one[0] = held[c];
+            one[a.Cp] = held[a.C + c];
+        }
+    }
+}
+
+// Joins the units' sums: a CTA takes sixteen channels, four a thread, and 128
+// units at a time.  Blocks y = 0 sum over all units; those above an image's
+// units for its dgate, an image a warp.
+constexpr int kJoin = 512, kJoinC = 16;
+__device__ __forceinline__ void add4(float4 &s, const float4 &v, float k) {
+    s.x = fmaf(k, v.x, s.x);
+    s.y = fmaf(k, v.y, s.y);
+    s.z = fmaf(k, v.z, s.z);
+    s.w = fmaf(k, v.w, s.w);
+}
+__device__ __forceinline__ float4 sum8(float4 v) {  // over the lanes of one four of channels
+#pragma unroll
+    for (int o = 4; o < 32; o *= 2) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, o);
+        v.w += __shfl_xor_sync(0xffffffffu, v.w, o);
+    }
+    return v;
+}
+__global__ void __launch_bounds__(kJoin) bn_join_kernel(const __grid_constant__ BnArgs a, int parts) {
+    __shared__ float4 red[SUMS][kJoin / 32][kJoinC / 4];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, four = lane & 3, group = lane >> 2;
+    const int c = blockIdx.x * kJoinC + four * 4;  // (channels are padded to fours in the workspace)
+    const bool on = c < a.C;
+    pdl_trigger();
+    pdl_wait();
+    const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (blockIdx.y > 0) {
+        const int n = (blockIdx.y - 1) * (kJoin / 32) + warp;
+        float4 A = zero, B = zero;
+        if (n < a.N && on)
+            for (int s = group; s < a.S; s += 8) {
+                const float *u = a.part + ((long long)n * a.S + s) * SUMS * a.Cp + c;
+                add4(A, *reinterpret_cast<const float4 *>(u + SUM_A * a.Cp), 1.0f);
+                add4(B, *reinterpret_cast<const float4 *>(u + SUM_B * a.Cp), 1.0f);
+            }
+        A = sum8(A);
+        B = sum8(B);
+        if (n < a.N && group < 4 && c + group < a.C) {
+            const int k = c + group;
+            const float g1 = a.g1 ? a.g1[k] : 1.0f, b1 = a.b1 ? a.b1[k] : 0.0f;
+            const float va = group == 0 ? A.x : (group == 1 ? A.y : (group == 2 ? A.z : A.w));
+            const float vb = group == 0 ? B.x : (group == 1 ? B.y : (group == 2 ? B.z : B.w));
+            a.dgate[(long long)n * a.C + k] = (a.scale ? a.scale[k] : 1.0f) * (g1 * va + b1 * vb);
+        }
+        return;
+    }
+    float4 v[SUMS] = {zero, zero, zero, zero};
+    const bool gated = a.gate && !a.whole;
+    if (on)
+        for (int u = warp * 8 + group; u < parts; u += kJoin / 4) {
+            const float4 *one = reinterpret_cast<const float4 *>(a.part + (long long)u * SUMS * a.Cp + c);
+            float4 w[SUMS];
+#pragma unroll
+            for (int s = 0; s < SUMS; ++s) w[s] = one[s * (a.Cp / 4)];
+            if (gated) {
+                const float *g = a.gate + (long long)(u / a.S) * a.C + c;
+                const float4 k = make_float4(g[0], c + 1 < a.C ? g[1] : 0.0f, c + 2 < a.C ? g[2] : 0.0f, c + 3 < a.C ? g[3] : 0.0f);
+#pragma unroll
+                for (int s = 0; s < SUM_G2; ++s) w[s] = make_float4(k.x * w[s].x, k.y * w[s].y, k.z * w[s].z, k.w * w[s].w);
+            }
+#pragma unroll
+            for (int s = 0; s < SUMS; ++s) add4(v[s], w[s], 1.0f);
+        }
+#pragma unroll
+    for (int s = 0; s < SUMS; ++s) {
+        v[s] = sum8(v[s]);
+        if (group == 0) red[s][warp][four] = v[s];
+    }
+    __syncthreads();
+    if (warp == 0) {  // a channel a lane, twice
+        const int at = lane & 15, k = blockIdx.x * kJoinC + at;
+        float t[SUMS];
+#pragma unroll
+        for (int s = 0; s < SUMS; ++s) {
+            t[s] = 0.0f;
+            const float *r = reinterpret_cast<const float *>(red[s]) + at;
+            for (int w = lane >> 4; w < kJoin / 32; w += 2) t[s] += r[w * kJoinC];
+            t[s] += __shfl_xor_sync(0xffffffffu, t[s], 16);
+        }
+        if (lane < 16 && k < a.C) {
+            const float sc = a.scale ? a.scale[k] : 1.0f;
+            if (a.dscale) a.dscale[k] = (a.g1 ? a.g1[k] : 1.0f) * t[SUM_A] + (a.b1 ? a.b1[k] : 0.0f) * t[SUM_B];
+            if (a.dg1) a.dg1[k] = sc * t[SUM_A];
+            if (a.db1) a.db1[k] = sc * t[SUM_B];
+            if (a.dg2) a.dg2[k] = t[SUM_G2];
+            if (a.db2) a.db2[k] = t[SUM_B2];
+        }
+    }
+}
+
+template <typename T, int VEC>
+const void *pick(int k, int tpr, bool all) {
+    if (k == 2) return all ? (const void *)&bn_bwd_kernel<T, VEC, 2, ROW_WARPS, true> : (const void *)&bn_bwd_kernel<T, VEC, 2, ROW_WARPS, false>;
+    if (!all) return (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_ANY, false>;
+    return tpr < 32 ? (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_PART, true>
+                    : (tpr == 32 ? (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_WARP, true> : (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_WARPS, true>);
+}
+const void *pick_bwd(conv_dtype_t dt, int vec, int k, int tpr, bool all) {
+    using B = __nv_bfloat16;
+    if (dt == CONV_F32) return vec == 4 ? pick<float, 4>(k, tpr, all) : pick<float, 1>(k, tpr, all);
+    return vec == 8 ? pick<B, 8>(k, tpr, all) : (vec == 2 ? pick<B, 2>(k, tpr, all) : pick<B, 1>(k, tpr, all));
+}
+
+cudaError_t launch_join(const BnArgs &a, int parts, cudaStream_t st) {
+    BnArgs b = a;
+    void *args[] = {&b, &parts};
+    const bool images = a.dgate && !a.whole;
+    const dim3 grid((unsigned)((a.C + kJoinC - 1) / kJoinC), 1 + (unsigned)(images ? (a.N + kJoin / 32 - 1) / (kJoin / 32) : 0));
+    return conv_launch((const void *)&bn_join_kernel, grid, dim3(kJoin), args, 0, st);
+}
+
+}  // namespace bn
