@@ -177,8 +177,8 @@ static_assert(3 * 4 * 8 * 2 >= SUMS * 8 * 4, "");
 size_t ring_bytes(const BnGeom &g, const BnGeom::Part &d, int es) {
     const size_t maps = (size_t)d.threads * 8 * g.k * es;
     if (d.rb) return 2 * kFwdStages * d.rb * maps;
-    const int stages = bwd_stages(es, g.k);  // (and a row's statistics)
-    return stages * (4 * maps + (size_t)d.threads / (g.tpr < 32 ? g.tpr : 32) * 16);
+    const int stages = bwd_stages(es, g.k);  // (and a row's statistics, and the parameters of long rows)
+    return stages * (4 * maps + (size_t)d.threads / (g.tpr < 32 ? g.tpr : 32) * 16) + (g.k > 1 ? (size_t)d.threads * 3 * 8 * g.k * 4 : 0);
 }
 
 cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a, size_t smem, cudaStream_t st) {
@@ -449,8 +449,7 @@ extern "C" int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, in
     a.want_b = d.post_beta || (w.post_beta && (d.scale || d.gate));
     const BnGeom::Part &g = w.gate ? p->bn.bwd_gated : p->bn.bwd;
     const Map all[6] = {in[0], in[1], in[2], in[3], out[0], out[1]};
-    const size_t smem = ring_bytes(p->bn, g, es) + (g.whole ? 2 * cb : 0);
-    if (launch(p, g, vec_for(p, all), a, smem, st) != cudaSuccess) return CONV_ERR_CUDA;
+    if (launch(p, g, vec_for(p, all), a, ring_bytes(p->bn, g, es), st) != cudaSuccess) return CONV_ERR_CUDA;
     const bool sums = d.scale || d.post_gamma || d.post_beta || d.pre_gamma || d.pre_beta, images = d.gate && !g.whole;
     if (!sums && !images) return CONV_OK;
     return launch_join(a, g.grid, st) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;

@@ -3,12 +3,12 @@
 
 namespace bn {
 
-// The sums of the CTA's threads over the rows side by side: take(sum, pair's
-// first channel, value), each channel by one thread.  ent: shared, of NS x
-// threads x P pairs; free on entry, free again on return.
-template <int FIRST, int NS, int VEC, int K, typename F>
-__device__ __forceinline__ void combine(const Lane<VEC, K> &l, int slots, const float2 (&acc)[SUMS][4 * K], float2 *ent, F &&take) {
-    constexpr int P = 4 * K;
+// The sums of the CTA's threads over the rows side by side: take(sum, channel,
+// value) for the sums FIRST and on, each by one thread, in every call the same.
+// ent: shared, NS x P pairs a thread; free on entry, free again on return.
+template <int FIRST, int NS, int VEC, typename F>
+__device__ __forceinline__ void combine(const Lane<VEC, 1> &l, int slots, float2 (&acc)[SUMS][4], float2 *ent, F &&take) {
+    constexpr int P = 4;
     if (slots == 1) {
 #pragma unroll
         for (int s = 0; s < NS; ++s)
@@ -19,20 +19,33 @@ __device__ __forceinline__ void combine(const Lane<VEC, K> &l, int slots, const 
             }
         return;
     }
+    const int tpr = l.tpr, line = tpr < 32 ? tpr : 32;
+    // rows of a part of a warp: first those of the warp, to every lane
+    for (int o = line; o < 32; o *= 2)
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                float2 &v = acc[FIRST + s][i];
+                v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+                v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+            }
+    const int rows = tpr < 32 ? blockDim.x / 32 : slots, wide = rows * tpr;
+    const int me = tpr < 32 ? (threadIdx.x >> 5) * tpr + (threadIdx.x & 31) : threadIdx.x;
     __syncthreads();
-    const int nt = blockDim.x;
+    if ((threadIdx.x & 31) < line)
 #pragma unroll
-    for (int s = 0; s < NS; ++s)
+        for (int s = 0; s < NS; ++s)
 #pragma unroll
-        for (int i = 0; i < P; ++i) ent[(s * P + i) * nt + threadIdx.x] = acc[FIRST + s][i];
+            for (int i = 0; i < P; ++i) ent[(s * P + i) * wide + me] = acc[FIRST + s][i];
     __syncthreads();
     // one (sum, pair, thread of a row) at a time, those of a sum next to one another
-    for (int k = threadIdx.x; k < NS * P * l.tpr; k += nt) {
-        const int at = k / l.tpr, t = k - at * l.tpr;
-        const float2 *e = ent + at * nt + t;
+    for (int k = threadIdx.x; k < NS * P * tpr; k += blockDim.x) {
+        const int at = k / tpr, t = k - at * tpr;
+        const float2 *e = ent + at * wide + t;
         float2 v = e[0];
-        for (int r = 1; r < slots; ++r) v = add2(v, e[r * l.tpr]);
-        Lane<VEC, K> o = l;
+        for (int r = 1; r < rows; ++r) v = add2(v, e[r * tpr]);
+        Lane<VEC, 1> o = l;
         o.t = t;
         const int s = at / P, i = at - s * P;
         if (o.has(i, 0)) take(FIRST + s, o.chan(i, 0), v.x);
@@ -41,34 +54,43 @@ __device__ __forceinline__ void combine(const Lane<VEC, K> &l, int slots, const 
     __syncthreads();
 }
 
+// A sum's place in the workspace: of unit, or CTA, `at`.
+__device__ __forceinline__ float *place(const BnArgs &a, int at, int s, int c) { return a.part + ((long long)at * SUMS + s) * a.Cp + c; }
+// A unit that is a whole image gives its dgate at once and adds gate times its
+// sums to the CTA's.
+__device__ __forceinline__ void add_image(const BnArgs &a, int n, bool first, int s, int c, float v) {
+    float *p = place(a, blockIdx.x, s, c);
+    const float gate = a.gate[(long long)n * a.C + c];
+    *p = first ? gate * v : fmaf(gate, v, *p);
+}
+__device__ __forceinline__ float gate_grad(const BnArgs &a, int c, float A, float B) {
+    return (a.scale ? a.scale[c] : 1.0f) * ((a.g1 ? a.g1[c] : 1.0f) * A + (a.b1 ? a.b1[c] : 0.0f) * B);
+}
+
 // dx and df of the rows of a CTA's units, and the units' channel sums.  ALL: the
 // block, dy and dz are given; what is then not asked for is formed all the same,
 // which is fewer instructions than asking.
-template <typename T, int VEC, int K, int ROW, bool ALL>
+template <typename T, int VEC, int ROW, bool ALL>
 __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_constant__ BnArgs a) {
-    using R = Row<T, VEC, K>;
+    using R = Row<T, VEC, 1>;
     using Raw = typename R::Raw;
-    constexpr int P = R::P, D = bwd_stages(sizeof(T), K), LINE = R::NV * R::step, STAGE = 4 * LINE;
+    constexpr int P = R::P, D = bwd_stages(sizeof(T), 1), LINE = R::NV * R::step, STAGE = 4 * LINE;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float meet[2 * kMostThreads / 32 * 2];
     const int nt = blockDim.x;
     Raw *ring = R::ring(smem, D * 4);  // [D][x, f, dy, dz]
-    const Lane<VEC, K> l(a);
+    const Lane<VEC, 1> l(a);
     // statistics [warp][D][rows of a warp], copied by a lane of each row
     const int line = l.tpr < 32 ? l.tpr : 32, lane = threadIdx.x & 31;
     float4 *const seen = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Raw)) +
                          (threadIdx.x >> 5) * (D * (32 / line)) + lane / line;
     const bool copies = lane % line == 0;
-    float *held = reinterpret_cast<float *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Raw) + (size_t)D * (nt / line) * 16);  // whole images: gate A, gate B [2][C]
     RowSum<ROW> sum(a.tpr, l.slot, meet);
     const bool block = ALL || a.f, stream = ALL || a.dy, norm = ALL || a.dz;
     const float mean_post = a.post == CONV_NORM_LAYER ? -a.inv_c : 0.0f, mean_pre = a.pre == CONV_NORM_LAYER ? -a.inv_c : 0.0f;
     const long long sx = a.slots * a.px, sf = a.slots * a.pf, sdy = a.slots * a.pdy, sdz = a.slots * a.pdz;
     const long long s0 = a.slots * a.p0, s1 = a.slots * a.p1;
     pdl_trigger();
-    if (a.whole)
-        for (int c = threadIdx.x; c < 2 * a.C; c += nt) held[c] = 0.0f;
-    __syncthreads();
     pdl_wait();
     float2 q[P], p[P], g2[P], acc[SUMS][P];
 #pragma unroll
@@ -114,11 +136,11 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             sto = last ? seen : sto + 32 / line;
         };
 #pragma unroll
-        for (int i = 0; i < (D > 1 ? D - 1 : 1); ++i) ask();
+        for (int i = 0; i < D - 1; ++i) ask();
         if (block && a.gate) factors(l, a, n, q, p);
         for (int base = r0; base < r1; base += a.slots) {
             const bool on = row < r1;
-            copy_wait<(D > 1 ? D - 2 : 0)>();
+            copy_wait<D - 2>();
             __syncwarp();
             const float4 st = *sd;
             float2 u[P], y[P], t[P];  // u^, y^, dY
@@ -162,7 +184,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             const bool last = d == ring + (D - 1) * STAGE;
             d = last ? ring : d + STAGE;
             sd = last ? seen : sd + 32 / line;
-            if (D > 1) ask();
+            ask();
             if (on) R::put(l, dx, t);
             if (block) {
                 // (what the mean's terms leave in a row beyond the run is 0: its sums are)
@@ -189,50 +211,258 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
                 }
                 if (on) R::put(l, df, t);
             }
-            if (D == 1) {
-                __syncwarp();
-                ask();
-            }
             row += a.slots;
             dx += s0;
             df += s1;
         }
         copy_wait<0>();
         float2 *ent = reinterpret_cast<float2 *>(smem);
-        if (a.whole) {  // the image's sums are complete
-            combine<SUM_A, 2, VEC, K>(l, a.slots, acc, ent, [&](int s, int c, float v) {
-                const float gate = a.gate[(long long)n * a.C + c];
-                held[s * a.C + c] += gate * v;
-                if (a.dgate) {
-                    const float k = (a.scale ? a.scale[c] : 1.0f) * (s == SUM_A ? (a.g1 ? a.g1[c] : 1.0f) : (a.b1 ? a.b1[c] : 0.0f)) * v;
-                    // (A and B of a channel are two threads': they meet in the CTA's part of the workspace)
-                    a.part[((long long)blockIdx.x * SUMS + s) * a.Cp + c] = k;
-                }
+        if (a.whole) {
+            const bool first = unit == (int)blockIdx.x;
+            float *both_sums = reinterpret_cast<float *>(ent + 2 * P * nt);  // [A, B][C]: of a channel, two threads'
+            if (a.slots == 1) __syncthreads();
+            combine<SUM_A, 2, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) {
+                add_image(a, n, first, s, c, v);
+                both_sums[s * a.C + c] = v;
             });
             if (a.dgate) {
                 __syncthreads();
-                const float *one = a.part + (long long)blockIdx.x * SUMS * a.Cp;
-                for (int c = threadIdx.x; c < a.C; c += nt) a.dgate[(long long)n * a.C + c] = one[c] + one[a.Cp + c];
+                for (int c = threadIdx.x; c < a.C; c += nt) a.dgate[(long long)n * a.C + c] = gate_grad(a, c, both_sums[c], both_sums[a.C + c]);
                 __syncthreads();
             }
 #pragma unroll
             for (int i = 0; i < P; ++i) acc[SUM_A][i] = acc[SUM_B][i] = make_float2(0.0f, 0.0f);
-        } else {
-            combine<0, SUMS, VEC, K>(l, a.slots, acc, ent, [&](int s, int c, float v) {
-                a.part[((long long)unit * SUMS + s) * a.Cp + c] = v;
-            });
-        }
+        } else combine<0, SUMS, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { *place(a, unit, s, c) = v; });
     }
-    if (a.whole) {
-        combine<SUM_G2, 2, VEC, K>(l, a.slots, acc, reinterpret_cast<float2 *>(smem), [&](int s, int c, float v) {
-            a.part[((long long)blockIdx.x * SUMS + s) * a.Cp + c] = v;
-        });
-        __syncthreads();
-        for (int c = threadIdx.x; c < a.C; c += nt) {
-            float *one = a.part + (long long)blockIdx.x * SUMS * a.Cp + c;
-            one[0] = held[c];
-            one[a.Cp] = held[a.C + c];
+    if (a.whole)
+        combine<SUM_G2, 2, VEC>(l, a.slots, acc, reinterpret_cast<float2 *>(smem), [&](int s, int c, float v) { *place(a, blockIdx.x, s, c) = v; });
+}
+
+// The same for rows of more than 4096 channels: sixteen a thread, in two chunks
+// of eight.  Their sums take 64 registers, so that the parameters stay in shared
+// memory and a chunk's values are formed again of the ring where they are needed
+// again: 1.3 times the instructions a channel, no registers spilled (kept in
+// registers, 340 to 600 bytes of a thread's were, and 4096x8192 bf16 rms took
+// 174 us).
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kMostThreads) bn_bwd_long_kernel(const __grid_constant__ BnArgs a) {
+    using R = Row<T, VEC, 1>;
+    using Raw = typename R::Raw;
+    constexpr int H = 2, P = R::P, D = bwd_stages(sizeof(T), H), LINE = R::NV * R::step, MAP = H * LINE, STAGE = 4 * MAP;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ float meet[2 * kMostThreads / 32 * 2];
+    const int nt = blockDim.x;
+    Raw *ring = R::ring(smem, D * 4 * H);  // [D][x, f, dy, dz][H]
+    float4 *const par = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * H * R::NV * nt * sizeof(Raw)) + threadIdx.x;  // [q, p, g2][H][2][threads]
+    float4 *const seen = par - threadIdx.x + 3 * H * 2 * nt + (threadIdx.x >> 5) * D;  // statistics [warp][D]
+    Lane<VEC, 1> l[H] = {Lane<VEC, 1>(a), Lane<VEC, 1>(a)};
+    l[1].t += R::NV * a.tpr;
+    RowSum<ROW_WARPS> sum(a.tpr, 0, meet);
+    const bool block = a.f, stream = a.dy, norm = a.dz, copies = (threadIdx.x & 31) == 0;
+    const float mean_post = a.post == CONV_NORM_LAYER ? -a.inv_c : 0.0f, mean_pre = a.pre == CONV_NORM_LAYER ? -a.inv_c : 0.0f;
+    enum { PAR_Q, PAR_P, PAR_G2 };
+    auto set = [&](int which, int h, const float2 (&v)[P]) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) par[((which * H + h) * 2 + j) * nt] = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+    };
+    auto param = [&](int which, int h, float2 (&v)[P]) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float4 f = par[((which * H + h) * 2 + j) * nt];
+            v[2 * j] = make_float2(f.x, f.y);
+            v[2 * j + 1] = make_float2(f.z, f.w);
         }
+    };
+    pdl_trigger();
+    pdl_wait();
+    float2 acc[H][SUMS][P];
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+#pragma unroll
+        for (int s = 0; s < SUMS; ++s)
+#pragma unroll
+            for (int i = 0; i < P; ++i) acc[h][s][i] = make_float2(0.0f, 0.0f);
+        float2 g2[P];
+        l[h].params(g2, a.g2, 1.0f);
+        set(PAR_G2, h, g2);
+    }
+    auto set_factors = [&](int n) {
+#pragma unroll
+        for (int h = 0; h < H; ++h) {
+            float2 q[P], p[P];
+            factors(l[h], a, n, q, p);
+            set(PAR_Q, h, q);
+            set(PAR_P, h, p);
+        }
+    };
+    if (block && !a.gate) set_factors(0);
+    for (int unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
+        const int n = unit / a.S, k0 = unit - n * a.S;
+        const int span = a.gate ? a.HW : a.rows;
+        const int r0 = n * span + min(span, k0 * a.run), r1 = n * span + min(span, (k0 + 1) * a.run);
+        const int at = l[0].first(0), far = l[1].first(0) - at;
+        int asked = r0;
+        const T *x = static_cast<const T *>(a.x) + r0 * a.px + at, *f = static_cast<const T *>(a.f) + r0 * a.pf + at;
+        const T *dy = static_cast<const T *>(a.dy) + r0 * a.pdy + at, *dz = static_cast<const T *>(a.dz) + r0 * a.pdz + at;
+        T *dx = static_cast<T *>(a.o0) + r0 * a.p0 + at, *df = static_cast<T *>(a.o1) + r0 * a.p1 + at;
+        if (!a.full)
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                for (int i = 0; i < D * 4; ++i) R::template blank<1>(l[h], ring + i * MAP + h * LINE);
+        const Raw *d = ring;
+        Raw *to = ring;
+        const float4 *sd = seen;
+        float4 *sto = seen;
+        auto ask = [&] {
+            if (asked < r1) {
+                if (copies) copy_async<16>(tc::smem_u32(sto), a.stats + asked);
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    const int o = h ? far : 0;
+                    R::ask(l[h], x + o, to + h * LINE);
+                    if (block) R::ask(l[h], f + o, to + MAP + h * LINE);
+                    if (stream) R::ask(l[h], dy + o, to + 2 * MAP + h * LINE);
+                    if (norm) R::ask(l[h], dz + o, to + 3 * MAP + h * LINE);
+                }
+            }
+            copy_commit();
+            ++asked;
+            x += a.px;
+            f += a.pf;
+            dy += a.pdy;
+            dz += a.pdz;
+            const bool last = to == ring + (D - 1) * STAGE;
+            to = last ? ring : to + STAGE;
+            sto = last ? seen : sto + 1;
+        };
+        if (block && a.gate) set_factors(n);
+#pragma unroll
+        for (int i = 0; i < D; ++i) ask();
+        for (int row = r0; row < r1; ++row) {
+            copy_wait<D - 1>();
+            __syncwarp();
+            const float4 st = *sd;
+            const float2 ur = both(st.y), uc = both(-st.x * st.y), yr = both(st.w), yc = both(-st.z * st.w);
+            auto block_out = [&](int h, float2 (&u)[P]) {  // u^
+                R::get(d + MAP + h * LINE, u);
+#pragma unroll
+                for (int k = 0; k < P; ++k) u[k] = fma2(u[k], ur, uc);
+            };
+            auto stream_in = [&](int h, const float2 (&u)[P], float2 (&y)[P]) {  // y^
+                R::get(d + h * LINE, y);
+                if (block) {
+                    float2 q[P];
+                    param(PAR_P, h, q);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) y[k] = add2(y[k], q[k]);
+                    param(PAR_Q, h, q);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) y[k] = fma2(q[k], u[k], y[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < P; ++k) y[k] = fma2(y[k], yr, yc);
+            };
+            float2 s = make_float2(0.0f, 0.0f);
+            if (norm) {
+                float2 w = s, v = s;
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    float2 u[P], y[P], e[P], g2[P];
+                    if (block) block_out(h, u);
+                    stream_in(h, u, y);
+                    R::get(d + 3 * MAP + h * LINE, e);
+                    param(PAR_G2, h, g2);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        acc[h][SUM_G2][k] = fma2(e[k], y[k], acc[h][SUM_G2][k]);
+                        acc[h][SUM_B2][k] = add2(acc[h][SUM_B2][k], e[k]);
+                        e[k] = mul2(e[k], g2[k]);
+                        w = add2(w, e[k]);
+                        v = fma2(e[k], y[k], v);
+                    }
+                }
+                s = sum(w.x + w.y, v.x + v.y);
+            }
+            const float2 my = both(-s.y * a.inv_c * st.w), m = both(s.x * mean_pre * st.w);
+            float2 t[H][P], w = make_float2(0.0f, 0.0f), v = w;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                float2 u[P];
+                if (block) block_out(h, u);
+                if (stream) R::get(d + 2 * MAP + h * LINE, t[h]);
+                else
+#pragma unroll
+                    for (int k = 0; k < P; ++k) t[h][k] = make_float2(0.0f, 0.0f);
+                if (norm) {
+                    float2 y[P], e[P], g2[P];
+                    stream_in(h, u, y);
+                    R::get(d + 3 * MAP + h * LINE, e);
+                    param(PAR_G2, h, g2);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) t[h][k] = fma2(y[k], my, fma2(mul2(e[k], g2[k]), yr, add2(t[h][k], m)));
+                }
+                R::put(l[h], dx + (h ? far : 0), t[h]);
+                if (block) {
+                    float2 q[P];
+                    param(PAR_Q, h, q);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        acc[h][SUM_A][k] = fma2(t[h][k], u[k], acc[h][SUM_A][k]);
+                        acc[h][SUM_B][k] = add2(acc[h][SUM_B][k], t[h][k]);
+                        t[h][k] = mul2(t[h][k], q[k]);
+                        w = add2(w, t[h][k]);
+                        v = fma2(t[h][k], u[k], v);
+                    }
+                }
+            }
+            if (block) {
+                if (a.post != CONV_NORM_NONE) {
+                    const float2 z = sum(w.x + w.y, v.x + v.y);
+                    const float2 mu = both(-z.y * a.inv_c * st.y), mm = both(z.x * mean_post * st.y);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        float2 u[P];
+                        block_out(h, u);
+#pragma unroll
+                        for (int k = 0; k < P; ++k) t[h][k] = fma2(u[k], mu, fma2(t[h][k], ur, mm));
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < H; ++h) R::put(l[h], df + (h ? far : 0), t[h]);
+            }
+            const bool last = d == ring + (D - 1) * STAGE;
+            d = last ? ring : d + STAGE;
+            sd = last ? seen : sd + 1;
+            __syncwarp();  // (the statistics' place is written again)
+            ask();
+            dx += a.p0;
+            df += a.p1;
+        }
+        copy_wait<0>();
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (!l[h].has(i, e)) continue;
+                    const int c = l[h].chan(i, e);
+                    auto one = [&](int s) { return e ? acc[h][s][i].y : acc[h][s][i].x; };
+                    if (!a.whole) {
+#pragma unroll
+                        for (int s = 0; s < SUMS; ++s) *place(a, unit, s, c) = one(s);
+                        continue;
+                    }
+                    for (int s = 0; s < SUM_G2; ++s) add_image(a, n, unit == (int)blockIdx.x, s, c, one(s));
+                    if (a.dgate) a.dgate[(long long)n * a.C + c] = gate_grad(a, c, one(SUM_A), one(SUM_B));
+                    if (unit + (int)gridDim.x >= a.units)
+                        for (int s = SUM_G2; s < SUMS; ++s) *place(a, blockIdx.x, s, c) = one(s);
+                }
+        if (a.whole)
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int i = 0; i < P; ++i) acc[h][SUM_A][i] = acc[h][SUM_B][i] = make_float2(0.0f, 0.0f);
     }
 }
 
@@ -330,10 +560,10 @@ __global__ void __launch_bounds__(kJoin) bn_join_kernel(const __grid_constant__ 
 
 template <typename T, int VEC>
 const void *pick(int k, int tpr, bool all) {
-    if (k == 2) return all ? (const void *)&bn_bwd_kernel<T, VEC, 2, ROW_WARPS, true> : (const void *)&bn_bwd_kernel<T, VEC, 2, ROW_WARPS, false>;
-    if (!all) return (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_ANY, false>;
-    return tpr < 32 ? (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_PART, true>
-                    : (tpr == 32 ? (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_WARP, true> : (const void *)&bn_bwd_kernel<T, VEC, 1, ROW_WARPS, true>);
+    if (k == 2) return (const void *)&bn_bwd_long_kernel<T, VEC>;
+    if (!all) return (const void *)&bn_bwd_kernel<T, VEC, ROW_ANY, false>;
+    return tpr < 32 ? (const void *)&bn_bwd_kernel<T, VEC, ROW_PART, true>
+                    : (tpr == 32 ? (const void *)&bn_bwd_kernel<T, VEC, ROW_WARP, true> : (const void *)&bn_bwd_kernel<T, VEC, ROW_WARPS, true>);
 }
 const void *pick_bwd(conv_dtype_t dt, int vec, int k, int tpr, bool all) {
     using B = __nv_bfloat16;
