@@ -76,6 +76,10 @@ struct Lane {
     }
 };
 
+// Bytes of an element in the ring.  Single bf16 values, which no asynchronous copy
+// takes, come as the word that holds them (another two bytes of the same four).
+__host__ __device__ constexpr int ring_element(int es, int vec) { return es * vec < 4 ? 4 : es; }
+
 // A thread's vectors of one row: from its ring of shared memory, to a map, and
 // from a map to the ring.  Vectors beyond the row's end stay 0 in the ring.
 template <typename T, int VEC, int K>
@@ -83,23 +87,34 @@ struct Row {
     using V = Vec<T, VEC>;
     using Raw = typename V::Raw;
     using L = Lane<VEC, K>;
+    static constexpr bool kWord = sizeof(Raw) < 4;
+    using Slot = typename std::conditional<kWord, uint32_t, Raw>::type;
     static constexpr int NV = L::NV, P = L::P;
+    static constexpr int kElement = ring_element(sizeof(T), VEC);
     static constexpr int step = 32;  // of a thread's vectors in the ring: a warp's lie together
     // the thread's first vector in a ring of `rows` rows
-    __device__ static __forceinline__ Raw *ring(uint8_t *smem, int rows) {
-        return reinterpret_cast<Raw *>(smem) + (threadIdx.x >> 5) * (rows * NV * step) + (threadIdx.x & 31);
+    __device__ static __forceinline__ Slot *ring(uint8_t *smem, int rows) {
+        return reinterpret_cast<Slot *>(smem) + (threadIdx.x >> 5) * (rows * NV * step) + (threadIdx.x & 31);
     }
-    __device__ static __forceinline__ void get(const Raw *src, float2 (&f)[P]) {
+    // whether a thread's first value of a row is the high half of its word
+    __device__ static __forceinline__ unsigned odd(const T *row) { return kWord ? (unsigned)(reinterpret_cast<uintptr_t>(row) >> 1) & 1u : 0u; }
+    __device__ static __forceinline__ void get(const L &l, const Slot *src, unsigned odd, float2 (&f)[P]) {
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-            float2 one[V::kPairs];
-            V::unpack(src[v * step], one);
+            if constexpr (kWord) {
+                const float one = __uint_as_float(src[v * step] << ((odd + v * l.tpr) & 1 ? 0 : 16) & 0xffff0000u);
+                if (v % 2) f[v / 2].y = one;
+                else f[v / 2].x = one;
+            } else {
+                float2 one[V::kPairs];
+                V::unpack(src[v * step], one);
 #pragma unroll
-            for (int e = 0; e < V::kPairs; ++e) {
-                if constexpr (VEC == 1) {
-                    if (v % 2) f[v / 2].y = one[0].x;
-                    else f[v / 2].x = one[0].x;
-                } else f[v * V::kPairs + e] = one[e];
+                for (int e = 0; e < V::kPairs; ++e) {
+                    if constexpr (VEC == 1) {
+                        if (v % 2) f[v / 2].y = one[0].x;
+                        else f[v / 2].x = one[0].x;
+                    } else f[v * V::kPairs + e] = one[e];
+                }
             }
         }
     }
@@ -116,22 +131,26 @@ struct Row {
             if (l.on(v)) *reinterpret_cast<Raw *>(row + v * l.tpr * VEC) = V::pack(one);
         }
     }
-    __device__ static __forceinline__ void ask(const L &l, const T *row, Raw *dst) {
+    __device__ static __forceinline__ void ask(const L &l, const T *row, Slot *dst) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            if (l.on(v)) copy_vec(dst + v * step, reinterpret_cast<const Raw *>(row + v * l.tpr * VEC));
+            if (l.on(v)) {
+                const T *at = row + v * l.tpr * VEC;
+                if constexpr (kWord) at = reinterpret_cast<const T *>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)3);
+                copy_async<(int)sizeof(Slot)>(tc::smem_u32(dst + v * step), at);
+            }
     }
     // the vectors beyond the row's end in `rows` rows of the ring
     template <int ROWS>
-    __device__ static __forceinline__ void blank(const L &l, Raw *dst) {
+    __device__ static __forceinline__ void blank(const L &l, Slot *dst) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
             if (!l.on(v))
-                for (int i = 0; i < ROWS; ++i) dst[(i * NV + v) * step] = Raw{};
+                for (int i = 0; i < ROWS; ++i) dst[(i * NV + v) * step] = Slot{};
     }
-    __device__ static __forceinline__ void zero(Raw *dst) {
+    __device__ static __forceinline__ void zero(Slot *dst) {
 #pragma unroll
-        for (int v = 0; v < NV; ++v) dst[v * step] = Raw{};
+        for (int v = 0; v < NV; ++v) dst[v * step] = Slot{};
     }
 };
 
@@ -248,7 +267,8 @@ __device__ __forceinline__ void factors(const Lane<VEC, K> &l, const BnArgs &a, 
 // Stages of the gradient's ring: what fits beside one another in shared memory.
 __host__ __device__ constexpr int bwd_stages(int es, int k) { return k == 1 ? 3 : (es == 2 ? 2 : 1); }
 
-constexpr int kFwdStages = 3;
+// ... and of the forward kernel's.
+__host__ __device__ constexpr int fwd_stages(int es, int k) { return k == 2 && es == 4 ? 2 : 3; }
 
 // The gradient's kernel for a vector width, k times 8 channels a thread and tpr
 // threads a row, and the launch that joins its sums.

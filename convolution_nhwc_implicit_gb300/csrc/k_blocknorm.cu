@@ -41,11 +41,11 @@ namespace {
 template <typename T, int VEC, int K, int RB, int ROW, bool ALL>
 __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_constant__ BnArgs a) {
     using R = Row<T, VEC, K>;
-    using Raw = typename R::Raw;
-    constexpr int P = R::P, D = kFwdStages, LINE = R::NV * R::step, STAGE = 2 * RB * LINE;
+    using Slot = typename R::Slot;
+    constexpr int P = R::P, D = fwd_stages(R::kElement, K), LINE = R::NV * R::step, STAGE = 2 * RB * LINE;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float meet[2 * kMostThreads / 32 * 2];
-    Raw *ring = R::ring(smem, D * 2 * RB);  // [D][x, f][RB]
+    Slot *ring = R::ring(smem, D * 2 * RB);  // [D][x, f][RB]
     const Lane<VEC, K> l(a);
     RowSum<ROW> sum(a.tpr, l.slot, meet);
     const int n = RB > 1 ? blockIdx.x / a.S : 0, s0 = RB > 1 ? blockIdx.x - n * a.S : blockIdx.x;
@@ -56,11 +56,14 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
     const T *x = static_cast<const T *>(a.x) + row * a.px + l.first(0), *f = static_cast<const T *>(a.f) + row * a.pf + l.first(0);
     T *y = static_cast<T *>(a.o0) + row * a.p0 + l.first(0), *z = static_cast<T *>(a.o1) + row * a.p1 + l.first(0);
     const long long sx = a.slots * a.px, sf = a.slots * a.pf, sy = a.slots * a.p0, sz = a.slots * a.p1;
+    // (of the rows at hand, and how they change from a row of the slot to its next)
+    unsigned ox = R::odd(x), of = R::odd(f);
+    const unsigned nx = sx & 1, nf = sf & 1;
     pdl_trigger();
     if (!a.full) R::template blank<D * 2 * RB>(l, ring);
     pdl_wait();
-    const Raw *d = ring;
-    Raw *to = ring;
+    const Slot *d = ring;
+    Slot *to = ring;
     auto ask = [&] {
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
@@ -78,20 +81,45 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
 #pragma unroll
     for (int i = 0; i < D - 1; ++i) ask();
     float2 q[P], p[P], g2[P], b2[P];
+    // pre's parameters: in registers, or, sixteen channels a thread, at a place of
+    // the thread's own in shared memory (with 64 registers of parameters some
+    // 130 bytes of a thread's were spilled: 4096x8192 bf16 63 us)
+    float4 *const par = reinterpret_cast<float4 *>(smem + (size_t)D * 2 * RB * R::NV * blockDim.x * sizeof(Slot)) + threadIdx.x;
+    auto pre = [&](float2 (&v)[P]) {
+        if constexpr (K == 1) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) v[i] = fma2(v[i], g2[i], b2[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; i += 2) {
+                const float4 g = par[i * blockDim.x], b = par[(i + 1) * blockDim.x];
+                v[i] = fma2(v[i], make_float2(g.x, g.y), make_float2(b.x, b.y));
+                v[i + 1] = fma2(v[i + 1], make_float2(g.z, g.w), make_float2(b.z, b.w));
+            }
+        }
+    };
     int image = n;
     const bool by_row = RB == 1 && a.gate;
     if (by_row) image = min(row, a.rows - 1) / a.HW;
     if (block) factors(l, a, image, q, p);
     l.params(g2, a.g2, 1.0f);
     l.params(b2, a.b2, 0.0f);
+    if constexpr (K > 1)
+#pragma unroll
+        for (int i = 0; i < P; i += 2) {
+            par[i * blockDim.x] = make_float4(g2[i].x, g2[i].y, g2[i + 1].x, g2[i + 1].y);
+            par[(i + 1) * blockDim.x] = make_float4(b2[i].x, b2[i].y, b2[i + 1].x, b2[i + 1].y);
+        }
     for (int base = r0; base < r1; base += a.slots * RB) {
         copy_wait<D - 2>();
         float2 v[RB][P], u[RB][P];
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
-            R::get(d + b * LINE, v[b]);
-            if (block) R::get(d + (RB + b) * LINE, u[b]);
+            R::get(l, d + b * LINE, ox + b * nx, v[b]);
+            if (block) R::get(l, d + (RB + b) * LINE, of + b * nf, u[b]);
         }
+        ox += RB * nx;
+        of += RB * nf;
         d = d == ring + (D - 1) * STAGE ? ring : d + STAGE;
         ask();
         float2 one[RB], two[RB];
@@ -121,8 +149,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
             normalise<VEC, K, RB>(l, sum, v, a.pre, a, two);
 #pragma unroll
             for (int b = 0; b < RB; ++b) {
-#pragma unroll
-                for (int i = 0; i < P; ++i) v[b][i] = fma2(v[b][i], g2[i], b2[i]);
+                pre(v[b]);
                 if (row + b * a.slots < r1) R::put(l, z + b * sz, v[b]);
             }
         }
@@ -174,14 +201,16 @@ int vec_for(const conv_plan *p, const Map (&maps)[N]) {
 // rows side by side have k = 1, so that it has 96 elements a thread where the
 // sums are SUMS * 8 in fp32.)
 static_assert(3 * 4 * 8 * 2 >= SUMS * 8 * 4, "");
+// es: of an element in the ring.
 size_t ring_bytes(const BnGeom &g, const BnGeom::Part &d, int es) {
     const size_t maps = (size_t)d.threads * 8 * g.k * es;
-    if (d.rb) return 2 * kFwdStages * d.rb * maps;
+    if (d.rb) return 2 * fwd_stages(es, g.k) * d.rb * maps + (g.k > 1 ? (size_t)d.threads * 2 * 8 * g.k * 4 : 0);
     const int stages = bwd_stages(es, g.k);  // (and a row's statistics, and the parameters of long rows)
     return stages * (4 * maps + (size_t)d.threads / (g.tpr < 32 ? g.tpr : 32) * 16) + (g.k > 1 ? (size_t)d.threads * 3 * 8 * g.k * 4 : 0);
 }
 
-cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a, size_t smem, cudaStream_t st) {
+cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a, cudaStream_t st) {
+    const size_t smem = ring_bytes(p->bn, d, ring_element(conv_esize(p->dtype), vec));
     const void *k = pick_kernel(p->dtype, vec, d.rb, p->bn.k, p->bn.tpr, d.rb ? a.f && a.o0 && a.o1 : a.f && a.dy && a.dz);
     if (smem > 40 * 1024) {  // (with the kernel's static shared memory: 48 KB are free)
         const int rc = conv_grant_smem_once(k, p->device, (int)smem);
@@ -392,7 +421,7 @@ extern "C" int conv_run_blocknorm(const conv_plan_t *plan, const void *x, int64_
     a.stats = reinterpret_cast<float4 *>(stats);
     const Map all[4] = {in[0], in[1], out[0], out[1]};
     const BnGeom::Part &g = w.gate ? p->bn.fwd_gated : p->bn.fwd;
-    return launch(p, g, vec_for(p, all), a, ring_bytes(p->bn, g, es), (cudaStream_t)stream) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+    return launch(p, g, vec_for(p, all), a, (cudaStream_t)stream) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }
 
 extern "C" int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, int64_t x_pitch, const void *f, int64_t f_pitch,
@@ -449,7 +478,7 @@ extern "C" int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, in
     a.want_b = d.post_beta || (w.post_beta && (d.scale || d.gate));
     const BnGeom::Part &g = w.gate ? p->bn.bwd_gated : p->bn.bwd;
     const Map all[6] = {in[0], in[1], in[2], in[3], out[0], out[1]};
-    if (launch(p, g, vec_for(p, all), a, ring_bytes(p->bn, g, es), st) != cudaSuccess) return CONV_ERR_CUDA;
+    if (launch(p, g, vec_for(p, all), a, st) != cudaSuccess) return CONV_ERR_CUDA;
     const bool sums = d.scale || d.post_gamma || d.post_beta || d.pre_gamma || d.pre_beta, images = d.gate && !g.whole;
     if (!sums && !images) return CONV_OK;
     return launch_join(a, g.grid, st) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;

@@ -73,16 +73,16 @@ __device__ __forceinline__ float gate_grad(const BnArgs &a, int c, float A, floa
 template <typename T, int VEC, int ROW, bool ALL>
 __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_constant__ BnArgs a) {
     using R = Row<T, VEC, 1>;
-    using Raw = typename R::Raw;
-    constexpr int P = R::P, D = bwd_stages(sizeof(T), 1), LINE = R::NV * R::step, STAGE = 4 * LINE;
+    using Slot = typename R::Slot;
+    constexpr int P = R::P, D = bwd_stages(R::kElement, 1), LINE = R::NV * R::step, STAGE = 4 * LINE;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float meet[2 * kMostThreads / 32 * 2];
     const int nt = blockDim.x;
-    Raw *ring = R::ring(smem, D * 4);  // [D][x, f, dy, dz]
+    Slot *ring = R::ring(smem, D * 4);  // [D][x, f, dy, dz]
     const Lane<VEC, 1> l(a);
     // statistics [warp][D][rows of a warp], copied by a lane of each row
     const int line = l.tpr < 32 ? l.tpr : 32, lane = threadIdx.x & 31;
-    float4 *const seen = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Raw)) +
+    float4 *const seen = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Slot)) +
                          (threadIdx.x >> 5) * (D * (32 / line)) + lane / line;
     const bool copies = lane % line == 0;
     RowSum<ROW> sum(a.tpr, l.slot, meet);
@@ -107,9 +107,10 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
         const T *x = static_cast<const T *>(a.x) + row * a.px + l.first(0), *f = static_cast<const T *>(a.f) + row * a.pf + l.first(0);
         const T *dy = static_cast<const T *>(a.dy) + row * a.pdy + l.first(0), *dz = static_cast<const T *>(a.dz) + row * a.pdz + l.first(0);
         T *dx = static_cast<T *>(a.o0) + row * a.p0 + l.first(0), *df = static_cast<T *>(a.o1) + row * a.p1 + l.first(0);
+        unsigned ox = R::odd(x), of = R::odd(f), ody = R::odd(dy), odz = R::odd(dz);
         if (!a.full) R::template blank<D * 4>(l, ring);  // (the sums were there between units)
-        const Raw *d = ring;
-        Raw *to = ring;
+        const Slot *d = ring;
+        Slot *to = ring;
         const float4 *sd = seen;
         float4 *sto = seen;
         // A row beyond the run counts as zeros.
@@ -144,9 +145,9 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             __syncwarp();
             const float4 st = *sd;
             float2 u[P], y[P], t[P];  // u^, y^, dY
-            R::get(d, y);
+            R::get(l, d, ox, y);
             if (block) {
-                R::get(d + LINE, u);
+                R::get(l, d + LINE, of, u);
                 const float2 r = both(st.y), c = both(-st.x * st.y);
                 if (ALL || a.b1)
 #pragma unroll
@@ -157,13 +158,13 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
                     y[k] = fma2(q[k], u[k], y[k]);
                 }
             }
-            if (stream) R::get(d + 2 * LINE, t);
+            if (stream) R::get(l, d + 2 * LINE, ody, t);
             else
 #pragma unroll
                 for (int k = 0; k < P; ++k) t[k] = make_float2(0.0f, 0.0f);
             if (norm) {
                 float2 e[P], w = make_float2(0.0f, 0.0f), v = w;
-                R::get(d + 3 * LINE, e);
+                R::get(l, d + 3 * LINE, odz, e);
                 const float2 r = both(st.w), c = both(-st.z * st.w);
                 if (ALL || a.db2)
 #pragma unroll
@@ -214,6 +215,10 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             row += a.slots;
             dx += s0;
             df += s1;
+            ox += (unsigned)sx;
+            of += (unsigned)sf;
+            ody += (unsigned)sdy;
+            odz += (unsigned)sdz;
         }
         copy_wait<0>();
         float2 *ent = reinterpret_cast<float2 *>(smem);
@@ -247,13 +252,13 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
 template <typename T, int VEC>
 __global__ void __launch_bounds__(kMostThreads) bn_bwd_long_kernel(const __grid_constant__ BnArgs a) {
     using R = Row<T, VEC, 1>;
-    using Raw = typename R::Raw;
-    constexpr int H = 2, P = R::P, D = bwd_stages(sizeof(T), H), LINE = R::NV * R::step, MAP = H * LINE, STAGE = 4 * MAP;
+    using Slot = typename R::Slot;
+    constexpr int H = 2, P = R::P, D = bwd_stages(R::kElement, H), LINE = R::NV * R::step, MAP = H * LINE, STAGE = 4 * MAP;
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ float meet[2 * kMostThreads / 32 * 2];
     const int nt = blockDim.x;
-    Raw *ring = R::ring(smem, D * 4 * H);  // [D][x, f, dy, dz][H]
-    float4 *const par = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * H * R::NV * nt * sizeof(Raw)) + threadIdx.x;  // [q, p, g2][H][2][threads]
+    Slot *ring = R::ring(smem, D * 4 * H);  // [D][x, f, dy, dz][H]
+    float4 *const par = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * H * R::NV * nt * sizeof(Slot)) + threadIdx.x;  // [q, p, g2][H][2][threads]
     float4 *const seen = par - threadIdx.x + 3 * H * 2 * nt + (threadIdx.x >> 5) * D;  // statistics [warp][D]
     Lane<VEC, 1> l[H] = {Lane<VEC, 1>(a), Lane<VEC, 1>(a)};
     l[1].t += R::NV * a.tpr;
@@ -305,12 +310,13 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_long_kernel(const __grid_
         const T *x = static_cast<const T *>(a.x) + r0 * a.px + at, *f = static_cast<const T *>(a.f) + r0 * a.pf + at;
         const T *dy = static_cast<const T *>(a.dy) + r0 * a.pdy + at, *dz = static_cast<const T *>(a.dz) + r0 * a.pdz + at;
         T *dx = static_cast<T *>(a.o0) + r0 * a.p0 + at, *df = static_cast<T *>(a.o1) + r0 * a.p1 + at;
+        unsigned ox = R::odd(x), of = R::odd(f), ody = R::odd(dy), odz = R::odd(dz);  // (both chunks': they are an even number apart)
         if (!a.full)
 #pragma unroll
             for (int h = 0; h < H; ++h)
                 for (int i = 0; i < D * 4; ++i) R::template blank<1>(l[h], ring + i * MAP + h * LINE);
-        const Raw *d = ring;
-        Raw *to = ring;
+        const Slot *d = ring;
+        Slot *to = ring;
         const float4 *sd = seen;
         float4 *sto = seen;
         auto ask = [&] {
@@ -344,12 +350,12 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_long_kernel(const __grid_
             const float4 st = *sd;
             const float2 ur = both(st.y), uc = both(-st.x * st.y), yr = both(st.w), yc = both(-st.z * st.w);
             auto block_out = [&](int h, float2 (&u)[P]) {  // u^
-                R::get(d + MAP + h * LINE, u);
+                R::get(l[h], d + MAP + h * LINE, of, u);
 #pragma unroll
                 for (int k = 0; k < P; ++k) u[k] = fma2(u[k], ur, uc);
             };
             auto stream_in = [&](int h, const float2 (&u)[P], float2 (&y)[P]) {  // y^
-                R::get(d + h * LINE, y);
+                R::get(l[h], d + h * LINE, ox, y);
                 if (block) {
                     float2 q[P];
                     param(PAR_P, h, q);
@@ -370,7 +376,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_long_kernel(const __grid_
                     float2 u[P], y[P], e[P], g2[P];
                     if (block) block_out(h, u);
                     stream_in(h, u, y);
-                    R::get(d + 3 * MAP + h * LINE, e);
+                    R::get(l[h], d + 3 * MAP + h * LINE, odz, e);
                     param(PAR_G2, h, g2);
 #pragma unroll
                     for (int k = 0; k < P; ++k) {
@@ -389,14 +395,14 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_long_kernel(const __grid_
             for (int h = 0; h < H; ++h) {
                 float2 u[P];
                 if (block) block_out(h, u);
-                if (stream) R::get(d + 2 * MAP + h * LINE, t[h]);
+                if (stream) R::get(l[h], d + 2 * MAP + h * LINE, ody, t[h]);
                 else
 #pragma unroll
                     for (int k = 0; k < P; ++k) t[h][k] = make_float2(0.0f, 0.0f);
                 if (norm) {
                     float2 y[P], e[P], g2[P];
                     stream_in(h, u, y);
-                    R::get(d + 3 * MAP + h * LINE, e);
+                    R::get(l[h], d + 3 * MAP + h * LINE, odz, e);
                     param(PAR_G2, h, g2);
 #pragma unroll
                     for (int k = 0; k < P; ++k) t[h][k] = fma2(y[k], my, fma2(mul2(e[k], g2[k]), yr, add2(t[h][k], m)));
@@ -437,6 +443,10 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_long_kernel(const __grid_
             ask();
             dx += a.p0;
             df += a.p1;
+            ox += (unsigned)a.px;
+            of += (unsigned)a.pf;
+            ody += (unsigned)a.pdy;
+            odz += (unsigned)a.pdz;
         }
         copy_wait<0>();
 #pragma unroll
