@@ -17,6 +17,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+from array import array
 
 __all__ = ["Plan", "ConvError", "conv2d_nhwc", "library_path", "load_library", "DTYPES", "ACTS",
            "ALGOS", "status_str", "abi_version", "run_i8_noalloc", "NOALLOC_MAX_COUT", "spp", "DwpwPlan",
@@ -155,7 +156,7 @@ def load_library():
             ("conv_run_blocknorm_bwd", [c_void_p, c_void_p, i64, c_void_p, i64, ctypes.POINTER(_BlockNormPointers), c_void_p] +
              [c_void_p, i64] * 4 + [ctypes.POINTER(_BlockNormPointers), c_void_p, c_void_p]),
             ("conv_plan_create_gradclip", [i32, ctypes.POINTER(i64), ctypes.POINTER(c_int), pp]),
-            ("conv_run_gradclip", [c_void_p, pp, pp, ctypes.c_float, c_void_p, c_void_p, c_void_p])):
+            ("conv_run_gradclip", [c_void_p, c_void_p, c_void_p, ctypes.c_float, c_void_p, c_void_p, c_void_p])):
         getattr(lib, name).argtypes = args
         getattr(lib, name).restype = c_int
     _lib = lib
@@ -433,14 +434,16 @@ _getters = None
 def _tensor_getters():
     """What is asked of every tensor of a call, to be mapped over all of them
     (about 0.04 us each, where a loop takes twice that): its shape, dtype,
-    whether it is dense, its device and its address.  Looked up once."""
+    whether it is dense, its device, its address and its number of elements.
+    Looked up once."""
     global _getters
     if _getters is None:
         import operator
 
         import torch
         t = torch.Tensor
-        _getters = operator.attrgetter("shape"), operator.attrgetter("dtype"), t.is_contiguous, t.get_device, t.data_ptr
+        _getters = (operator.attrgetter("shape"), operator.attrgetter("dtype"), t.is_contiguous, t.get_device, t.data_ptr,
+                    t.numel)
     return _getters
 
 
@@ -707,7 +710,7 @@ class BlockNormPlan(_MapPlan):
         given, shapes, dtypes, devices, maps = known
         ts = tensors if len(given) == len(names) else [t for t in tensors if t is not None]
         pitches = [0] * maps
-        shape_of, dtype_of, dense, device_of, address = _tensor_getters()
+        shape_of, dtype_of, dense, device_of, address, _ = _tensor_getters()
         try:
             good = (list(map(shape_of, ts)) == shapes and list(map(dtype_of, ts)) == dtypes and
                     list(map(device_of, ts)) == devices and all(map(dense, ts)))
@@ -789,7 +792,6 @@ class GradClipPlan(_OpPlan):
         codes = (ctypes.c_int * count)(*(DTYPES[d] for d in names))
         self._create("conv_plan_create_gradclip", count, counts, codes)
         self._dtypes, self._devices = [_torch_dtype(d) for d in names], [self._device] * count
-        self._array = ctypes.c_void_p * count
 
     @property
     def output_shape(self):
@@ -798,17 +800,18 @@ class GradClipPlan(_OpPlan):
     y_shape = output_shape
 
     def _addresses(self, name, tensors):
+        """The tensors' addresses, one after the other in memory of the host."""
         if len(tensors) != len(self._counts):
             raise ValueError(f"{len(tensors)} {name} for a plan of {len(self._counts)}")
-        _, dtype_of, dense, device_of, address = _tensor_getters()
+        _, dtype_of, dense, device_of, address, count_of = _tensor_getters()
         try:
             if (list(map(dtype_of, tensors)) == self._dtypes and list(map(device_of, tensors)) == self._devices and
-                    [t.numel() for t in tensors] == self._counts and all(map(dense, tensors))):
-                return self._array(*map(address, tensors))
+                    list(map(count_of, tensors)) == self._counts and all(map(dense, tensors))):
+                return array("Q", map(address, tensors))
         except (AttributeError, TypeError):  # (not tensors)
             pass
-        return self._array(*[_check(f"{name}[{i}]", t, t.shape if t is not None and t.numel() == k else self.shapes[i], d, self._device)
-                             for i, (t, k, d) in enumerate(zip(tensors, self._counts, self._dtypes))])
+        return array("Q", [_check(f"{name}[{i}]", t, t.shape if t is not None and t.numel() == k else self.shapes[i], d, self._device)
+                           for i, (t, k, d) in enumerate(zip(tensors, self._counts, self._dtypes))])
 
     def run(self, grads, max_norm, norm, out=None, stream=None) -> None:  # noqa: D401
         """Enqueue the norm (a float32 scalar tensor) and the clipped gradients
@@ -820,7 +823,7 @@ class GradClipPlan(_OpPlan):
         o = None if out is None else self._addresses("out", out)
         pn = _check("norm", norm, (), self._f32, dev)
         ws = self._workspace(self.workspace_bytes, norm, stream)
-        rc = self._lib.conv_run_gradclip(self._handle, g, o, float(max_norm), pn, _ptr(ws), _stream_handle(stream, dev))
+        rc = self._lib.conv_run_gradclip(self._handle, g.buffer_info()[0], o and o.buffer_info()[0], float(max_norm), pn, _ptr(ws), _stream_handle(stream, dev))
         if rc != 0:
             raise ConvError("conv_run_gradclip", rc)
 

@@ -18,6 +18,8 @@ using namespace convk;
 constexpr int kMaxC = 8192;        // channels: 512 threads of 16
 constexpr int kThreads = 256;      // of a forward CTA whose rows take no more
 constexpr int kMostThreads = 512;  // of a row, and of the gradient's CTAs
+constexpr int kCluster = 8;        // CTAs of a gradient in one launch, and the sets of rows that each takes at most
+constexpr int kClusterSets = 4;
 enum { SUM_A, SUM_B, SUM_G2, SUM_B2, SUMS };
 
 struct BnArgs {
@@ -35,6 +37,7 @@ struct BnArgs {
     int run, S, units;             // rows of a unit, units an image (of all rows without a gate), units in all
     int whole;                     // gradient: a unit is a whole image of a gated map
     int want_b;                    // gradient: B is asked for
+    int joined;                    // gradient: the CTAs are one cluster and join their sums themselves
 };
 
 // Where a thread stands: which row of those side by side, which of the row's

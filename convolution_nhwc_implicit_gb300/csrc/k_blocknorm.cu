@@ -196,11 +196,15 @@ int vec_for(const conv_plan *p, const Map (&maps)[N]) {
     return 1;
 }
 
+long long up(long long a, long long b) { return (a + b - 1) / b; }
+
 // Bytes of the ring of a CTA: a thread's 8 k channels of each map and stage.
 // (The gradient's holds the sums of rows side by side after its last row:
 // rows side by side have k = 1, so that it has 96 elements a thread where the
-// sums are SUMS * 8 in fp32.)
-static_assert(3 * 4 * 8 * 2 >= SUMS * 8 * 4, "");
+// sums are SUMS * 8 in fp32.
+// A cluster's also holds the CTA's sums of its channels, at most 8 a thread of a
+// row, and there are rows side by side where that is at most half of them: 64.)
+static_assert(3 * 4 * 8 * 2 >= SUMS * 8 * 4 + SUMS * 8 * 4 / 2, "");
 // es: of an element in the ring.
 size_t ring_bytes(const BnGeom &g, const BnGeom::Part &d, int es) {
     const size_t maps = (size_t)d.threads * 8 * g.k * es;
@@ -216,9 +220,9 @@ cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a
         const int rc = conv_grant_smem_once(k, p->device, (int)smem);
         if (rc != CONV_OK) return cudaErrorInvalidValue;
     }
-    a.slots = d.slots; a.run = d.run; a.S = d.S; a.units = d.units; a.whole = d.whole;
+    a.slots = d.slots; a.run = d.run; a.S = d.S; a.units = d.units; a.whole = d.whole; a.joined = d.joined;
     void *args[] = {&a};
-    return conv_launch(k, dim3((unsigned)d.grid), dim3((unsigned)d.threads), args, smem, st);
+    return conv_launch(k, dim3((unsigned)d.grid), dim3((unsigned)d.threads), args, smem, st, d.joined ? d.grid : 1);
 }
 
 int check_map(const conv_plan *p, const void *t, int64_t *pitch) {
@@ -261,15 +265,13 @@ bool shared(const Map (&in)[M], const Map (&out)[W], const Small (&small_in)[I],
 }
 bool bad_f32(const void *t) { return t && ((uintptr_t)t & 3u); }
 
-long long up(long long a, long long b) { return (a + b - 1) / b; }
-
 // All rows in runs of whole sets of rows side by side, one wave of CTAs.
 void divide_rows(BnGeom::Part &d, long long rows, long long set, long long wave) {
     long long run = up(up(rows, wave), set) * set;
     if (run < set) run = set;
     d.run = (int)run;
     d.S = d.units = d.grid = (int)up(rows, run);
-    d.whole = 0;
+    d.whole = d.joined = 0;
 }
 // Each image in runs of whole sets, as many as fill the CTAs best: a run costs
 // its sets and about four more for its start and end.
@@ -285,7 +287,7 @@ void divide_images(BnGeom::Part &d, long long N, long long HW, long long set, lo
         d.run = (int)(S == 1 ? HW : sets * set);
     }
     d.units = d.grid = (int)(N * d.S);
-    d.whole = 0;
+    d.whole = d.joined = 0;
 }
 
 // Threads of a row, rows of a CTA, and how the rows are divided.
@@ -329,9 +331,24 @@ void plan_geometry(conv_plan *p) {
     const long long w = wave(g.bwd);
     divide_rows(g.bwd, rows, g.bwd.slots, w);
     divide_images(g.bwd_gated, N, HW, g.bwd.slots, w);
-    g.bwd_gated.whole = g.bwd_gated.S == 1;
-    if (g.bwd_gated.whole && N > w) g.bwd_gated.grid = (int)w;
-    const long long parts = g.bwd.grid > g.bwd_gated.grid ? g.bwd.grid : g.bwd_gated.grid;
+    // few rows: the CTAs of one cluster, a unit each, which join their sums
+    // themselves, where none takes more than four sets of rows
+    auto cluster = [&](BnGeom::Part &d, long long images, long long each) {
+        const long long most = images <= kCluster ? kCluster / images : 0, sets = most ? up(each, most * d.slots) : 0;
+        if (g.k > 1 || !most || sets > kClusterSets) return;
+        d.run = (int)(sets * d.slots);
+        d.S = (int)up(each, d.run);
+        d.units = d.grid = (int)images * d.S;
+        d.joined = 1;
+    };
+    cluster(g.bwd, 1, rows);
+    cluster(g.bwd_gated, N, HW);
+    if (!g.bwd_gated.joined) {
+        g.bwd_gated.whole = g.bwd_gated.S == 1;
+        if (g.bwd_gated.whole && N > w) g.bwd_gated.grid = (int)w;
+    }
+    const long long open = g.bwd.joined ? 0 : g.bwd.grid, gated = g.bwd_gated.joined ? 0 : g.bwd_gated.grid;
+    const long long parts = open > gated ? open : gated;
     p->ws_bwd_bytes = (size_t)parts * SUMS * ((C + 3) / 4 * 4) * 4;
 }
 
@@ -460,7 +477,7 @@ extern "C" int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, in
         (rc = check_map(p, df, &df_pitch)) != CONV_OK)
         return rc;
     if (((uintptr_t)stats & 15u) || ((uintptr_t)workspace & 15u)) return CONV_ERR_MISALIGNED;
-    if (!workspace) return CONV_ERR_NULL_ARG;
+    if (p->ws_bwd_bytes && !workspace) return CONV_ERR_NULL_ARG;
     const long long rows = (long long)p->s.n * p->s.h * p->s.w;
     const size_t nb = (size_t)p->s.n * cb;
     const Map in[4] = {{x, x_pitch}, {f, f_pitch}, {dy, dy_pitch}, {dz, dz_pitch}}, out[2] = {{dx, dx_pitch}, {df, df_pitch}};
@@ -480,6 +497,6 @@ extern "C" int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, in
     const Map all[6] = {in[0], in[1], in[2], in[3], out[0], out[1]};
     if (launch(p, g, vec_for(p, all), a, st) != cudaSuccess) return CONV_ERR_CUDA;
     const bool sums = d.scale || d.post_gamma || d.post_beta || d.pre_gamma || d.pre_beta, images = d.gate && !g.whole;
-    if (!sums && !images) return CONV_OK;
+    if (g.joined || (!sums && !images)) return CONV_OK;
     return launch_join(a, g.grid, st) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }

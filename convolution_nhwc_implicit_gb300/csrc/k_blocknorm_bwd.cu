@@ -67,6 +67,52 @@ __device__ __forceinline__ float gate_grad(const BnArgs &a, int c, float A, floa
     return (a.scale ? a.scale[c] : 1.0f) * ((a.g1 ? a.g1[c] : 1.0f) * A + (a.b1 ? a.b1[c] : 0.0f) * B);
 }
 
+// The parameters' gradients of a channel, from its sums over all pixels (A and B
+// times the gates).
+__device__ __forceinline__ void param_grads(const BnArgs &a, int c, float A, float B, float G2, float B2) {
+    const float scale = a.scale ? a.scale[c] : 1.0f;
+    if (a.dscale) a.dscale[c] = (a.g1 ? a.g1[c] : 1.0f) * A + (a.b1 ? a.b1[c] : 0.0f) * B;
+    if (a.dg1) a.dg1[c] = scale * A;
+    if (a.db1) a.db1[c] = scale * B;
+    if (a.dg2) a.dg2[c] = G2;
+    if (a.db2) a.db2[c] = B2;
+}
+
+// The sum of a shared value over `n` CTAs of the cluster from `from` on, in their
+// order.
+__device__ __forceinline__ float cluster_sum(const float *p, int from, int n) {
+    const uint32_t at = tc::smem_u32(p);
+    float v[kCluster];
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r)
+        if (r < n) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(tc::mapa_shared(at, from + r)) : "memory");
+    float s = 0.0f;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r)
+        if (r < n) s += v[r];
+    return s;
+}
+// The CTAs of a cluster, a unit each, join their sums: `mine` [SUMS][Cp] is the
+// calling CTA's, which joins a share of the channels.
+__device__ __forceinline__ void join_cluster(const BnArgs &a, const float *mine) {
+    cluster_arrive();
+    cluster_wait();
+    const int ranks = (int)gridDim.x, share = (a.C + ranks - 1) / ranks, c1 = min(a.C, ((int)blockIdx.x + 1) * share);
+    for (int c = (int)blockIdx.x * share + threadIdx.x; c < c1; c += blockDim.x) {
+        float A = 0.0f, B = 0.0f;
+        for (int n = 0, from = 0; from < ranks; ++n, from += a.S) {  // (without a gate, one image)
+            const float ia = cluster_sum(mine + SUM_A * a.Cp + c, from, a.S), ib = cluster_sum(mine + SUM_B * a.Cp + c, from, a.S);
+            const float gate = a.gate ? a.gate[(long long)n * a.C + c] : 1.0f;
+            if (a.dgate) a.dgate[(long long)n * a.C + c] = gate_grad(a, c, ia, ib);
+            A = fmaf(gate, ia, A);
+            B = fmaf(gate, ib, B);
+        }
+        param_grads(a, c, A, B, cluster_sum(mine + SUM_G2 * a.Cp + c, 0, ranks), cluster_sum(mine + SUM_B2 * a.Cp + c, 0, ranks));
+    }
+    cluster_arrive();  // (no CTA ends while its sums may still be read)
+    cluster_wait();
+}
+
 // dx and df of the rows of a CTA's units, and the units' channel sums.  ALL: the
 // block, dy and dz are given; what is then not asked for is formed all the same,
 // which is fewer instructions than asking.
@@ -85,6 +131,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
     float4 *const seen = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Slot)) +
                          (threadIdx.x >> 5) * (D * (32 / line)) + lane / line;
     const bool copies = lane % line == 0;
+    float2 *const ent = reinterpret_cast<float2 *>(smem);  // after a unit's rows: the threads' sums
     RowSum<ROW> sum(a.tpr, l.slot, meet);
     const bool block = ALL || a.f, stream = ALL || a.dy, norm = ALL || a.dz;
     const float mean_post = a.post == CONV_NORM_LAYER ? -a.inv_c : 0.0f, mean_pre = a.pre == CONV_NORM_LAYER ? -a.inv_c : 0.0f;
@@ -221,8 +268,13 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             odz += (unsigned)sdz;
         }
         copy_wait<0>();
-        float2 *ent = reinterpret_cast<float2 *>(smem);
-        if (a.whole) {
+        if (a.joined) {
+            // (the CTA's sums after the threads')
+            float *mine = reinterpret_cast<float *>(ent + (a.slots > 1 ? SUMS * P * nt : 0));
+            if (a.slots == 1) __syncthreads();
+            combine<0, SUMS, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { mine[s * a.Cp + c] = v; });
+            join_cluster(a, mine);
+        } else if (a.whole) {
             const bool first = unit == (int)blockIdx.x;
             float *both_sums = reinterpret_cast<float *>(ent + 2 * P * nt);  // [A, B][C]: of a channel, two threads'
             if (a.slots == 1) __syncthreads();
@@ -240,7 +292,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
         } else combine<0, SUMS, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { *place(a, unit, s, c) = v; });
     }
     if (a.whole)
-        combine<SUM_G2, 2, VEC>(l, a.slots, acc, reinterpret_cast<float2 *>(smem), [&](int s, int c, float v) { *place(a, blockIdx.x, s, c) = v; });
+        combine<SUM_G2, 2, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { *place(a, blockIdx.x, s, c) = v; });
 }
 
 // The same for rows of more than 4096 channels: sixteen a thread, in two chunks
@@ -558,12 +610,7 @@ __global__ void __launch_bounds__(kJoin) bn_join_kernel(const __grid_constant__ 
             t[s] += __shfl_xor_sync(0xffffffffu, t[s], 16);
         }
         if (lane < 16 && k < a.C) {
-            const float sc = a.scale ? a.scale[k] : 1.0f;
-            if (a.dscale) a.dscale[k] = (a.g1 ? a.g1[k] : 1.0f) * t[SUM_A] + (a.b1 ? a.b1[k] : 0.0f) * t[SUM_B];
-            if (a.dg1) a.dg1[k] = sc * t[SUM_A];
-            if (a.db1) a.db1[k] = sc * t[SUM_B];
-            if (a.dg2) a.dg2[k] = t[SUM_G2];
-            if (a.db2) a.db2[k] = t[SUM_B2];
+            param_grads(a, k, t[SUM_A], t[SUM_B], t[SUM_G2], t[SUM_B2]);
         }
     }
 }

@@ -40,6 +40,7 @@ struct ClipGeom {
     std::vector<uint8_t> es;
     std::vector<ClipBatch> batches;
     int parts = 0;
+    bool small = false;  // one launch of one cluster
     uint4 *items = nullptr;  // device: (tensor of the batch | fp32 << 31, elements, first element as two words)
     int *first = nullptr;    // device: [grid + 1] of each batch
 };
@@ -50,6 +51,8 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kCtas = 2;          // a SM
 constexpr int kItem = 4096;       // elements of an item, at most
 constexpr int kItemLeast = 256;   // ... and at least, but for a tensor's end: a vector a lane
+constexpr int kCluster = 16;      // CTAs of the one-launch form, and the bytes up to which it is taken
+constexpr long long kSmall = 1536 * 1024;
 constexpr int kMostTensors = 1900;  // of a launch: their addresses are kernel parameters (32 KB at most)
 
 template <int M> struct Tensors { const void *p[M]; };
@@ -129,15 +132,10 @@ __device__ __forceinline__ double warp_sum64(double v) {
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
+// A warp's sum of squares over items i, i + kWarps, ... before `end`; it is the
+// first of them.
 template <int M>
-__global__ void __launch_bounds__(kThreads, kCtas) clip_norm_kernel(const __grid_constant__ Tensors<M> t, const uint4 *items,
-                                                                    const int *first, double *part) {
-    __shared__ double red[kWarps];
-    pdl_trigger();
-    const int end = first[blockIdx.x + 1];
-    int i = first[blockIdx.x] + (threadIdx.x >> 5);
-    uint4 it = i < end ? items[i] : make_uint4(0, 0, 0, 0);
-    pdl_wait();
+__device__ __forceinline__ double sum_items(const Tensors<M> &t, const uint4 *items, int i, int end, uint4 it) {
     double s = 0.0;
     while (i < end) {
         const uint4 now = it;
@@ -148,13 +146,26 @@ __global__ void __launch_bounds__(kThreads, kCtas) clip_norm_kernel(const __grid
         if (now.x >> 31) s += item_sum(static_cast<const float *>(p) + at, (int)now.y);
         else s += item_sum(static_cast<const __nv_bfloat16 *>(p) + at, (int)now.y);
     }
+    return s;
+}
+// The CTA's sum of its warps' lanes' sums, in the first warp.
+__device__ __forceinline__ double cta_sum(double s, double *red) {
     s = warp_sum64(s);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
     __syncthreads();
-    if (threadIdx.x < 32) {
-        s = warp_sum64(threadIdx.x < kWarps ? red[threadIdx.x] : 0.0);
-        if (threadIdx.x == 0) part[blockIdx.x] = s;
-    }
+    return threadIdx.x < 32 ? warp_sum64(threadIdx.x < kWarps ? red[threadIdx.x] : 0.0) : 0.0;
+}
+
+template <int M>
+__global__ void __launch_bounds__(kThreads, kCtas) clip_norm_kernel(const __grid_constant__ Tensors<M> t, const uint4 *items,
+                                                                    const int *first, double *part) {
+    __shared__ double red[kWarps];
+    pdl_trigger();
+    const int end = first[blockIdx.x + 1], i = first[blockIdx.x] + (int)(threadIdx.x >> 5);
+    const uint4 it = i < end ? items[i] : make_uint4(0, 0, 0, 0);
+    pdl_wait();
+    const double s = cta_sum(sum_items(t, items, i, end, it), red);
+    if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
 template <typename T>
@@ -201,6 +212,23 @@ __device__ __forceinline__ float root32(double s) {
     return scalbnf(sqrtf((float)m), (e - (e & 1)) / 2);
 }
 
+// k for a norm.
+__device__ __forceinline__ float clip_factor(float norm, float max_norm) {
+    return isfinite(norm) ? fminf(1.0f, max_norm / (norm + 1e-6f)) : 1.0f;
+}
+// A warp's items i, i - kWarps, ... down to `start`, times k: from the end, which
+// is what is still in L2.
+template <int M>
+__device__ __forceinline__ void scale_items(const Tensors<M> &t, const Tensors<M> &o, const uint4 *items, int i, int start, float k) {
+    for (; i >= start; i -= kWarps) {
+        const uint4 now = items[i];
+        const long long at = (long long)(((unsigned long long)now.w << 32) | now.z);
+        const int j = now.x & 0x7fffffffu;
+        if (now.x >> 31) scale_item(static_cast<const float *>(t.p[j]) + at, (float *)o.p[j] + at, (int)now.y, k);
+        else scale_item(static_cast<const __nv_bfloat16 *>(t.p[j]) + at, (__nv_bfloat16 *)o.p[j] + at, (int)now.y, k);
+    }
+}
+
 // in place: outs are the gradients, which stay as they are where k = 1.
 template <int M>
 __global__ void __launch_bounds__(kThreads, kCtas) clip_scale_kernel(const __grid_constant__ Tensors<M> t,
@@ -209,28 +237,54 @@ __global__ void __launch_bounds__(kThreads, kCtas) clip_scale_kernel(const __gri
                                                                      float max_norm, float *norm, int in_place) {
     __shared__ float factor;
     pdl_trigger();
-    const int start = first[blockIdx.x];
-    int i = first[blockIdx.x + 1] - 1 - (int)(threadIdx.x >> 5);  // from the end: what the first launch left in L2
+    const int start = first[blockIdx.x], i = first[blockIdx.x + 1] - 1 - (int)(threadIdx.x >> 5);
     pdl_wait();
     if (threadIdx.x < 32) {
         double s = 0.0;
         for (int j = threadIdx.x; j < parts; j += 32) s += part[j];
         const float whole = root32(warp_sum64(s));
         if (threadIdx.x == 0) {
-            factor = isfinite(whole) ? fminf(1.0f, max_norm / (whole + 1e-6f)) : 1.0f;
+            factor = clip_factor(whole, max_norm);
             if (norm && blockIdx.x == 0) *norm = whole;
         }
     }
     __syncthreads();
-    const float k = factor;
-    if (in_place && k == 1.0f) return;
-    for (; i >= start; i -= kWarps) {
-        const uint4 now = items[i];
-        const long long at = (long long)(((unsigned long long)now.w << 32) | now.z);
-        const int j = now.x & 0x7fffffffu;
-        if (now.x >> 31) scale_item(static_cast<const float *>(t.p[j]) + at, (float *)o.p[j] + at, (int)now.y, k);
-        else scale_item(static_cast<const __nv_bfloat16 *>(t.p[j]) + at, (__nv_bfloat16 *)o.p[j] + at, (int)now.y, k);
+    if (in_place && factor == 1.0f) return;
+    scale_items(t, o, items, i, start, factor);
+}
+
+// Both of a small set in one launch: one cluster, whose CTAs read each other's
+// sums.
+template <int M>
+__global__ void __launch_bounds__(kThreads, kCtas) clip_small_kernel(const __grid_constant__ Tensors<M> t,
+                                                                     const __grid_constant__ Tensors<M> o, const uint4 *items,
+                                                                     const int *first, float max_norm, float *norm, int in_place) {
+    __shared__ double red[kWarps], mine;
+    __shared__ float factor;
+    pdl_trigger();
+    const int start = first[blockIdx.x], end = first[blockIdx.x + 1], warp = (int)(threadIdx.x >> 5), i = start + warp;
+    const uint4 it = i < end ? items[i] : make_uint4(0, 0, 0, 0);
+    pdl_wait();
+    double s = cta_sum(sum_items(t, items, i, end, it), red);
+    if (threadIdx.x == 0) mine = s;
+    cluster_arrive();
+    cluster_wait();
+    if (threadIdx.x < 32) {
+        s = 0.0;
+        if (threadIdx.x < gridDim.x) {
+            const uint32_t at = tc::mapa_shared(tc::smem_u32(&mine), threadIdx.x);
+            asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(s) : "r"(at) : "memory");
+        }
+        const float whole = root32(warp_sum64(s));
+        if (threadIdx.x == 0) {
+            factor = clip_factor(whole, max_norm);
+            if (blockIdx.x == 0) *norm = whole;
+        }
     }
+    cluster_arrive();  // (no CTA ends while its sum may still be read)
+    __syncthreads();
+    if (!in_place || factor != 1.0f) scale_items(t, o, items, end - 1 - warp, start, factor);
+    cluster_wait();
 }
 
 // ------------------------------------------------------------------ host side
@@ -242,8 +296,9 @@ struct Run {
     cudaStream_t st;
 };
 
+enum { NORM, SCALE, SMALL };
 template <int M>
-cudaError_t launch(const Run &r, const ClipBatch &b, bool scale) {
+cudaError_t launch(const Run &r, const ClipBatch &b, int which) {
     Tensors<M> t, o;
     for (int i = b.t0; i < b.t1; ++i) {
         t.p[i - b.t0] = r.grads[i];
@@ -251,21 +306,29 @@ cudaError_t launch(const Run &r, const ClipBatch &b, bool scale) {
     }
     const uint4 *items = r.g->items;
     const int *first = r.g->first + b.first;
-    if (!scale) {
+    int parts = r.g->parts, in_place = r.outs == nullptr;
+    float max_norm = r.max_norm, *norm = b.part == 0 ? r.norm : nullptr;
+    if (which == SMALL) {
+        if (b.grid > 8 && cudaFuncSetAttribute((const void *)&clip_small_kernel<M>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+            return cudaErrorInvalidValue;
+        void *args[] = {&t, &o, &items, &first, &max_norm, &norm, &in_place};
+        return conv_launch((const void *)&clip_small_kernel<M>, dim3((unsigned)b.grid), dim3(kThreads), args, 0, r.st, b.grid);
+    }
+    if (which == NORM) {
         double *part = r.part + b.part;
         void *args[] = {&t, &items, &first, &part};
         return conv_launch((const void *)&clip_norm_kernel<M>, dim3((unsigned)b.grid), dim3(kThreads), args, 0, r.st);
     }
     const double *part = r.part;
-    int parts = r.g->parts, in_place = r.outs == nullptr;
-    float max_norm = r.max_norm, *norm = b.part == 0 ? r.norm : nullptr;
     void *args[] = {&t, &o, &items, &first, &part, &parts, &max_norm, &norm, &in_place};
     return conv_launch((const void *)&clip_scale_kernel<M>, dim3((unsigned)b.grid), dim3(kThreads), args, 0, r.st);
 }
 
-cudaError_t launch_batch(const Run &r, const ClipBatch &b, bool scale) {
+cudaError_t launch_batch(const Run &r, const ClipBatch &b, int which) {
     const int n = b.t1 - b.t0;
-    return n <= 64 ? launch<64>(r, b, scale) : (n <= 448 ? launch<448>(r, b, scale) : launch<kMostTensors>(r, b, scale));
+    if (n <= 32) return launch<32>(r, b, which);
+    if (n <= 128) return launch<128>(r, b, which);
+    return n <= 512 ? launch<512>(r, b, which) : launch<kMostTensors>(r, b, which);
 }
 
 // Divides the tensors [b.t0, b.t1) among at most `wave` CTAs.
@@ -305,12 +368,20 @@ void divide(const ClipGeom &g, ClipBatch &b, int wave, std::vector<uint4> &items
     b.grid = ctas;
 }
 
-// Whether a tensor that the run writes shares a byte with another.
-struct Range { uintptr_t from, to; bool written; };
-bool overlap(std::vector<Range> &r) {
-    std::sort(r.begin(), r.end(), [](const Range &a, const Range &b) { return a.from < b.from; });
+// Whether a tensor that the run writes shares a byte with another.  (Each list is
+// most often in the order of its addresses already.)
+struct Range {
+    uintptr_t from, to;
+    bool written;
+    bool operator<(const Range &o) const { return from < o.from; }
+};
+bool overlap(std::vector<Range> &in, std::vector<Range> &out) {
+    for (std::vector<Range> *r : {&in, &out})
+        if (!std::is_sorted(r->begin(), r->end())) std::sort(r->begin(), r->end());
     uintptr_t any = 0, written = 0;  // ends of what came before
-    for (const Range &i : r) {
+    auto a = in.begin(), b = out.begin();
+    while (a != in.end() || b != out.end()) {
+        const Range &i = b == out.end() || (a != in.end() && *a < *b) ? *a++ : *b++;
         if (i.from < (i.written ? any : written)) return true;
         any = std::max(any, i.to);
         if (i.written) written = std::max(written, i.to);
@@ -326,7 +397,7 @@ void clip_destroy(ClipGeom *g) {
     if (g->first) cudaFree(g->first);
     delete g;
 }
-int clip_launches(const ClipGeom *g) { return 2 * (int)g->batches.size(); }
+int clip_launches(const ClipGeom *g) { return g->small ? 1 : 2 * (int)g->batches.size(); }
 
 extern "C" int conv_plan_create_gradclip(int32_t tensors, const int64_t *counts, const conv_dtype_t *dtypes,
                                          conv_plan_t **out_plan) {
@@ -355,15 +426,18 @@ extern "C" int conv_plan_create_gradclip(int32_t tensors, const int64_t *counts,
             for (int i = 0; i < tensors; ++i) g.es.push_back((uint8_t)conv_esize(dtypes[i]));
             std::vector<uint4> items;
             std::vector<int> first;
+            long long bytes = 0;
+            for (int i = 0; i < tensors; ++i) bytes += counts[i] * g.es[i];
+            g.small = bytes <= kSmall && tensors <= kMostTensors;
             int t = 0;
             do {
                 ClipBatch b = {t, std::min(tensors, t + kMostTensors), 0, 0, g.parts};
-                divide(g, b, kCtas * p->num_sms, items, first);
+                divide(g, b, g.small ? kCluster : kCtas * p->num_sms, items, first);
                 g.parts += b.grid;
                 g.batches.push_back(b);
                 t = b.t1;
             } while (t < tensors);
-            p->ws_bytes = (size_t)g.parts * sizeof(double);
+            p->ws_bytes = g.small ? 0 : (size_t)g.parts * sizeof(double);
             const size_t ib = std::max<size_t>(1, items.size()) * sizeof(uint4), fb = first.size() * sizeof(int);
             if (cudaMalloc(&g.items, ib) != cudaSuccess || cudaMalloc(&g.first, fb) != cudaSuccess) rc = CONV_ERR_OOM;
             else if ((!items.empty() && cudaMemcpy(g.items, items.data(), items.size() * sizeof(uint4), cudaMemcpyHostToDevice) != cudaSuccess) ||
@@ -391,32 +465,34 @@ extern "C" int conv_run_gradclip(const conv_plan_t *plan, void *const *grads, vo
     const ClipGeom &g = *p->clip;
     const int tensors = (int)g.counts.size();
     if (!(max_norm > 0.0f)) return CONV_ERR_INVALID_ARG;
-    if ((tensors > 0 && !grads) || !norm || !workspace) return CONV_ERR_NULL_ARG;
+    if ((tensors > 0 && !grads) || !norm || (p->ws_bytes && !workspace)) return CONV_ERR_NULL_ARG;
     if (((uintptr_t)norm & 3u) || ((uintptr_t)workspace & 15u)) return CONV_ERR_MISALIGNED;
     try {
-        std::vector<Range> ranges;
-        ranges.reserve((size_t)tensors * 2 + 2);
-        auto add = [&](const void *t, size_t bytes, bool written) {
-            if (bytes) ranges.push_back({(uintptr_t)t, (uintptr_t)t + bytes, written});
-        };
-        add(norm, 4, true);
-        add(workspace, p->ws_bytes, true);
+        std::vector<Range> read, written;
+        read.reserve((size_t)tensors);
+        written.reserve((size_t)tensors + 2);
         for (int i = 0; i < tensors; ++i) {
             if (g.counts[i] == 0) continue;
-            const void *in = grads[i], *out = outs ? outs[i] : in;
+            const uintptr_t in = (uintptr_t)grads[i], out = outs ? (uintptr_t)outs[i] : in;
             if (!in || !out) return CONV_ERR_NULL_ARG;
-            if ((uintptr_t)in % g.es[i] || (uintptr_t)out % g.es[i]) return CONV_ERR_MISALIGNED;
-            const size_t bytes = (size_t)g.counts[i] * g.es[i];
-            add(out, bytes, true);
-            if (in != out) add(in, bytes, false);
+            if ((in | out) % g.es[i]) return CONV_ERR_MISALIGNED;
+            const uintptr_t bytes = (uintptr_t)g.counts[i] * g.es[i];
+            written.push_back({out, out + bytes, true});
+            if (in != out) read.push_back({in, in + bytes, false});
         }
-        if (overlap(ranges)) return CONV_ERR_ALIASING;
+        if (overlap(read, written)) return CONV_ERR_ALIASING;
+        const uintptr_t n0 = (uintptr_t)norm, w0 = (uintptr_t)workspace, w1 = w0 + p->ws_bytes;
+        for (const std::vector<Range> *list : {&read, &written})
+            for (const Range &i : *list)
+                if ((i.from < n0 + 4 && n0 < i.to) || (i.from < w1 && w0 < i.to)) return CONV_ERR_ALIASING;
+        if (conv_overlaps(norm, 4, workspace, p->ws_bytes)) return CONV_ERR_ALIASING;
     } catch (...) {
         return CONV_ERR_OOM;
     }
     const Run r = {&g, grads, outs, max_norm, norm, static_cast<double *>(workspace), (cudaStream_t)stream};
-    for (const bool scale : {false, true})
+    if (g.small) return launch_batch(r, g.batches[0], SMALL) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+    for (const int which : {NORM, SCALE})
         for (const ClipBatch &b : g.batches)
-            if (launch_batch(r, b, scale) != cudaSuccess) return CONV_ERR_CUDA;
+            if (launch_batch(r, b, which) != cudaSuccess) return CONV_ERR_CUDA;
     return CONV_OK;
 }

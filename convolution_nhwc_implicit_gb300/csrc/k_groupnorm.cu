@@ -323,16 +323,6 @@ __device__ __forceinline__ float2 about(float K, float2 s, float cnt) {
     return make_float2(K + d, fmaxf(s.y - s.x * d, 0.0f) + 0.0f * s.y);  // (NaN stays NaN)
 }
 
-// Distributed shared memory: another CTA's copy of a variable of this one's.
-__device__ __forceinline__ float2 ld_peer(const float2 *p, uint32_t rank) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(tc::mapa_shared(tc::smem_u32(p), rank)) : "memory");
-    return v;
-}
-// (every thread of the CTA, warps converged)
-__device__ __forceinline__ void cluster_arrive() { __syncwarp(); asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { __syncwarp(); asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-
 // (mean, M2) of a group over `n` consecutive runs of `len` pixels of `total`
 // (the last ones short or empty), run q's from get(q); n <= 8.
 template <typename F>

@@ -75,6 +75,16 @@ __device__ __forceinline__ void copy_vec(Raw *dst, const Raw *src) {
     else *dst = *src;
 }
 
+// Distributed shared memory: another CTA's copy of a variable of this one's.
+__device__ __forceinline__ float2 ld_peer(const float2 *p, uint32_t rank) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(tc::mapa_shared(tc::smem_u32(p), rank)) : "memory");
+    return v;
+}
+// (every thread of the CTA, warps converged)
+__device__ __forceinline__ void cluster_arrive() { __syncwarp(); asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { __syncwarp(); asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Whether two maps of `rows` pixels share an element.  Two channel slices of
 // one buffer (the same pitch) interleave without sharing any.
 inline bool maps_overlap(const void *a, long long pa, const void *b, long long pb, long long rows, int C, int es) {

@@ -178,6 +178,10 @@ CASES = [
     (700, 1, 1, 96, "layer", "layer", "bf16", True, 0, 0),     # a pixel an image: whole images, more than CTAs
     (350, 3, 3, 40, "rms", "layer", "f32", True, 0, 0),
     (3, 50, 50, 64, "none", "rms", "bf16", True, 0, 0),        # runs of an image
+    (4, 8, 8, 96, "layer", "layer", "bf16", True, 0, 0),       # a cluster: four images of few rows
+    (1, 10, 50, 256, "rms", "rms", "bf16", False, 0, 0),       # ... four sets of rows a CTA, the last one short
+    (1, 1, 9, 3001, "layer", "rms", "f32", True, 0, 0),        # ... a row at a time
+    (5, 3, 2, 70, "rms", "layer", "bf16", True, 0, 0),         # more images than that
     (1, 80, 80, 256, "none", "none", "bf16", True, 0, 0),      # a gated residual add
     (2, 30, 30, 32, "layer", "none", "f32", True, 0, 0),
     (2, 160, 160, 64, "rms", "layer", "bf16", False, 0, 0),
@@ -456,8 +460,16 @@ def test_refusals(cl):
     assert lib.conv_run_blocknorm(*(args[:10] + [y.data_ptr(), None])) == -5
     back = [plan.handle, x.data_ptr(), 0, f.data_ptr(), 0, None, stats.data_ptr(), None, 0, dz.data_ptr(), 0, dx.data_ptr(), 0,
             df.data_ptr(), 0, None]
-    assert lib.conv_run_blocknorm_bwd(*back, None, None) == -1               # no workspace
-    assert lib.conv_run_blocknorm_bwd(*back, x.data_ptr(), None) == -5       # a workspace over x
+    assert plan.workspace_bytes_backward == 0 and lib.conv_run_blocknorm_bwd(*back, None, None) == 0
+    big = cl.BlockNormPlan(1, 160, 160, 64, "rms", "layer")
+    m = torch.zeros(5, 1, 160, 160, 64, device="cuda", dtype=torch.bfloat16)
+    st = torch.zeros(1, 160, 160, 4, device="cuda")
+    big.run(m[0], m[1], None, m[2], st)
+    big.run_backward(m[0], m[1], st, None, m[2], m[3], m[4], dscale=torch.empty(64, device="cuda"))
+    back = [big.handle, m[0].data_ptr(), 0, m[1].data_ptr(), 0, None, st.data_ptr(), None, 0, m[2].data_ptr(), 0, m[3].data_ptr(), 0,
+            m[4].data_ptr(), 0, None]
+    assert big.workspace_bytes_backward > 0 and lib.conv_run_blocknorm_bwd(*back, None, None) == -1  # no workspace
+    assert lib.conv_run_blocknorm_bwd(*back, m[0].data_ptr(), None) == -5                            # one over x
     assert lib.conv_run(plan.handle, x.data_ptr(), x.data_ptr(), None, y.data_ptr(), None) == -9
     assert plan.algo == "blocknorm" and plan.launches == 1 and plan.describe().startswith("blocknorm")
     plan.check_device_status()
