@@ -63,51 +63,67 @@ __device__ __forceinline__ void add_image(const BnArgs &a, int n, bool first, in
     const float gate = a.gate[(long long)n * a.C + c];
     *p = first ? gate * v : fmaf(gate, v, *p);
 }
-__device__ __forceinline__ float gate_grad(const BnArgs &a, int c, float A, float B) {
-    return (a.scale ? a.scale[c] : 1.0f) * ((a.g1 ? a.g1[c] : 1.0f) * A + (a.b1 ? a.b1[c] : 0.0f) * B);
-}
+// What the parameters' gradients of a channel need of the others, loaded ahead.
+struct Others {
+    float scale, g1, b1;
+    __device__ __forceinline__ Others(const BnArgs &a, int c, bool on)
+        : scale(on && a.scale ? a.scale[c] : 1.0f), g1(on && a.g1 ? a.g1[c] : 1.0f), b1(on && a.b1 ? a.b1[c] : 0.0f) {}
+    // (A and B over an image)
+    __device__ __forceinline__ float gate(float A, float B) const { return scale * (g1 * A + b1 * B); }
+    // from the sums over all pixels, A and B times the gates
+    __device__ __forceinline__ void put(const BnArgs &a, int c, float A, float B, float G2, float B2) const {
+        if (a.dscale) a.dscale[c] = g1 * A + b1 * B;
+        if (a.dg1) a.dg1[c] = scale * A;
+        if (a.db1) a.db1[c] = scale * B;
+        if (a.dg2) a.dg2[c] = G2;
+        if (a.db2) a.db2[c] = B2;
+    }
+};
 
-// The parameters' gradients of a channel, from its sums over all pixels (A and B
-// times the gates).
-__device__ __forceinline__ void param_grads(const BnArgs &a, int c, float A, float B, float G2, float B2) {
-    const float scale = a.scale ? a.scale[c] : 1.0f;
-    if (a.dscale) a.dscale[c] = (a.g1 ? a.g1[c] : 1.0f) * A + (a.b1 ? a.b1[c] : 0.0f) * B;
-    if (a.dg1) a.dg1[c] = scale * A;
-    if (a.db1) a.db1[c] = scale * B;
-    if (a.dg2) a.dg2[c] = G2;
-    if (a.db2) a.db2[c] = B2;
-}
-
-// The sum of a shared value over `n` CTAs of the cluster from `from` on, in their
-// order.
-__device__ __forceinline__ float cluster_sum(const float *p, int from, int n) {
-    const uint32_t at = tc::smem_u32(p);
-    float v[kCluster];
-#pragma unroll
-    for (int r = 0; r < kCluster; ++r)
-        if (r < n) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(tc::mapa_shared(at, from + r)) : "memory");
-    float s = 0.0f;
-#pragma unroll
-    for (int r = 0; r < kCluster; ++r)
-        if (r < n) s += v[r];
-    return s;
-}
 // The CTAs of a cluster, a unit each, join their sums: `mine` [SUMS][Cp] is the
-// calling CTA's, which joins a share of the channels.
+// calling CTA's, which joins a share of the channels, a thread each.  What a
+// channel needs besides is on its way while the CTAs wait for one another.
 __device__ __forceinline__ void join_cluster(const BnArgs &a, const float *mine) {
     cluster_arrive();
-    cluster_wait();
     const int ranks = (int)gridDim.x, share = (a.C + ranks - 1) / ranks, c1 = min(a.C, ((int)blockIdx.x + 1) * share);
-    for (int c = (int)blockIdx.x * share + threadIdx.x; c < c1; c += blockDim.x) {
-        float A = 0.0f, B = 0.0f;
-        for (int n = 0, from = 0; from < ranks; ++n, from += a.S) {  // (without a gate, one image)
-            const float ia = cluster_sum(mine + SUM_A * a.Cp + c, from, a.S), ib = cluster_sum(mine + SUM_B * a.Cp + c, from, a.S);
-            const float gate = a.gate ? a.gate[(long long)n * a.C + c] : 1.0f;
-            if (a.dgate) a.dgate[(long long)n * a.C + c] = gate_grad(a, c, ia, ib);
-            A = fmaf(gate, ia, A);
-            B = fmaf(gate, ib, B);
-        }
-        param_grads(a, c, A, B, cluster_sum(mine + SUM_G2 * a.Cp + c, 0, ranks), cluster_sum(mine + SUM_B2 * a.Cp + c, 0, ranks));
+    for (int c = (int)blockIdx.x * share + threadIdx.x; c - (int)threadIdx.x < c1; c += blockDim.x) {
+        const bool on = c < c1, first = c == (int)blockIdx.x * share + (int)threadIdx.x;
+        const Others others(a, c, on);
+        float gate[kCluster];
+#pragma unroll
+        for (int n = 0; n < kCluster; ++n) gate[n] = on && a.gate && n < a.N ? a.gate[(long long)n * a.C + c] : 1.0f;
+        if (first) cluster_wait();
+        if (!on) continue;
+        const uint32_t at = tc::smem_u32(mine + c);
+        float v[SUMS][kCluster];
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r)
+            if (r < ranks) {
+                const uint32_t peer = tc::mapa_shared(at, r);
+#pragma unroll
+                for (int s = 0; s < SUMS; ++s)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[s][r]) : "r"(peer + s * a.Cp * 4) : "memory");
+            }
+        float A = 0.0f, B = 0.0f, G2 = 0.0f, B2 = 0.0f, ia = 0.0f, ib = 0.0f;
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r)  // (S CTAs an image; without a gate, all of one)
+            if (r < ranks) {
+                ia += v[SUM_A][r];
+                ib += v[SUM_B][r];
+                G2 += v[SUM_G2][r];
+                B2 += v[SUM_B2][r];
+                if ((r + 1) % a.S == 0) {
+                    const int n = r / a.S;
+                    float k = gate[0];
+#pragma unroll
+                    for (int j = 1; j < kCluster; ++j) k = n == j ? gate[j] : k;
+                    if (a.dgate) a.dgate[(long long)n * a.C + c] = others.gate(ia, ib);
+                    A = fmaf(k, ia, A);
+                    B = fmaf(k, ib, B);
+                    ia = ib = 0.0f;
+                }
+            }
+        others.put(a, c, A, B, G2, B2);
     }
     cluster_arrive();  // (no CTA ends while its sums may still be read)
     cluster_wait();
@@ -268,13 +284,8 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             odz += (unsigned)sdz;
         }
         copy_wait<0>();
-        if (a.joined) {
-            // (the CTA's sums after the threads')
-            float *mine = reinterpret_cast<float *>(ent + (a.slots > 1 ? SUMS * P * nt : 0));
-            if (a.slots == 1) __syncthreads();
-            combine<0, SUMS, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { mine[s * a.Cp + c] = v; });
-            join_cluster(a, mine);
-        } else if (a.whole) {
+        if (a.joined) break;  // (a CTA has one unit)
+        if (a.whole) {
             const bool first = unit == (int)blockIdx.x;
             float *both_sums = reinterpret_cast<float *>(ent + 2 * P * nt);  // [A, B][C]: of a channel, two threads'
             if (a.slots == 1) __syncthreads();
@@ -284,14 +295,20 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             });
             if (a.dgate) {
                 __syncthreads();
-                for (int c = threadIdx.x; c < a.C; c += nt) a.dgate[(long long)n * a.C + c] = gate_grad(a, c, both_sums[c], both_sums[a.C + c]);
+                for (int c = threadIdx.x; c < a.C; c += nt) a.dgate[(long long)n * a.C + c] = Others(a, c, true).gate(both_sums[c], both_sums[a.C + c]);
                 __syncthreads();
             }
 #pragma unroll
             for (int i = 0; i < P; ++i) acc[SUM_A][i] = acc[SUM_B][i] = make_float2(0.0f, 0.0f);
         } else combine<0, SUMS, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { *place(a, unit, s, c) = v; });
     }
-    if (a.whole)
+    if (a.joined) {
+        // (the CTA's sums after the threads')
+        float *mine = reinterpret_cast<float *>(ent + (a.slots > 1 ? SUMS * P * nt : 0));
+        if (a.slots == 1) __syncthreads();
+        combine<0, SUMS, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { mine[s * a.Cp + c] = v; });
+        join_cluster(a, mine);
+    } else if (a.whole)
         combine<SUM_G2, 2, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { *place(a, blockIdx.x, s, c) = v; });
 }
 
@@ -516,7 +533,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_long_kernel(const __grid_
                         continue;
                     }
                     for (int s = 0; s < SUM_G2; ++s) add_image(a, n, unit == (int)blockIdx.x, s, c, one(s));
-                    if (a.dgate) a.dgate[(long long)n * a.C + c] = gate_grad(a, c, one(SUM_A), one(SUM_B));
+                    if (a.dgate) a.dgate[(long long)n * a.C + c] = Others(a, c, true).gate(one(SUM_A), one(SUM_B));
                     if (unit + (int)gridDim.x >= a.units)
                         for (int s = SUM_G2; s < SUMS; ++s) *place(a, blockIdx.x, s, c) = one(s);
                 }
@@ -556,6 +573,8 @@ __global__ void __launch_bounds__(kJoin) bn_join_kernel(const __grid_constant__ 
     pdl_trigger();
     pdl_wait();
     const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int at = blockIdx.x * kJoinC + (lane & 15);  // the first warp's channels, a lane each, twice
+    const Others others(a, at, warp == 0 && at < a.C && blockIdx.y == 0);
     if (blockIdx.y > 0) {
         const int n = (blockIdx.y - 1) * (kJoin / 32) + warp;
         float4 A = zero, B = zero;
@@ -569,10 +588,9 @@ __global__ void __launch_bounds__(kJoin) bn_join_kernel(const __grid_constant__ 
         B = sum8(B);
         if (n < a.N && group < 4 && c + group < a.C) {
             const int k = c + group;
-            const float g1 = a.g1 ? a.g1[k] : 1.0f, b1 = a.b1 ? a.b1[k] : 0.0f;
             const float va = group == 0 ? A.x : (group == 1 ? A.y : (group == 2 ? A.z : A.w));
             const float vb = group == 0 ? B.x : (group == 1 ? B.y : (group == 2 ? B.z : B.w));
-            a.dgate[(long long)n * a.C + k] = (a.scale ? a.scale[k] : 1.0f) * (g1 * va + b1 * vb);
+            a.dgate[(long long)n * a.C + k] = Others(a, k, true).gate(va, vb);
         }
         return;
     }
@@ -599,19 +617,16 @@ __global__ void __launch_bounds__(kJoin) bn_join_kernel(const __grid_constant__ 
         if (group == 0) red[s][warp][four] = v[s];
     }
     __syncthreads();
-    if (warp == 0) {  // a channel a lane, twice
-        const int at = lane & 15, k = blockIdx.x * kJoinC + at;
+    if (warp == 0) {
         float t[SUMS];
 #pragma unroll
         for (int s = 0; s < SUMS; ++s) {
             t[s] = 0.0f;
-            const float *r = reinterpret_cast<const float *>(red[s]) + at;
+            const float *r = reinterpret_cast<const float *>(red[s]) + (lane & 15);
             for (int w = lane >> 4; w < kJoin / 32; w += 2) t[s] += r[w * kJoinC];
             t[s] += __shfl_xor_sync(0xffffffffu, t[s], 16);
         }
-        if (lane < 16 && k < a.C) {
-            param_grads(a, k, t[SUM_A], t[SUM_B], t[SUM_G2], t[SUM_B2]);
-        }
+        if (lane < 16 && at < a.C) others.put(a, at, t[SUM_A], t[SUM_B], t[SUM_G2], t[SUM_B2]);
     }
 }
 
