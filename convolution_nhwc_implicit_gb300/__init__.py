@@ -207,6 +207,28 @@ def _current_stream(device=None):
     return stream_of(device_of() if device is None else device)
 
 
+_raw_memory = None
+
+
+def _raw_memory_calls():
+    """Torch's allocator without a tensor around the block: an address of a
+    stream's memory, and its return.  A run's scratch is a block of the run's own
+    stream, given back when the run is queued: whoever gets it next is ordered
+    after the run.  Looked up once.  (Among launches a tensor costs a call 5 us,
+    this 1.5.)"""
+    global _raw_memory
+    if _raw_memory is None:
+        import torch
+        torch.cuda.init()
+        try:
+            _raw_memory = torch._C._cuda_cudaCachingAllocator_raw_alloc, torch._C._cuda_cudaCachingAllocator_raw_delete
+        except AttributeError:
+            def alloc(nbytes, handle):
+                return torch.cuda.caching_allocator_alloc(nbytes, stream=handle)
+            _raw_memory = alloc, torch.cuda.caching_allocator_delete
+    return _raw_memory
+
+
 def _stream_handle(stream, device=None):
     if stream is None:
         return _current_stream(device)
@@ -760,10 +782,15 @@ class BlockNormPlan(_MapPlan):
         p, (ix, jf, iy, iz, kx, kf) = self._addresses(
             _BLOCKNORM_BWD, (x, f, dy, dz, dx, df, stats, scale, gate, post_gamma, post_beta, pre_gamma, dscale, dgate,
                              dpost_gamma, dpost_beta, dpre_gamma, dpre_beta))
-        ws = self._workspace(self.workspace_bytes_backward, x, stream)
-        rc = self._lib.conv_run_blocknorm_bwd(self._handle, p[0], ix, p[1], jf, _BlockNormPointers(*p[7:12]), p[6], p[2], iy,
-                                              p[3], iz, p[4], kx, p[5], kf, _BlockNormPointers(*p[12:]), _ptr(ws),
-                                              _stream_handle(stream, dev))
+        handle = _stream_handle(stream, dev)
+        take, give = _raw_memory_calls()
+        ws = take(self.workspace_bytes_backward, handle) if self.workspace_bytes_backward else None
+        try:
+            rc = self._lib.conv_run_blocknorm_bwd(self._handle, p[0], ix, p[1], jf, _BlockNormPointers(*p[7:12]), p[6], p[2],
+                                                  iy, p[3], iz, p[4], kx, p[5], kf, _BlockNormPointers(*p[12:]), ws, handle)
+        finally:
+            if ws is not None:
+                give(ws)
         if rc != 0:
             raise ConvError("conv_run_blocknorm_bwd", rc)
 
@@ -822,8 +849,15 @@ class GradClipPlan(_OpPlan):
         g = self._addresses("grads", grads)
         o = None if out is None else self._addresses("out", out)
         pn = _check("norm", norm, (), self._f32, dev)
-        ws = self._workspace(self.workspace_bytes, norm, stream)
-        rc = self._lib.conv_run_gradclip(self._handle, g.buffer_info()[0], o and o.buffer_info()[0], float(max_norm), pn, _ptr(ws), _stream_handle(stream, dev))
+        handle = _stream_handle(stream, dev)
+        take, give = _raw_memory_calls()
+        ws = take(self.workspace_bytes, handle) if self.workspace_bytes else None
+        try:
+            rc = self._lib.conv_run_gradclip(self._handle, g.buffer_info()[0], o and o.buffer_info()[0], float(max_norm), pn,
+                                             ws, handle)
+        finally:
+            if ws is not None:
+                give(ws)
         if rc != 0:
             raise ConvError("conv_run_gradclip", rc)
 
