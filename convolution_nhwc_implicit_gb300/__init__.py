@@ -527,14 +527,17 @@ class _MapPlan(_OpPlan):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {self.shape}")
         if t.get_device() != self._device:
             raise ValueError(f"{name} must be on cuda:{self._device}, got a tensor on {t.device}")
-        if t.is_contiguous():
-            return t.data_ptr(), c
+        return t.data_ptr(), c if t.is_contiguous() else self._pitch(name, t)
+
+    def _pitch(self, name, t):
+        """Pixel pitch of a feature map that is not dense."""
+        n, h, w, c = self.shape
         sn, sh, sw, sc = t.stride()
         # a size of one says nothing about its stride
         pitch = sw if w > 1 else (sh if h > 1 else (sn if n > 1 else c))
         if ((c > 1 and sc != 1) or pitch < c or (h > 1 and sh != w * pitch) or (n > 1 and sn != h * w * pitch)):
             raise ValueError(f"{name}: pixels must lie one pitch apart with their channels together, got strides {t.stride()}")
-        return t.data_ptr(), pitch
+        return pitch
 
 
 class GroupNormPlan(_MapPlan):
@@ -734,13 +737,17 @@ class BlockNormPlan(_MapPlan):
         pitches = [0] * maps
         shape_of, dtype_of, dense, device_of, address, _ = _tensor_getters()
         try:
-            good = (list(map(shape_of, ts)) == shapes and list(map(dtype_of, ts)) == dtypes and
-                    list(map(device_of, ts)) == devices and all(map(dense, ts)))
-            if good:
-                found = list(map(address, ts))
+            good = list(map(shape_of, ts)) == shapes and list(map(dtype_of, ts)) == dtypes and list(map(device_of, ts)) == devices
+            whole = list(map(dense, ts))
+            if good and False in whole:  # slices, unless it is no map
+                for k, t, flat in zip(given, ts, whole):
+                    if not flat and k in _BLOCKNORM_MAPS:
+                        pitches[names.index(k)] = self._pitch(k, t)
+                    good = good and (flat or k in _BLOCKNORM_MAPS)
+            found = list(map(address, ts))
         except (AttributeError, TypeError):  # (not tensors)
             good = False
-        if not good:  # slices, or what is to be refused: one by one
+        if not good:  # what is to be refused: one by one
             found = []
             for k, t, shape, dtype in zip(given, ts, shapes, dtypes):
                 if k in _BLOCKNORM_MAPS:

@@ -18,8 +18,8 @@ using namespace convk;
 constexpr int kMaxC = 8192;        // channels: 512 threads of 16
 constexpr int kThreads = 256;      // of a forward CTA whose rows take no more
 constexpr int kMostThreads = 512;  // of a row, and of the gradient's CTAs
-constexpr int kCluster = 8;        // CTAs of a gradient in one launch, and the sets of rows that each takes at most
-constexpr int kClusterSets = 4;
+constexpr int kCluster = 16;       // CTAs of a gradient in one launch, and the sets of rows that each takes at most
+constexpr int kClusterSets = 2;
 enum { SUM_A, SUM_B, SUM_G2, SUM_B2, SUMS };
 
 struct BnArgs {
@@ -162,15 +162,19 @@ enum { ROW_PART, ROW_WARP, ROW_WARPS, ROW_ANY };
 
 // Two sums over the threads of a row, to all of them.  The first exchange
 // leaves one sum to each half of the lanes, which halves the exchanges.  Rows of
-// more than a warp then meet in one of two sets of shared entries in turn:
-// whoever writes an entry again has passed the barrier of the other set, and
-// with it everyone's reading of this one.
-template <int ROW>
+// more than a warp then meet in one of two sets of shared entries in turn, a pair
+// of warps an entry: whoever writes an entry again has passed the barrier of the
+// other set, and with it everyone's reading of this one.
+constexpr int kMeet = 12;  // entries of a set: an odd number of warps a row leaves halves empty
+template <int ROW, bool FEW = true>
 struct RowSum {
-    int tpr, slot;
-    float *buf;  // [2][warps][2]
+    int tpr, slot, pairs;
+    float4 *buf;  // [2][kMeet] (two sums of a warp, two of the next)
     int flip;
-    __device__ __forceinline__ RowSum(int tpr_, int slot_, float *b) : tpr(tpr_), slot(slot_), buf(b), flip(0) {}
+    __device__ __forceinline__ RowSum(int tpr_, int slot_, float4 *b) : tpr(tpr_), slot(slot_), pairs((tpr_ / 32 + 1) / 2), buf(b + slot_ * pairs), flip(0) {
+        if (ROW >= ROW_WARPS && tpr > 32 && (tpr / 32) % 2 && threadIdx.x - slot * tpr < 2)  // (ordered by the first barrier)
+            reinterpret_cast<float2 *>(buf + (threadIdx.x - slot * tpr) * kMeet + pairs - 1)[1] = make_float2(0.0f, 0.0f);
+    }
     __device__ static __forceinline__ float across(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
     __device__ __forceinline__ float2 operator()(float a, float b) {
         const int lane = threadIdx.x & 31;
@@ -188,12 +192,23 @@ struct RowSum {
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1) v += across(v, o);
         if (ROW == ROW_WARPS || (ROW == ROW_ANY && tpr > 32)) {
-            float *e = buf + flip;
-            flip ^= kMostThreads / 32 * 2;
-            if ((lane & 15) == 0) e[(threadIdx.x >> 5) * 2 + (lane >> 4)] = v;
+            float4 *e = buf + flip;
+            flip ^= kMeet;
+            if ((lane & 15) == 0) reinterpret_cast<float *>(e)[(threadIdx.x - slot * tpr) / 32 * 2 + (lane >> 4)] = v;
             asm volatile("bar.sync %0, %1;" ::"r"(1 + slot), "r"(tpr) : "memory");
-            const int n = tpr >> 5, k = lane & 15;
-            v = k < n ? e[(slot * n + k) * 2 + (lane >> 4)] : 0.0f;
+            // up to six warps: every thread reads them all (8x40x40x512 bf16 12.5 us
+            // forward, 14.0 where lanes read one each and exchange; 4096 channels,
+            // sixteen warps, 57 and 54).  FEW false spares registers.
+            if (FEW && pairs <= 3) {
+                float2 s = make_float2(0.0f, 0.0f);
+                for (int i = 0; i < pairs; ++i) {
+                    const float4 f = e[i];
+                    s = add2(s, add2(make_float2(f.x, f.y), make_float2(f.z, f.w)));
+                }
+                return s;
+            }
+            const int k = lane & 15;
+            v = k < 2 * pairs ? reinterpret_cast<const float *>(e)[k * 2 + (lane >> 4)] : 0.0f;
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) v += across(v, o);
         }
@@ -212,8 +227,8 @@ __device__ __forceinline__ float total(const float2 (&v)[P]) {
 }
 
 // m and r of one norm of RB rows (1 or 2), and the values normalised in place.
-template <int VEC, int K, int RB, int ROW>
-__device__ __forceinline__ void normalise(const Lane<VEC, K> &l, RowSum<ROW> &sum, float2 (&v)[RB][4 * K], int kind, const BnArgs &a,
+template <int VEC, int K, int RB, typename SUM>
+__device__ __forceinline__ void normalise(const Lane<VEC, K> &l, SUM &sum, float2 (&v)[RB][4 * K], int kind, const BnArgs &a,
                                           float2 (&mr)[RB]) {
     constexpr int P = 4 * K;
     float2 m = make_float2(0.0f, 0.0f);

@@ -99,16 +99,15 @@ struct XentGeom {
     int dx_split, dx_kper, dw_split, dw_kper;
 };
 
-// Norms around a block: threads of a row, k times 8 channels a thread (full: all
-// of them in the row).  How each direction divides the rows, without a gate and
-// with one: rows side by side in a CTA and rb of them at a time in a thread (0:
-// the gradient), units of `run` rows, S an image (or of all rows); whole: a unit
-// is an image; joined: the CTAs are one cluster.
+// Norms around a block: how each direction covers and divides the rows, without
+// a gate and with one.  k times 8 channels a thread, tpr threads a row (full: all
+// their channels in the row), rows side by side in a CTA and rb of them at a time
+// in a thread (0: the gradient), units of `run` rows, S an image (or of all rows);
+// whole: a unit is an image; joined: the CTAs are one cluster.
 struct BnGeom {
     int post, pre;
     float eps;
-    int k, tpr, full;
-    struct Part { int rb, slots, threads, run, S, units, grid, whole, joined; } fwd, fwd_gated, bwd, bwd_gated;
+    struct Part { int rb, k, tpr, full, slots, threads, run, S, units, grid, whole, joined; } fwd, fwd_gated, bwd, bwd_gated;
 };
 
 struct ClipGeom;  // gradient norm and clipping (k_gradclip.cu)

@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
     using Slot = typename R::Slot;
     constexpr int P = R::P, D = fwd_stages(R::kElement, K), LINE = R::NV * R::step, STAGE = 2 * RB * LINE;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float meet[2 * kMostThreads / 32 * 2];
+    __shared__ float4 meet[2 * kMeet];
     Slot *ring = R::ring(smem, D * 2 * RB);  // [D][x, f][RB]
     const Lane<VEC, K> l(a);
     RowSum<ROW> sum(a.tpr, l.slot, meet);
@@ -167,6 +167,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
 // ------------------------------------------------------------------ host side
 template <typename T, int VEC>
 const void *pick_fwd(int k, int rb, int tpr, bool all) {
+    if (k == 2 && tpr <= 32) return all && tpr == 32 ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARP, true> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_ANY, false>;
     if (k == 2) return all ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, true> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, false>;
     if (rb == 1) return (const void *)&bn_fwd_kernel<T, VEC, 1, 1, ROW_ANY, false>;
     if (!all) return (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_ANY, false>;
@@ -206,21 +207,21 @@ long long up(long long a, long long b) { return (a + b - 1) / b; }
 // row, and there are rows side by side where that is at most half of them: 64.)
 static_assert(3 * 4 * 8 * 2 >= SUMS * 8 * 4 + SUMS * 8 * 4 / 2, "");
 // es: of an element in the ring.
-size_t ring_bytes(const BnGeom &g, const BnGeom::Part &d, int es) {
-    const size_t maps = (size_t)d.threads * 8 * g.k * es;
-    if (d.rb) return 2 * fwd_stages(es, g.k) * d.rb * maps + (g.k > 1 ? (size_t)d.threads * 2 * 8 * g.k * 4 : 0);
-    const int stages = bwd_stages(es, g.k);  // (and a row's statistics, and the parameters of long rows)
-    return stages * (4 * maps + (size_t)d.threads / (g.tpr < 32 ? g.tpr : 32) * 16) + (g.k > 1 ? (size_t)d.threads * 3 * 8 * g.k * 4 : 0);
+size_t ring_bytes(const BnGeom::Part &d, int es) {
+    const size_t maps = (size_t)d.threads * 8 * d.k * es;
+    if (d.rb) return 2 * fwd_stages(es, d.k) * d.rb * maps + (d.k > 1 ? (size_t)d.threads * 2 * 8 * d.k * 4 : 0);
+    const int stages = bwd_stages(es, d.k);  // (and a row's statistics, and the parameters of long rows)
+    return stages * (4 * maps + (size_t)d.threads / (d.tpr < 32 ? d.tpr : 32) * 16) + (d.k > 1 ? (size_t)d.threads * 3 * 8 * d.k * 4 : 0);
 }
 
 cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a, cudaStream_t st) {
-    const size_t smem = ring_bytes(p->bn, d, ring_element(conv_esize(p->dtype), vec));
-    const void *k = pick_kernel(p->dtype, vec, d.rb, p->bn.k, p->bn.tpr, d.rb ? a.f && a.o0 && a.o1 : a.f && a.dy && a.dz);
+    const size_t smem = ring_bytes(d, ring_element(conv_esize(p->dtype), vec));
+    const void *k = pick_kernel(p->dtype, vec, d.rb, d.k, d.tpr, d.rb ? a.f && a.o0 && a.o1 : a.f && a.dy && a.dz);
     if (smem > 40 * 1024) {  // (with the kernel's static shared memory: 48 KB are free)
         const int rc = conv_grant_smem_once(k, p->device, (int)smem);
         if (rc != CONV_OK) return cudaErrorInvalidValue;
     }
-    a.slots = d.slots; a.run = d.run; a.S = d.S; a.units = d.units; a.whole = d.whole; a.joined = d.joined;
+    a.tpr = d.tpr; a.full = d.full; a.slots = d.slots; a.run = d.run; a.S = d.S; a.units = d.units; a.whole = d.whole; a.joined = d.joined;
     void *args[] = {&a};
     return conv_launch(k, dim3((unsigned)d.grid), dim3((unsigned)d.threads), args, smem, st, d.joined ? d.grid : 1);
 }
@@ -294,30 +295,35 @@ void divide_images(BnGeom::Part &d, long long N, long long HW, long long set, lo
 void plan_geometry(conv_plan *p) {
     BnGeom &g = p->bn;
     const int C = p->s.c_in, es = conv_esize(p->dtype);
-    g.k = C <= 8 * kMostThreads ? 1 : 2;
-    const int want = (C + 8 * g.k - 1) / (8 * g.k);
-    int tpr = 1;
-    if (want > 32) tpr = (want + 31) / 32 * 32;
-    else while (tpr < want) tpr *= 2;
-    g.tpr = tpr;
-    g.full = C == tpr * 8 * g.k;
     const long long N = p->s.n, HW = (long long)p->s.h * p->s.w, rows = N * HW;
     p->ws_bytes = p->ws_bwd_bytes = 0;
     if (rows == 0) return;
-    auto part = [&](BnGeom::Part &d, int rb, int threads) {
+    auto part = [&](BnGeom::Part &d, int rb, int k, int threads) {
         d.rb = rb;
-        d.slots = tpr <= threads ? threads / tpr : 1;
-        d.threads = tpr * d.slots;
+        d.k = k;
+        const int want = (C + 8 * k - 1) / (8 * k);
+        d.tpr = 1;
+        if (want > 32) d.tpr = (want + 31) / 32 * 32;
+        else while (d.tpr < want) d.tpr *= 2;
+        d.full = C == d.tpr * 8 * k;
+        d.slots = d.tpr <= threads ? threads / d.tpr : 1;
+        d.threads = d.tpr * d.slots;
     };
     // CTAs of one wave: 512 threads a SM, where their rings fit
     auto wave = [&](const BnGeom::Part &d) {
-        const long long smem = (220 * 1024) / (long long)(ring_bytes(g, d, es) + 1024), regs = kMostThreads / d.threads;
+        const long long smem = (228 * 1024) / (long long)(ring_bytes(d, es) + 1024 + 256), regs = kMostThreads / d.threads;
         const long long n = smem < regs ? smem : regs;
         return (long long)p->num_sms * (n < 1 ? 1 : n);
     };
     // two rows at a time where a CTA takes more than one set of rows
-    part(g.fwd, 1, kThreads);
-    if (g.k == 1 && rows > (long long)p->num_sms * g.fwd.slots) g.fwd.rb = 2;
+    // sixteen channels a thread: beyond 4096, where eight would take more threads
+    // than a CTA has registers for, and forward beyond 2048, where eight leave one
+    // CTA a SM (6144x2560 bf16 36 us, with sixteen 27; 8192x4096 55 and 51; below,
+    // 4096x2048 16.5 and 15.7, 3200x1024 7.2 and 7.7; the gradient 58 and 84, 91
+    // and 133)
+    const int fk = C > 2048 ? 2 : 1, bk = C > 8 * kMostThreads ? 2 : 1;
+    part(g.fwd, 1, fk, kThreads);
+    if (fk == 1 && rows > (long long)p->num_sms * g.fwd.slots) g.fwd.rb = 2;
     g.fwd_gated = g.fwd;
     divide_rows(g.fwd, rows, (long long)g.fwd.slots * g.fwd.rb, wave(g.fwd));
     if (g.fwd.rb == 2 && HW >= 4LL * g.fwd.slots) divide_images(g.fwd_gated, N, HW, 2LL * g.fwd.slots, wave(g.fwd_gated));
@@ -326,7 +332,7 @@ void plan_geometry(conv_plan *p) {
         divide_rows(g.fwd_gated, rows, g.fwd.slots, wave(g.fwd_gated));
     }
     // the gradient in large CTAs: a part of the sums from each
-    part(g.bwd, 0, kMostThreads);
+    part(g.bwd, 0, bk, bk > 1 ? 1 : kMostThreads);
     g.bwd_gated = g.bwd;
     const long long w = wave(g.bwd);
     divide_rows(g.bwd, rows, g.bwd.slots, w);
@@ -335,7 +341,7 @@ void plan_geometry(conv_plan *p) {
     // themselves, where none takes more than four sets of rows
     auto cluster = [&](BnGeom::Part &d, long long images, long long each) {
         const long long most = images <= kCluster ? kCluster / images : 0, sets = most ? up(each, most * d.slots) : 0;
-        if (g.k > 1 || !most || sets > kClusterSets) return;
+        if (bk > 1 || !most || sets > kClusterSets) return;
         d.run = (int)(sets * d.slots);
         d.S = (int)up(each, d.run);
         d.units = d.grid = (int)images * d.S;
@@ -378,9 +384,16 @@ extern "C" int conv_plan_create_blocknorm(int32_t n, int32_t h, int32_t w, int32
         return rc;
     }
     plan_geometry(p);
+    if ((p->bn.bwd.joined && p->bn.bwd.grid > 8) || (p->bn.bwd_gated.joined && p->bn.bwd_gated.grid > 8))
+        for (const int vec : {dtype == CONV_F32 ? 4 : 8, dtype == CONV_F32 ? 1 : 2, 1})
+            for (const bool all : {false, true})
+                if (cudaFuncSetAttribute(bn::pick_bwd(dtype, vec, p->bn.bwd.k, p->bn.bwd.tpr, all), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+                    conv_plan_destroy(p);
+                    return CONV_ERR_CUDA;
+                }
     static const char *const names[] = {"none", "layer", "rms"};
     snprintf(p->desc, sizeof(p->desc), "blocknorm %s post=%s pre=%s threads=%dx%d channels/thread=%d ctas=%d gradient: %d, gated %d in %d",
-             dtype == CONV_F32 ? "f32" : "bf16", names[post], names[pre], p->bn.fwd.slots, p->bn.tpr, 8 * p->bn.k, p->bn.fwd.grid,
+             dtype == CONV_F32 ? "f32" : "bf16", names[post], names[pre], p->bn.fwd.slots, p->bn.fwd.tpr, 8 * p->bn.fwd.k, p->bn.fwd.grid,
              p->bn.bwd.grid, p->bn.bwd_gated.units, p->bn.bwd_gated.grid);
     *out_plan = p;
     return CONV_OK;
@@ -394,7 +407,6 @@ BnArgs base_args(const conv_plan *p, const conv_blocknorm_params_t &w, const voi
     a.eps = p->bn.eps; a.inv_c = 1.0f / (float)p->s.c_in;
     a.N = p->s.n; a.HW = p->s.h * p->s.w; a.rows = a.N * a.HW; a.C = p->s.c_in; a.Cp = (a.C + 3) / 4 * 4;
     a.post = p->bn.post; a.pre = p->bn.pre;
-    a.tpr = p->bn.tpr; a.full = p->bn.full;
     return a;
 }
 int check_params(const conv_plan *p, const conv_blocknorm_params_t &w, const void *f) {

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
     using Slot = typename R::Slot;
     constexpr int P = R::P, D = bwd_stages(R::kElement, 1), LINE = R::NV * R::step, STAGE = 4 * LINE;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float meet[2 * kMostThreads / 32 * 2];
+    __shared__ float4 meet[2 * kMeet];
     const int nt = blockDim.x;
     Slot *ring = R::ring(smem, D * 4);  // [D][x, f, dy, dz]
     const Lane<VEC, 1> l(a);
@@ -148,7 +148,9 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
                          (threadIdx.x >> 5) * (D * (32 / line)) + lane / line;
     const bool copies = lane % line == 0;
     float2 *const ent = reinterpret_cast<float2 *>(smem);  // after a unit's rows: the threads' sums
-    RowSum<ROW> sum(a.tpr, l.slot, meet);
+    // (fp32: with both ways of meeting, 36 bytes of a thread's registers are spilled,
+    // and 8192x4096 takes 171 us for 135)
+    RowSum<ROW, sizeof(T) == 2> sum(a.tpr, l.slot, meet);
     const bool block = ALL || a.f, stream = ALL || a.dy, norm = ALL || a.dz;
     const float mean_post = a.post == CONV_NORM_LAYER ? -a.inv_c : 0.0f, mean_pre = a.pre == CONV_NORM_LAYER ? -a.inv_c : 0.0f;
     const long long sx = a.slots * a.px, sf = a.slots * a.pf, sdy = a.slots * a.pdy, sdz = a.slots * a.pdz;
@@ -324,14 +326,14 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_long_kernel(const __grid_
     using Slot = typename R::Slot;
     constexpr int H = 2, P = R::P, D = bwd_stages(R::kElement, H), LINE = R::NV * R::step, MAP = H * LINE, STAGE = 4 * MAP;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float meet[2 * kMostThreads / 32 * 2];
+    __shared__ float4 meet[2 * kMeet];
     const int nt = blockDim.x;
     Slot *ring = R::ring(smem, D * 4 * H);  // [D][x, f, dy, dz][H]
     float4 *const par = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * H * R::NV * nt * sizeof(Slot)) + threadIdx.x;  // [q, p, g2][H][2][threads]
     float4 *const seen = par - threadIdx.x + 3 * H * 2 * nt + (threadIdx.x >> 5) * D;  // statistics [warp][D]
     Lane<VEC, 1> l[H] = {Lane<VEC, 1>(a), Lane<VEC, 1>(a)};
     l[1].t += R::NV * a.tpr;
-    RowSum<ROW_WARPS> sum(a.tpr, 0, meet);
+    RowSum<ROW_WARPS, false> sum(a.tpr, 0, meet);
     const bool block = a.f, stream = a.dy, norm = a.dz, copies = (threadIdx.x & 31) == 0;
     const float mean_post = a.post == CONV_NORM_LAYER ? -a.inv_c : 0.0f, mean_pre = a.pre == CONV_NORM_LAYER ? -a.inv_c : 0.0f;
     enum { PAR_Q, PAR_P, PAR_G2 };
