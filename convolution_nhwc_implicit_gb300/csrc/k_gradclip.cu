@@ -41,6 +41,7 @@ struct ClipGeom {
     std::vector<ClipBatch> batches;
     int parts = 0;
     bool small = false;  // one launch of one cluster
+    int past = 0;        // the second reading and the results go past L2
     uint4 *items = nullptr;  // device: (tensor of the batch | fp32 << 31, elements, first element as two words)
     int *first = nullptr;    // device: [grid + 1] of each batch
 };
@@ -53,6 +54,11 @@ constexpr int kItem = 4096;       // elements of an item, at most
 constexpr int kItemLeast = 256;   // ... and at least, but for a tensor's end: a vector a lane
 constexpr int kCluster = 16;      // CTAs of the one-launch form, and the bytes up to which it is taken
 constexpr long long kSmall = 1536 * 1024;
+// Bytes of a set whose second reading and whose results do not displace what is
+// still to be read in L2 (66 MB 34.0 us, 31.5 so; 247 MB 122.4 and 120.6; 2.1 GB,
+// of which L2 holds a twentieth, 916 and 926).
+constexpr long long kPast = 1ll << 29;
+constexpr int kTurn = 1024;       // elements of four vectors a lane, bf16
 constexpr int kMostTensors = 1900;  // of a launch: their addresses are kernel parameters (32 KB at most)
 
 template <int M> struct Tensors { const void *p[M]; };
@@ -168,8 +174,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) clip_norm_kernel(const __grid
     if (threadIdx.x == 0) part[blockIdx.x] = s;
 }
 
+// past: read and written as data that is not used again soon.
 template <typename T>
-__device__ __forceinline__ void scale_item(const T *p, T *q, int n, float k) {
+__device__ __forceinline__ void scale_item(const T *p, T *q, int n, float k, bool past) {
     using W = Words<T>;
     using Raw = typename W::Raw;
     constexpr int U = 4;
@@ -188,7 +195,7 @@ __device__ __forceinline__ void scale_item(const T *p, T *q, int n, float k) {
         Raw r[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            if (i + 32 * u < c.vecs) r[u] = v[i + 32 * u];
+            if (i + 32 * u < c.vecs) r[u] = past ? __ldcs(v + i + 32 * u) : v[i + 32 * u];
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (i + 32 * u < c.vecs) {
@@ -196,7 +203,8 @@ __device__ __forceinline__ void scale_item(const T *p, T *q, int n, float k) {
                 W::unpack(r[u], f);
 #pragma unroll
                 for (int e = 0; e < W::kPairs; ++e) f[e] = mul2(f[e], make_float2(k, k));
-                o[i + 32 * u] = W::pack(f);
+                if (past) __stcs(o + i + 32 * u, W::pack(f));
+                else o[i + 32 * u] = W::pack(f);
             }
     }
 }
@@ -217,15 +225,18 @@ __device__ __forceinline__ float clip_factor(float norm, float max_norm) {
     return isfinite(norm) ? fminf(1.0f, max_norm / (norm + 1e-6f)) : 1.0f;
 }
 // A warp's items i, i - kWarps, ... down to `start`, times k: from the end, which
-// is what is still in L2.
+// is what is still in L2.  it: the first of them.
 template <int M>
-__device__ __forceinline__ void scale_items(const Tensors<M> &t, const Tensors<M> &o, const uint4 *items, int i, int start, float k) {
-    for (; i >= start; i -= kWarps) {
-        const uint4 now = items[i];
+__device__ __forceinline__ void scale_items(const Tensors<M> &t, const Tensors<M> &o, const uint4 *items, int i, int start, uint4 it, float k,
+                                            bool past) {
+    while (i >= start) {
+        const uint4 now = it;
+        i -= kWarps;
+        if (i >= start) it = items[i];
         const long long at = (long long)(((unsigned long long)now.w << 32) | now.z);
         const int j = now.x & 0x7fffffffu;
-        if (now.x >> 31) scale_item(static_cast<const float *>(t.p[j]) + at, (float *)o.p[j] + at, (int)now.y, k);
-        else scale_item(static_cast<const __nv_bfloat16 *>(t.p[j]) + at, (__nv_bfloat16 *)o.p[j] + at, (int)now.y, k);
+        if (now.x >> 31) scale_item(static_cast<const float *>(t.p[j]) + at, (float *)o.p[j] + at, (int)now.y, k, past);
+        else scale_item(static_cast<const __nv_bfloat16 *>(t.p[j]) + at, (__nv_bfloat16 *)o.p[j] + at, (int)now.y, k, past);
     }
 }
 
@@ -234,10 +245,11 @@ template <int M>
 __global__ void __launch_bounds__(kThreads, kCtas) clip_scale_kernel(const __grid_constant__ Tensors<M> t,
                                                                      const __grid_constant__ Tensors<M> o, const uint4 *items,
                                                                      const int *first, const double *part, int parts,
-                                                                     float max_norm, float *norm, int in_place) {
+                                                                     float max_norm, float *norm, int in_place, int past) {
     __shared__ float factor;
     pdl_trigger();
     const int start = first[blockIdx.x], i = first[blockIdx.x + 1] - 1 - (int)(threadIdx.x >> 5);
+    const uint4 it = i >= start ? items[i] : make_uint4(0, 0, 0, 0);
     pdl_wait();
     if (threadIdx.x < 32) {
         double s = 0.0;
@@ -250,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) clip_scale_kernel(const __gri
     }
     __syncthreads();
     if (in_place && factor == 1.0f) return;
-    scale_items(t, o, items, i, start, factor);
+    scale_items(t, o, items, i, start, it, factor, past);
 }
 
 // Both of a small set in one launch: one cluster, whose CTAs read each other's
@@ -263,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) clip_small_kernel(const __gri
     __shared__ float factor;
     pdl_trigger();
     const int start = first[blockIdx.x], end = first[blockIdx.x + 1], warp = (int)(threadIdx.x >> 5), i = start + warp;
-    const uint4 it = i < end ? items[i] : make_uint4(0, 0, 0, 0);
+    const int last = end - 1 - warp;
+    const uint4 it = i < end ? items[i] : make_uint4(0, 0, 0, 0), back = last >= start ? items[last] : make_uint4(0, 0, 0, 0);
     pdl_wait();
     double s = cta_sum(sum_items(t, items, i, end, it), red);
     if (threadIdx.x == 0) mine = s;
@@ -283,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) clip_small_kernel(const __gri
     }
     cluster_arrive();  // (no CTA ends while its sum may still be read)
     __syncthreads();
-    if (!in_place || factor != 1.0f) scale_items(t, o, items, end - 1 - warp, start, factor);
+    if (!in_place || factor != 1.0f) scale_items(t, o, items, last, start, back, factor, false);
     cluster_wait();
 }
 
@@ -320,7 +333,8 @@ cudaError_t launch(const Run &r, const ClipBatch &b, int which) {
         return conv_launch((const void *)&clip_norm_kernel<M>, dim3((unsigned)b.grid), dim3(kThreads), args, 0, r.st);
     }
     const double *part = r.part;
-    void *args[] = {&t, &o, &items, &first, &part, &parts, &max_norm, &norm, &in_place};
+    int past = r.g->past;
+    void *args[] = {&t, &o, &items, &first, &part, &parts, &max_norm, &norm, &in_place, &past};
     return conv_launch((const void *)&clip_scale_kernel<M>, dim3((unsigned)b.grid), dim3(kThreads), args, 0, r.st);
 }
 
@@ -350,8 +364,9 @@ void divide(const ClipGeom &g, ClipBatch &b, int wave, std::vector<uint4> &items
     };
     for (int t = b.t0; t < b.t1; ++t) {
         const int es = g.es[t];
-        const long long per = share / es / kWarps;
-        const int item = (int)std::max<long long>(kItemLeast, std::min<long long>(kItem, (per + kItemLeast - 1) / kItemLeast * kItemLeast));
+        // a warp's elements in one item, in whole turns of its loads where they take several
+        const long long per = share / es / kWarps, unit = per > kTurn ? kTurn : kItemLeast;
+        const int item = (int)std::max<long long>(kItemLeast, std::min<long long>(kItem, (per + unit - 1) / unit * unit));
         for (long long at = 0; at < g.counts[t];) {
             long long n = std::min<long long>(g.counts[t] - at, item);
             // (a share ends on a whole number of vectors of the tensor)
@@ -429,6 +444,7 @@ extern "C" int conv_plan_create_gradclip(int32_t tensors, const int64_t *counts,
             long long bytes = 0;
             for (int i = 0; i < tensors; ++i) bytes += counts[i] * g.es[i];
             g.small = bytes <= kSmall && tensors <= kMostTensors;
+            g.past = bytes < kPast;
             int t = 0;
             do {
                 ClipBatch b = {t, std::min(tensors, t + kMostTensors), 0, 0, g.parts};
