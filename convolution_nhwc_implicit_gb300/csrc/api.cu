@@ -115,6 +115,26 @@ cudaError_t conv_launch(const void *kernel, dim3 grid, dim3 block, void **args, 
     return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
+bool conv_cluster_fits(const void *k, int ctas, int threads, size_t smem) {
+    if (ctas > 8 && cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)ctas;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, k, &cfg) != cudaSuccess) {
+        (void)cudaGetLastError();  // (a size that this device refuses is an answer)
+        return false;
+    }
+    return clusters > 0;
+}
+
 int conv_grant_smem(const void *k, int device, int need) {
     int optin = 0;
     cudaFuncAttributes fa;

@@ -342,9 +342,18 @@ void plan_geometry(conv_plan *p) {
     auto cluster = [&](BnGeom::Part &d, long long images, long long each) {
         const long long most = images <= kCluster ? kCluster / images : 0, sets = most ? up(each, most * d.slots) : 0;
         if (bk > 1 || !most || sets > kClusterSets) return;
-        d.run = (int)(sets * d.slots);
-        d.S = (int)up(each, d.run);
-        d.units = d.grid = (int)images * d.S;
+        const long long run = sets * d.slots, S = up(each, run);
+        for (const int vec : {16 / es, es == 2 ? 2 : 1, 1})
+            for (const bool all : {false, true}) {
+                const void *kernel = pick_kernel(p->dtype, vec, 0, 1, d.tpr, all);
+                const size_t smem = ring_bytes(d, ring_element(es, vec));
+                if (conv_grant_smem_once(kernel, p->device, (int)smem) != CONV_OK ||
+                    !conv_cluster_fits(kernel, (int)(images * S), d.threads, smem))
+                    return;
+            }
+        d.run = (int)run;
+        d.S = (int)S;
+        d.units = d.grid = (int)(images * S);
         d.joined = 1;
     };
     cluster(g.bwd, 1, rows);
@@ -384,13 +393,6 @@ extern "C" int conv_plan_create_blocknorm(int32_t n, int32_t h, int32_t w, int32
         return rc;
     }
     plan_geometry(p);
-    if ((p->bn.bwd.joined && p->bn.bwd.grid > 8) || (p->bn.bwd_gated.joined && p->bn.bwd_gated.grid > 8))
-        for (const int vec : {dtype == CONV_F32 ? 4 : 8, dtype == CONV_F32 ? 1 : 2, 1})
-            for (const bool all : {false, true})
-                if (cudaFuncSetAttribute(bn::pick_bwd(dtype, vec, p->bn.bwd.k, p->bn.bwd.tpr, all), cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-                    conv_plan_destroy(p);
-                    return CONV_ERR_CUDA;
-                }
     static const char *const names[] = {"none", "layer", "rms"};
     snprintf(p->desc, sizeof(p->desc), "blocknorm %s post=%s pre=%s threads=%dx%d channels/thread=%d ctas=%d gradient: %d, gated %d in %d",
              dtype == CONV_F32 ? "f32" : "bf16", names[post], names[pre], p->bn.fwd.slots, p->bn.fwd.tpr, 8 * p->bn.fwd.k, p->bn.fwd.grid,

@@ -322,8 +322,6 @@ cudaError_t launch(const Run &r, const ClipBatch &b, int which) {
     int parts = r.g->parts, in_place = r.outs == nullptr;
     float max_norm = r.max_norm, *norm = b.part == 0 ? r.norm : nullptr;
     if (which == SMALL) {
-        if (b.grid > 8 && cudaFuncSetAttribute((const void *)&clip_small_kernel<M>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-            return cudaErrorInvalidValue;
         void *args[] = {&t, &o, &items, &first, &max_norm, &norm, &in_place};
         return conv_launch((const void *)&clip_small_kernel<M>, dim3((unsigned)b.grid), dim3(kThreads), args, 0, r.st, b.grid);
     }
@@ -336,6 +334,12 @@ cudaError_t launch(const Run &r, const ClipBatch &b, int which) {
     int past = r.g->past;
     void *args[] = {&t, &o, &items, &first, &part, &parts, &max_norm, &norm, &in_place, &past};
     return conv_launch((const void *)&clip_scale_kernel<M>, dim3((unsigned)b.grid), dim3(kThreads), args, 0, r.st);
+}
+
+const void *small_kernel(int tensors) {
+    return tensors <= 32 ? (const void *)&clip_small_kernel<32>
+                         : (tensors <= 128 ? (const void *)&clip_small_kernel<128>
+                                           : (tensors <= 512 ? (const void *)&clip_small_kernel<512> : (const void *)&clip_small_kernel<kMostTensors>));
 }
 
 cudaError_t launch_batch(const Run &r, const ClipBatch &b, int which) {
@@ -443,7 +447,7 @@ extern "C" int conv_plan_create_gradclip(int32_t tensors, const int64_t *counts,
             std::vector<int> first;
             long long bytes = 0;
             for (int i = 0; i < tensors; ++i) bytes += counts[i] * g.es[i];
-            g.small = bytes <= kSmall && tensors <= kMostTensors;
+            g.small = bytes <= kSmall && tensors <= kMostTensors && conv_cluster_fits(small_kernel(tensors), kCluster, kThreads, 0);
             g.past = bytes < kPast;
             int t = 0;
             do {

@@ -265,7 +265,8 @@ def test_without_parameters(cl, post, pre):
 
 def test_in_place(cl):
     """y over x, z over f; dx over dy, df over dz: the bits of separate buffers."""
-    for shape, dtype in (((2, 9, 9, 256), "bf16"), ((2, 5, 5, 8192), "bf16"), ((3, 7, 7, 33), "f32")):
+    for shape, dtype in (((2, 9, 9, 256), "bf16"), ((2, 5, 5, 8192), "bf16"), ((3, 7, 7, 33), "f32"), ((2, 21, 20, 255), "bf16"),
+                         ((2, 30, 30, 66), "bf16")):
         n, h, w, c = shape
         x, f, dy, dz = (draw(shape, DT[dtype], 30 + i) for i in range(4))
         p = parameters(n, c, "layer", "rms", True)
