@@ -167,7 +167,6 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
 // ------------------------------------------------------------------ host side
 template <typename T, int VEC>
 const void *pick_fwd(int k, int rb, int tpr, bool all) {
-    if (k == 2 && tpr <= 32) return all && tpr == 32 ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARP, true> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_ANY, false>;
     if (k == 2) return all ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, true> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, false>;
     if (rb == 1) return (const void *)&bn_fwd_kernel<T, VEC, 1, 1, ROW_ANY, false>;
     if (!all) return (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_ANY, false>;
