@@ -333,11 +333,15 @@ void plan_geometry(conv_plan *p) {
     // the gradient in large CTAs: a part of the sums from each
     part(g.bwd, 0, bk, bk > 1 ? 1 : kMostThreads);
     g.bwd_gated = g.bwd;
-    const long long w = wave(g.bwd);
-    divide_rows(g.bwd, rows, g.bwd.slots, w);
-    divide_images(g.bwd_gated, N, HW, g.bwd.slots, w);
+    // (images of fewer rows than lie side by side: smaller CTAs, more of them.
+    // 2048 images of one pixel of 1024 channels, bf16: 90 us in CTAs of 512, 50 so)
+    if (bk == 1 && HW < g.bwd.slots) part(g.bwd_gated, 0, 1, (int)up(g.bwd.tpr * HW, 32) * 32);
+    const long long w = wave(g.bwd_gated);
+    divide_rows(g.bwd, rows, g.bwd.slots, wave(g.bwd));
+    divide_images(g.bwd_gated, N, HW, g.bwd_gated.slots, w);
     // few rows: the CTAs of one cluster, a unit each, which join their sums
-    // themselves, where none takes more than four sets of rows
+    // themselves, where none takes more than two sets of rows (2x7x7x512: the call
+    // 14 us on the host and 8.5 on the device; in two launches 19 and 7.1)
     auto cluster = [&](BnGeom::Part &d, long long images, long long each) {
         const long long most = images <= kCluster ? kCluster / images : 0, sets = most ? up(each, most * d.slots) : 0;
         if (bk > 1 || !most || sets > kClusterSets) return;
