@@ -10,6 +10,14 @@
 // thousand elements, one of its warps to an item.  The plan holds that table on
 // the device; addresses come with each call as kernel parameters.
 //
+// Measured on a GB300 by graph replay: 1.0 billion bf16 elements 925 us, 6.2 GB in
+// its three passes (two readings, one writing) at 6.7 TB/s, of which the norm
+// cannot spare one: the 602 us of two would need it before the first reading;
+// 0.37 GB that need no clipping 59 us, one pass at 6.2 TB/s; 66 MB 31 us (the
+// second reading from L2).  Sets up to 1.5 MB take one launch of one cluster of
+// sixteen CTAs, 5.2 us for 0.55 MB where two launches took 5.9: the call then
+// costs 11 us on the host instead of 21.
+//
 // A lane sums the squares of an item in fp32 (up to about 130 terms), and items
 // in fp64.  Where a lane's sum would overflow (above 2^100, or not finite) or
 // its squares vanish (below 2^-100, but not all zero), the item is read again
