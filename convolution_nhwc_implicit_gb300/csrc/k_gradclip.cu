@@ -217,15 +217,18 @@ __device__ __forceinline__ void scale_item(const T *p, T *q, int n, float k, boo
     }
 }
 
-// The root of a sum in fp32, off by a rounding and a half: s = m 4^e with m in
-// [1, 4).  (fp64 has a root of its own, some forty instructions on a unit that
-// takes sixteen clocks for each: with it and a division in every warp the second
-// launch took 12 us where nothing was to be clipped.)
+// The root of a sum in fp32: s = m 4^e with m in [1, 4), and the fp32 root r of m
+// with a step of Newton's, r + (m - r^2) / 2r, whose difference is taken in fp64:
+// off by half a rounding and little more.  (fp64 has a root of its own, some
+// forty instructions on a unit that takes sixteen clocks for each: with it and a
+// division in every warp the second launch took 12 us where nothing was to be
+// clipped.)
 __device__ __forceinline__ float root32(double s) {
     const int high = __double2hiint(s), e = (high >> 20) - 1023;
     if (s == 0.0 || e >= 1024) return (float)s;  // (infinite or NaN)
     const double m = __hiloint2double((high & 0xfffff) | (1023 + (e & 1)) << 20, __double2loint(s));
-    return scalbnf(sqrtf((float)m), (e - (e & 1)) / 2);
+    const float r = sqrtf((float)m), rest = (float)fma(-(double)r, (double)r, m);
+    return scalbnf(r + 0.5f * rest / r, (e - (e & 1)) / 2);
 }
 
 // k for a norm.

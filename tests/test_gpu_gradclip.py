@@ -3,7 +3,7 @@
 The norm: a lane sums up to 160 squares of an item in four chains of fp32
 multiply-adds, at most 40 roundings one after another and two to join them, then
 fp64: the sum is off by at most 43 u of itself, u = 2^-24, its root by half of
-that and two roundings, 24 u; allowed are 82 u.  The factor adds two roundings,
+that and a rounding, 23 u; allowed are 82 u.  The factor adds two roundings,
 a product one, 27 u (allowed 83 u), and a bf16 result 2^-8 of an element."""
 import math
 
