@@ -429,7 +429,8 @@ CONV_API int conv_run_w4(const conv_plan_t *plan, const void *x, const void *pac
  * trained, df over dz); otherwise nothing that a run writes shares an element
  * with another map or a byte with anything else (CONV_ERR_ALIASING).  n = 0
  * does nothing (the gradient writes zeros to the sums over pixels).  The
- * gradient takes conv_plan_workspace_bwd bytes of scratch. */
+ * gradient takes conv_plan_workspace_bwd bytes of scratch (0 where all rows fit a
+ * cluster). */
 typedef enum { CONV_NORM_NONE = 0, CONV_NORM_LAYER = 1, CONV_NORM_RMS = 2 } conv_norm_t;
 
 typedef struct {
@@ -470,7 +471,7 @@ CONV_API int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, int6
  * Squares are summed in fp32 over a few thousand elements, scaled by a power of
  * two where they would overflow or vanish, and those sums in fp64, in a fixed
  * order; k is rounded once to fp32, each product once to the tensor's type.
- * Takes conv_plan_workspace bytes of scratch. */
+ * Takes conv_plan_workspace bytes of scratch (0 for a small set). */
 CONV_API int conv_plan_create_gradclip(int32_t tensors, const int64_t *counts, const conv_dtype_t *dtypes,
                                        conv_plan_t **out_plan);
 CONV_API int conv_run_gradclip(const conv_plan_t *plan, void *const *grads, void *const *outs, float max_norm,
