@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
         Slot *to = ring;
         const float4 *sd = seen;
         float4 *sto = seen;
+        __syncwarp();  // (every lane has read the last unit's statistics)
         // A row beyond the run counts as zeros.
         auto ask = [&] {
             if (asked < r1) {
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             if (a.slots == 1) __syncthreads();
             combine<SUM_A, 2, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) {
                 add_image(a, n, first, s, c, v);
-                both_sums[s * a.C + c] = v;
+                if (a.dgate) both_sums[s * a.C + c] = v;
             });
             if (a.dgate) {
                 __syncthreads();

@@ -476,6 +476,30 @@ def test_refusals(cl):
     plan.check_device_status()
 
 
+@pytest.mark.parametrize("shape", [(200, 1, 2, 2056), (400, 1, 1, 1024), (170, 2, 2, 40), (160, 1, 3, 4200)])
+def test_gradients_not_asked_for_change_nothing(cl, shape):
+    """Images that a CTA takes one after the other: the bits of every gradient do
+    not depend on which others are asked for."""
+    n, h, w, c = shape
+    x, f, dy, dz = (draw(shape, torch.bfloat16, 120 + i) for i in range(4))
+    p = parameters(n, c, "layer", "layer", True)
+    back = {k: v for k, v in p.items() if k != "pre_beta"}
+    plan = cl.BlockNormPlan(*shape, "layer", "layer")
+    _, _, dx, df = buffers(shape, torch.bfloat16, 0, 0)
+    stats = torch.empty(n, h, w, 4, device="cuda")
+    plan.run(x, f, torch.empty_like(x), torch.empty_like(x), stats, **p)
+    every = grads_of(p)
+    plan.run_backward(x, f, stats, dy, dz, dx, df, **back, **every)
+    ref, tol = reference(x, f, p, "layer", "layer", 1e-5, dy, dz, True)
+    for k, v in every.items():
+        close(v, ref[k], tol[k], False, k)
+    for _ in range(3):
+        for k in every:
+            one, (dx2, df2) = torch.full_like(every[k], 9.0), (torch.empty_like(x), torch.empty_like(x))
+            plan.run_backward(x, f, stats, dy, dz, dx2, df2, **back, **{k: one})
+            assert torch.equal(one, every[k]) and torch.equal(dx, dx2) and torch.equal(df, df2), k
+
+
 def test_empty_batch(cl):
     plan = cl.BlockNormPlan(0, 4, 4, 16)
     x = torch.empty(0, 4, 4, 16, device="cuda", dtype=torch.bfloat16)
