@@ -724,14 +724,14 @@ class BlockNormPlan(_MapPlan):
         """Addresses of a call's tensors (None where there is none) and the pixel
         pitches of its maps (0: dense).  Maps come first in `names`."""
         none = tuple([t is None for t in tensors])
-        known = self._known.get((names, none))
+        known = self._known.get(none)  # (as long as the call's tensors: forward and gradient differ)
         if known is None:
             maps = [k for k in names if k in _BLOCKNORM_MAPS]
             shape = {"stats": self._sshape, "gate": self._gshape, "dgate": self._gshape, **{k: self.shape for k in maps}}
             given = [k for k, absent in zip(names, none) if not absent]
             known = (given, [shape.get(k, self._cshape) for k in given],
                      [self._dt if k in maps else self._f32 for k in given], [self._device] * len(given), len(maps))
-            self._known[names, none] = known
+            self._known[none] = known
         given, shapes, dtypes, devices, maps = known
         ts = tensors if len(given) == len(names) else [t for t in tensors if t is not None]
         pitches = [0] * maps
