@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
 // ------------------------------------------------------------------ host side
 template <typename T, int VEC>
 const void *pick_fwd(int k, int rb, int tpr, bool all) {
+    if (k == 2 && tpr == 32) return all ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARP, true> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARP, false>;
     if (k == 2) return all ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, true> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, false>;
     if (rb == 1) return (const void *)&bn_fwd_kernel<T, VEC, 1, 1, ROW_ANY, false>;
     if (!all) return (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_ANY, false>;
@@ -330,8 +331,13 @@ void plan_geometry(conv_plan *p) {
     // than a CTA has registers for, and forward beyond 2048, where eight leave one
     // CTA a SM (6144x2560 bf16 36 us, with sixteen 27; 8192x4096 55 and 51; below,
     // 4096x2048 16.5 and 15.7, 3200x1024 7.2 and 7.7; the gradient 58 and 84, 91
-    // and 133)
-    const int fk = C > 2048 ? 2 : 1, bk = C > 8 * kMostThreads ? 2 : 1;
+    // and 133).  Up to 512 sixteen make a row a warp's, whose sums need no barrier:
+    // many rows whose channels are no whole 16-byte vectors, or bf16 with a layer
+    // norm, are faster so (8x40x40x510 layer and rms 16.4 and 15.4, 512 two layer
+    // norms 14.6 and 14.0; but two rms norms 11.7 and 12.4, fp32 19.0 and 19.9)
+    const bool layers = g.post == CONV_NORM_LAYER || g.pre == CONV_NORM_LAYER;
+    const bool warp = C > 256 && C <= 512 && rows > 1024 && (C * es % 16 != 0 || (es == 2 && layers));
+    const int fk = C > 2048 || warp ? 2 : 1, bk = C > 8 * kMostThreads ? 2 : 1;
     // two rows at a time where one wave of CTAs takes more than one set of rows
     // (64x25x5x61 fp32, 0.8 of a set: one at a time 4.5 us, two 5.7)
     part(g.fwd, 1, fk, kThreads);

@@ -77,9 +77,10 @@ class Part:
         self.units = self.grid = n * self.S
 
 
-def plan(n, hw, c, es):
+def plan(n, hw, c, es, layers=True):
     rows = n * hw
-    k = 2 if c > 2048 else 1
+    warp = 256 < c <= 512 and rows > 1024 and (c * es % 16 != 0 or (es == 2 and layers))
+    k = 2 if c > 2048 or warp else 1
     fwd = Part(c, 1, k, THREADS)
     if k == 1 and rows > fwd.wave(es) * fwd.slots:
         fwd.rb = 2
@@ -136,7 +137,7 @@ def widths(c, es):
 def test_threads_and_shared_memory():
     for n, hw, c, es in shapes(4000, 1):
         cp = up(c, 4) * 4
-        for d in plan(n, hw, c, es):
+        for d in plan(n, hw, c, es) + plan(n, hw, c, es, False):
             assert d.threads % 32 == 0 and 32 <= d.threads <= MOST and (d.tpr < 32 or d.tpr % 32 == 0)
             assert d.tpr * 8 * d.k >= c and (d.slots <= 15 or d.tpr <= 32)     # (named barriers 1 .. slots)
             if d.tpr > 32:

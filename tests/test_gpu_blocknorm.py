@@ -172,6 +172,9 @@ CASES = [
     (1, 2, 5, 8191, "layer", "layer", "bf16", True, 0, 0),
     (1, 2, 5, 8192, "layer", "layer", "f32", True, 0, 0),
     (1, 2, 3, 6001, "rms", "rms", "f32", False, 0, 0),
+    (3, 20, 20, 510, "layer", "rms", "bf16", True, 0, 0),      # sixteen channels a thread, a warp a row
+    (1, 40, 30, 300, "rms", "rms", "f32", False, 1, 0),
+    (2, 25, 25, 512, "layer", "none", "bf16", False, 0, 0),
     (4, 20, 20, 64, "layer", "rms", "bf16", True, 64, 64),     # a slice of a concatenated buffer
     (2, 10, 10, 48, "layer", "layer", "bf16", False, 13, 5),   # a slice at odd addresses
     (2, 10, 10, 48, "rms", "rms", "f32", True, 3, 1),
