@@ -115,8 +115,26 @@ cudaError_t conv_launch(const void *kernel, dim3 grid, dim3 block, void **args, 
     return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
-bool conv_cluster_fits(const void *k, int ctas, int threads, size_t smem) {
-    if (ctas > 8 && cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
+int conv_allow_cluster_once(const void *k, int device, int ctas) {
+    // (like the grants below: permissions last as long as the process)
+    struct Leave { const void *k; int device; };
+    static std::mutex mu;
+    static std::vector<Leave> done;
+    if (ctas <= 8) return CONV_OK;
+    std::lock_guard<std::mutex> lock(mu);
+    for (const Leave &l : done)
+        if (l.k == k && l.device == device) return CONV_OK;
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return CONV_ERR_CUDA;
+    try {
+        done.push_back({k, device});
+    } catch (...) {
+        return CONV_ERR_OOM;
+    }
+    return CONV_OK;
+}
+
+bool conv_cluster_fits(const void *k, int device, int ctas, int threads, size_t smem) {
+    if (conv_allow_cluster_once(k, device, ctas) != CONV_OK) return false;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)ctas;

@@ -166,9 +166,12 @@ static inline int conv_esize(conv_dtype_t t) { return t == CONV_F32 ? 4 : (t == 
 cudaError_t conv_launch(const void *kernel, dim3 grid, dim3 block, void **args, size_t smem, cudaStream_t st,
                         int cluster_x = 1);
 
+// Clusters of nine to sixteen CTAs need a kernel's leave, given once a kernel and
+// device (a CONV_* status).
+int conv_allow_cluster_once(const void *k, int device, int ctas);
 // Whether the device can run a cluster of `ctas` CTAs (up to 16) of kernel k, whose
-// shared memory has been granted; from nine on it also gives the kernel leave.
-bool conv_cluster_fits(const void *k, int ctas, int threads, size_t smem);
+// shared memory has been granted (and whose leave this gives).
+bool conv_cluster_fits(const void *k, int device, int ctas, int threads, size_t smem);
 
 // Launchers (stream-ordered, no allocation, no synchronisation).
 cudaError_t launch_direct(const conv_plan *p, const void *x, const void *w, const void *bias,

@@ -233,6 +233,7 @@ cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a
         const int rc = conv_grant_smem_once(k, p->device, (int)smem);
         if (rc != CONV_OK) return cudaErrorInvalidValue;
     }
+    if (d.joined && conv_allow_cluster_once(k, p->device, d.grid) != CONV_OK) return cudaErrorInvalidValue;
     a.tpr = d.tpr; a.full = d.full; a.slots = d.slots; a.run = d.run; a.S = d.S; a.units = d.units; a.whole = d.whole; a.joined = d.joined;
     void *args[] = {&a};
     return conv_launch(k, dim3((unsigned)d.grid), dim3((unsigned)d.threads), args, smem, st, d.joined ? d.grid : 1);
@@ -365,14 +366,13 @@ void plan_geometry(conv_plan *p) {
         const long long most = images <= kCluster ? kCluster / images : 0, sets = most ? up(each, most * d.slots) : 0;
         if (bk > 1 || !most || sets > kClusterSets) return;
         const long long run = sets * d.slots, S = up(each, run);
-        for (const int vec : {16 / es, es == 2 ? 2 : 1, 1})
-            for (const bool all : {false, true}) {
-                const void *kernel = pick_kernel(p->dtype, vec, 0, 1, d.tpr, all);
-                const size_t smem = ring_bytes(d, ring_element(es, vec));
-                if (conv_grant_smem_once(kernel, p->device, (int)smem) != CONV_OK ||
-                    !conv_cluster_fits(kernel, (int)(images * S), d.threads, smem))
-                    return;
-            }
+        // (of the instances that a call may choose, the one of the widest vectors
+        // stands for all, with the shared memory of the one that takes the most)
+        const void *kernel = pick_kernel(p->dtype, 16 / es, 0, 1, d.tpr, true);
+        const size_t smem = ring_bytes(d, 4);
+        if (conv_grant_smem_once(kernel, p->device, (int)smem) != CONV_OK ||
+            !conv_cluster_fits(kernel, p->device, (int)(images * S), d.threads, smem))
+            return;
         d.run = (int)run;
         d.S = (int)S;
         d.units = d.grid = (int)(images * S);

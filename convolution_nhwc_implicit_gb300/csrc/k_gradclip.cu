@@ -26,6 +26,7 @@
 #include <math.h>
 #include <stdint.h>
 #include <stdio.h>
+#include <string.h>
 
 #include <algorithm>
 #include <new>
@@ -51,7 +52,7 @@ struct ClipGeom {
     bool small = false;  // one launch of one cluster
     int past = 0;        // the second reading and the results go past L2
     uint4 *items = nullptr;  // device: (tensor of the batch | fp32 << 31, elements, first element as two words)
-    int *first = nullptr;    // device: [grid + 1] of each batch
+    int *first = nullptr;    // after them: [grid + 1] of each batch
 };
 
 namespace {
@@ -424,7 +425,6 @@ bool overlap(std::vector<Range> &in, std::vector<Range> &out) {
 void clip_destroy(ClipGeom *g) {
     if (!g) return;
     if (g->items) cudaFree(g->items);
-    if (g->first) cudaFree(g->first);
     delete g;
 }
 int clip_launches(const ClipGeom *g) { return g->small ? 1 : 2 * (int)g->batches.size(); }
@@ -458,7 +458,7 @@ extern "C" int conv_plan_create_gradclip(int32_t tensors, const int64_t *counts,
             std::vector<int> first;
             long long bytes = 0;
             for (int i = 0; i < tensors; ++i) bytes += counts[i] * g.es[i];
-            g.small = bytes <= kSmall && tensors <= kMostTensors && conv_cluster_fits(small_kernel(tensors), kCluster, kThreads, 0);
+            g.small = bytes <= kSmall && tensors <= kMostTensors && conv_cluster_fits(small_kernel(tensors), p->device, kCluster, kThreads, 0);
             g.past = bytes < kPast;
             int t = 0;
             do {
@@ -469,13 +469,16 @@ extern "C" int conv_plan_create_gradclip(int32_t tensors, const int64_t *counts,
                 t = b.t1;
             } while (t < tensors);
             p->ws_bytes = g.small ? 0 : (size_t)g.parts * sizeof(double);
-            const size_t ib = std::max<size_t>(1, items.size()) * sizeof(uint4), fb = first.size() * sizeof(int);
-            if (cudaMalloc(&g.items, ib) != cudaSuccess || cudaMalloc(&g.first, fb) != cudaSuccess) rc = CONV_ERR_OOM;
-            else if ((!items.empty() && cudaMemcpy(g.items, items.data(), items.size() * sizeof(uint4), cudaMemcpyHostToDevice) != cudaSuccess) ||
-                     cudaMemcpy(g.first, first.data(), fb, cudaMemcpyHostToDevice) != cudaSuccess)
-                rc = CONV_ERR_CUDA;
+            // one table: the items, then the CTAs' first ones
+            const size_t count = items.size();
+            items.resize(count + (first.size() + 3) / 4);
+            memcpy(items.data() + count, first.data(), first.size() * sizeof(int));
+            const size_t table = items.size() * sizeof(uint4);
+            if (cudaMalloc(&g.items, table) != cudaSuccess) rc = CONV_ERR_OOM;
+            else if (cudaMemcpy(g.items, items.data(), table, cudaMemcpyHostToDevice) != cudaSuccess) rc = CONV_ERR_CUDA;
+            g.first = reinterpret_cast<int *>(g.items + count);
             snprintf(p->desc, sizeof(p->desc), "gradclip %d tensors, %lld elements in %zu items, ctas=%d launches=%d", tensors, total,
-                     items.size(), g.parts, clip_launches(&g));
+                     count, g.parts, clip_launches(&g));
         }
     } catch (...) {
         rc = CONV_ERR_OOM;
