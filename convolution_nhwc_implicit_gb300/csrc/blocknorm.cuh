@@ -157,8 +157,9 @@ struct Row {
     }
 };
 
-// Rows of a part of a warp, of a warp, of several; or any of these.
-enum { ROW_PART, ROW_WARP, ROW_WARPS, ROW_ANY };
+// Rows of a part of a warp, of a warp, of several; any of these; of two CTAs
+// (the gradient's beyond 4096 channels).
+enum { ROW_PART, ROW_WARP, ROW_WARPS, ROW_ANY, ROW_PAIR };
 
 // Two sums over the threads of a row, to all of them.  The first exchange
 // leaves one sum to each half of the lanes, which halves the exchanges.  Rows of
@@ -282,15 +283,15 @@ __device__ __forceinline__ void factors(const Lane<VEC, K> &l, const BnArgs &a, 
     }
 }
 
-// Stages of the gradient's ring: what fits beside one another in shared memory.
-__host__ __device__ constexpr int bwd_stages(int es, int k) { return k == 1 ? 3 : (es == 2 ? 2 : 1); }
+// Stages of the gradient's ring: what fits beside one another in shared memory,
+__host__ __device__ constexpr int bwd_stages() { return 3; }
 
 // ... and of the forward kernel's.
 __host__ __device__ constexpr int fwd_stages(int es, int k) { return k == 2 && es == 4 ? 2 : 3; }
 
-// The gradient's kernel for a vector width, k times 8 channels a thread and tpr
-// threads a row, and the launch that joins its sums.
-const void *pick_bwd(conv_dtype_t dt, int vec, int k, int tpr, bool all);
+// The gradient's kernel for a vector width and tpr threads a row (or half a row,
+// of a pair of CTAs), and the launch that joins its sums.
+const void *pick_bwd(conv_dtype_t dt, int vec, bool pair, int tpr, bool all);
 cudaError_t launch_join(const BnArgs &a, int parts, cudaStream_t st);
 
 }  // namespace bn

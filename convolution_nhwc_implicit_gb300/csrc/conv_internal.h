@@ -107,7 +107,8 @@ struct XentGeom {
 struct BnGeom {
     int post, pre;
     float eps;
-    struct Part { int rb, k, tpr, full, slots, threads, run, S, units, grid, whole, joined; } fwd, fwd_gated, bwd, bwd_gated;
+    struct Part { int rb, k, pair, tpr, full, slots, threads, run, S, units, grid, whole, joined; }  // (a pair of CTAs counts once)
+         fwd, fwd_gated, bwd, bwd_gated;
 };
 
 struct ClipGeom;  // gradient norm and clipping (k_gradclip.cu)

@@ -187,9 +187,10 @@ const void *pick_fwd(int k, int rb, int tpr, bool all) {
                     : (tpr == 32 ? (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_WARP, true> : (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_WARPS, true>);
 }
 // (rb: rows at a time of the forward kernel, 0: the gradient)
-const void *pick_kernel(conv_dtype_t dt, int vec, int rb, int k, int tpr, bool all) {
+const void *pick_kernel(conv_dtype_t dt, int vec, const BnGeom::Part &d, bool all) {
     using B = __nv_bfloat16;
-    if (!rb) return bn::pick_bwd(dt, vec, k, tpr, all);
+    const int rb = d.rb, k = d.k, tpr = d.tpr;
+    if (!rb) return bn::pick_bwd(dt, vec, d.pair, tpr, all);
     if (dt == CONV_F32) return vec == 4 ? pick_fwd<float, 4>(k, rb, tpr, all) : pick_fwd<float, 1>(k, rb, tpr, all);
     return vec == 8 ? pick_fwd<B, 8>(k, rb, tpr, all) : (vec == 2 ? pick_fwd<B, 2>(k, rb, tpr, all) : pick_fwd<B, 1>(k, rb, tpr, all));
 }
@@ -212,9 +213,8 @@ int vec_for(const conv_plan *p, const Map (&maps)[N]) {
 long long up(long long a, long long b) { return (a + b - 1) / b; }
 
 // Bytes of the ring of a CTA: a thread's 8 k channels of each map and stage.
-// (The gradient's holds the sums of rows side by side after its last row:
-// rows side by side have k = 1, so that it has 96 elements a thread where the
-// sums are SUMS * 8 in fp32.
+// (The gradient's holds the sums of rows side by side after its last row: it has
+// 96 elements a thread where the sums are SUMS * 8 in fp32.
 // A cluster's also holds the CTA's sums of its channels, at most 8 a thread of a
 // row, and there are rows side by side where that is at most half of them: 64.)
 static_assert(3 * 4 * 8 * 2 >= SUMS * 8 * 4 + SUMS * 8 * 4 / 2, "");
@@ -222,13 +222,12 @@ static_assert(3 * 4 * 8 * 2 >= SUMS * 8 * 4 + SUMS * 8 * 4 / 2, "");
 size_t ring_bytes(const BnGeom::Part &d, int es) {
     const size_t maps = (size_t)d.threads * 8 * d.k * es;
     if (d.rb) return 2 * fwd_stages(es, d.k) * d.rb * maps + (d.k > 1 ? (size_t)d.threads * 2 * 8 * d.k * 4 : 0);
-    const int stages = bwd_stages(es, d.k);  // (and a row's statistics, and the parameters of long rows)
-    return stages * (4 * maps + (size_t)d.threads / (d.tpr < 32 ? d.tpr : 32) * 16) + (d.k > 1 ? (size_t)d.threads * 3 * 8 * d.k * 4 : 0);
+    return bwd_stages() * (4 * maps + (size_t)d.threads / (d.tpr < 32 ? d.tpr : 32) * 16);  // (and a row's statistics)
 }
 
 cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a, cudaStream_t st) {
     const size_t smem = ring_bytes(d, ring_element(conv_esize(p->dtype), vec));
-    const void *k = pick_kernel(p->dtype, vec, d.rb, d.k, d.tpr, d.rb ? a.f && a.o0 && a.o1 : a.f && a.dy && a.dz);
+    const void *k = pick_kernel(p->dtype, vec, d, d.rb ? a.f && a.o0 && a.o1 : a.f && a.dy && a.dz);
     if (smem > 40 * 1024) {  // (with the kernel's static shared memory: 48 KB are free)
         const int rc = conv_grant_smem_once(k, p->device, (int)smem);
         if (rc != CONV_OK) return cudaErrorInvalidValue;
@@ -236,7 +235,7 @@ cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a
     if (d.joined && conv_allow_cluster_once(k, p->device, d.grid) != CONV_OK) return cudaErrorInvalidValue;
     a.tpr = d.tpr; a.full = d.full; a.slots = d.slots; a.run = d.run; a.S = d.S; a.units = d.units; a.whole = d.whole; a.joined = d.joined;
     void *args[] = {&a};
-    return conv_launch(k, dim3((unsigned)d.grid), dim3((unsigned)d.threads), args, smem, st, d.joined ? d.grid : 1);
+    return conv_launch(k, dim3((unsigned)d.grid << d.pair), dim3((unsigned)d.threads), args, smem, st, d.joined ? d.grid : 1 << d.pair);
 }
 
 int check_map(const conv_plan *p, const void *t, int64_t *pitch) {
@@ -311,14 +310,15 @@ void plan_geometry(conv_plan *p) {
     const long long N = p->s.n, HW = (long long)p->s.h * p->s.w, rows = N * HW;
     p->ws_bytes = p->ws_bwd_bytes = 0;
     if (rows == 0) return;
-    auto part = [&](BnGeom::Part &d, int rb, int k, int threads) {
+    auto part = [&](BnGeom::Part &d, int rb, int k, int threads, int pair = 0) {
         d.rb = rb;
         d.k = k;
-        const int want = (C + 8 * k - 1) / (8 * k);
+        d.pair = pair;
+        const int one = 8 * k << pair, want = (C + one - 1) / one;
         d.tpr = 1;
         if (want > 32) d.tpr = (want + 31) / 32 * 32;
         else while (d.tpr < want) d.tpr *= 2;
-        d.full = C == d.tpr * 8 * k;
+        d.full = C == d.tpr * one;
         d.slots = d.tpr <= threads ? threads / d.tpr : 1;
         d.threads = d.tpr * d.slots;
     };
@@ -326,19 +326,22 @@ void plan_geometry(conv_plan *p) {
     auto wave = [&](const BnGeom::Part &d) {
         const long long smem = (228 * 1024) / (long long)(ring_bytes(d, es) + 1024 + 256), regs = kMostThreads / d.threads;
         const long long n = smem < regs ? smem : regs;
-        return (long long)p->num_sms * (n < 1 ? 1 : n);
+        return ((long long)p->num_sms * (n < 1 ? 1 : n)) >> d.pair;
     };
-    // sixteen channels a thread: beyond 4096, where eight would take more threads
-    // than a CTA has registers for, and forward beyond 2048, where eight leave one
-    // CTA a SM (6144x2560 bf16 36 us, with sixteen 27; 8192x4096 55 and 51; below,
-    // 4096x2048 16.5 and 15.7, 3200x1024 7.2 and 7.7; the gradient 58 and 84, 91
-    // and 133).  Up to 512 sixteen make a row a warp's, whose sums need no barrier:
-    // many rows whose channels are no whole 16-byte vectors, or bf16 with a layer
-    // norm, are faster so (8x40x40x510 layer and rms 16.4 and 15.4, 512 two layer
+    // sixteen channels a thread, forward: beyond 2048, where eight leave one CTA a
+    // SM, and beyond 4096 would take more threads than a CTA has registers for
+    // (6144x2560 bf16 36 us, with sixteen 27; 8192x4096 55 and 51; below, 4096x2048
+    // 16.5 and 15.7, 3200x1024 7.2 and 7.7).  The gradient keeps to eight (58 and 84,
+    // 91 and 133) and gives a row beyond 4096 to two CTAs of a cluster (4096x8192 bf16
+    // 147 and 106, 2048x8192 fp32 117 and 76; up to 4096 a CTA holds it: 8192x4096
+    // bf16 91, a pair 104, 4096x4096 fp32 77 and 74, 8192x2560 bf16 73 and 74).
+    // Up to 512 sixteen make a row a warp's, whose sums need no barrier: many rows
+    // whose channels are no whole 16-byte vectors, or bf16 with a layer norm, are
+    // faster so (8x40x40x510 layer and rms 16.4 and 15.4, 512 two layer
     // norms 14.6 and 14.0; but two rms norms 11.7 and 12.4, fp32 19.0 and 19.9)
     const bool layers = g.post == CONV_NORM_LAYER || g.pre == CONV_NORM_LAYER;
     const bool warp = C > 256 && C <= 512 && rows > 1024 && (C * es % 16 != 0 || (es == 2 && layers));
-    const int fk = C > 2048 || warp ? 2 : 1, bk = C > 8 * kMostThreads ? 2 : 1;
+    const int fk = C > 2048 || warp ? 2 : 1, pair = C > 8 * kMostThreads;
     // two rows at a time where one wave of CTAs takes more than one set of rows
     // (64x25x5x61 fp32, 0.8 of a set: one at a time 4.5 us, two 5.7)
     part(g.fwd, 1, fk, kThreads);
@@ -351,11 +354,11 @@ void plan_geometry(conv_plan *p) {
         divide_rows(g.fwd_gated, rows, g.fwd.slots, wave(g.fwd_gated));
     }
     // the gradient in large CTAs: a part of the sums from each
-    part(g.bwd, 0, bk, bk > 1 ? 1 : kMostThreads);
+    part(g.bwd, 0, 1, pair ? 1 : kMostThreads, pair);
     g.bwd_gated = g.bwd;
     // (images of fewer rows than lie side by side: smaller CTAs, more of them.
     // 2048 images of one pixel of 1024 channels, bf16: 90 us in CTAs of 512, 50 so)
-    if (bk == 1 && HW < g.bwd.slots) part(g.bwd_gated, 0, 1, (int)up(g.bwd.tpr * HW, 32) * 32);
+    if (HW < g.bwd.slots) part(g.bwd_gated, 0, 1, (int)up(g.bwd.tpr * HW, 32) * 32);
     const long long w = wave(g.bwd_gated);
     divide_rows(g.bwd, rows, g.bwd.slots, wave(g.bwd));
     divide_images(g.bwd_gated, N, HW, g.bwd_gated.slots, w);
@@ -364,11 +367,11 @@ void plan_geometry(conv_plan *p) {
     // 14 us on the host and 8.5 on the device; in two launches 19 and 7.1)
     auto cluster = [&](BnGeom::Part &d, long long images, long long each) {
         const long long most = images <= kCluster ? kCluster / images : 0, sets = most ? up(each, most * d.slots) : 0;
-        if (bk > 1 || !most || sets > kClusterSets) return;
+        if (pair || !most || sets > kClusterSets) return;
         const long long run = sets * d.slots, S = up(each, run);
         // (of the instances that a call may choose, the one of the widest vectors
         // stands for all, with the shared memory of the one that takes the most)
-        const void *kernel = pick_kernel(p->dtype, 16 / es, 0, 1, d.tpr, true);
+        const void *kernel = pick_kernel(p->dtype, 16 / es, d, true);
         const size_t smem = ring_bytes(d, 4);
         if (conv_grant_smem_once(kernel, p->device, (int)smem) != CONV_OK ||
             !conv_cluster_fits(kernel, p->device, (int)(images * S), d.threads, smem))

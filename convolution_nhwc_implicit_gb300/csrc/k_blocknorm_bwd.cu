@@ -58,8 +58,8 @@ __device__ __forceinline__ void combine(const Lane<VEC, 1> &l, int slots, float2
 __device__ __forceinline__ float *place(const BnArgs &a, int at, int s, int c) { return a.part + ((long long)at * SUMS + s) * a.Cp + c; }
 // A unit that is a whole image gives its dgate at once and adds gate times its
 // sums to the CTA's.
-__device__ __forceinline__ void add_image(const BnArgs &a, int n, bool first, int s, int c, float v) {
-    float *p = place(a, blockIdx.x, s, c);
+__device__ __forceinline__ void add_image(const BnArgs &a, int n, int cta, bool first, int s, int c, float v) {
+    float *p = place(a, cta, s, c);
     const float gate = a.gate[(long long)n * a.C + c];
     *p = first ? gate * v : fmaf(gate, v, *p);
 }
@@ -129,22 +129,77 @@ __device__ __forceinline__ void join_cluster(const BnArgs &a, const float *mine)
     cluster_wait();
 }
 
+// Eight sums over a row that a cluster of two CTAs holds, half each.  A warp halves
+// them over its lanes three times (a lane then holds one of them) and leaves them
+// in both CTAs' shared memory, in one of two sets of entries in turn (as in
+// RowSum); a lane then reads four of a warp's of each CTA.
+struct PairSums {
+    static constexpr int kWarps = kMostThreads / 32, kSet = 2 * kWarps * 2;
+    float4 *buf;  // [2][CTA][warp][2]
+    uint32_t peer;
+    int rank, warps, flip;
+    __device__ __forceinline__ PairSums(float4 *b, int rank_, int tpr)
+        : buf(b), peer(tc::mapa_shared(tc::smem_u32(b), rank_ ^ 1)), rank(rank_), warps(tpr / 32), flip(0) {}
+    __device__ static __forceinline__ float across(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+    __device__ static __forceinline__ float halved(bool hi, float a, float b, int o) { return (hi ? b : a) + across(hi ? a : b, o); }
+    __device__ __forceinline__ void give(const float (&v)[8]) {
+        const int lane = threadIdx.x & 31;
+        const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
+        float a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = halved(h16, v[i], v[i + 4], 16);
+        float f = halved(h4, halved(h8, a[0], a[2], 8), halved(h8, a[1], a[3], 8), 4);
+        f += across(f, 2);
+        f += across(f, 1);
+        if ((lane & 3) == 0) {
+            const int at = (flip + (rank * kWarps + (threadIdx.x >> 5)) * 2) * 4 + lane / 4;
+            reinterpret_cast<float *>(buf)[at] = f;
+            asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(peer + at * 4), "f"(f) : "memory");
+        }
+        cluster_arrive();
+    }
+    // (what lies between give and take hides a part of the way)
+    __device__ __forceinline__ void take(float (&v)[8]) {
+        const int lane = threadIdx.x & 31;
+        const bool h16 = lane & 16, h8 = lane & 8;
+        const float4 *e = buf + flip + lane;
+        flip ^= kSet;
+        cluster_wait();
+        float4 w = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (lane < 2 * warps) {
+            const float4 x = e[0], y = e[2 * kWarps];
+            w = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+        }
+        float f = halved(h8, halved(h16, w.x, w.z, 16), halved(h16, w.y, w.w, 16), 8);
+        f += across(f, 4);
+        f += across(f, 2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, f, (i & 4 ? 1 : 0) | (i & 2 ? 16 : 0) | (i & 1 ? 8 : 0));
+    }
+};
+
 // dx and df of the rows of a CTA's units, and the units' channel sums.  ALL: the
 // block, dy and dz are given; what is then not asked for is formed all the same,
 // which is fewer instructions than asking (8x80x80x256 bf16: 18.5 M warp
 // instructions with the branches, 13.7 M without).  The statistics come through
 // the ring too: read a row ahead they were what the warps waited for (37 us, 31.5
-// so).
+// so).  A pair of CTAs (ROW_PAIR) meets once a row, for the sums of both norms: a
+// meeting of the cluster takes about half a microsecond (4096x8192 bf16 143 us with
+// two, 106 with one; floor 60).  Within a CTA one meeting for both gains less than
+// its instructions cost up to 1024 channels and 4 % at 4096, and was not taken.
 template <typename T, int VEC, int ROW, bool ALL>
 __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_constant__ BnArgs a) {
     using R = Row<T, VEC, 1>;
     using Slot = typename R::Slot;
-    constexpr int P = R::P, D = bwd_stages(R::kElement, 1), LINE = R::NV * R::step, STAGE = 4 * LINE;
+    constexpr int P = R::P, D = bwd_stages(), LINE = R::NV * R::step, STAGE = 4 * LINE;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float4 meet[2 * kMeet];
+    constexpr bool PAIR = ROW == ROW_PAIR;
+    __shared__ float4 meet[PAIR ? 2 * PairSums::kSet : 2 * kMeet];
     const int nt = blockDim.x;
     Slot *ring = R::ring(smem, D * 4);  // [D][x, f, dy, dz]
-    const Lane<VEC, 1> l(a);
+    const int rank = PAIR ? blockIdx.x & 1 : 0, cta = PAIR ? blockIdx.x >> 1 : blockIdx.x, ctas = PAIR ? gridDim.x >> 1 : gridDim.x;
+    Lane<VEC, 1> l(a);
+    if (PAIR) l.t += rank * R::NV * a.tpr;
     // statistics [warp][D][rows of a warp], copied by a lane of each row
     const int line = l.tpr < 32 ? l.tpr : 32, lane = threadIdx.x & 31;
     float4 *const seen = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * R::NV * nt * sizeof(Slot)) +
@@ -153,13 +208,15 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
     float2 *const ent = reinterpret_cast<float2 *>(smem);  // after a unit's rows: the threads' sums
     // (fp32: with both ways of meeting, 36 bytes of a thread's registers are spilled,
     // and 8192x4096 takes 171 us for 135)
-    RowSum<ROW, sizeof(T) == 2> sum(a.tpr, l.slot, meet);
+    RowSum<PAIR ? ROW_WARP : ROW, sizeof(T) == 2> sum(a.tpr, l.slot, meet);
+    PairSums pair(meet, rank, a.tpr);
     const bool block = ALL || a.f, stream = ALL || a.dy, norm = ALL || a.dz;
     const float mean_post = a.post == CONV_NORM_LAYER ? -a.inv_c : 0.0f, mean_pre = a.pre == CONV_NORM_LAYER ? -a.inv_c : 0.0f;
     const long long sx = a.slots * a.px, sf = a.slots * a.pf, sdy = a.slots * a.pdy, sdz = a.slots * a.pdz;
     const long long s0 = a.slots * a.p0, s1 = a.slots * a.p1;
     pdl_trigger();
     pdl_wait();
+    if (PAIR) cluster_arrive();
     float2 q[P], p[P], g2[P], acc[SUMS][P];
 #pragma unroll
     for (int s = 0; s < SUMS; ++s)
@@ -167,7 +224,8 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
         for (int i = 0; i < P; ++i) acc[s][i] = make_float2(0.0f, 0.0f);
     l.params(g2, a.g2, 1.0f);
     if (block && !a.gate) factors(l, a, 0, q, p);
-    for (int unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
+    if (PAIR) cluster_wait();  // (the other CTA's shared memory is there)
+    for (int unit = cta; unit < a.units; unit += ctas) {
         const int n = unit / a.S, k0 = unit - n * a.S;
         const int span = a.gate ? a.HW : a.rows;
         const int r0 = n * span + min(span, k0 * a.run), r1 = n * span + min(span, (k0 + 1) * a.run);
@@ -231,7 +289,54 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             else
 #pragma unroll
                 for (int k = 0; k < P; ++k) t[k] = make_float2(0.0f, 0.0f);
-            if (norm) {
+            float2 both_norms = make_float2(0.0f, 0.0f);  // PAIR: the sums of dY q and of dY q u^
+            if constexpr (PAIR) {
+                // One exchange: dY = T + m + my y^ of T = dy + r2 g2 dz, so that the sums of
+                // dY q and of dY q u^ are made of T's, q's and y^ q's.  (They lose what T, m and
+                // my y^ cancel, as the roundings of each dY do.)
+                float2 w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = make_float2(0.0f, 0.0f);
+                if (norm) {
+                    float2 e[P];
+                    R::get(l, d + 3 * LINE, odz, e);
+                    const float2 r = both(st.w), c = both(-st.z * st.w);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        acc[SUM_B2][k] = add2(acc[SUM_B2][k], e[k]);
+                        y[k] = fma2(y[k], r, c);
+                        acc[SUM_G2][k] = fma2(e[k], y[k], acc[SUM_G2][k]);
+                        e[k] = mul2(e[k], g2[k]);
+                        t[k] = fma2(e[k], r, t[k]);
+                        w[0] = add2(w[0], e[k]);
+                        w[1] = fma2(e[k], y[k], w[1]);
+                    }
+                } else
+#pragma unroll
+                    for (int k = 0; k < P; ++k) y[k] = make_float2(0.0f, 0.0f);
+                if (block && a.post != CONV_NORM_NONE)
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        const float2 tq = mul2(t[k], q[k]), yq = mul2(y[k], q[k]);
+                        w[2] = add2(w[2], tq);
+                        w[3] = fma2(tq, u[k], w[3]);
+                        w[4] = add2(w[4], q[k]);
+                        w[5] = add2(w[5], yq);
+                        w[6] = fma2(q[k], u[k], w[6]);
+                        w[7] = fma2(yq, u[k], w[7]);
+                    }
+                float v[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = w[i].x + w[i].y;
+                pair.give(v);
+                ask();
+                pair.take(v);
+                // (without the second norm its statistics may be anything)
+                const float my = norm ? -v[1] * a.inv_c * st.w : 0.0f, m = norm ? v[0] * mean_pre * st.w : 0.0f;
+                both_norms = make_float2(fmaf(my, v[5], fmaf(m, v[4], v[2])), fmaf(my, v[7], fmaf(m, v[6], v[3])));
+#pragma unroll
+                for (int k = 0; k < P; ++k) t[k] = fma2(y[k], both(my), add2(t[k], both(m)));
+            } else if (norm) {
                 float2 e[P], w = make_float2(0.0f, 0.0f), v = w;
                 R::get(l, d + 3 * LINE, odz, e);
                 const float2 r = both(st.w), c = both(-st.z * st.w);
@@ -254,7 +359,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             const bool last = d == ring + (D - 1) * STAGE;
             d = last ? ring : d + STAGE;
             sd = last ? seen : sd + 32 / line;
-            ask();
+            if (!PAIR) ask();
             if (on) R::put(l, dx, t);
             if (block) {
                 // (what the mean's terms leave in a row beyond the run is 0: its sums are)
@@ -267,13 +372,16 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
                     t[k] = mul2(t[k], q[k]);
                 }
                 if (a.post != CONV_NORM_NONE) {
-                    float2 w = make_float2(0.0f, 0.0f), v = w;
+                    float2 s = both_norms;
+                    if (!PAIR) {
+                        float2 w = make_float2(0.0f, 0.0f), v = w;
 #pragma unroll
-                    for (int k = 0; k < P; ++k) {
-                        w = add2(w, t[k]);
-                        v = fma2(t[k], u[k], v);
+                        for (int k = 0; k < P; ++k) {
+                            w = add2(w, t[k]);
+                            v = fma2(t[k], u[k], v);
+                        }
+                        s = sum(w.x + w.y, v.x + v.y);
                     }
-                    const float2 s = sum(w.x + w.y, v.x + v.y);
                     const float2 r = both(st.y), mu = both(-s.y * a.inv_c * st.y);
                     const float2 m = both(s.x * mean_post * st.y);
 #pragma unroll
@@ -290,13 +398,37 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             odz += (unsigned)sdz;
         }
         copy_wait<0>();
+        if constexpr (PAIR) {
+            // (one row at a time: a thread holds its channels' sums)
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (!l.has(i, e)) continue;
+                    const int c = l.chan(i, e);
+                    auto one = [&](int s) { return e ? acc[s][i].y : acc[s][i].x; };
+                    if (!a.whole) {
+#pragma unroll
+                        for (int s = 0; s < SUMS; ++s) *place(a, unit, s, c) = one(s);
+                        continue;
+                    }
+                    for (int s = 0; s < SUM_G2; ++s) add_image(a, n, cta, unit == cta, s, c, one(s));
+                    if (a.dgate) a.dgate[(long long)n * a.C + c] = Others(a, c, true).gate(one(SUM_A), one(SUM_B));
+                    if (unit + ctas >= a.units)
+                        for (int s = SUM_G2; s < SUMS; ++s) *place(a, cta, s, c) = one(s);
+                }
+            if (a.whole)
+#pragma unroll
+                for (int i = 0; i < P; ++i) acc[SUM_A][i] = acc[SUM_B][i] = make_float2(0.0f, 0.0f);
+            continue;
+        }
         if (a.joined) break;  // (a CTA has one unit)
         if (a.whole) {
             const bool first = unit == (int)blockIdx.x;
             float *both_sums = reinterpret_cast<float *>(ent + 2 * P * nt);  // [A, B][C]: of a channel, two threads'
             if (a.slots == 1) __syncthreads();
             combine<SUM_A, 2, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) {
-                add_image(a, n, first, s, c, v);
+                add_image(a, n, cta, first, s, c, v);
                 if (a.dgate) both_sums[s * a.C + c] = v;
             });
             if (a.dgate) {
@@ -308,6 +440,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             for (int i = 0; i < P; ++i) acc[SUM_A][i] = acc[SUM_B][i] = make_float2(0.0f, 0.0f);
         } else combine<0, SUMS, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { *place(a, unit, s, c) = v; });
     }
+    if constexpr (PAIR) return;
     if (a.joined) {
         // (the CTA's sums after the threads')
         float *mine = reinterpret_cast<float *>(ent + (a.slots > 1 ? SUMS * P * nt : 0));
@@ -316,239 +449,6 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
         join_cluster(a, mine);
     } else if (a.whole)
         combine<SUM_G2, 2, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { *place(a, blockIdx.x, s, c) = v; });
-}
-
-// The same for rows of more than 4096 channels: sixteen a thread, in two chunks
-// of eight.  Their sums take 64 registers, so that the parameters stay in shared
-// memory and a chunk's values are formed again of the ring where they are needed
-// again.  4096x8192 bf16 rms 147 us (184 with the values kept, 600 to 1000 bytes
-// of a thread's registers spilled; 140 to 220 are so); its bytes take 60: one row
-// at a time passes through two joins of sixteen warps and three readings.
-template <typename T, int VEC>
-__global__ void __launch_bounds__(kMostThreads) bn_bwd_long_kernel(const __grid_constant__ BnArgs a) {
-    using R = Row<T, VEC, 1>;
-    using Slot = typename R::Slot;
-    constexpr int H = 2, P = R::P, D = bwd_stages(R::kElement, H), LINE = R::NV * R::step, MAP = H * LINE, STAGE = 4 * MAP;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ float4 meet[2 * kMeet];
-    const int nt = blockDim.x;
-    Slot *ring = R::ring(smem, D * 4 * H);  // [D][x, f, dy, dz][H]
-    float4 *const par = reinterpret_cast<float4 *>(smem + (size_t)D * 4 * H * R::NV * nt * sizeof(Slot)) + threadIdx.x;  // [q, p, g2][H][2][threads]
-    float4 *const seen = par - threadIdx.x + 3 * H * 2 * nt + (threadIdx.x >> 5) * D;  // statistics [warp][D]
-    Lane<VEC, 1> l[H] = {Lane<VEC, 1>(a), Lane<VEC, 1>(a)};
-    l[1].t += R::NV * a.tpr;
-    RowSum<ROW_WARPS, false> sum(a.tpr, 0, meet);
-    const bool block = a.f, stream = a.dy, norm = a.dz, copies = (threadIdx.x & 31) == 0;
-    const float mean_post = a.post == CONV_NORM_LAYER ? -a.inv_c : 0.0f, mean_pre = a.pre == CONV_NORM_LAYER ? -a.inv_c : 0.0f;
-    enum { PAR_Q, PAR_P, PAR_G2 };
-    auto set = [&](int which, int h, const float2 (&v)[P]) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) par[((which * H + h) * 2 + j) * nt] = make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
-    };
-    auto param = [&](int which, int h, float2 (&v)[P]) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float4 f = par[((which * H + h) * 2 + j) * nt];
-            v[2 * j] = make_float2(f.x, f.y);
-            v[2 * j + 1] = make_float2(f.z, f.w);
-        }
-    };
-    pdl_trigger();
-    pdl_wait();
-    float2 acc[H][SUMS][P];
-#pragma unroll
-    for (int h = 0; h < H; ++h) {
-#pragma unroll
-        for (int s = 0; s < SUMS; ++s)
-#pragma unroll
-            for (int i = 0; i < P; ++i) acc[h][s][i] = make_float2(0.0f, 0.0f);
-        float2 g2[P];
-        l[h].params(g2, a.g2, 1.0f);
-        set(PAR_G2, h, g2);
-    }
-    auto set_factors = [&](int n) {
-#pragma unroll
-        for (int h = 0; h < H; ++h) {
-            float2 q[P], p[P];
-            factors(l[h], a, n, q, p);
-            set(PAR_Q, h, q);
-            set(PAR_P, h, p);
-        }
-    };
-    if (block && !a.gate) set_factors(0);
-    for (int unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
-        const int n = unit / a.S, k0 = unit - n * a.S;
-        const int span = a.gate ? a.HW : a.rows;
-        const int r0 = n * span + min(span, k0 * a.run), r1 = n * span + min(span, (k0 + 1) * a.run);
-        const int at = l[0].first(0), far = l[1].first(0) - at;
-        int asked = r0;
-        const T *x = static_cast<const T *>(a.x) + r0 * a.px + at, *f = static_cast<const T *>(a.f) + r0 * a.pf + at;
-        const T *dy = static_cast<const T *>(a.dy) + r0 * a.pdy + at, *dz = static_cast<const T *>(a.dz) + r0 * a.pdz + at;
-        T *dx = static_cast<T *>(a.o0) + r0 * a.p0 + at, *df = static_cast<T *>(a.o1) + r0 * a.p1 + at;
-        unsigned ox = R::odd(x), of = R::odd(f), ody = R::odd(dy), odz = R::odd(dz);  // (both chunks': they are an even number apart)
-        if (!a.full)
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-                for (int i = 0; i < D * 4; ++i) R::template blank<1>(l[h], ring + i * MAP + h * LINE);
-        const Slot *d = ring;
-        Slot *to = ring;
-        const float4 *sd = seen;
-        float4 *sto = seen;
-        auto ask = [&] {
-            if (asked < r1) {
-                if (copies) copy_async<16>(tc::smem_u32(sto), a.stats + asked);
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    const int o = h ? far : 0;
-                    R::ask(l[h], x + o, to + h * LINE);
-                    if (block) R::ask(l[h], f + o, to + MAP + h * LINE);
-                    if (stream) R::ask(l[h], dy + o, to + 2 * MAP + h * LINE);
-                    if (norm) R::ask(l[h], dz + o, to + 3 * MAP + h * LINE);
-                }
-            }
-            copy_commit();
-            ++asked;
-            x += a.px;
-            f += a.pf;
-            dy += a.pdy;
-            dz += a.pdz;
-            const bool last = to == ring + (D - 1) * STAGE;
-            to = last ? ring : to + STAGE;
-            sto = last ? seen : sto + 1;
-        };
-        if (block && a.gate) set_factors(n);
-#pragma unroll
-        for (int i = 0; i < D; ++i) ask();
-        for (int row = r0; row < r1; ++row) {
-            copy_wait<D - 1>();
-            __syncwarp();
-            const float4 st = *sd;
-            const float2 ur = both(st.y), uc = both(-st.x * st.y), yr = both(st.w), yc = both(-st.z * st.w);
-            auto block_out = [&](int h, float2 (&u)[P]) {  // u^
-                R::get(l[h], d + MAP + h * LINE, of, u);
-#pragma unroll
-                for (int k = 0; k < P; ++k) u[k] = fma2(u[k], ur, uc);
-            };
-            auto stream_in = [&](int h, const float2 (&u)[P], float2 (&y)[P]) {  // y^
-                R::get(l[h], d + h * LINE, ox, y);
-                if (block) {
-                    float2 q[P];
-                    param(PAR_P, h, q);
-#pragma unroll
-                    for (int k = 0; k < P; ++k) y[k] = add2(y[k], q[k]);
-                    param(PAR_Q, h, q);
-#pragma unroll
-                    for (int k = 0; k < P; ++k) y[k] = fma2(q[k], u[k], y[k]);
-                }
-#pragma unroll
-                for (int k = 0; k < P; ++k) y[k] = fma2(y[k], yr, yc);
-            };
-            float2 s = make_float2(0.0f, 0.0f);
-            if (norm) {
-                float2 w = s, v = s;
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    float2 u[P], y[P], e[P], g2[P];
-                    if (block) block_out(h, u);
-                    stream_in(h, u, y);
-                    R::get(l[h], d + 3 * MAP + h * LINE, odz, e);
-                    param(PAR_G2, h, g2);
-#pragma unroll
-                    for (int k = 0; k < P; ++k) {
-                        acc[h][SUM_G2][k] = fma2(e[k], y[k], acc[h][SUM_G2][k]);
-                        acc[h][SUM_B2][k] = add2(acc[h][SUM_B2][k], e[k]);
-                        e[k] = mul2(e[k], g2[k]);
-                        w = add2(w, e[k]);
-                        v = fma2(e[k], y[k], v);
-                    }
-                }
-                s = sum(w.x + w.y, v.x + v.y);
-            }
-            const float2 my = both(-s.y * a.inv_c * st.w), m = both(s.x * mean_pre * st.w);
-            float2 t[H][P], w = make_float2(0.0f, 0.0f), v = w;
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                float2 u[P];
-                if (block) block_out(h, u);
-                if (stream) R::get(l[h], d + 2 * MAP + h * LINE, ody, t[h]);
-                else
-#pragma unroll
-                    for (int k = 0; k < P; ++k) t[h][k] = make_float2(0.0f, 0.0f);
-                if (norm) {
-                    float2 y[P], e[P], g2[P];
-                    stream_in(h, u, y);
-                    R::get(l[h], d + 3 * MAP + h * LINE, odz, e);
-                    param(PAR_G2, h, g2);
-#pragma unroll
-                    for (int k = 0; k < P; ++k) t[h][k] = fma2(y[k], my, fma2(mul2(e[k], g2[k]), yr, add2(t[h][k], m)));
-                }
-                R::put(l[h], dx + (h ? far : 0), t[h]);
-                if (block) {
-                    float2 q[P];
-                    param(PAR_Q, h, q);
-#pragma unroll
-                    for (int k = 0; k < P; ++k) {
-                        acc[h][SUM_A][k] = fma2(t[h][k], u[k], acc[h][SUM_A][k]);
-                        acc[h][SUM_B][k] = add2(acc[h][SUM_B][k], t[h][k]);
-                        t[h][k] = mul2(t[h][k], q[k]);
-                        w = add2(w, t[h][k]);
-                        v = fma2(t[h][k], u[k], v);
-                    }
-                }
-            }
-            if (block) {
-                if (a.post != CONV_NORM_NONE) {
-                    const float2 z = sum(w.x + w.y, v.x + v.y);
-                    const float2 mu = both(-z.y * a.inv_c * st.y), mm = both(z.x * mean_post * st.y);
-#pragma unroll
-                    for (int h = 0; h < H; ++h) {
-                        float2 u[P];
-                        block_out(h, u);
-#pragma unroll
-                        for (int k = 0; k < P; ++k) t[h][k] = fma2(u[k], mu, fma2(t[h][k], ur, mm));
-                    }
-                }
-#pragma unroll
-                for (int h = 0; h < H; ++h) R::put(l[h], df + (h ? far : 0), t[h]);
-            }
-            const bool last = d == ring + (D - 1) * STAGE;
-            d = last ? ring : d + STAGE;
-            sd = last ? seen : sd + 1;
-            __syncwarp();  // (the statistics' place is written again)
-            ask();
-            dx += a.p0;
-            df += a.p1;
-            ox += (unsigned)a.px;
-            of += (unsigned)a.pf;
-            ody += (unsigned)a.pdy;
-            odz += (unsigned)a.pdz;
-        }
-        copy_wait<0>();
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int i = 0; i < P; ++i)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (!l[h].has(i, e)) continue;
-                    const int c = l[h].chan(i, e);
-                    auto one = [&](int s) { return e ? acc[h][s][i].y : acc[h][s][i].x; };
-                    if (!a.whole) {
-#pragma unroll
-                        for (int s = 0; s < SUMS; ++s) *place(a, unit, s, c) = one(s);
-                        continue;
-                    }
-                    for (int s = 0; s < SUM_G2; ++s) add_image(a, n, unit == (int)blockIdx.x, s, c, one(s));
-                    if (a.dgate) a.dgate[(long long)n * a.C + c] = Others(a, c, true).gate(one(SUM_A), one(SUM_B));
-                    if (unit + (int)gridDim.x >= a.units)
-                        for (int s = SUM_G2; s < SUMS; ++s) *place(a, blockIdx.x, s, c) = one(s);
-                }
-        if (a.whole)
-#pragma unroll
-            for (int h = 0; h < H; ++h)
-#pragma unroll
-                for (int i = 0; i < P; ++i) acc[h][SUM_A][i] = acc[h][SUM_B][i] = make_float2(0.0f, 0.0f);
-    }
 }
 
 // Joins the units' sums: a CTA takes sixteen channels, four a thread, and 128
@@ -637,16 +537,16 @@ __global__ void __launch_bounds__(kJoin) bn_join_kernel(const __grid_constant__ 
 }
 
 template <typename T, int VEC>
-const void *pick(int k, int tpr, bool all) {
-    if (k == 2) return (const void *)&bn_bwd_long_kernel<T, VEC>;
+const void *pick(bool pair, int tpr, bool all) {
+    if (pair) return all ? (const void *)&bn_bwd_kernel<T, VEC, ROW_PAIR, true> : (const void *)&bn_bwd_kernel<T, VEC, ROW_PAIR, false>;
     if (!all) return (const void *)&bn_bwd_kernel<T, VEC, ROW_ANY, false>;
     return tpr < 32 ? (const void *)&bn_bwd_kernel<T, VEC, ROW_PART, true>
                     : (tpr == 32 ? (const void *)&bn_bwd_kernel<T, VEC, ROW_WARP, true> : (const void *)&bn_bwd_kernel<T, VEC, ROW_WARPS, true>);
 }
-const void *pick_bwd(conv_dtype_t dt, int vec, int k, int tpr, bool all) {
+const void *pick_bwd(conv_dtype_t dt, int vec, bool pair, int tpr, bool all) {
     using B = __nv_bfloat16;
-    if (dt == CONV_F32) return vec == 4 ? pick<float, 4>(k, tpr, all) : pick<float, 1>(k, tpr, all);
-    return vec == 8 ? pick<B, 8>(k, tpr, all) : (vec == 2 ? pick<B, 2>(k, tpr, all) : pick<B, 1>(k, tpr, all));
+    if (dt == CONV_F32) return vec == 4 ? pick<float, 4>(pair, tpr, all) : pick<float, 1>(pair, tpr, all);
+    return vec == 8 ? pick<B, 8>(pair, tpr, all) : (vec == 2 ? pick<B, 2>(pair, tpr, all) : pick<B, 1>(pair, tpr, all));
 }
 
 cudaError_t launch_join(const BnArgs &a, int parts, cudaStream_t st) {

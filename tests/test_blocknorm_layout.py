@@ -9,7 +9,7 @@ import re
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "convolution_nhwc_implicit_gb300", "csrc")
 TEXT = open(os.path.join(CSRC, "blocknorm.cuh")).read()
-SMS, SMEM, STATIC = 152, 227 * 1024, 2 * 12 * 16
+SMS, SMEM, STATIC = 152, 227 * 1024, 2048
 
 
 def constant(name):
@@ -28,8 +28,7 @@ def element(es, vec):
     return 4 if es * vec < 4 else es
 
 
-def bwd_stages(es, k):
-    return 3 if k == 1 else (2 if es == 2 else 1)
+BWD_STAGES = 3
 
 
 def fwd_stages(es, k):
@@ -37,9 +36,9 @@ def fwd_stages(es, k):
 
 
 class Part:
-    def __init__(self, c, rb, k, threads):
-        self.rb, self.k = rb, k
-        want = up(c, 8 * k)
+    def __init__(self, c, rb, k, threads, pair=False):
+        self.rb, self.k, self.ctas = rb, k, 2 if pair else 1                    # (CTAs of a row)
+        want = up(c, 8 * k * self.ctas)
         if want > 32:
             self.tpr = up(want, 32) * 32
         else:
@@ -54,12 +53,11 @@ class Part:
         maps = self.threads * 8 * self.k * es
         if self.rb:
             return 2 * fwd_stages(es, self.k) * self.rb * maps + (self.threads * 2 * 8 * self.k * 4 if self.k > 1 else 0)
-        return (bwd_stages(es, self.k) * (4 * maps + self.threads // min(self.tpr, 32) * 16) +
-                (self.threads * 3 * 8 * self.k * 4 if self.k > 1 else 0))
+        return BWD_STAGES * (4 * maps + self.threads // min(self.tpr, 32) * 16)
 
     def wave(self, es):
         n = min(228 * 1024 // (self.smem(es) + 1024 + 256), MOST // self.threads)
-        return SMS * max(n, 1)
+        return SMS * max(n, 1) // self.ctas
 
     def divide_rows(self, rows, sets, wave):
         self.run = max(up(up(rows, wave), sets) * sets, sets)
@@ -91,10 +89,10 @@ def plan(n, hw, c, es, layers=True):
     else:
         gated.rb = 1
         gated.divide_rows(rows, gated.slots, gated.wave(es))
-    kb = 2 if c > 8 * MOST else 1
-    bwd = Part(c, 0, kb, 1 if kb > 1 else MOST)
-    bgate = Part(c, 0, kb, 1 if kb > 1 else MOST)
-    if kb == 1 and hw < bwd.slots:
+    pair = c > 8 * MOST
+    bwd = Part(c, 0, 1, 1 if pair else MOST, pair)
+    bgate = Part(c, 0, 1, 1 if pair else MOST, pair)
+    if hw < bwd.slots:
         bgate = Part(c, 0, 1, up(bwd.tpr * hw, 32) * 32)
     w = bgate.wave(es)
     bwd.divide_rows(rows, bwd.slots, bwd.wave(es))
@@ -102,7 +100,7 @@ def plan(n, hw, c, es, layers=True):
 
     def cluster(d, images, each):
         most = CLUSTER // images if images <= CLUSTER else 0
-        if kb > 1 or not most or up(each, most * d.slots) > SETS:
+        if pair or not most or up(each, most * d.slots) > SETS:
             return
         d.run = up(each, most * d.slots) * d.slots
         d.S = up(each, d.run)
@@ -139,11 +137,11 @@ def test_threads_and_shared_memory():
         cp = up(c, 4) * 4
         for d in plan(n, hw, c, es) + plan(n, hw, c, es, False):
             assert d.threads % 32 == 0 and 32 <= d.threads <= MOST and (d.tpr < 32 or d.tpr % 32 == 0)
-            assert d.tpr * 8 * d.k >= c and (d.slots <= 15 or d.tpr <= 32)     # (named barriers 1 .. slots)
+            assert d.tpr * 8 * d.k * d.ctas >= c > d.tpr * 8 * d.k * (d.ctas - 1) and (d.slots <= 15 or d.tpr <= 32)     # (named barriers 1 .. slots)
             if d.tpr > 32:
                 assert d.slots * up(d.tpr // 32, 2) <= MEET
-            if d.rb == 0 and d.k > 1:
-                assert d.slots == 1 and d.tpr > 32
+            if d.ctas == 2:
+                assert d.rb == 0 and d.slots == 1 and d.tpr > 32 and not d.joined
             for vec in widths(c, es):
                 el = element(es, vec)
                 assert 8 * d.k % vec == 0
@@ -153,11 +151,10 @@ def test_threads_and_shared_memory():
                     ring = 2 * fwd_stages(el, d.k) * d.rb * d.threads * 8 * d.k * el
                     assert ring % 16 == 0 and ring + (d.threads * 16 * 8 if d.k > 1 else 0) <= total
                     continue
-                ring = bwd_stages(el, d.k) * 4 * d.threads * 8 * d.k * el
-                stats = bwd_stages(el, d.k) * (d.threads // min(d.tpr, 32)) * 16
-                params = d.threads * 16 * 3 * 2 * d.k if d.k > 1 else 0
-                assert ring + stats + params <= total
-                if d.k == 1:
+                ring = BWD_STAGES * 4 * d.threads * 8 * d.k * el
+                stats = BWD_STAGES * (d.threads // min(d.tpr, 32)) * 16
+                assert ring + stats <= total
+                if d.ctas == 1:
                     sums = SUMS * 4 * 8 * d.threads                            # the threads' sums, four pairs of each
                     if d.slots > 1:
                         assert sums <= ring

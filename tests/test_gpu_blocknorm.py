@@ -266,6 +266,87 @@ def test_without_parameters(cl, post, pre):
     close(ds, ref["dscale"], tol["dscale"], False, "dscale")
 
 
+# A row of two CTAs: units of one and several rows, images one after another in a
+# pair of CTAs, odd channels and addresses, and what a call may leave out.
+PAIRS = [
+    # n, h, w, c, post, pre, dtype, gate, wide, off, f, dy, dz
+    (1, 1, 200, 8192, "layer", "layer", "bf16", False, 0, 0, True, True, True),
+    (1, 1, 200, 4097, "rms", "layer", "bf16", False, 0, 0, True, True, True),
+    (160, 1, 1, 5000, "layer", "rms", "bf16", True, 0, 0, True, True, True),
+    (90, 3, 1, 4104, "layer", "layer", "f32", True, 0, 0, True, True, True),
+    (3, 7, 11, 4352, "layer", "layer", "f32", True, 0, 0, True, True, True),
+    (1, 1, 160, 6002, "layer", "rms", "bf16", False, 0, 0, True, True, True),
+    (1, 1, 160, 4099, "layer", "layer", "bf16", True, 13, 5, True, True, True),
+    (1, 1, 160, 7001, "rms", "rms", "f32", True, 3, 1, True, True, True),
+    (1, 1, 160, 5120, "layer", "none", "bf16", False, 0, 0, True, True, False),
+    (1, 1, 160, 5120, "none", "layer", "bf16", True, 0, 0, True, True, True),
+    (1, 1, 160, 5121, "none", "none", "bf16", True, 0, 0, True, True, False),
+    (1, 1, 160, 5120, "layer", "layer", "bf16", False, 0, 0, True, False, True),
+    (1, 1, 160, 5121, "rms", "rms", "f32", True, 0, 0, True, False, True),
+    (1, 1, 160, 5120, "none", "layer", "bf16", False, 0, 0, False, True, True),
+    (1, 1, 160, 5122, "none", "rms", "bf16", False, 0, 0, False, False, True),
+]
+
+
+@pytest.mark.parametrize("n,h,w,c,post,pre,dtype,gate,wide,off,has_f,has_dy,has_dz", PAIRS)
+def test_gradient_of_rows_of_two_ctas(cl, n, h, w, c, post, pre, dtype, gate, wide, off, has_f, has_dy, has_dz):
+    shape, dt, bf = (n, h, w, c), DT[dtype], dtype == "bf16"
+    x, f = draw(shape, dt, 31, wide, off, 0.4, 0.8), draw(shape, dt, 32, wide, off, -0.3, 2.0) if has_f else None
+    dy = draw(shape, dt, 33, wide, off, 0.1, 0.5) if has_dy else None
+    dz = draw(shape, dt, 34, wide, off, 0.1, 0.5) if has_dz else None
+    p = parameters(n, c, post, pre, gate)
+    if not has_f:
+        p.update(scale=None, gate=None, post_gamma=None, post_beta=None)
+    ref, tol = reference(x, f, p, post, pre, 1e-5, dy, dz, True)
+    y, z, dx, df = buffers(shape, dt, wide, off)
+    stats = torch.full((n, h, w, 4), float("nan"), device="cuda")   # (what a norm leaves out stays so)
+    plan = cl.BlockNormPlan(n, h, w, c, post, pre, 1e-5, dtype)
+    plan.run(x, f, y if has_f else None, z if has_dz else None, stats, **p)
+    d = grads_of(p)
+    args = (x, f, stats, dy, dz, dx, df if has_f else None)
+    plan.run_backward(*args, **{k: v for k, v in p.items() if k != "pre_beta"}, **d)
+    first = [t.clone() for t in (dx, df, *d.values()) if t is not None]
+    plan.run_backward(*args, **{k: v for k, v in p.items() if k != "pre_beta"}, **d)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, (t for t in (dx, df, *d.values()) if t is not None)))
+    close(dx, ref["dx"], tol["dx"], bf, "dx")
+    if has_f:
+        close(df, ref["df"], tol["df"], bf, "df")
+    for k, v in d.items():
+        if v is not None:
+            close(v, ref[k], tol[k], False, k)
+    for t in (dx, df):
+        if wide:
+            whole = t._base
+            assert bool((whole[..., :off] == 7).all()) and bool((whole[..., off + c:] == 7).all())
+
+
+@pytest.mark.parametrize("c", [520, 8192])
+@pytest.mark.parametrize("pre", ["layer", "rms"])
+def test_gradient_that_cancels(cl, c, pre):
+    """dz along the normalised stream, and dy against what is left: dY is a rounding of
+    its terms.  (The bounds count each term's roundings, not dY's alone: a sum of
+    dY's terms apart, 22 roundings deep, is inside dY's own 34 a term.)"""
+    shape = (1, 1, 100, c)
+    x, f = draw(shape, torch.float32, 41, mean=0.4), draw(shape, torch.float32, 42, mean=-0.3, std=2.0)
+    p = parameters(1, c, "layer", pre, False)
+    plan = cl.BlockNormPlan(*shape, "layer", pre, 1e-5, "f32")
+    y, z, dx, df = (torch.empty_like(x) for _ in range(4))
+    stats = torch.empty(1, 1, 100, 4, device="cuda")
+    plan.run(x, f, y, z, stats, **p)
+    y64 = y.double()
+    m = mean(y64) if pre == "layer" else 0.0
+    hat = (y64 - m) / torch.sqrt(mean((y64 - m) ** 2) + 1e-5)
+    noise = draw(shape, torch.float32, 43)
+    for dz, dy in (((hat / p["pre_gamma"]).float(), None), (noise, None)):
+        if dz is noise:
+            dy = (-reference(x, f, p, "layer", pre, 1e-5, None, dz, True)[0]["dx"]).float()
+        ref, tol = reference(x, f, p, "layer", pre, 1e-5, dy, dz, True)
+        plan.run_backward(x, f, stats, dy, dz, dx, df, **{k: v for k, v in p.items() if k != "pre_beta"})
+        close(dx, ref["dx"], tol["dx"], False, "dx")
+        close(df, ref["df"], tol["df"], False, "df")
+
+
 def test_in_place(cl):
     """y over x, z over f; dx over dy, df over dz: the bits of separate buffers."""
     for shape, dtype in (((2, 9, 9, 256), "bf16"), ((2, 5, 5, 8192), "bf16"), ((3, 7, 7, 33), "f32"), ((2, 21, 20, 255), "bf16"),
