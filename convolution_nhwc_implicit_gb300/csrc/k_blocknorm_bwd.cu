@@ -3,22 +3,13 @@
 
 namespace bn {
 
-// The sums of the CTA's threads over the rows side by side: take(sum, channel,
-// value) for the sums FIRST and on, each by one thread, in every call the same.
+// The sums of the CTA's threads over the rows side by side (two or more):
+// take(sum, channel, value) for the sums FIRST and on, each by one thread, in every
+// call the same.
 // ent: shared, NS x P pairs a thread; free on entry, free again on return.
 template <int FIRST, int NS, int VEC, typename F>
 __device__ __forceinline__ void combine(const Lane<VEC, 1> &l, int slots, float2 (&acc)[SUMS][4], float2 *ent, F &&take) {
     constexpr int P = 4;
-    if (slots == 1) {
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                if (l.has(i, 0)) take(FIRST + s, l.chan(i, 0), acc[FIRST + s][i].x);
-                if (l.has(i, 1)) take(FIRST + s, l.chan(i, 1), acc[FIRST + s][i].y);
-            }
-        return;
-    }
     const int tpr = l.tpr, line = tpr < 32 ? tpr : 32;
     // rows of a part of a warp: first those of the warp, to every lane
     for (int o = line; o < 32; o *= 2)
@@ -62,6 +53,52 @@ __device__ __forceinline__ void add_image(const BnArgs &a, int n, int cta, bool 
     float *p = place(a, cta, s, c);
     const float gate = a.gate[(long long)n * a.C + c];
     *p = first ? gate * v : fmaf(gate, v, *p);
+}
+// A thread's channels of a row of fp32 values, in the widest vectors that they lie in.
+// (own: a row of the workspace, whose rows lie on 16 bytes)
+template <int VEC>
+__device__ __forceinline__ void store(const Lane<VEC, 1> &l, float *row, const float2 (&v)[4], bool own = true) {
+    if (VEC % 4 == 0 && (own || (reinterpret_cast<uintptr_t>(row) & 15) == 0)) {
+#pragma unroll
+        for (int i = 0; i < 4; i += 2)
+            if (l.has(i, 0)) *reinterpret_cast<float4 *>(row + l.chan(i, 0)) = make_float4(v[i].x, v[i].y, v[i + 1].x, v[i + 1].y);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (l.has(i, 0)) row[l.chan(i, 0)] = v[i].x;
+        if (l.has(i, 1)) row[l.chan(i, 1)] = v[i].y;
+    }
+}
+// add_image and the gate's gradient of a whole image, by the threads that hold its
+// sums of their channels; these start anew.
+template <int VEC>
+__device__ __forceinline__ void add_own_image(const Lane<VEC, 1> &l, const BnArgs &a, int n, int cta, bool first, float2 (&acc)[SUMS][4]) {
+    float2 gate[4];
+    l.params(gate, a.gate + (long long)n * a.C, 0.0f);
+    if (a.dgate) {
+        float2 scale[4], g1[4], b1[4];
+        l.params(scale, a.scale, 1.0f);
+        l.params(g1, a.g1, 1.0f);
+        l.params(b1, a.b1, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) scale[i] = mul2(scale[i], fma2(g1[i], acc[SUM_A][i], mul2(b1[i], acc[SUM_B][i])));
+        store(l, a.dgate + (long long)n * a.C, scale, false);
+    }
+#pragma unroll
+    for (int s = 0; s < SUM_G2; ++s) {
+        float2 sum[4];
+        if (first)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.0f, 0.0f);
+        else l.params(sum, place(a, cta, s, 0), 0.0f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sum[i] = fma2(gate[i], acc[s][i], sum[i]);
+            acc[s][i] = make_float2(0.0f, 0.0f);
+        }
+        store(l, place(a, cta, s, 0), sum);
+    }
 }
 // What the parameters' gradients of a channel need of the others, loaded ahead.
 struct Others {
@@ -398,35 +435,26 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             odz += (unsigned)sdz;
         }
         copy_wait<0>();
-        if constexpr (PAIR) {
-            // (one row at a time: a thread holds its channels' sums)
+        // One row at a time: a thread holds its channels' sums of the CTA's rows, and
+        // writes them as vectors (one value at a time, 32 bytes apart, took 8 us:
+        // 152x4096 bf16 19.0 us and 10.4; 2048x1x1x1024 with a gate, which also went
+        // through shared memory for its gradient, 50 and 26).
+        if (PAIR || (ROW != ROW_PART && a.slots == 1 && !a.joined)) {
+            if (!a.whole) {
 #pragma unroll
-            for (int i = 0; i < P; ++i)
+                for (int s = 0; s < SUMS; ++s) store(l, place(a, unit, s, 0), acc[s]);
+                continue;
+            }
+            add_own_image(l, a, n, cta, unit == cta, acc);
+            if (unit + ctas >= a.units)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (!l.has(i, e)) continue;
-                    const int c = l.chan(i, e);
-                    auto one = [&](int s) { return e ? acc[s][i].y : acc[s][i].x; };
-                    if (!a.whole) {
-#pragma unroll
-                        for (int s = 0; s < SUMS; ++s) *place(a, unit, s, c) = one(s);
-                        continue;
-                    }
-                    for (int s = 0; s < SUM_G2; ++s) add_image(a, n, cta, unit == cta, s, c, one(s));
-                    if (a.dgate) a.dgate[(long long)n * a.C + c] = Others(a, c, true).gate(one(SUM_A), one(SUM_B));
-                    if (unit + ctas >= a.units)
-                        for (int s = SUM_G2; s < SUMS; ++s) *place(a, cta, s, c) = one(s);
-                }
-            if (a.whole)
-#pragma unroll
-                for (int i = 0; i < P; ++i) acc[SUM_A][i] = acc[SUM_B][i] = make_float2(0.0f, 0.0f);
+                for (int s = SUM_G2; s < SUMS; ++s) store(l, place(a, cta, s, 0), acc[s]);
             continue;
         }
         if (a.joined) break;  // (a CTA has one unit)
         if (a.whole) {
             const bool first = unit == (int)blockIdx.x;
             float *both_sums = reinterpret_cast<float *>(ent + 2 * P * nt);  // [A, B][C]: of a channel, two threads'
-            if (a.slots == 1) __syncthreads();
             combine<SUM_A, 2, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) {
                 add_image(a, n, cta, first, s, c, v);
                 if (a.dgate) both_sums[s * a.C + c] = v;
@@ -440,12 +468,15 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             for (int i = 0; i < P; ++i) acc[SUM_A][i] = acc[SUM_B][i] = make_float2(0.0f, 0.0f);
         } else combine<0, SUMS, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { *place(a, unit, s, c) = v; });
     }
-    if constexpr (PAIR) return;
+    if (PAIR || (ROW != ROW_PART && a.slots == 1 && !a.joined)) return;
     if (a.joined) {
         // (the CTA's sums after the threads')
         float *mine = reinterpret_cast<float *>(ent + (a.slots > 1 ? SUMS * P * nt : 0));
-        if (a.slots == 1) __syncthreads();
-        combine<0, SUMS, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { mine[s * a.Cp + c] = v; });
+        if (ROW != ROW_PART && a.slots == 1) {
+            __syncthreads();
+#pragma unroll
+            for (int s = 0; s < SUMS; ++s) store(l, mine + s * a.Cp, acc[s]);
+        } else combine<0, SUMS, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { mine[s * a.Cp + c] = v; });
         join_cluster(a, mine);
     } else if (a.whole)
         combine<SUM_G2, 2, VEC>(l, a.slots, acc, ent, [&](int s, int c, float v) { *place(a, blockIdx.x, s, c) = v; });

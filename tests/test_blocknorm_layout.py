@@ -140,6 +140,8 @@ def test_threads_and_shared_memory():
             assert d.tpr * 8 * d.k * d.ctas >= c > d.tpr * 8 * d.k * (d.ctas - 1) and (d.slots <= 15 or d.tpr <= 32)     # (named barriers 1 .. slots)
             if d.tpr > 32:
                 assert d.slots * up(d.tpr // 32, 2) <= MEET
+            if d.rb == 0 and d.slots == 1:
+                assert d.tpr >= 32                                             # (a part of a warp never holds a CTA's sums alone)
             if d.ctas == 2:
                 assert d.rb == 0 and d.slots == 1 and d.tpr > 32 and not d.joined
             for vec in widths(c, es):
