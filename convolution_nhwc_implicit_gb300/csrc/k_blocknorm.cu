@@ -333,8 +333,9 @@ void plan_geometry(conv_plan *p) {
     // (6144x2560 bf16 36 us, with sixteen 27; 8192x4096 55 and 51; below, 4096x2048
     // 16.5 and 15.7, 3200x1024 7.2 and 7.7).  The gradient keeps to eight (58 and 84,
     // 91 and 133) and gives a row beyond 4096 to two CTAs of a cluster (4096x8192 bf16
-    // 147 and 106, 2048x8192 fp32 117 and 76; up to 4096 a CTA holds it: 8192x4096
-    // bf16 91, a pair 104, 4096x4096 fp32 77 and 74, 8192x2560 bf16 73 and 74).
+    // 98 us, 2048x8192 fp32 73, where sixteen took 147 and 117; up to 4096 a CTA
+    // holds it: 8192x4096 bf16 84, a pair 97, 4096x4096 fp32 71 and 71, 8192x2560
+    // bf16 70 and 67).
     // Up to 512 sixteen make a row a warp's, whose sums need no barrier: many rows
     // whose channels are no whole 16-byte vectors, or bf16 with a layer norm, are
     // faster so (8x40x40x510 layer and rms 16.4 and 15.4, 512 two layer

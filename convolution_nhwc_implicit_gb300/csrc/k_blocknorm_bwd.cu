@@ -222,8 +222,9 @@ struct PairSums {
 // the ring too: read a row ahead they were what the warps waited for (37 us, 31.5
 // so).  A pair of CTAs (ROW_PAIR) meets once a row, for the sums of both norms: a
 // meeting of the cluster takes about half a microsecond (4096x8192 bf16 143 us with
-// two, 106 with one; floor 60).  Within a CTA one meeting for both gains less than
-// its instructions cost up to 1024 channels and 4 % at 4096, and was not taken.
+// two, 106 with one, 98 with its sums written as vectors; floor 60).  Within a CTA
+// one meeting for both gained less than its instructions cost up to 1024 channels
+// and 4 % at 4096, and was not taken.
 template <typename T, int VEC, int ROW, bool ALL>
 __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_constant__ BnArgs a) {
     using R = Row<T, VEC, 1>;
