@@ -321,6 +321,102 @@ def test_gradient_of_rows_of_two_ctas(cl, n, h, w, c, post, pre, dtype, gate, wi
             assert bool((whole[..., :off] == 7).all()) and bool((whole[..., off + c:] == 7).all())
 
 
+# One row at a time and images one after another in a CTA: a thread adds its own
+# sums, writes the gate's gradient, and either may lie on no 16 bytes.
+OWN = [
+    # n, h, w, c, post, pre, dtype, parameters' address off by elements
+    (1300, 1, 1, 264, "layer", "layer", "bf16", 0),
+    (1300, 1, 1, 264, "layer", "layer", "bf16", 1),
+    (5000, 1, 1, 256, "rms", "layer", "bf16", 3),      # a warp a row
+    (200, 2, 1, 2056, "layer", "rms", "f32", 2),
+    (200, 1, 1, 2058, "layer", "layer", "bf16", 1),    # 4-byte vectors
+    (200, 1, 1, 2057, "rms", "rms", "f32", 0),
+    (160, 1, 1, 4104, "layer", "layer", "bf16", 1),    # two CTAs a row
+    (160, 1, 1, 8192, "layer", "rms", "f32", 3),
+]
+
+
+@pytest.mark.parametrize("n,h,w,c,post,pre,dtype,shift", OWN)
+def test_gradient_of_many_small_gated_images(cl, n, h, w, c, post, pre, dtype, shift):
+    shape, dt, bf = (n, h, w, c), DT[dtype], dtype == "bf16"
+    x, f = draw(shape, dt, 61, mean=0.4, std=0.8), draw(shape, dt, 62, mean=-0.3, std=2.0)
+    dy, dz = draw(shape, dt, 63, mean=0.1, std=0.5), draw(shape, dt, 64, mean=0.1, std=0.5)
+
+    def moved(t):
+        if t is None:
+            return None
+        buf = torch.full((t.numel() + 8,), 9.0, device="cuda")
+        buf[shift:shift + t.numel()] = t.flatten()
+        return buf[shift:shift + t.numel()].view(t.shape)
+
+    p = {k: moved(v) for k, v in parameters(n, c, post, pre, True).items()}
+    d = {k: moved(v) for k, v in grads_of(p).items()}
+    ref, tol = reference(x, f, p, post, pre, 1e-5, dy, dz, True)
+    y, z, dx, df = buffers(shape, dt, 0, 0)
+    stats = torch.empty(n, h, w, 4, device="cuda")
+    plan = cl.BlockNormPlan(n, h, w, c, post, pre, 1e-5, dtype)
+    plan.run(x, f, y, z, stats, **p)
+    plan.run_backward(x, f, stats, dy, dz, dx, df, **{k: v for k, v in p.items() if k != "pre_beta"}, **d)
+    torch.cuda.synchronize()
+    close(y, ref["y"], tol["y"], bf, "y")
+    close(z, ref["z"], tol["z"], bf, "z")
+    close(dx, ref["dx"], tol["dx"], bf, "dx")
+    close(df, ref["df"], tol["df"], bf, "df")
+    for k, v in d.items():
+        if v is not None:
+            close(v, ref[k], tol[k], False, k)
+            assert bool((v._base[:shift] == 9).all()) and bool((v._base[shift + v.numel():] == 9).all())
+
+
+def test_rows_of_two_ctas_on_two_streams_and_in_graphs(cl):
+    """Two gradients at once, then captured on two streams and replayed together: the bits of one alone."""
+    shape = (1, 1, 400, 5120)
+    plan = cl.BlockNormPlan(*shape, "layer", "rms")
+    sides = []
+    for i in range(2):
+        x, f, dy, dz = (draw(shape, torch.bfloat16, 70 + 10 * i + j) for j in range(4))
+        y, z, dx, df = (torch.empty_like(x) for _ in range(4))
+        stats = torch.empty(1, 1, 400, 4, device="cuda")
+        p = parameters(1, 5120, "layer", "rms", True, seed=80 + i)
+        d = grads_of(p)
+        plan.run(x, f, y, z, stats, **p)
+        kw = {**{k: v for k, v in p.items() if k != "pre_beta"}, **d}
+        run = (lambda a, k: lambda: plan.run_backward(*a, **k))((x, f, stats, dy, dz, dx, df), kw)
+        sides.append((run, [dx, df] + [v for v in d.values() if v is not None]))
+    alone = []
+    for run, outs in sides:
+        run()
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in outs])
+
+    def check():
+        torch.cuda.synchronize()
+        for (_, outs), ref in zip(sides, alone):
+            assert all(torch.equal(a, b) for a, b in zip(outs, ref))
+            for t in outs:
+                t.fill_(3.0)
+        torch.cuda.synchronize()
+
+    check()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for (run, _), st in zip(sides, streams):
+        with torch.cuda.stream(st):
+            for _ in range(3):
+                run()
+    check()
+    graphs = []
+    for run, _ in sides:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        graphs.append(g)
+    for _ in range(2):
+        for g, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                g.replay()
+        check()
+
+
 @pytest.mark.parametrize("c", [520, 8192])
 @pytest.mark.parametrize("pre", ["layer", "rms"])
 def test_gradient_that_cancels(cl, c, pre):
