@@ -118,13 +118,15 @@ struct Others {
 };
 
 // The CTAs of a cluster, a unit each, join their sums: `mine` [SUMS][Cp] is the
-// calling CTA's, which joins a share of the channels, a thread each.  What a
-// channel needs besides is on its way while the CTAs wait for one another.
+// calling CTA's, which joins a share of the channels, a thread each (the last
+// CTAs' shares may be empty).  What a channel needs besides is on its way while
+// the CTAs wait for one another, which each of them does between its arrivals.
 __device__ __forceinline__ void join_cluster(const BnArgs &a, const float *mine) {
     cluster_arrive();
-    const int ranks = (int)gridDim.x, share = (a.C + ranks - 1) / ranks, c1 = min(a.C, ((int)blockIdx.x + 1) * share);
-    for (int c = (int)blockIdx.x * share + threadIdx.x; c - (int)threadIdx.x < c1; c += blockDim.x) {
-        const bool on = c < c1, first = c == (int)blockIdx.x * share + (int)threadIdx.x;
+    const int ranks = (int)gridDim.x, share = (a.C + ranks - 1) / ranks, c0 = (int)blockIdx.x * share, c1 = min(a.C, c0 + share);
+    if (c0 >= c1) cluster_wait();
+    for (int c = c0 + threadIdx.x; c - (int)threadIdx.x < c1; c += blockDim.x) {
+        const bool on = c < c1, first = c == c0 + (int)threadIdx.x;
         const Others others(a, c, on);
         float gate[kCluster];
 #pragma unroll
