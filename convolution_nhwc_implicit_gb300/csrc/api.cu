@@ -166,6 +166,14 @@ int conv_grant_smem(const void *k, int device, int need) {
     return CONV_OK;
 }
 
+int conv_upload(void *dst, const void *src, size_t bytes) {
+    // (a copy from pageable memory may return when its bytes are staged, and a
+    // stream of its own is not ordered after the legacy one)
+    return cudaMemcpy(dst, src, bytes, cudaMemcpyHostToDevice) == cudaSuccess && cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess
+               ? CONV_OK
+               : CONV_ERR_CUDA;
+}
+
 int conv_plan_bind_device(conv_plan *p, bool status_word) {
     int major = 0, minor = 0;
     if (cudaGetDevice(&p->device) != cudaSuccess ||

@@ -148,6 +148,9 @@ struct conv_plan {
 // word if its kernels have waits to report on.  Returns a CONV_* status.
 int conv_plan_bind_device(conv_plan *p, bool status_word);
 
+// Host memory to the device, there for every stream when this returns (a CONV_* status).
+int conv_upload(void *dst, const void *src, size_t bytes);
+
 // Whether [a, a + na) and [b, b + nb) share a byte (a null pointer: no).
 static inline bool conv_overlaps(const void *a, size_t na, const void *b, size_t nb) {
     if (!a || !b || na == 0 || nb == 0) return false;

@@ -475,7 +475,7 @@ extern "C" int conv_plan_create_gradclip(int32_t tensors, const int64_t *counts,
             memcpy(items.data() + count, first.data(), first.size() * sizeof(int));
             const size_t table = items.size() * sizeof(uint4);
             if (cudaMalloc(&g.items, table) != cudaSuccess) rc = CONV_ERR_OOM;
-            else if (cudaMemcpy(g.items, items.data(), table, cudaMemcpyHostToDevice) != cudaSuccess) rc = CONV_ERR_CUDA;
+            else rc = conv_upload(g.items, items.data(), table);
             g.first = reinterpret_cast<int *>(g.items + count);
             snprintf(p->desc, sizeof(p->desc), "gradclip %d tensors, %lld elements in %zu items, ctas=%d launches=%d", tensors, total,
                      count, g.parts, clip_launches(&g));
