@@ -174,6 +174,9 @@ int conv_upload(void *dst, const void *src, size_t bytes) {
                : CONV_ERR_CUDA;
 }
 
+// A plan's status word before anything was waited for in vain.
+static const int kNoStatus = 0;
+
 int conv_plan_bind_device(conv_plan *p, bool status_word) {
     int major = 0, minor = 0;
     if (cudaGetDevice(&p->device) != cudaSuccess ||
@@ -184,8 +187,7 @@ int conv_plan_bind_device(conv_plan *p, bool status_word) {
     if (major != 10 || minor != 3) return CONV_ERR_UNSUPPORTED;
     if (!status_word) return CONV_OK;
     if (cudaMalloc(&p->d_status, sizeof(int)) != cudaSuccess) return CONV_ERR_OOM;
-    if (cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess) return CONV_ERR_CUDA;
-    return CONV_OK;
+    return conv_upload(p->d_status, &kNoStatus, sizeof(int));
 }
 
 int conv_grant_smem_once(const void *k, int device, int need) {
@@ -314,7 +316,7 @@ int conv_plan_create_fused(const conv_shape_t *shape, int stride, int pad_h, int
         delete p;
         return CONV_ERR_OOM;
     }
-    if (cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess) {
+    if (conv_upload(p->d_status, &kNoStatus, sizeof(int)) != CONV_OK) {
         conv_plan_destroy(p);
         return CONV_ERR_CUDA;
     }
@@ -329,9 +331,9 @@ int conv_plan_create_fused(const conv_shape_t *shape, int stride, int pad_h, int
             conv_plan_destroy(p);
             return CONV_ERR_OOM;
         }
-        const cudaError_t e = cudaMemcpy(p->d_mult, hm, sizeof(float) * shape->c_out, cudaMemcpyHostToDevice);
+        rc = conv_upload(p->d_mult, hm, sizeof(float) * shape->c_out);
         free(hm);
-        if (e != cudaSuccess) { conv_plan_destroy(p); return CONV_ERR_CUDA; }
+        if (rc != CONV_OK) { conv_plan_destroy(p); return rc; }
     }
 
     if (chosen == CONV_ALGO_IGEMM) {
@@ -407,7 +409,7 @@ int conv_plan_create_dwpw(const conv_shape_t *shape, int stride, int pad, conv_d
         delete p;
         return CONV_ERR_OOM;
     }
-    if (cudaMemset(p->d_status, 0, sizeof(int)) != cudaSuccess) {
+    if (conv_upload(p->d_status, &kNoStatus, sizeof(int)) != CONV_OK) {
         conv_plan_destroy(p);
         return CONV_ERR_CUDA;
     }
@@ -552,7 +554,7 @@ int conv_plan_check_device_status(conv_plan_t *plan, void *stream) {
     if (!plan->d_status) return CONV_OK;  // kernels without waits
     if (cudaMemcpy(&h, plan->d_status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return CONV_ERR_CUDA;
     if (h != 0) {
-        if (cudaMemset(plan->d_status, 0, sizeof(int)) != cudaSuccess) return CONV_ERR_CUDA;
+        if (conv_upload(plan->d_status, &kNoStatus, sizeof(int)) != CONV_OK) return CONV_ERR_CUDA;
         return CONV_ERR_DEVICE_TIMEOUT;
     }
     return CONV_OK;
