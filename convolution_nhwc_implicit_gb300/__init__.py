@@ -860,8 +860,8 @@ class GradClipPlan(_OpPlan):
         take, give = _raw_memory_calls()
         ws = take(self.workspace_bytes, handle) if self.workspace_bytes else None
         try:
-            rc = self._lib.conv_run_gradclip(self._handle, g.buffer_info()[0], o and o.buffer_info()[0], float(max_norm), pn,
-                                             ws, handle)
+            rc = self._lib.conv_run_gradclip(self._handle, g.buffer_info()[0], None if o is None else o.buffer_info()[0],
+                                             float(max_norm), pn, ws, handle)
         finally:
             if ws is not None:
                 give(ws)
