@@ -38,6 +38,7 @@ struct BnArgs {
     int whole;                     // gradient: a unit is a whole image of a gated map
     int want_b;                    // gradient: B is asked for
     int joined;                    // gradient: the CTAs are one cluster and join their sums themselves
+    int last_t, last_v;            // where a row's last value is, of single ones: Lane::t and the vector
 };
 
 // Where a thread stands: which row of those side by side, which of the row's
@@ -80,12 +81,17 @@ struct Lane {
 };
 
 // Bytes of an element in the ring.  Single bf16 values, which no asynchronous copy
-// takes, come as the word that holds them (another two bytes of the same four).
+// takes, come as the word that holds them (another two bytes of the same four, which
+// are not used).
 __host__ __device__ constexpr int ring_element(int es, int vec) { return es * vec < 4 ? 4 : es; }
 
 // A thread's vectors of one row: from its ring of shared memory, to a map, and
-// from a map to the ring.  Vectors beyond the row's end stay 0 in the ring.
-template <typename T, int VEC, int K>
+// from a map to the ring.  Vectors beyond the row's end stay 0 in the ring.  CUT: of
+// single bf16 values, a map starts in the middle of a word or ends in one; the half
+// that is not the map's is not read.  (An instance of its own, 1 to 4 % slower, and 9
+// to 13 % forward beyond 2048 channels: 8191x3001 takes 73 and 160 us, 8192x3001, whose
+// maps are whole words, 67 and 155.)
+template <typename T, int VEC, int K, bool CUT = false>
 struct Row {
     using V = Vec<T, VEC>;
     using Raw = typename V::Raw;
@@ -134,14 +140,22 @@ struct Row {
             if (l.on(v)) *reinterpret_cast<Raw *>(row + v * l.tpr * VEC) = V::pack(one);
         }
     }
-    __device__ static __forceinline__ void ask(const L &l, const T *row, Slot *dst) {
+    __device__ static __forceinline__ const void *word(const T *p) { return reinterpret_cast<const void *>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)3); }
+    // row: the address of the thread's first vector.  CUT: channels from `upto` on are
+    // left out, and the first one where `late`; a map's ends are asked for apart.
+    __device__ static __forceinline__ void ask(const L &l, const T *row, Slot *dst, int upto, bool late) {
 #pragma unroll
         for (int v = 0; v < NV; ++v)
-            if (l.on(v)) {
+            if (CUT ? l.first(v) < upto && !(v == 0 && late) : l.on(v)) {
                 const T *at = row + v * l.tpr * VEC;
-                if constexpr (kWord) at = reinterpret_cast<const T *>(reinterpret_cast<uintptr_t>(at) & ~(uintptr_t)3);
-                copy_async<(int)sizeof(Slot)>(tc::smem_u32(dst + v * step), at);
+                copy_async<(int)sizeof(Slot)>(tc::smem_u32(dst + v * step), kWord ? word(at) : at);
             }
+    }
+    // A map's last value, and its first (alone: the only one).
+    __device__ static __forceinline__ void ask_last(const T *at, Slot *dst) { copy_async_part(tc::smem_u32(dst), word(at), odd(at) ? 4 : 2); }
+    __device__ static __forceinline__ void ask_first(const T *at, Slot *dst, bool alone) {
+        if (odd(at)) *reinterpret_cast<uint32_t *>(dst) = (uint32_t)*reinterpret_cast<const uint16_t *>(at) << 16;
+        else copy_async_part(tc::smem_u32(dst), word(at), alone ? 2 : 4);
     }
     // the vectors beyond the row's end in `rows` rows of the ring
     template <int ROWS>
@@ -289,9 +303,10 @@ __host__ __device__ constexpr int bwd_stages() { return 3; }
 // ... and of the forward kernel's.
 __host__ __device__ constexpr int fwd_stages(int es, int k) { return k == 2 && es == 4 ? 2 : 3; }
 
-// The gradient's kernel for a vector width and tpr threads a row (or half a row,
-// of a pair of CTAs), and the launch that joins its sums.
-const void *pick_bwd(conv_dtype_t dt, int vec, bool pair, int tpr, bool all);
+// The gradient's kernel for a vector width (cut: as Row's, of single bf16 values) and
+// tpr threads a row (or half a row, of a pair of CTAs), and the launch that joins its
+// sums.
+const void *pick_bwd(conv_dtype_t dt, int vec, bool cut, bool pair, int tpr, bool all);
 cudaError_t launch_join(const BnArgs &a, int parts, cudaStream_t st);
 
 }  // namespace bn

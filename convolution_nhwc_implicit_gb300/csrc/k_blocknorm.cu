@@ -50,9 +50,9 @@ namespace {
 // y and z of a run of rows, RB at a time.  With RB = 1 and one row of 8 channels
 // a thread the rows that a CTA takes of a gated map may be of several images;
 // otherwise a run is of one.  ALL: f, y and z are given.
-template <typename T, int VEC, int K, int RB, int ROW, bool ALL>
+template <typename T, int VEC, int K, int RB, int ROW, bool ALL, bool CUT>
 __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_constant__ BnArgs a) {
-    using R = Row<T, VEC, K>;
+    using R = Row<T, VEC, K, CUT>;
     using Slot = typename R::Slot;
     constexpr int P = R::P, D = fwd_stages(R::kElement, K), LINE = R::NV * R::step, STAGE = 2 * RB * LINE;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -76,12 +76,24 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
     pdl_wait();
     const Slot *d = ring;
     Slot *to = ring;
-    auto ask = [&] {
+    auto ask = [&](auto start) {  // (whether the map's first row may be among them)
+        constexpr bool START = decltype(start)::value;
 #pragma unroll
         for (int b = 0; b < RB; ++b) {
             if (asked < r1) {
-                R::ask(l, x, to + b * LINE);
-                if (block) R::ask(l, f, to + (RB + b) * LINE);
+                const bool late = CUT && START && asked == 0 && l.t == 0, bottom = CUT && asked == a.rows - 1;
+                const int upto = bottom ? l.C - 1 : l.C;
+                R::ask(l, x, to + b * LINE, upto, late);
+                if (block) R::ask(l, f, to + (RB + b) * LINE, upto, late);
+                if (bottom && l.t == a.last_t && !(late && upto == 0)) {
+                    const int at = a.last_v * a.tpr, slot = a.last_v * R::step;
+                    R::ask_last(x + at, to + b * LINE + slot);
+                    if (block) R::ask_last(f + at, to + (RB + b) * LINE + slot);
+                }
+                if (late) {
+                    R::ask_first(x, to + b * LINE, upto == 0);
+                    if (block) R::ask_first(f, to + (RB + b) * LINE, upto == 0);
+                }
             }
             asked += a.slots;
             x += sx;
@@ -91,7 +103,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
         to = to == ring + (D - 1) * STAGE ? ring : to + STAGE;
     };
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i) ask();
+    for (int i = 0; i < D - 1; ++i) ask(std::true_type());
     float2 q[P], p[P], g2[P], b2[P];
     // pre's parameters: in registers, or, sixteen channels a thread, at a place of
     // the thread's own in shared memory (with 64 registers of parameters some
@@ -133,7 +145,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
         ox += RB * nx;
         of += RB * nf;
         d = d == ring + (D - 1) * STAGE ? ring : d + STAGE;
-        ask();
+        ask(std::false_type());
         float2 one[RB], two[RB];
 #pragma unroll
         for (int b = 0; b < RB; ++b) one[b] = two[b] = make_float2(0.0f, 1.0f);
@@ -177,22 +189,23 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
 }
 
 // ------------------------------------------------------------------ host side
-template <typename T, int VEC>
+template <typename T, int VEC, bool CUT = false>
 const void *pick_fwd(int k, int rb, int tpr, bool all) {
-    if (k == 2 && tpr == 32) return all ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARP, true> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARP, false>;
-    if (k == 2) return all ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, true> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, false>;
-    if (rb == 1) return (const void *)&bn_fwd_kernel<T, VEC, 1, 1, ROW_ANY, false>;
-    if (!all) return (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_ANY, false>;
-    return tpr < 32 ? (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_PART, true>
-                    : (tpr == 32 ? (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_WARP, true> : (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_WARPS, true>);
+    if (k == 2 && tpr == 32) return all ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARP, true, CUT> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARP, false, CUT>;
+    if (k == 2) return all ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, true, CUT> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, false, CUT>;
+    if (rb == 1) return (const void *)&bn_fwd_kernel<T, VEC, 1, 1, ROW_ANY, false, CUT>;
+    if (!all) return (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_ANY, false, CUT>;
+    return tpr < 32 ? (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_PART, true, CUT>
+                    : (tpr == 32 ? (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_WARP, true, CUT> : (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_WARPS, true, CUT>);
 }
 // (rb: rows at a time of the forward kernel, 0: the gradient)
-const void *pick_kernel(conv_dtype_t dt, int vec, const BnGeom::Part &d, bool all) {
+const void *pick_kernel(conv_dtype_t dt, int vec, bool cut, const BnGeom::Part &d, bool all) {
     using B = __nv_bfloat16;
     const int rb = d.rb, k = d.k, tpr = d.tpr;
-    if (!rb) return bn::pick_bwd(dt, vec, d.pair, tpr, all);
+    if (!rb) return bn::pick_bwd(dt, vec, cut, d.pair, tpr, all);
     if (dt == CONV_F32) return vec == 4 ? pick_fwd<float, 4>(k, rb, tpr, all) : pick_fwd<float, 1>(k, rb, tpr, all);
-    return vec == 8 ? pick_fwd<B, 8>(k, rb, tpr, all) : (vec == 2 ? pick_fwd<B, 2>(k, rb, tpr, all) : pick_fwd<B, 1>(k, rb, tpr, all));
+    if (vec > 1) return vec == 8 ? pick_fwd<B, 8>(k, rb, tpr, all) : pick_fwd<B, 2>(k, rb, tpr, all);
+    return cut ? pick_fwd<B, 1, true>(k, rb, tpr, all) : pick_fwd<B, 1>(k, rb, tpr, all);
 }
 
 // Channels a vector access takes: the widest that the channel count, every
@@ -210,6 +223,16 @@ int vec_for(const conv_plan *p, const Map (&maps)[N]) {
     return 1;
 }
 
+// Whether one of the maps of single bf16 values starts in the middle of a 4-byte word
+// or ends in one.
+template <int N>
+bool cuts_words(const conv_plan *p, const Map (&maps)[N]) {
+    const long long rows = (long long)p->s.n * p->s.h * p->s.w;
+    for (const Map &m : maps)
+        if (m.p && (((uintptr_t)m.p | ((uintptr_t)m.p + 2 * ((rows - 1) * m.pitch + p->s.c_in))) & 3u)) return true;
+    return false;
+}
+
 long long up(long long a, long long b) { return (a + b - 1) / b; }
 
 // Bytes of the ring of a CTA: a thread's 8 k channels of each map and stage.
@@ -225,14 +248,18 @@ size_t ring_bytes(const BnGeom::Part &d, int es) {
     return bwd_stages() * (4 * maps + (size_t)d.threads / (d.tpr < 32 ? d.tpr : 32) * 16);  // (and a row's statistics)
 }
 
-cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, BnArgs &a, cudaStream_t st) {
+// in: the maps that are read.
+template <int N>
+cudaError_t launch(const conv_plan *p, const BnGeom::Part &d, int vec, const Map (&in)[N], BnArgs &a, cudaStream_t st) {
     const size_t smem = ring_bytes(d, ring_element(conv_esize(p->dtype), vec));
-    const void *k = pick_kernel(p->dtype, vec, d, d.rb ? a.f && a.o0 && a.o1 : a.f && a.dy && a.dz);
+    const void *k = pick_kernel(p->dtype, vec, cuts_words(p, in), d, d.rb ? a.f && a.o0 && a.o1 : a.f && a.dy && a.dz);
     if (smem > 40 * 1024) {  // (with the kernel's static shared memory: 48 KB are free)
         const int rc = conv_grant_smem_once(k, p->device, (int)smem);
         if (rc != CONV_OK) return cudaErrorInvalidValue;
     }
     if (d.joined && conv_allow_cluster_once(k, p->device, d.grid) != CONV_OK) return cudaErrorInvalidValue;
+    const int last = (a.C - 1) / d.tpr, vectors = 8 * d.k;
+    a.last_v = last % vectors; a.last_t = (a.C - 1) % d.tpr + (last - a.last_v) * d.tpr;
     a.tpr = d.tpr; a.full = d.full; a.slots = d.slots; a.run = d.run; a.S = d.S; a.units = d.units; a.whole = d.whole; a.joined = d.joined;
     void *args[] = {&a};
     return conv_launch(k, dim3((unsigned)d.grid << d.pair), dim3((unsigned)d.threads), args, smem, st, d.joined ? d.grid : 1 << d.pair);
@@ -372,7 +399,7 @@ void plan_geometry(conv_plan *p) {
         const long long run = sets * d.slots, S = up(each, run);
         // (of the instances that a call may choose, the one of the widest vectors
         // stands for all, with the shared memory of the one that takes the most)
-        const void *kernel = pick_kernel(p->dtype, 16 / es, d, true);
+        const void *kernel = pick_kernel(p->dtype, 16 / es, false, d, true);
         const size_t smem = ring_bytes(d, 4);
         if (conv_grant_smem_once(kernel, p->device, (int)smem) != CONV_OK ||
             !conv_cluster_fits(kernel, p->device, (int)(images * S), d.threads, smem))
@@ -478,7 +505,7 @@ extern "C" int conv_run_blocknorm(const conv_plan_t *plan, const void *x, int64_
     a.stats = reinterpret_cast<float4 *>(stats);
     const Map all[4] = {in[0], in[1], out[0], out[1]};
     const BnGeom::Part &g = w.gate ? p->bn.fwd_gated : p->bn.fwd;
-    return launch(p, g, vec_for(p, all), a, (cudaStream_t)stream) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
+    return launch(p, g, vec_for(p, all), in, a, (cudaStream_t)stream) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;
 }
 
 extern "C" int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, int64_t x_pitch, const void *f, int64_t f_pitch,
@@ -535,7 +562,7 @@ extern "C" int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, in
     a.want_b = d.post_beta || (w.post_beta && (d.scale || d.gate));
     const BnGeom::Part &g = w.gate ? p->bn.bwd_gated : p->bn.bwd;
     const Map all[6] = {in[0], in[1], in[2], in[3], out[0], out[1]};
-    if (launch(p, g, vec_for(p, all), a, st) != cudaSuccess) return CONV_ERR_CUDA;
+    if (launch(p, g, vec_for(p, all), in, a, st) != cudaSuccess) return CONV_ERR_CUDA;
     const bool sums = d.scale || d.post_gamma || d.post_beta || d.pre_gamma || d.pre_beta, images = d.gate && !g.whole;
     if (g.joined || (!sums && !images)) return CONV_OK;
     return launch_join(a, g.grid, st) == cudaSuccess ? CONV_OK : CONV_ERR_CUDA;

@@ -227,9 +227,9 @@ struct PairSums {
 // two, 106 with one, 98 with its sums written as vectors; floor 60).  Within a CTA
 // one meeting for both gained less than its instructions cost up to 1024 channels
 // and 4 % at 4096, and was not taken.
-template <typename T, int VEC, int ROW, bool ALL>
+template <typename T, int VEC, int ROW, bool ALL, bool CUT>
 __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_constant__ BnArgs a) {
-    using R = Row<T, VEC, 1>;
+    using R = Row<T, VEC, 1, CUT>;
     using Slot = typename R::Slot;
     constexpr int P = R::P, D = bwd_stages(), LINE = R::NV * R::step, STAGE = 4 * LINE;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -281,13 +281,29 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
         float4 *sto = seen;
         __syncwarp();  // (every lane has read the last unit's statistics)
         // A row beyond the run counts as zeros.
-        auto ask = [&] {
+        auto ask = [&](auto start) {  // (whether the map's first row may be it)
+            constexpr bool START = decltype(start)::value;
             if (asked < r1) {
                 if (copies) copy_async<16>(tc::smem_u32(sto), a.stats + asked);
-                R::ask(l, x, to);
-                if (block) R::ask(l, f, to + LINE);
-                if (stream) R::ask(l, dy, to + 2 * LINE);
-                if (norm) R::ask(l, dz, to + 3 * LINE);
+                const bool late = CUT && START && asked == 0 && l.t == 0, bottom = CUT && asked == a.rows - 1;
+                const int upto = bottom ? l.C - 1 : l.C;
+                R::ask(l, x, to, upto, late);
+                if (block) R::ask(l, f, to + LINE, upto, late);
+                if (stream) R::ask(l, dy, to + 2 * LINE, upto, late);
+                if (norm) R::ask(l, dz, to + 3 * LINE, upto, late);
+                if (bottom && l.t == a.last_t && !(late && upto == 0)) {
+                    const int at = a.last_v * a.tpr, slot = a.last_v * R::step;
+                    R::ask_last(x + at, to + slot);
+                    if (block) R::ask_last(f + at, to + LINE + slot);
+                    if (stream) R::ask_last(dy + at, to + 2 * LINE + slot);
+                    if (norm) R::ask_last(dz + at, to + 3 * LINE + slot);
+                }
+                if (late) {
+                    R::ask_first(x, to, upto == 0);
+                    if (block) R::ask_first(f, to + LINE, upto == 0);
+                    if (stream) R::ask_first(dy, to + 2 * LINE, upto == 0);
+                    if (norm) R::ask_first(dz, to + 3 * LINE, upto == 0);
+                }
             } else {
                 if (copies) *sto = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -304,7 +320,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             sto = last ? seen : sto + 32 / line;
         };
 #pragma unroll
-        for (int i = 0; i < D - 1; ++i) ask();
+        for (int i = 0; i < D - 1; ++i) ask(std::true_type());
         if (block && a.gate) factors(l, a, n, q, p);
         for (int base = r0; base < r1; base += a.slots) {
             const bool on = row < r1;
@@ -369,7 +385,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] = w[i].x + w[i].y;
                 pair.give(v);
-                ask();
+                ask(std::false_type());
                 pair.take(v);
                 // (without the second norm its statistics may be anything)
                 const float my = norm ? -v[1] * a.inv_c * st.w : 0.0f, m = norm ? v[0] * mean_pre * st.w : 0.0f;
@@ -399,7 +415,7 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             const bool last = d == ring + (D - 1) * STAGE;
             d = last ? ring : d + STAGE;
             sd = last ? seen : sd + 32 / line;
-            if (!PAIR) ask();
+            if (!PAIR) ask(std::false_type());
             if (on) R::put(l, dx, t);
             if (block) {
                 // (what the mean's terms leave in a row beyond the run is 0: its sums are)
@@ -570,17 +586,18 @@ __global__ void __launch_bounds__(kJoin) bn_join_kernel(const __grid_constant__ 
     }
 }
 
-template <typename T, int VEC>
+template <typename T, int VEC, bool CUT = false>
 const void *pick(bool pair, int tpr, bool all) {
-    if (pair) return all ? (const void *)&bn_bwd_kernel<T, VEC, ROW_PAIR, true> : (const void *)&bn_bwd_kernel<T, VEC, ROW_PAIR, false>;
-    if (!all) return (const void *)&bn_bwd_kernel<T, VEC, ROW_ANY, false>;
-    return tpr < 32 ? (const void *)&bn_bwd_kernel<T, VEC, ROW_PART, true>
-                    : (tpr == 32 ? (const void *)&bn_bwd_kernel<T, VEC, ROW_WARP, true> : (const void *)&bn_bwd_kernel<T, VEC, ROW_WARPS, true>);
+    if (pair) return all ? (const void *)&bn_bwd_kernel<T, VEC, ROW_PAIR, true, CUT> : (const void *)&bn_bwd_kernel<T, VEC, ROW_PAIR, false, CUT>;
+    if (!all) return (const void *)&bn_bwd_kernel<T, VEC, ROW_ANY, false, CUT>;
+    return tpr < 32 ? (const void *)&bn_bwd_kernel<T, VEC, ROW_PART, true, CUT>
+                    : (tpr == 32 ? (const void *)&bn_bwd_kernel<T, VEC, ROW_WARP, true, CUT> : (const void *)&bn_bwd_kernel<T, VEC, ROW_WARPS, true, CUT>);
 }
-const void *pick_bwd(conv_dtype_t dt, int vec, bool pair, int tpr, bool all) {
+const void *pick_bwd(conv_dtype_t dt, int vec, bool cut, bool pair, int tpr, bool all) {
     using B = __nv_bfloat16;
     if (dt == CONV_F32) return vec == 4 ? pick<float, 4>(pair, tpr, all) : pick<float, 1>(pair, tpr, all);
-    return vec == 8 ? pick<B, 8>(pair, tpr, all) : (vec == 2 ? pick<B, 2>(pair, tpr, all) : pick<B, 1>(pair, tpr, all));
+    if (vec > 1) return vec == 8 ? pick<B, 8>(pair, tpr, all) : pick<B, 2>(pair, tpr, all);
+    return cut ? pick<B, 1, true>(pair, tpr, all) : pick<B, 1>(pair, tpr, all);
 }
 
 cudaError_t launch_join(const BnArgs &a, int parts, cudaStream_t st) {

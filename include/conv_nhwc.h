@@ -427,8 +427,10 @@ CONV_API int conv_run_w4(const conv_plan_t *plan, const void *x, const void *pac
  * z, dz is required there and NULL otherwise.  A written map may be one of the
  * input maps itself (address and pitch alike: y over x in a stream that is not
  * trained, df over dz); otherwise nothing that a run writes shares an element
- * with another map or a byte with anything else (CONV_ERR_ALIASING).  n = 0
- * does nothing (the gradient writes zeros to the sums over pixels).  The
+ * with another map or a byte with anything else (CONV_ERR_ALIASING).  Nothing
+ * before a map's first value or behind its last is read; what lies between its
+ * pixels may be (words that hold a bf16 value of the map), and is not used.
+ * n = 0 does nothing (the gradient writes zeros to the sums over pixels).  The
  * gradient takes conv_plan_workspace_bwd bytes of scratch (0 where all rows fit a
  * cluster). */
 typedef enum { CONV_NORM_NONE = 0, CONV_NORM_LAYER = 1, CONV_NORM_RMS = 2 } conv_norm_t;
