@@ -1,0 +1,78 @@
+"""The plans of the norms around a block as the library makes them, against what
+test_blocknorm_layout.py restates of them: the threads, grids, clusters, shared
+memory and scratch of every launch, on a fake runtime that leaves a line for each.
+(Its device runs every cluster that is asked about, as a GB300 does.)"""
+import ctypes
+
+import pytest
+from fake_cuda import load
+from test_blocknorm_layout import SUMS, plan, shapes, up, widths
+
+
+class Params(ctypes.Structure):
+    _fields_ = [(k, ctypes.c_void_p) for k in ("scale", "gate", "post_gamma", "post_beta", "pre_gamma", "pre_beta")]
+
+
+@pytest.fixture(scope="module")
+def lib(tmp_path_factory):
+    out = load(tmp_path_factory.mktemp("fake"))
+    p, i64 = ctypes.c_void_p, ctypes.c_int64
+    out.conv_plan_create_blocknorm.argtypes = [ctypes.c_int] * 6 + [ctypes.c_float, ctypes.c_int, ctypes.POINTER(p)]
+    out.conv_run_blocknorm.argtypes = [p, p, i64, p, i64, p, p, i64, p, i64, p, p]
+    out.conv_run_blocknorm_bwd.argtypes = [p, p, i64, p, i64, p, p] + [p, i64] * 4 + [p, p, p]
+    out.conv_plan_destroy.argtypes = [p]
+    for k in ("conv_plan_workspace", "conv_plan_workspace_bwd"):
+        getattr(out, k).argtypes = [p, ctypes.POINTER(ctypes.c_size_t)]
+    return out
+
+
+# Addresses that no launch follows: a part of the address space for each tensor.
+def place(i, shift=0):
+    return (i + 1 << 42) + shift
+
+
+def launches(lib):
+    lines = lib.fake_log().decode().split("\n")[:-1]
+    lib.fake_clear()
+    out = []
+    for line in lines:
+        name, grid, threads, smem, cluster = line.split()
+        out.append((name, tuple(map(int, grid.split(","))), int(threads), int(smem), int(cluster)))
+    return out
+
+
+def test_launches_are_the_restated_ones(lib):
+    kinds = {"layers": (1, 1), "rms": (2, 2)}
+    for number, (n, hw, c, es) in enumerate(shapes(1200, 11)):
+        post, pre = kinds["layers" if number % 2 else "rms"]
+        h = ctypes.c_void_p()
+        assert lib.conv_plan_create_blocknorm(n, hw, 1, c, post, pre, 1e-5, 0 if es == 4 else 1, ctypes.byref(h)) == 0
+        fwd, gated, bwd, bgate = plan(n, hw, c, es, post == 1)
+        parts = max(0 if d.joined else d.grid for d in (bwd, bgate))
+        sizes = ctypes.c_size_t(9), ctypes.c_size_t(9)
+        assert lib.conv_plan_workspace(h, ctypes.byref(sizes[0])) == 0 and lib.conv_plan_workspace_bwd(h, ctypes.byref(sizes[1])) == 0
+        assert (sizes[0].value, sizes[1].value) == (0, parts * SUMS * up(c, 4) * 4 * 4)
+        lib.fake_clear()
+        for vec in widths(c, es):
+            shift = {8: 0, 4: 0, 2: 4, 1: es}[vec]            # (what makes the accesses that narrow)
+            for gate in (None, place(20)):
+                w, d = Params(gate=gate), Params(place(21), place(22) if gate else None, place(23), None, place(25), None)
+                x, f, y, z, dy, dz, dx, df = (place(i, shift) for i in range(8))
+                where = (n, hw, c, es, vec, gate)
+                assert lib.conv_run_blocknorm(h, x, 0, f, 0, ctypes.byref(w), y, 0, z, 0, place(10), None) == 0
+                (name, grid, threads, smem, cluster), = launches(lib)
+                one = gated if gate else fwd
+                el = 4 if es * vec < 4 else es
+                assert "bn_fwd_kernel" in name and (grid, threads, cluster) == ((one.grid, 1, 1), one.threads, 1), where
+                assert smem == one.smem(el), where
+                assert lib.conv_run_blocknorm_bwd(h, x, 0, f, 0, ctypes.byref(w), place(10), dy, 0, dz, 0, dx, 0, df, 0, ctypes.byref(d),
+                                                  place(11) if parts else None, None) == 0
+                (name, grid, threads, smem, cluster), *join = launches(lib)
+                one = bgate if gate else bwd
+                assert "bn_bwd_kernel" in name and (grid, threads) == ((one.grid * one.ctas, 1, 1), one.threads), where
+                assert smem == one.smem(el) and cluster == (one.grid if one.joined else one.ctas), where
+                assert [j[0].count("bn_join_kernel") for j in join] == ([] if one.joined else [1]), where
+                if join:
+                    images = 0 if not gate or one.whole else up(n, 16)
+                    assert join[0][1] == (up(c, 16), 1 + images, 1), where
+        lib.conv_plan_destroy(h)
