@@ -220,7 +220,10 @@ struct PairSums {
 // dx and df of the rows of a CTA's units, and the units' channel sums.  ALL: the
 // block, dy and dz are given; what is then not asked for is formed all the same,
 // which is fewer instructions than asking (8x80x80x256 bf16: 18.5 M warp
-// instructions with the branches, 13.7 M without).  The statistics come through
+// instructions with the branches, 13.7 M without).  Normalised values are
+// (v - m) r: as v r - m r, one instruction fewer a norm, they bore the rounding of
+// m r, many times their own where the mean is far above the spread (8x80x80x256
+// 31.6 us either way, 8x40x40x511 41.8 so and 42.8).  The statistics come through
 // the ring too: read a row ahead they were what the warps waited for (37 us, 31.5
 // so).  A pair of CTAs (ROW_PAIR) meets once a row, for the sums of both norms: a
 // meeting of the cluster takes about half a microsecond (4096x8192 bf16 143 us with
@@ -331,13 +334,13 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             R::get(l, d, ox, y);
             if (block) {
                 R::get(l, d + LINE, of, u);
-                const float2 r = both(st.y), c = both(-st.x * st.y);
+                const float2 r = both(st.y), m = both(-st.x);
                 if (ALL || a.b1)
 #pragma unroll
                     for (int k = 0; k < P; ++k) y[k] = add2(y[k], p[k]);
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
-                    u[k] = fma2(u[k], r, c);
+                    u[k] = mul2(add2(u[k], m), r);
                     y[k] = fma2(q[k], u[k], y[k]);
                 }
             }
@@ -356,11 +359,11 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
                 if (norm) {
                     float2 e[P];
                     R::get(l, d + 3 * LINE, odz, e);
-                    const float2 r = both(st.w), c = both(-st.z * st.w);
+                    const float2 r = both(st.w), mean = both(-st.z);
 #pragma unroll
                     for (int k = 0; k < P; ++k) {
                         acc[SUM_B2][k] = add2(acc[SUM_B2][k], e[k]);
-                        y[k] = fma2(y[k], r, c);
+                        y[k] = mul2(add2(y[k], mean), r);
                         acc[SUM_G2][k] = fma2(e[k], y[k], acc[SUM_G2][k]);
                         e[k] = mul2(e[k], g2[k]);
                         t[k] = fma2(e[k], r, t[k]);
@@ -395,13 +398,13 @@ __global__ void __launch_bounds__(kMostThreads) bn_bwd_kernel(const __grid_const
             } else if (norm) {
                 float2 e[P], w = make_float2(0.0f, 0.0f), v = w;
                 R::get(l, d + 3 * LINE, odz, e);
-                const float2 r = both(st.w), c = both(-st.z * st.w);
+                const float2 r = both(st.w), mean = both(-st.z);
                 if (ALL || a.db2)
 #pragma unroll
                     for (int k = 0; k < P; ++k) acc[SUM_B2][k] = add2(acc[SUM_B2][k], e[k]);
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
-                    y[k] = fma2(y[k], r, c);
+                    y[k] = mul2(add2(y[k], mean), r);
                     acc[SUM_G2][k] = fma2(e[k], y[k], acc[SUM_G2][k]);
                     e[k] = mul2(e[k], g2[k]);
                     w = add2(w, e[k]);
