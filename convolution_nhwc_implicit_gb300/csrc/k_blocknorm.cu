@@ -25,7 +25,9 @@
 // CTA takes several rows side by side and a run of sets of them.  Rows are copied
 // ahead into a ring of shared memory (cp.async), each thread its own values, so
 // that nothing waits for another thread but the sums over a row.  All statistics
-// and sums are fp32, in a fixed order: results do not change from run to run.
+// and sums are fp32, in a fixed order: results do not change from run to run.  (A
+// thread adds its rows' terms of a sum over pixels one after another: all rows of
+// 4096 channels over 152 CTAs, of 16 channels over 256 times as many.)
 //
 // Measured on a GB300 by graph replay over changing inputs, of HBM's 6.7 TB/s:
 // 8x80x80x256 bf16, both norms rms and a gate, 19.8 us forward (105 MB, 15.8 us of
