@@ -19,12 +19,13 @@
 // and spares its rounding.  About 20 operations an element forward and 45
 // backward against 8 to 24 bytes moved: memory bounds it.
 //
-// A thread holds 8 K channels of a row (K = 2 where rows are long) and, in the
-// gradient, the channels' sums over its rows; a row is shared by as many threads
-// as that takes: lanes of a warp, or whole warps that meet in shared memory.  A
-// CTA takes several rows side by side and a run of sets of them.  Rows are copied
-// ahead into a ring of shared memory (cp.async), each thread its own values, so
-// that nothing waits for another thread but the sums over a row.  All statistics
+// A thread holds 8 K channels of a row (K = 2 where rows are long, or many and a
+// warp's) and, in the gradient, the channels' sums over its rows; a row is shared
+// by as many threads as that takes: lanes of a warp, or whole warps that meet in
+// shared memory.  A CTA takes several rows side by side and a run of sets of them.
+// Rows are copied ahead into a ring of shared memory (cp.async), each thread its
+// own values, so that nothing waits for another thread but the sums over a row.
+// All statistics
 // and sums are fp32, in a fixed order: results do not change from run to run.  (A
 // thread adds its rows' terms of a sum over pixels one after another: all rows of
 // 4096 channels over 152 CTAs, of 16 channels over 256 times as many.)
@@ -365,23 +366,38 @@ void plan_geometry(conv_plan *p) {
     // 98 us, 2048x8192 fp32 73, where sixteen took 147 and 117; up to 4096 a CTA
     // holds it: 8192x4096 bf16 84, a pair 97, 4096x4096 fp32 71 and 71, 8192x2560
     // bf16 70 and 67).
-    // Up to 512 sixteen make a row a warp's, whose sums need no barrier: many rows
-    // whose channels are no whole 16-byte vectors, or bf16 with a layer norm, are
-    // faster so (8x40x40x510 layer and rms 16.4 and 15.4, 512 two layer
-    // norms 14.6 and 14.0; but two rms norms 11.7 and 12.4, fp32 19.0 and 19.9)
-    const bool layers = g.post == CONV_NORM_LAYER || g.pre == CONV_NORM_LAYER;
-    const bool warp = C > 256 && C <= 512 && rows > 1024 && (C * es % 16 != 0 || (es == 2 && layers));
-    const int fk = C > 2048 || warp ? 2 : 1, pair = C > 8 * kMostThreads;
+    // From 257 to 512 channels sixteen make a row a warp's, whose sums need no barrier.
+    // That pays for more rows than four sets of eight channels a thread (4864 on 152
+    // SMs), of maps whose channels are no whole 16-byte vectors, and of bf16 without a
+    // gate under a layer norm.  Eight and sixteen, us, ungated:
+    //   rows                     2432          4864          12800         51200
+    //   510 bf16 layer, rms      4.2, 4.8      6.3, 6.5      16.4, 15.3    48.5, 44.8
+    //   511 bf16 rms, rms        5.2, 5.9      8.4, 8.4      21.7, 20.2    67.5, 61.1
+    //   511 fp32 layer, layer    5.5, 6.3      12.0, 12.1    26.8, 24.8    86.5, 80.0
+    //   264 bf16 layer, rms      3.5, 4.0      5.2, 5.4      11.9, 10.8    38.0, 32.5
+    //   512 bf16 layer, layer    4.0, 4.7      6.0, 6.4      14.6, 14.1    42.8, 37.9
+    //   512 bf16 layer, rms      3.7, 4.4      5.4, 5.9      13.2, 13.2    38.0, 39.5
+    //   512 bf16 rms, rms        3.3, 4.1      4.8, 5.5      11.7, 12.4    36.4, 39.7
+    // and with a gate at 12800 rows: 511 bf16 layer, rms 23.2, 22.9; 512 13.3, 14.8.
+    // (Slices at addresses that allow no vectors go by their channel count all the
+    // same: 512 of 513 bf16 rms, rms at 12800 rows 21.8, 19.5.)
+    const bool layers = g.post == CONV_NORM_LAYER || g.pre == CONV_NORM_LAYER, ragged = C * es % 16 != 0;
+    part(g.fwd, 1, 1, kThreads);
+    const bool many = C > 256 && C <= 512 && rows > 4 * wave(g.fwd) * g.fwd.slots;
+    const int pair = C > 8 * kMostThreads;
     // two rows at a time where one wave of CTAs takes more than one set of rows
     // (64x25x5x61 fp32, 0.8 of a set: one at a time 4.5 us, two 5.7)
-    part(g.fwd, 1, fk, kThreads);
-    if (fk == 1 && rows > wave(g.fwd) * g.fwd.slots) g.fwd.rb = 2;
-    g.fwd_gated = g.fwd;
+    auto forward = [&](BnGeom::Part &d, bool sixteen) {
+        part(d, 1, sixteen ? 2 : 1, kThreads);
+        if (!sixteen && rows > wave(d) * d.slots) d.rb = 2;
+    };
+    forward(g.fwd, C > 2048 || (many && (ragged || (es == 2 && layers))));
+    forward(g.fwd_gated, C > 2048 || (many && ragged));
     divide_rows(g.fwd, rows, (long long)g.fwd.slots * g.fwd.rb, wave(g.fwd));
-    if (g.fwd.rb == 2 && HW >= 4LL * g.fwd.slots) divide_images(g.fwd_gated, N, HW, 2LL * g.fwd.slots, wave(g.fwd_gated));
+    if (g.fwd_gated.rb == 2 && HW >= 4LL * g.fwd_gated.slots) divide_images(g.fwd_gated, N, HW, 2LL * g.fwd_gated.slots, wave(g.fwd_gated));
     else {
         g.fwd_gated.rb = 1;
-        divide_rows(g.fwd_gated, rows, g.fwd.slots, wave(g.fwd_gated));
+        divide_rows(g.fwd_gated, rows, g.fwd_gated.slots, wave(g.fwd_gated));
     }
     // the gradient in large CTAs: a part of the sums from each
     part(g.bwd, 0, 1, pair ? 1 : kMostThreads, pair);
