@@ -25,10 +25,10 @@
 // shared memory.  A CTA takes several rows side by side and a run of sets of them.
 // Rows are copied ahead into a ring of shared memory (cp.async), each thread its
 // own values, so that nothing waits for another thread but the sums over a row.
-// All statistics
-// and sums are fp32, in a fixed order: results do not change from run to run.  (A
-// thread adds its rows' terms of a sum over pixels one after another: all rows of
-// 4096 channels over 152 CTAs, of 16 channels over 256 times as many.)
+// All statistics and sums are fp32, in a fixed order: results do not change from
+// run to run.  (A thread adds its rows' terms of a sum over pixels one after
+// another: all rows of 4096 channels over 152 CTAs, of 16 channels over 256 times
+// as many.)
 //
 // Measured on a GB300 by graph replay over changing inputs, of HBM's 6.7 TB/s:
 // 8x80x80x256 bf16, both norms rms and a gate, 19.8 us forward (105 MB, 15.8 us of
@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(kMostThreads) bn_fwd_kernel(const __grid_const
 // ------------------------------------------------------------------ host side
 template <typename T, int VEC, bool CUT = false>
 const void *pick_fwd(int k, int rb, int tpr, bool all) {
-    if (k == 2 && tpr == 32) return all ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARP, true, CUT> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARP, false, CUT>;
+    if constexpr (sizeof(T) == 2 || VEC == 1)  // (fp32 rows of a warp and sixteen channels are ragged)
+        if (k == 2 && tpr == 32) return all ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARP, true, CUT> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARP, false, CUT>;
     if (k == 2) return all ? (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, true, CUT> : (const void *)&bn_fwd_kernel<T, VEC, 2, 1, ROW_WARPS, false, CUT>;
     if (rb == 1) return (const void *)&bn_fwd_kernel<T, VEC, 1, 1, ROW_ANY, false, CUT>;
     if (!all) return (const void *)&bn_fwd_kernel<T, VEC, 1, 2, ROW_ANY, false, CUT>;

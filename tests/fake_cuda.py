@@ -9,7 +9,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 
 
 def load(tmp):
-    """The library (its C ABI untyped, and fake_log, fake_clear, fake_queued), linked under `tmp`."""
+    """The library (its C ABI untyped, and fake_log, fake_clear, fake_queued, fake_kernel), linked under `tmp`."""
     from convolution_nhwc_implicit_gb300 import build
     build.build()
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build._nvcc()))), "include")
@@ -17,5 +17,5 @@ def load(tmp):
     subprocess.run(["gcc", "-std=gnu11", "-O1", "-fPIC", "-w", "-I", cuda, "-c", os.path.join(HERE, "fake_cudart.c"), "-o", fake], check=True)
     subprocess.run(["g++", "-shared", "-Wl,-Bsymbolic", "-o", lib, fake] + sorted(glob.glob(os.path.join(build.BUILD, "*.o"))), check=True)
     out = ctypes.CDLL(lib)
-    out.fake_log.restype = ctypes.c_char_p
+    out.fake_log.restype = out.fake_kernel.restype = ctypes.c_char_p
     return out

@@ -109,6 +109,7 @@ cudaError_t cudaGetSymbolAddress(void **p, const void *symbol) { return cudaErro
 
 static struct { const void *host; char name[256]; } kernels[2048];
 static int known;
+const char *fake_kernel(int i) { return i < known ? kernels[i].name : 0; }
 static const char *name_of(const void *f) {
     for (int i = 0; i < known; ++i)
         if (kernels[i].host == f) return kernels[i].name;

@@ -107,3 +107,28 @@ def test_launches_are_the_restated_ones(lib):
                     images = 0 if not gate or one.whole else up(n, 16)
                     assert join[0][1] == (up(c, 16), 1 + images, 1), where
         lib.conv_plan_destroy(h)
+
+
+def test_every_instance_that_is_built_is_reached(lib):
+    built, i = set(), 0
+    while name := lib.fake_kernel(i):
+        if b"bn_fwd_kernel" in name or b"bn_bwd_kernel" in name:
+            built.add(name.decode())
+        i += 1
+    reached = set()
+    channels = (3, 8, 12, 250, 251, 256, 301, 302, 320, 511, 512, 1000, 1001, 1002, 2500, 2501, 2502, 5000, 5001, 5002)
+    for c in channels:
+        for es in (2, 4):
+            for rows in (1, 2, 200000, 200001):
+                for kind in (1, 2):
+                    h = ctypes.c_void_p()
+                    assert lib.conv_plan_create_blocknorm(1, rows, 1, c, kind, kind, 1e-5, 0 if es == 4 else 1, ctypes.byref(h)) == 0
+                    x, f, y, z, dy, dz, dx, df = (place(i) for i in range(8))
+                    lib.fake_clear()
+                    for whole in (True, False):
+                        assert lib.conv_run_blocknorm(h, x, 0, f, 0, None, y if whole else None, 0, z, 0, None, None) == 0
+                        assert lib.conv_run_blocknorm_bwd(h, x, 0, f, 0, None, place(10), dy if whole else None, 0, dz, 0, dx, 0, df, 0, None,
+                                                          place(11), None) == 0
+                    reached |= {line[0] for line in launches(lib)}
+                    lib.conv_plan_destroy(h)
+    assert len(built) > 60 and built - reached == set()
