@@ -851,7 +851,8 @@ class GradClipPlan(_OpPlan):
         """Enqueue the norm (a float32 scalar tensor) and the clipped gradients
         on `stream` (default: torch's current stream): into the tensors of `out`
         (any of which may be the gradient itself), or in place.  max_norm
-        infinite: the norm alone.  A norm that is not finite clips nothing."""
+        infinite: the norm alone.  A norm that is not finite (or passes the
+        largest float32 number) clips nothing: leave that step out."""
         dev = self._on_device()
         g = self._addresses("grads", grads)
         o = None if out is None else self._addresses("out", out)

@@ -88,9 +88,9 @@ __host__ __device__ constexpr int ring_element(int es, int vec) { return es * ve
 // A thread's vectors of one row: from its ring of shared memory, to a map, and
 // from a map to the ring.  Vectors beyond the row's end stay 0 in the ring.  CUT: of
 // single bf16 values, a map starts in the middle of a word or ends in one; the half
-// that is not the map's is not read.  (An instance of its own, 1 to 4 % slower, and 9
-// to 13 % forward beyond 2048 channels: 8191x3001 takes 73 and 160 us, 8192x3001, whose
-// maps are whole words, 67 and 155.)
+// that is not the map's is not read.  (An instance of its own.  Forward beyond 2048
+// channels it is 9 to 13 % slower: 4095x8191 117 us, 4096x8191, whose maps are whole
+// words, 103; elsewhere up to 4 %.)
 template <typename T, int VEC, int K, bool CUT = false>
 struct Row {
     using V = Vec<T, VEC>;

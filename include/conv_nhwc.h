@@ -460,7 +460,9 @@ CONV_API int conv_run_blocknorm_bwd(const conv_plan_t *plan, const void *x, int6
  *   norm = sqrt( sum over all tensors and elements of g^2 )
  *   k = min( 1, max_norm / (norm + 1e-6) )        out = k g
  * A norm that is not finite clips nothing (k = 1): it says itself that the
- * step is to be left out.  `counts` and `dtypes` (HOST arrays of `tensors`
+ * step is to be left out, and whoever takes the step all the same takes it
+ * unclipped.  That holds for finite gradients whose norm passes the largest
+ * float32 number, too: the norm is then infinite.  `counts` and `dtypes` (HOST arrays of `tensors`
  * entries, copied) give each tensor's elements (>= 0; all together < 2^40) and
  * type, CONV_F32 or CONV_BF16 (CONV_I8: CONV_ERR_UNSUPPORTED).
  *   grads  HOST array of `tensors` device addresses, multiples of the element
