@@ -1,7 +1,6 @@
 """The library's own objects linked with fake_cudart.c instead of the CUDA
 runtime: plans and runs on the CPU, whose launches only leave a line in a log."""
 import ctypes
-import glob
 import os
 import subprocess
 
@@ -13,9 +12,10 @@ def load(tmp):
     from convolution_nhwc_implicit_gb300 import build
     build.build()
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(build._nvcc()))), "include")
+    objects = [os.path.join(build.BUILD, os.path.basename(s)[:-3] + ".o") for s in build._sources()]
     fake, lib = os.path.join(str(tmp), "fake_cudart.o"), os.path.join(str(tmp), "libconv_fake.so")
     subprocess.run(["gcc", "-std=gnu11", "-O1", "-fPIC", "-w", "-I", cuda, "-c", os.path.join(HERE, "fake_cudart.c"), "-o", fake], check=True)
-    subprocess.run(["g++", "-shared", "-Wl,-Bsymbolic", "-o", lib, fake] + sorted(glob.glob(os.path.join(build.BUILD, "*.o"))), check=True)
+    subprocess.run(["g++", "-shared", "-Wl,-Bsymbolic", "-o", lib, fake] + objects, check=True)
     out = ctypes.CDLL(lib)
     out.fake_log.restype = out.fake_kernel.restype = ctypes.c_char_p
     return out
